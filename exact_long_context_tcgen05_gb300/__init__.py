@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libcqsa_gb300.so")
 
 CQSA_OK, CQSA_ERR_INVALID, CQSA_ERR_UNSUPPORTED, CQSA_ERR_CUDA, CQSA_ERR_OOM, CQSA_ERR_TIMEOUT, CQSA_ERR_DEVICE = (
     0, -1, -2, -3, -4, -5, -6)
-CQSA_F16, CQSA_BF16, CQSA_F32 = 0, 1, 2
+CQSA_F16, CQSA_BF16, CQSA_F32, CQSA_E4M3 = 0, 1, 2, 3
 CQSA_LAYOUT_BHND, CQSA_LAYOUT_BNHD = 0, 1
 CQSA_ENGINE_CLASSIC, CQSA_ENGINE_WAVE = 0, 1
 
@@ -25,7 +25,8 @@ EXPORTED = ("cqsa_attn_fwd", "cqsa_attn_fwd_chunk", "cqsa_merge_partials", "cqsa
             "cqsa_quorum_attn_fwd_ex", "cqsa_release_cache", "cqsa_attn_bwd_workspace_size", "cqsa_attn_bwd", "cqsa_attn_bwd_dvec",
             "cqsa_attn_bwd_chunk", "cqsa_attn_bwd_cast", "cqsa_stream_attn_bwd", "cqsa_stream_attn_bwd_ex",
             "cqsa_status_string", "cqsa_last_error", "cqsa_device_error", "cqsa_set_timeout_ms",
-            "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes")
+            "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes", "cqsa_kv_cache_write",
+            "cqsa_kv_cache_read", "cqsa_attn_paged_workspace_size", "cqsa_attn_paged_fwd")
 CQSA_STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -90,6 +91,14 @@ def _load() -> ctypes.CDLL:
                                             _ll, ctypes.POINTER(cqsa_stream_stats), _vp]
     lib.cqsa_set_stream_kv_resident_bytes.argtypes = [_ll]
     lib.cqsa_set_stream_kv_resident_bytes.restype = None
+    lib.cqsa_kv_cache_write.argtypes = [_vp, _vp, _ll, _ll, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
+                                        _i, _i, _i, _vp]
+    lib.cqsa_kv_cache_read.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                                       _vp]
+    lib.cqsa_attn_paged_workspace_size.argtypes = [_i] * 10
+    lib.cqsa_attn_paged_workspace_size.restype = ctypes.c_size_t
+    lib.cqsa_attn_paged_fwd.argtypes = [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
+                                        _i, _i, _i, _i, _i, _f, _i, _i, _vp, ctypes.c_size_t, _vp]
     lib.cqsa_release_cache.argtypes = []
     lib.cqsa_release_cache.restype = _i
     lib.cqsa_status_string.argtypes = [_i]
@@ -289,6 +298,36 @@ def cqsa_stream_attn_bwd_ex(q, k, v, out, dout, lse, dq, dk, dv, B, H, N, d, cau
     return st
 
 
+def cqsa_kv_cache_write(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, cu_seqlens,
+                        kv_lens, n_seqs, T, Hkv, d, page_size, n_pages, dtype, cache_dtype, stream=None) -> int:
+    return _check(lib.cqsa_kv_cache_write(_ptr(k), _ptr(v), k_stride, v_stride, _ptr(k_cache), _ptr(v_cache),
+                                          _ptr(k_scale), _ptr(v_scale), _ptr(block_table), max_pages, _ptr(cu_seqlens),
+                                          _ptr(kv_lens), n_seqs, T, Hkv, d, page_size, n_pages, dtype, cache_dtype,
+                                          _stream(stream)))
+
+
+def cqsa_kv_cache_read(k, v, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, cu_seqlens, kv_lens, n_seqs, T,
+                       Hkv, d, page_size, n_pages, dtype, cache_dtype, stream=None) -> int:
+    return _check(lib.cqsa_kv_cache_read(_ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                         _ptr(block_table), max_pages, _ptr(cu_seqlens), _ptr(kv_lens), n_seqs, T, Hkv,
+                                         d, page_size, n_pages, dtype, cache_dtype, _stream(stream)))
+
+
+def cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page_size, max_q_len, max_kv_len, dtype, cache_dtype) -> int:
+    return int(lib.cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page_size, max_q_len, max_kv_len, dtype,
+                                                  cache_dtype))
+
+
+def cqsa_attn_paged_fwd(q, q_stride, out, lse, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, cu_seqlens,
+                        kv_lens, n_seqs, T, max_q_len, max_kv_len, Hq, Hkv, d, page_size, n_pages, causal, scale, dtype,
+                        cache_dtype, workspace, workspace_bytes, stream=None) -> int:
+    return _check(lib.cqsa_attn_paged_fwd(_ptr(q), q_stride, _ptr(out), _ptr(lse), _ptr(k_cache), _ptr(v_cache),
+                                          _ptr(k_scale), _ptr(v_scale), _ptr(block_table), max_pages, _ptr(cu_seqlens),
+                                          _ptr(kv_lens), n_seqs, T, max_q_len, max_kv_len, Hq, Hkv, d, page_size,
+                                          n_pages, int(bool(causal)), float(scale), dtype, cache_dtype, _ptr(workspace),
+                                          int(workspace_bytes), _stream(stream)))
+
+
 def cqsa_set_stream_kv_resident_bytes(nbytes: int) -> None:
     """K/V of cqsa_stream_attn_fwd stay on the device when they take at most nbytes (< 0: half of the free
     device memory, the default; 0: never, every pair through the fp32 accumulator)."""
@@ -352,3 +391,131 @@ def attention_backward(q, k, v, out, dout, lse, *, causal=False, scale=None, str
     cqsa_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, ws, ws.numel(), B, H, N, d, causal,
                   0.0 if scale is None else scale, dtype_code(q.dtype), stream)
     return dq, dk, dv
+
+
+# Sequences of different lengths: torch conveniences (checks and marshalling only). They run on the tensors' own
+# device, whichever is current, on `stream` (a torch stream or a cudaStream_t value) or that device's current
+# stream; what they allocate belongs to that stream.
+
+def _on(device, stream):
+    import contextlib
+
+    import torch
+    stack = contextlib.ExitStack()
+    if device.index != torch.cuda.current_device():
+        stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def _tokens(name, t, heads, d, like):
+    """A [T, heads, d] tensor of like's dtype and device, its heads dense; returns it (a copy if need be) and its token stride."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be a [T, {heads}, {d}] tensor of {like.dtype} on {like.device}")
+    s = t.stride()
+    if (s[2] != 1 or (s[1] != d and heads > 1) or s[0] < heads * d or s[0] % 8 or t.data_ptr() % 16) and t.shape[0] > 0:
+        t = t.contiguous()
+        if t.data_ptr() % 16:
+            t = t.clone()
+    return t, (t.stride(0) if t.shape[0] > 1 else 0)
+
+
+def _ints(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be an int32 tensor of shape {shape} on {device}")
+    return t.contiguous()
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, dtype, device):
+    """The checks that the calls on a paged cache share; returns the arguments they pass on."""
+    import torch
+    if not k_cache.is_cuda or k_cache.device != device or v_cache.device != device:
+        raise ValueError("k_cache and v_cache must be CUDA tensors on the tokens' device")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must be tensors of one shape and dtype [n_pages, Hkv, page_size, d]")
+    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("k_cache and v_cache must be contiguous")
+    if k_cache.dtype in (torch.uint8, torch.float8_e4m3fn):
+        code = CQSA_E4M3
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None or t.element_size() != 1 or t.shape != k_cache.shape[:3] or t.device != device or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous byte tensor [n_pages, Hkv, page_size] beside an e4m3 cache")
+    elif k_cache.dtype == dtype:
+        code = dtype_code(dtype)
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a 16-bit cache takes no scales")
+    else:
+        raise ValueError(f"a cache of {k_cache.dtype} does not go with tokens of {dtype}")
+    if block_table.dim() != 2 or kv_lens.dim() != 1 or block_table.shape[0] != kv_lens.shape[0]:
+        raise ValueError("block_table must be [n_seqs, max_pages] and kv_lens [n_seqs]")
+    n_seqs, max_pages = block_table.shape
+    return (code, n_seqs, max_pages, _ints("block_table", block_table, (n_seqs, max_pages), device),
+            _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), device), _ints("kv_lens", kv_lens, (n_seqs,), device))
+
+
+def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, k_scale=None, v_scale=None, stream=None):
+    """New tokens k, v [T, Hkv, d] into their pages of the caches [n_pages, Hkv, page_size, d] (k's dtype, or
+    uint8 / float8_e4m3fn codes with byte tensors k_scale, v_scale [n_pages, Hkv, page_size])."""
+    n_pages, Hkv, page, d = k_cache.shape
+    with _on(k.device, stream):
+        code, n_seqs, max_pages, table, cu, lens = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                          kv_lens, k.dtype, k.device)
+        (k, ks), (v, vs) = _tokens("k", k, Hkv, d, k), _tokens("v", v, Hkv, d, k)
+        if v.shape != k.shape:
+            raise ValueError("k and v must have one shape")
+        cqsa_kv_cache_write(k, v, ks, vs, k_cache, v_cache, k_scale, v_scale, table, max_pages, cu, lens, n_seqs,
+                            k.shape[0], Hkv, d, page, n_pages, dtype_code(k.dtype), code)
+
+
+def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, *, k_scale=None, v_scale=None, out=None,
+                  stream=None):
+    """The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as (k, v) [T, Hkv, d] of dtype (into `out`, a
+    pair of such tensors, if given)."""
+    import torch
+    n_pages, Hkv, page, d = k_cache.shape
+    with _on(k_cache.device, stream):
+        code, n_seqs, max_pages, table, cu, lens = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                          kv_lens, dtype, k_cache.device)
+        k, v = out if out is not None else (torch.empty((T, Hkv, d), dtype=dtype, device=k_cache.device) for _ in range(2))
+        for t in (k, v):
+            if t.shape != (T, Hkv, d) or t.dtype != dtype or t.device != k_cache.device or not t.is_contiguous():
+                raise ValueError(f"out must be two contiguous [{T}, {Hkv}, {d}] tensors of {dtype}")
+        cqsa_kv_cache_read(k, v, k_cache, v_cache, k_scale, v_scale, table, max_pages, cu, lens, n_seqs, T, Hkv, d, page,
+                           n_pages, dtype_code(dtype), code)
+    return k, v
+
+
+def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len, max_kv_len, *, causal=True,
+                    scale=None, k_scale=None, v_scale=None, return_lse=False, out=None, workspace=None, stream=None):
+    """Attention of each sequence's new tokens q [T, Hq, d] over its positions in the paged cache: out [T, Hq, d] (and
+    lse [Hq, T] fp32). max_q_len: at least the most new tokens of a sequence; max_kv_len: about the longest kv_lens.
+    `workspace`: a byte tensor of at least cqsa_attn_paged_workspace_size bytes (allocated if not given)."""
+    import torch
+    n_pages, Hkv, page, d = k_cache.shape
+    with _on(q.device, stream):
+        code, n_seqs, max_pages, table, cu, lens = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                          kv_lens, q.dtype, q.device)
+        q, qs = _tokens("q", q, q.shape[1] if q.dim() == 3 else 0, d, q)
+        T, Hq, dt = q.shape[0], q.shape[1], dtype_code(q.dtype)
+        out = _out(out, q)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
+        need = cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page, max_q_len, max_kv_len, dt, code)
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        cqsa_attn_paged_fwd(q, qs, out, lse, k_cache, v_cache, k_scale, v_scale, table, max_pages, cu, lens, n_seqs, T,
+                            max_q_len, max_kv_len, Hq, Hkv, d, page, n_pages, causal, 0.0 if scale is None else scale, dt,
+                            code, workspace, workspace.numel() * workspace.element_size())
+    return (out, lse) if return_lse else out
+
+
+def _out(out, q):
+    import torch
+    if out is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {tuple(q.shape)} tensor of {q.dtype} on {q.device}")
+    return out

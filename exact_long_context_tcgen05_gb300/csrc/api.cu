@@ -13,6 +13,7 @@ namespace cqsa {
 
 int device_error_word(DevErr* out, int clear);  // attn_fwd.cu (owns the forward's device word)
 int bwd_error_word(DevErr* out, int clear);     // attn_bwd.cu (the backward's)
+int decode_error_word(DevErr* out, int clear);  // attn_decode.cu
 int device_error_word_on(DevErr* out, cudaStream_t s);  // read on one stream; cleared when set
 int bwd_error_word_on(DevErr* out, cudaStream_t s);
 
@@ -146,11 +147,11 @@ int cqsa_device_error(int* code, int* block, int clear) {
   DevErr e;
   int rc = cuda_status(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
   if (rc != CQSA_OK) return rc;
-  rc = device_error_word(&e, clear);
-  if (rc != CQSA_OK) return rc;
-  if (e.code == 0) {
-    rc = bwd_error_word(&e, clear);
+  int (*const words[])(DevErr*, int) = {device_error_word, bwd_error_word, decode_error_word};
+  for (auto word : words) {
+    rc = word(&e, clear);
     if (rc != CQSA_OK) return rc;
+    if (e.code != 0) break;
   }
   if (code) *code = e.code;
   if (block) *block = e.block;

@@ -96,6 +96,56 @@ int launch_bwd_cast(const float* acc, void* out, long long n, int dtype, cudaStr
 int launch_merge(const float* const* O_parts, const float* const* LSE_parts, int n, void* out, float* lse,
                  long long rows, int d, int out_dtype, cudaStream_t stream);
 
+// The paged cache (kv_cache.cu) and the attention over it (attn_decode.cu, attn_seq.cu). Sequence s owns
+// tokens [cu[s], cu[s+1]) of the packed tensors and positions [0, kv_lens[s]) of its pages.
+struct CacheArgs {
+  const void* k;        // [T, Hkv, d] new tokens, `*_stride` elements from token to token
+  const void* v;
+  void* k_out;          // reading: [T, Hkv, d]
+  void* v_out;
+  void* k_cache;        // [n_pages, Hkv, page, d]
+  void* v_cache;
+  unsigned char* k_scale;  // e4m3: [n_pages, Hkv, page] exponent bytes
+  unsigned char* v_scale;
+  const int* table;     // [n_seqs, max_pages]
+  const int* cu;
+  const int* kv_lens;
+  long long k_stride, v_stride;
+  int n_seqs, T, Hkv, d, page, n_pages, max_pages, dtype, cache_dtype;
+};
+int launch_kv_cache(const CacheArgs& a, bool write, cudaStream_t stream);
+
+struct PagedArgs {
+  const void* q;        // [T, Hq, d]
+  void* out;            // [T, Hq, d]
+  float* lse;           // [Hq, T] or null
+  const void* k_cache;
+  const void* v_cache;
+  const unsigned char* k_scale;
+  const unsigned char* v_scale;
+  const int* table;
+  const int* cu;
+  const int* kv_lens;
+  void* workspace;
+  long long q_stride;
+  int n_seqs, T, Hq, Hkv, d, page, n_pages, max_pages, max_q_len, max_kv_len, causal, dtype, cache_dtype;
+  float scale;          // resolved
+};
+// Few rows per sequence: the split kernel of attn_decode.cu.
+bool decode_applies(const PagedArgs& a);
+size_t decode_workspace(const PagedArgs& a);
+int launch_decode(const PagedArgs& a, cudaStream_t stream);
+// Chunks of new tokens: the tensor-core kernel of attn_seq.cu.
+size_t chunk_workspace(const PagedArgs& a);
+int launch_chunk(const PagedArgs& a, cudaStream_t stream);
+
+// Tensor maps (seq_api.cu). `strides` are bytes of dimensions 1 and up.
+int encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                      const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
+// A cache as (feature, slot, head, page) with boxes of `rows` slots of one page: 64 features of 16-bit
+// data (128-byte swizzle), a whole vector of e4m3 (128- or 64-byte swizzle, the row's size).
+int make_page_map(CUtensorMap* m, const void* cache, const PagedArgs& a, int rows);
+
 // Copy tokens [t0, t0+n) of a [B,H,N,d] / [B,N,H,d] tensor (host or device) into a packed chunk buffer.
 cudaError_t copy_chunk(void* dst, const void* src, int layout, int B, int H, long long N, int d, long long t0, int n,
                        cudaMemcpyKind kind, cudaStream_t s, long long* bytes);
@@ -147,6 +197,7 @@ int sm_count();
 void set_error(const char* fmt, ...);
 int cuda_status(cudaError_t e, const char* what);
 unsigned long long timeout_ns();
+unsigned timeout_us();  // the same limit in microseconds, held in 32 bits
 int debug_fault();
 
 }  // namespace cqsa

@@ -47,7 +47,7 @@ typedef enum {
                                 (see cqsa_device_error) */
 } cqsa_status;
 
-typedef enum { CQSA_F16 = 0, CQSA_BF16 = 1, CQSA_F32 = 2 /* outputs only */ } cqsa_dtype;
+typedef enum { CQSA_F16 = 0, CQSA_BF16 = 1, CQSA_F32 = 2 /* outputs only */, CQSA_E4M3 = 3 /* caches only */ } cqsa_dtype;
 typedef enum { CQSA_LAYOUT_BHND = 0, CQSA_LAYOUT_BNHD = 1 } cqsa_layout;
 
 /*
@@ -334,6 +334,69 @@ int cqsa_stream_attn_bwd_ex(const void* q, const void* k, const void* v, const v
 int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, void* out, float* lse, int B,
                                  int H, int N, int d, int causal, float scale, int dtype, int chunk_tokens,
                                  cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Sequences of different lengths, grouped heads, and a paged key/value cache. The call on the source pages
+ * has none of these; they are a library facility beside it: a prompt's attention (and its gradient), the cache its keys
+ * and values go into, and the attention of later tokens over that cache.
+ *
+ * Packed tokens: the tokens of n_seqs sequences lie end to end in one [T, heads, d] tensor; sequence s owns
+ * tokens [cu_seqlens[s], cu_seqlens[s+1]). cu_seqlens: device int32 [n_seqs + 1], non-decreasing. Lengths of
+ * zero are allowed; rows of T that belong to no sequence are not read for any other row and are left as they
+ * were in every output. Inputs may have a token stride (elements, a multiple of 8, at least heads * d, 0 for exactly
+ * that), as a slice of a fused projection has; d is contiguous and heads follow each other by d elements.
+ * Grouped heads: query head h reads key head h / (Hq / Hkv); Hq is a multiple of Hkv, at most 64 times it.
+ * lse: device fp32 [Hq, T], natural log, or NULL. Types, scale and status as above; T * Hq < 2^31.
+ *
+ * The values in cu_seqlens, kv_lens and block_table are on the device and cannot be refused: counts outside
+ * [0, T] are held inside it, and a page outside [0, n_pages) is skipped by a write and stands for page 0 in
+ * a read, so that no call leaves the buffers it was given; results for the rows concerned are then unspecified.
+ *
+ * Paged cache: k_cache, v_cache device [n_pages, Hkv, page_size, d], page_size 16, 32, 64, 128 or 256;
+ * block_table device int32 [n_seqs, max_pages]: position t of sequence s is slot t % page_size of page
+ * block_table[s][t / page_size]. cache_dtype: dtype itself, or CQSA_E4M3: each vector is e4m3 codes times one
+ * power of two, 2^(b - 127) for its byte b in k_scale / v_scale (device [n_pages, Hkv, page_size], 16-byte
+ * aligned; ignored otherwise). The power is the smallest (at least 2^-126) under which the vector's largest finite magnitude is
+ * at most 448; codes are rounded to nearest even; an infinity becomes NaN. kv_lens: device int32 [n_seqs], the
+ * positions of each sequence, its new tokens included: token i of a sequence's n new tokens has position
+ * kv_lens[s] - n + i. Slots past a sequence's length may hold anything. Pages may be shared between
+ * sequences as long as no two tokens of one write go to the same slot.
+ *
+ * Every call is asynchronous on `stream` and allocates nothing. Two calls whose work may overlap on the GPU
+ * need a workspace each (a captured graph keeps the one it was captured with).
+ * ------------------------------------------------------------------------------------------------ */
+
+/* New tokens into their pages: k, v device [T, Hkv, d] of dtype. Tokens whose position is negative or beyond the
+ * table, or whose page is outside the cache, are skipped. */
+int cqsa_kv_cache_write(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache, void* v_cache,
+                        unsigned char* k_scale, unsigned char* v_scale, const int* block_table, int max_pages,
+                        const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int Hkv, int d, int page_size,
+                        int n_pages, int dtype, int cache_dtype, cudaStream_t stream);
+
+/* The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence back out of the cache (all of them where
+ * that is kv_lens[s]): k, v device [T, Hkv, d], written in dtype; e4m3 values are rounded to dtype once. Tokens whose position
+ * is negative or beyond the table give zeros. */
+int cqsa_kv_cache_read(void* k, void* v, const void* k_cache, const void* v_cache, const unsigned char* k_scale,
+                       const unsigned char* v_scale, const int* block_table, int max_pages, const int* cu_seqlens,
+                       const int* kv_lens, int n_seqs, int T, int Hkv, int d, int page_size, int n_pages, int dtype,
+                       int cache_dtype, cudaStream_t stream);
+
+/* Attention of each sequence's new tokens (one, a few, or a chunk; already written to the cache) over its
+ * positions: q device [T, Hq, d], out device [T, Hq, d] of dtype, contiguous. causal: token i sees positions up to its own;
+ * otherwise all kv_lens[s]. A row that sees nothing gives out = 0, lse = -inf. max_q_len: at least the most new tokens of a
+ * sequence (rows beyond it may be left as they were); max_kv_len: about the longest kv_lens (it sets how the work is
+ * split, not the result). At most 32 rows per sequence and key head (max_q_len * Hq / Hkv) run as one
+ * split over the keys; more run on the tensor cores in tiles of 128. P is rounded to dtype (fp16 for an e4m3
+ * cache) for its product with V; sums are fp32. workspace: device memory, 16-byte aligned, of at least
+ * cqsa_attn_paged_workspace_size bytes for the same arguments (0: none is needed); its contents on entry do not
+ * matter. */
+size_t cqsa_attn_paged_workspace_size(int n_seqs, int T, int Hq, int Hkv, int d, int page_size, int max_q_len, int max_kv_len,
+                                      int dtype, int cache_dtype);
+int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse, const void* k_cache, const void* v_cache,
+                        const unsigned char* k_scale, const unsigned char* v_scale, const int* block_table, int max_pages,
+                        const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int max_q_len, int max_kv_len, int Hq,
+                        int Hkv, int d, int page_size, int n_pages, int causal, float scale, int dtype, int cache_dtype,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Human-readable name of a status code. */
 const char* cqsa_status_string(int status);
