@@ -25,7 +25,7 @@ EXPORTED = ("cqsa_attn_fwd", "cqsa_attn_fwd_chunk", "cqsa_merge_partials", "cqsa
             "cqsa_quorum_attn_fwd_ex", "cqsa_release_cache", "cqsa_attn_bwd_workspace_size", "cqsa_attn_bwd", "cqsa_attn_bwd_dvec",
             "cqsa_attn_bwd_chunk", "cqsa_attn_bwd_cast", "cqsa_stream_attn_bwd", "cqsa_stream_attn_bwd_ex",
             "cqsa_status_string", "cqsa_last_error", "cqsa_device_error", "cqsa_set_timeout_ms",
-            "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes", "cqsa_kv_cache_write",
+            "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes", "cqsa_attn_packed_fwd", "cqsa_kv_cache_write",
             "cqsa_kv_cache_read", "cqsa_attn_paged_workspace_size", "cqsa_attn_paged_fwd")
 CQSA_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -91,6 +91,7 @@ def _load() -> ctypes.CDLL:
                                             _ll, ctypes.POINTER(cqsa_stream_stats), _vp]
     lib.cqsa_set_stream_kv_resident_bytes.argtypes = [_ll]
     lib.cqsa_set_stream_kv_resident_bytes.restype = None
+    lib.cqsa_attn_packed_fwd.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp]
     lib.cqsa_kv_cache_write.argtypes = [_vp, _vp, _ll, _ll, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
                                         _i, _i, _i, _vp]
     lib.cqsa_kv_cache_read.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
@@ -298,6 +299,13 @@ def cqsa_stream_attn_bwd_ex(q, k, v, out, dout, lse, dq, dk, dv, B, H, N, d, cau
     return st
 
 
+def cqsa_attn_packed_fwd(q, k, v, q_stride, k_stride, v_stride, out, lse, cu_seqlens, n_seqs, T, Hq, Hkv, d, causal, scale,
+                         dtype, stream=None) -> int:
+    return _check(lib.cqsa_attn_packed_fwd(_ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, _ptr(out), _ptr(lse),
+                                           _ptr(cu_seqlens), n_seqs, T, Hq, Hkv, d, int(bool(causal)), float(scale), dtype,
+                                           _stream(stream)))
+
+
 def cqsa_kv_cache_write(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, cu_seqlens,
                         kv_lens, n_seqs, T, Hkv, d, page_size, n_pages, dtype, cache_dtype, stream=None) -> int:
     return _check(lib.cqsa_kv_cache_write(_ptr(k), _ptr(v), k_stride, v_stride, _ptr(k_cache), _ptr(v_cache),
@@ -455,6 +463,34 @@ def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens,
     n_seqs, max_pages = block_table.shape
     return (code, n_seqs, max_pages, _ints("block_table", block_table, (n_seqs, max_pages), device),
             _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), device), _ints("kv_lens", kv_lens, (n_seqs,), device))
+
+
+def _packed(q, k, v, cu_seqlens):
+    """The checks that the calls on packed tokens share: (q, k, v) with their strides, cu_seqlens, and the sizes."""
+    if q.dim() != 3 or k.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [T, Hq, d], k and v [T, Hkv, d]")
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    if k.shape[0] != T or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, d] with q's T")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [n_seqs + 1]")
+    n_seqs = cu_seqlens.shape[0] - 1
+    return (_tokens("q", q, Hq, d, q), _tokens("k", k, Hkv, d, q), _tokens("v", v, Hkv, d, q),
+            _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), q.device), n_seqs, T, Hq, Hkv, d)
+
+
+def attention_packed(q, k, v, cu_seqlens, *, causal=True, scale=None, return_lse=False, out=None, stream=None):
+    """Attention of whole prompts packed end to end: q [T, Hq, d], k, v [T, Hkv, d], cu_seqlens int32 [n_seqs + 1] on the
+    device; returns out [T, Hq, d] (and lse [Hq, T] fp32). Rows behind the last sequence are left as they were in `out`."""
+    import torch
+    with _on(q.device, stream):
+        (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
+        out = _out(out, q)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
+        cqsa_attn_packed_fwd(q, k, v, qs, ks, vs, out, lse, cu, n_seqs, T, Hq, Hkv, d, causal,
+                             0.0 if scale is None else scale, dtype_code(q.dtype))
+    return (out, lse) if return_lse else out
 
 
 def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, k_scale=None, v_scale=None, stream=None):

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libcqsa_gb300.so")
 SOURCES = ["attn_fwd.cu", "attn_bwd.cu", "merge.cu", "api.cu", "stream_driver.cu", "chunked_static.cu", "quorum.cu", "pool.cu", "stream_bwd.cu",
-           "seq_api.cu", "kv_cache.cu", "attn_decode.cu"]
+           "seq_api.cu", "kv_cache.cu", "attn_decode.cu", "attn_seq.cu"]
 HEADERS = ["sm103_ptx.cuh", "cqsa_internal.h", "seq_common.cuh", "attn_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

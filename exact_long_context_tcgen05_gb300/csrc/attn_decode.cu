@@ -738,4 +738,3 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream) {
 DEV_ERR_READERS(decode, g_decode_err)
 
 }  // namespace cqsa
-namespace cqsa { size_t chunk_workspace(const PagedArgs&) { return 0; } int launch_chunk(const PagedArgs&, cudaStream_t) { set_error("more than 32 rows per sequence and key head are not supported"); return CQSA_ERR_UNSUPPORTED; } }

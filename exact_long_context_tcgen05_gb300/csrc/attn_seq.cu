@@ -1,0 +1,1059 @@
+// Attention forward on the tensor cores for sequences of different lengths with grouped heads: whole prompts
+// packed end to end (cqsa_attn_packed_fwd), and chunks of new tokens over a paged cache, 16-bit or e4m3
+// (cqsa_attn_paged_fwd with more than 32 rows per sequence and key head).
+//
+// The pipeline is attn_fwd2_kernel's (attn_fwd.cu): TMA producer, one MMA-issuing warp per query tile, one
+// softmax warpgroup per query tile, tcgen05 products accumulating in tensor memory, an integer running reference
+// maximum with rare exact rescales. What differs:
+//   Rows     a tile's 128 rows are floor(128 / G) tokens times the G query heads of one key head (row
+//            r = token r / G, head r % G), loaded by one 3-D TMA box, so that a short sequence or chunk fills tiles G
+//            times better and K/V are loaded once for the whole group.
+//   Units    a CTA takes two row tiles of one (sequence, key head); it finds its unit from cu_seqlens alone.
+//            Units are ranked by their place in their sequence, the latest (under the causal mask the
+//            heaviest) first, so that the grid ends on light ones.
+//   Split    a chunk over a long cache has few units: each may be cut into n_splits ranges of its key tiles
+//            (grid * n_splits CTAs), which leave normalised fp32 partials that seq_combine_kernel joins.
+//   P        is rounded once to dtype for P V (2^-8 relative for bf16, as the output is; attn_fwd.cu's
+//            hi/lo split, half as many products again, serves fp32 partial results), scaled by 2^14 so that
+//            fp16 keeps its relative precision down to p = 2^-28.
+//   Tails    rows of V past a sequence's end (another sequence's tokens, or whatever an unused slot holds) are zeroed in
+//            shared memory before the product: p = 0 does not hide an infinity or NaN there.
+//   e4m3     four converter warps take the place of the K/V copies: they gather codes from the pages,
+//            a 16-byte piece a lane, and store fp16 tiles in the swizzled layout. Each warp converts 32
+//            keys relative to their largest power of two (exact but for values 2^-15 below it); that power
+//            goes into the scores' scale (K) and into an exponent that P is shifted by (V). Queries are fp16:
+//            bf16 ones are first scaled to [1, 2) by a power of two per row, in place.
+#include <math.h>
+#include <string.h>
+
+#include "attn_common.cuh"
+#include "cqsa_internal.h"
+#include "seq_common.cuh"
+#include "sm103_ptx.cuh"
+
+namespace cqsa {
+namespace {
+
+__device__ DevErr g_seq_err;
+
+constexpr int BN = 128;  // keys per tile
+constexpr uint32_t TILE_BYTES = 128 * 64 * 2;  // one 128 x 64 box of 16-bit elements
+constexpr uint32_t TMEM_COLS = 512;
+constexpr float kPShift = 14.0f;  // probabilities (and their sums) are kept as 2^14 p
+
+enum : int { kSrcPacked = 0, kSrcPages = 1, kSrcE4m3 = 2 };
+
+template <int D, int SRC>
+struct SeqCfg {
+  static constexpr bool CONV = SRC == kSrcE4m3;
+  // P over S where tensor memory (d = 128) or registers (beside the converter warps) leave no room for both
+  static constexpr bool ALIAS = D == 128 || CONV;
+  static constexpr int KSUB = D / 64;
+  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr uint32_t QT_BYTES = KSUB * TILE_BYTES;
+  static constexpr uint32_t KV_BYTES = KSUB * TILE_BYTES;
+  static constexpr uint32_t COL_S0 = 0, COL_S1 = 128;
+  static constexpr uint32_t COL_P0 = ALIAS ? 0u : 256u, COL_P1 = ALIAS ? 128u : 320u;
+  static constexpr uint32_t COL_O0 = ALIAS ? 256u : 384u, COL_O1 = COL_O0 + D;
+  static constexpr int NBARS = 1 + 3 * STAGES + 2 * 5 + 2 + 2;
+  // key tiles between folds of O into the fp32 running sum (attn_fwd.cu explains why): in shared memory
+  // for d = 64, in the SM's slot of attn_fwd.cu's array for d = 128
+  static constexpr int FLUSH = D == 64 ? 128 : 32;
+  static constexpr bool OSUM_SMEM = D == 64;
+  static constexpr uint32_t OSUM_BYTES = OSUM_SMEM ? 2u * D * 128u * 4u : 0u;
+  static constexpr uint32_t EXP_BYTES = CONV ? STAGES * 8u * 4u + 256u * 4u : 0u;
+  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + EXP_BYTES + NBARS * 8 + 64;
+  static_assert(SMEM_BYTES <= 232448, "shared memory exceeds 227 KiB");
+  static_assert(COL_O1 + D <= TMEM_COLS, "tensor memory layout exceeds 512 columns");
+  // setmaxnreg shares of warpgroup 0, the two softmax warpgroups and the converters
+  static constexpr int NTHR = CONV ? 512 : 384;
+  static constexpr int LAUNCH_REGS = CONV ? 128 : 168;
+  static constexpr int LOW = CONV ? 56 : 72, HIGH = CONV ? 184 : 216, CVT = 88;
+  static_assert(128 * LOW + 256 * HIGH + (CONV ? 128 * CVT : 0) <= NTHR * LAUNCH_REGS, "register split exceeds the launch allocation");
+};
+
+struct SeqParams {
+  const int* cu;
+  const int* kv_lens;  // null: a sequence's positions are its tokens (packed prompts)
+  const int* table;
+  const uint8_t* k_cache;  // e4m3 only (16-bit pages go through the tensor maps)
+  const uint8_t* v_cache;
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+  void* out;
+  float* lse;
+  float* part_o;  // [n_splits][T][Hq][D]
+  float* part_l;  // [n_splits][T][Hq], base 2
+  float* osum;
+  int n_osum;
+  int n_seqs, T, Hq, Hkv, G, tpt;  // tpt: tokens of a row tile, floor(128 / G)
+  int n_splits, max_pages, n_pages, page_log2, causal;
+  float scale_log2;
+  unsigned timeout_us;
+  int fault;  // test hook: 1 = block 0 never loads key tile 1
+};
+
+// What a CTA works on.
+struct Unit {
+  int seq;     // -1: nothing
+  int pair;    // which pair of row tiles of the sequence
+};
+
+// Rank `rank` among the pairs of all sequences, the latest pairs of their sequences first; among pairs of one
+// place the sequences' order. One warp: count(L) = pairs at place L or later is a sum over the sequences; a
+// binary search finds the place, a walk along the sequences the one of that rank.
+__device__ __forceinline__ Unit find_unit(const SeqParams& p, int rank, int lane) {
+  const int per = 2 * p.tpt;
+  auto pairs_of = [&](int s) -> int {
+    int first;
+    return s < p.n_seqs ? (seq_tokens(p.cu, s, p.T, &first) + per - 1) / per : 0;
+  };
+  const int u0 = pairs_of(lane);  // the first 32 sequences stay in a register
+  auto count = [&](int L) -> int {
+    int c = max(0, u0 - L);
+    for (int s = 32 + lane; s < p.n_seqs; s += 32) c += max(0, pairs_of(s) - L);
+    return __reduce_add_sync(0xffffffffu, c);
+  };
+  int most = u0;
+  for (int s = 32 + lane; s < p.n_seqs; s += 32) most = max(most, pairs_of(s));
+  most = __reduce_max_sync(0xffffffffu, most);
+  Unit u;
+  u.seq = -1;
+  u.pair = 0;
+  if (rank >= count(0)) return u;
+  int lo = 0, hi = most;  // count(lo) > rank >= count(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (count(mid) > rank) lo = mid;
+    else hi = mid;
+  }
+  int k = rank - count(lo + 1);
+  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+    const bool has = (s0 == 0 ? u0 : pairs_of(s0 + lane)) > lo;
+    unsigned b = __ballot_sync(0xffffffffu, has);
+    const int n = __popc(b);
+    if (k < n) {
+      for (int i = 0; i < k; ++i) b &= b - 1;
+      u.seq = s0 + __ffs(b) - 1;
+      break;
+    }
+    k -= n;
+  }
+  u.pair = lo;
+  return u;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void issue_s(uint32_t dcol, uint64_t a0, uint64_t b0, uint32_t idesc) {
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const uint32_t off = static_cast<uint32_t>((ks >> 2) * (TILE_BYTES >> 4) + (ks & 3) * 2);
+    if (ks == 0) mma_ss_i<0>(dcol, a0 + off, b0 + off, idesc);
+    else mma_ss_i<1>(dcol, a0 + off, b0 + off, idesc);
+  }
+}
+template <bool FIRST>
+__device__ __forceinline__ void issue_o(uint32_t ocol, uint32_t pcol, uint64_t v0, uint32_t idesc) {
+#pragma unroll
+  for (int ks = 0; ks < BN / 16; ++ks) {
+    const uint64_t bd = v0 + static_cast<uint32_t>(ks * (2048 >> 4));
+    if (FIRST && ks == 0) mma_ts_i<0>(ocol, pcol + ks * 8, bd, idesc);
+    else mma_ts_i<1>(ocol, pcol + ks * 8, bd, idesc);
+  }
+}
+
+__device__ __forceinline__ float row_max32(const float* x) {
+  float m0 = x[0], m1 = x[1];
+#pragma unroll
+  for (int c = 2; c < 30; c += 4) {
+    m0 = max3(m0, x[c], x[c + 1]);
+    m1 = max3(m1, x[c + 2], x[c + 3]);
+  }
+  return fmaxf(max3(m0, x[30], x[31]), m1);
+}
+
+// Zero rows [r0, 128) of a 128-row tile of KSUB boxes (a whole warp). A row is 128 bytes of each box, and the swizzle
+// only moves 16-byte pieces inside it.
+template <int KSUB>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int lane) {
+  const int n = (128 - r0) * 8;
+#pragma unroll
+  for (int x = 0; x < KSUB; ++x)
+    for (int i = lane; i < n; i += 32) st_shared_zero16(smem_u32(tile) + x * TILE_BYTES + r0 * 128 + i * 16);
+}
+
+template <int D, int BF16, int SRC>
+__global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
+    attn_seq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const SeqParams p) {
+  using C = SeqCfg<D, SRC>;
+  constexpr int STAGES = C::STAGES, KSUB = C::KSUB;
+  constexpr bool ALIAS = C::ALIAS, CONV = C::CONV;
+  constexpr int MB = CONV ? 0 : BF16;  // type of the products
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + 2 * C::QT_BYTES;
+  uint8_t* sV = sK + STAGES * C::KV_BYTES;
+  float* sOsum = reinterpret_cast<float*>(sV + STAGES * C::KV_BYTES);
+  int* sExp = reinterpret_cast<int*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES);  // [STAGES][K 4 | V 4]
+  float* sRow = reinterpret_cast<float*>(sExp + STAGES * 8);                       // [256] factor of a row's queries
+  bool osum_ok = true;
+  if (!C::OSUM_SMEM) {
+    uint32_t smid;
+    asm volatile("mov.u32 %0, %%smid;" : "=r"(smid));
+    osum_ok = smid < static_cast<uint32_t>(p.n_osum);
+    sOsum = p.osum + static_cast<size_t>(osum_ok ? smid : 0u) * (2 * 128 * 128);
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES + C::EXP_BYTES);
+  uint64_t* bar_q = bars;
+  uint64_t* bar_k_full = bar_q + 1;
+  uint64_t* bar_v_full = bar_k_full + STAGES;
+  uint64_t* bar_kv_empty = bar_v_full + STAGES;
+  uint64_t* bar_s_full = bar_kv_empty + STAGES;  // [2]
+  uint64_t* bar_s_free = bar_s_full + 2;         // [2] (P kept apart only)
+  uint64_t* bar_p_full = bar_s_free + 2;         // [2]
+  uint64_t* bar_pv_done = bar_p_full + 2;        // [2]
+  uint64_t* bar_o_final = bar_pv_done + 2;       // [2]
+  uint64_t* bar_mma_idle = bar_o_final + 2;      // [2]
+  uint64_t* bar_fix = bar_mma_idle + 2;          // the last V tile landed (its rows past the end are zeroed then)
+  uint64_t* bar_q2 = bar_fix + 1;                // e4m3, bf16 queries: converted in place
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q2 + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* sUnit = reinterpret_cast<int*>(tmem_slot + 2);  // [2]
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // ---- this CTA's unit, tensor memory and barriers, side by side
+  const int per_rank = p.Hkv * p.n_splits;
+  const int rank = static_cast<int>(blockIdx.x / static_cast<unsigned>(per_rank));
+  const int sub = static_cast<int>(blockIdx.x) - rank * per_rank;
+  const int split = sub % p.n_splits, hk = sub / p.n_splits;
+  if (warp == 0) {
+    const Unit u = find_unit(p, rank, lane);
+    if (lane == 0) {
+      sUnit[0] = u.seq;
+      sUnit[1] = u.pair;
+    }
+  } else if (warp == 1) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  } else if (warp == 2 && lane == 0) {
+    mbar_init(bar_q, 1);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&bar_k_full[s], CONV ? 4 : 1);  // e4m3: one arrival per converter warp
+      mbar_init(&bar_v_full[s], CONV ? 4 : 1);
+      mbar_init(&bar_kv_empty[s], 2);  // one arrival per MMA warp
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bar_s_full[t], 1);
+      mbar_init(&bar_s_free[t], ALIAS ? 128 : 4);
+      mbar_init(&bar_p_full[t], ALIAS ? 128 : 4);
+      mbar_init(&bar_pv_done[t], 1);
+      mbar_init(&bar_o_final[t], 1);
+      mbar_init(&bar_mma_idle[t], 1);
+    }
+    mbar_init(bar_fix, 1);
+    mbar_init(bar_q2, 4);
+    *abort_flag = 0;
+    fence_mbar_init();
+  } else if (warp == 3 && lane == 0) {
+    prefetch_tensormap(&tmQ);
+    if (!CONV) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int seq = sUnit[0];
+  if (seq < 0) {  // the grid is an upper bound on the units
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+    return;
+  }
+  if (threadIdx.x == 0 && !osum_ok) record_dev_error(&g_seq_err, kDevSmSlot, 30);  // exact all the same; only the fold is skipped
+
+  // ---- the unit: two row tiles of tpt tokens each, and the key tiles [jb, jb + n_max) of the sequence
+  int tok_first;
+  const int qlen = seq_tokens(p.cu, seq, p.T, &tok_first);
+  const int kvlen = SRC == kSrcPacked ? qlen
+                                      : seq_positions(p.kv_lens, seq, static_cast<long long>(p.max_pages) << p.page_log2);
+  const int q_off = kvlen - qlen;  // position of the sequence's first new token (negative: rows that see nothing)
+  const int ta = sUnit[1] * 2 * p.tpt, tb = ta + p.tpt;  // first token of each row tile
+  auto tile_kv = [&](int t0) -> int {  // key tiles that the row tile may see
+    const int n = min(p.tpt, qlen - t0);
+    if (n <= 0 || kvlen == 0) return 0;
+    const int last = p.causal ? min(kvlen - 1, q_off + t0 + n - 1) : kvlen - 1;
+    return last < 0 ? 0 : last / BN + 1;
+  };
+  const int all0 = tile_kv(ta), all1 = tile_kv(tb), all = max(all0, all1);
+  const int jb = static_cast<int>(static_cast<long long>(all) * split / p.n_splits);
+  const int je = static_cast<int>(static_cast<long long>(all) * (split + 1) / p.n_splits);
+  const int nkv0 = min(max(all0 - jb, 0), je - jb), nkv1 = min(max(all1 - jb, 0), je - jb);
+  const int n_max = max(nkv0, nkv1);
+  const int kbase = jb * BN;         // position of the range's first key
+  const int kleft = kvlen - kbase;   // positions of the sequence from there
+  const uint32_t tmo_us = p.timeout_us;
+  const uint64_t tmo = static_cast<uint64_t>(tmo_us) * 1000ull;
+  const uint32_t a_abort = smem_u32(const_cast<int*>(abort_flag));
+  constexpr bool CONVQ = CONV && BF16;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LOW));
+    if (warp == 0 && n_max > 0) {
+      // ------------------------------------------------------------------ TMA producer
+      const uint32_t q_bytes = static_cast<uint32_t>(p.tpt) * p.G * 128u;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar_q, 2 * KSUB * q_bytes);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < KSUB; ++x)
+            tma_load_3d(sQ + t * C::QT_BYTES + x * TILE_BYTES, &tmQ, bar_q, x * 64, hk * p.G, tok_first + (t ? tb : ta));
+      }
+      if constexpr (!CONV) {
+        const int page = SRC == kSrcPages ? 1 << p.page_log2 : BN;
+        const int rows = min(page, BN);
+        const int boxes = BN / rows;
+        const int* trow = SRC == kSrcPages ? p.table + static_cast<long long>(seq) * p.max_pages : nullptr;
+        int issued = 0, skipped = -1;
+        bool fixed = false;
+        for (int j = 0; j < n_max; ++j) {
+          const int stage = j % STAGES;
+          const uint32_t round = j / STAGES;
+          const int left = kleft - j * BN;
+          const int nb = min(boxes, (left + rows - 1) / rows);
+          int pg = 0, y = 0;
+          if (SRC == kSrcPages && lane < nb) {  // page entries are fetched before the wait
+            const int pos = kbase + j * BN + lane * rows;
+            pg = page_at(trow, pos >> p.page_log2, p.n_pages);
+            y = pos & (page - 1);
+          }
+          bool ok = wait_or_abort(smem_u32(&bar_kv_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          issued = j + 1;
+          if (p.fault == 1 && blockIdx.x == 0 && j == 1) {
+            skipped = j;
+            continue;
+          }
+          const bool tail = left < BN;
+          const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
+          uint64_t* vbar = tail ? bar_fix : &bar_v_full[stage];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar_k_full[stage], bytes);
+            mbar_arrive_expect_tx(vbar, bytes);
+          }
+          __syncwarp();
+          if (lane < nb) {
+            uint8_t* dk = sK + stage * C::KV_BYTES + lane * rows * 128;
+            uint8_t* dv = sV + stage * C::KV_BYTES + lane * rows * 128;
+#pragma unroll
+            for (int x = 0; x < KSUB; ++x) {
+              if (SRC == kSrcPages) tma_load_4d(dk + x * TILE_BYTES, &tmK, &bar_k_full[stage], x * 64, y, hk, pg);
+              else tma_load_3d(dk + x * TILE_BYTES, &tmK, &bar_k_full[stage], x * 64, hk, tok_first + kbase + j * BN);
+            }
+#pragma unroll
+            for (int x = 0; x < KSUB; ++x) {
+              if (SRC == kSrcPages) tma_load_4d(dv + x * TILE_BYTES, &tmV, vbar, x * 64, y, hk, pg);
+              else tma_load_3d(dv + x * TILE_BYTES, &tmV, vbar, x * 64, hk, tok_first + kbase + j * BN);
+            }
+          }
+          __syncwarp();
+          if (tail) {  // at most the last key tile of the sequence
+            fixed = true;
+            ok = wait_or_abort(smem_u32(bar_fix), 0, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 31);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            zero_rows<KSUB>(sV + stage * C::KV_BYTES, left, lane);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_v_full[stage]);
+          }
+        }
+        // every load issued lands before the CTA exits (bounded waits; already complete on the normal path)
+        for (int j = max(0, issued - STAGES); j < issued; ++j) {
+          if (j == skipped) continue;
+          const int stage = j % STAGES;
+          mbar_wait_bounded(&bar_k_full[stage], (j / STAGES) & 1u, tmo);
+          if (kleft - j * BN >= BN) mbar_wait_bounded(&bar_v_full[stage], (j / STAGES) & 1u, tmo);
+        }
+        if (fixed) mbar_wait_bounded(bar_fix, 0, tmo);
+      }
+      mbar_wait_bounded(bar_q, 0, tmo);
+    } else if ((warp == 1 || warp == 2) && n_max > 0) {
+      // ------------------------------------------------------------------ MMA issuers
+      const int t = warp - 1;
+      const bool leader = elect_one();
+      const int nkv = t ? nkv1 : nkv0;
+      constexpr uint32_t IDESC_S = idesc_f16(MB, 0, 128, 128);
+      constexpr uint32_t IDESC_O = idesc_f16(MB, 1, 128, D);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(sQ + t * C::QT_BYTES), 16, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(sV), D == 128 ? TILE_BYTES : 1024, 1024);
+      const uint32_t col_s = tmem + (t ? C::COL_S1 : C::COL_S0);
+      const uint32_t col_p = tmem + (t ? C::COL_P1 : C::COL_P0);
+      const uint32_t col_o = tmem + (t ? C::COL_O1 : C::COL_O0);
+      auto wait_all = [&](uint64_t* bar, uint32_t parity, int code, int where) -> bool {
+        const bool w = wait_or_abort(smem_u32(bar), parity, tmo_us, a_abort, &g_seq_err, code, where);
+        return __all_sync(0xffffffffu, w);
+      };
+      auto do_s = [&](int j) {
+        const uint64_t b0 = dK + static_cast<uint32_t>(j % STAGES) * (C::KV_BYTES >> 4);
+        tc_fence_after();
+        if (leader) {
+          issue_s<D>(col_s, dQ, b0, IDESC_S);
+          tc_commit(&bar_s_full[t]);
+        }
+        __syncwarp();
+      };
+      auto do_pv = [&](int j) {
+        const uint64_t v0 = dV + static_cast<uint32_t>(j % STAGES) * (C::KV_BYTES >> 4);
+        const bool first = (j == 0) || (osum_ok && j % C::FLUSH == 0);
+        tc_fence_after();
+        if (leader) {
+          if (first) issue_o<true>(col_o, col_p, v0, IDESC_O);
+          else issue_o<false>(col_o, col_p, v0, IDESC_O);
+          tc_commit(&bar_pv_done[t]);
+          if (j == nkv - 1) tc_commit(&bar_o_final[t]);
+        }
+        __syncwarp();
+      };
+      bool ok = wait_all(CONVQ ? bar_q2 : bar_q, 0, kDevTimeoutQ, 11);
+      if (ok && nkv > 0) {
+        ok = wait_all(&bar_k_full[0], 0, kDevTimeoutKV, 12);
+        if (ok) do_s(0);
+      }
+      for (int j = 0; ok && j < n_max; ++j) {
+        const int stage = j % STAGES;
+        const int n1 = (j + 1) % STAGES;
+        const uint32_t par1 = ((j + 1) / STAGES) & 1u;
+        if (j < nkv) {
+          if (!ALIAS) {
+            if (j + 1 < nkv) {
+              ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
+              if (ok) ok = wait_all(&bar_s_free[t], j & 1u, kDevTimeoutSoftmax, 14);
+              if (ok) do_s(j + 1);
+            }
+            if (ok) ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 15);
+            if (ok) ok = wait_all(&bar_p_full[t], j & 1u, kDevTimeoutSoftmax, 16);
+            if (ok) do_pv(j);
+          } else {
+            ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 15);
+            if (ok) ok = wait_all(&bar_p_full[t], j & 1u, kDevTimeoutSoftmax, 16);
+            if (ok) do_pv(j);
+            if (ok && j + 1 < nkv) {
+              ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
+              // P_t(j) lies over S_t: S_t(j+1) is issued by this thread behind PV_t(j), and MMAs of one issuing
+              // thread run in order
+              if (ok) do_s(j + 1);
+            }
+          }
+          if (ok && leader) tc_commit(&bar_kv_empty[stage]);
+        } else {
+          // a key tile that only the other row tile sees: wait for its load, so that this release belongs to its phase
+          ok = wait_all(&bar_k_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 21);
+          if (ok) ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 22);
+          if (ok && leader) mbar_arrive(&bar_kv_empty[stage]);
+        }
+        __syncwarp();
+      }
+      if (leader) tc_commit(&bar_mma_idle[t]);
+      __syncwarp();
+      mbar_wait_bounded(&bar_mma_idle[t], 0, tmo);
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 0;" ::: "memory");
+    if (warp == 1) {
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc(tmem, TMEM_COLS);
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::HIGH));
+    // ------------------------------------------------------------------ softmax warpgroups
+    const int wg = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t colS = wg ? C::COL_S1 : C::COL_S0;
+    const uint32_t colP = wg ? C::COL_P1 : C::COL_P0;
+    const uint32_t colO = wg ? C::COL_O1 : C::COL_O0;
+    const uint32_t a_s_full = smem_u32(&bar_s_full[wg]), a_s_free = smem_u32(&bar_s_free[wg]);
+    const uint32_t a_p_full = smem_u32(&bar_p_full[wg]), a_pv_done = smem_u32(&bar_pv_done[wg]);
+    const int nkv = wg ? nkv1 : nkv0;
+    const int t0 = wg ? tb : ta;
+    const int rt = r / p.G;                     // token of this thread's row within the tile
+    const int rel = q_off + t0 - kbase;         // key position (in the range) of the tile's first token
+    const int row_lim = p.causal ? rel + rt + 1 : 0x7fffffff;
+    float sl2 = p.scale_log2;
+    float m_ref = -INFINITY, l = 0.0f, m_sum = -INFINITY;
+    int ev = -100000, ev_sum = 0;  // e4m3: exponent of the values that O (the running sum) is relative to
+    bool ok = true;
+    const int SEG = osum_ok ? C::FLUSH : (1 << 30);
+    for (int j0 = 0; ok && j0 < nkv; j0 += SEG) {
+      if (j0 > 0) {
+        // fold O into the running sum, brought from its reference to the current one by an exact power of two
+        ok = wait_or_abort(a_pv_done, (j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool have = j0 > C::FLUSH;
+        float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
+        if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
+        if (C::OSUM_SMEM) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(trow + colO + c * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+            const uint32_t os = smem_u32(sOsum) + static_cast<uint32_t>(((wg * D) * 128 + r) * 4);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t a = os + static_cast<uint32_t>((c * 32 + e) * 128 * 4);
+              const float prev = have ? ld_shared_f32(a) * sc : 0.0f;
+              st_shared_f32(a, prev + __uint_as_float(o[e]));
+            }
+          }
+        } else {
+          float* og = sOsum + (wg * D) * 128 + r;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float prev[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) prev[e] = have ? __ldcg(og + (c * 32 + e) * 128) : 0.0f;
+            uint32_t o[32];
+            tmem_ld32(trow + colO + c * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) __stcg(og + (c * 32 + e) * 128, prev[e] * sc + __uint_as_float(o[e]));
+          }
+        }
+        m_sum = m_ref;
+        ev_sum = ev;
+      }
+      const int j1 = (nkv - j0 < SEG) ? nkv : j0 + SEG;
+      for (int j = j0; j < j1; ++j) {
+        ok = wait_or_abort(a_s_full, j & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (CONVQ && j == 0) sl2 = p.scale_log2 * sRow[wg * 128 + r];  // written before the queries were released
+        tc_fence_after();
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(trow + colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+        if (!ALIAS) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_a(a_s_free);  // S_t may now take S_t(j+1)
+        }
+        float x[128];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c]);
+        const int k0 = j * BN;
+        if (k0 + BN > kleft || (p.causal && k0 + BN - 1 > rel)) {
+          const int lim = min(kleft, row_lim) - k0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= lim) x[c] = -INFINITY;
+        }
+        // e4m3: each 32 keys have their own scale of scores and exponent of values
+        float slc[4], shc[4];
+        float alpha = 1.0f;
+        bool rescale = false;
+        float tmax;
+        if constexpr (CONV) {
+          const int* ex = sExp + (j % STAGES) * 8;
+          int top = -100000;
+          tmax = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // held above 0, so that a masked score times it stays -inf (scores that small are 0 either way)
+            slc[c] = fmaxf(sl2 * exp2_int_any(ex[c]), 0x1p-100f);
+            tmax = fmaxf(tmax, row_max32(x + c * 32) * slc[c]);
+            top = max(top, ex[4 + c]);
+          }
+          if (top > ev) {
+            if (ev > -100000) {
+              alpha = exp2_int(static_cast<float>(max(ev - top, -200)));
+              rescale = true;
+            }
+            ev = top;
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) shc[c] = static_cast<float>(max(ex[4 + c] - ev, -60));
+        } else {
+          tmax = row_max128(x) * sl2;
+        }
+        float al_l = 1.0f;  // what the row's sum is multiplied by (it does not depend on the values' exponent)
+        if (tmax > m_ref) {
+          const float m_new = ceilf(tmax);
+          if (m_ref != -INFINITY) {
+            al_l = exp2_int(m_ref - m_new);
+            alpha *= al_l;
+            rescale = true;
+          }
+          m_ref = m_new;
+        }
+        const float cm = 192.0f - kPShift + ((m_ref == -INFINITY) ? 0.0f : m_ref);
+        const uint32_t pbuf = trow + colP;
+        float sum;
+        if constexpr (!ALIAS) {
+          const float2 sl2v = make_float2(sl2, sl2), ncm = make_float2(-cm, -cm);
+          float2 rs2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          uint32_t pk[64];
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float2 pp = exp_pair(x[2 * c], x[2 * c + 1], sl2v, ncm);
+            rs2[c & 1] = __fadd2_rn(rs2[c & 1], pp);
+            pk[c] = pack2(pp.x, pp.y, MB);
+          }
+          if (j > 0) {
+            ok = wait_or_abort(a_pv_done, (j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          tmem_st32(pbuf, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+          tmem_st32(pbuf + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+          sum = (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
+        } else {
+          // P over S: S_t(j) is complete, and its commit covers every earlier MMA of the issuing thread, PV_t(j-1)
+          // included
+          sum = 0.0f;
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) {
+            const float s1 = CONV ? slc[c4] : sl2;
+            const float c1 = CONV ? cm - shc[c4] : cm;
+            const float2 sl2v = make_float2(s1, s1), ncm = make_float2(-c1, -c1);
+            float2 rs2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            uint32_t hi[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int c = c4 * 16 + e;
+              const float2 pp = exp_pair(x[2 * c], x[2 * c + 1], sl2v, ncm);
+              rs2[e & 1] = __fadd2_rn(rs2[e & 1], pp);
+              hi[e] = pack2(pp.x, pp.y, MB);
+            }
+            tmem_st16(pbuf + c4 * 16, hi);
+            const float part = (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
+            sum += CONV ? part * exp2_int_any(static_cast<int>(-shc[c4])) : part;
+          }
+        }
+        l = l * al_l + sum;
+        if (__any_sync(0xffffffffu, rescale) && j > 0) {
+          // O takes the new reference (the running sum keeps its own)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(trow + colO + c * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(trow + colO + c * 32, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        if (ALIAS) {
+          mbar_arrive_a(a_p_full);
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_a(a_p_full);
+        }
+      }
+    }
+
+    // ---------------------------------------------------------------- epilogue
+    if (ok && nkv > 0) {
+      ok = wait_or_abort(smem_u32(&bar_o_final[wg]), 0, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 20);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    // a row with a NaN score has l = NaN and passes it on; an empty one is 0 / -inf
+    const bool has = (nkv > 0) && !(l <= 0.0f);
+    float inv_l = has ? 1.0f / l : 0.0f;
+    const float lse2 = has ? m_ref - kPShift + log2f(l) : -INFINITY;
+    if (CONV) inv_l *= has ? exp2_int_any(min(max(ev, -126), 127)) : 1.0f;
+    const int tok = t0 + rt;
+    const bool write = ok && rt < p.tpt && tok < qlen;
+    const int hq = hk * p.G + (r - rt * p.G);
+    const long long row = static_cast<long long>(tok_first + tok) * p.Hq + hq;
+    const long long prow = static_cast<long long>(split) * p.T * p.Hq + row;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      if (ok && nkv > 0) {
+        tmem_ld32(trow + colO + c * 32, o);
+        tmem_wait_ld();
+        reg_fence32(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      float v[32];
+      if (osum_ok && nkv > C::FLUSH) {
+        const float* os = sOsum + (wg * D + c * 32) * 128 + r;
+        float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
+        if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
+        float prev[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) prev[e] = C::OSUM_SMEM ? os[e * 128] : __ldcg(os + e * 128);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = (prev[e] * sc + __uint_as_float(o[e])) * inv_l;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = has ? __uint_as_float(o[e]) * inv_l : 0.0f;
+      }
+      if (write) {
+        if (p.n_splits == 1) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c * 32);
+#pragma unroll
+          for (int q8 = 0; q8 < 4; ++q8) {
+            uint4 w;
+            w.x = pack2(v[8 * q8 + 0], v[8 * q8 + 1], BF16);
+            w.y = pack2(v[8 * q8 + 2], v[8 * q8 + 3], BF16);
+            w.z = pack2(v[8 * q8 + 4], v[8 * q8 + 5], BF16);
+            w.w = pack2(v[8 * q8 + 6], v[8 * q8 + 7], BF16);
+            dst[q8] = w;
+          }
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+          for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+        }
+      }
+    }
+    if (write) {
+      if (p.n_splits > 1) p.part_l[prow] = lse2;
+      else if (p.lse) p.lse[static_cast<long long>(hq) * p.T + tok_first + tok] = lse2 * 0.69314718055994531f;
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 0;" ::: "memory");
+  } else {
+    // ------------------------------------------------------------------ e4m3 converters
+    if constexpr (CONV) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CVT));
+      const int w = warp - 12;
+      bool ok = true;
+      if (CONVQ && n_max > 0) {
+        // queries in place: this thread's row of each tile, brought to fp16 relative to its largest power of two
+        ok = wait_or_abort(smem_u32(bar_q), 0, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 32);
+        ok = __all_sync(0xffffffffu, ok);
+        const int r = w * 32 + lane;
+        for (int t = 0; ok && t < 2; ++t) {
+          uint8_t* q = sQ + t * C::QT_BYTES + r * 128;
+          float amax = 0.0f;
+          for (int i = 0; i < 8 * KSUB; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
+            const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float2 f = unpack16(ws[u], 1);
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+          const float inv = pow2i(-e);
+          sRow[t * 128 + r] = pow2i(e);
+          for (int i = 0; i < 8 * KSUB; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
+            const uint4 v = *at;
+            uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float2 f = unpack16(ws[u], 1);
+              ws[u] = pack16(f.x * inv, f.y * inv, 0);
+            }
+            *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar_q2);
+      }
+      // K and V tiles: this warp's 32 keys; a 16-byte piece of a code vector per lane and step
+      constexpr int LPR = D / 16;        // lanes of a row
+      constexpr int RPS = 32 / LPR;      // rows of a step
+      constexpr int NST = 32 / RPS;      // steps
+      const int* trow = p.table + static_cast<long long>(seq) * p.max_pages;
+      const int page_mask = (1 << p.page_log2) - 1;
+      auto row_of = [&](int j) -> long long {  // lane's key row of tile j as a vector index of its head, -1 past the end
+        const int k = j * BN + w * 32 + lane;
+        if (j >= n_max || k >= kleft) return -1;
+        const int pos = kbase + k;
+        const int pg = page_at(trow, pos >> p.page_log2, p.n_pages);
+        return ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + (pos & page_mask);
+      };
+      auto fetch = [&](const uint8_t* cache, long long vec, uint4 (&raw)[NST]) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+          const long long v = __shfl_sync(0xffffffffu, vec, i * RPS + lane / LPR);
+          raw[i] = v < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(cache + v * D) + lane % LPR);
+        }
+      };
+      auto store = [&](uint8_t* tile, const uint4 (&raw)[NST], int exps, int ref) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) {
+          const int rr = i * RPS + lane / LPR;
+          const int e = __shfl_sync(0xffffffffu, exps, rr) - ref;  // <= 0
+          const __half f = e < -24 ? __ushort_as_half(0) : __ushort_as_half(e >= -14 ? static_cast<unsigned short>((e + 15) << 10)
+                                                                                     : static_cast<unsigned short>(1 << (e + 24)));
+          const __half2 f2 = __halves2half2(f, f);
+          const int row = w * 32 + rr;
+          const uint32_t cw[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t a = e4m3x2_to_f16x2(cw[u] & 0xffffu), b = e4m3x2_to_f16x2(cw[u] >> 16);
+            __half2 ha = __hmul2(*reinterpret_cast<__half2*>(&a), f2), hb = __hmul2(*reinterpret_cast<__half2*>(&b), f2);
+            h[2 * u] = *reinterpret_cast<uint32_t*>(&ha);
+            h[2 * u + 1] = *reinterpret_cast<uint32_t*>(&hb);
+          }
+          const int c0 = 2 * (lane % LPR);  // 16 features = two 16-byte pieces of the fp16 row
+          uint8_t* dst = tile + (c0 >> 3) * TILE_BYTES + row * 128;
+          *reinterpret_cast<uint4*>(dst + (((c0 & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + ((((c0 + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      };
+      long long vec = row_of(0), next = row_of(1);
+      uint4 rk[NST], rv[NST];
+      int ek = -100000, evv = -100000;
+      auto fetch_tile = [&]() {
+        ek = vec < 0 ? -100000 : static_cast<int>(__ldg(p.k_scale + vec)) - 127;
+        evv = vec < 0 ? -100000 : static_cast<int>(__ldg(p.v_scale + vec)) - 127;
+        fetch(p.k_cache, vec, rk);
+        fetch(p.v_cache, vec, rv);
+      };
+      if (n_max > 0 && ok) fetch_tile();
+      for (int j = 0; ok && j < n_max; ++j) {
+        const int stage = j % STAGES;
+        ok = wait_or_abort(smem_u32(&bar_kv_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (p.fault == 1 && blockIdx.x == 0 && j == 1) break;  // test hook: the tile never arrives
+        const int kref = __reduce_max_sync(0xffffffffu, ek), vref = __reduce_max_sync(0xffffffffu, evv);
+        if (lane == 0) {
+          sExp[stage * 8 + w] = kref < -1000 ? 0 : kref;
+          sExp[stage * 8 + 4 + w] = vref;
+        }
+        store(sK + stage * C::KV_BYTES, rk, ek, kref);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_k_full[stage]);
+        store(sV + stage * C::KV_BYTES, rv, evv, vref);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_v_full[stage]);
+        vec = next;
+        next = row_of(j + 2);
+        if (j + 1 < n_max) fetch_tile();
+      }
+    }
+    tc_fence_before();
+    asm volatile("bar.sync 0;" ::: "memory");
+  }
+}
+
+// Joins the partials of n_splits ranges: M = max_k lse_k, out = sum_k 2^(lse_k - lse) O_k in the order of the ranges.
+template <int D, int BF16>
+__global__ void __launch_bounds__(256) seq_combine_kernel(const SeqParams p) {
+  constexpr int TPR = D / 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long row = e / TPR, rows = static_cast<long long>(p.T) * p.Hq;
+  const int c = static_cast<int>(e % TPR);
+  if (row >= rows) return;
+  const int tok = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - static_cast<long long>(tok) * p.Hq);
+  if (tok < cu_at(p.cu, 0, p.T) || tok >= cu_at(p.cu, p.n_seqs, p.T)) return;
+  float M = -INFINITY;
+  for (int k = 0; k < p.n_splits; ++k) M = fmaxf(M, __ldg(p.part_l + k * rows + row));
+  float L = 0.0f;
+  float4 a = make_float4(0, 0, 0, 0);
+  for (int k = 0; k < p.n_splits; ++k) {
+    const float lk = __ldg(p.part_l + k * rows + row);
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p.part_o) + (k * rows + row) * TPR + c);
+    if (lk == -INFINITY) continue;
+    const float w = exp2f(lk - M);
+    L += w;
+    a.x = fmaf(w, b.x, a.x);
+    a.y = fmaf(w, b.y, a.y);
+    a.z = fmaf(w, b.z, a.z);
+    a.w = fmaf(w, b.w, a.w);
+  }
+  const bool has = !(L <= 0.0f);
+  const float inv = has ? 1.0f / L : 0.0f;
+  reinterpret_cast<uint2*>(p.out)[row * TPR + c] = make_uint2(pack2(a.x * inv, a.y * inv, BF16), pack2(a.z * inv, a.w * inv, BF16));
+  if (p.lse && c == 0) p.lse[static_cast<long long>(hq) * p.T + tok] = has ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D, int BF16, int SRC>
+int launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const SeqParams& p, long long grid,
+             cudaStream_t stream) {
+  using C = SeqCfg<D, SRC>;
+  auto kern = attn_seq_kernel<D, BF16, SRC>;
+  static PerDeviceOnce attr;
+  int dev = 0;
+  if (!attr.done(&dev)) {
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncGetAttributes(sequence attention)");
+    // setmaxnreg.inc waits for its registers: refuse to launch unless the launch holds the split
+    const int need = 128 * C::LOW + 256 * C::HIGH + (C::CONV ? 128 * C::CVT : 0);
+    if (fa.numRegs * C::NTHR < need) {
+      set_error("sequence attention kernel built with %d registers/thread; the register split needs %d", fa.numRegs,
+                (need + C::NTHR - 1) / C::NTHR);
+      return CQSA_ERR_UNSUPPORTED;
+    }
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(sequence attention smem)");
+    attr.mark(dev);
+  }
+  kern<<<static_cast<unsigned>(grid), C::NTHR, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
+  int rc = cuda_status(cudaGetLastError(), "sequence attention kernel launch");
+  if (rc != CQSA_OK || p.n_splits == 1) return rc;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.T) * p.Hq * (D / 4) + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, seq_combine_kernel<D, BF16>, p), "sequence attention joining kernel launch");
+}
+
+template <int SRC>
+int dispatch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const SeqParams& p, int d, int dtype,
+             long long grid, cudaStream_t s) {
+  if (grid > 0x7fffffffLL) {
+    set_error("problem too large for one launch (%lld units)", grid);
+    return CQSA_ERR_UNSUPPORTED;
+  }
+  const bool bf = dtype == CQSA_BF16;
+  if (d == 64) return bf ? launch_t<64, 1, SRC>(mq, mk, mv, p, grid, s) : launch_t<64, 0, SRC>(mq, mk, mv, p, grid, s);
+  return bf ? launch_t<128, 1, SRC>(mq, mk, mv, p, grid, s) : launch_t<128, 0, SRC>(mq, mk, mv, p, grid, s);
+}
+
+// Packed tokens [T, heads, d] as (feature, head, token) with boxes of 64 features, `heads_box` heads and `rows` tokens.
+int make_token_map(CUtensorMap* m, const void* base, int dtype, int d, int heads, int T, long long stride, int heads_box, int rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads_box), static_cast<cuuint32_t>(rows)};
+  return encode_tensor_map(m, dtype == CQSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base,
+                           dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// An upper bound on the pairs of row tiles of n_seqs sequences that hold T tokens together.
+long long pairs_bound(int T, int n_seqs, int tpt) { return T / (2 * tpt) + (T < n_seqs ? T : n_seqs); }
+
+// Ranges that the key tiles of a unit are cut into.
+int chunk_splits(const PagedArgs& a) {
+  const int G = a.Hq / a.Hkv, tpt = 128 / G;
+  const long long by_tokens = pairs_bound(a.T, a.n_seqs, tpt);
+  const long long by_longest = static_cast<long long>(a.n_seqs) * ((a.max_q_len + 2 * tpt - 1) / (2 * tpt));
+  const long long units = (by_tokens < by_longest ? by_tokens : by_longest) * a.Hkv;
+  const long long tiles = (a.max_kv_len + BN - 1) / BN;
+  long long s = units > 0 ? sm_count() / units : 1;
+  if (s > tiles / 4) s = tiles / 4;
+  return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
+}
+
+void fill_common(SeqParams* p, int n_seqs, int T, int Hq, int Hkv, int causal, float scale) {
+  memset(p, 0, sizeof(*p));
+  p->n_seqs = n_seqs;
+  p->T = T;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->G = Hq / Hkv;
+  p->tpt = 128 / p->G;
+  p->n_splits = 1;
+  p->causal = causal;
+  p->scale_log2 = scale * 1.4426950408889634f;
+  p->timeout_us = timeout_us();
+  p->fault = debug_fault();
+}
+
+}  // namespace
+
+size_t chunk_workspace(const PagedArgs& a) {
+  const size_t s = static_cast<size_t>(chunk_splits(a));
+  if (s == 1) return 0;
+  const size_t rows = static_cast<size_t>(a.T) * a.Hq;
+  return ((s * rows * a.d * 4 + 255) & ~size_t(255)) + s * rows * 4;
+}
+
+int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
+  SeqParams p;
+  fill_common(&p, a.n_seqs, a.T, a.Hq, a.Hkv, a.causal, a.scale);
+  p.cu = a.cu;
+  p.kv_lens = a.kv_lens;
+  p.table = a.table;
+  p.k_cache = static_cast<const uint8_t*>(a.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(a.v_cache);
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.max_pages = a.max_pages;
+  p.n_pages = a.n_pages;
+  p.page_log2 = 31 - __builtin_clz(static_cast<unsigned>(a.page));
+  p.n_splits = chunk_splits(a);
+  const size_t rows = static_cast<size_t>(a.T) * a.Hq;
+  p.part_o = static_cast<float*>(a.workspace);
+  p.part_l = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
+                                      ((static_cast<size_t>(p.n_splits) * rows * a.d * 4 + 255) & ~size_t(255)));
+  int rc = osum_slots(&p.osum, &p.n_osum);
+  CUtensorMap mq, mk, mv;
+  if (rc == CQSA_OK) rc = make_token_map(&mq, a.q, a.dtype, a.d, a.Hq, a.T, a.q_stride, p.G, p.tpt);
+  const int box = a.page < BN ? a.page : BN;
+  if (rc == CQSA_OK) rc = make_page_map(&mk, a.k_cache, a, box);
+  if (rc == CQSA_OK) rc = make_page_map(&mv, a.v_cache, a, box);
+  if (rc != CQSA_OK) return rc;
+  const long long grid = pairs_bound(a.T, a.n_seqs, p.tpt) * a.Hkv * p.n_splits;
+  return a.cache_dtype == CQSA_E4M3 ? dispatch<kSrcE4m3>(mq, mk, mv, p, a.d, a.dtype, grid, stream)
+                                    : dispatch<kSrcPages>(mq, mk, mv, p, a.d, a.dtype, grid, stream);
+}
+
+int launch_packed(const PackedArgs& a, cudaStream_t stream) {
+  SeqParams p;
+  fill_common(&p, a.n_seqs, a.T, a.Hq, a.Hkv, a.causal, a.scale);
+  p.cu = a.cu;
+  p.out = a.out;
+  p.lse = a.lse;
+  int rc = osum_slots(&p.osum, &p.n_osum);
+  CUtensorMap mq, mk, mv;
+  if (rc == CQSA_OK) rc = make_token_map(&mq, a.q, a.dtype, a.d, a.Hq, a.T, a.q_stride, p.G, p.tpt);
+  if (rc == CQSA_OK) rc = make_token_map(&mk, a.k, a.dtype, a.d, a.Hkv, a.T, a.k_stride, 1, BN);
+  if (rc == CQSA_OK) rc = make_token_map(&mv, a.v, a.dtype, a.d, a.Hkv, a.T, a.v_stride, 1, BN);
+  if (rc != CQSA_OK) return rc;
+  return dispatch<kSrcPacked>(mq, mk, mv, p, a.d, a.dtype, pairs_bound(a.T, a.n_seqs, p.tpt) * a.Hkv, stream);
+}
+
+DEV_ERR_READERS(seq, g_seq_err)
+
+}  // namespace cqsa

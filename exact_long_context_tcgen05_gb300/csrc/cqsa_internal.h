@@ -92,6 +92,10 @@ int launch_bwd_dvec_range(const void* out, const void* dout, float* dvec, long l
                           long long t0, int d, int dtype, cudaStream_t stream);
 int launch_bwd_cast(const float* acc, void* out, long long n, int dtype, cudaStream_t stream);
 
+// The running sums of the d = 128 forward kernels on the current device: `n` slots of 2 x 128 x 128 floats, one
+// per SM id (attn_fwd.cu).
+int osum_slots(float** slots, int* n);
+
 // LSE merge of n partials (device pointer arrays passed by value).
 int launch_merge(const float* const* O_parts, const float* const* LSE_parts, int n, void* out, float* lse,
                  long long rows, int d, int out_dtype, cudaStream_t stream);
@@ -138,6 +142,20 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream);
 // Chunks of new tokens: the tensor-core kernel of attn_seq.cu.
 size_t chunk_workspace(const PagedArgs& a);
 int launch_chunk(const PagedArgs& a, cudaStream_t stream);
+
+// Whole prompts packed end to end (attn_seq.cu; backward: attn_bwd.cu).
+struct PackedArgs {
+  const void* q;        // [T, Hq, d], `*_stride` elements from token to token
+  const void* k;        // [T, Hkv, d]
+  const void* v;
+  void* out;            // [T, Hq, d]
+  float* lse;           // [Hq, T] or null
+  const int* cu;
+  long long q_stride, k_stride, v_stride;
+  int n_seqs, T, Hq, Hkv, d, causal, dtype;
+  float scale;          // resolved
+};
+int launch_packed(const PackedArgs& a, cudaStream_t stream);
 
 // Tensor maps (seq_api.cu). `strides` are bytes of dimensions 1 and up.
 int encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,

@@ -191,6 +191,41 @@ using namespace cqsa;
 
 extern "C" {
 
+int cqsa_attn_packed_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                         long long v_stride, void* out, float* lse, const int* cu_seqlens, int n_seqs, int T, int Hq, int Hkv,
+                         int d, int causal, float scale, int dtype, cudaStream_t stream) {
+  set_error("%s", "");
+  int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
+  if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
+  if (rc == CQSA_OK) rc = resolve_stride(&k_stride, Hkv, d, "k");
+  if (rc == CQSA_OK) rc = resolve_stride(&v_stride, Hkv, d, "v");
+  if (rc != CQSA_OK) return rc;
+  if (!cu_seqlens || !aligned(cu_seqlens, 4)) return invalid("cu_seqlens must be a non-null 4-byte aligned device pointer");
+  if (T == 0) return CQSA_OK;
+  if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)))
+    return invalid("q, k, v and out must be non-null 16-byte aligned device pointers (lse 4-byte)");
+  PackedArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.cu = cu_seqlens;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.n_seqs = n_seqs;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.causal = causal != 0;
+  a.dtype = dtype;
+  a.scale = resolve_scale(scale, d);
+  return launch_packed(a, stream);
+}
+
 int cqsa_kv_cache_write(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache, void* v_cache,
                         unsigned char* k_scale, unsigned char* v_scale, const int* block_table, int max_pages,
                         const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int Hkv, int d, int page_size,

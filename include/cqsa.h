@@ -366,6 +366,13 @@ int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, vo
  * need a workspace each (a captured graph keeps the one it was captured with).
  * ------------------------------------------------------------------------------------------------ */
 
+/* Attention of whole prompts: q device [T, Hq, d], k, v device [T, Hkv, d], out device [T, Hq, d] contiguous; a token sees
+ * its own sequence's tokens, up to itself when causal. A sequence's result does not depend on the others, whatever
+ * their values are. P is rounded to dtype for its product with V; sums are fp32. Bitwise reproducible. */
+int cqsa_attn_packed_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                         long long v_stride, void* out, float* lse, const int* cu_seqlens, int n_seqs, int T, int Hq, int Hkv,
+                         int d, int causal, float scale, int dtype, cudaStream_t stream);
+
 /* New tokens into their pages: k, v device [T, Hkv, d] of dtype. Tokens whose position is negative or beyond the
  * table, or whose page is outside the cache, are skipped. */
 int cqsa_kv_cache_write(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache, void* v_cache,
