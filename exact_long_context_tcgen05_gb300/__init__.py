@@ -25,7 +25,8 @@ EXPORTED = ("cqsa_attn_fwd", "cqsa_attn_fwd_chunk", "cqsa_merge_partials", "cqsa
             "cqsa_quorum_attn_fwd_ex", "cqsa_release_cache", "cqsa_attn_bwd_workspace_size", "cqsa_attn_bwd", "cqsa_attn_bwd_dvec",
             "cqsa_attn_bwd_chunk", "cqsa_attn_bwd_cast", "cqsa_stream_attn_bwd", "cqsa_stream_attn_bwd_ex",
             "cqsa_status_string", "cqsa_last_error", "cqsa_device_error", "cqsa_set_timeout_ms",
-            "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes", "cqsa_attn_packed_fwd", "cqsa_kv_cache_write",
+            "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes", "cqsa_attn_packed_fwd",
+            "cqsa_attn_packed_bwd_workspace_size", "cqsa_attn_packed_bwd", "cqsa_kv_cache_write",
             "cqsa_kv_cache_read", "cqsa_attn_paged_workspace_size", "cqsa_attn_paged_fwd")
 CQSA_STATIC_SCRATCH_BYTES = 32 << 20
 
@@ -92,6 +93,10 @@ def _load() -> ctypes.CDLL:
     lib.cqsa_set_stream_kv_resident_bytes.argtypes = [_ll]
     lib.cqsa_set_stream_kv_resident_bytes.restype = None
     lib.cqsa_attn_packed_fwd.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp]
+    lib.cqsa_attn_packed_bwd_workspace_size.argtypes = [_i, _i, _i]
+    lib.cqsa_attn_packed_bwd_workspace_size.restype = ctypes.c_size_t
+    lib.cqsa_attn_packed_bwd.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                                         _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp]
     lib.cqsa_kv_cache_write.argtypes = [_vp, _vp, _ll, _ll, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
                                         _i, _i, _i, _vp]
     lib.cqsa_kv_cache_read.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
@@ -306,6 +311,18 @@ def cqsa_attn_packed_fwd(q, k, v, q_stride, k_stride, v_stride, out, lse, cu_seq
                                            _stream(stream)))
 
 
+def cqsa_attn_packed_bwd_workspace_size(T, Hq, d) -> int:
+    return int(lib.cqsa_attn_packed_bwd_workspace_size(T, Hq, d))
+
+
+def cqsa_attn_packed_bwd(q, k, v, q_stride, k_stride, v_stride, out, dout, lse, dq, dk, dv, workspace, workspace_bytes,
+                         cu_seqlens, n_seqs, T, Hq, Hkv, d, causal, scale, dtype, stream=None) -> int:
+    return _check(lib.cqsa_attn_packed_bwd(_ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, _ptr(out), _ptr(dout),
+                                           _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), int(workspace_bytes),
+                                           _ptr(cu_seqlens), n_seqs, T, Hq, Hkv, d, int(bool(causal)), float(scale), dtype,
+                                           _stream(stream)))
+
+
 def cqsa_kv_cache_write(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, cu_seqlens,
                         kv_lens, n_seqs, T, Hkv, d, page_size, n_pages, dtype, cache_dtype, stream=None) -> int:
     return _check(lib.cqsa_kv_cache_write(_ptr(k), _ptr(v), k_stride, v_stride, _ptr(k_cache), _ptr(v_cache),
@@ -491,6 +508,31 @@ def attention_packed(q, k, v, cu_seqlens, *, causal=True, scale=None, return_lse
         cqsa_attn_packed_fwd(q, k, v, qs, ks, vs, out, lse, cu, n_seqs, T, Hq, Hkv, d, causal,
                              0.0 if scale is None else scale, dtype_code(q.dtype))
     return (out, lse) if return_lse else out
+
+
+def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=True, scale=None, grads=None, stream=None):
+    """Gradients (dq, dk, dv) of attention_packed from its out and lse and the upstream gradient dout; dk and dv sum over the
+    query heads of a group. Rows behind the last sequence are left as they were in `grads` (three contiguous tensors),
+    which are allocated if not given."""
+    import torch
+    with _on(q.device, stream):
+        (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
+        for name, t in (("out", out), ("dout", dout)):
+            if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device:
+                raise ValueError(f"{name} must be a {tuple(q.shape)} tensor of {q.dtype} on {q.device}")
+        if lse.shape != (Hq, T) or lse.dtype != torch.float32 or lse.device != q.device:
+            raise ValueError("lse must be a float32 tensor [Hq, T]")
+        out, dout, lse = out.contiguous(), dout.contiguous(), lse.contiguous()
+        if grads is None:
+            grads = (_out(None, q), *(torch.empty((T, Hkv, d), dtype=q.dtype, device=q.device) for _ in range(2)))
+        dq, dk, dv = grads
+        for t, h in ((dq, Hq), (dk, Hkv), (dv, Hkv)):
+            if t.shape != (T, h, d) or t.dtype != q.dtype or t.device != q.device or not t.is_contiguous():
+                raise ValueError("grads must be contiguous tensors of q's, k's and v's shapes and dtype")
+        ws = torch.empty(max(cqsa_attn_packed_bwd_workspace_size(T, Hq, d), 16), dtype=torch.uint8, device=q.device)
+        cqsa_attn_packed_bwd(q, k, v, qs, ks, vs, out, dout, lse, dq, dk, dv, ws, ws.numel(), cu, n_seqs, T, Hq, Hkv, d,
+                             causal, 0.0 if scale is None else scale, dtype_code(q.dtype))
+    return dq, dk, dv
 
 
 def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, k_scale=None, v_scale=None, stream=None):

@@ -28,6 +28,11 @@
 //                    (d = 128: two) elementwise warpgroups, joined by mbarriers. dK_j, dV_j are written once, after the last
 //                    query tile.
 //   bwd_dq_kernel    fp32 dQ accumulator -> dQ in the input dtype
+// Packed sequences with grouped heads (cqsa_attn_packed_bwd, ACCUM = 2) run the same kernel: a key tile belongs to one
+// (sequence, key head), found from cu_seqlens, and its steps walk over floor(128 / G) tokens times the G query heads that
+// share the key head, so dK_j and dV_j sum over the group in tensor memory, in a fixed order and without atomics.
+// Rows past a sequence's end (other sequences' tokens) are zeroed in shared memory after their loads: P = dS = 0
+// there would not hide a NaN. packed_prep_kernel and packed_dq_kernel take the places of the first and last.
 // P and dS enter the MMAs rounded to the input dtype; everything else is fp32. Head dimension 64 or 128
 // (d = 128 holds one Q/dO tile instead of two, and shares tensor and shared memory between phases: see
 // BwdCfg).
@@ -36,10 +41,12 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include <algorithm>
 
 #include "cqsa_internal.h"
+#include "seq_common.cuh"
 #include "sm103_ptx.cuh"
 
 #ifndef CQSA_BWD_GROUP_MB
@@ -54,7 +61,7 @@ __device__ DevErr g_bwd_err;
 constexpr int BT = 128;                         // keys per CTA tile, queries per step
 constexpr uint32_t BOX = BT * 64 * 2;           // one 128 x 64 box of 16-bit elements (16 KiB)
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int NBAR = 17;
+constexpr int NBAR = 18;
 
 // Shared- and tensor-memory layout per head dimension.
 // d = 64: K, V, a three-slot ring of Q and dO tiles (the tile two steps ahead loads while a step's
@@ -81,7 +88,7 @@ struct BwdCfg {
   // row values: per elementwise warpgroup and slot, lse2 and D of the step's 128 / NWG queries (2 KiB)
   static constexpr uint32_t OFF_BAR = OFF_ROW + 2 * 2 * 128 * 4;
   // the dynamic shared memory base is 1024-byte aligned (the kernel checks, and stops with an error if not)
-  static constexpr uint32_t SMEM_BYTES = OFF_BAR + NBAR * 8 + 16;
+  static constexpr uint32_t SMEM_BYTES = OFF_BAR + NBAR * 8 + 24;
   static constexpr uint32_t COL_S = 0, COL_DP = 128;
   static constexpr uint32_t COL_DV = 256, COL_DK = 256 + HD;
   static constexpr uint32_t COL_DQ = HD == 64 ? 384 : 128;
@@ -147,6 +154,9 @@ struct BwdParams {
   int fault;  // test hook: 2 = block 0 never loads its key/value tile (its waits must time out cleanly)
   int head_group;  // heads whose key tiles are interleaved; the rest follow group by group
   int n_kv_tiles;
+  // packed sequences (ACCUM = 2): lse holds -lse * log2 e and dvec -D, both [T, Hq]; dk, dv are [T, Hkv, d]
+  const int* cu;
+  int n_seqs, T, Hq, Hkv, G, tpt;  // tpt: tokens of a step, floor(128 / G)
 };
 
 __device__ __forceinline__ void record_bwd_error(int code, int where) {
@@ -287,8 +297,16 @@ __device__ __forceinline__ void issue_grads(uint32_t tmem, uint64_t dG, uint64_t
   }
 }
 
+// Zero rows [r0, 128) of a 128-row tile of HD / 64 boxes (a whole warp): a row is 128 bytes of each box, and the
+// swizzle only moves 16-byte pieces inside it.
+template <int HD>
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int r0, int lane) {
+  for (int x = 0; x < HD / 64; ++x)
+    for (int i = lane; i < (128 - r0) * 8; i += 32) st_shared_v4(smem_u32(tile) + x * BOX + r0 * 128 + i * 16, 0, 0, 0, 0);
+}
+
 // ACCUM = 0: monolithic (dK, dV written in the input dtype); ACCUM = 1: one chunk pair, dK and dV
-// added into fp32 accumulators.
+// added into fp32 accumulators; ACCUM = 2: packed sequences with grouped heads (written).
 template <int DT, bool CAUSAL, int ACCUM, int HD>
 __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -329,24 +347,27 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
   uint64_t* bar_dqfree = bars + 13; // [2] dQ staging slot read by its reduction
   uint64_t* bar_idle = bars + 15;   // every MMA done (commit)
   uint64_t* bar_idle3 = bars + 16;  // d = 64: every dQ product of warp 3 done (commit)
+  uint64_t* bar_fix = bars + 17;    // packed: a tile whose last rows are zeroed before it is released has landed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBAR);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_unit = reinterpret_cast<int*>(tmem_slot + 2);  // [2] packed
 
+  constexpr bool PACKED = ACCUM == 2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // Key tiles of head_group heads at a time, heaviest (first) key tiles first within a group, so that the
   // fp32 dQ accumulators and the Q / dO tiles of the heads in flight stay in L2.
   const int unit = static_cast<int>(blockIdx.x);
-  const int per_group = p.head_group * p.n_kv_tiles;
-  const int g0 = (unit / per_group) * p.head_group;
-  const int gn = min(p.head_group, p.BH - g0);
+  const int per_group = PACKED ? 1 : p.head_group * p.n_kv_tiles;
+  const int g0 = PACKED ? 0 : (unit / per_group) * p.head_group;
+  const int gn = PACKED ? 1 : min(p.head_group, p.BH - g0);
   const int ur = unit - (unit / per_group) * per_group;
   const int bh = g0 + ur % gn, jt = ur / gn;
-  const int b = bh / p.H, h = bh % p.H;
-  const int k0 = jt * BT;
-  const int Nkv = ACCUM ? p.Nkv : p.Nq;
+  const int b = PACKED ? 0 : bh / p.H, h = PACKED ? unit % p.Hkv : bh % p.H;
+  int k0 = jt * BT;  // packed: k0, Nkv, it0 and nit are set with the unit, below
+  int Nkv = ACCUM ? p.Nkv : p.Nq;
   // first query tile with a query at or after this key tile's first key (causal; absolute positions)
-  int it0 = 0;
-  if constexpr (ACCUM) {
+  int it0 = 0, seq_first = 0;
+  if constexpr (ACCUM == 1) {
     if (CAUSAL) {
       const long long first = p.kv_off + k0 - p.q_off - (BT - 1);
       it0 = first <= 0 ? 0 : static_cast<int>(first / BT + (first % BT != 0));
@@ -354,9 +375,9 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
   } else {
     it0 = CAUSAL ? jt : 0;
   }
-  const int nit = p.n_q_tiles - it0;  // >= 1 for the monolithic call
+  int nit = p.n_q_tiles - it0;  // >= 1 for the monolithic call
   const unsigned long long tmo = p.timeout_ns;
-  if constexpr (ACCUM) {
+  if constexpr (ACCUM == 1) {
     if (nit <= 0) return;  // every key of this tile lies after every query of the chunk: nothing to add
   }
 
@@ -376,6 +397,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     mbar_init(bar_ready, NWG * 128);
     mbar_init(bar_idle, 1);
     mbar_init(bar_idle3, 1);
+    if (PACKED) mbar_init(bar_fix, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -383,13 +405,147 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
+  if constexpr (PACKED) {
+    if (warp == 2) {
+      // key tiles by how many follow them in their sequence: under the causal mask, heaviest first
+      const Unit u = find_unit(p.n_seqs, unit / p.Hkv, lane, [&](int i) {
+        int first;
+        return (seq_tokens(p.cu, i, p.T, &first) + BT - 1) / BT;
+      });
+      if (lane == 0) {
+        s_unit[0] = u.seq;
+        s_unit[1] = u.place;
+      }
+    } else if (warp >= 4 && p.tpt * p.G < 128) {
+      // rows of a step that no box fills (G does not divide 128) stay zero throughout
+      for (int x = warp - 4; x < 2 * NSLOT; x += 4 * NWG) zero_tail<HD>(sQ + x * TILE, p.tpt * p.G, lane);
+      fence_proxy_async_smem();
+    }
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (PACKED) {
+    if (s_unit[0] < 0) {  // the grid is an upper bound on the key tiles
+      __syncthreads();
+      if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+      return;
+    }
+    Nkv = seq_tokens(p.cu, s_unit[0], p.T, &seq_first);
+    k0 = ((Nkv + BT - 1) / BT - 1 - s_unit[1]) * BT;
+    it0 = CAUSAL ? k0 / p.tpt : 0;
+    nit = (Nkv + p.tpt - 1) / p.tpt - it0;  // >= 1: the tile's own tokens
+  }
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TH::LOW));
-    if (warp == 0 && lane == 0) {
+    if (PACKED && warp == 0) {
+      // ---------------------------------------------------------------- TMA producer, packed sequences (whole warp)
+      if (lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+        prefetch_tensormap(&tmG);
+      }
+      int issued[3] = {0, 0, 0};
+      uint32_t fixes = 0;
+      // a tile with rows past the sequence's end lands on bar_fix; they are zeroed, then it is released
+      auto fix = [&](uint8_t* tile, int r0, uint64_t* bar) -> bool {
+        const bool w = wait_abort(bar_fix, fixes & 1u, tmo, abort_flag, kBwdTimeoutLoad, 11);
+        ++fixes;
+        if (!__all_sync(0xffffffffu, w)) return false;
+        zero_tail<HD>(tile, r0, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (bar != nullptr && lane == 0) mbar_arrive(bar);
+        return true;
+      };
+      const uint32_t q_bytes = static_cast<uint32_t>(p.tpt) * p.G * 128u * (HD / 64);
+      auto load_rows = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int it) {
+        for (int x = 0; x < HD / 64; ++x)
+          tma_load_3d(dst + x * BOX, map, bar, x * 64, h * p.G, seq_first + (it0 + it) * p.tpt);
+      };
+      const bool skip_kv = (p.fault == 2 && blockIdx.x == 0);
+      bool ok = true;
+      if (!skip_kv) {
+        const bool tail = k0 + BT > Nkv;
+        uint64_t* bar = tail ? bar_fix : bar_kv;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, 2 * TILE);
+          for (int x = 0; x < HD / 64; ++x) {
+            tma_load_3d(sK + x * BOX, &tmK, bar, x * 64, h, seq_first + k0);
+            tma_load_3d(sV + x * BOX, &tmV, bar, x * 64, h, seq_first + k0);
+          }
+        }
+        __syncwarp();
+        if (tail) {
+          ok = fix(sK, Nkv - k0, nullptr);
+          if (ok) {
+            zero_tail<HD>(sV, Nkv - k0, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_kv);
+          }
+        }
+      }
+      auto rows_left = [&](int it) -> int { return (Nkv - (it0 + it) * p.tpt) * p.G; };
+      auto load_q = [&](int it) -> bool {  // d = 64: Q and dO of a step on one barrier
+        const int slot = it % NSLOT;
+        const bool tail = rows_left(it) < p.tpt * p.G;
+        uint64_t* bar = tail ? bar_fix : &bar_q[slot];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, 2 * q_bytes);
+          load_rows(sQ + slot * TILE, &tmQ, bar, it);
+          load_rows(sG + slot * TILE, &tmG, bar, it);
+        }
+        __syncwarp();
+        if (!tail) {
+          ++issued[slot];
+          return true;
+        }
+        if (!fix(sQ + slot * TILE, rows_left(it), nullptr)) return false;
+        zero_tail<HD>(sG + slot * TILE, rows_left(it), lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_q[slot]);
+        ++issued[slot];
+        return true;
+      };
+      auto load_one = [&](int it, int which) -> bool {  // d = 128: Q (0) or dO (1) of a step on its own barrier
+        uint8_t* dst = which ? sG : sQ;
+        const bool tail = rows_left(it) < p.tpt * p.G;
+        uint64_t* bar = tail ? bar_fix : &bar_q[which];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, q_bytes);
+          load_rows(dst, which ? &tmG : &tmQ, bar, it);
+        }
+        __syncwarp();
+        if (tail && !fix(dst, rows_left(it), &bar_q[which])) return false;
+        ++issued[which];
+        return true;
+      };
+      auto freed = [&](int slot, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait_abort(&bar_qfree[slot], parity, tmo, abort_flag, kBwdTimeoutLoad, 5));
+      };
+      if constexpr (HD == 64) {
+        for (int it = 0; ok && it < nit; ++it) {
+          if (it >= NSLOT) ok = freed(it % NSLOT, static_cast<uint32_t>(((it - NSLOT) / NSLOT) & 1));
+          if (ok) ok = load_q(it);
+        }
+      } else {
+        ok = ok && load_one(0, 0) && load_one(0, 1);
+        for (int it = 0; ok && it + 1 < nit; ++it) {
+          ok = freed(1, static_cast<uint32_t>(it & 1)) && load_one(it + 1, 1) && freed(0, static_cast<uint32_t>(it & 1)) &&
+               load_one(it + 1, 0);
+        }
+      }
+      // every load issued lands before the CTA exits (bounded waits; a tile on bar_fix has been waited for, or a
+      // wait for it ran out, which is given one more limit here)
+      if (!ok && fixes > 0) mbar_wait_bounded(bar_fix, (fixes - 1) & 1u, tmo);
+      if (!skip_kv && k0 + BT <= Nkv) mbar_wait_bounded(bar_kv, 0, tmo);
+      for (int s = 0; s < 3; ++s)
+        if (issued[s] > 0) mbar_wait_bounded(&bar_q[s], static_cast<uint32_t>((issued[s] - 1) & 1), tmo);
+    } else if (!PACKED && warp == 0 && lane == 0) {
       // ---------------------------------------------------------------- TMA producer
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmK);
@@ -578,7 +734,10 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         if (!wait_abort(&bar_staged[slot], par, tmo, abort_flag, kBwdTimeoutSoftmax, 8)) break;
         const uint32_t src = smem_u32(sdQ) + static_cast<uint32_t>(slot * C::DQ_SLOT);
 #pragma unroll
-        for (int x = 0; x < HD / 32; ++x) tma_reduce_add_3d(src + x * (BT * 128), &tmDQ, 32 * x, (it0 + it) * BT, bh);
+        for (int x = 0; x < HD / 32; ++x) {
+          if constexpr (PACKED) tma_reduce_add_3d(src + x * (BT * 128), &tmDQ, 32 * x, h * p.G, seq_first + (it0 + it) * p.tpt);
+          else tma_reduce_add_3d(src + x * (BT * 128), &tmDQ, 32 * x, (it0 + it) * BT, bh);
+        }
         bulk_commit();
         bulk_wait_read_all();
         mbar_arrive(&bar_dqfree[slot]);
@@ -641,10 +800,28 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     struct RowVals {
       float l[QC / 32], d[QC / 32];
     };
+    // packed: token and place in [T, Hq] (from the step's first token) of this lane's row of each 32
+    int ptok[QC / 32], pat[QC / 32];
+    if constexpr (PACKED) {
+#pragma unroll
+      for (int k = 0; k < QC / 32; ++k) {
+        const int row = wg * QC + k * 32 + lane, t = row / p.G;
+        ptok[k] = t < p.tpt ? t : (1 << 30);
+        pat[k] = t * p.Hq + h * p.G + (row - t * p.G);
+      }
+    }
     auto row_vals = [&](int it) -> RowVals {
       RowVals v;
 #pragma unroll
       for (int k = 0; k < QC / 32; ++k) {
+        if constexpr (PACKED) {
+          const int t0 = (it0 + it) * p.tpt;
+          const bool in = it < nit && ptok[k] < Nkv - t0;
+          const long long at = static_cast<long long>(seq_first + t0) * p.Hq + pat[k];
+          v.l[k] = in ? p.lse[at] : -INFINITY;
+          v.d[k] = in ? p.dvec[at] : 0.0f;
+          continue;
+        }
         const long long i = static_cast<long long>(it0 + it) * BT + wg * QC + k * 32 + lane;
         if (it >= nit || i >= p.Nq) {
           v.l[k] = -INFINITY;  // P = 0 for rows past the end
@@ -670,6 +847,9 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     // dQ of step it (after its products completed): scaled rows into the staging slot, then hand-off
     auto stage_dq = [&](int it) -> bool {
       const int slot = HD == 64 ? (it & 1) : 0;
+      // packed: rows of the last step past the sequence's end are another sequence's; they are added zeros, even
+      // where this sequence's keys hold a NaN
+      const bool dead = PACKED && it == nit - 1 && r >= (Nkv - (it0 + it) * p.tpt) * p.G;
       if constexpr (HD == 64) {
         bool w = true;
         if (it >= 2) w = wait_abort(&bar_dqfree[slot], static_cast<uint32_t>(((it - 2) >> 1) & 1), tmo, abort_flag,
@@ -683,6 +863,10 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         tmem_ld16(trow + C::COL_DQ + wg * 16, o);
         tmem_wait_ld();
         reg_fence16(o);
+        if (dead) {
+#pragma unroll
+          for (int u = 0; u < 16; ++u) o[u] = 0u;
+        }
         const uint32_t dst = dq_row + static_cast<uint32_t>(slot * C::DQ_SLOT);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -698,6 +882,10 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         tmem_ld32(trow + C::COL_DQ + wg * (HD / 2) + c * 32, o);
         tmem_wait_ld();
         reg_fence32(o);
+        if (dead) {
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = 0u;
+        }
         const uint32_t dst = HD == 64 ? dq_row + static_cast<uint32_t>(slot * C::DQ_SLOT)
                                       : smem_u32(sdQ) + static_cast<uint32_t>((2 * wg + c) * (BT * 128) + r * 128);
 #pragma unroll
@@ -727,7 +915,12 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         // on its diagonal tile and no other masked tile.
         int dlt = 0;
         bool diag;
-        if constexpr (ACCUM) {
+        int qmin = 0;  // packed: this key hides from the rows before qmin (row q0 is token q0 / G of the step)
+        if constexpr (PACKED) {
+          dlt = (it0 + it) * p.tpt - k0;
+          diag = CAUSAL && dlt < BT - 1;
+          qmin = (r - dlt) * p.G;
+        } else if constexpr (ACCUM) {
           dlt = static_cast<int>(p.q_off - p.kv_off) + (it0 + it) * BT - k0;
           diag = CAUSAL && dlt < BT - 1;
         } else {
@@ -769,7 +962,10 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
             float p1 = ex2(arg.y);
             if (!key_ok) p0 = p1 = 0.0f;
             if (diag) {
-              if constexpr (ACCUM) {
+              if constexpr (PACKED) {
+                if (q0 < qmin) p0 = 0.0f;
+                if (q0 + 1 < qmin) p1 = 0.0f;
+              } else if constexpr (ACCUM) {
                 if (r - q0 > dlt) p0 = 0.0f;
                 if (r - q0 - 1 > dlt) p1 = 0.0f;
               } else {
@@ -880,8 +1076,9 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       tmem_wait_ld();
       reg_fence16(a);
       reg_fence16(g);
-      const long long row = static_cast<long long>(bh) * Nkv + k0 + r;
-      if (ACCUM && key_ok) {
+      const long long row = PACKED ? static_cast<long long>(seq_first + k0 + r) * p.Hkv + h
+                                   : static_cast<long long>(bh) * Nkv + k0 + r;
+      if (ACCUM == 1 && key_ok) {
         float4* dv = reinterpret_cast<float4*>(p.dv_acc + row * HD + fb);
         float4* dk = reinterpret_cast<float4*>(p.dk_acc + row * HD + fb);
 #pragma unroll
@@ -892,7 +1089,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
                                         __uint_as_float(g[4 * u + 2]) * p.scale,
                                         __uint_as_float(g[4 * u + 3]) * p.scale));
         }
-      } else if (!ACCUM && key_ok) {
+      } else if (ACCUM != 1 && key_ok) {
         uint4* dv = reinterpret_cast<uint4*>(p.dv + row * HD + fb);
         uint4* dk = reinterpret_cast<uint4*>(p.dk + row * HD + fb);
 #pragma unroll
@@ -920,7 +1117,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       tmem_wait_ld();
       reg_fence32(a);
       reg_fence32(g);
-      if (ACCUM && key_ok) {
+      if (ACCUM == 1 && key_ok) {
         const long long row = static_cast<long long>(bh) * Nkv + k0 + r;
         float4* dv = reinterpret_cast<float4*>(p.dv_acc + row * HD + fb);
         float4* dk = reinterpret_cast<float4*>(p.dk_acc + row * HD + fb);
@@ -932,8 +1129,9 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
                                         __uint_as_float(g[4 * u + 2]) * p.scale,
                                         __uint_as_float(g[4 * u + 3]) * p.scale));
         }
-      } else if (!ACCUM && key_ok) {
-        const long long row = static_cast<long long>(bh) * Nkv + k0 + r;
+      } else if (ACCUM != 1 && key_ok) {
+        const long long row = PACKED ? static_cast<long long>(seq_first + k0 + r) * p.Hkv + h
+                                     : static_cast<long long>(bh) * Nkv + k0 + r;
         uint4* dv = reinterpret_cast<uint4*>(p.dv + row * HD + fb);
         uint4* dk = reinterpret_cast<uint4*>(p.dk + row * HD + fb);
 #pragma unroll
@@ -994,6 +1192,48 @@ template <int DT>
 __global__ void __launch_bounds__(256) bwd_dq_kernel(const float4* acc, uint2* dq, long long n4) {
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4;
        i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const float4 v = acc[i];
+    dq[i] = make_uint2(pack_pair(v.x, v.y, DT), pack_pair(v.z, v.w, DT));
+  }
+}
+
+// Packed sequences: for each row (token, head) of [T, Hq], -lse * log2 e and -D_i where the main kernel reads them in
+// its row order (lse itself is [Hq, T]), and the row's zeroed dQ accumulator. d / 8 threads per row.
+template <int DT, int HD>
+__global__ void __launch_bounds__(256) packed_prep_kernel(const uint4* o, const uint4* g, const float* lse, float* nlse,
+                                                          float* ndvec, float4* dq_acc, int T, int Hq) {
+  constexpr int TPR = HD / 8;
+  const long long t = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long row = t / TPR;
+  const bool in = row < static_cast<long long>(T) * Hq;
+  float acc = 0.0f;
+  if (in) {
+    const uint4 a = __ldg(o + t), c = __ldg(g + t);
+    dq_acc[2 * t] = dq_acc[2 * t + 1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float2 x = unpack_pair(aw[u], DT), y = unpack_pair(cw[u], DT);
+      acc = fmaf(x.x, y.x, acc);
+      acc = fmaf(x.y, y.y, acc);
+    }
+  }
+#pragma unroll
+  for (int m = TPR / 2; m >= 1; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+  if (in && t % TPR == 0) {
+    const int tok = static_cast<int>(row / Hq), hq = static_cast<int>(row - static_cast<long long>(tok) * Hq);
+    nlse[row] = -(__ldg(lse + static_cast<long long>(hq) * T + tok) * LOG2E);
+    ndvec[row] = -acc;
+  }
+}
+
+// fp32 dQ accumulator -> dQ of the tokens that belong to a sequence (the others' rows are left as they were).
+template <int DT>
+__global__ void __launch_bounds__(256) packed_dq_kernel(const float4* acc, uint2* dq, const int* cu, int n_seqs, int T,
+                                                        int row4) {  // row4: four-element pieces of a token
+  const long long first = static_cast<long long>(cu_at(cu, 0, T)) * row4, last = static_cast<long long>(cu_at(cu, n_seqs, T)) * row4;
+  for (long long i = first + static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < last;
+       i += static_cast<long long>(gridDim.x) * 256) {
     const float4 v = acc[i];
     dq[i] = make_uint2(pack_pair(v.x, v.y, DT), pack_pair(v.z, v.w, DT));
   }
@@ -1143,6 +1383,79 @@ int run_main(const BwdArgs& a, float* dq_acc, const float* dvec, int accum, cuda
 }
 
 }  // namespace
+
+size_t packed_bwd_workspace(int T, int Hq, int d) {
+  const size_t rows = static_cast<size_t>(T) * Hq;
+  return ((rows * d * 4 + 255) & ~size_t(255)) + 2 * ((rows * 4 + 255) & ~size_t(255));
+}
+
+int launch_packed_bwd(const PackedArgs& a, const void* dout, void* dq, void* dk, void* dv, void* workspace, cudaStream_t stream) {
+  const size_t rows = static_cast<size_t>(a.T) * a.Hq;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* dq_acc = reinterpret_cast<float*>(ws);
+  float* nlse = reinterpret_cast<float*>(ws + ((rows * a.d * 4 + 255) & ~size_t(255)));
+  float* ndvec = nlse + ((rows * 4 + 255) & ~size_t(255)) / 4;
+  BwdParams p;
+  memset(&p, 0, sizeof(p));
+  p.G = a.Hq / a.Hkv;
+  p.tpt = 128 / p.G;
+  const bool bf = a.dtype == CQSA_BF16;
+  const CUtensorMapDataType type = bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint64_t d = static_cast<cuuint64_t>(a.d), T = static_cast<cuuint64_t>(a.T);
+  const cuuint64_t Hq = static_cast<cuuint64_t>(a.Hq), Hkv = static_cast<cuuint64_t>(a.Hkv);
+  const cuuint64_t qdims[3] = {d, Hq, T}, kdims[3] = {d, Hkv, T};
+  const cuuint64_t qs[2] = {d * 2, static_cast<cuuint64_t>(a.q_stride) * 2}, gs[2] = {d * 2, Hq * d * 2};
+  const cuuint64_t ks[2] = {d * 2, static_cast<cuuint64_t>(a.k_stride) * 2}, vs[2] = {d * 2, static_cast<cuuint64_t>(a.v_stride) * 2};
+  const cuuint64_t ds[2] = {d * 4, Hq * d * 4};
+  const cuuint32_t rbox[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.tpt)};
+  const cuuint32_t dbox[3] = {32, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.tpt)};
+  const cuuint32_t kbox[3] = {64, 1, BT};
+  CUtensorMap mq, mk, mv, mg, mdq;
+  int rc = encode_map(&mq, type, 3, a.q, qdims, qs, rbox);
+  if (rc == CQSA_OK) rc = encode_map(&mg, type, 3, dout, qdims, gs, rbox);
+  if (rc == CQSA_OK) rc = encode_map(&mk, type, 3, a.k, kdims, ks, kbox);
+  if (rc == CQSA_OK) rc = encode_map(&mv, type, 3, a.v, kdims, vs, kbox);
+  if (rc == CQSA_OK) rc = encode_map(&mdq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dq_acc, qdims, ds, dbox);
+  if (rc != CQSA_OK) return rc;
+  const long long prep = (static_cast<long long>(rows) * (a.d / 8) + 255) / 256;
+  const long long tiles = (a.T / BT + static_cast<long long>(a.T < a.n_seqs ? a.T : a.n_seqs)) * a.Hkv;  // upper bound
+  if (tiles > 0x7fffffffLL || prep > 0x7fffffffLL) {
+    set_error("problem too large for one launch");
+    return CQSA_ERR_UNSUPPORTED;
+  }
+  const uint4 *o = static_cast<const uint4*>(a.out), *g = static_cast<const uint4*>(dout);
+  auto run_prep = [&](auto kern) {
+    kern<<<static_cast<unsigned>(prep), 256, 0, stream>>>(o, g, a.lse, nlse, ndvec, reinterpret_cast<float4*>(dq_acc), a.T, a.Hq);
+  };
+  if (a.d == 128) bf ? run_prep(packed_prep_kernel<1, 128>) : run_prep(packed_prep_kernel<0, 128>);
+  else bf ? run_prep(packed_prep_kernel<1, 64>) : run_prep(packed_prep_kernel<0, 64>);
+  rc = cuda_status(cudaGetLastError(), "packed attention backward preparation launch");
+  if (rc != CQSA_OK) return rc;
+  p.lse = nlse;
+  p.dvec = ndvec;
+  p.dk = static_cast<uint16_t*>(dk);
+  p.dv = static_cast<uint16_t*>(dv);
+  p.scale = a.scale;
+  p.scale_log2 = a.scale * LOG2E;
+  p.timeout_ns = timeout_ns();
+  p.fault = debug_fault();
+  p.cu = a.cu;
+  p.n_seqs = a.n_seqs;
+  p.T = a.T;
+  p.Hq = a.Hq;
+  p.Hkv = a.Hkv;
+  p.BH = 1;  // launch_main's grid is n_kv_tiles * BH
+  const int nt = static_cast<int>(tiles);
+  rc = a.d == 128 ? dispatch_main<2, 128>(mq, mk, mv, mg, mdq, p, nt, a.dtype, a.causal, stream)
+                  : dispatch_main<2, 64>(mq, mk, mv, mg, mdq, p, nt, a.dtype, a.causal, stream);
+  if (rc != CQSA_OK) return rc;
+  const long long n4 = static_cast<long long>(rows) * a.d / 4;
+  const unsigned cblocks = static_cast<unsigned>(std::min<long long>((n4 + 255) / 256, sm_count() * 16LL));
+  const int row4 = a.Hq * a.d / 4;
+  if (bf) packed_dq_kernel<1><<<cblocks, 256, 0, stream>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint2*>(dq), a.cu, a.n_seqs, a.T, row4);
+  else packed_dq_kernel<0><<<cblocks, 256, 0, stream>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint2*>(dq), a.cu, a.n_seqs, a.T, row4);
+  return cuda_status(cudaGetLastError(), "packed attention backward cast launch");
+}
 
 size_t attention_bwd_workspace(int B, int H, int N, int d) {
   const size_t rows = static_cast<size_t>(B) * H * N;

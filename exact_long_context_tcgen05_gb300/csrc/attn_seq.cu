@@ -93,64 +93,6 @@ struct SeqParams {
   int fault;  // test hook: 1 = block 0 never loads key tile 1
 };
 
-// What a CTA works on.
-struct Unit {
-  int seq;     // -1: nothing
-  int pair;    // which pair of row tiles of the sequence
-};
-
-// Rank `rank` among the pairs of all sequences, the latest pairs of their sequences first; among pairs of one
-// place the sequences' order. One warp: count(L) = pairs at place L or later is a sum over the sequences; a
-// binary search finds the place, a walk along the sequences the one of that rank.
-__device__ __forceinline__ Unit find_unit(const SeqParams& p, int rank, int lane) {
-  const int per = 2 * p.tpt;
-  auto pairs_of = [&](int s) -> int {
-    int first;
-    return s < p.n_seqs ? (seq_tokens(p.cu, s, p.T, &first) + per - 1) / per : 0;
-  };
-  const int u0 = pairs_of(lane);  // the first 32 sequences stay in a register
-  auto count = [&](int L) -> int {
-    int c = max(0, u0 - L);
-    for (int s = 32 + lane; s < p.n_seqs; s += 32) c += max(0, pairs_of(s) - L);
-    return __reduce_add_sync(0xffffffffu, c);
-  };
-  int most = u0;
-  for (int s = 32 + lane; s < p.n_seqs; s += 32) most = max(most, pairs_of(s));
-  most = __reduce_max_sync(0xffffffffu, most);
-  Unit u;
-  u.seq = -1;
-  u.pair = 0;
-  if (rank >= count(0)) return u;
-  int lo = 0, hi = most;  // count(lo) > rank >= count(hi)
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (count(mid) > rank) lo = mid;
-    else hi = mid;
-  }
-  int k = rank - count(lo + 1);
-  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-    const bool has = (s0 == 0 ? u0 : pairs_of(s0 + lane)) > lo;
-    unsigned b = __ballot_sync(0xffffffffu, has);
-    const int n = __popc(b);
-    if (k < n) {
-      for (int i = 0; i < k; ++i) b &= b - 1;
-      u.seq = s0 + __ffs(b) - 1;
-      break;
-    }
-    k -= n;
-  }
-  u.pair = lo;
-  return u;
-}
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 template <int D>
 __device__ __forceinline__ void issue_s(uint32_t dcol, uint64_t a0, uint64_t b0, uint32_t idesc) {
 #pragma unroll
@@ -239,10 +181,14 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   const int sub = static_cast<int>(blockIdx.x) - rank * per_rank;
   const int split = sub % p.n_splits, hk = sub / p.n_splits;
   if (warp == 0) {
-    const Unit u = find_unit(p, rank, lane);
+    const int per = 2 * p.tpt;
+    const Unit u = find_unit(p.n_seqs, rank, lane, [&](int i) {
+      int first;
+      return (seq_tokens(p.cu, i, p.T, &first) + per - 1) / per;
+    });
     if (lane == 0) {
       sUnit[0] = u.seq;
-      sUnit[1] = u.pair;
+      sUnit[1] = u.place;
     }
   } else if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);

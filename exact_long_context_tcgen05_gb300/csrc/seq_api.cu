@@ -162,6 +162,40 @@ int cache_args(CacheArgs* a, void* k_cache, void* v_cache, unsigned char* k_scal
   return CQSA_OK;
 }
 
+// The checks and arguments that the packed forward and backward share.
+int packed_args(PackedArgs* a, const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                long long v_stride, void* out, float* lse, const int* cu, int n_seqs, int T, int Hq, int Hkv, int d, int causal,
+                float scale, int dtype) {
+  set_error("%s", "");
+  int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
+  if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
+  if (rc == CQSA_OK) rc = resolve_stride(&k_stride, Hkv, d, "k");
+  if (rc == CQSA_OK) rc = resolve_stride(&v_stride, Hkv, d, "v");
+  if (rc != CQSA_OK) return rc;
+  if (!cu || !aligned(cu, 4)) return invalid("cu_seqlens must be a non-null 4-byte aligned device pointer");
+  if (T > 0 && (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4)))
+    return invalid("q, k, v and out must be non-null 16-byte aligned device pointers (lse 4-byte)");
+  memset(a, 0, sizeof(*a));
+  a->q = q;
+  a->k = k;
+  a->v = v;
+  a->out = out;
+  a->lse = lse;
+  a->cu = cu;
+  a->q_stride = q_stride;
+  a->k_stride = k_stride;
+  a->v_stride = v_stride;
+  a->n_seqs = n_seqs;
+  a->T = T;
+  a->Hq = Hq;
+  a->Hkv = Hkv;
+  a->d = d;
+  a->causal = causal != 0;
+  a->dtype = dtype;
+  a->scale = resolve_scale(scale, d);
+  return CQSA_OK;
+}
+
 int paged_sizes(PagedArgs* a, int n_seqs, int T, int Hq, int Hkv, int d, int page, int max_q_len, int max_kv_len,
                 int dtype, int cache_dtype) {
   memset(a, 0, sizeof(*a));
@@ -194,36 +228,35 @@ extern "C" {
 int cqsa_attn_packed_fwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
                          long long v_stride, void* out, float* lse, const int* cu_seqlens, int n_seqs, int T, int Hq, int Hkv,
                          int d, int causal, float scale, int dtype, cudaStream_t stream) {
-  set_error("%s", "");
-  int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
-  if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
-  if (rc == CQSA_OK) rc = resolve_stride(&k_stride, Hkv, d, "k");
-  if (rc == CQSA_OK) rc = resolve_stride(&v_stride, Hkv, d, "v");
-  if (rc != CQSA_OK) return rc;
-  if (!cu_seqlens || !aligned(cu_seqlens, 4)) return invalid("cu_seqlens must be a non-null 4-byte aligned device pointer");
-  if (T == 0) return CQSA_OK;
-  if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)))
-    return invalid("q, k, v and out must be non-null 16-byte aligned device pointers (lse 4-byte)");
   PackedArgs a;
-  memset(&a, 0, sizeof(a));
-  a.q = q;
-  a.k = k;
-  a.v = v;
-  a.out = out;
-  a.lse = lse;
-  a.cu = cu_seqlens;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.n_seqs = n_seqs;
-  a.T = T;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.d = d;
-  a.causal = causal != 0;
-  a.dtype = dtype;
-  a.scale = resolve_scale(scale, d);
+  const int rc = packed_args(&a, q, k, v, q_stride, k_stride, v_stride, out, lse, cu_seqlens, n_seqs, T, Hq, Hkv, d, causal,
+                             scale, dtype);
+  if (rc != CQSA_OK || T == 0) return rc;
   return launch_packed(a, stream);
+}
+
+size_t cqsa_attn_packed_bwd_workspace_size(int T, int Hq, int d) {
+  if (T < 1 || Hq < 1 || (d != 64 && d != 128) || static_cast<long long>(T) * Hq > 0x7fffffffLL) return 0;
+  return packed_bwd_workspace(T, Hq, d);
+}
+
+int cqsa_attn_packed_bwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                         long long v_stride, const void* out, const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                         void* workspace, size_t workspace_bytes, const int* cu_seqlens, int n_seqs, int T, int Hq, int Hkv,
+                         int d, int causal, float scale, int dtype, cudaStream_t stream) {
+  PackedArgs a;
+  const int rc = packed_args(&a, q, k, v, q_stride, k_stride, v_stride, const_cast<void*>(out), const_cast<float*>(lse),
+                             cu_seqlens, n_seqs, T, Hq, Hkv, d, causal, scale, dtype);
+  if (rc != CQSA_OK || T == 0) return rc;
+  if (!dout || !lse || !dq || !dk || !dv || !aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16))
+    return invalid("dout, dq, dk, dv (16-byte aligned) and lse must be non-null device pointers");
+  const size_t need = packed_bwd_workspace(T, Hq, d);
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) {
+    set_error("a 16-byte aligned workspace of the %zu bytes that cqsa_attn_packed_bwd_workspace_size reports is needed (got %zu)",
+              need, workspace ? workspace_bytes : static_cast<size_t>(0));
+    return CQSA_ERR_INVALID;
+  }
+  return launch_packed_bwd(a, dout, dq, dk, dv, workspace, stream);
 }
 
 int cqsa_kv_cache_write(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache, void* v_cache,

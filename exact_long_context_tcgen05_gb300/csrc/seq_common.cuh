@@ -48,6 +48,51 @@ __device__ __forceinline__ int seq_of_token(const int* cu, int n_seqs, int T, in
   return lo;
 }
 
+// A CTA's share of a ragged batch: piece number `place` of sequence `seq` (-1: nothing).
+struct Unit {
+  int seq, place;
+};
+
+// Rank `rank` among the pieces of all sequences (pieces(s) of sequence s), the highest places first; among the pieces of
+// one place the sequences' order. One warp: count(L) = pieces at place L or above is a sum over the
+// sequences, a binary search finds the place, a walk along the sequences the one of that rank.
+template <class F>
+__device__ __forceinline__ Unit find_unit(int n_seqs, int rank, int lane, F pieces) {
+  const int u0 = lane < n_seqs ? pieces(lane) : 0;  // the first 32 sequences stay in a register
+  auto count = [&](int L) -> int {
+    int c = max(0, u0 - L);
+    for (int s = 32 + lane; s < n_seqs; s += 32) c += max(0, pieces(s) - L);
+    return __reduce_add_sync(0xffffffffu, c);
+  };
+  int most = u0;
+  for (int s = 32 + lane; s < n_seqs; s += 32) most = max(most, pieces(s));
+  most = __reduce_max_sync(0xffffffffu, most);
+  Unit u;
+  u.seq = -1;
+  u.place = 0;
+  if (rank >= count(0)) return u;
+  int lo = 0, hi = most;  // count(lo) > rank >= count(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (count(mid) > rank) lo = mid;
+    else hi = mid;
+  }
+  int k = rank - count(lo + 1);
+  for (int s0 = 0; s0 < n_seqs; s0 += 32) {
+    const bool has = (s0 == 0 ? u0 : (s0 + lane < n_seqs ? pieces(s0 + lane) : 0)) > lo;
+    unsigned b = __ballot_sync(0xffffffffu, has);
+    const int n = __popc(b);
+    if (k < n) {
+      for (int i = 0; i < k; ++i) b &= b - 1;
+      u.seq = s0 + __ffs(b) - 1;
+      break;
+    }
+    k -= n;
+  }
+  u.place = lo;
+  return u;
+}
+
 // e4m3 with one power of two per vector: the smallest 2^e (e >= -126) under which the largest finite
 // |x| is at most 448 = 1.75 * 2^8. A power of two costs e4m3 no precision (the code is a floating-point
 // number itself) and makes the value code * 2^e exact in fp32 and, inside its range, in 16 bits; the byte

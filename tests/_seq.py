@@ -107,3 +107,47 @@ def quantise(x):
     val = torch.where(torch.isfinite(x), torch.round(y / step) * step, torch.full_like(x, math.nan))
     code = val.float().to(torch.float8_e4m3fn).view(torch.uint8)
     return code, (e[..., 0] + 127).to(torch.uint8), val * unit
+
+
+def gradients(q, k, v, out, dout, causal, scale=None):
+    """dq, dk, dv of the definition in 64 bits for one sequence ([n, heads, d]), with D from the forward's rounded `out` as the
+    kernel takes it, and for each the sums of magnitudes that check_grad's bounds scale with."""
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    sc = 1.0 / math.sqrt(d) if scale is None else scale
+    q, k, v, out, dout = (x.double() for x in (q, k, v, out, dout))
+    kk, vv = (x.repeat_interleave(hq // hkv, 1) for x in (k, v))
+    s = torch.einsum("nhd,mhd->hnm", q, kk) * sc
+    if causal:
+        s = s.masked_fill(torch.ones(n, n, dtype=torch.bool, device=q.device).triu(1)[None], -math.inf)
+    p = torch.softmax(s, -1)
+    dp = torch.einsum("nhd,mhd->hnm", dout, vv)
+    ds = p * (dp - (dout * out).sum(-1).T[:, :, None])
+
+    def group(x):
+        return x.reshape(n, hkv, hq // hkv, d).sum(2)
+
+    def three(ds, p, q, kk, dout):
+        return (torch.einsum("hnm,mhd->nhd", ds, kk) * sc, group(torch.einsum("hnm,nhd->mhd", ds, q)) * sc,
+                group(torch.einsum("hnm,nhd->mhd", p, dout)))
+
+    size = torch.einsum("nhd,mhd->hnm", dout.abs(), vv.abs()) + (dout * out).abs().sum(-1).T[:, :, None]
+    seen = torch.isfinite(s).double()
+    mags = q.abs(), kk.abs(), dout.abs()
+    return three(ds, p, q, kk, dout), tuple(zip(three(ds.abs(), p, *mags), three(p * size, 0 * p, *mags), three(seen, seen, *mags)))
+
+
+def check_grad(got, ref, mass, dtype, what=""):
+    """|got - ref| element by element, from the three sums of magnitudes that gradients() gives beside a gradient:
+    mass[0], sum |dS| |k| (or |q|; sum P |dout|): P and dS are rounded once to dtype, u each; exp of a score off by 2^-17 and an lse off
+      by 2^-16 (scores under 2^6 in fp32) move P, and dS with it, by 2^-14 relative;
+    mass[1], sum P (sum_d |dout v| + sum_d |dout out|) |k|: dP and D are sums of d products in fp32, off by at most d * 2^-23 of
+      the magnitudes they add (2^-23 a step, as the tensor core truncates), and dS = P (dP - D) may cancel to less than that;
+    mass[2], sum |k| over the visible pairs: below fp16's normal numbers P and dS are off by 2^-25 absolutely.
+    The result is rounded once: u |ref|, at least fp16's 2^-25."""
+    u, tiny = U[dtype], 2.0 ** -25 if dtype == torch.float16 else 0.0
+    d = got.shape[-1]
+    tol = 1.01 * (u * ref.abs() + (u + 2.0 ** -14) * mass[0] + d * 2.0 ** -23 * mass[1] + tiny * mass[2] + tiny) + 2.0 ** -40
+    assert torch.isfinite(got).all(), what
+    excess = ((got.double() - ref).abs() - tol).max().item()
+    assert excess <= 0, f"{what}: {excess:.3e} beyond the tolerance"

@@ -139,3 +139,129 @@ def test_a_wait_that_gives_up(cq):
     out, lse = cq.attention_packed(q, k, v, cu, return_lse=True)
     _ok(cq)
     _check(out, lse, q, k, v, [400], True)
+
+
+def _grads(cq, q, k, v, g, cu, causal, scale=None, **kw):
+    out, lse = cq.attention_packed(q, k, v, cu, causal=causal, scale=scale, return_lse=True, out=torch.zeros_like(q))
+    got = cq.attention_packed_backward(q, k, v, out, g, lse, cu, causal=causal, scale=scale, **kw)
+    _ok(cq)
+    return out, got
+
+
+def _check_grads(got, q, k, v, out, g, lens, causal, scale=None, what=""):
+    at = 0
+    for s, n in enumerate(lens):
+        if n:
+            i = slice(at, at + n)
+            ref, mass = sq.gradients(q[i], k[i], v[i], out[i], g[i], causal, scale)
+            for name, x, r, m in zip(("dq", "dk", "dv"), got, ref, mass):
+                sq.check_grad(x[i], r, m, q.dtype, f"{what} {name} of sequence {s}")
+        at += n
+
+
+@pytest.mark.parametrize("lens,hq,hkv", CASES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_backward(cq, lens, hq, hkv, d, dt):
+    dtype, total = sq.DT[dt], sum(lens) + 3
+    q, k, v = sq.normal((total, hq, d), dtype, 1), sq.normal((total, hkv, d), dtype, 2, 1.5), sq.normal((total, hkv, d), dtype, 3)
+    g = sq.normal((total, hq, d), dtype, 4)
+    for t in (q, k, v, g):
+        t[sum(lens):] = math.nan  # nobody's
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    for causal in (True, False):
+        into = tuple(torch.full_like(t, 7.0) for t in (q, k, v))
+        out, got = _grads(cq, q, k, v, g, cu, causal, grads=into)
+        _check_grads(got, q, k, v, out, g, lens, causal, what=f"causal={causal}")
+        for t in got:
+            assert (t[sum(lens):] == 7.0).all()
+
+
+def test_backward_against_differences(cq):
+    """Central differences of the loss sum(dout * out) in 64 bits, in directions drawn at random."""
+    lens, hq, hkv, d, dtype = [37, 90], 4, 2, 64, torch.float16
+    q, k, v = (sq.normal((127, h, d), dtype, i) for i, h in ((1, hq), (2, hkv), (3, hkv)))
+    g = sq.normal((127, hq, d), dtype, 4)
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    _, got = _grads(cq, q, k, v, g, cu, True)
+
+    def loss(q, k, v):
+        total, at = 0.0, 0
+        for n in lens:
+            i = slice(at, at + n)
+            total += (sq.attend(q[i], k[i], v[i], 0, True)[0] * g[i].double()).sum().item()
+            at += n
+        return total
+
+    x = [t.double() for t in (q, k, v)]
+    for which in range(3):
+        for seed in range(3):
+            w = sq.normal(x[which].shape, torch.float64, 50 + 3 * which + seed)
+            h = 1e-4
+            up, down = ([t + (h * sign * w if i == which else 0.0) for i, t in enumerate(x)] for sign in (1, -1))
+            slope = (loss(*up) - loss(*down)) / (2 * h)
+            mine = (got[which].double() * w).sum().item()
+            # every element is off by at most about 4 u of the tensor's largest, at random: the sum over N of them by
+            # 4 u sqrt(N) times that and the direction's spread of 1, taken four times
+            bound = 16 * sq.U[dtype] * got[which].abs().max().item() * math.sqrt(w.numel())
+            assert abs(mine - slope) <= bound, (which, mine, slope, bound)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_backward_sequences_do_not_meet(cq, d):
+    """NaN and infinities in one sequence do not reach the others' gradients; dk and dv repeat bit by bit."""
+    dtype, lens, hq, hkv = torch.bfloat16, [100, 333, 60], 6, 2
+    q, k, v, g = (sq.normal((sum(lens), h, d), dtype, i) for i, h in ((1, hq), (2, hkv), (3, hkv), (4, hq)))
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    out, got = _grads(cq, q, k, v, g, cu, True)
+    _, again = _grads(cq, q, k, v, g, cu, True)
+    assert torch.equal(got[1], again[1]) and torch.equal(got[2], again[2])
+    bad = [t.clone() for t in (q, k, v, g)]
+    for t in bad:
+        t[100:433] = math.nan
+    bad[2][100:433] = math.inf
+    _, got2 = _grads(cq, *bad, cu, True)
+    for a, b in zip(got[1:], got2[1:]):
+        assert torch.equal(a[:100], b[:100]) and torch.equal(a[433:], b[433:])
+    _check_grads([t[:100] for t in got2], q[:100], k[:100], v[:100], out[:100], g[:100], [100], True)
+    _check_grads([t[433:] for t in got2], q[433:], k[433:], v[433:], out[433:], g[433:], [60], True)
+
+
+def test_backward_strides_scale_stream_and_graph(cq):
+    d, dtype, lens = 64, torch.float16, [70, 200]
+    fused, g = sq.normal((270, 8, d), dtype, 4), sq.normal((270, 4, d), dtype, 5)
+    q, k, v = fused[:, :4], fused[:, 4:6], fused[:, 6:]
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = cq.attention_packed(q, k, v, cu, scale=0.2, return_lse=True, stream=side)
+    got = cq.attention_packed_backward(q, k, v, out, g, lse, cu, scale=0.2, stream=side)
+    side.synchronize()
+    _check_grads(got, q, k, v, out, g, lens, True, 0.2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = cq.attention_packed(q, k, v, cu, return_lse=True)
+        got = cq.attention_packed_backward(q, k, v, out, g, lse, cu)
+    for lens in ([270, 0], [1, 269], [135, 135]):
+        cu.copy_(torch.tensor(sq.starts(lens), dtype=torch.int32))
+        graph.replay()
+        _ok(cq)
+        _check_grads(got, q, k, v, out, g, lens, True, what=str(lens))
+
+
+def test_backward_wait_that_gives_up(cq):
+    d, dtype = 64, torch.float16
+    q, k, v = (sq.normal((400, 2, d), dtype, i) for i in range(3))
+    cu = torch.tensor([0, 400], dtype=torch.int32, device="cuda")
+    out, lse = cq.attention_packed(q, k, v, cu, return_lse=True)
+    cq.cqsa_set_timeout_ms(50)
+    try:
+        cq.cqsa_debug_set_fault(2)
+        cq.attention_packed_backward(q, k, v, out, q, lse, cu)
+        rc, code, _ = cq.cqsa_device_error()
+        assert rc == cq.CQSA_ERR_TIMEOUT and code != 0
+    finally:
+        cq.cqsa_debug_set_fault(0)
+        cq.cqsa_set_timeout_ms(0)
+    out, got = _grads(cq, q, k, v, q, cu, True)
+    _check_grads(got, q, k, v, out, q, [400], True)
