@@ -108,6 +108,13 @@ __device__ __forceinline__ uint32_t sw_off(int r, int c) {
   return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// The same for a 16-bit tile, [8 rows][half of the features][8][64 features] (make_page_map), 16-byte chunk c of the
+// whole vector.
+template <int D>
+__device__ __forceinline__ uint32_t tile16_off(int r, int c) {
+  return static_cast<uint32_t>((r >> 3) * (1024 * (D / 64)) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
 // Where a CTA's walk over its range of key tiles stands: sequence, its tiles per head, tokens and positions.
 struct Walk {
   int s, n, qlen, first, len;
@@ -253,16 +260,17 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
         for (int i = lane; i < nb; i += 32) {
           const int pos = k0 + i * rows;
           const int pg = page_at(row, pos >> p.page_log2, p.n_pages), y = pos & (page - 1);
-#pragma unroll
-          for (int x = 0; x < C::XB; ++x) {
-            const uint32_t off = static_cast<uint32_t>(x * KT + i * rows) * C::ROWB;
-            tma_load_4d(st + off, &tmK, &full[stage], x * 64, y, h, pg);
-            tma_load_4d(st + C::TILE + off, &tmV, &full[stage], x * 64, y, h, pg);
-          }
+          const uint32_t off = static_cast<uint32_t>(i * rows) * C::ROWB * C::XB;
+          const int block = pg * p.Hkv + h;
           if (E4M3) {
-            const long long at = ((static_cast<long long>(pg) * p.Hkv + h) << p.page_log2) + y;
+            tma_load_3d(st + off, &tmK, &full[stage], 0, y, block);
+            tma_load_3d(st + C::TILE + off, &tmV, &full[stage], 0, y, block);
+            const long long at = (static_cast<long long>(block) << p.page_log2) + y;
             bulk_load(st + 2 * C::TILE + i * rows, p.k_scale + at, rows, &full[stage]);
             bulk_load(st + 2 * C::TILE + 512 + i * rows, p.v_scale + at, rows, &full[stage]);
+          } else {
+            tma_load_5d(st + off, &tmK, &full[stage], 0, 0, 0, y >> 3, block);
+            tma_load_5d(st + C::TILE + off, &tmV, &full[stage], 0, 0, 0, y >> 3, block);
           }
         }
       }
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
             for (int j = 0; j < KW / 16; ++j) {
               const int r = kw0 + j * 16 + ((lane >> 4) << 3) + (lane & 7);
               uint32_t b[4];
-              ldsm4(sk + static_cast<uint32_t>((ks >> 2) * KT * 128) + sw_off<128>(r, (ks & 3) * 2 + ((lane >> 3) & 1)), b);
+              ldsm4(sk + tile16_off<D>(r, ks * 2 + ((lane >> 3) & 1)), b);
               mma16816<MB>(s[2 * j], qf[ks], b[0], b[1]);
               mma16816<MB>(s[2 * j + 1], qf[ks], b[2], b[3]);
             }
@@ -467,10 +475,10 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
         // ---- values past the sequence's end are zero, whatever the page holds there (0 * NaN is NaN)
         if (left < KW) {
           const int z0 = max(left, 0);
-          for (int i = lane; i < (KW - z0) * (C::ROWB / 16) * C::XB; i += 32) {
-            const int c = i % (C::ROWB / 16), rx = i / (C::ROWB / 16);
-            const int r = kw0 + z0 + rx % (KW - z0), x = rx / (KW - z0);
-            st_shared_zero16(sv + static_cast<uint32_t>(x * KT + r) * C::ROWB + c * 16);
+          constexpr int PIECES = C::ROWB * C::XB / 16;  // 16-byte pieces of a vector
+          for (int i = lane; i < (KW - z0) * PIECES; i += 32) {
+            const int c = i % PIECES, r = kw0 + z0 + i / PIECES;
+            st_shared_zero16(sv + (E4M3 ? sw_off<C::ROWB>(r, c) : tile16_off<D>(r, c)));
           }
           fence_async_smem();  // before the next copy into these rows
           __syncwarp();
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
             for (int c = 0; c < D / 16; ++c) {
               uint32_t b[4];
               const int r = kw0 + j * 16 + (((lane >> 3) & 1) << 3) + (lane & 7);
-              ldsm4t(sv + static_cast<uint32_t>((c >> 2) * KT * 128) + sw_off<128>(r, (c & 3) * 2 + (lane >> 4)), b);
+              ldsm4t(sv + tile16_off<D>(r, c * 2 + (lane >> 4)), b);
               mma16816<MB>(o[2 * c], pf[j], b[0], b[1]);
               mma16816<MB>(o[2 * c + 1], pf[j], b[2], b[3]);
             }

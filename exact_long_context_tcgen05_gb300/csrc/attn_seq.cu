@@ -39,7 +39,11 @@ __device__ DevErr g_seq_err;
 constexpr int BN = 128;  // keys per tile
 constexpr uint32_t TILE_BYTES = 128 * 64 * 2;  // one 128 x 64 box of 16-bit elements
 constexpr uint32_t TMEM_COLS = 512;
-constexpr float kPShift = 14.0f;  // probabilities (and their sums) are kept as 2^14 p
+// Probabilities (and their sums) are kept as 2^6 p relative to a reference that may lie up to 2^8 below a row's
+// largest score before it is raised: rows in mid-sequence then almost never rescale O (each rescale reads and writes
+// d columns of tensor memory, and the slowest of a tile's warps sets its pace), and fp16's range holds
+// 2^14 above and, with full precision, 2^-14 below.
+constexpr float kPShift = 6.0f, kTau = 8.0f;
 
 enum : int { kSrcPacked = 0, kSrcPages = 1, kSrcE4m3 = 2 };
 
@@ -49,19 +53,24 @@ struct SeqCfg {
   // P over S where tensor memory (d = 128) or registers (beside the converter warps) leave no room for both
   static constexpr bool ALIAS = D == 128 || CONV;
   static constexpr int KSUB = D / 64;
+  // K and V tiles in shared memory, in atoms of 8 keys x 64 features (1 KiB, 128-byte swizzle). A page arrives as one
+  // five-dimensional box, [8 keys][half][8][64 features]; packed tokens and converted tiles as [half][128 keys][64].
+  static constexpr bool BY8 = SRC == kSrcPages;
+  static constexpr uint32_t GROUP = BY8 ? 1024u * (D / 64) : 1024u;   // from 8 keys to the next 8
+  static constexpr uint32_t HALF = BY8 ? 1024u : TILE_BYTES;          // from features 0-63 to 64-127
   static constexpr int STAGES = D == 64 ? 4 : 2;
   static constexpr uint32_t QT_BYTES = KSUB * TILE_BYTES;
   static constexpr uint32_t KV_BYTES = KSUB * TILE_BYTES;
   static constexpr uint32_t COL_S0 = 0, COL_S1 = 128;
   static constexpr uint32_t COL_P0 = ALIAS ? 0u : 256u, COL_P1 = ALIAS ? 128u : 320u;
   static constexpr uint32_t COL_O0 = ALIAS ? 256u : 384u, COL_O1 = COL_O0 + D;
-  static constexpr int NBARS = 1 + 3 * STAGES + 2 * 5 + 2 + 2;
+  static constexpr int NBARS = 1 + 4 * STAGES + 2 * 7 + 2 + 2;
   // key tiles between folds of O into the fp32 running sum (attn_fwd.cu explains why): in shared memory
   // for d = 64, in the SM's slot of attn_fwd.cu's array for d = 128
   static constexpr int FLUSH = D == 64 ? 128 : 32;
   static constexpr bool OSUM_SMEM = D == 64;
   static constexpr uint32_t OSUM_BYTES = OSUM_SMEM ? 2u * D * 128u * 4u : 0u;
-  static constexpr uint32_t EXP_BYTES = CONV ? STAGES * 8u * 4u + 256u * 4u : 0u;
+  static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 8u * 4u + 256u * 4u : 0u;
   static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + EXP_BYTES + NBARS * 8 + 64;
   static_assert(SMEM_BYTES <= 232448, "shared memory exceeds 227 KiB");
   static_assert(COL_O1 + D <= TMEM_COLS, "tensor memory layout exceeds 512 columns");
@@ -93,20 +102,23 @@ struct SeqParams {
   int fault;  // test hook: 1 = block 0 never loads key tile 1
 };
 
-template <int D>
+// Feature steps [K0, K1) of S = Q K^T; HALF: bytes from a K tile's first 64 features to the others.
+template <int K0, int K1, uint32_t HALF>
 __device__ __forceinline__ void issue_s(uint32_t dcol, uint64_t a0, uint64_t b0, uint32_t idesc) {
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    const uint32_t off = static_cast<uint32_t>((ks >> 2) * (TILE_BYTES >> 4) + (ks & 3) * 2);
-    if (ks == 0) mma_ss_i<0>(dcol, a0 + off, b0 + off, idesc);
-    else mma_ss_i<1>(dcol, a0 + off, b0 + off, idesc);
+  for (int ks = K0; ks < K1; ++ks) {
+    const uint32_t ao = static_cast<uint32_t>((ks >> 2) * (TILE_BYTES >> 4) + (ks & 3) * 2);
+    const uint32_t bo = static_cast<uint32_t>((ks >> 2) * (HALF >> 4) + (ks & 3) * 2);
+    if (ks == 0) mma_ss_i<0>(dcol, a0 + ao, b0 + bo, idesc);
+    else mma_ss_i<1>(dcol, a0 + ao, b0 + bo, idesc);
   }
 }
-template <bool FIRST>
+// Keys [16 K0, 16 K1) of O += P V; GROUP: bytes from 8 keys of a V tile to the next 8.
+template <bool FIRST, int K0, int K1, uint32_t GROUP>
 __device__ __forceinline__ void issue_o(uint32_t ocol, uint32_t pcol, uint64_t v0, uint32_t idesc) {
 #pragma unroll
-  for (int ks = 0; ks < BN / 16; ++ks) {
-    const uint64_t bd = v0 + static_cast<uint32_t>(ks * (2048 >> 4));
+  for (int ks = K0; ks < K1; ++ks) {
+    const uint64_t bd = v0 + static_cast<uint32_t>(ks) * (GROUP >> 3);
     if (FIRST && ks == 0) mma_ts_i<0>(ocol, pcol + ks * 8, bd, idesc);
     else mma_ts_i<1>(ocol, pcol + ks * 8, bd, idesc);
   }
@@ -122,14 +134,14 @@ __device__ __forceinline__ float row_max32(const float* x) {
   return fmaxf(max3(m0, x[30], x[31]), m1);
 }
 
-// Zero rows [r0, 128) of a 128-row tile of KSUB boxes (a whole warp). A row is 128 bytes of each box, and the swizzle
-// only moves 16-byte pieces inside it.
-template <int KSUB>
+// Zero keys [r0, 128) of a K or V tile (a whole warp): a key's row is 128 bytes of each half, and the swizzle only
+// moves 16-byte pieces inside it.
+template <class C>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int lane) {
-  const int n = (128 - r0) * 8;
 #pragma unroll
-  for (int x = 0; x < KSUB; ++x)
-    for (int i = lane; i < n; i += 32) st_shared_zero16(smem_u32(tile) + x * TILE_BYTES + r0 * 128 + i * 16);
+  for (int x = 0; x < C::KSUB; ++x)
+    for (int i = r0 * 8 + lane; i < 128 * 8; i += 32)
+      st_shared_zero16(smem_u32(tile) + x * C::HALF + (i >> 6) * C::GROUP + (i & 63) * 16);
 }
 
 template <int D, int BF16, int SRC>
@@ -146,8 +158,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   uint8_t* sK = sQ + 2 * C::QT_BYTES;
   uint8_t* sV = sK + STAGES * C::KV_BYTES;
   float* sOsum = reinterpret_cast<float*>(sV + STAGES * C::KV_BYTES);
-  int* sExp = reinterpret_cast<int*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES);  // [STAGES][K 4 | V 4]
-  float* sRow = reinterpret_cast<float*>(sExp + STAGES * 8);                       // [256] factor of a row's queries
+  int* sExp = reinterpret_cast<int*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES);  // [2 * STAGES][K 4 | V 4]
+  float* sRow = reinterpret_cast<float*>(sExp + 2 * STAGES * 8);                     // [256] factor of a row's queries
   bool osum_ok = true;
   if (!C::OSUM_SMEM) {
     uint32_t smid;
@@ -159,11 +171,16 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   uint64_t* bar_q = bars;
   uint64_t* bar_k_full = bar_q + 1;
   uint64_t* bar_v_full = bar_k_full + STAGES;
-  uint64_t* bar_kv_empty = bar_v_full + STAGES;
-  uint64_t* bar_s_full = bar_kv_empty + STAGES;  // [2]
+  // P over S (two stages at d = 128): K and V of a stage are released apart, K after S, V after P V; P apart (four
+  // stages): together, after P V, on bar_v_empty
+  uint64_t* bar_k_empty = bar_v_full + STAGES;
+  uint64_t* bar_v_empty = bar_k_empty + STAGES;
+  uint64_t* bar_s_full = bar_v_empty + STAGES;   // [2]
   uint64_t* bar_s_free = bar_s_full + 2;         // [2] (P kept apart only)
   uint64_t* bar_p_full = bar_s_free + 2;         // [2]
-  uint64_t* bar_pv_done = bar_p_full + 2;        // [2]
+  uint64_t* bar_p_half = bar_p_full + 2;         // [2] P of the first 64 keys written (P over S only)
+  uint64_t* bar_turn = bar_p_half + 2;           // [2] a row tile's turn at the tensor pipe (P over S only)
+  uint64_t* bar_pv_done = bar_turn + 2;          // [2]
   uint64_t* bar_o_final = bar_pv_done + 2;       // [2]
   uint64_t* bar_mma_idle = bar_o_final + 2;      // [2]
   uint64_t* bar_fix = bar_mma_idle + 2;          // the last V tile landed (its rows past the end are zeroed then)
@@ -198,12 +215,15 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&bar_k_full[s], CONV ? 4 : 1);  // e4m3: one arrival per converter warp
       mbar_init(&bar_v_full[s], CONV ? 4 : 1);
-      mbar_init(&bar_kv_empty[s], 2);  // one arrival per MMA warp
+      mbar_init(&bar_k_empty[s], 2);  // one arrival per MMA warp
+      mbar_init(&bar_v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar_s_full[t], 1);
       mbar_init(&bar_s_free[t], ALIAS ? 128 : 4);
       mbar_init(&bar_p_full[t], ALIAS ? 128 : 4);
+      mbar_init(&bar_p_half[t], 128);
+      mbar_init(&bar_turn[t], 1);
       mbar_init(&bar_pv_done[t], 1);
       mbar_init(&bar_o_final[t], 1);
       mbar_init(&bar_mma_idle[t], 1);
@@ -274,7 +294,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         const int rows = min(page, BN);
         const int boxes = BN / rows;
         const int* trow = SRC == kSrcPages ? p.table + static_cast<long long>(seq) * p.max_pages : nullptr;
-        int issued = 0, skipped = -1;
+        int k_issued = 0, v_issued = 0, skipped = -1;
         bool fixed = false;
         for (int j = 0; j < n_max; ++j) {
           const int stage = j % STAGES;
@@ -287,33 +307,44 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             pg = page_at(trow, pos >> p.page_log2, p.n_pages);
             y = pos & (page - 1);
           }
-          bool ok = wait_or_abort(smem_u32(&bar_kv_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
+          const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
+          bool ok = wait_or_abort(smem_u32(ALIAS ? &bar_k_empty[stage] : &bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
           if (!__all_sync(0xffffffffu, ok)) break;
-          issued = j + 1;
+          k_issued = j + 1;
           if (p.fault == 1 && blockIdx.x == 0 && j == 1) {
+            v_issued = j + 1;
             skipped = j;
             continue;
           }
-          const bool tail = left < BN;
-          const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
-          uint64_t* vbar = tail ? bar_fix : &bar_v_full[stage];
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bar_k_full[stage], bytes);
-            mbar_arrive_expect_tx(vbar, bytes);
-          }
+          if (lane == 0) mbar_arrive_expect_tx(&bar_k_full[stage], bytes);
           __syncwarp();
           if (lane < nb) {
-            uint8_t* dk = sK + stage * C::KV_BYTES + lane * rows * 128;
-            uint8_t* dv = sV + stage * C::KV_BYTES + lane * rows * 128;
+            uint8_t* dk = sK + stage * C::KV_BYTES + lane * rows * 128 * KSUB;
+            if (SRC == kSrcPages) {
+              tma_load_5d(dk, &tmK, &bar_k_full[stage], 0, 0, 0, y >> 3, pg * p.Hkv + hk);
+            } else {
 #pragma unroll
-            for (int x = 0; x < KSUB; ++x) {
-              if (SRC == kSrcPages) tma_load_4d(dk + x * TILE_BYTES, &tmK, &bar_k_full[stage], x * 64, y, hk, pg);
-              else tma_load_3d(dk + x * TILE_BYTES, &tmK, &bar_k_full[stage], x * 64, hk, tok_first + kbase + j * BN);
+              for (int x = 0; x < KSUB; ++x)
+                tma_load_3d(dk + x * TILE_BYTES, &tmK, &bar_k_full[stage], x * 64, hk, tok_first + kbase + j * BN);
             }
+          }
+          if (ALIAS) {
+            ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 34);
+            if (!__all_sync(0xffffffffu, ok)) break;
+          }
+          v_issued = j + 1;
+          const bool tail = left < BN;
+          uint64_t* vbar = tail ? bar_fix : &bar_v_full[stage];
+          if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
+          __syncwarp();
+          if (lane < nb) {
+            uint8_t* dv = sV + stage * C::KV_BYTES + lane * rows * 128 * KSUB;
+            if (SRC == kSrcPages) {
+              tma_load_5d(dv, &tmV, vbar, 0, 0, 0, y >> 3, pg * p.Hkv + hk);
+            } else {
 #pragma unroll
-            for (int x = 0; x < KSUB; ++x) {
-              if (SRC == kSrcPages) tma_load_4d(dv + x * TILE_BYTES, &tmV, vbar, x * 64, y, hk, pg);
-              else tma_load_3d(dv + x * TILE_BYTES, &tmV, vbar, x * 64, hk, tok_first + kbase + j * BN);
+              for (int x = 0; x < KSUB; ++x)
+                tma_load_3d(dv + x * TILE_BYTES, &tmV, vbar, x * 64, hk, tok_first + kbase + j * BN);
             }
           }
           __syncwarp();
@@ -321,32 +352,34 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             fixed = true;
             ok = wait_or_abort(smem_u32(bar_fix), 0, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 31);
             if (!__all_sync(0xffffffffu, ok)) break;
-            zero_rows<KSUB>(sV + stage * C::KV_BYTES, left, lane);
+            zero_rows<C>(sV + stage * C::KV_BYTES, left, lane);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_v_full[stage]);
           }
         }
         // every load issued lands before the CTA exits (bounded waits; already complete on the normal path)
-        for (int j = max(0, issued - STAGES); j < issued; ++j) {
-          if (j == skipped) continue;
-          const int stage = j % STAGES;
-          mbar_wait_bounded(&bar_k_full[stage], (j / STAGES) & 1u, tmo);
-          if (kleft - j * BN >= BN) mbar_wait_bounded(&bar_v_full[stage], (j / STAGES) & 1u, tmo);
-        }
+        for (int j = max(0, k_issued - STAGES); j < k_issued; ++j)
+          if (j != skipped) mbar_wait_bounded(&bar_k_full[j % STAGES], (j / STAGES) & 1u, tmo);
+        for (int j = max(0, v_issued - STAGES); j < v_issued; ++j)
+          if (j != skipped && kleft - j * BN >= BN) mbar_wait_bounded(&bar_v_full[j % STAGES], (j / STAGES) & 1u, tmo);
         if (fixed) mbar_wait_bounded(bar_fix, 0, tmo);
       }
       mbar_wait_bounded(bar_q, 0, tmo);
     } else if ((warp == 1 || warp == 2) && n_max > 0) {
-      // ------------------------------------------------------------------ MMA issuers
+      // ------------------------------------------------------------------ MMA issuers, one per row tile
+      // P apart from S: each on its own schedule. P over S: the tiles take turns, so that a tile's P V and next S run
+      // back to back. Without turns the two tiles' groups interleave in the tensor pipe, both finish late, and both softmax
+      // warpgroups then compute at the same time (3,640 cycles a key tile at d = 128); one warp issuing for both took
+      // 3,300, of which 1,250 went into its own waits and commits.
       const int t = warp - 1;
-      const bool leader = elect_one();
       const int nkv = t ? nkv1 : nkv0;
+      const bool leader = elect_one();
       constexpr uint32_t IDESC_S = idesc_f16(MB, 0, 128, 128);
       constexpr uint32_t IDESC_O = idesc_f16(MB, 1, 128, D);
       const uint64_t dQ = smem_desc_sw128(smem_u32(sQ + t * C::QT_BYTES), 16, 1024);
-      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t dV = smem_desc_sw128(smem_u32(sV), D == 128 ? TILE_BYTES : 1024, 1024);
+      const uint64_t dK = smem_desc_sw128(smem_u32(sK), 16, C::GROUP);
+      const uint64_t dV = smem_desc_sw128(smem_u32(sV), D == 128 ? C::HALF : 1024, C::GROUP);
       const uint32_t col_s = tmem + (t ? C::COL_S1 : C::COL_S0);
       const uint32_t col_p = tmem + (t ? C::COL_P1 : C::COL_P0);
       const uint32_t col_o = tmem + (t ? C::COL_O1 : C::COL_O0);
@@ -354,69 +387,87 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         const bool w = wait_or_abort(smem_u32(bar), parity, tmo_us, a_abort, &g_seq_err, code, where);
         return __all_sync(0xffffffffu, w);
       };
-      auto do_s = [&](int j) {
+      auto do_s = [&](int j, bool pass) {
         const uint64_t b0 = dK + static_cast<uint32_t>(j % STAGES) * (C::KV_BYTES >> 4);
         tc_fence_after();
         if (leader) {
-          issue_s<D>(col_s, dQ, b0, IDESC_S);
+          issue_s<0, D / 32, C::HALF>(col_s, dQ, b0, IDESC_S);
+          if (pass) mbar_arrive(&bar_turn[t ^ 1]);  // the other tile's issuer wakes up while the rest goes in
+          issue_s<D / 32, D / 16, C::HALF>(col_s, dQ, b0, IDESC_S);
           tc_commit(&bar_s_full[t]);
+          if (ALIAS) tc_commit(&bar_k_empty[j % STAGES]);
         }
         __syncwarp();
       };
-      auto do_pv = [&](int j) {
+      // keys of half `part` (P over S: the first half's product runs while the softmax writes the second), or all (2)
+      auto do_pv = [&](int j, int part) {
         const uint64_t v0 = dV + static_cast<uint32_t>(j % STAGES) * (C::KV_BYTES >> 4);
-        const bool first = (j == 0) || (osum_ok && j % C::FLUSH == 0);
+        const bool first = (j == 0) || (osum_ok && j % C::FLUSH == 0);  // O restarts at every segment
         tc_fence_after();
         if (leader) {
-          if (first) issue_o<true>(col_o, col_p, v0, IDESC_O);
-          else issue_o<false>(col_o, col_p, v0, IDESC_O);
-          tc_commit(&bar_pv_done[t]);
-          if (j == nkv - 1) tc_commit(&bar_o_final[t]);
+          if (part == 2) {
+            if (first) issue_o<true, 0, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
+            else issue_o<false, 0, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
+          } else if (part == 0) {
+            if (first) issue_o<true, 0, 4, C::GROUP>(col_o, col_p, v0, IDESC_O);
+            else issue_o<false, 0, 4, C::GROUP>(col_o, col_p, v0, IDESC_O);
+          } else {
+            issue_o<false, 4, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
+          }
+          if (part != 0) {
+            tc_commit(&bar_pv_done[t]);
+            if (j == nkv - 1) tc_commit(&bar_o_final[t]);
+            tc_commit(&bar_v_empty[j % STAGES]);
+          }
         }
         __syncwarp();
       };
       bool ok = wait_all(CONVQ ? bar_q2 : bar_q, 0, kDevTimeoutQ, 11);
       if (ok && nkv > 0) {
         ok = wait_all(&bar_k_full[0], 0, kDevTimeoutKV, 12);
-        if (ok) do_s(0);
+        if (ok) do_s(0, false);
       }
       for (int j = 0; ok && j < n_max; ++j) {
-        const int stage = j % STAGES;
-        const int n1 = (j + 1) % STAGES;
+        const int stage = j % STAGES, n1 = (j + 1) % STAGES;
         const uint32_t par1 = ((j + 1) / STAGES) & 1u;
         if (j < nkv) {
           if (!ALIAS) {
             if (j + 1 < nkv) {
               ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
               if (ok) ok = wait_all(&bar_s_free[t], j & 1u, kDevTimeoutSoftmax, 14);
-              if (ok) do_s(j + 1);
+              if (ok) do_s(j + 1, false);
             }
             if (ok) ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 15);
             if (ok) ok = wait_all(&bar_p_full[t], j & 1u, kDevTimeoutSoftmax, 16);
-            if (ok) do_pv(j);
+            if (ok) do_pv(j, 2);
           } else {
             ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 15);
+            if (ok && j + 1 < nkv) ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
+            if (ok) ok = wait_all(&bar_p_half[t], j & 1u, kDevTimeoutSoftmax, 17);
+            if (ok) ok = wait_all(&bar_turn[t], (j & 1u) ^ (t ? 0u : 1u), kDevTimeoutMMA, 24);
+            if (ok) do_pv(j, 0);
             if (ok) ok = wait_all(&bar_p_full[t], j & 1u, kDevTimeoutSoftmax, 16);
-            if (ok) do_pv(j);
-            if (ok && j + 1 < nkv) {
-              ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
-              // P_t(j) lies over S_t: S_t(j+1) is issued by this thread behind PV_t(j), and MMAs of one issuing
-              // thread run in order
-              if (ok) do_s(j + 1);
-            }
+            if (ok) do_pv(j, 1);
+            // P_t(j) lies over S_t: MMAs of one issuing thread run in order, so S_t(j+1) follows P V's reads
+            if (ok && j + 1 < nkv) do_s(j + 1, true);
+            else if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
           }
-          if (ok && leader) tc_commit(&bar_kv_empty[stage]);
         } else {
-          // a key tile that only the other row tile sees: wait for its load, so that this release belongs to its phase
+          // a key tile that only the other row tile sees: wait for its loads, so that the releases belong to their phases
           ok = wait_all(&bar_k_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 21);
+          if (ALIAS && ok && leader) mbar_arrive(&bar_k_empty[stage]);
           if (ok) ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 22);
-          if (ok && leader) mbar_arrive(&bar_kv_empty[stage]);
+          if (ok && leader) mbar_arrive(&bar_v_empty[stage]);
+          if (ALIAS) {
+            if (ok) ok = wait_all(&bar_turn[t], (j & 1u) ^ (t ? 0u : 1u), kDevTimeoutMMA, 25);
+            if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
+          }
         }
         __syncwarp();
       }
-      if (leader) tc_commit(&bar_mma_idle[t]);
+      if (leader) tc_commit(&bar_mma_idle[warp - 1]);
       __syncwarp();
-      mbar_wait_bounded(&bar_mma_idle[t], 0, tmo);
+      mbar_wait_bounded(&bar_mma_idle[warp - 1], 0, tmo);
     }
     tc_fence_before();
     asm volatile("bar.sync 0;" ::: "memory");
@@ -528,7 +579,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         bool rescale = false;
         float tmax;
         if constexpr (CONV) {
-          const int* ex = sExp + (j % STAGES) * 8;
+          const int* ex = sExp + (j % (2 * STAGES)) * 8;
           int top = -100000;
           tmax = -INFINITY;
 #pragma unroll
@@ -551,7 +602,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           tmax = row_max128(x) * sl2;
         }
         float al_l = 1.0f;  // what the row's sum is multiplied by (it does not depend on the values' exponent)
-        if (tmax > m_ref) {
+        if (tmax > m_ref + kTau || (m_ref == -INFINITY && tmax > -INFINITY)) {
           const float m_new = ceilf(tmax);
           if (m_ref != -INFINITY) {
             al_l = exp2_int(m_ref - m_new);
@@ -560,6 +611,20 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           }
           m_ref = m_new;
         }
+        // O takes the new reference (the running sum keeps its own), once PV_t(j-1) has been accumulated
+        auto rescale_o = [&]() {
+          if (!(__any_sync(0xffffffffu, rescale) && j > 0)) return;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(trow + colO + c * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(trow + colO + c * 32, o);
+          }
+        };
         const float cm = 192.0f - kPShift + ((m_ref == -INFINITY) ? 0.0f : m_ref);
         const uint32_t pbuf = trow + colP;
         float sum;
@@ -583,10 +648,12 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           }
           tmem_st32(pbuf, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
           tmem_st32(pbuf + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+          rescale_o();
           sum = (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
         } else {
           // P over S: S_t(j) is complete, and its commit covers every earlier MMA of the issuing thread, PV_t(j-1)
           // included
+          rescale_o();
           sum = 0.0f;
 #pragma unroll
           for (int c4 = 0; c4 < 4; ++c4) {
@@ -603,24 +670,19 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
               hi[e] = pack2(pp.x, pp.y, MB);
             }
             tmem_st16(pbuf + c4 * 16, hi);
+            if (c4 == 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive_a(smem_u32(&bar_p_half[wg]));
+              // keep the second half's work behind this point (it would be interleaved with the first's)
+#pragma unroll
+              for (int e = 64; e < 128; ++e) asm volatile("" : "+f"(x[e]));
+            }
             const float part = (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
             sum += CONV ? part * exp2_int_any(static_cast<int>(-shc[c4])) : part;
           }
         }
         l = l * al_l + sum;
-        if (__any_sync(0xffffffffu, rescale) && j > 0) {
-          // O takes the new reference (the running sum keeps its own)
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(trow + colO + c * 32, o);
-            tmem_wait_ld();
-            reg_fence32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(trow + colO + c * 32, o);
-          }
-        }
         tmem_wait_st();
         tc_fence_before();
         if (ALIAS) {
@@ -796,19 +858,24 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       if (n_max > 0 && ok) fetch_tile();
       for (int j = 0; ok && j < n_max; ++j) {
         const int stage = j % STAGES;
-        ok = wait_or_abort(smem_u32(&bar_kv_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
+        ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (p.fault == 1 && blockIdx.x == 0 && j == 1) break;  // test hook: the tile never arrives
         const int kref = __reduce_max_sync(0xffffffffu, ek), vref = __reduce_max_sync(0xffffffffu, evv);
         if (lane == 0) {
-          sExp[stage * 8 + w] = kref < -1000 ? 0 : kref;
-          sExp[stage * 8 + 4 + w] = vref;
+          // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
+          int* ex = sExp + (j % (2 * STAGES)) * 8;
+          ex[w] = kref < -1000 ? 0 : kref;
+          ex[4 + w] = vref;
         }
         store(sK + stage * C::KV_BYTES, rk, ek, kref);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_k_full[stage]);
+        ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         store(sV + stage * C::KV_BYTES, rv, evv, vref);
         fence_async_smem();
         __syncwarp();

@@ -163,8 +163,9 @@ int launch_packed_bwd(const PackedArgs& a, const void* dout, void* dq, void* dk,
 // Tensor maps (seq_api.cu). `strides` are bytes of dimensions 1 and up.
 int encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
-// A cache as (feature, slot, head, page) with boxes of `rows` slots of one page: 64 features of 16-bit
-// data (128-byte swizzle), a whole vector of e4m3 (128- or 64-byte swizzle, the row's size).
+// A cache by blocks (page * Hkv + head), with boxes of `rows` slots of one block: 16-bit data as (64 features, 8 slots,
+// half of the features, 8-slot group, block), which lands as [group][half][8 slots][64 features] under the 128-byte
+// swizzle; e4m3 as (feature, slot, block), a whole vector a row (128- or 64-byte swizzle, the row's size).
 int make_page_map(CUtensorMap* m, const void* cache, const PagedArgs& a, int rows);
 
 // Copy tokens [t0, t0+n) of a [B,H,N,d] / [B,N,H,d] tensor (host or device) into a packed chunk buffer.

@@ -39,17 +39,21 @@ int encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const 
 }
 
 int make_page_map(CUtensorMap* m, const void* cache, const PagedArgs& a, int rows) {
-  const bool e4m3 = a.cache_dtype == CQSA_E4M3;
-  const cuuint64_t vec = static_cast<cuuint64_t>(a.d) * (e4m3 ? 1 : 2);
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.d), static_cast<cuuint64_t>(a.page),
-                              static_cast<cuuint64_t>(a.Hkv), static_cast<cuuint64_t>(a.n_pages)};
-  const cuuint64_t strides[3] = {vec, vec * a.page, vec * a.page * a.Hkv};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(e4m3 ? a.d : 64), static_cast<cuuint32_t>(rows), 1, 1};
-  return encode_tensor_map(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : (a.cache_dtype == CQSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16),
-                           4, cache, dims, strides, box,
-                           e4m3 && a.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint64_t blocks = static_cast<cuuint64_t>(a.n_pages) * a.Hkv;  // (page, head)
+  if (a.cache_dtype == CQSA_E4M3) {
+    const cuuint64_t vec = static_cast<cuuint64_t>(a.d);
+    const cuuint64_t dims[3] = {vec, static_cast<cuuint64_t>(a.page), blocks};
+    const cuuint64_t strides[2] = {vec, vec * a.page};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(a.d), static_cast<cuuint32_t>(rows), 1};
+    return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cache, dims, strides, box,
+                             a.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  }
+  const cuuint64_t vec = static_cast<cuuint64_t>(a.d) * 2, halves = static_cast<cuuint64_t>(a.d / 64);
+  const cuuint64_t dims[5] = {64, 8, halves, static_cast<cuuint64_t>(a.page / 8), blocks};
+  const cuuint64_t strides[4] = {vec, 128, vec * 8, vec * a.page};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(halves), static_cast<cuuint32_t>(rows / 8), 1};
+  return encode_tensor_map(m, a.cache_dtype == CQSA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           5, cache, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 unsigned timeout_us() {
@@ -107,7 +111,7 @@ int resolve_stride(long long* stride, int heads, int d, const char* name) {
   return CQSA_OK;
 }
 
-int check_cache(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale, const int* table,
+int check_cache(int Hkv, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale, const int* table,
                 int max_pages, int page, int n_pages, int dtype, int cache_dtype) {
   if (!k_cache || !v_cache || !table) return invalid("k_cache, v_cache and block_table must be non-null device pointers");
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(table, 4))
@@ -119,6 +123,10 @@ int check_cache(const void* k_cache, const void* v_cache, const void* k_scale, c
   if (n_pages < 1 || max_pages < 1) return invalid("n_pages and max_pages must be positive");
   if (static_cast<long long>(max_pages) * page > 0x7fffffffLL - 512) {
     set_error("max_pages * page_size = %lld positions are too many", static_cast<long long>(max_pages) * page);
+    return CQSA_ERR_UNSUPPORTED;
+  }
+  if (static_cast<long long>(n_pages) * Hkv > 0x7fffffffLL) {
+    set_error("n_pages * Hkv = %lld is too large (2^31 - 1 at most)", static_cast<long long>(n_pages) * Hkv);
     return CQSA_ERR_UNSUPPORTED;
   }
   if (cache_dtype == CQSA_E4M3) {
@@ -138,7 +146,7 @@ int cache_args(CacheArgs* a, void* k_cache, void* v_cache, unsigned char* k_scal
                const int* block_table, int max_pages, const int* cu, const int* kv_lens, int n_seqs, int T, int Hkv, int d,
                int page, int n_pages, int dtype, int cache_dtype) {
   int rc = check_seqs(n_seqs, T, Hkv, Hkv, d, 0.0f, dtype);
-  if (rc == CQSA_OK) rc = check_cache(k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page, n_pages, dtype, cache_dtype);
+  if (rc == CQSA_OK) rc = check_cache(Hkv, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page, n_pages, dtype, cache_dtype);
   if (rc != CQSA_OK) return rc;
   if (!cu || !kv_lens || !aligned(cu, 4) || !aligned(kv_lens, 4))
     return invalid("cu_seqlens and kv_lens must be non-null 4-byte aligned device pointers");
@@ -311,7 +319,7 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
                         void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   set_error("%s", "");
   int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
-  if (rc == CQSA_OK) rc = check_cache(k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page_size, n_pages, dtype, cache_dtype);
+  if (rc == CQSA_OK) rc = check_cache(Hkv, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page_size, n_pages, dtype, cache_dtype);
   if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
   if (rc != CQSA_OK) return rc;
   if (!cu_seqlens || !kv_lens || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
