@@ -93,7 +93,7 @@ def _load() -> ctypes.CDLL:
     lib.cqsa_set_stream_kv_resident_bytes.argtypes = [_ll]
     lib.cqsa_set_stream_kv_resident_bytes.restype = None
     lib.cqsa_attn_packed_fwd.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp]
-    lib.cqsa_attn_packed_bwd_workspace_size.argtypes = [_i, _i, _i]
+    lib.cqsa_attn_packed_bwd_workspace_size.argtypes = [_i] * 5
     lib.cqsa_attn_packed_bwd_workspace_size.restype = ctypes.c_size_t
     lib.cqsa_attn_packed_bwd.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                                          _vp, _i, _i, _i, _i, _i, _i, _f, _i, _vp]
@@ -311,8 +311,8 @@ def cqsa_attn_packed_fwd(q, k, v, q_stride, k_stride, v_stride, out, lse, cu_seq
                                            _stream(stream)))
 
 
-def cqsa_attn_packed_bwd_workspace_size(T, Hq, d) -> int:
-    return int(lib.cqsa_attn_packed_bwd_workspace_size(T, Hq, d))
+def cqsa_attn_packed_bwd_workspace_size(n_seqs, T, Hq, Hkv, d) -> int:
+    return int(lib.cqsa_attn_packed_bwd_workspace_size(n_seqs, T, Hq, Hkv, d))
 
 
 def cqsa_attn_packed_bwd(q, k, v, q_stride, k_stride, v_stride, out, dout, lse, dq, dk, dv, workspace, workspace_bytes,
@@ -420,14 +420,18 @@ def attention_backward(q, k, v, out, dout, lse, *, causal=False, scale=None, str
 
 # Sequences of different lengths: torch conveniences (checks and marshalling only). They run on the tensors' own
 # device, whichever is current, on `stream` (a torch stream or a cudaStream_t value) or that device's current
-# stream; what they allocate belongs to that stream.
+# stream; what they allocate belongs to that stream. A serving step makes one of these calls per layer, so they look at
+# each tensor once and pass addresses straight on.
 
-def _on(device, stream):
-    import contextlib
-
+def _elsewhere(device, stream):
+    """A context that makes `device` current and `stream` its current stream, or None where they already are."""
     import torch
+    here = device.index == torch.cuda.current_device()
+    if here and stream is None:
+        return None
+    import contextlib
     stack = contextlib.ExitStack()
-    if device.index != torch.cuda.current_device():
+    if not here:
         stack.enter_context(torch.cuda.device(device))
     if stream is not None:
         if isinstance(stream, int):
@@ -436,61 +440,84 @@ def _on(device, stream):
     return stack
 
 
+def _current(device):
+    """The cudaStream_t of the device's current stream."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return (raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream) or None
+
+
 def _tokens(name, t, heads, d, like):
     """A [T, heads, d] tensor of like's dtype and device, its heads dense; returns it (a copy if need be) and its token stride."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype != like.dtype or t.device != like.device:
+    if t.shape[1:] != (heads, d) or t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} must be a [T, {heads}, {d}] tensor of {like.dtype} on {like.device}")
+    if t.is_contiguous() and not t.data_ptr() & 15:
+        return t, heads * d
+    T = t.shape[0]
     s = t.stride()
-    if (s[2] != 1 or (s[1] != d and heads > 1) or s[0] < heads * d or s[0] % 8 or t.data_ptr() % 16) and t.shape[0] > 0:
-        t = t.contiguous()
-        if t.data_ptr() % 16:
-            t = t.clone()
-    return t, (t.stride(0) if t.shape[0] > 1 else 0)
+    if (s[2] != 1 or (s[1] != d and heads > 1) or s[0] < heads * d or s[0] % 8 or t.data_ptr() & 15) and T > 0:
+        t = t.clone() if t.is_contiguous() else t.contiguous()
+        return t, heads * d
+    return t, (s[0] if T > 1 else heads * d)
 
 
 def _ints(name, t, shape, device):
     import torch
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape:
+    if t.dtype != torch.int32 or t.device != device or t.shape != shape:
         raise ValueError(f"{name} must be an int32 tensor of shape {shape} on {device}")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _out(out, q):
+    import torch
+    if out is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {tuple(q.shape)} tensor of {q.dtype} on {q.device}")
+    return out
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, dtype, device):
-    """The checks that the calls on a paged cache share; returns the arguments they pass on."""
+    """The checks that the calls on a paged cache share; returns the cache's dtype code, n_seqs, max_pages, the three index
+    tensors and the scales' addresses."""
     import torch
-    if not k_cache.is_cuda or k_cache.device != device or v_cache.device != device:
+    shape, kind = k_cache.shape, k_cache.dtype
+    if device.type != "cuda" or k_cache.device != device or v_cache.device != device:
         raise ValueError("k_cache and v_cache must be CUDA tensors on the tokens' device")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != kind:
         raise ValueError("k_cache and v_cache must be tensors of one shape and dtype [n_pages, Hkv, page_size, d]")
     if not k_cache.is_contiguous() or not v_cache.is_contiguous():
         raise ValueError("k_cache and v_cache must be contiguous")
-    if k_cache.dtype in (torch.uint8, torch.float8_e4m3fn):
-        code = CQSA_E4M3
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is None or t.element_size() != 1 or t.shape != k_cache.shape[:3] or t.device != device or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous byte tensor [n_pages, Hkv, page_size] beside an e4m3 cache")
-    elif k_cache.dtype == dtype:
+    ks = vs = None
+    if kind == dtype:
         code = dtype_code(dtype)
         if k_scale is not None or v_scale is not None:
             raise ValueError("a 16-bit cache takes no scales")
+    elif kind == torch.uint8 or kind == torch.float8_e4m3fn:
+        code = CQSA_E4M3
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None or t.element_size() != 1 or t.shape != shape[:3] or t.device != device or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous byte tensor [n_pages, Hkv, page_size] beside an e4m3 cache")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     else:
-        raise ValueError(f"a cache of {k_cache.dtype} does not go with tokens of {dtype}")
-    if block_table.dim() != 2 or kv_lens.dim() != 1 or block_table.shape[0] != kv_lens.shape[0]:
+        raise ValueError(f"a cache of {kind} does not go with tokens of {dtype}")
+    table = block_table.shape
+    if len(table) != 2 or kv_lens.shape != table[:1]:
         raise ValueError("block_table must be [n_seqs, max_pages] and kv_lens [n_seqs]")
-    n_seqs, max_pages = block_table.shape
-    return (code, n_seqs, max_pages, _ints("block_table", block_table, (n_seqs, max_pages), device),
-            _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), device), _ints("kv_lens", kv_lens, (n_seqs,), device))
+    n_seqs = table[0]
+    return (code, n_seqs, table[1], _ints("block_table", block_table, table, device),
+            _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), device), _ints("kv_lens", kv_lens, (n_seqs,), device), ks, vs)
 
 
 def _packed(q, k, v, cu_seqlens):
     """The checks that the calls on packed tokens share: (q, k, v) with their strides, cu_seqlens, and the sizes."""
-    if q.dim() != 3 or k.dim() != 3 or not q.is_cuda:
+    if len(q.shape) != 3 or len(k.shape) != 3 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [T, Hq, d], k and v [T, Hkv, d]")
     T, Hq, d = q.shape
     Hkv = k.shape[1]
     if k.shape[0] != T or v.shape != k.shape:
         raise ValueError("k and v must be [T, Hkv, d] with q's T")
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+    if len(cu_seqlens.shape) != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [n_seqs + 1]")
     n_seqs = cu_seqlens.shape[0] - 1
     return (_tokens("q", q, Hq, d, q), _tokens("k", k, Hkv, d, q), _tokens("v", v, Hkv, d, q),
@@ -501,12 +528,17 @@ def attention_packed(q, k, v, cu_seqlens, *, causal=True, scale=None, return_lse
     """Attention of whole prompts packed end to end: q [T, Hq, d], k, v [T, Hkv, d], cu_seqlens int32 [n_seqs + 1] on the
     device; returns out [T, Hq, d] (and lse [Hq, T] fp32). Rows behind the last sequence are left as they were in `out`."""
     import torch
-    with _on(q.device, stream):
-        (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
-        out = _out(out, q)
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
-        cqsa_attn_packed_fwd(q, k, v, qs, ks, vs, out, lse, cu, n_seqs, T, Hq, Hkv, d, causal,
-                             0.0 if scale is None else scale, dtype_code(q.dtype))
+    (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
+    ctx = _elsewhere(q.device, stream)
+    if ctx is not None:
+        with ctx:
+            return attention_packed(q, k, v, cu, causal=causal, scale=scale, return_lse=return_lse, out=out)
+    out = _out(out, q)
+    lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
+    _check(lib.cqsa_attn_packed_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(),
+                                    lse.data_ptr() if return_lse else None, cu.data_ptr(), n_seqs, T, Hq, Hkv, d,
+                                    1 if causal else 0, 0.0 if scale is None else scale, dtype_code(q.dtype),
+                                    _current(q.device)))
     return (out, lse) if return_lse else out
 
 
@@ -515,38 +547,51 @@ def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=Tru
     query heads of a group. Rows behind the last sequence are left as they were in `grads` (three contiguous tensors),
     which are allocated if not given."""
     import torch
-    with _on(q.device, stream):
-        (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
-        for name, t in (("out", out), ("dout", dout)):
-            if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device:
-                raise ValueError(f"{name} must be a {tuple(q.shape)} tensor of {q.dtype} on {q.device}")
-        if lse.shape != (Hq, T) or lse.dtype != torch.float32 or lse.device != q.device:
-            raise ValueError("lse must be a float32 tensor [Hq, T]")
-        out, dout, lse = out.contiguous(), dout.contiguous(), lse.contiguous()
-        if grads is None:
-            grads = (_out(None, q), *(torch.empty((T, Hkv, d), dtype=q.dtype, device=q.device) for _ in range(2)))
+    (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
+    device, dtype = q.device, q.dtype
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return attention_packed_backward(q, k, v, out, dout, lse, cu, causal=causal, scale=scale, grads=grads)
+    for name, t in (("out", out), ("dout", dout)):
+        if t.shape != q.shape or t.dtype != dtype or t.device != device:
+            raise ValueError(f"{name} must be a {tuple(q.shape)} tensor of {dtype} on {device}")
+    if lse.shape != (Hq, T) or lse.dtype != torch.float32 or lse.device != device:
+        raise ValueError("lse must be a float32 tensor [Hq, T]")
+    out, dout, lse = out.contiguous(), dout.contiguous(), lse.contiguous()
+    if grads is None:
+        dq = torch.empty((T, Hq, d), dtype=dtype, device=device)
+        dk, dv = (torch.empty((T, Hkv, d), dtype=dtype, device=device) for _ in range(2))
+    else:
         dq, dk, dv = grads
         for t, h in ((dq, Hq), (dk, Hkv), (dv, Hkv)):
-            if t.shape != (T, h, d) or t.dtype != q.dtype or t.device != q.device or not t.is_contiguous():
+            if t.shape != (T, h, d) or t.dtype != dtype or t.device != device or not t.is_contiguous():
                 raise ValueError("grads must be contiguous tensors of q's, k's and v's shapes and dtype")
-        ws = torch.empty(max(cqsa_attn_packed_bwd_workspace_size(T, Hq, d), 16), dtype=torch.uint8, device=q.device)
-        cqsa_attn_packed_bwd(q, k, v, qs, ks, vs, out, dout, lse, dq, dk, dv, ws, ws.numel(), cu, n_seqs, T, Hq, Hkv, d,
-                             causal, 0.0 if scale is None else scale, dtype_code(q.dtype))
+    need = lib.cqsa_attn_packed_bwd_workspace_size(n_seqs, T, Hq, Hkv, d)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _check(lib.cqsa_attn_packed_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(), dout.data_ptr(),
+                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), need,
+                                    cu.data_ptr(), n_seqs, T, Hq, Hkv, d, 1 if causal else 0,
+                                    0.0 if scale is None else scale, dtype_code(dtype), _current(device)))
     return dq, dk, dv
 
 
 def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, k_scale=None, v_scale=None, stream=None):
     """New tokens k, v [T, Hkv, d] into their pages of the caches [n_pages, Hkv, page_size, d] (k's dtype, or
     uint8 / float8_e4m3fn codes with byte tensors k_scale, v_scale [n_pages, Hkv, page_size])."""
+    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                kv_lens, k.dtype, k.device)
     n_pages, Hkv, page, d = k_cache.shape
-    with _on(k.device, stream):
-        code, n_seqs, max_pages, table, cu, lens = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
-                                                          kv_lens, k.dtype, k.device)
-        (k, ks), (v, vs) = _tokens("k", k, Hkv, d, k), _tokens("v", v, Hkv, d, k)
-        if v.shape != k.shape:
-            raise ValueError("k and v must have one shape")
-        cqsa_kv_cache_write(k, v, ks, vs, k_cache, v_cache, k_scale, v_scale, table, max_pages, cu, lens, n_seqs,
-                            k.shape[0], Hkv, d, page, n_pages, dtype_code(k.dtype), code)
+    (k, ks), (v, vs) = _tokens("k", k, Hkv, d, k), _tokens("v", v, Hkv, d, k)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    ctx = _elsewhere(k.device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_cache_write(k, v, k_cache, v_cache, table, cu, lens, k_scale=k_scale, v_scale=v_scale)
+    _check(lib.cqsa_kv_cache_write(k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
+                                   table.data_ptr(), max_pages, cu.data_ptr(), lens.data_ptr(), n_seqs, k.shape[0], Hkv, d,
+                                   page, n_pages, dtype_code(k.dtype), code, _current(k.device)))
 
 
 def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, *, k_scale=None, v_scale=None, out=None,
@@ -554,16 +599,24 @@ def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, 
     """The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as (k, v) [T, Hkv, d] of dtype (into `out`, a
     pair of such tensors, if given)."""
     import torch
+    device = k_cache.device
+    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                kv_lens, dtype, device)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_cache_read(k_cache, v_cache, table, cu, lens, T, dtype, k_scale=k_scale, v_scale=v_scale, out=out)
     n_pages, Hkv, page, d = k_cache.shape
-    with _on(k_cache.device, stream):
-        code, n_seqs, max_pages, table, cu, lens = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
-                                                          kv_lens, dtype, k_cache.device)
-        k, v = out if out is not None else (torch.empty((T, Hkv, d), dtype=dtype, device=k_cache.device) for _ in range(2))
+    if out is None:
+        k, v = (torch.empty((T, Hkv, d), dtype=dtype, device=device) for _ in range(2))
+    else:
+        k, v = out
         for t in (k, v):
-            if t.shape != (T, Hkv, d) or t.dtype != dtype or t.device != k_cache.device or not t.is_contiguous():
+            if t.shape != (T, Hkv, d) or t.dtype != dtype or t.device != device or not t.is_contiguous():
                 raise ValueError(f"out must be two contiguous [{T}, {Hkv}, {d}] tensors of {dtype}")
-        cqsa_kv_cache_read(k, v, k_cache, v_cache, k_scale, v_scale, table, max_pages, cu, lens, n_seqs, T, Hkv, d, page,
-                           n_pages, dtype_code(dtype), code)
+    _check(lib.cqsa_kv_cache_read(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
+                                  table.data_ptr(), max_pages, cu.data_ptr(), lens.data_ptr(), n_seqs, T, Hkv, d, page,
+                                  n_pages, dtype_code(dtype), code, _current(device)))
     return k, v
 
 
@@ -573,27 +626,30 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
     lse [Hq, T] fp32). max_q_len: at least the most new tokens of a sequence; max_kv_len: about the longest kv_lens.
     `workspace`: a byte tensor of at least cqsa_attn_paged_workspace_size bytes (allocated if not given)."""
     import torch
+    device, dtype = q.device, q.dtype
+    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                kv_lens, dtype, device)
     n_pages, Hkv, page, d = k_cache.shape
-    with _on(q.device, stream):
-        code, n_seqs, max_pages, table, cu, lens = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
-                                                          kv_lens, q.dtype, q.device)
-        q, qs = _tokens("q", q, q.shape[1] if q.dim() == 3 else 0, d, q)
-        T, Hq, dt = q.shape[0], q.shape[1], dtype_code(q.dtype)
-        out = _out(out, q)
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
-        need = cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page, max_q_len, max_kv_len, dt, code)
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        cqsa_attn_paged_fwd(q, qs, out, lse, k_cache, v_cache, k_scale, v_scale, table, max_pages, cu, lens, n_seqs, T,
-                            max_q_len, max_kv_len, Hq, Hkv, d, page, n_pages, causal, 0.0 if scale is None else scale, dt,
-                            code, workspace, workspace.numel() * workspace.element_size())
+    if len(q.shape) != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    T, Hq = q.shape[:2]
+    q, qs = _tokens("q", q, Hq, d, q)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return attention_paged(q, k_cache, v_cache, table, cu, lens, max_q_len, max_kv_len, causal=causal, scale=scale,
+                                   k_scale=k_scale, v_scale=v_scale, return_lse=return_lse, out=out, workspace=workspace)
+    dt = dtype_code(dtype)
+    out = _out(out, q)
+    lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if return_lse else None
+    if workspace is None:
+        size = lib.cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page, max_q_len, max_kv_len, dt, code)
+        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _check(lib.cqsa_attn_paged_fwd(q.data_ptr(), qs, out.data_ptr(), lse.data_ptr() if return_lse else None,
+                                   k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc, table.data_ptr(), max_pages,
+                                   cu.data_ptr(), lens.data_ptr(), n_seqs, T, max_q_len, max_kv_len, Hq, Hkv, d, page,
+                                   n_pages, 1 if causal else 0, 0.0 if scale is None else scale, dt, code,
+                                   workspace.data_ptr(), size, _current(device)))
     return (out, lse) if return_lse else out
-
-
-def _out(out, q):
-    import torch
-    if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {tuple(q.shape)} tensor of {q.dtype} on {q.device}")
-    return out

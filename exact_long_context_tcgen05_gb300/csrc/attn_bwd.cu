@@ -32,7 +32,7 @@
 // (sequence, key head), found from cu_seqlens, and its steps walk over floor(128 / G) tokens times the G query heads that
 // share the key head, so dK_j and dV_j sum over the group in tensor memory, in a fixed order and without atomics.
 // Rows past a sequence's end (other sequences' tokens) are zeroed in shared memory after their loads: P = dS = 0
-// there would not hide a NaN. packed_prep_kernel and packed_dq_kernel take the places of the first and last.
+// there would not hide a NaN. packed_prep_kernel and packed_out_kernel take the places of the first and last.
 // P and dS enter the MMAs rounded to the input dtype; everything else is fp32. Head dimension 64 or 128
 // (d = 128 holds one Q/dO tile instead of two, and shares tensor and shared memory between phases: see
 // BwdCfg).
@@ -157,6 +157,7 @@ struct BwdParams {
   // packed sequences (ACCUM = 2): lse holds -lse * log2 e and dvec -D, both [T, Hq]; dk, dv are [T, Hkv, d]
   const int* cu;
   int n_seqs, T, Hq, Hkv, G, tpt;  // tpt: tokens of a step, floor(128 / G)
+  int n_splits;  // ranges that a key tile's steps are cut into; more than one leave fp32 parts [n_splits][T][Hkv][d] in dk_acc, dv_acc
 };
 
 __device__ __forceinline__ void record_bwd_error(int code, int where) {
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
   int k0 = jt * BT;  // packed: k0, Nkv, it0 and nit are set with the unit, below
   int Nkv = ACCUM ? p.Nkv : p.Nq;
   // first query tile with a query at or after this key tile's first key (causal; absolute positions)
-  int it0 = 0, seq_first = 0;
+  int it0 = 0, seq_first = 0, split = 0;
   if constexpr (ACCUM == 1) {
     if (CAUSAL) {
       const long long first = p.kv_off + k0 - p.q_off - (BT - 1);
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
   if constexpr (PACKED) {
     if (warp == 2) {
       // key tiles by how many follow them in their sequence: under the causal mask, heaviest first
-      const Unit u = find_unit(p.n_seqs, unit / p.Hkv, lane, [&](int i) {
+      const Unit u = find_unit(p.n_seqs, unit / (p.Hkv * p.n_splits), lane, [&](int i) {
         int first;
         return (seq_tokens(p.cu, i, p.T, &first) + BT - 1) / BT;
       });
@@ -435,6 +436,22 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     k0 = ((Nkv + BT - 1) / BT - 1 - s_unit[1]) * BT;
     it0 = CAUSAL ? k0 / p.tpt : 0;
     nit = (Nkv + p.tpt - 1) / p.tpt - it0;  // >= 1: the tile's own tokens
+    if (p.n_splits > 1) {
+      split = (unit / p.Hkv) % p.n_splits;
+      auto bound = [&](int i) -> int { return static_cast<int>((static_cast<long long>(nit) * i + p.n_splits - 1) / p.n_splits); };
+      const int b0 = bound(split), b1 = bound(split + 1);
+      it0 += b0;
+      nit = b1 - b0;
+      if (nit == 0) {  // fewer steps than ranges: this range's part is zero
+        for (int i = tid; i < min(BT, Nkv - k0) * (HD / 4); i += TH::NTHR) {
+          const long long at = ((static_cast<long long>(split) * p.T + seq_first + k0 + i / (HD / 4)) * p.Hkv + h) * (HD / 4) + i % (HD / 4);
+          reinterpret_cast<float4*>(p.dk_acc)[at] = reinterpret_cast<float4*>(p.dv_acc)[at] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        __syncthreads();
+        if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+        return;
+      }
+    }
   }
 
   if (warp < 4) {
@@ -1089,6 +1106,17 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
                                         __uint_as_float(g[4 * u + 2]) * p.scale,
                                         __uint_as_float(g[4 * u + 3]) * p.scale));
         }
+      } else if (PACKED && p.n_splits > 1 && key_ok) {
+        const long long at = (static_cast<long long>(split) * p.T * p.Hkv + row) * HD + fb;
+        float4* dv = reinterpret_cast<float4*>(p.dv_acc + at);
+        float4* dk = reinterpret_cast<float4*>(p.dk_acc + at);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          dv[u] = make_float4(__uint_as_float(a[4 * u]), __uint_as_float(a[4 * u + 1]), __uint_as_float(a[4 * u + 2]),
+                              __uint_as_float(a[4 * u + 3]));
+          dk[u] = make_float4(__uint_as_float(g[4 * u]) * p.scale, __uint_as_float(g[4 * u + 1]) * p.scale,
+                              __uint_as_float(g[4 * u + 2]) * p.scale, __uint_as_float(g[4 * u + 3]) * p.scale);
+        }
       } else if (ACCUM != 1 && key_ok) {
         uint4* dv = reinterpret_cast<uint4*>(p.dv + row * HD + fb);
         uint4* dk = reinterpret_cast<uint4*>(p.dk + row * HD + fb);
@@ -1128,6 +1156,18 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
           atomicAdd(dk + u, make_float4(__uint_as_float(g[4 * u]) * p.scale, __uint_as_float(g[4 * u + 1]) * p.scale,
                                         __uint_as_float(g[4 * u + 2]) * p.scale,
                                         __uint_as_float(g[4 * u + 3]) * p.scale));
+        }
+      } else if (PACKED && p.n_splits > 1 && key_ok) {
+        const long long row = static_cast<long long>(seq_first + k0 + r) * p.Hkv + h;
+        const long long at = (static_cast<long long>(split) * p.T * p.Hkv + row) * HD + fb;
+        float4* dv = reinterpret_cast<float4*>(p.dv_acc + at);
+        float4* dk = reinterpret_cast<float4*>(p.dk_acc + at);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          dv[u] = make_float4(__uint_as_float(a[4 * u]), __uint_as_float(a[4 * u + 1]), __uint_as_float(a[4 * u + 2]),
+                              __uint_as_float(a[4 * u + 3]));
+          dk[u] = make_float4(__uint_as_float(g[4 * u]) * p.scale, __uint_as_float(g[4 * u + 1]) * p.scale,
+                              __uint_as_float(g[4 * u + 2]) * p.scale, __uint_as_float(g[4 * u + 3]) * p.scale);
         }
       } else if (ACCUM != 1 && key_ok) {
         const long long row = PACKED ? static_cast<long long>(seq_first + k0 + r) * p.Hkv + h
@@ -1227,15 +1267,33 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const uint4* o, const 
   }
 }
 
-// fp32 dQ accumulator -> dQ of the tokens that belong to a sequence (the others' rows are left as they were).
+// The fp32 results into dtype, for the tokens that belong to a sequence (the others' rows are left as they were):
+// blockIdx.y 0, the dQ accumulator; 1 and 2, dK and dV as the sums of their n_splits parts, in their order.
+struct PackedOut {
+  const float4* src[3];
+  uint2* dst[3];
+  int row4[3];         // four-element pieces of a token
+  int parts[3];
+};
 template <int DT>
-__global__ void __launch_bounds__(256) packed_dq_kernel(const float4* acc, uint2* dq, const int* cu, int n_seqs, int T,
-                                                        int row4) {  // row4: four-element pieces of a token
-  const long long first = static_cast<long long>(cu_at(cu, 0, T)) * row4, last = static_cast<long long>(cu_at(cu, n_seqs, T)) * row4;
+__global__ void __launch_bounds__(256) packed_out_kernel(const PackedOut o, const int* cu, int n_seqs, int T) {
+  const int y = blockIdx.y;
+  const float4* src = y == 0 ? o.src[0] : (y == 1 ? o.src[1] : o.src[2]);
+  uint2* dst = y == 0 ? o.dst[0] : (y == 1 ? o.dst[1] : o.dst[2]);
+  const long long row4 = y == 0 ? o.row4[0] : (y == 1 ? o.row4[1] : o.row4[2]);
+  const int parts = y == 0 ? o.parts[0] : (y == 1 ? o.parts[1] : o.parts[2]);
+  const long long first = cu_at(cu, 0, T) * row4, last = cu_at(cu, n_seqs, T) * row4, step = T * row4;
   for (long long i = first + static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < last;
        i += static_cast<long long>(gridDim.x) * 256) {
-    const float4 v = acc[i];
-    dq[i] = make_uint2(pack_pair(v.x, v.y, DT), pack_pair(v.z, v.w, DT));
+    float4 v = src[i];
+    for (int k = 1; k < parts; ++k) {
+      const float4 w = src[i + k * step];
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    dst[i] = make_uint2(pack_pair(v.x, v.y, DT), pack_pair(v.z, v.w, DT));
   }
 }
 
@@ -1384,17 +1442,41 @@ int run_main(const BwdArgs& a, float* dq_acc, const float* dvec, int accum, cuda
 
 }  // namespace
 
-size_t packed_bwd_workspace(int T, int Hq, int d) {
-  const size_t rows = static_cast<size_t>(T) * Hq;
-  return ((rows * d * 4 + 255) & ~size_t(255)) + 2 * ((rows * 4 + 255) & ~size_t(255));
+namespace {
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// An upper bound on the key tiles of n_seqs sequences that hold T tokens together, times the key heads.
+long long packed_tiles(int n_seqs, int T, int Hkv) { return (T / BT + static_cast<long long>(T < n_seqs ? T : n_seqs)) * Hkv; }
+
+// Ranges of steps per key tile: a CTA takes a key tile through all its queries, so few tiles leave SMs idle and the
+// first tile of the longest sequence sets the time (9 sequences, 4,099 tokens, 2 key heads at d = 64: 83 us in one range).
+// Parts cost fp32 traffic and each CTA its set-up, so about CQSA_BWD_FILL CTAs per SM are enough.
+#ifndef CQSA_BWD_FILL
+#define CQSA_BWD_FILL 3
+#endif
+int packed_splits(int n_seqs, int T, int Hkv) {
+  const long long s = static_cast<long long>(sm_count()) * CQSA_BWD_FILL / std::max<long long>(1, packed_tiles(n_seqs, T, Hkv));
+  return static_cast<int>(std::min<long long>(std::max<long long>(s, 1), 16));
+}
+
+}  // namespace
+
+// The fp32 dQ accumulator, -lse log2 e and -D of every row, and the parts of dK and dV where there are several.
+size_t packed_bwd_workspace(int n_seqs, int T, int Hq, int Hkv, int d) {
+  const size_t rows = static_cast<size_t>(T) * Hq, s = static_cast<size_t>(packed_splits(n_seqs, T, Hkv));
+  return up256(rows * d * 4) + 2 * up256(rows * 4) + (s > 1 ? 2 * up256(s * T * Hkv * d * 4) : 0);
 }
 
 int launch_packed_bwd(const PackedArgs& a, const void* dout, void* dq, void* dk, void* dv, void* workspace, cudaStream_t stream) {
   const size_t rows = static_cast<size_t>(a.T) * a.Hq;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* dq_acc = reinterpret_cast<float*>(ws);
-  float* nlse = reinterpret_cast<float*>(ws + ((rows * a.d * 4 + 255) & ~size_t(255)));
-  float* ndvec = nlse + ((rows * 4 + 255) & ~size_t(255)) / 4;
+  float* nlse = reinterpret_cast<float*>(ws + up256(rows * a.d * 4));
+  float* ndvec = nlse + up256(rows * 4) / 4;
+  const int splits = packed_splits(a.n_seqs, a.T, a.Hkv);
+  float* part_k = ndvec + up256(rows * 4) / 4;
+  float* part_v = part_k + up256(static_cast<size_t>(splits) * a.T * a.Hkv * a.d * 4) / 4;
   BwdParams p;
   memset(&p, 0, sizeof(p));
   p.G = a.Hq / a.Hkv;
@@ -1418,7 +1500,7 @@ int launch_packed_bwd(const PackedArgs& a, const void* dout, void* dq, void* dk,
   if (rc == CQSA_OK) rc = encode_map(&mdq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dq_acc, qdims, ds, dbox);
   if (rc != CQSA_OK) return rc;
   const long long prep = (static_cast<long long>(rows) * (a.d / 8) + 255) / 256;
-  const long long tiles = (a.T / BT + static_cast<long long>(a.T < a.n_seqs ? a.T : a.n_seqs)) * a.Hkv;  // upper bound
+  const long long tiles = packed_tiles(a.n_seqs, a.T, a.Hkv) * splits;
   if (tiles > 0x7fffffffLL || prep > 0x7fffffffLL) {
     set_error("problem too large for one launch");
     return CQSA_ERR_UNSUPPORTED;
@@ -1444,17 +1526,28 @@ int launch_packed_bwd(const PackedArgs& a, const void* dout, void* dq, void* dk,
   p.T = a.T;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
+  p.n_splits = splits;
+  p.dk_acc = part_k;
+  p.dv_acc = part_v;
   p.BH = 1;  // launch_main's grid is n_kv_tiles * BH
   const int nt = static_cast<int>(tiles);
   rc = a.d == 128 ? dispatch_main<2, 128>(mq, mk, mv, mg, mdq, p, nt, a.dtype, a.causal, stream)
                   : dispatch_main<2, 64>(mq, mk, mv, mg, mdq, p, nt, a.dtype, a.causal, stream);
   if (rc != CQSA_OK) return rc;
   const long long n4 = static_cast<long long>(rows) * a.d / 4;
-  const unsigned cblocks = static_cast<unsigned>(std::min<long long>((n4 + 255) / 256, sm_count() * 16LL));
-  const int row4 = a.Hq * a.d / 4;
-  if (bf) packed_dq_kernel<1><<<cblocks, 256, 0, stream>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint2*>(dq), a.cu, a.n_seqs, a.T, row4);
-  else packed_dq_kernel<0><<<cblocks, 256, 0, stream>>>(reinterpret_cast<const float4*>(dq_acc), static_cast<uint2*>(dq), a.cu, a.n_seqs, a.T, row4);
-  return cuda_status(cudaGetLastError(), "packed attention backward cast launch");
+  const dim3 cgrid(static_cast<unsigned>(std::min<long long>((n4 + 255) / 256, sm_count() * 16LL)), splits > 1 ? 3 : 1);
+  PackedOut po;
+  const float* src[3] = {dq_acc, part_k, part_v};
+  void* dst[3] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i) {
+    po.src[i] = reinterpret_cast<const float4*>(src[i]);
+    po.dst[i] = static_cast<uint2*>(dst[i]);
+    po.row4[i] = (i ? a.Hkv : a.Hq) * a.d / 4;
+    po.parts[i] = i ? splits : 1;
+  }
+  if (bf) packed_out_kernel<1><<<cgrid, 256, 0, stream>>>(po, a.cu, a.n_seqs, a.T);
+  else packed_out_kernel<0><<<cgrid, 256, 0, stream>>>(po, a.cu, a.n_seqs, a.T);
+  return cuda_status(cudaGetLastError(), "packed attention backward output launch");
 }
 
 size_t attention_bwd_workspace(int B, int H, int N, int d) {

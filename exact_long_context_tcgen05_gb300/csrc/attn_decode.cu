@@ -15,7 +15,7 @@
 // launched with programmatic stream serialisation, so its start overlaps the main kernel's tail.
 //
 // A CTA: one producer warp copies key tiles page by page with TMA through a ring of stages (a lane per page
-// box); 4 warps (8 for 32 rows) each take a quarter of a tile's keys through S = Q K^T, an online softmax in
+// box); 4 warps (8 for 32 rows), each on a quarter of a tile's keys, take them through S = Q K^T, an online softmax in
 // registers, and O += P V, and join their rows in shared memory at the end of a unit's range.
 //
 // e4m3 pages: codes become fp16 in registers (exact). A key's power of two multiplies its scores in fp32, a
@@ -35,26 +35,30 @@ namespace {
 
 __device__ DevErr g_decode_err;
 
-constexpr int kKeyWarps = 4;  // warps that share a tile's keys
+constexpr int kQuarters = 4;  // warps that share a tile's keys
 // Probabilities are kept as 2^14 p (and so are their sums): fp16 holds them without loss of relative precision
 // down to p = 2^-28, where plain p would turn subnormal at 2^-14.
 constexpr float kPShift = 14.0f;
 
+constexpr int decode_occ(bool e4m3, int nmt) { return e4m3 && nmt == 1 ? 2 : 1; }
+
 template <int D, bool E4M3, int NMT>
 struct DecCfg {
   static constexpr int KT = E4M3 ? 128 : (D == 64 ? 128 : 64);   // keys of a tile
-  static constexpr int KW = KT / kKeyWarps;                      // keys of a warp
+  static constexpr int KW = KT / kQuarters;                      // keys of a warp
   static constexpr int ROWB = E4M3 ? D : 128;                    // bytes of a shared-memory row
   static constexpr int XB = E4M3 ? 1 : D / 64;                   // boxes along the features
   static constexpr uint32_t TILE = static_cast<uint32_t>(KT) * ROWB * XB;
-  static constexpr uint32_t STAGE = 2 * TILE + (E4M3 ? 1024 : 0);  // K, V (and their exponent bytes)
+  static constexpr uint32_t STAGE = 2 * TILE + (E4M3 ? 1024 : 0);
   static constexpr int LDO = D + 8;                              // row of the joining buffer, padded against bank conflicts
-  static constexpr uint32_t JOIN = static_cast<uint32_t>(NMT) * kKeyWarps * 16 * LDO * 4;
-  static constexpr uint32_t ML = NMT * kKeyWarps * 16 * 4 * 4;   // m, l, exponent reference of each warp's rows
-  static constexpr int NST_MAX = static_cast<int>((232448 - 1024 - 512 - JOIN - ML) / STAGE);
+  static constexpr uint32_t JOIN = static_cast<uint32_t>(NMT) * kQuarters * 16 * LDO * 4;
+  static constexpr uint32_t ML = NMT * kQuarters * 32 * 4;            // m and l of each warp's rows
+  // CTAs of an SM
+  static constexpr int OCC = decode_occ(E4M3, NMT);
+  static constexpr int NST_MAX = static_cast<int>((232448 / OCC - (OCC - 1) * 1024 - 1024 - 512 - JOIN - ML) / STAGE);
   static constexpr int NST = NST_MAX > 6 ? 6 : NST_MAX;
   static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + 512;
-  static constexpr int NTHR = 32 + 32 * kKeyWarps * NMT;
+  static constexpr int NTHR = 32 + 32 * kQuarters * NMT;
   static_assert(SMEM <= 232448, "shared memory exceeds 227 KiB");
 };
 
@@ -64,7 +68,8 @@ struct DecParams {
   float* lse;
   float* part_o;  // [2 * CTAs][16 * NMT][D]
   float* part_l;  // [2 * CTAs][16 * NMT], base 2
-  int4* meta;     // [CTAs] the unit a CTA's range begins in the middle of: sequence, head, first and last CTA of it
+  int4* meta;     // [CTAs][2] the unit a CTA's range begins in the middle of: sequence (-1: none), head, first and last
+                  // CTA of it; the sequence's first token and tokens
   const int* table;
   const int* cu;
   const int* kv_lens;
@@ -115,18 +120,39 @@ __device__ __forceinline__ uint32_t tile16_off(int r, int c) {
   return static_cast<uint32_t>((r >> 3) * (1024 * (D / 64)) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Where a CTA's walk over its range of key tiles stands: sequence, its tiles per head, tokens and positions.
+// A unit counts as its key tiles and kUnit more: what its queries' loads and the joining of its rows cost. Without them
+// a CTA that gets many short sequences finishes late (128 ragged sequences of e4m3: the last CTA at 311 us, the mean at 231).
+constexpr int kUnit = 2;
+
+// Where a CTA's walk over its range stands: sequence, the length of each of its units, tokens and positions.
 struct Walk {
   int s, n, qlen, first, len;
-  long long base;  // tile index of the sequence's first tile
+  long long base;  // where the sequence's first unit begins
 };
+
+// What a range [w, w1) does in the unit it stands in: head, and key tiles [t0, t1) (none when it only reaches into the
+// unit's kUnit). `next`: where the unit (or the range) ends.
+struct Piece {
+  int h, t0, t1;
+  long long next;
+};
+__device__ __forceinline__ Piece piece_at(const Walk& k, long long w, long long w1) {
+  Piece r;
+  const long long rel = w - k.base;
+  r.h = static_cast<int>(rel / k.n);
+  const long long u0 = k.base + static_cast<long long>(r.h) * k.n;
+  r.next = min(u0 + k.n, w1);
+  r.t0 = max(0, static_cast<int>(w - u0) - kUnit);
+  r.t1 = max(0, static_cast<int>(r.next - u0) - kUnit);
+  return r;
+}
 
 template <int KT>
 __device__ __forceinline__ void walk_load(const DecParams& p, Walk& w) {
   w.qlen = seq_tokens(p.cu, w.s, p.T, &w.first);
   w.len = seq_positions(p.kv_lens, w.s, static_cast<long long>(p.max_pages) << p.page_log2);
   // a sequence without new tokens is no work; one without positions is one empty tile (its rows are zero)
-  w.n = w.qlen == 0 ? 0 : max(1, (w.len + KT - 1) / KT);
+  w.n = w.qlen == 0 ? 0 : max(1, (w.len + KT - 1) / KT) + kUnit;
 }
 template <int KT>
 __device__ __forceinline__ void walk_next(const DecParams& p, Walk& w) {
@@ -139,7 +165,7 @@ __device__ __forceinline__ void walk_next(const DecParams& p, Walk& w) {
 }
 
 template <int D, int BF16, bool E4M3, int NMT>
-__global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
+__global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NMT>::OCC)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecParams p) {
   using C = DecCfg<D, E4M3, NMT>;
   constexpr int KT = C::KT, KW = C::KW, NST = C::NST, NTHR = C::NTHR;
@@ -147,7 +173,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* join = reinterpret_cast<float*>(sm + NST * C::STAGE);
-  float* ml = join + C::JOIN / 4;  // [NMT][kKeyWarps][m 16 | l 16 | exponent 16 | -]
+  float* ml = join + C::JOIN / 4;  // [NMT][kQuarters][m 16 | l 16]
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ml) + C::ML);
   uint64_t* empty = full + NST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NST);
@@ -160,7 +186,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kKeyWarps * NMT);
+      mbar_init(&empty[i], kQuarters * NMT);
     }
     *abort_flag = 0;
     *s_seq = -1;
@@ -194,28 +220,35 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
     *before = b + x - v;
     return t;
   };
-  long long W = 0, dummy;
-  const long long mine = tiles_of(tid);  // the first NTHR sequences, kept for the search
-  W = block_scan(mine, &dummy);
-  for (int s0 = NTHR; s0 < p.n_seqs; s0 += NTHR) W += block_scan(tiles_of(s0 + tid), &dummy);
+  long long mine, before;
+  {
+    Walk w;
+    w.s = tid;
+    w.n = 0;
+    if (tid < p.n_seqs) walk_load<KT>(p, w);
+    mine = static_cast<long long>(w.n) * p.Hkv;
+  }
+  long long W = block_scan(mine, &before);  // the first NTHR sequences
+  const long long W_first = W;
+  long long unused;
+  for (int s0 = NTHR; s0 < p.n_seqs; s0 += NTHR) W += block_scan(tiles_of(s0 + tid), &unused);
   // every range holds a tile: with fewer tiles than CTAs (sequences shorter than the caller said) the last CTAs idle
   const long long nc = min(static_cast<long long>(gridDim.x), W);
   const long long bx = blockIdx.x;
   const long long w0 = bx < nc ? W * bx / nc : 0, w1 = bx < nc ? W * (bx + 1) / nc : 0;
-  {
-    long long base = 0;
-    for (int s0 = 0; s0 < p.n_seqs; s0 += NTHR) {
-      const long long v = s0 == 0 ? mine : tiles_of(s0 + tid);
-      long long before;
-      const long long t = block_scan(v, &before);
-      before += base;
-      if (w0 < w1 && before <= w0 && w0 < before + v) {
-        *s_seq = s0 + tid;
-        *s_base = before;
-      }
-      base += t;
-      if (base > w0) break;
+  if (w0 < w1 && before <= w0 && w0 < before + mine) {
+    *s_seq = tid;
+    *s_base = before;
+  }
+  for (long long base = W_first, s0 = NTHR; base <= w0 && s0 < p.n_seqs; s0 += NTHR) {
+    const long long v = tiles_of(static_cast<int>(s0) + tid);
+    const long long t = block_scan(v, &before);
+    before += base;
+    if (w0 < w1 && before <= w0 && w0 < before + v) {
+      *s_seq = static_cast<int>(s0) + tid;
+      *s_base = before;
     }
+    base += t;
   }
   __syncthreads();
   // the joining kernel may be set up from here on; it waits for this grid's end before it reads anything
@@ -227,7 +260,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
   wk.n = 0;
   if (wk.s >= 0) walk_load<KT>(p, wk);
   if (wk.s < 0) {
-    if (tid == 0) p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (tid == 0) p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   } else if (warp == NW - 1) {
     // ------------------------------------------------------------------ producer warp
     if (lane == 0) {
@@ -240,9 +273,8 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
     int it = 0;
     bool ok = true;
     for (long long w = w0; ok && w < w1;) {
-      const long long rel = w - wk.base;
-      const int h = static_cast<int>(rel / wk.n), t0 = static_cast<int>(rel - static_cast<long long>(h) * wk.n);
-      const int t1 = static_cast<int>(min(static_cast<long long>(wk.n), t0 + (w1 - w)));
+      const Piece pc = piece_at(wk, w, w1);
+      const int h = pc.h, t0 = pc.t0, t1 = pc.t1;
       const int* row = p.table + static_cast<long long>(wk.s) * p.max_pages;
       for (int t = t0; ok && t < t1; ++t, ++it) {
         const int stage = it % NST;
@@ -274,8 +306,8 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
           }
         }
       }
-      w += t1 - t0;
-      if (w < w1 && t1 == wk.n && h == p.Hkv - 1) walk_next<KT>(p, wk);
+      w = pc.next;
+      if (w < w1 && h == p.Hkv - 1) walk_next<KT>(p, wk);
     }
     __syncwarp();
     // every copy issued has landed before the CTA ends (bounded)
@@ -283,17 +315,27 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
       mbar_wait_bounded(&full[j % NST], (j / NST) & 1u, p.timeout_us * 1000ull);
   } else {
     // ------------------------------------------------------------------ key warps
-    const int mt = warp / kKeyWarps, kg = warp % kKeyWarps;  // row tile, quarter of the keys
+    const int mt = warp / kQuarters, kg = warp % kQuarters;  // row tile, quarter of the keys
     const int g = lane >> 2, t4 = lane & 3;
-    float* jbuf = join + mt * kKeyWarps * 16 * C::LDO;
-    float* mlb = ml + mt * kKeyWarps * 64;
+    float* jbuf = join + mt * kQuarters * 16 * C::LDO;
+    float* mlb = ml + mt * kQuarters * 32;
     bool ok = true;
     int it = 0;
-    bool first_piece = true;
     for (long long w = w0; w < w1;) {
-      const long long rel = w - wk.base;
-      const int h = static_cast<int>(rel / wk.n), t0 = static_cast<int>(rel - static_cast<long long>(h) * wk.n);
-      const int t1 = static_cast<int>(min(static_cast<long long>(wk.n), t0 + (w1 - w)));
+      const Piece pc = piece_at(wk, w, w1);
+      const int h = pc.h, t0 = pc.t0, t1 = pc.t1;
+      if (w == w0 && tid == 0) {
+        // the unit this range begins in the middle of, and the CTAs whose ranges hold its first and last tile
+        const long long u0 = wk.base + static_cast<long long>(h) * wk.n, u1 = u0 + wk.n - 1;
+        const int c0 = static_cast<int>(((u0 + kUnit + 1) * nc - 1) / W), c1 = static_cast<int>(((u1 + 1) * nc - 1) / W);
+        p.meta[2 * blockIdx.x] = t0 == 0 ? make_int4(-1, 0, 0, 0) : make_int4(wk.s, h, c0, c1);
+        p.meta[2 * blockIdx.x + 1] = make_int4(wk.first, wk.qlen, 0, 0);
+      }
+      if (t1 <= t0) {
+        w = pc.next;
+        if (w < w1 && h == p.Hkv - 1) walk_next<KT>(p, wk);
+        continue;
+      }
       // ---- the rows' queries as A fragments, and the keys each of this thread's two rows may see
       uint32_t qf[D / 16][4];
       int lim[2];
@@ -352,7 +394,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-      int ev = -1000;  // e4m3: exponent the output sums are relative to
+      int ev = -1;  // e4m3: exponent byte the output sums are relative to
       for (int t = t0; t < t1; ++t, ++it) {
         const int stage = it % NST;
         if (ok) ok = wait_or_abort(smem_u32(&full[stage]), (it / NST) & 1u, p.timeout_us, a_abort, &g_decode_err,
@@ -363,6 +405,42 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
         const int kw0 = kg * KW;                 // first key of this warp in the tile
         const int k0 = t * KT + kw0;             // its position
         const int left = wk.len - k0;            // positions of the sequence from there
+        // ---- e4m3: this thread's keys' exponents (before the products, which hide their way), and the largest of the values'.
+        // Slots past the end hold anything: their scores keep a factor of 1, their values' exponents do not count.
+        uint32_t kexp[E4M3 ? KW / 8 : 1][2], vexp[E4M3 ? KW / 8 : 1][2];
+        if constexpr (E4M3) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 0; j < KW / 8; ++j) {
+            const uint8_t* sc = st + 2 * C::TILE + kw0 + j * 8 + 2 * t4;
+            const uint32_t kb = *reinterpret_cast<const uint16_t*>(sc), vb = *reinterpret_cast<const uint16_t*>(sc + 512);
+            kexp[j][0] = kb & 255u;
+            kexp[j][1] = kb >> 8;
+            vexp[j][0] = vb & 255u;
+            vexp[j][1] = vb >> 8;
+          }
+          if (left < KW) {
+#pragma unroll
+            for (int j = 0; j < KW / 8; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (j * 8 + 2 * t4 + i >= left) {
+                  kexp[j][i] = 127u;
+                  vexp[j][i] = 0u;
+                }
+          }
+#pragma unroll
+          for (int j = 0; j < KW / 8; ++j) top = max(top, max(vexp[j][0], vexp[j][1]));
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (static_cast<int>(top) > ev) {
+            const float a = ev < 0 ? 0.0f : exp2_int_any(ev - static_cast<int>(top));
+            ev = static_cast<int>(top);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[j][i] *= a;
+          }
+        }
         // ---- S = Q K^T
         float s[KW / 8][4];
 #pragma unroll
@@ -371,16 +449,15 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
           for (int i = 0; i < 4; ++i) s[j][i] = 0.0f;
         if constexpr (E4M3) {
 #pragma unroll
-          for (int j = 0; j < KW / 8; ++j) {
-            const int r = kw0 + j * 8 + (lane & 7);
+          for (int c = 0; c < D / 64; ++c) {  // 64 features: four ldmatrix matrices of 16 codes
+            uint32_t b[KW / 8][4];
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {  // 64 features: four ldmatrix matrices of 16 codes
-              uint32_t b[4];
-              ldsm4(sk + sw_off<C::ROWB>(r, c * 4 + (lane >> 3)), b);
+            for (int j = 0; j < KW / 8; ++j) ldsm4(sk + sw_off<C::ROWB>(kw0 + j * 8 + (lane & 7), c * 4 + (lane >> 3)), b[j]);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma16816<0>(s[j], qf[c * 4 + i], e4m3x2_to_f16x2(b[i] & 0xffffu), e4m3x2_to_f16x2(b[i] >> 16));
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < KW / 8; ++j)  // neighbouring products are independent
+                mma16816<0>(s[j], qf[c * 4 + i], e4m3x2_to_f16x2(b[j][i] & 0xffffu), e4m3x2_to_f16x2(b[j][i] >> 16));
           }
         } else {
 #pragma unroll
@@ -396,40 +473,14 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
           }
         }
         // ---- scores in base 2, masks, running maximum
-        int vexp[E4M3 ? KW / 8 : 1][2];
-        if constexpr (E4M3) {
-          int top = -1000;
-#pragma unroll
-          for (int j = 0; j < KW / 8; ++j) {
-            const int kk = j * 8 + 2 * t4;
-            const uint8_t* sc = st + 2 * C::TILE + kw0 + kk;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const bool in = kk + i < left;  // slots past the end hold anything
-              const float ke = in ? exp2_byte(sc[i]) : 1.0f;
-              s[j][i] *= ke;
-              s[j][2 + i] *= ke;
-              vexp[j][i] = in ? static_cast<int>(sc[512 + i]) - 127 : -1000;
-              top = max(top, vexp[j][i]);
-            }
-          }
-          top = __reduce_max_sync(0xffffffffu, top);
-          if (top > ev) {
-            const float a = ev == -1000 ? 0.0f : exp2f(static_cast<float>(ev - top));
-            ev = top;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[j][i] *= a;
-          }
-        }
         const bool mask = left < KW || k0 + KW > lim_all || lim[0] == 0 || lim[1] == 0;
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < KW / 8; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float x = s[j][i] * rs[i >> 1];
+            // (a byte is an fp32 exponent field; 0, never written, counts as 0)
+            float x = s[j][i] * (E4M3 ? rs[i >> 1] * __uint_as_float(kexp[j][i & 1] << 23) : rs[i >> 1]);
             if (mask && k0 + j * 8 + 2 * t4 + (i & 1) >= lim[i >> 1]) x = -INFINITY;
             s[j][i] = x;
             mx[i >> 1] = fmaxf(mx[i >> 1], x);
@@ -467,7 +518,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
           }
           if constexpr (E4M3) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) pr[i] *= ex2(static_cast<float>(max(vexp[j][i & 1] - ev, -126)));
+            for (int i = 0; i < 4; ++i) pr[i] *= exp2_int_any(static_cast<int>(vexp[j][i & 1]) - ev);
           }
           pf[j >> 1][(j & 1) * 2] = pack16(pr[0], pr[1], MB);
           pf[j >> 1][(j & 1) * 2 + 1] = pack16(pr[2], pr[3], MB);
@@ -518,30 +569,30 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
       }
-      // ---- join the four warps' rows
+      // ---- join the warps' rows: each brings its sums to the common maximum and scale
+      // (the exponent reference of e4m3 values is a power of two that is multiplied out here)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         l[u] += __shfl_xor_sync(0xffffffffu, l[u], 1);
         l[u] += __shfl_xor_sync(0xffffffffu, l[u], 2);
         if (t4 == 0) {
-          mlb[kg * 64 + g + 8 * u] = m[u];
-          mlb[kg * 64 + 16 + g + 8 * u] = l[u];
+          mlb[kg * 32 + g + 8 * u] = m[u];
+          mlb[kg * 32 + 16 + g + 8 * u] = l[u];
         }
       }
-      named_sync(1 + mt, 32 * kKeyWarps);
-      float f[2];
+      named_sync(1 + mt, 32 * kQuarters);
+      float f[2], lse2[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float M = -INFINITY, L = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kKeyWarps; ++i) M = fmaxf(M, mlb[i * 64 + g + 8 * u]);
+        for (int i = 0; i < kQuarters; ++i) M = fmaxf(M, mlb[i * 32 + g + 8 * u]);
         const float Mu = M == -INFINITY ? 0.0f : M;
 #pragma unroll
-        for (int i = 0; i < kKeyWarps; ++i) L += mlb[i * 64 + 16 + g + 8 * u] * ex2(mlb[i * 64 + g + 8 * u] - Mu);
-        f[u] = L > 0.0f ? ex2(m[u] - Mu) / L : 0.0f;
-        if (M != M || L != L) f[u] = NAN;
-        if (kg == 0 && t4 == 0) mlb[32 + g + 8 * u] = L > 0.0f ? M - kPShift + log2f(L) : (L != L ? NAN : -INFINITY);
-        if (E4M3) f[u] *= ev == -1000 ? 0.0f : pow2i(min(max(ev, -126), 127));
+        for (int i = 0; i < kQuarters; ++i) L += mlb[i * 32 + 16 + g + 8 * u] * ex2(mlb[i * 32 + g + 8 * u] - Mu);
+        f[u] = L > 0.0f ? ex2(m[u] - Mu) / L : (L != L ? NAN : 0.0f);
+        lse2[u] = L > 0.0f ? M - kPShift + log2f(L) : (L != L ? NAN : -INFINITY);
+        if (E4M3) f[u] *= ev < 0 ? 0.0f : exp2_byte(static_cast<uint32_t>(ev));
       }
 #pragma unroll
       for (int j = 0; j < D / 8; ++j) {
@@ -559,17 +610,20 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
           *reinterpret_cast<float2*>(b1 + j * 8 + 2 * t4) = make_float2(o[j][2] * f[1], o[j][3] * f[1]);
         }
       }
-      named_sync(1 + mt, 32 * kKeyWarps);
-      const bool whole = t0 == 0 && t1 == wk.n;
+      if (kg == 0 && t4 == 0) {  // a column of the padding carries the rows' lse
+        jbuf[g * C::LDO + D] = lse2[0];
+        jbuf[(g + 8) * C::LDO + D] = lse2[1];
+      }
+      named_sync(1 + mt, 32 * kQuarters);
+      const bool whole = t0 == 0 && t1 == wk.n - kUnit;
       const long long slot = 2 * static_cast<long long>(blockIdx.x) + (t0 == 0 ? 1 : 0);
-      const int i128 = kg * 32 + lane;
-      for (int e = i128; e < 16 * (D / 4); e += 128) {
+      for (int e = kg * 32 + lane; e < 16 * (D / 4); e += 32 * kQuarters) {
         const int row = e / (D / 4), c = e % (D / 4);
         const int r = mt * 16 + row, tok = r / p.G;
         if (tok >= wk.qlen || !ok) continue;
         float4 a = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kKeyWarps; ++i) {
+        for (int i = 0; i < kQuarters; ++i) {
           const float4 b = *reinterpret_cast<const float4*>(jbuf + (i * 16 + row) * C::LDO + c * 4);
           a.x += b.x;
           a.y += b.y;
@@ -580,21 +634,14 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
           const long long at = static_cast<long long>(wk.first + tok) * p.Hq + h * p.G + (r - tok * p.G);
           reinterpret_cast<uint2*>(p.out)[at * (D / 4) + c] = make_uint2(pack16(a.x, a.y, BF16), pack16(a.z, a.w, BF16));
           if (p.lse && c == 0)
-            p.lse[static_cast<long long>(h * p.G + (r - tok * p.G)) * p.T + wk.first + tok] = mlb[32 + row] * 0.69314718055994531f;
+            p.lse[static_cast<long long>(h * p.G + (r - tok * p.G)) * p.T + wk.first + tok] = jbuf[row * C::LDO + D] * 0.69314718055994531f;
         } else {
           reinterpret_cast<float4*>(p.part_o)[(slot * (16 * NMT) + r) * (D / 4) + c] = a;
-          if (c == 0) p.part_l[slot * (16 * NMT) + r] = mlb[32 + row];
+          if (c == 0) p.part_l[slot * (16 * NMT) + r] = jbuf[row * C::LDO + D];
         }
       }
-      if (first_piece && tid == 0) {
-        // first and last CTA of the unit this range begins in the middle of (whose ranges hold its first and last tile)
-        const long long u0 = wk.base + static_cast<long long>(h) * wk.n, u1 = u0 + wk.n - 1;
-        const int c0 = static_cast<int>(((u0 + 1) * nc - 1) / W), c1 = static_cast<int>(((u1 + 1) * nc - 1) / W);
-        p.meta[blockIdx.x] = t0 == 0 ? make_int4(-1, 0, 0, 0) : make_int4(wk.s, h, c0, c1);
-      }
-      first_piece = false;
-      w += t1 - t0;
-      if (w < w1 && t1 == wk.n && h == p.Hkv - 1) walk_next<KT>(p, wk);
+      w = pc.next;
+      if (w < w1 && h == p.Hkv - 1) walk_next<KT>(p, wk);
     }
   }
   __syncthreads();
@@ -603,38 +650,60 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, 1)
 // Joins the partials of the units that several ranges share. Block c looks after the unit that range c begins in
 // the middle of, if it is the first such range: M = max lse_k, lse = M + log2 sum 2^(lse_k - M),
 // out = sum 2^(lse_k - lse) O_k, in the order of the ranges (deterministic).
+// A warp takes a row (d = 128: a float4 a lane; d = 64: two rows): its lanes fetch the parts' lse side by side, and the
+// parts' values are fetched eight at a time before they are needed, so the chain is two trips to L2 for up to 32 parts.
 template <int D, int BF16>
 __global__ void __launch_bounds__(128) combine_kernel(const DecParams p, int rows) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 m = p.meta[blockIdx.x];
+  const int4 m = __ldcg(p.meta + 2 * blockIdx.x), q = __ldcg(p.meta + 2 * blockIdx.x + 1);
   if (m.x < 0 || static_cast<int>(blockIdx.x) != m.z + 1) return;
-  const int h = m.y, c0 = m.z, c1 = m.w;
-  int first;
-  const int qlen = seq_tokens(p.cu, m.x, p.T, &first);
-  const int n = min(rows, qlen * p.G);
-  auto slot_of = [&](int c) -> long long { return 2LL * c + (c == c0 ? 1 : 0); };
-  for (int e = threadIdx.x; e < n * (D / 4); e += 128) {
-    const int r = e / (D / 4), c = e % (D / 4);
-    float M = -INFINITY;
-    for (int k = c0; k <= c1; ++k) M = fmaxf(M, p.part_l[slot_of(k) * rows + r]);
+  const int h = m.y, c0 = m.z, parts = m.w - c0 + 1;
+  const int first = q.x, n = min(rows, q.y * p.G);  // the sequence's first token and rows
+  constexpr int LPR = D / 4;       // lanes of a row
+  constexpr int RPW = 32 / LPR;    // rows of a warp
+  const int lane = threadIdx.x & 31, c = lane % LPR;
+  auto slot_of = [&](int k) -> long long { return 2LL * (c0 + k) + (k == 0 ? 1 : 0); };
+  for (int r0 = (threadIdx.x >> 5) * RPW; r0 < n; r0 += 4 * RPW) {
+    const int r = min(r0 + lane / LPR, n - 1);  // (a row past the end repeats the last one)
+    float M = -INFINITY, L = 0.0f;
     float4 a = make_float4(0, 0, 0, 0);
-    float L = 0.0f;
-    for (int k = c0; k <= c1; ++k) {
-      const long long at = slot_of(k) * rows + r;
-      const float lk = p.part_l[at];
-      const float4 b = reinterpret_cast<const float4*>(p.part_o)[at * (D / 4) + c];
-      if (lk == -INFINITY) continue;
-      const float wgt = exp2f(lk - M);
-      L += wgt;
-      a.x = fmaf(wgt, b.x, a.x);
-      a.y = fmaf(wgt, b.y, a.y);
-      a.z = fmaf(wgt, b.z, a.z);
-      a.w = fmaf(wgt, b.w, a.w);
+    for (int k0 = 0; k0 < parts; k0 += LPR) {
+      const int kk = min(LPR, parts - k0);
+      const float lk = c < kk ? __ldcg(p.part_l + slot_of(k0 + c) * rows + r) : -INFINITY;
+      float top = lk;
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float Mn = fmaxf(M, top), Mu = Mn == -INFINITY ? 0.0f : Mn;
+      const float fix = M == -INFINITY ? 0.0f : exp2f(M - Mu);
+      const float w = lk == -INFINITY ? 0.0f : exp2f(lk - Mu);  // NaN passes on
+      M = Mn;
+      L *= fix;
+      a.x *= fix;
+      a.y *= fix;
+      a.z *= fix;
+      a.w *= fix;
+      for (int k = 0; k < kk; k += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (slot_of(k0 + min(k + u, kk - 1)) * rows + r) * LPR + c);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, w, (lane & ~(LPR - 1)) + min(k + u, LPR - 1));
+          if (k + u < kk) {
+            L += wu;
+            a.x = fmaf(wu, v[u].x, a.x);
+            a.y = fmaf(wu, v[u].y, a.y);
+            a.z = fmaf(wu, v[u].z, a.z);
+            a.w = fmaf(wu, v[u].w, a.w);
+          }
+        }
+      }
     }
     const float inv = L > 0.0f ? 1.0f / L : (L != L ? NAN : 0.0f);
     const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
     const long long at = static_cast<long long>(first + tok) * p.Hq + hq;
-    reinterpret_cast<uint2*>(p.out)[at * (D / 4) + c] =
+    reinterpret_cast<uint2*>(p.out)[at * LPR + c] =
         make_uint2(pack16(a.x * inv, a.y * inv, BF16), pack16(a.z * inv, a.w * inv, BF16));
     if (p.lse && c == 0)
       p.lse[static_cast<long long>(hq) * p.T + first + tok] =
@@ -676,14 +745,16 @@ int launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p
 
 int tile_keys(const PagedArgs& a) { return a.cache_dtype == CQSA_E4M3 || a.d == 64 ? 128 : 64; }
 
+int decode_rows(const PagedArgs& a) { return static_cast<long long>(a.max_q_len) * (a.Hq / a.Hkv) <= 16 ? 16 : 32; }
+
 // One CTA per SM, fewer when there are fewer key tiles (by the caller's longest sequence; longer ones are
 // still computed, with fewer CTAs than they could use).
 int decode_ctas(const PagedArgs& a) {
   const long long kt = tile_keys(a);
   const long long tiles = (a.max_kv_len + kt - 1) / kt;
-  const long long all = (tiles < 1 ? 1 : tiles) * a.n_seqs * a.Hkv;
-  const int sms = sm_count();
-  return static_cast<int>(all < sms ? all : sms);
+  const long long all = ((tiles < 1 ? 1 : tiles) + kUnit) * a.n_seqs * a.Hkv;
+  const int most = sm_count() * decode_occ(a.cache_dtype == CQSA_E4M3, decode_rows(a) / 16);
+  return static_cast<int>(all < most ? all : most);
 }
 
 }  // namespace
@@ -691,9 +762,9 @@ int decode_ctas(const PagedArgs& a) {
 bool decode_applies(const PagedArgs& a) { return static_cast<long long>(a.max_q_len) * (a.Hq / a.Hkv) <= 32; }
 
 size_t decode_workspace(const PagedArgs& a) {
-  const size_t rows = static_cast<long long>(a.max_q_len) * (a.Hq / a.Hkv) <= 16 ? 16 : 32;
+  const size_t rows = static_cast<size_t>(decode_rows(a));
   const size_t n = 2 * static_cast<size_t>(decode_ctas(a));
-  return ((n * rows * a.d * 4 + 255) & ~size_t(255)) + ((n * rows * 4 + 255) & ~size_t(255)) + n / 2 * sizeof(int4);
+  return ((n * rows * a.d * 4 + 255) & ~size_t(255)) + ((n * rows * 4 + 255) & ~size_t(255)) + n * sizeof(int4);
 }
 
 int launch_decode(const PagedArgs& a, cudaStream_t stream) {
@@ -703,7 +774,7 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream) {
   int rc = make_page_map(&mk, a.k_cache, a, rows_box);
   if (rc == CQSA_OK) rc = make_page_map(&mv, a.v_cache, a, rows_box);
   if (rc != CQSA_OK) return rc;
-  const int rows = a.max_q_len * (a.Hq / a.Hkv), rr = rows <= 16 ? 16 : 32;
+  const int rr = decode_rows(a);
   const int ctas = decode_ctas(a);
   DecParams p;
   memset(&p, 0, sizeof(p));
@@ -736,11 +807,11 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream) {
   p.timeout_us = timeout_us();
   const bool bf = a.dtype == CQSA_BF16;
   if (a.cache_dtype == CQSA_E4M3) {
-    if (a.d == 64) return bf ? launch_rows<64, 1, true>(mk, mv, p, rows, ctas, stream) : launch_rows<64, 0, true>(mk, mv, p, rows, ctas, stream);
-    return bf ? launch_rows<128, 1, true>(mk, mv, p, rows, ctas, stream) : launch_rows<128, 0, true>(mk, mv, p, rows, ctas, stream);
+    if (a.d == 64) return bf ? launch_rows<64, 1, true>(mk, mv, p, rr, ctas, stream) : launch_rows<64, 0, true>(mk, mv, p, rr, ctas, stream);
+    return bf ? launch_rows<128, 1, true>(mk, mv, p, rr, ctas, stream) : launch_rows<128, 0, true>(mk, mv, p, rr, ctas, stream);
   }
-  if (a.d == 64) return bf ? launch_rows<64, 1, false>(mk, mv, p, rows, ctas, stream) : launch_rows<64, 0, false>(mk, mv, p, rows, ctas, stream);
-  return bf ? launch_rows<128, 1, false>(mk, mv, p, rows, ctas, stream) : launch_rows<128, 0, false>(mk, mv, p, rows, ctas, stream);
+  if (a.d == 64) return bf ? launch_rows<64, 1, false>(mk, mv, p, rr, ctas, stream) : launch_rows<64, 0, false>(mk, mv, p, rr, ctas, stream);
+  return bf ? launch_rows<128, 1, false>(mk, mv, p, rr, ctas, stream) : launch_rows<128, 0, false>(mk, mv, p, rr, ctas, stream);
 }
 
 DEV_ERR_READERS(decode, g_decode_err)

@@ -157,7 +157,7 @@ struct PackedArgs {
 };
 int launch_packed(const PackedArgs& a, cudaStream_t stream);
 // The gradients: a.out and a.lse are the forward's. workspace: packed_bwd_workspace bytes.
-size_t packed_bwd_workspace(int T, int Hq, int d);
+size_t packed_bwd_workspace(int n_seqs, int T, int Hq, int Hkv, int d);
 int launch_packed_bwd(const PackedArgs& a, const void* dout, void* dq, void* dk, void* dv, void* workspace, cudaStream_t stream);
 
 // Tensor maps (seq_api.cu). `strides` are bytes of dimensions 1 and up.

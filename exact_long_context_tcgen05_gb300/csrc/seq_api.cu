@@ -243,9 +243,9 @@ int cqsa_attn_packed_fwd(const void* q, const void* k, const void* v, long long 
   return launch_packed(a, stream);
 }
 
-size_t cqsa_attn_packed_bwd_workspace_size(int T, int Hq, int d) {
-  if (T < 1 || Hq < 1 || (d != 64 && d != 128) || static_cast<long long>(T) * Hq > 0x7fffffffLL) return 0;
-  return packed_bwd_workspace(T, Hq, d);
+size_t cqsa_attn_packed_bwd_workspace_size(int n_seqs, int T, int Hq, int Hkv, int d) {
+  if (T < 1 || check_seqs(n_seqs, T, Hq, Hkv, d, 0.0f, CQSA_F16) != CQSA_OK) return 0;
+  return packed_bwd_workspace(n_seqs, T, Hq, Hkv, d);
 }
 
 int cqsa_attn_packed_bwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
@@ -258,7 +258,7 @@ int cqsa_attn_packed_bwd(const void* q, const void* k, const void* v, long long 
   if (rc != CQSA_OK || T == 0) return rc;
   if (!dout || !lse || !dq || !dk || !dv || !aligned(dout, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16))
     return invalid("dout, dq, dk, dv (16-byte aligned) and lse must be non-null device pointers");
-  const size_t need = packed_bwd_workspace(T, Hq, d);
+  const size_t need = packed_bwd_workspace(n_seqs, T, Hq, Hkv, d);
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) {
     set_error("a 16-byte aligned workspace of the %zu bytes that cqsa_attn_packed_bwd_workspace_size reports is needed (got %zu)",
               need, workspace ? workspace_bytes : static_cast<size_t>(0));

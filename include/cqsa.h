@@ -376,9 +376,9 @@ int cqsa_attn_packed_fwd(const void* q, const void* k, const void* v, long long 
 /* Its gradients, from the forward's out and lse and the upstream gradient dout (device [T, Hq, d] contiguous): dq device
  * [T, Hq, d], dk, dv device [T, Hkv, d], contiguous, written for the sequences' tokens; dk and dv sum over the query heads of
  * a group. The formulas are cqsa_attn_bwd's; P and dS are rounded to dtype for their products, sums are fp32.
- * workspace: at least cqsa_attn_packed_bwd_workspace_size(T, Hq, d) bytes, 16-byte aligned, contents on entry do not
+ * workspace: at least cqsa_attn_packed_bwd_workspace_size bytes for the same arguments, 16-byte aligned, contents on entry do not
  * matter. dk and dv are bitwise reproducible; dq follows the order of fp32 atomic adds, as in cqsa_attn_bwd. */
-size_t cqsa_attn_packed_bwd_workspace_size(int T, int Hq, int d);
+size_t cqsa_attn_packed_bwd_workspace_size(int n_seqs, int T, int Hq, int Hkv, int d);
 int cqsa_attn_packed_bwd(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
                          long long v_stride, const void* out, const void* dout, const float* lse, void* dq, void* dk, void* dv,
                          void* workspace, size_t workspace_bytes, const int* cu_seqlens, int n_seqs, int T, int Hq, int Hkv,

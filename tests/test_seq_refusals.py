@@ -52,7 +52,7 @@ CACHE = dict(k=FAKE, v=FAKE, k_stride=0, v_stride=0, k_cache=FAKE, v_cache=FAKE,
 PAGES = [(dict(k_cache=0), -1, "non-null"), (dict(v_cache=FAKE + 8), -1, "16-byte"), (dict(block_table=0), -1, "non-null"),
          (dict(block_table=FAKE + 2), -1, "4-byte"), (dict(page_size=8), -2, "page size"), (dict(page_size=48), -2, "page size"),
          (dict(page_size=512), -2, "page size"), (dict(n_pages=0), -1, "positive"), (dict(max_pages=0), -1, "positive"),
-         (dict(max_pages=2 ** 27, page_size=16), -2, "too many"), (dict(cache_dtype=1), -2, "cache_dtype"),
+         (dict(max_pages=2 ** 27, page_size=16), -2, "too many"), (dict(n_pages=2 ** 30), -2, "too large"), (dict(cache_dtype=1), -2, "cache_dtype"),
          (dict(cache_dtype=2), -2, "cache_dtype"), (dict(cache_dtype=3), -1, "k_scale"),
          (dict(cache_dtype=3, k_scale=FAKE, v_scale=FAKE + 8), -1, "16-byte"), (dict(kv_lens=0), -1, "kv_lens"),
          (dict(cu_seqlens=FAKE + 1), -1, "cu_seqlens")]
@@ -84,8 +84,8 @@ def test_paged(cq, change, status, word):
 
 
 def test_workspace_sizes(cq):
-    assert cq.cqsa_attn_packed_bwd_workspace_size(1000, 8, 64) >= 1000 * 8 * (64 * 4 + 8)
-    for bad in ((0, 8, 64), (10, 0, 64), (10, 8, 96), (2 ** 30, 8, 64)):
+    assert cq.cqsa_attn_packed_bwd_workspace_size(3, 1000, 8, 2, 64) >= 1000 * 8 * (64 * 4 + 8)
+    for bad in ((3, 0, 8, 2, 64), (3, 10, 0, 2, 64), (3, 10, 8, 2, 96), (3, 2 ** 30, 8, 2, 64), (0, 10, 8, 2, 64), (3, 10, 8, 0, 64)):
         assert cq.cqsa_attn_packed_bwd_workspace_size(*bad) == 0
     assert cq.cqsa_attn_paged_workspace_size(4, 4, 8, 2, 128, 16, 1, 1000, 0, 0) > 0
     assert cq.cqsa_attn_paged_workspace_size(4, 0, 8, 2, 128, 16, 1, 1000, 0, 0) == 0
