@@ -18,11 +18,10 @@
 //            fp16 keeps its relative precision down to p = 2^-28.
 //   Tails    rows of V past a sequence's end (another sequence's tokens, or whatever an unused slot holds) are zeroed in
 //            shared memory before the product: p = 0 does not hide an infinity or NaN there.
-//   e4m3     four converter warps take the place of the K/V copies: they gather codes from the pages,
-//            a 16-byte piece a lane, and store fp16 tiles in the swizzled layout. Each warp converts 32
-//            keys relative to their largest power of two (exact but for values 2^-15 below it); that power
-//            goes into the scores' scale (K) and into an exponent that P is shifted by (V). Queries are fp16:
-//            bf16 ones are first scaled to [1, 2) by a power of two per row, in place.
+//   e4m3     the producer copies code vectors as they lie in the pages, and four converter warps turn them into
+//            swizzled fp16 tiles, each key relative to the largest power of two met so far (exact but for values 2^-15
+//            below it). K's power goes into the scores' scale; V's is a reference that O is rescaled to when it rises.
+//            Queries are fp16: bf16 ones are first scaled to [1, 2) by a power of two per row, in place.
 #include <math.h>
 #include <string.h>
 
@@ -58,26 +57,28 @@ struct SeqCfg {
   static constexpr bool BY8 = SRC == kSrcPages;
   static constexpr uint32_t GROUP = BY8 ? 1024u * (D / 64) : 1024u;   // from 8 keys to the next 8
   static constexpr uint32_t HALF = BY8 ? 1024u : TILE_BYTES;          // from features 0-63 to 64-127
-  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int STAGES = D == 64 ? (CONV ? 3 : 4) : 2;
   static constexpr uint32_t QT_BYTES = KSUB * TILE_BYTES;
   static constexpr uint32_t KV_BYTES = KSUB * TILE_BYTES;
   static constexpr uint32_t COL_S0 = 0, COL_S1 = 128;
   static constexpr uint32_t COL_P0 = ALIAS ? 0u : 256u, COL_P1 = ALIAS ? 128u : 320u;
   static constexpr uint32_t COL_O0 = ALIAS ? 256u : 384u, COL_O1 = COL_O0 + D;
-  static constexpr int NBARS = 1 + 4 * STAGES + 2 * 7 + 2 + 2;
+  static constexpr int NBARS = 1 + 4 * STAGES + 2 * 7 + 2 + 2 + 4;
   // key tiles between folds of O into the fp32 running sum (attn_fwd.cu explains why): in shared memory
   // for d = 64, in the SM's slot of attn_fwd.cu's array for d = 128
   static constexpr int FLUSH = D == 64 ? 128 : 32;
   static constexpr bool OSUM_SMEM = D == 64;
   static constexpr uint32_t OSUM_BYTES = OSUM_SMEM ? 2u * D * 128u * 4u : 0u;
-  static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 8u * 4u + 256u * 4u : 0u;
-  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + EXP_BYTES + NBARS * 8 + 64;
+  static constexpr uint32_t RAW = CONV ? 128u * D : 0u;  // a K or V tile's codes as they lie in the pages
+  // running exponents per tile, factors of the queries' rows, the converter warps' largest exponents
+  static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 2u * 4u + 256u * 4u + 64u : 0u;
+  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 64;
   static_assert(SMEM_BYTES <= 232448, "shared memory exceeds 227 KiB");
   static_assert(COL_O1 + D <= TMEM_COLS, "tensor memory layout exceeds 512 columns");
   // setmaxnreg shares of warpgroup 0, the two softmax warpgroups and the converters
   static constexpr int NTHR = CONV ? 512 : 384;
   static constexpr int LAUNCH_REGS = CONV ? 128 : 168;
-  static constexpr int LOW = CONV ? 56 : 72, HIGH = CONV ? 184 : 216, CVT = 88;
+  static constexpr int LOW = CONV ? 40 : 72, HIGH = CONV ? 200 : 216, CVT = 72;
   static_assert(128 * LOW + 256 * HIGH + (CONV ? 128 * CVT : 0) <= NTHR * LAUNCH_REGS, "register split exceeds the launch allocation");
 };
 
@@ -130,16 +131,6 @@ __device__ __forceinline__ float2 exp2_pair(float x0, float x1, float2 sl2v, flo
   return make_float2(fast_exp2(r.x), fast_exp2(r.y));
 }
 
-__device__ __forceinline__ float row_max32(const float* x) {
-  float m0 = x[0], m1 = x[1];
-#pragma unroll
-  for (int c = 2; c < 30; c += 4) {
-    m0 = max3(m0, x[c], x[c + 1]);
-    m1 = max3(m1, x[c + 2], x[c + 3]);
-  }
-  return fmaxf(max3(m0, x[30], x[31]), m1);
-}
-
 // Zero keys [r0, 128) of a K or V tile (a whole warp): a key's row is 128 bytes of each half, and the swizzle only
 // moves 16-byte pieces inside it.
 template <class C>
@@ -164,8 +155,10 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   uint8_t* sK = sQ + 2 * C::QT_BYTES;
   uint8_t* sV = sK + STAGES * C::KV_BYTES;
   float* sOsum = reinterpret_cast<float*>(sV + STAGES * C::KV_BYTES);
-  int* sExp = reinterpret_cast<int*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES);  // [2 * STAGES][K 4 | V 4]
-  float* sRow = reinterpret_cast<float*>(sExp + 2 * STAGES * 8);                     // [256] factor of a row's queries
+  uint8_t* sRaw = sV + STAGES * C::KV_BYTES + C::OSUM_BYTES;  // e4m3: K and V codes
+  int* sExp = reinterpret_cast<int*>(sRaw + 2 * C::RAW);       // [2 * STAGES][K, V] exponents that a tile is relative to
+  float* sRow = reinterpret_cast<float*>(sExp + 2 * STAGES * 2);  // [256] factor of a row's queries
+  int* sTop = reinterpret_cast<int*>(sRow + 256);                 // [2][4 warps][K, V] largest exponents of a tile
   bool osum_ok = true;
   if (!C::OSUM_SMEM) {
     uint32_t smid;
@@ -173,7 +166,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     osum_ok = smid < static_cast<uint32_t>(p.n_osum);
     sOsum = p.osum + static_cast<size_t>(osum_ok ? smid : 0u) * (2 * 128 * 128);
   }
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES + C::EXP_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES + 2 * C::RAW + C::EXP_BYTES);
   uint64_t* bar_q = bars;
   uint64_t* bar_k_full = bar_q + 1;
   uint64_t* bar_v_full = bar_k_full + STAGES;
@@ -191,7 +184,9 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   uint64_t* bar_mma_idle = bar_o_final + 2;      // [2]
   uint64_t* bar_fix = bar_mma_idle + 2;          // the last V tile landed (its rows past the end are zeroed then)
   uint64_t* bar_q2 = bar_fix + 1;                // e4m3, bf16 queries: converted in place
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_q2 + 1);
+  uint64_t* bar_raw = bar_q2 + 1;                // [2] e4m3: codes of K, V landed
+  uint64_t* bar_raw_free = bar_raw + 2;          // [2] read by the converters
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_raw_free + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* sUnit = reinterpret_cast<int*>(tmem_slot + 2);  // [2]
 
@@ -237,6 +232,10 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     }
     mbar_init(bar_fix, 1);
     mbar_init(bar_q2, 4);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bar_raw[x], 1);
+      mbar_init(&bar_raw_free[x], 4);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   } else if (warp == 3 && lane == 0) {
@@ -371,6 +370,36 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         for (int j = max(0, v_issued - STAGES); j < v_issued; ++j)
           if (j != skipped && kleft - j * BN >= BN) mbar_wait_bounded(&bar_v_full[j % STAGES], (j / STAGES) & 1u, tmo);
         if (fixed) mbar_wait_bounded(bar_fix, 0, tmo);
+      }
+      if constexpr (CONV) {
+        // codes of a tile, page by page (a page's vectors of one head lie together), into the one raw buffer of K and of V
+        const int page = 1 << p.page_log2, rows = min(page, BN), boxes = BN / rows;
+        const int* trow = p.table + static_cast<long long>(seq) * p.max_pages;
+        int issued[2] = {0, 0};
+        bool ok = true;
+        for (int j = 0; ok && j < n_max; ++j) {
+          if (p.fault == 1 && blockIdx.x == 0 && j == 1) break;
+          const int nb = min(boxes, (kleft - j * BN + rows - 1) / rows);
+          long long at = 0;
+          if (lane < nb) {
+            const int pos = kbase + j * BN + lane * rows;
+            const int pg = page_at(trow, pos >> p.page_log2, p.n_pages);
+            at = (((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + (pos & (page - 1))) * D;
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            ok = ok && wait_or_abort(smem_u32(&bar_raw_free[x]), (j & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 36 + x);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], static_cast<uint32_t>(nb) * rows * D);
+            __syncwarp();
+            if (lane < nb)
+              bulk_load(sRaw + x * C::RAW + lane * rows * D, (x ? p.v_cache : p.k_cache) + at, rows * D, &bar_raw[x]);
+            issued[x] = j + 1;
+          }
+        }
+        for (int x = 0; x < 2; ++x)
+          if (issued[x] > 0) mbar_wait_bounded(&bar_raw[x], (issued[x] - 1) & 1u, tmo);
       }
       mbar_wait_bounded(bar_q, 0, tmo);
     } else if ((warp == 1 || warp == 2) && n_max > 0) {
@@ -581,35 +610,23 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           for (int c = 0; c < 128; ++c)
             if (c >= lim) x[c] = -INFINITY;
         }
-        // e4m3: each 32 keys have their own scale of scores and exponent of values
-        float slc[4], shc[4];
         float alpha = 1.0f;
         bool rescale = false;
-        float tmax;
-        if constexpr (CONV) {
-          const int* ex = sExp + (j % (2 * STAGES)) * 8;
-          int top = -100000;
-          tmax = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // held above 0, so that a masked score times it stays -inf (scores that small are 0 either way)
-            slc[c] = fmaxf(sl2 * exp2_int_any(ex[c]), 0x1p-100f);
-            tmax = fmaxf(tmax, row_max32(x + c * 32) * slc[c]);
-            top = max(top, ex[4 + c]);
-          }
-          if (top > ev) {
-            if (ev > -100000) {
-              alpha = exp2_int(static_cast<float>(max(ev - top, -200)));
+        float slt = sl2;
+        if constexpr (CONV) {  // this tile's K and V are relative to these powers of two, which only rise
+          const int2 ex = *reinterpret_cast<const int2*>(sExp + (j % (2 * STAGES)) * 2);
+          // held above 0, so that a masked score times it stays -inf (scores that small are 0 either way)
+          slt = fmaxf(sl2 * exp2_int_any(ex.x), 0x1p-100f);
+          if (ex.y > ev) {
+            if (j > 0) {
+              alpha = exp2_int(static_cast<float>(max(ev - ex.y, -200)));
               rescale = true;
             }
-            ev = top;
+            ev = ex.y;
           }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) shc[c] = static_cast<float>(max(ex[4 + c] - ev, -60));
-        } else {
-          tmax = row_max128(x) * sl2;
         }
-        float al_l = 1.0f;  // what the row's sum is multiplied by (it does not depend on the values' exponent)
+        const float tmax = row_max128(x) * slt;
+        float al_l = 1.0f;  // what the row's sum is multiplied by (the values' exponent does not matter to it)
         if (tmax > m_ref + kTau || (m_ref == -INFINITY && tmax > -INFINITY)) {
           const float m_new = ceilf(tmax);
           if (m_ref != -INFINITY) {
@@ -667,9 +684,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           sum = 0.0f;
 #pragma unroll
           for (int c4 = 0; c4 < 4; ++c4) {
-            const float s1 = CONV ? slc[c4] : sl2;
-            const float c1 = CONV ? cm - shc[c4] : cm;
-            const float2 sl2v = make_float2(s1, s1), ncm = make_float2(-c1, -c1);
+            const float2 sl2v = make_float2(slt, slt), ncm = make_float2(-cm, -cm);
             float2 rs2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             uint32_t hi[16];
 #pragma unroll
@@ -688,8 +703,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
               for (int e = 64; e < 128; ++e) asm volatile("" : "+f"(x[e]));
             }
-            const float part = (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
-            sum += CONV ? part * exp2_int_any(static_cast<int>(-shc[c4])) : part;
+            sum += (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
           }
         }
         l = l * al_l + sum;
@@ -807,87 +821,105 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bar_q2);
       }
-      // K and V tiles: this warp's 32 keys; a 16-byte piece of a code vector per lane and step
+      // K and V tiles: this warp's 32 keys, a 16-byte piece of a code vector per lane and step. The exponents of this
+      // lane's key are fetched a tile ahead, its page two.
       constexpr int LPR = D / 16;        // lanes of a row
       constexpr int RPS = 32 / LPR;      // rows of a step
-      constexpr int NST = 32 / RPS;      // steps
       const int* trow = p.table + static_cast<long long>(seq) * p.max_pages;
       const int page_mask = (1 << p.page_log2) - 1;
-      auto row_of = [&](int j) -> long long {  // lane's key row of tile j as a vector index of its head, -1 past the end
+      constexpr int NONE = -100000;
+      // (what a load returns is left alone until a later tile: any arithmetic on it here would wait for it)
+      auto page_of = [&](int j) -> int {
         const int k = j * BN + w * 32 + lane;
-        if (j >= n_max || k >= kleft) return -1;
-        const int pos = kbase + k;
-        const int pg = page_at(trow, pos >> p.page_log2, p.n_pages);
-        return ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + (pos & page_mask);
+        return j < n_max && k < kleft ? __ldg(trow + ((kbase + k) >> p.page_log2)) : NONE;
       };
-      auto fetch = [&](const uint8_t* cache, long long vec, uint4 (&raw)[NST]) {
-#pragma unroll
-        for (int i = 0; i < NST; ++i) {
-          const long long v = __shfl_sync(0xffffffffu, vec, i * RPS + lane / LPR);
-          raw[i] = v < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4*>(cache + v * D) + lane % LPR);
-        }
+      auto exps_of = [&](int j, int pg) -> int2 {  // this lane's key's bytes in tile j, 0 past the end
+        if (j >= n_max || j * BN + w * 32 + lane >= kleft) return make_int2(0, 0);
+        if (pg < 0 || pg >= p.n_pages) pg = 0;
+        const long long vec = ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + ((kbase + j * BN + w * 32 + lane) & page_mask);
+        return make_int2(__ldg(p.k_scale + vec), __ldg(p.v_scale + vec));
       };
-      auto store = [&](uint8_t* tile, const uint4 (&raw)[NST], int exps, int ref) {
+      // 2^e in both halves of a register, for e <= 0 (0 below fp16's numbers)
+      auto pow2h = [&](int e) -> uint32_t { return (e >= -14 ? (e + 15) << 10 : (e < -24 ? 0 : 1 << (e + 24))) * 0x10001u; };
+      // row of step i: w * 32 + i * RPS + lane / LPR. 16 features are two 16-byte pieces of the fp16 row; at d = 128 the
+      // lanes of the second half store them in the other order, so that a row's eight lanes always meet eight different
+      // banks. The swizzle of step i differs from that of step 0 by bit 2 of the row (d = 128) or not at all.
+      const int c0 = 2 * (lane % LPR);
+      const int flip = D == 128 ? (c0 >> 3) : 0;
+      const int r0 = w * 32 + lane / LPR;
+      const uint32_t to = (c0 >> 3) * TILE_BYTES + r0 * 128;
+      const uint32_t p0 = (((c0 + flip) & 7) ^ (r0 & 7)) << 4, p1 = (((c0 + 1 - flip) & 7) ^ (r0 & 7)) << 4;
+      const uint32_t from = smem_u32(sRaw) + r0 * D + (lane % LPR) * 16;
+      auto convert = [&](uint32_t raw, uint32_t tile, uint32_t factor, bool tail) {
 #pragma unroll
-        for (int i = 0; i < NST; ++i) {
-          const int rr = i * RPS + lane / LPR;
-          const int e = __shfl_sync(0xffffffffu, exps, rr) - ref;  // <= 0
-          const __half f = e < -24 ? __ushort_as_half(0) : __ushort_as_half(e >= -14 ? static_cast<unsigned short>((e + 15) << 10)
-                                                                                     : static_cast<unsigned short>(1 << (e + 24)));
-          const __half2 f2 = __halves2half2(f, f);
-          const int row = w * 32 + rr;
-          const uint32_t cw[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          uint32_t h[8];
+        for (int i = 0; i < 32 / RPS; ++i) {
+          uint32_t c[4], h[8];
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + i * RPS * D));
+          const uint32_t f = __shfl_sync(0xffffffffu, factor, i * RPS + lane / LPR);
+          if (tail && f == 0xffffffffu) c[0] = c[1] = c[2] = c[3] = 0u;  // past the end: whatever the slot holds
+          const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            uint32_t a = e4m3x2_to_f16x2(cw[u] & 0xffffu), b = e4m3x2_to_f16x2(cw[u] >> 16);
+            uint32_t a = e4m3x2_to_f16x2(c[u] & 0xffffu), b = e4m3x2_to_f16x2(c[u] >> 16);
             __half2 ha = __hmul2(*reinterpret_cast<__half2*>(&a), f2), hb = __hmul2(*reinterpret_cast<__half2*>(&b), f2);
+            if (tail && f == 0xffffffffu) ha = hb = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
             h[2 * u] = *reinterpret_cast<uint32_t*>(&ha);
             h[2 * u + 1] = *reinterpret_cast<uint32_t*>(&hb);
           }
-          const int c0 = 2 * (lane % LPR);  // 16 features = two 16-byte pieces of the fp16 row
-          uint8_t* dst = tile + (c0 >> 3) * TILE_BYTES + row * 128;
-          *reinterpret_cast<uint4*>(dst + (((c0 & 7) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + ((((c0 + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+          const uint32_t dst = tile + to + i * RPS * 128, x = D == 128 ? (i & 1) * 64u : 0u;
+          const bool fl = flip != 0;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (p0 ^ x)), "r"(fl ? h[4] : h[0]), "r"(fl ? h[5] : h[1]),
+                       "r"(fl ? h[6] : h[2]), "r"(fl ? h[7] : h[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (p1 ^ x)), "r"(fl ? h[0] : h[4]), "r"(fl ? h[1] : h[5]),
+                       "r"(fl ? h[2] : h[6]), "r"(fl ? h[3] : h[7]) : "memory");
         }
       };
-      long long vec = row_of(0), next = row_of(1);
-      uint4 rk[NST], rv[NST];
-      int ek = -100000, evv = -100000;
-      auto fetch_tile = [&]() {
-        ek = vec < 0 ? -100000 : static_cast<int>(__ldg(p.k_scale + vec)) - 127;
-        evv = vec < 0 ? -100000 : static_cast<int>(__ldg(p.v_scale + vec)) - 127;
-        fetch(p.k_cache, vec, rk);
-        fetch(p.v_cache, vec, rv);
-      };
-      if (n_max > 0 && ok) fetch_tile();
-      for (int j = 0; ok && j < n_max; ++j) {
+      int pg = page_of(1);
+      int2 eb = exps_of(0, page_of(0));
+      int kref = NONE, vref = NONE;  // the largest exponents so far
+      for (int j = 0; j < n_max; ++j) {
         const int stage = j % STAGES;
-        ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (p.fault == 1 && blockIdx.x == 0 && j == 1) break;  // test hook: the tile never arrives
-        const int kref = __reduce_max_sync(0xffffffffu, ek), vref = __reduce_max_sync(0xffffffffu, evv);
-        if (lane == 0) {
-          // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
-          int* ex = sExp + (j % (2 * STAGES)) * 8;
-          ex[w] = kref < -1000 ? 0 : kref;
-          ex[4 + w] = vref;
+        const bool tail = kleft - j * BN < BN;
+        const bool in = j * BN + w * 32 + lane < kleft;
+        const int2 ex = in ? make_int2(eb.x - 127, eb.y - 127) : make_int2(NONE, NONE);
+        eb = exps_of(j + 1, pg);
+        pg = page_of(j + 2);
+        const int kt = __reduce_max_sync(0xffffffffu, ex.x), vt = __reduce_max_sync(0xffffffffu, ex.y);
+        int* top = sTop + (j & 1) * 8;
+        if (lane == 0) *reinterpret_cast<int2*>(top + w * 2) = make_int2(kt, vt);
+        named_sync(1, 128);  // every converter warp comes here for every tile, whatever else has given up
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int2 t = *reinterpret_cast<const int2*>(top + i * 2);
+          kref = max(kref, t.x);
+          vref = max(vref, t.y);
         }
-        store(sK + stage * C::KV_BYTES, rk, ek, kref);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_k_full[stage]);
-        ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
+        if (ok) ok = wait_or_abort(smem_u32(&bar_raw[0]), j & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 38);
+        if (ok) ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        store(sV + stage * C::KV_BYTES, rv, evv, vref);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_v_full[stage]);
-        vec = next;
-        next = row_of(j + 2);
-        if (j + 1 < n_max) fetch_tile();
+        if (ok) {
+          // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
+          if (w == 0 && lane == 0) *reinterpret_cast<int2*>(sExp + (j % (2 * STAGES)) * 2) = make_int2(kref, vref);
+          convert(from, smem_u32(sK) + stage * C::KV_BYTES, in ? pow2h(ex.x - kref) : 0xffffffffu, tail);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar_k_full[stage]);
+            mbar_arrive(&bar_raw_free[0]);
+          }
+          ok = wait_or_abort(smem_u32(&bar_raw[1]), j & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 39);
+          if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (ok) {
+          convert(from + C::RAW, smem_u32(sV) + stage * C::KV_BYTES, in ? pow2h(ex.y - vref) : 0xffffffffu, tail);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bar_v_full[stage]);
+            mbar_arrive(&bar_raw_free[1]);
+          }
+        }
       }
     }
     tc_fence_before();
