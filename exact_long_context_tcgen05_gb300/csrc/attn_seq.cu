@@ -63,7 +63,7 @@ struct SeqCfg {
   static constexpr uint32_t COL_S0 = 0, COL_S1 = 128;
   static constexpr uint32_t COL_P0 = ALIAS ? 0u : 256u, COL_P1 = ALIAS ? 128u : 320u;
   static constexpr uint32_t COL_O0 = ALIAS ? 256u : 384u, COL_O1 = COL_O0 + D;
-  static constexpr int NBARS = 1 + 4 * STAGES + 2 * 7 + 2 + 2 + 4;
+  static constexpr int NBARS = 1 + 4 * STAGES + 2 * 7 + 2 + 2 + 4 + 6;
   // key tiles between folds of O into the fp32 running sum (attn_fwd.cu explains why): in shared memory
   // for d = 64, in the SM's slot of attn_fwd.cu's array for d = 128
   static constexpr int FLUSH = D == 64 ? 128 : 32;
@@ -71,8 +71,8 @@ struct SeqCfg {
   static constexpr uint32_t OSUM_BYTES = OSUM_SMEM ? 2u * D * 128u * 4u : 0u;
   static constexpr uint32_t RAW = CONV ? 128u * D : 0u;  // a K or V tile's codes as they lie in the pages
   // running exponents per tile, factors of the queries' rows, the converter warps' largest exponents
-  static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 2u * 4u + 256u * 4u + 64u : 0u;
-  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 64;
+  static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 2u * 4u + 512u + 64u : 0u;
+  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 80;
   static_assert(SMEM_BYTES <= 232448, "shared memory exceeds 227 KiB");
   static_assert(COL_O1 + D <= TMEM_COLS, "tensor memory layout exceeds 512 columns");
   // setmaxnreg shares of warpgroup 0, the two softmax warpgroups and the converters
@@ -80,6 +80,11 @@ struct SeqCfg {
   static constexpr int LAUNCH_REGS = CONV ? 128 : 168;
   static constexpr int LOW = CONV ? 40 : 72, HIGH = CONV ? 200 : 216, CVT = 72;
   static_assert(128 * LOW + 256 * HIGH + (CONV ? 128 * CVT : 0) <= NTHR * LAUNCH_REGS, "register split exceeds the launch allocation");
+};
+
+// What a CTA works on next, as its scheduling warp hands it to the others.
+struct Work {
+  int valid, seq, tok_first, qlen, kvlen, ta, hk, split;
 };
 
 struct SeqParams {
@@ -157,8 +162,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   float* sOsum = reinterpret_cast<float*>(sV + STAGES * C::KV_BYTES);
   uint8_t* sRaw = sV + STAGES * C::KV_BYTES + C::OSUM_BYTES;  // e4m3: K and V codes
   int* sExp = reinterpret_cast<int*>(sRaw + 2 * C::RAW);       // [2 * STAGES][K, V] exponents that a tile is relative to
-  float* sRow = reinterpret_cast<float*>(sExp + 2 * STAGES * 2);  // [256] factor of a row's queries
-  int* sTop = reinterpret_cast<int*>(sRow + 256);                 // [2][4 warps][K, V] largest exponents of a tile
+  int8_t* sRow = reinterpret_cast<int8_t*>(sExp + 2 * STAGES * 2);  // [2][256] exponents that the queries' rows are relative to
+  int* sTop = reinterpret_cast<int*>(sRow + 512);                   // [2][4 warps][K, V] largest exponents of a tile
   bool osum_ok = true;
   if (!C::OSUM_SMEM) {
     uint32_t smid;
@@ -186,29 +191,19 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   uint64_t* bar_q2 = bar_fix + 1;                // e4m3, bf16 queries: converted in place
   uint64_t* bar_raw = bar_q2 + 1;                // [2] e4m3: codes of K, V landed
   uint64_t* bar_raw_free = bar_raw + 2;          // [2] read by the converters
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_raw_free + 2);
+  uint64_t* bar_top = bar_raw_free + 2;          // e4m3: a tile's exponents exchanged between the converters
+  uint64_t* bar_q_free = bar_top + 1;            // every S of the unit issued and done
+  uint64_t* bar_unit = bar_q_free + 1;           // [2] next unit written
+  uint64_t* bar_unit_free = bar_unit + 2;        // [2] read by every warp that works on it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar_unit_free + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* sUnit = reinterpret_cast<int*>(tmem_slot + 2);  // [2]
+  Work* sWork = reinterpret_cast<Work*>(tmem_slot + 2);  // [2]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // ---- this CTA's unit, tensor memory and barriers, side by side
-  const int per_rank = p.Hkv * p.n_splits;
-  const int rank = static_cast<int>(blockIdx.x / static_cast<unsigned>(per_rank));
-  const int sub = static_cast<int>(blockIdx.x) - rank * per_rank;
-  const int split = sub % p.n_splits, hk = sub / p.n_splits;
-  if (warp == 0) {
-    const int per = 2 * p.tpt;
-    const Unit u = find_unit(p.n_seqs, rank, lane, [&](int i) {
-      int first;
-      return (seq_tokens(p.cu, i, p.T, &first) + per - 1) / per;
-    });
-    if (lane == 0) {
-      sUnit[0] = u.seq;
-      sUnit[1] = u.place;
-    }
-  } else if (warp == 1) {
+  // ---- tensor memory and barriers, side by side
+  if (warp == 1) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   } else if (warp == 2 && lane == 0) {
@@ -235,7 +230,11 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bar_raw[x], 1);
       mbar_init(&bar_raw_free[x], 4);
+      mbar_init(&bar_unit[x], 1);
+      mbar_init(&bar_unit_free[x], 1 + 2 + 8 + (CONV ? 4 : 0));
     }
+    mbar_init(bar_top, 4);
+    mbar_init(bar_q_free, 2);
     *abort_flag = 0;
     fence_mbar_init();
   } else if (warp == 3 && lane == 0) {
@@ -249,43 +248,101 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int seq = sUnit[0];
-  if (seq < 0) {  // the grid is an upper bound on the units
-    __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
-    return;
-  }
   if (threadIdx.x == 0 && !osum_ok) record_dev_error(&g_seq_err, kDevSmSlot, 30);  // exact all the same; only the fold is skipped
-
-  // ---- the unit: two row tiles of tpt tokens each, and the key tiles [jb, jb + n_max) of the sequence
-  int tok_first;
-  const int qlen = seq_tokens(p.cu, seq, p.T, &tok_first);
-  const int kvlen = SRC == kSrcPacked ? qlen
-                                      : seq_positions(p.kv_lens, seq, static_cast<long long>(p.max_pages) << p.page_log2);
-  const int q_off = kvlen - qlen;  // position of the sequence's first new token (negative: rows that see nothing)
-  const int ta = sUnit[1] * 2 * p.tpt, tb = ta + p.tpt;  // first token of each row tile
-  auto tile_kv = [&](int t0) -> int {  // key tiles that the row tile may see
-    const int n = min(p.tpt, qlen - t0);
-    if (n <= 0 || kvlen == 0) return 0;
-    const int last = p.causal ? min(kvlen - 1, q_off + t0 + n - 1) : kvlen - 1;
-    return last < 0 ? 0 : last / BN + 1;
-  };
-  const int all0 = tile_kv(ta), all1 = tile_kv(tb), all = max(all0, all1);
-  const int jb = static_cast<int>(static_cast<long long>(all) * split / p.n_splits);
-  const int je = static_cast<int>(static_cast<long long>(all) * (split + 1) / p.n_splits);
-  const int nkv0 = min(max(all0 - jb, 0), je - jb), nkv1 = min(max(all1 - jb, 0), je - jb);
-  const int n_max = max(nkv0, nkv1);
-  const int kbase = jb * BN;         // position of the range's first key
-  const int kleft = kvlen - kbase;   // positions of the sequence from there
   const uint32_t tmo_us = p.timeout_us;
   const uint64_t tmo = static_cast<uint64_t>(tmo_us) * 1000ull;
   const uint32_t a_abort = smem_u32(const_cast<int*>(abort_flag));
   constexpr bool CONVQ = CONV && BF16;
 
+  // A CTA works through units u = blockIdx.x, and then one of every gridDim.x, in an order that turns round every time (the
+  // heaviest of one round with the lightest of the next). Warp 3 finds them, two ahead; every other warp takes them from
+  // shared memory, so a unit's loads and first products run beside the end of the one before. Barrier phases count
+  // on across units: kb key tiles of the CTA, tb of a row tile.
+  struct View {
+    Work w;
+    int tb, jb, nkv0, nkv1, n_max, kbase, kleft, q_off;
+  };
+  // The unit's two row tiles of tpt tokens each, and its key tiles [jb, jb + n_max) of the sequence.
+  auto view_of = [&](const Work& w) -> View {
+    View v;
+    v.w = w;
+    v.tb = w.ta + p.tpt;
+    v.q_off = w.kvlen - w.qlen;  // position of the sequence's first new token (negative: rows that see nothing)
+    auto tile_kv = [&](int t0) -> int {  // key tiles that the row tile may see
+      const int n = min(p.tpt, w.qlen - t0);
+      if (n <= 0 || w.kvlen == 0) return 0;
+      const int last = p.causal ? min(w.kvlen - 1, v.q_off + t0 + n - 1) : w.kvlen - 1;
+      return last < 0 ? 0 : last / BN + 1;
+    };
+    const int all0 = tile_kv(w.ta), all1 = tile_kv(v.tb), all = max(all0, all1);
+    v.jb = static_cast<int>(static_cast<long long>(all) * w.split / p.n_splits);
+    const int je = static_cast<int>(static_cast<long long>(all) * (w.split + 1) / p.n_splits);
+    v.nkv0 = min(max(all0 - v.jb, 0), je - v.jb);
+    v.nkv1 = min(max(all1 - v.jb, 0), je - v.jb);
+    v.n_max = max(v.nkv0, v.nkv1);
+    v.kbase = v.jb * BN;             // position of the range's first key
+    v.kleft = w.kvlen - v.kbase;     // positions of the sequence from there
+    return v;
+  };
+  // The i-th unit of this CTA; false when there is none, or a role has given up.
+  auto take = [&](int i, View* v) -> bool {
+    const bool ok = wait_or_abort(smem_u32(&bar_unit[i & 1]), (i >> 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 40);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const int4 a = *reinterpret_cast<const int4*>(&sWork[i & 1]), b = *(reinterpret_cast<const int4*>(&sWork[i & 1]) + 1);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar_unit_free[i & 1]);
+    const Work w = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (!w.valid) return false;
+    *v = view_of(w);
+    return true;
+  };
+
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LOW));
-    if (warp == 0 && n_max > 0) {
+    if (warp == 3) {
+      // ------------------------------------------------------------------ units
+      const unsigned per_rank = static_cast<unsigned>(p.Hkv * p.n_splits);
+      const int per = 2 * p.tpt;
+      for (int i = 0;; ++i) {
+        const unsigned u = static_cast<unsigned>(i) * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const int rank = static_cast<int>(u / per_rank), sub = static_cast<int>(u - rank * per_rank);
+        const Unit f = find_unit(p.n_seqs, rank, lane, [&](int k) {
+          int first;
+          return (seq_tokens(p.cu, k, p.T, &first) + per - 1) / per;
+        });
+        Work w = {f.seq >= 0, f.seq, 0, 0, 0, f.place * per, sub / p.n_splits, sub % p.n_splits};
+        if (w.valid) {
+          w.qlen = seq_tokens(p.cu, f.seq, p.T, &w.tok_first);
+          w.kvlen = SRC == kSrcPacked ? w.qlen : seq_positions(p.kv_lens, f.seq, static_cast<long long>(p.max_pages) << p.page_log2);
+        }
+        if (i >= 2) {
+          const bool ok = wait_or_abort(smem_u32(&bar_unit_free[i & 1]), ((i >> 1) - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 41);
+          if (!__all_sync(0xffffffffu, ok)) break;
+        }
+        if (lane == 0) {
+          *reinterpret_cast<int4*>(&sWork[i & 1]) = make_int4(w.valid, w.seq, w.tok_first, w.qlen);
+          *(reinterpret_cast<int4*>(&sWork[i & 1]) + 1) = make_int4(w.kvlen, w.ta, w.hk, w.split);
+          mbar_arrive(&bar_unit[i & 1]);
+        }
+        __syncwarp();
+        if (!w.valid) break;
+      }
+    } else if (warp == 0) {
       // ------------------------------------------------------------------ TMA producer
+      View v;
+      int kb = 0, uq = 0, fixes = 0;          // key tiles, units with any, tails so far
+      int k_last[4] = {0, 0, 0, 0}, v_last[4] = {0, 0, 0, 0};  // loads of each stage
+      int raw_last[2] = {0, 0};
+      bool ok = true;
+      for (int unit = 0; ok && take(unit, &v); ++unit) {
+      if (v.n_max == 0) continue;
+      const int tok_first = v.w.tok_first, hk = v.w.hk, kbase = v.kbase, kleft = v.kleft, n_max = v.n_max, seq = v.w.seq;
+      if (uq > 0) {
+        ok = wait_or_abort(smem_u32(bar_q_free), (uq - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 42);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      ++uq;
       const uint32_t q_bytes = static_cast<uint32_t>(p.tpt) * p.G * 128u;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar_q, 2 * KSUB * q_bytes);
@@ -293,18 +350,16 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int x = 0; x < KSUB; ++x)
-            tma_load_3d(sQ + t * C::QT_BYTES + x * TILE_BYTES, &tmQ, bar_q, x * 64, hk * p.G, tok_first + (t ? tb : ta));
+            tma_load_3d(sQ + t * C::QT_BYTES + x * TILE_BYTES, &tmQ, bar_q, x * 64, hk * p.G, tok_first + (t ? v.tb : v.w.ta));
       }
       if constexpr (!CONV) {
         const int page = SRC == kSrcPages ? 1 << p.page_log2 : BN;
         const int rows = min(page, BN);
         const int boxes = BN / rows;
         const int* trow = SRC == kSrcPages ? p.table + static_cast<long long>(seq) * p.max_pages : nullptr;
-        int k_issued = 0, v_issued = 0, skipped = -1;
-        bool fixed = false;
         for (int j = 0; j < n_max; ++j) {
-          const int stage = j % STAGES;
-          const uint32_t round = j / STAGES;
+          const int stage = (kb + j) % STAGES;
+          const uint32_t round = (kb + j) / STAGES;
           const int left = kleft - j * BN;
           const int nb = min(boxes, (left + rows - 1) / rows);
           int pg = 0, y = 0;
@@ -314,14 +369,14 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             y = pos & (page - 1);
           }
           const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
-          bool ok = wait_or_abort(smem_u32(ALIAS ? &bar_k_empty[stage] : &bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          k_issued = j + 1;
-          if (p.fault == 1 && blockIdx.x == 0 && j == 1) {
-            v_issued = j + 1;
-            skipped = j;
-            continue;
+          ok = wait_or_abort(smem_u32(ALIAS ? &bar_k_empty[stage] : &bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (p.fault == 1 && blockIdx.x == 0 && j == 1) {  // (every wait on the tile runs out)
+            ok = false;
+            break;
           }
+          k_last[stage & 3] = round + 1;
           if (lane == 0) mbar_arrive_expect_tx(&bar_k_full[stage], bytes);
           __syncwarp();
           if (lane < nb) {
@@ -336,10 +391,11 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           }
           if (ALIAS) {
             ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 34);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
           }
-          v_issued = j + 1;
           const bool tail = left < BN;
+          if (!tail) v_last[stage & 3] = round + 1;
           uint64_t* vbar = tail ? bar_fix : &bar_v_full[stage];
           if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
           __syncwarp();
@@ -355,30 +411,25 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           }
           __syncwarp();
           if (tail) {  // at most the last key tile of the sequence
-            fixed = true;
-            ok = wait_or_abort(smem_u32(bar_fix), 0, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 31);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            ok = wait_or_abort(smem_u32(bar_fix), fixes & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 31);
+            ++fixes;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             zero_rows<C>(sV + stage * C::KV_BYTES, left, lane);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_v_full[stage]);
+            v_last[stage & 3] = 0;  // waited for
           }
         }
-        // every load issued lands before the CTA exits (bounded waits; already complete on the normal path)
-        for (int j = max(0, k_issued - STAGES); j < k_issued; ++j)
-          if (j != skipped) mbar_wait_bounded(&bar_k_full[j % STAGES], (j / STAGES) & 1u, tmo);
-        for (int j = max(0, v_issued - STAGES); j < v_issued; ++j)
-          if (j != skipped && kleft - j * BN >= BN) mbar_wait_bounded(&bar_v_full[j % STAGES], (j / STAGES) & 1u, tmo);
-        if (fixed) mbar_wait_bounded(bar_fix, 0, tmo);
       }
       if constexpr (CONV) {
         // codes of a tile, page by page (a page's vectors of one head lie together), into the one raw buffer of K and of V
         const int page = 1 << p.page_log2, rows = min(page, BN), boxes = BN / rows;
         const int* trow = p.table + static_cast<long long>(seq) * p.max_pages;
-        int issued[2] = {0, 0};
-        bool ok = true;
         for (int j = 0; ok && j < n_max; ++j) {
-          if (p.fault == 1 && blockIdx.x == 0 && j == 1) break;
+          if (p.fault == 1 && blockIdx.x == 0 && j == 1) ok = false;  // (every wait on the tile runs out)
+          if (!ok) break;
           const int nb = min(boxes, (kleft - j * BN + rows - 1) / rows);
           long long at = 0;
           if (lane < nb) {
@@ -388,28 +439,37 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            ok = ok && wait_or_abort(smem_u32(&bar_raw_free[x]), (j & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 36 + x);
+            ok = ok && wait_or_abort(smem_u32(&bar_raw_free[x]), ((kb + j) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 36 + x);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], static_cast<uint32_t>(nb) * rows * D);
             __syncwarp();
             if (lane < nb)
               bulk_load(sRaw + x * C::RAW + lane * rows * D, (x ? p.v_cache : p.k_cache) + at, rows * D, &bar_raw[x]);
-            issued[x] = j + 1;
+            raw_last[x] = kb + j + 1;
           }
         }
-        for (int x = 0; x < 2; ++x)
-          if (issued[x] > 0) mbar_wait_bounded(&bar_raw[x], (issued[x] - 1) & 1u, tmo);
       }
-      mbar_wait_bounded(bar_q, 0, tmo);
-    } else if ((warp == 1 || warp == 2) && n_max > 0) {
+      kb += n_max;
+      }
+      // every load issued lands before the CTA exits (bounded waits; already complete on the normal path; a tail that ran
+      // out is given one more limit)
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i) {
+        if (k_last[i] > 0) mbar_wait_bounded(&bar_k_full[i], (k_last[i] - 1) & 1u, tmo);
+        if (v_last[i] > 0) mbar_wait_bounded(&bar_v_full[i], (v_last[i] - 1) & 1u, tmo);
+      }
+      for (int x = 0; x < 2; ++x)
+        if (raw_last[x] > 0) mbar_wait_bounded(&bar_raw[x], (raw_last[x] - 1) & 1u, tmo);
+      if (!ok && fixes > 0) mbar_wait_bounded(bar_fix, (fixes - 1) & 1u, tmo);
+      if (uq > 0) mbar_wait_bounded(bar_q, (uq - 1) & 1u, tmo);
+    } else {
       // ------------------------------------------------------------------ MMA issuers, one per row tile
       // P apart from S: each on its own schedule. P over S: the tiles take turns, so that a tile's P V and next S run
       // back to back. Without turns the two tiles' groups interleave in the tensor pipe, both finish late, and both softmax
       // warpgroups then compute at the same time (3,640 cycles a key tile at d = 128); one warp issuing for both took
       // 3,300, of which 1,250 went into its own waits and commits.
       const int t = warp - 1;
-      const int nkv = t ? nkv1 : nkv0;
       const bool leader = elect_one();
       constexpr uint32_t IDESC_S = idesc_f16(MB, 0, 128, 128);
       constexpr uint32_t IDESC_O = idesc_f16(MB, 1, 128, D);
@@ -423,83 +483,101 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         const bool w = wait_or_abort(smem_u32(bar), parity, tmo_us, a_abort, &g_seq_err, code, where);
         return __all_sync(0xffffffffu, w);
       };
-      auto do_s = [&](int j, bool pass) {
-        const uint64_t b0 = dK + static_cast<uint32_t>(j % STAGES) * (C::KV_BYTES >> 4);
-        tc_fence_after();
-        if (leader) {
-          issue_s<0, D / 32, C::HALF>(col_s, dQ, b0, IDESC_S);
-          if (pass) mbar_arrive(&bar_turn[t ^ 1]);  // the other tile's issuer wakes up while the rest goes in
-          issue_s<D / 32, D / 16, C::HALF>(col_s, dQ, b0, IDESC_S);
-          tc_commit(&bar_s_full[t]);
-          if (ALIAS) tc_commit(&bar_k_empty[j % STAGES]);
-        }
-        __syncwarp();
-      };
-      // keys of half `part` (P over S: the first half's product runs while the softmax writes the second), or all (2)
-      auto do_pv = [&](int j, int part) {
-        const uint64_t v0 = dV + static_cast<uint32_t>(j % STAGES) * (C::KV_BYTES >> 4);
-        const bool first = (j == 0) || (osum_ok && j % C::FLUSH == 0);  // O restarts at every segment
-        tc_fence_after();
-        if (leader) {
-          if (part == 2) {
-            if (first) issue_o<true, 0, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
-            else issue_o<false, 0, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
-          } else if (part == 0) {
-            if (first) issue_o<true, 0, 4, C::GROUP>(col_o, col_p, v0, IDESC_O);
-            else issue_o<false, 0, 4, C::GROUP>(col_o, col_p, v0, IDESC_O);
-          } else {
-            issue_o<false, 4, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
+      View v;
+      int kb = 0, tb = 0, uq = 0;  // key tiles of the CTA, of this row tile, units with any
+      bool ok = true;
+      for (int unit = 0; ok && take(unit, &v); ++unit) {
+        const int nkv = t ? v.nkv1 : v.nkv0, n_max = v.n_max;
+        if (n_max == 0) continue;
+        auto do_s = [&](int j, bool pass) {
+          const int stage = (kb + j) % STAGES;
+          const uint64_t b0 = dK + static_cast<uint32_t>(stage) * (C::KV_BYTES >> 4);
+          tc_fence_after();
+          if (leader) {
+            issue_s<0, D / 32, C::HALF>(col_s, dQ, b0, IDESC_S);
+            if (pass) mbar_arrive(&bar_turn[t ^ 1]);  // the other tile's issuer wakes up while the rest goes in
+            issue_s<D / 32, D / 16, C::HALF>(col_s, dQ, b0, IDESC_S);
+            tc_commit(&bar_s_full[t]);
+            if (ALIAS) tc_commit(&bar_k_empty[stage]);
+            if (j == nkv - 1) tc_commit(bar_q_free);
           }
-          if (part != 0) {
-            tc_commit(&bar_pv_done[t]);
-            if (j == nkv - 1) tc_commit(&bar_o_final[t]);
-            tc_commit(&bar_v_empty[j % STAGES]);
-          }
-        }
-        __syncwarp();
-      };
-      bool ok = wait_all(CONVQ ? bar_q2 : bar_q, 0, kDevTimeoutQ, 11);
-      if (ok && nkv > 0) {
-        ok = wait_all(&bar_k_full[0], 0, kDevTimeoutKV, 12);
-        if (ok) do_s(0, false);
-      }
-      for (int j = 0; ok && j < n_max; ++j) {
-        const int stage = j % STAGES, n1 = (j + 1) % STAGES;
-        const uint32_t par1 = ((j + 1) / STAGES) & 1u;
-        if (j < nkv) {
-          if (!ALIAS) {
-            if (j + 1 < nkv) {
-              ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
-              if (ok) ok = wait_all(&bar_s_free[t], j & 1u, kDevTimeoutSoftmax, 14);
-              if (ok) do_s(j + 1, false);
+          __syncwarp();
+        };
+        // keys of half `part` (P over S: the first half's product runs while the softmax writes the second), or all (2)
+        auto do_pv = [&](int j, int part) {
+          const int stage = (kb + j) % STAGES;
+          const uint64_t v0 = dV + static_cast<uint32_t>(stage) * (C::KV_BYTES >> 4);
+          const bool first = (j == 0) || (osum_ok && j % C::FLUSH == 0);  // O restarts at every segment
+          tc_fence_after();
+          if (leader) {
+            if (part == 2) {
+              if (first) issue_o<true, 0, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
+              else issue_o<false, 0, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
+            } else if (part == 0) {
+              if (first) issue_o<true, 0, 4, C::GROUP>(col_o, col_p, v0, IDESC_O);
+              else issue_o<false, 0, 4, C::GROUP>(col_o, col_p, v0, IDESC_O);
+            } else {
+              issue_o<false, 4, 8, C::GROUP>(col_o, col_p, v0, IDESC_O);
             }
-            if (ok) ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 15);
-            if (ok) ok = wait_all(&bar_p_full[t], j & 1u, kDevTimeoutSoftmax, 16);
-            if (ok) do_pv(j, 2);
-          } else {
-            ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 15);
-            if (ok && j + 1 < nkv) ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
-            if (ok) ok = wait_all(&bar_p_half[t], j & 1u, kDevTimeoutSoftmax, 17);
-            if (ok) ok = wait_all(&bar_turn[t], (j & 1u) ^ (t ? 0u : 1u), kDevTimeoutMMA, 24);
-            if (ok) do_pv(j, 0);
-            if (ok) ok = wait_all(&bar_p_full[t], j & 1u, kDevTimeoutSoftmax, 16);
-            if (ok) do_pv(j, 1);
-            // P_t(j) lies over S_t: MMAs of one issuing thread run in order, so S_t(j+1) follows P V's reads
-            if (ok && j + 1 < nkv) do_s(j + 1, true);
-            else if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
+            if (part != 0) {
+              tc_commit(&bar_pv_done[t]);
+              if (j == nkv - 1) tc_commit(&bar_o_final[t]);
+              tc_commit(&bar_v_empty[stage]);
+            }
           }
-        } else {
-          // a key tile that only the other row tile sees: wait for its loads, so that the releases belong to their phases
-          ok = wait_all(&bar_k_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 21);
-          if (ALIAS && ok && leader) mbar_arrive(&bar_k_empty[stage]);
-          if (ok) ok = wait_all(&bar_v_full[stage], (j / STAGES) & 1u, kDevTimeoutKV, 22);
-          if (ok && leader) mbar_arrive(&bar_v_empty[stage]);
-          if (ALIAS) {
-            if (ok) ok = wait_all(&bar_turn[t], (j & 1u) ^ (t ? 0u : 1u), kDevTimeoutMMA, 25);
-            if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
-          }
+          __syncwarp();
+        };
+        ok = wait_all(CONVQ ? bar_q2 : bar_q, uq & 1u, kDevTimeoutQ, 11);
+        ++uq;
+        if (ok && nkv > 0) {
+          ok = wait_all(&bar_k_full[kb % STAGES], (kb / STAGES) & 1u, kDevTimeoutKV, 12);
+          // (P apart: the softmax has read the last S of the unit before; P over S: P V before it in this thread's order)
+          if (!ALIAS && ok && tb > 0) ok = wait_all(&bar_s_free[t], (tb - 1) & 1u, kDevTimeoutSoftmax, 43);
+          if (ok) do_s(0, false);
+        } else if (ok && leader) {
+          mbar_arrive(bar_q_free);
         }
-        __syncwarp();
+        for (int j = 0; ok && j < n_max; ++j) {
+          const int stage = (kb + j) % STAGES, n1 = (kb + j + 1) % STAGES;
+          const uint32_t par0 = ((kb + j) / STAGES) & 1u, par1 = ((kb + j + 1) / STAGES) & 1u;
+          const uint32_t tp = (tb + j) & 1u, turn = ((kb + j) & 1u) ^ (t ? 0u : 1u);
+          if (j < nkv) {
+            if (!ALIAS) {
+              if (j + 1 < nkv) {
+                ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
+                if (ok) ok = wait_all(&bar_s_free[t], tp, kDevTimeoutSoftmax, 14);
+                if (ok) do_s(j + 1, false);
+              }
+              if (ok) ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 15);
+              if (ok) ok = wait_all(&bar_p_full[t], tp, kDevTimeoutSoftmax, 16);
+              if (ok) do_pv(j, 2);
+            } else {
+              ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 15);
+              if (ok && j + 1 < nkv) ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
+              if (ok) ok = wait_all(&bar_p_half[t], tp, kDevTimeoutSoftmax, 17);
+              if (ok) ok = wait_all(&bar_turn[t], turn, kDevTimeoutMMA, 24);
+              if (ok) do_pv(j, 0);
+              if (ok) ok = wait_all(&bar_p_full[t], tp, kDevTimeoutSoftmax, 16);
+              if (ok) do_pv(j, 1);
+              // P_t(j) lies over S_t: MMAs of one issuing thread run in order, so S_t(j+1) follows P V's reads
+              if (ok && j + 1 < nkv) do_s(j + 1, true);
+              else if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
+            }
+          } else {
+            // a key tile that only the other row tile sees: wait for its loads, so that the releases belong to their phases
+            ok = wait_all(&bar_k_full[stage], par0, kDevTimeoutKV, 21);
+            if (ALIAS && ok && leader) mbar_arrive(&bar_k_empty[stage]);
+            if (ok) ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 22);
+            if (ok && leader) mbar_arrive(&bar_v_empty[stage]);
+            if (ALIAS) {
+              if (ok) ok = wait_all(&bar_turn[t], turn, kDevTimeoutMMA, 25);
+              if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
+            }
+          }
+          __syncwarp();
+        }
+        kb += n_max;
+        tb += nkv;
       }
       if (leader) tc_commit(&bar_mma_idle[warp - 1]);
       __syncwarp();
@@ -524,21 +602,24 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     const uint32_t colO = wg ? C::COL_O1 : C::COL_O0;
     const uint32_t a_s_full = smem_u32(&bar_s_full[wg]), a_s_free = smem_u32(&bar_s_free[wg]);
     const uint32_t a_p_full = smem_u32(&bar_p_full[wg]), a_pv_done = smem_u32(&bar_pv_done[wg]);
-    const int nkv = wg ? nkv1 : nkv0;
-    const int t0 = wg ? tb : ta;
     const int rt = r / p.G;                     // token of this thread's row within the tile
-    const int rel = q_off + t0 - kbase;         // key position (in the range) of the tile's first token
+    const int SEG = osum_ok ? C::FLUSH : (1 << 30);
+    View v;
+    int kb = 0, tb = 0, uq = 0, uo = 0;  // key tiles of the CTA and of this row tile, units with any for either
+    bool ok = true;
+    for (int unit = 0; ok && take(unit, &v); ++unit) {
+    const int nkv = wg ? v.nkv1 : v.nkv0, n_max = v.n_max, kleft = v.kleft;
+    const int t0 = wg ? v.tb : v.w.ta;
+    const int rel = v.q_off + t0 - v.kbase;     // key position (in the range) of the tile's first token
     const int row_lim = p.causal ? rel + rt + 1 : 0x7fffffff;
     const int diag = p.causal ? rel - (BN - 1) : 0x7fffffff;  // tiles from beyond this key on hide keys from some row
     float sl2 = p.scale_log2;
     float m_ref = -INFINITY, l = 0.0f, m_sum = -INFINITY;
     int ev = -100000, ev_sum = 0;  // e4m3: exponent of the values that O (the running sum) is relative to
-    bool ok = true;
-    const int SEG = osum_ok ? C::FLUSH : (1 << 30);
     for (int j0 = 0; ok && j0 < nkv; j0 += SEG) {
       if (j0 > 0) {
         // fold O into the running sum, brought from its reference to the current one by an exact power of two
-        ok = wait_or_abort(a_pv_done, (j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
+        ok = wait_or_abort(a_pv_done, (tb + j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -582,12 +663,12 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       }
       const int j1 = (nkv - j0 < SEG) ? nkv : j0 + SEG;
       for (int j = j0; j < j1; ++j) {
-        ok = wait_or_abort(a_s_full, j & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
+        ok = wait_or_abort(a_s_full, (tb + j) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        if (CONVQ && j == 0) sl2 = p.scale_log2 * sRow[wg * 128 + r];  // written before the queries were released
+        if (CONVQ && j == 0) sl2 = p.scale_log2 * exp2_int_any(sRow[(uq & 1) * 256 + wg * 128 + r]);  // written before the queries were released
         tc_fence_after();
         uint32_t sr[128];
 #pragma unroll
@@ -614,7 +695,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         bool rescale = false;
         float slt = sl2;
         if constexpr (CONV) {  // this tile's K and V are relative to these powers of two, which only rise
-          const int2 ex = *reinterpret_cast<const int2*>(sExp + (j % (2 * STAGES)) * 2);
+          const int2 ex = *reinterpret_cast<const int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2);
           // held above 0, so that a masked score times it stays -inf (scores that small are 0 either way)
           slt = fmaxf(sl2 * exp2_int_any(ex.x), 0x1p-100f);
           if (ex.y > ev) {
@@ -666,7 +747,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             pk[c] = pack2(pp.x, pp.y, MB);
           }
           if (j > 0) {
-            ok = wait_or_abort(a_pv_done, (j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
+            ok = wait_or_abort(a_pv_done, (tb + j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
               break;
@@ -715,7 +796,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 
     // ---------------------------------------------------------------- epilogue
     if (ok && nkv > 0) {
-      ok = wait_or_abort(smem_u32(&bar_o_final[wg]), 0, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 20);
+      ok = wait_or_abort(smem_u32(&bar_o_final[wg]), uo & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 20);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
@@ -725,10 +806,10 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     const float lse2 = has ? m_ref - kPShift + log2f(l) : -INFINITY;
     if (CONV) inv_l *= has ? exp2_int_any(min(max(ev, -126), 127)) : 1.0f;
     const int tok = t0 + rt;
-    const bool write = ok && rt < p.tpt && tok < qlen;
-    const int hq = hk * p.G + (r - rt * p.G);
-    const long long row = static_cast<long long>(tok_first + tok) * p.Hq + hq;
-    const long long prow = static_cast<long long>(split) * p.T * p.Hq + row;
+    const bool write = ok && rt < p.tpt && tok < v.w.qlen;
+    const int hq = v.w.hk * p.G + (r - rt * p.G);
+    const long long row = static_cast<long long>(v.w.tok_first + tok) * p.Hq + hq;
+    const long long prow = static_cast<long long>(v.w.split) * p.T * p.Hq + row;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -740,7 +821,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
-      float v[32];
+      float y[32];
       if (osum_ok && nkv > C::FLUSH) {
         const float* os = sOsum + (wg * D + c * 32) * 128 + r;
         float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
@@ -749,10 +830,10 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) prev[e] = C::OSUM_SMEM ? os[e * 128] : __ldcg(os + e * 128);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = (prev[e] * sc + __uint_as_float(o[e])) * inv_l;
+        for (int e = 0; e < 32; ++e) y[e] = (prev[e] * sc + __uint_as_float(o[e])) * inv_l;
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = has ? __uint_as_float(o[e]) * inv_l : 0.0f;
+        for (int e = 0; e < 32; ++e) y[e] = has ? __uint_as_float(o[e]) * inv_l : 0.0f;
       }
       if (write) {
         if (p.n_splits == 1) {
@@ -760,22 +841,28 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
           for (int q8 = 0; q8 < 4; ++q8) {
             uint4 w;
-            w.x = pack2(v[8 * q8 + 0], v[8 * q8 + 1], BF16);
-            w.y = pack2(v[8 * q8 + 2], v[8 * q8 + 3], BF16);
-            w.z = pack2(v[8 * q8 + 4], v[8 * q8 + 5], BF16);
-            w.w = pack2(v[8 * q8 + 6], v[8 * q8 + 7], BF16);
+            w.x = pack2(y[8 * q8 + 0], y[8 * q8 + 1], BF16);
+            w.y = pack2(y[8 * q8 + 2], y[8 * q8 + 3], BF16);
+            w.z = pack2(y[8 * q8 + 4], y[8 * q8 + 5], BF16);
+            w.w = pack2(y[8 * q8 + 6], y[8 * q8 + 7], BF16);
             dst[q8] = w;
           }
         } else {
           float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
 #pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]);
+          for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(y[4 * q4], y[4 * q4 + 1], y[4 * q4 + 2], y[4 * q4 + 3]);
         }
       }
     }
     if (write) {
       if (p.n_splits > 1) p.part_l[prow] = lse2;
-      else if (p.lse) p.lse[static_cast<long long>(hq) * p.T + tok_first + tok] = lse2 * 0.69314718055994531f;
+      else if (p.lse) p.lse[static_cast<long long>(hq) * p.T + v.w.tok_first + tok] = lse2 * 0.69314718055994531f;
+    }
+    tc_fence_before();  // O has been read: the next unit's P hand-offs release its columns
+    kb += n_max;
+    tb += nkv;
+    uq += n_max > 0;
+    uo += nkv > 0;
     }
     tc_fence_before();
     asm volatile("bar.sync 0;" ::: "memory");
@@ -784,18 +871,23 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     if constexpr (CONV) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CVT));
       const int w = warp - 12;
+      View v;
+      int kb = 0, uq = 0;
       bool ok = true;
-      if (CONVQ && n_max > 0) {
+      for (int unit = 0; ok && take(unit, &v); ++unit) {
+      const int n_max = v.n_max, kbase = v.kbase, kleft = v.kleft, hk = v.w.hk;
+      if (n_max == 0) continue;
+      if (CONVQ) {
         // queries in place: this thread's row of each tile, brought to fp16 relative to its largest power of two
-        ok = wait_or_abort(smem_u32(bar_q), 0, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 32);
+        ok = wait_or_abort(smem_u32(bar_q), uq & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 32);
         ok = __all_sync(0xffffffffu, ok);
         const int r = w * 32 + lane;
         for (int t = 0; ok && t < 2; ++t) {
           uint8_t* q = sQ + t * C::QT_BYTES + r * 128;
           float amax = 0.0f;
           for (int i = 0; i < 8 * KSUB; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
-            const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+            const uint4 x = *reinterpret_cast<const uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
+            const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const float2 f = unpack16(ws[u], 1);
@@ -804,11 +896,11 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           }
           const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
           const float inv = pow2i(-e);
-          sRow[t * 128 + r] = pow2i(e);
+          sRow[(uq & 1) * 256 + t * 128 + r] = static_cast<int8_t>(e);
           for (int i = 0; i < 8 * KSUB; ++i) {
             uint4* at = reinterpret_cast<uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
-            const uint4 v = *at;
-            uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+            const uint4 x = *at;
+            uint32_t ws[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const float2 f = unpack16(ws[u], 1);
@@ -825,7 +917,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       // lane's key are fetched a tile ahead, its page two.
       constexpr int LPR = D / 16;        // lanes of a row
       constexpr int RPS = 32 / LPR;      // rows of a step
-      const int* trow = p.table + static_cast<long long>(seq) * p.max_pages;
+      const int* trow = p.table + static_cast<long long>(v.w.seq) * p.max_pages;
       const int page_mask = (1 << p.page_log2) - 1;
       constexpr int NONE = -100000;
       // (what a load returns is left alone until a later tile: any arithmetic on it here would wait for it)
@@ -877,29 +969,33 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       int pg = page_of(1);
       int2 eb = exps_of(0, page_of(0));
       int kref = NONE, vref = NONE;  // the largest exponents so far
-      for (int j = 0; j < n_max; ++j) {
-        const int stage = j % STAGES;
+      for (int j = 0; ok && j < n_max; ++j) {
+        const int stage = (kb + j) % STAGES;
+        const uint32_t free_par = (((kb + j) / STAGES) & 1u) ^ 1u, raw_par = (kb + j) & 1u;
         const bool tail = kleft - j * BN < BN;
         const bool in = j * BN + w * 32 + lane < kleft;
         const int2 ex = in ? make_int2(eb.x - 127, eb.y - 127) : make_int2(NONE, NONE);
         eb = exps_of(j + 1, pg);
         pg = page_of(j + 2);
         const int kt = __reduce_max_sync(0xffffffffu, ex.x), vt = __reduce_max_sync(0xffffffffu, ex.y);
-        int* top = sTop + (j & 1) * 8;
-        if (lane == 0) *reinterpret_cast<int2*>(top + w * 2) = make_int2(kt, vt);
-        named_sync(1, 128);  // every converter warp comes here for every tile, whatever else has given up
+        int* top = sTop + (raw_par) * 8;
+        if (lane == 0) {
+          *reinterpret_cast<int2*>(top + w * 2) = make_int2(kt, vt);
+          mbar_arrive(bar_top);
+        }
+        ok = wait_or_abort(smem_u32(bar_top), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 44);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int2 t = *reinterpret_cast<const int2*>(top + i * 2);
           kref = max(kref, t.x);
           vref = max(vref, t.y);
         }
-        if (ok) ok = wait_or_abort(smem_u32(&bar_raw[0]), j & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 38);
-        if (ok) ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
+        if (ok) ok = wait_or_abort(smem_u32(&bar_raw[0]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 38);
+        if (ok) ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
           // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
-          if (w == 0 && lane == 0) *reinterpret_cast<int2*>(sExp + (j % (2 * STAGES)) * 2) = make_int2(kref, vref);
+          if (w == 0 && lane == 0) *reinterpret_cast<int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2) = make_int2(kref, vref);
           convert(from, smem_u32(sK) + stage * C::KV_BYTES, in ? pow2h(ex.x - kref) : 0xffffffffu, tail);
           fence_async_smem();
           __syncwarp();
@@ -907,8 +1003,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             mbar_arrive(&bar_k_full[stage]);
             mbar_arrive(&bar_raw_free[0]);
           }
-          ok = wait_or_abort(smem_u32(&bar_raw[1]), j & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 39);
-          if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), ((j / STAGES) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
+          ok = wait_or_abort(smem_u32(&bar_raw[1]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 39);
+          if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
           ok = __all_sync(0xffffffffu, ok);
         }
         if (ok) {
@@ -920,6 +1016,9 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             mbar_arrive(&bar_raw_free[1]);
           }
         }
+      }
+      kb += n_max;
+      ++uq;
       }
     }
     tc_fence_before();
@@ -981,7 +1080,8 @@ int launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv
     if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(sequence attention smem)");
     attr.mark(dev);
   }
-  kern<<<static_cast<unsigned>(grid), C::NTHR, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
+  const long long sms = sm_count();
+  kern<<<static_cast<unsigned>(grid < sms ? grid : sms), C::NTHR, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
   int rc = cuda_status(cudaGetLastError(), "sequence attention kernel launch");
   if (rc != CQSA_OK || p.n_splits == 1) return rc;
   cudaLaunchConfig_t cfg;
@@ -1021,16 +1121,29 @@ int make_token_map(CUtensorMap* m, const void* base, int dtype, int d, int heads
 // An upper bound on the pairs of row tiles of n_seqs sequences that hold T tokens together.
 long long pairs_bound(int T, int n_seqs, int tpt) { return T / (2 * tpt) + (T < n_seqs ? T : n_seqs); }
 
-// Ranges that the key tiles of a unit are cut into.
+// Ranges that the key tiles of a unit are cut into: the number with the least estimated time, in microseconds. A key tile
+// takes about 1.2 (d = 64, 0.9), a range about 3 on top, and each further range writes and reads its rows in fp32 at
+// 4 TB/s. One sequence: its units go over the SMs in whole rounds. Several: their lengths are not known here, so
+// the average is taken as 2/5 of the longest, and the longest range follows on the others.
 int chunk_splits(const PagedArgs& a) {
-  const int G = a.Hq / a.Hkv, tpt = 128 / G;
+  const int G = a.Hq / a.Hkv, tpt = 128 / G, sms = sm_count();
   const long long by_tokens = pairs_bound(a.T, a.n_seqs, tpt);
   const long long by_longest = static_cast<long long>(a.n_seqs) * ((a.max_q_len + 2 * tpt - 1) / (2 * tpt));
-  const long long units = (by_tokens < by_longest ? by_tokens : by_longest) * a.Hkv;
-  const long long tiles = (a.max_kv_len + BN - 1) / BN;
-  long long s = units > 0 ? sm_count() / units : 1;
-  if (s > tiles / 4) s = tiles / 4;
-  return static_cast<int>(s < 1 ? 1 : (s > 64 ? 64 : s));
+  const double units = static_cast<double>((by_tokens < by_longest ? by_tokens : by_longest) * a.Hkv);
+  const double n = (a.max_kv_len + BN - 1) / BN, tile = a.d == 64 ? 0.9 : 1.2;
+  const double part = static_cast<double>(a.T) * a.Hq * a.d * 8.0 / 4e6;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= 32 && (s == 1 || s * 4 <= n); ++s) {
+    double us = s > 1 ? s * part + 4.0 : 0.0;
+    if (a.n_seqs == 1) us += ceil(units * s / sms) * (n / s * tile + 3.0);
+    else us += n / s * tile + 3.0 + units * (0.4 * n * tile + 3.0 * s) / sms;
+    if (us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
 }
 
 void fill_common(SeqParams* p, int n_seqs, int T, int Hq, int Hkv, int causal, float scale) {
