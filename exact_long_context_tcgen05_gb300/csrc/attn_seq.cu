@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bar_s_full[t], 1);
-      mbar_init(&bar_s_free[t], 4);
-      // one arrival per thread: per-warp ones measured 1,084 us against 1,000 on 32,768 causal tokens at d = 64
+      // one arrival per thread: with per-warp ones 1,026 us against 1,002 on 32,768 causal tokens at d = 64
+      mbar_init(&bar_s_free[t], 128);
       mbar_init(&bar_p_full[t], 128);
       mbar_init(&bar_p_half[t], 128);
       mbar_init(&bar_turn[t], 1);
@@ -678,8 +678,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
         if (!ALIAS) {
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_a(a_s_free);  // S_t may now take S_t(j+1)
+          mbar_arrive_a(a_s_free);  // S_t may now take S_t(j+1)
         }
         float x[128];
 #pragma unroll
@@ -735,14 +734,12 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         const uint32_t pbuf = trow + colP;
         float sum;
         if constexpr (!ALIAS) {
-          // the two-step exponent of attn_fwd.cu: one instruction a pair more than exp2_pair, and still 988 us against
-          // 1,081 on 32,768 causal tokens (the row tiles' softmax warps fall out of step with each other)
-          const float2 sl2v = make_float2(sl2, sl2), ncm = make_float2(-192.0f - cm, -192.0f - cm);
+          const float2 sl2v = make_float2(sl2, sl2), ncm = make_float2(-cm, -cm);
           float2 rs2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
           uint32_t pk[64];
 #pragma unroll
           for (int c = 0; c < 64; ++c) {
-            const float2 pp = exp_pair(x[2 * c], x[2 * c + 1], sl2v, ncm);
+            const float2 pp = exp2_pair(x[2 * c], x[2 * c + 1], sl2v, ncm);
             rs2[c & 1] = __fadd2_rn(rs2[c & 1], pp);
             pk[c] = pack2(pp.x, pp.y, MB);
           }
@@ -966,23 +963,32 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
                        "r"(fl ? h[2] : h[6]), "r"(fl ? h[3] : h[7]) : "memory");
         }
       };
-      int pg = page_of(1);
+      auto exps_in = [&](int j, int2 b) -> int2 {
+        return j * BN + w * 32 + lane < kleft ? make_int2(b.x - 127, b.y - 127) : make_int2(NONE, NONE);
+      };
+      // the largest exponents of tile j's quarter go to the other warps a tile before they are needed
+      auto send_top = [&](int j, int2 b) {
+        if (j >= n_max) return;
+        const int2 e = exps_in(j, b);
+        const int kt = __reduce_max_sync(0xffffffffu, e.x), vt = __reduce_max_sync(0xffffffffu, e.y);
+        if (lane == 0) {
+          *reinterpret_cast<int2*>(sTop + ((kb + j) & 1) * 8 + w * 2) = make_int2(kt, vt);
+          mbar_arrive(bar_top);
+        }
+      };
       int2 eb = exps_of(0, page_of(0));
+      int pg = page_of(1);
+      send_top(0, eb);
       int kref = NONE, vref = NONE;  // the largest exponents so far
       for (int j = 0; ok && j < n_max; ++j) {
         const int stage = (kb + j) % STAGES;
         const uint32_t free_par = (((kb + j) / STAGES) & 1u) ^ 1u, raw_par = (kb + j) & 1u;
         const bool tail = kleft - j * BN < BN;
         const bool in = j * BN + w * 32 + lane < kleft;
-        const int2 ex = in ? make_int2(eb.x - 127, eb.y - 127) : make_int2(NONE, NONE);
+        const int2 ex = exps_in(j, eb);
         eb = exps_of(j + 1, pg);
         pg = page_of(j + 2);
-        const int kt = __reduce_max_sync(0xffffffffu, ex.x), vt = __reduce_max_sync(0xffffffffu, ex.y);
-        int* top = sTop + (raw_par) * 8;
-        if (lane == 0) {
-          *reinterpret_cast<int2*>(top + w * 2) = make_int2(kt, vt);
-          mbar_arrive(bar_top);
-        }
+        const int* top = sTop + raw_par * 8;
         ok = wait_or_abort(smem_u32(bar_top), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 44);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1003,6 +1009,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             mbar_arrive(&bar_k_full[stage]);
             mbar_arrive(&bar_raw_free[0]);
           }
+          send_top(j + 1, eb);
           ok = wait_or_abort(smem_u32(&bar_raw[1]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 39);
           if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
           ok = __all_sync(0xffffffffu, ok);
