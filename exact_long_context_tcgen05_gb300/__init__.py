@@ -423,9 +423,23 @@ def attention_backward(q, k, v, out, dout, lse, *, causal=False, scale=None, str
 # stream; what they allocate belongs to that stream. A serving step makes one of these calls per layer, so they look at
 # each tensor once and pass addresses straight on.
 
+_torch = None
+_codes: dict = {}
+
+
+def _tc():
+    """torch, imported by the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        _codes.update({torch.float16: CQSA_F16, torch.bfloat16: CQSA_BF16})
+    return _torch
+
+
 def _elsewhere(device, stream):
     """A context that makes `device` current and `stream` its current stream, or None where they already are."""
-    import torch
+    torch = _tc()
     here = device.index == torch.cuda.current_device()
     if here and stream is None:
         return None
@@ -442,18 +456,26 @@ def _elsewhere(device, stream):
 
 def _current(device):
     """The cudaStream_t of the device's current stream."""
-    import torch
+    torch = _tc()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return (raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream) or None
 
 
+def _code(dtype):
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype} (float16 or bfloat16)")
+    return code
+
+
 def _tokens(name, t, heads, d, like):
     """A [T, heads, d] tensor of like's dtype and device, its heads dense; returns it (a copy if need be) and its token stride."""
-    if t.shape[1:] != (heads, d) or t.dtype != like.dtype or t.device != like.device:
+    shape = t.shape
+    if t is not like and (t.dtype != like.dtype or t.device != like.device) or len(shape) != 3 or shape[1] != heads or shape[2] != d:
         raise ValueError(f"{name} must be a [T, {heads}, {d}] tensor of {like.dtype} on {like.device}")
     if t.is_contiguous() and not t.data_ptr() & 15:
         return t, heads * d
-    T = t.shape[0]
+    T = shape[0]
     s = t.stride()
     if (s[2] != 1 or (s[1] != d and heads > 1) or s[0] < heads * d or s[0] % 8 or t.data_ptr() & 15) and T > 0:
         t = t.clone() if t.is_contiguous() else t.contiguous()
@@ -462,14 +484,13 @@ def _tokens(name, t, heads, d, like):
 
 
 def _ints(name, t, shape, device):
-    import torch
-    if t.dtype != torch.int32 or t.device != device or t.shape != shape:
-        raise ValueError(f"{name} must be an int32 tensor of shape {shape} on {device}")
+    if t.dtype != _tc().int32 or t.device != device or t.shape != shape:
+        raise ValueError(f"{name} must be an int32 tensor of shape {tuple(shape)} on {device}")
     return t if t.is_contiguous() else t.contiguous()
 
 
 def _out(out, q):
-    import torch
+    torch = _tc()
     if out is None:
         return torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
@@ -480,7 +501,7 @@ def _out(out, q):
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, dtype, device):
     """The checks that the calls on a paged cache share; returns the cache's dtype code, n_seqs, max_pages, the three index
     tensors and the scales' addresses."""
-    import torch
+    torch = _tc()
     shape, kind = k_cache.shape, k_cache.dtype
     if device.type != "cuda" or k_cache.device != device or v_cache.device != device:
         raise ValueError("k_cache and v_cache must be CUDA tensors on the tokens' device")
@@ -490,7 +511,7 @@ def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens,
         raise ValueError("k_cache and v_cache must be contiguous")
     ks = vs = None
     if kind == dtype:
-        code = dtype_code(dtype)
+        code = _code(dtype)
         if k_scale is not None or v_scale is not None:
             raise ValueError("a 16-bit cache takes no scales")
     elif kind == torch.uint8 or kind == torch.float8_e4m3fn:
@@ -527,7 +548,7 @@ def _packed(q, k, v, cu_seqlens):
 def attention_packed(q, k, v, cu_seqlens, *, causal=True, scale=None, return_lse=False, out=None, stream=None):
     """Attention of whole prompts packed end to end: q [T, Hq, d], k, v [T, Hkv, d], cu_seqlens int32 [n_seqs + 1] on the
     device; returns out [T, Hq, d] (and lse [Hq, T] fp32). Rows behind the last sequence are left as they were in `out`."""
-    import torch
+    torch = _tc()
     (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
     ctx = _elsewhere(q.device, stream)
     if ctx is not None:
@@ -537,7 +558,7 @@ def attention_packed(q, k, v, cu_seqlens, *, causal=True, scale=None, return_lse
     lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
     _check(lib.cqsa_attn_packed_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(),
                                     lse.data_ptr() if return_lse else None, cu.data_ptr(), n_seqs, T, Hq, Hkv, d,
-                                    1 if causal else 0, 0.0 if scale is None else scale, dtype_code(q.dtype),
+                                    1 if causal else 0, 0.0 if scale is None else scale, _code(q.dtype),
                                     _current(q.device)))
     return (out, lse) if return_lse else out
 
@@ -546,7 +567,7 @@ def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=Tru
     """Gradients (dq, dk, dv) of attention_packed from its out and lse and the upstream gradient dout; dk and dv sum over the
     query heads of a group. Rows behind the last sequence are left as they were in `grads` (three contiguous tensors),
     which are allocated if not given."""
-    import torch
+    torch = _tc()
     (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
     device, dtype = q.device, q.dtype
     ctx = _elsewhere(device, stream)
@@ -572,7 +593,7 @@ def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=Tru
     _check(lib.cqsa_attn_packed_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(), dout.data_ptr(),
                                     lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), need,
                                     cu.data_ptr(), n_seqs, T, Hq, Hkv, d, 1 if causal else 0,
-                                    0.0 if scale is None else scale, dtype_code(dtype), _current(device)))
+                                    0.0 if scale is None else scale, _code(dtype), _current(device)))
     return dq, dk, dv
 
 
@@ -591,14 +612,14 @@ def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, 
             return kv_cache_write(k, v, k_cache, v_cache, table, cu, lens, k_scale=k_scale, v_scale=v_scale)
     _check(lib.cqsa_kv_cache_write(k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
                                    table.data_ptr(), max_pages, cu.data_ptr(), lens.data_ptr(), n_seqs, k.shape[0], Hkv, d,
-                                   page, n_pages, dtype_code(k.dtype), code, _current(k.device)))
+                                   page, n_pages, _code(k.dtype), code, _current(k.device)))
 
 
 def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, *, k_scale=None, v_scale=None, out=None,
                   stream=None):
     """The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as (k, v) [T, Hkv, d] of dtype (into `out`, a
     pair of such tensors, if given)."""
-    import torch
+    torch = _tc()
     device = k_cache.device
     code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
                                                                 kv_lens, dtype, device)
@@ -616,8 +637,11 @@ def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, 
                 raise ValueError(f"out must be two contiguous [{T}, {Hkv}, {d}] tensors of {dtype}")
     _check(lib.cqsa_kv_cache_read(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
                                   table.data_ptr(), max_pages, cu.data_ptr(), lens.data_ptr(), n_seqs, T, Hkv, d, page,
-                                  n_pages, dtype_code(dtype), code, _current(device)))
+                                  n_pages, _code(dtype), code, _current(device)))
     return k, v
+
+
+_sizes: dict = {}  # workspace sizes by the arguments that set them
 
 
 def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len, max_kv_len, *, causal=True,
@@ -625,7 +649,7 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
     """Attention of each sequence's new tokens q [T, Hq, d] over its positions in the paged cache: out [T, Hq, d] (and
     lse [Hq, T] fp32). max_q_len: at least the most new tokens of a sequence; max_kv_len: about the longest kv_lens.
     `workspace`: a byte tensor of at least cqsa_attn_paged_workspace_size bytes (allocated if not given)."""
-    import torch
+    torch = _tc()
     device, dtype = q.device, q.dtype
     code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
                                                                 kv_lens, dtype, device)
@@ -639,11 +663,16 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
         with ctx:
             return attention_paged(q, k_cache, v_cache, table, cu, lens, max_q_len, max_kv_len, causal=causal, scale=scale,
                                    k_scale=k_scale, v_scale=v_scale, return_lse=return_lse, out=out, workspace=workspace)
-    dt = dtype_code(dtype)
+    dt = _code(dtype)
     out = _out(out, q)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if return_lse else None
     if workspace is None:
-        size = lib.cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page, max_q_len, max_kv_len, dt, code)
+        key = (n_seqs, T, Hq, Hkv, d, page, max_q_len, max_kv_len, dt, code, device.index)
+        size = _sizes.get(key)
+        if size is None:
+            if len(_sizes) >= 4096:  # (lengths differ from step to step)
+                _sizes.clear()
+            size = _sizes[key] = lib.cqsa_attn_paged_workspace_size(*key[:-1])
         workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
     else:
         size = workspace.numel() * workspace.element_size()
