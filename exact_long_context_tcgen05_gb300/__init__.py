@@ -440,6 +440,8 @@ def _tc():
 def _elsewhere(device, stream):
     """A context that makes `device` current and `stream` its current stream, or None where they already are."""
     torch = _tc()
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
     here = device.index == torch.cuda.current_device()
     if here and stream is None:
         return None
@@ -549,11 +551,11 @@ def attention_packed(q, k, v, cu_seqlens, *, causal=True, scale=None, return_lse
     """Attention of whole prompts packed end to end: q [T, Hq, d], k, v [T, Hkv, d], cu_seqlens int32 [n_seqs + 1] on the
     device; returns out [T, Hq, d] (and lse [Hq, T] fp32). Rows behind the last sequence are left as they were in `out`."""
     torch = _tc()
-    (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
     ctx = _elsewhere(q.device, stream)
     if ctx is not None:
         with ctx:
-            return attention_packed(q, k, v, cu, causal=causal, scale=scale, return_lse=return_lse, out=out)
+            return attention_packed(q, k, v, cu_seqlens, causal=causal, scale=scale, return_lse=return_lse, out=out)
+    (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
     out = _out(out, q)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if return_lse else None
     _check(lib.cqsa_attn_packed_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, out.data_ptr(),
@@ -568,12 +570,12 @@ def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=Tru
     query heads of a group. Rows behind the last sequence are left as they were in `grads` (three contiguous tensors),
     which are allocated if not given."""
     torch = _tc()
-    (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
     device, dtype = q.device, q.dtype
     ctx = _elsewhere(device, stream)
     if ctx is not None:
         with ctx:
-            return attention_packed_backward(q, k, v, out, dout, lse, cu, causal=causal, scale=scale, grads=grads)
+            return attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, causal=causal, scale=scale, grads=grads)
+    (q, qs), (k, ks), (v, vs), cu, n_seqs, T, Hq, Hkv, d = _packed(q, k, v, cu_seqlens)
     for name, t in (("out", out), ("dout", dout)):
         if t.shape != q.shape or t.dtype != dtype or t.device != device:
             raise ValueError(f"{name} must be a {tuple(q.shape)} tensor of {dtype} on {device}")
@@ -600,16 +602,16 @@ def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=Tru
 def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, k_scale=None, v_scale=None, stream=None):
     """New tokens k, v [T, Hkv, d] into their pages of the caches [n_pages, Hkv, page_size, d] (k's dtype, or
     uint8 / float8_e4m3fn codes with byte tensors k_scale, v_scale [n_pages, Hkv, page_size])."""
+    ctx = _elsewhere(k.device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, k_scale=k_scale, v_scale=v_scale)
     code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
                                                                 kv_lens, k.dtype, k.device)
     n_pages, Hkv, page, d = k_cache.shape
     (k, ks), (v, vs) = _tokens("k", k, Hkv, d, k), _tokens("v", v, Hkv, d, k)
     if v.shape != k.shape:
         raise ValueError("k and v must have one shape")
-    ctx = _elsewhere(k.device, stream)
-    if ctx is not None:
-        with ctx:
-            return kv_cache_write(k, v, k_cache, v_cache, table, cu, lens, k_scale=k_scale, v_scale=v_scale)
     _check(lib.cqsa_kv_cache_write(k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
                                    table.data_ptr(), max_pages, cu.data_ptr(), lens.data_ptr(), n_seqs, k.shape[0], Hkv, d,
                                    page, n_pages, _code(k.dtype), code, _current(k.device)))
@@ -621,12 +623,13 @@ def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, 
     pair of such tensors, if given)."""
     torch = _tc()
     device = k_cache.device
-    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
-                                                                kv_lens, dtype, device)
     ctx = _elsewhere(device, stream)
     if ctx is not None:
         with ctx:
-            return kv_cache_read(k_cache, v_cache, table, cu, lens, T, dtype, k_scale=k_scale, v_scale=v_scale, out=out)
+            return kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, k_scale=k_scale,
+                                 v_scale=v_scale, out=out)
+    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                kv_lens, dtype, device)
     n_pages, Hkv, page, d = k_cache.shape
     if out is None:
         k, v = (torch.empty((T, Hkv, d), dtype=dtype, device=device) for _ in range(2))
@@ -651,6 +654,12 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
     `workspace`: a byte tensor of at least cqsa_attn_paged_workspace_size bytes (allocated if not given)."""
     torch = _tc()
     device, dtype = q.device, q.dtype
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len, max_kv_len,
+                                   causal=causal, scale=scale, k_scale=k_scale, v_scale=v_scale, return_lse=return_lse,
+                                   out=out, workspace=workspace)
     code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
                                                                 kv_lens, dtype, device)
     n_pages, Hkv, page, d = k_cache.shape
@@ -658,14 +667,11 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
         raise ValueError("q must be [T, Hq, d]")
     T, Hq = q.shape[:2]
     q, qs = _tokens("q", q, Hq, d, q)
-    ctx = _elsewhere(device, stream)
-    if ctx is not None:
-        with ctx:
-            return attention_paged(q, k_cache, v_cache, table, cu, lens, max_q_len, max_kv_len, causal=causal, scale=scale,
-                                   k_scale=k_scale, v_scale=v_scale, return_lse=return_lse, out=out, workspace=workspace)
     dt = _code(dtype)
     out = _out(out, q)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if return_lse else None
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if workspace is None:
         key = (n_seqs, T, Hq, Hkv, d, page, max_q_len, max_kv_len, dt, code, device.index)
         size = _sizes.get(key)

@@ -409,10 +409,13 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
   if constexpr (PACKED) {
     if (warp == 2) {
       // key tiles by how many follow them in their sequence: under the causal mask, heaviest first
-      const Unit u = find_unit(p.n_seqs, unit / (p.Hkv * p.n_splits), lane, [&](int i) {
+      auto tiles = [&](int i) {
         int first;
         return (seq_tokens(p.cu, i, p.T, &first) + BT - 1) / BT;
-      });
+      };
+      const int rank = unit / (p.Hkv * p.n_splits);
+      Walker walk;
+      const Unit u = p.n_seqs > kRankedSeqs ? walk.find(p.n_seqs, rank, lane, tiles) : find_unit(p.n_seqs, rank, lane, tiles);
       if (lane == 0) {
         s_unit[0] = u.seq;
         s_unit[1] = u.place;
@@ -1449,11 +1452,11 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 // An upper bound on the key tiles of n_seqs sequences that hold T tokens together, times the key heads.
 long long packed_tiles(int n_seqs, int T, int Hkv) { return (T / BT + static_cast<long long>(T < n_seqs ? T : n_seqs)) * Hkv; }
 
-// Ranges of steps per key tile: a CTA takes a key tile through all its queries, so few tiles leave SMs idle and the
-// first tile of the longest sequence sets the time (9 sequences, 4,099 tokens, 2 key heads at d = 64: 83 us in one range).
-// Parts cost fp32 traffic and each CTA its set-up, so about CQSA_BWD_FILL CTAs per SM are enough.
+// Ranges of steps per key tile: a CTA takes a key tile through all its queries, so few tiles leave SMs idle and the first
+// tile of the longest sequence sets the time. Each range costs fp32 parts and a CTA's set-up, so about two CTAs per SM are
+// aimed at (9 sequences, 4,099 tokens, 2 key heads at d = 64: 88 us in one range, 50 in three, 61 in five, 77 in eight).
 #ifndef CQSA_BWD_FILL
-#define CQSA_BWD_FILL 3
+#define CQSA_BWD_FILL 2
 #endif
 int packed_splits(int n_seqs, int T, int Hkv) {
   const long long s = static_cast<long long>(sm_count()) * CQSA_BWD_FILL / std::max<long long>(1, packed_tiles(n_seqs, T, Hkv));

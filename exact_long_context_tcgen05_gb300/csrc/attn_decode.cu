@@ -79,6 +79,7 @@ struct DecParams {
   int n_seqs, T, Hq, Hkv, G, max_pages, n_pages, page_log2, causal;
   float scale_log2;
   unsigned timeout_us;
+  int fault;  // test hook: 1 = the first key tile of sequence 0 and head 0 is never loaded
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -283,6 +284,10 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
                              kDevTimeoutKV, 40);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (p.fault == 1 && wk.s == 0 && h == 0 && t == 0) {  // (every wait on the tile runs out)
+          ok = false;
+          break;
+        }
         uint8_t* st = sm + stage * C::STAGE;
         const int k0 = t * KT;
         const int nb = min(boxes, max(0, (wk.len - k0 + rows - 1) >> (31 - __clz(rows))));
@@ -805,6 +810,7 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream) {
   p.causal = a.causal;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.timeout_us = timeout_us();
+  p.fault = debug_fault();
   const bool bf = a.dtype == CQSA_BF16;
   if (a.cache_dtype == CQSA_E4M3) {
     if (a.d == 64) return bf ? launch_rows<64, 1, true>(mk, mv, p, rr, ctas, stream) : launch_rows<64, 0, true>(mk, mv, p, rr, ctas, stream);

@@ -304,13 +304,15 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       // ------------------------------------------------------------------ units
       const unsigned per_rank = static_cast<unsigned>(p.Hkv * p.n_splits);
       const int per = 2 * p.tpt;
+      auto pieces = [&](int k) {
+        int first;
+        return (seq_tokens(p.cu, k, p.T, &first) + per - 1) / per;
+      };
+      Walker walk;
       for (int i = 0;; ++i) {
         const unsigned u = static_cast<unsigned>(i) * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         const int rank = static_cast<int>(u / per_rank), sub = static_cast<int>(u - rank * per_rank);
-        const Unit f = find_unit(p.n_seqs, rank, lane, [&](int k) {
-          int first;
-          return (seq_tokens(p.cu, k, p.T, &first) + per - 1) / per;
-        });
+        const Unit f = p.n_seqs > kRankedSeqs ? walk.find(p.n_seqs, rank, lane, pieces) : find_unit(p.n_seqs, rank, lane, pieces);
         Work w = {f.seq >= 0, f.seq, 0, 0, 0, f.place * per, sub / p.n_splits, sub % p.n_splits};
         if (w.valid) {
           w.qlen = seq_tokens(p.cu, f.seq, p.T, &w.tok_first);
@@ -336,122 +338,122 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       int raw_last[2] = {0, 0};
       bool ok = true;
       for (int unit = 0; ok && take(unit, &v); ++unit) {
-      if (v.n_max == 0) continue;
-      const int tok_first = v.w.tok_first, hk = v.w.hk, kbase = v.kbase, kleft = v.kleft, n_max = v.n_max, seq = v.w.seq;
-      if (uq > 0) {
-        ok = wait_or_abort(smem_u32(bar_q_free), (uq - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 42);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
-      ++uq;
-      const uint32_t q_bytes = static_cast<uint32_t>(p.tpt) * p.G * 128u;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar_q, 2 * KSUB * q_bytes);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < KSUB; ++x)
-            tma_load_3d(sQ + t * C::QT_BYTES + x * TILE_BYTES, &tmQ, bar_q, x * 64, hk * p.G, tok_first + (t ? v.tb : v.w.ta));
-      }
-      if constexpr (!CONV) {
-        const int page = SRC == kSrcPages ? 1 << p.page_log2 : BN;
-        const int rows = min(page, BN);
-        const int boxes = BN / rows;
-        const int* trow = SRC == kSrcPages ? p.table + static_cast<long long>(seq) * p.max_pages : nullptr;
-        for (int j = 0; j < n_max; ++j) {
-          const int stage = (kb + j) % STAGES;
-          const uint32_t round = (kb + j) / STAGES;
-          const int left = kleft - j * BN;
-          const int nb = min(boxes, (left + rows - 1) / rows);
-          int pg = 0, y = 0;
-          if (SRC == kSrcPages && lane < nb) {  // page entries are fetched before the wait
-            const int pos = kbase + j * BN + lane * rows;
-            pg = page_at(trow, pos >> p.page_log2, p.n_pages);
-            y = pos & (page - 1);
-          }
-          const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
-          ok = wait_or_abort(smem_u32(ALIAS ? &bar_k_empty[stage] : &bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
+        if (v.n_max == 0) continue;
+        const int tok_first = v.w.tok_first, hk = v.w.hk, kbase = v.kbase, kleft = v.kleft, n_max = v.n_max, seq = v.w.seq;
+        if (uq > 0) {
+          ok = wait_or_abort(smem_u32(bar_q_free), (uq - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 42);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (p.fault == 1 && blockIdx.x == 0 && j == 1) {  // (every wait on the tile runs out)
-            ok = false;
-            break;
-          }
-          k_last[stage & 3] = round + 1;
-          if (lane == 0) mbar_arrive_expect_tx(&bar_k_full[stage], bytes);
-          __syncwarp();
-          if (lane < nb) {
-            uint8_t* dk = sK + stage * C::KV_BYTES + lane * rows * 128 * KSUB;
-            if (SRC == kSrcPages) {
-              tma_load_5d(dk, &tmK, &bar_k_full[stage], 0, 0, 0, y >> 3, pg * p.Hkv + hk);
-            } else {
+        }
+        ++uq;
+        const uint32_t q_bytes = static_cast<uint32_t>(p.tpt) * p.G * 128u;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar_q, 2 * KSUB * q_bytes);
 #pragma unroll
-              for (int x = 0; x < KSUB; ++x)
-                tma_load_3d(dk + x * TILE_BYTES, &tmK, &bar_k_full[stage], x * 64, hk, tok_first + kbase + j * BN);
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < KSUB; ++x)
+              tma_load_3d(sQ + t * C::QT_BYTES + x * TILE_BYTES, &tmQ, bar_q, x * 64, hk * p.G, tok_first + (t ? v.tb : v.w.ta));
+        }
+        if constexpr (!CONV) {
+          const int page = SRC == kSrcPages ? 1 << p.page_log2 : BN;
+          const int rows = min(page, BN);
+          const int boxes = BN / rows;
+          const int* trow = SRC == kSrcPages ? p.table + static_cast<long long>(seq) * p.max_pages : nullptr;
+          for (int j = 0; j < n_max; ++j) {
+            const int stage = (kb + j) % STAGES;
+            const uint32_t round = (kb + j) / STAGES;
+            const int left = kleft - j * BN;
+            const int nb = min(boxes, (left + rows - 1) / rows);
+            int pg = 0, y = 0;
+            if (SRC == kSrcPages && lane < nb) {  // page entries are fetched before the wait
+              const int pos = kbase + j * BN + lane * rows;
+              pg = page_at(trow, pos >> p.page_log2, p.n_pages);
+              y = pos & (page - 1);
+            }
+            const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
+            ok = wait_or_abort(smem_u32(ALIAS ? &bar_k_empty[stage] : &bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (p.fault == 1 && blockIdx.x == 0 && j == 1) {  // (every wait on the tile runs out)
+              ok = false;
+              break;
+            }
+            k_last[stage & 3] = round + 1;
+            if (lane == 0) mbar_arrive_expect_tx(&bar_k_full[stage], bytes);
+            __syncwarp();
+            if (lane < nb) {
+              uint8_t* dk = sK + stage * C::KV_BYTES + lane * rows * 128 * KSUB;
+              if (SRC == kSrcPages) {
+                tma_load_5d(dk, &tmK, &bar_k_full[stage], 0, 0, 0, y >> 3, pg * p.Hkv + hk);
+              } else {
+#pragma unroll
+                for (int x = 0; x < KSUB; ++x)
+                  tma_load_3d(dk + x * TILE_BYTES, &tmK, &bar_k_full[stage], x * 64, hk, tok_first + kbase + j * BN);
+              }
+            }
+            if (ALIAS) {
+              ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 34);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+            const bool tail = left < BN;
+            if (!tail) v_last[stage & 3] = round + 1;
+            uint64_t* vbar = tail ? bar_fix : &bar_v_full[stage];
+            if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
+            __syncwarp();
+            if (lane < nb) {
+              uint8_t* dv = sV + stage * C::KV_BYTES + lane * rows * 128 * KSUB;
+              if (SRC == kSrcPages) {
+                tma_load_5d(dv, &tmV, vbar, 0, 0, 0, y >> 3, pg * p.Hkv + hk);
+              } else {
+#pragma unroll
+                for (int x = 0; x < KSUB; ++x)
+                  tma_load_3d(dv + x * TILE_BYTES, &tmV, vbar, x * 64, hk, tok_first + kbase + j * BN);
+              }
+            }
+            __syncwarp();
+            if (tail) {  // at most the last key tile of the sequence
+              ok = wait_or_abort(smem_u32(bar_fix), fixes & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 31);
+              ++fixes;
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              zero_rows<C>(sV + stage * C::KV_BYTES, left, lane);
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar_v_full[stage]);
+              v_last[stage & 3] = 0;  // waited for
             }
           }
-          if (ALIAS) {
-            ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 34);
-            ok = __all_sync(0xffffffffu, ok);
+        }
+        if constexpr (CONV) {
+          // codes of a tile, page by page (a page's vectors of one head lie together), into the one raw buffer of K and of V
+          const int page = 1 << p.page_log2, rows = min(page, BN), boxes = BN / rows;
+          const int* trow = p.table + static_cast<long long>(seq) * p.max_pages;
+          for (int j = 0; ok && j < n_max; ++j) {
+            if (p.fault == 1 && blockIdx.x == 0 && j == 1) ok = false;  // (every wait on the tile runs out)
             if (!ok) break;
-          }
-          const bool tail = left < BN;
-          if (!tail) v_last[stage & 3] = round + 1;
-          uint64_t* vbar = tail ? bar_fix : &bar_v_full[stage];
-          if (lane == 0) mbar_arrive_expect_tx(vbar, bytes);
-          __syncwarp();
-          if (lane < nb) {
-            uint8_t* dv = sV + stage * C::KV_BYTES + lane * rows * 128 * KSUB;
-            if (SRC == kSrcPages) {
-              tma_load_5d(dv, &tmV, vbar, 0, 0, 0, y >> 3, pg * p.Hkv + hk);
-            } else {
+            const int nb = min(boxes, (kleft - j * BN + rows - 1) / rows);
+            long long at = 0;
+            if (lane < nb) {
+              const int pos = kbase + j * BN + lane * rows;
+              const int pg = page_at(trow, pos >> p.page_log2, p.n_pages);
+              at = (((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + (pos & (page - 1))) * D;
+            }
 #pragma unroll
-              for (int x = 0; x < KSUB; ++x)
-                tma_load_3d(dv + x * TILE_BYTES, &tmV, vbar, x * 64, hk, tok_first + kbase + j * BN);
+            for (int x = 0; x < 2; ++x) {
+              ok = ok && wait_or_abort(smem_u32(&bar_raw_free[x]), ((kb + j) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 36 + x);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], static_cast<uint32_t>(nb) * rows * D);
+              __syncwarp();
+              if (lane < nb)
+                bulk_load(sRaw + x * C::RAW + lane * rows * D, (x ? p.v_cache : p.k_cache) + at, rows * D, &bar_raw[x]);
+              raw_last[x] = kb + j + 1;
             }
           }
-          __syncwarp();
-          if (tail) {  // at most the last key tile of the sequence
-            ok = wait_or_abort(smem_u32(bar_fix), fixes & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 31);
-            ++fixes;
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            zero_rows<C>(sV + stage * C::KV_BYTES, left, lane);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_v_full[stage]);
-            v_last[stage & 3] = 0;  // waited for
-          }
         }
-      }
-      if constexpr (CONV) {
-        // codes of a tile, page by page (a page's vectors of one head lie together), into the one raw buffer of K and of V
-        const int page = 1 << p.page_log2, rows = min(page, BN), boxes = BN / rows;
-        const int* trow = p.table + static_cast<long long>(seq) * p.max_pages;
-        for (int j = 0; ok && j < n_max; ++j) {
-          if (p.fault == 1 && blockIdx.x == 0 && j == 1) ok = false;  // (every wait on the tile runs out)
-          if (!ok) break;
-          const int nb = min(boxes, (kleft - j * BN + rows - 1) / rows);
-          long long at = 0;
-          if (lane < nb) {
-            const int pos = kbase + j * BN + lane * rows;
-            const int pg = page_at(trow, pos >> p.page_log2, p.n_pages);
-            at = (((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + (pos & (page - 1))) * D;
-          }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            ok = ok && wait_or_abort(smem_u32(&bar_raw_free[x]), ((kb + j) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 36 + x);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], static_cast<uint32_t>(nb) * rows * D);
-            __syncwarp();
-            if (lane < nb)
-              bulk_load(sRaw + x * C::RAW + lane * rows * D, (x ? p.v_cache : p.k_cache) + at, rows * D, &bar_raw[x]);
-            raw_last[x] = kb + j + 1;
-          }
-        }
-      }
-      kb += n_max;
+        kb += n_max;
       }
       // every load issued lands before the CTA exits (bounded waits; already complete on the normal path; a tail that ran
       // out is given one more limit)
@@ -609,258 +611,258 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     int kb = 0, tb = 0, uq = 0, uo = 0;  // key tiles of the CTA and of this row tile, units with any for either
     bool ok = true;
     for (int unit = 0; ok && take(unit, &v); ++unit) {
-    const int nkv = wg ? v.nkv1 : v.nkv0, n_max = v.n_max, kleft = v.kleft;
-    const int t0 = wg ? v.tb : v.w.ta;
-    const int rel = v.q_off + t0 - v.kbase;     // key position (in the range) of the tile's first token
-    const int row_lim = p.causal ? rel + rt + 1 : 0x7fffffff;
-    const int diag = p.causal ? rel - (BN - 1) : 0x7fffffff;  // tiles from beyond this key on hide keys from some row
-    float sl2 = p.scale_log2;
-    float m_ref = -INFINITY, l = 0.0f, m_sum = -INFINITY;
-    int ev = -100000, ev_sum = 0;  // e4m3: exponent of the values that O (the running sum) is relative to
-    for (int j0 = 0; ok && j0 < nkv; j0 += SEG) {
-      if (j0 > 0) {
-        // fold O into the running sum, brought from its reference to the current one by an exact power of two
-        ok = wait_or_abort(a_pv_done, (tb + j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const bool have = j0 > C::FLUSH;
-        float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
-        if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
-        if (C::OSUM_SMEM) {
+      const int nkv = wg ? v.nkv1 : v.nkv0, n_max = v.n_max, kleft = v.kleft;
+      const int t0 = wg ? v.tb : v.w.ta;
+      const int rel = v.q_off + t0 - v.kbase;     // key position (in the range) of the tile's first token
+      const int row_lim = p.causal ? rel + rt + 1 : 0x7fffffff;
+      const int diag = p.causal ? rel - (BN - 1) : 0x7fffffff;  // tiles from beyond this key on hide keys from some row
+      float sl2 = p.scale_log2;
+      float m_ref = -INFINITY, l = 0.0f, m_sum = -INFINITY;
+      int ev = -100000, ev_sum = 0;  // e4m3: exponent of the values that O (the running sum) is relative to
+      for (int j0 = 0; ok && j0 < nkv; j0 += SEG) {
+        if (j0 > 0) {
+          // fold O into the running sum, brought from its reference to the current one by an exact power of two
+          ok = wait_or_abort(a_pv_done, (tb + j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const bool have = j0 > C::FLUSH;
+          float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
+          if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
+          if (C::OSUM_SMEM) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(trow + colO + c * 32, o);
-            tmem_wait_ld();
-            reg_fence32(o);
-            const uint32_t os = smem_u32(sOsum) + static_cast<uint32_t>(((wg * D) * 128 + r) * 4);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(trow + colO + c * 32, o);
+              tmem_wait_ld();
+              reg_fence32(o);
+              const uint32_t os = smem_u32(sOsum) + static_cast<uint32_t>(((wg * D) * 128 + r) * 4);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const uint32_t a = os + static_cast<uint32_t>((c * 32 + e) * 128 * 4);
-              const float prev = have ? ld_shared_f32(a) * sc : 0.0f;
-              st_shared_f32(a, prev + __uint_as_float(o[e]));
+              for (int e = 0; e < 32; ++e) {
+                const uint32_t a = os + static_cast<uint32_t>((c * 32 + e) * 128 * 4);
+                const float prev = have ? ld_shared_f32(a) * sc : 0.0f;
+                st_shared_f32(a, prev + __uint_as_float(o[e]));
+              }
+            }
+          } else {
+            float* og = sOsum + (wg * D) * 128 + r;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float prev[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) prev[e] = have ? __ldcg(og + (c * 32 + e) * 128) : 0.0f;
+              uint32_t o[32];
+              tmem_ld32(trow + colO + c * 32, o);
+              tmem_wait_ld();
+              reg_fence32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) __stcg(og + (c * 32 + e) * 128, prev[e] * sc + __uint_as_float(o[e]));
             }
           }
-        } else {
-          float* og = sOsum + (wg * D) * 128 + r;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float prev[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) prev[e] = have ? __ldcg(og + (c * 32 + e) * 128) : 0.0f;
-            uint32_t o[32];
-            tmem_ld32(trow + colO + c * 32, o);
-            tmem_wait_ld();
-            reg_fence32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) __stcg(og + (c * 32 + e) * 128, prev[e] * sc + __uint_as_float(o[e]));
+          m_sum = m_ref;
+          ev_sum = ev;
+        }
+        const int j1 = (nkv - j0 < SEG) ? nkv : j0 + SEG;
+        for (int j = j0; j < j1; ++j) {
+          ok = wait_or_abort(a_s_full, (tb + j) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
           }
-        }
-        m_sum = m_ref;
-        ev_sum = ev;
-      }
-      const int j1 = (nkv - j0 < SEG) ? nkv : j0 + SEG;
-      for (int j = j0; j < j1; ++j) {
-        ok = wait_or_abort(a_s_full, (tb + j) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        if (CONVQ && j == 0) sl2 = p.scale_log2 * exp2_int_any(sRow[(uq & 1) * 256 + wg * 128 + r]);  // written before the queries were released
-        tc_fence_after();
-        uint32_t sr[128];
+          if (CONVQ && j == 0) sl2 = p.scale_log2 * exp2_int_any(sRow[(uq & 1) * 256 + wg * 128 + r]);  // written before the queries were released
+          tc_fence_after();
+          uint32_t sr[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(trow + colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        tmem_wait_ld();
+          for (int c = 0; c < 4; ++c) tmem_ld32(trow + colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        if (!ALIAS) {
-          tc_fence_before();
-          mbar_arrive_a(a_s_free);  // S_t may now take S_t(j+1)
-        }
-        float x[128];
+          for (int c = 0; c < 4; ++c) reg_fence32(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          if (!ALIAS) {
+            tc_fence_before();
+            mbar_arrive_a(a_s_free);  // S_t may now take S_t(j+1)
+          }
+          float x[128];
 #pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c]);
-        const int k0 = j * BN;
-        if (k0 > kleft - BN || k0 > diag) {
-          const int lim = min(kleft, row_lim) - k0;
+          for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr[c]);
+          const int k0 = j * BN;
+          if (k0 > kleft - BN || k0 > diag) {
+            const int lim = min(kleft, row_lim) - k0;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= lim) x[c] = -INFINITY;
-        }
-        float alpha = 1.0f;
-        bool rescale = false;
-        float slt = sl2;
-        if constexpr (CONV) {  // this tile's K and V are relative to these powers of two, which only rise
-          const int2 ex = *reinterpret_cast<const int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2);
-          // held above 0, so that a masked score times it stays -inf (scores that small are 0 either way)
-          slt = fmaxf(sl2 * exp2_int_any(ex.x), 0x1p-100f);
-          if (ex.y > ev) {
-            if (j > 0) {
-              alpha = exp2_int(static_cast<float>(max(ev - ex.y, -200)));
+            for (int c = 0; c < 128; ++c)
+              if (c >= lim) x[c] = -INFINITY;
+          }
+          float alpha = 1.0f;
+          bool rescale = false;
+          float slt = sl2;
+          if constexpr (CONV) {  // this tile's K and V are relative to these powers of two, which only rise
+            const int2 ex = *reinterpret_cast<const int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2);
+            // held above 0, so that a masked score times it stays -inf (scores that small are 0 either way)
+            slt = fmaxf(sl2 * exp2_int_any(ex.x), 0x1p-100f);
+            if (ex.y > ev) {
+              if (j > 0) {
+                alpha = exp2_int(static_cast<float>(max(ev - ex.y, -200)));
+                rescale = true;
+              }
+              ev = ex.y;
+            }
+          }
+          const float tmax = row_max128(x) * slt;
+          float al_l = 1.0f;  // what the row's sum is multiplied by (the values' exponent does not matter to it)
+          if (tmax > m_ref + kTau || (m_ref == -INFINITY && tmax > -INFINITY)) {
+            const float m_new = ceilf(tmax);
+            if (m_ref != -INFINITY) {
+              al_l = exp2_int(m_ref - m_new);
+              alpha *= al_l;
               rescale = true;
             }
-            ev = ex.y;
+            m_ref = m_new;
           }
-        }
-        const float tmax = row_max128(x) * slt;
-        float al_l = 1.0f;  // what the row's sum is multiplied by (the values' exponent does not matter to it)
-        if (tmax > m_ref + kTau || (m_ref == -INFINITY && tmax > -INFINITY)) {
-          const float m_new = ceilf(tmax);
-          if (m_ref != -INFINITY) {
-            al_l = exp2_int(m_ref - m_new);
-            alpha *= al_l;
-            rescale = true;
-          }
-          m_ref = m_new;
-        }
-        // O takes the new reference (the running sum keeps its own), once PV_t(j-1) has been accumulated
-        auto rescale_o = [&]() {
-          if (!(__any_sync(0xffffffffu, rescale) && j > 0)) return;
+          // O takes the new reference (the running sum keeps its own), once PV_t(j-1) has been accumulated
+          auto rescale_o = [&]() {
+            if (!(__any_sync(0xffffffffu, rescale) && j > 0)) return;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(trow + colO + c * 32, o);
-            tmem_wait_ld();
-            reg_fence32(o);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(trow + colO + c * 32, o);
+              tmem_wait_ld();
+              reg_fence32(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(trow + colO + c * 32, o);
-          }
-        };
-        const float cm = ((m_ref == -INFINITY) ? 0.0f : m_ref) - kPShift;
-        const uint32_t pbuf = trow + colP;
-        float sum;
-        if constexpr (!ALIAS) {
-          const float2 sl2v = make_float2(sl2, sl2), ncm = make_float2(-cm, -cm);
-          float2 rs2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-          uint32_t pk[64];
-#pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const float2 pp = exp2_pair(x[2 * c], x[2 * c + 1], sl2v, ncm);
-            rs2[c & 1] = __fadd2_rn(rs2[c & 1], pp);
-            pk[c] = pack2(pp.x, pp.y, MB);
-          }
-          if (j > 0) {
-            ok = wait_or_abort(a_pv_done, (tb + j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
-            if (!__all_sync(0xffffffffu, ok)) {
-              ok = false;
-              break;
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(trow + colO + c * 32, o);
             }
-            tc_fence_after();
-          }
-          tmem_st32(pbuf, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
-          tmem_st32(pbuf + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
-          rescale_o();
-          sum = (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
-        } else {
-          // P over S: S_t(j) is complete, and its commit covers every earlier MMA of the issuing thread, PV_t(j-1)
-          // included
-          rescale_o();
-          sum = 0.0f;
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            const float2 sl2v = make_float2(slt, slt), ncm = make_float2(-cm, -cm);
+          };
+          const float cm = ((m_ref == -INFINITY) ? 0.0f : m_ref) - kPShift;
+          const uint32_t pbuf = trow + colP;
+          float sum;
+          if constexpr (!ALIAS) {
+            const float2 sl2v = make_float2(sl2, sl2), ncm = make_float2(-cm, -cm);
             float2 rs2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            uint32_t hi[16];
+            uint32_t pk[64];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int c = c4 * 16 + e;
+            for (int c = 0; c < 64; ++c) {
               const float2 pp = exp2_pair(x[2 * c], x[2 * c + 1], sl2v, ncm);
-              rs2[e & 1] = __fadd2_rn(rs2[e & 1], pp);
-              hi[e] = pack2(pp.x, pp.y, MB);
+              rs2[c & 1] = __fadd2_rn(rs2[c & 1], pp);
+              pk[c] = pack2(pp.x, pp.y, MB);
             }
-            tmem_st16(pbuf + c4 * 16, hi);
-            if (c4 == 1) {
-              tmem_wait_st();
-              tc_fence_before();
-              mbar_arrive_a(smem_u32(&bar_p_half[wg]));
-              // keep the second half's work behind this point (it would be interleaved with the first's)
+            if (j > 0) {
+              ok = wait_or_abort(a_pv_done, (tb + j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
+              if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            tmem_st32(pbuf, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
+            tmem_st32(pbuf + 32, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
+            rescale_o();
+            sum = (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
+          } else {
+            // P over S: S_t(j) is complete, and its commit covers every earlier MMA of the issuing thread, PV_t(j-1)
+            // included
+            rescale_o();
+            sum = 0.0f;
 #pragma unroll
-              for (int e = 64; e < 128; ++e) asm volatile("" : "+f"(x[e]));
+            for (int c4 = 0; c4 < 4; ++c4) {
+              const float2 sl2v = make_float2(slt, slt), ncm = make_float2(-cm, -cm);
+              float2 rs2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+              uint32_t hi[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int c = c4 * 16 + e;
+                const float2 pp = exp2_pair(x[2 * c], x[2 * c + 1], sl2v, ncm);
+                rs2[e & 1] = __fadd2_rn(rs2[e & 1], pp);
+                hi[e] = pack2(pp.x, pp.y, MB);
+              }
+              tmem_st16(pbuf + c4 * 16, hi);
+              if (c4 == 1) {
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive_a(smem_u32(&bar_p_half[wg]));
+                // keep the second half's work behind this point (it would be interleaved with the first's)
+#pragma unroll
+                for (int e = 64; e < 128; ++e) asm volatile("" : "+f"(x[e]));
+              }
+              sum += (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
             }
-            sum += (rs2[0].x + rs2[1].x) + (rs2[0].y + rs2[1].y);
+          }
+          l = l * al_l + sum;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive_a(a_p_full);
+        }
+      }
+
+      // ---------------------------------------------------------------- epilogue
+      if (ok && nkv > 0) {
+        ok = wait_or_abort(smem_u32(&bar_o_final[wg]), uo & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 20);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      }
+      // a row with a NaN score has l = NaN and passes it on; an empty one is 0 / -inf
+      const bool has = (nkv > 0) && !(l <= 0.0f);
+      float inv_l = has ? 1.0f / l : 0.0f;
+      const float lse2 = has ? m_ref - kPShift + log2f(l) : -INFINITY;
+      if (CONV) inv_l *= has ? exp2_int_any(min(max(ev, -126), 127)) : 1.0f;
+      const int tok = t0 + rt;
+      const bool write = ok && rt < p.tpt && tok < v.w.qlen;
+      const int hq = v.w.hk * p.G + (r - rt * p.G);
+      const long long row = static_cast<long long>(v.w.tok_first + tok) * p.Hq + hq;
+      const long long prow = static_cast<long long>(v.w.split) * p.T * p.Hq + row;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (ok && nkv > 0) {
+          tmem_ld32(trow + colO + c * 32, o);
+          tmem_wait_ld();
+          reg_fence32(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        float y[32];
+        if (osum_ok && nkv > C::FLUSH) {
+          const float* os = sOsum + (wg * D + c * 32) * 128 + r;
+          float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
+          if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
+          float prev[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) prev[e] = C::OSUM_SMEM ? os[e * 128] : __ldcg(os + e * 128);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = (prev[e] * sc + __uint_as_float(o[e])) * inv_l;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = has ? __uint_as_float(o[e]) * inv_l : 0.0f;
+        }
+        if (write) {
+          if (p.n_splits == 1) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c * 32);
+#pragma unroll
+            for (int q8 = 0; q8 < 4; ++q8) {
+              uint4 w;
+              w.x = pack2(y[8 * q8 + 0], y[8 * q8 + 1], BF16);
+              w.y = pack2(y[8 * q8 + 2], y[8 * q8 + 3], BF16);
+              w.z = pack2(y[8 * q8 + 4], y[8 * q8 + 5], BF16);
+              w.w = pack2(y[8 * q8 + 6], y[8 * q8 + 7], BF16);
+              dst[q8] = w;
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(y[4 * q4], y[4 * q4 + 1], y[4 * q4 + 2], y[4 * q4 + 3]);
           }
         }
-        l = l * al_l + sum;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive_a(a_p_full);
-      }
-    }
-
-    // ---------------------------------------------------------------- epilogue
-    if (ok && nkv > 0) {
-      ok = wait_or_abort(smem_u32(&bar_o_final[wg]), uo & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 20);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    // a row with a NaN score has l = NaN and passes it on; an empty one is 0 / -inf
-    const bool has = (nkv > 0) && !(l <= 0.0f);
-    float inv_l = has ? 1.0f / l : 0.0f;
-    const float lse2 = has ? m_ref - kPShift + log2f(l) : -INFINITY;
-    if (CONV) inv_l *= has ? exp2_int_any(min(max(ev, -126), 127)) : 1.0f;
-    const int tok = t0 + rt;
-    const bool write = ok && rt < p.tpt && tok < v.w.qlen;
-    const int hq = v.w.hk * p.G + (r - rt * p.G);
-    const long long row = static_cast<long long>(v.w.tok_first + tok) * p.Hq + hq;
-    const long long prow = static_cast<long long>(v.w.split) * p.T * p.Hq + row;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t o[32];
-      if (ok && nkv > 0) {
-        tmem_ld32(trow + colO + c * 32, o);
-        tmem_wait_ld();
-        reg_fence32(o);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0u;
-      }
-      float y[32];
-      if (osum_ok && nkv > C::FLUSH) {
-        const float* os = sOsum + (wg * D + c * 32) * 128 + r;
-        float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
-        if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
-        float prev[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) prev[e] = C::OSUM_SMEM ? os[e * 128] : __ldcg(os + e * 128);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = (prev[e] * sc + __uint_as_float(o[e])) * inv_l;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = has ? __uint_as_float(o[e]) * inv_l : 0.0f;
       }
       if (write) {
-        if (p.n_splits == 1) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c * 32);
-#pragma unroll
-          for (int q8 = 0; q8 < 4; ++q8) {
-            uint4 w;
-            w.x = pack2(y[8 * q8 + 0], y[8 * q8 + 1], BF16);
-            w.y = pack2(y[8 * q8 + 2], y[8 * q8 + 3], BF16);
-            w.z = pack2(y[8 * q8 + 4], y[8 * q8 + 5], BF16);
-            w.w = pack2(y[8 * q8 + 6], y[8 * q8 + 7], BF16);
-            dst[q8] = w;
-          }
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
-#pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(y[4 * q4], y[4 * q4 + 1], y[4 * q4 + 2], y[4 * q4 + 3]);
-        }
+        if (p.n_splits > 1) p.part_l[prow] = lse2;
+        else if (p.lse) p.lse[static_cast<long long>(hq) * p.T + v.w.tok_first + tok] = lse2 * 0.69314718055994531f;
       }
-    }
-    if (write) {
-      if (p.n_splits > 1) p.part_l[prow] = lse2;
-      else if (p.lse) p.lse[static_cast<long long>(hq) * p.T + v.w.tok_first + tok] = lse2 * 0.69314718055994531f;
-    }
-    tc_fence_before();  // O has been read: the next unit's P hand-offs release its columns
-    kb += n_max;
-    tb += nkv;
-    uq += n_max > 0;
-    uo += nkv > 0;
+      tc_fence_before();  // O has been read: the next unit's P hand-offs release its columns
+      kb += n_max;
+      tb += nkv;
+      uq += n_max > 0;
+      uo += nkv > 0;
     }
     tc_fence_before();
     asm volatile("bar.sync 0;" ::: "memory");
@@ -873,160 +875,160 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       int kb = 0, uq = 0;
       bool ok = true;
       for (int unit = 0; ok && take(unit, &v); ++unit) {
-      const int n_max = v.n_max, kbase = v.kbase, kleft = v.kleft, hk = v.w.hk;
-      if (n_max == 0) continue;
-      if (CONVQ) {
-        // queries in place: this thread's row of each tile, brought to fp16 relative to its largest power of two
-        ok = wait_or_abort(smem_u32(bar_q), uq & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 32);
-        ok = __all_sync(0xffffffffu, ok);
-        const int r = w * 32 + lane;
-        for (int t = 0; ok && t < 2; ++t) {
-          uint8_t* q = sQ + t * C::QT_BYTES + r * 128;
-          float amax = 0.0f;
-          for (int i = 0; i < 8 * KSUB; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
-            const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 f = unpack16(ws[u], 1);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          }
-          const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
-          const float inv = pow2i(-e);
-          sRow[(uq & 1) * 256 + t * 128 + r] = static_cast<int8_t>(e);
-          for (int i = 0; i < 8 * KSUB; ++i) {
-            uint4* at = reinterpret_cast<uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
-            const uint4 x = *at;
-            uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float2 f = unpack16(ws[u], 1);
-              ws[u] = pack16(f.x * inv, f.y * inv, 0);
-            }
-            *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar_q2);
-      }
-      // K and V tiles: this warp's 32 keys, a 16-byte piece of a code vector per lane and step. The exponents of this
-      // lane's key are fetched a tile ahead, its page two.
-      constexpr int LPR = D / 16;        // lanes of a row
-      constexpr int RPS = 32 / LPR;      // rows of a step
-      const int* trow = p.table + static_cast<long long>(v.w.seq) * p.max_pages;
-      const int page_mask = (1 << p.page_log2) - 1;
-      constexpr int NONE = -100000;
-      // (what a load returns is left alone until a later tile: any arithmetic on it here would wait for it)
-      auto page_of = [&](int j) -> int {
-        const int k = j * BN + w * 32 + lane;
-        return j < n_max && k < kleft ? __ldg(trow + ((kbase + k) >> p.page_log2)) : NONE;
-      };
-      auto exps_of = [&](int j, int pg) -> int2 {  // this lane's key's bytes in tile j, 0 past the end
-        if (j >= n_max || j * BN + w * 32 + lane >= kleft) return make_int2(0, 0);
-        if (pg < 0 || pg >= p.n_pages) pg = 0;
-        const long long vec = ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + ((kbase + j * BN + w * 32 + lane) & page_mask);
-        return make_int2(__ldg(p.k_scale + vec), __ldg(p.v_scale + vec));
-      };
-      // 2^e in both halves of a register, for e <= 0 (0 below fp16's numbers)
-      auto pow2h = [&](int e) -> uint32_t { return (e >= -14 ? (e + 15) << 10 : (e < -24 ? 0 : 1 << (e + 24))) * 0x10001u; };
-      // row of step i: w * 32 + i * RPS + lane / LPR. 16 features are two 16-byte pieces of the fp16 row; at d = 128 the
-      // lanes of the second half store them in the other order, so that a row's eight lanes always meet eight different
-      // banks. The swizzle of step i differs from that of step 0 by bit 2 of the row (d = 128) or not at all.
-      const int c0 = 2 * (lane % LPR);
-      const int flip = D == 128 ? (c0 >> 3) : 0;
-      const int r0 = w * 32 + lane / LPR;
-      const uint32_t to = (c0 >> 3) * TILE_BYTES + r0 * 128;
-      const uint32_t p0 = (((c0 + flip) & 7) ^ (r0 & 7)) << 4, p1 = (((c0 + 1 - flip) & 7) ^ (r0 & 7)) << 4;
-      const uint32_t from = smem_u32(sRaw) + r0 * D + (lane % LPR) * 16;
-      auto convert = [&](uint32_t raw, uint32_t tile, uint32_t factor, bool tail) {
-#pragma unroll
-        for (int i = 0; i < 32 / RPS; ++i) {
-          uint32_t c[4], h[8];
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + i * RPS * D));
-          const uint32_t f = __shfl_sync(0xffffffffu, factor, i * RPS + lane / LPR);
-          if (tail && f == 0xffffffffu) c[0] = c[1] = c[2] = c[3] = 0u;  // past the end: whatever the slot holds
-          const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t a = e4m3x2_to_f16x2(c[u] & 0xffffu), b = e4m3x2_to_f16x2(c[u] >> 16);
-            __half2 ha = __hmul2(*reinterpret_cast<__half2*>(&a), f2), hb = __hmul2(*reinterpret_cast<__half2*>(&b), f2);
-            if (tail && f == 0xffffffffu) ha = hb = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
-            h[2 * u] = *reinterpret_cast<uint32_t*>(&ha);
-            h[2 * u + 1] = *reinterpret_cast<uint32_t*>(&hb);
-          }
-          const uint32_t dst = tile + to + i * RPS * 128, x = D == 128 ? (i & 1) * 64u : 0u;
-          const bool fl = flip != 0;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (p0 ^ x)), "r"(fl ? h[4] : h[0]), "r"(fl ? h[5] : h[1]),
-                       "r"(fl ? h[6] : h[2]), "r"(fl ? h[7] : h[3]) : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (p1 ^ x)), "r"(fl ? h[0] : h[4]), "r"(fl ? h[1] : h[5]),
-                       "r"(fl ? h[2] : h[6]), "r"(fl ? h[3] : h[7]) : "memory");
-        }
-      };
-      auto exps_in = [&](int j, int2 b) -> int2 {
-        return j * BN + w * 32 + lane < kleft ? make_int2(b.x - 127, b.y - 127) : make_int2(NONE, NONE);
-      };
-      // the largest exponents of tile j's quarter go to the other warps a tile before they are needed
-      auto send_top = [&](int j, int2 b) {
-        if (j >= n_max) return;
-        const int2 e = exps_in(j, b);
-        const int kt = __reduce_max_sync(0xffffffffu, e.x), vt = __reduce_max_sync(0xffffffffu, e.y);
-        if (lane == 0) {
-          *reinterpret_cast<int2*>(sTop + ((kb + j) & 1) * 8 + w * 2) = make_int2(kt, vt);
-          mbar_arrive(bar_top);
-        }
-      };
-      int2 eb = exps_of(0, page_of(0));
-      int pg = page_of(1);
-      send_top(0, eb);
-      int kref = NONE, vref = NONE;  // the largest exponents so far
-      for (int j = 0; ok && j < n_max; ++j) {
-        const int stage = (kb + j) % STAGES;
-        const uint32_t free_par = (((kb + j) / STAGES) & 1u) ^ 1u, raw_par = (kb + j) & 1u;
-        const bool tail = kleft - j * BN < BN;
-        const bool in = j * BN + w * 32 + lane < kleft;
-        const int2 ex = exps_in(j, eb);
-        eb = exps_of(j + 1, pg);
-        pg = page_of(j + 2);
-        const int* top = sTop + raw_par * 8;
-        ok = wait_or_abort(smem_u32(bar_top), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 44);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int2 t = *reinterpret_cast<const int2*>(top + i * 2);
-          kref = max(kref, t.x);
-          vref = max(vref, t.y);
-        }
-        if (ok) ok = wait_or_abort(smem_u32(&bar_raw[0]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 38);
-        if (ok) ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
-          if (w == 0 && lane == 0) *reinterpret_cast<int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2) = make_int2(kref, vref);
-          convert(from, smem_u32(sK) + stage * C::KV_BYTES, in ? pow2h(ex.x - kref) : 0xffffffffu, tail);
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bar_k_full[stage]);
-            mbar_arrive(&bar_raw_free[0]);
-          }
-          send_top(j + 1, eb);
-          ok = wait_or_abort(smem_u32(&bar_raw[1]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 39);
-          if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
+        const int n_max = v.n_max, kbase = v.kbase, kleft = v.kleft, hk = v.w.hk;
+        if (n_max == 0) continue;
+        if (CONVQ) {
+          // queries in place: this thread's row of each tile, brought to fp16 relative to its largest power of two
+          ok = wait_or_abort(smem_u32(bar_q), uq & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 32);
           ok = __all_sync(0xffffffffu, ok);
-        }
-        if (ok) {
-          convert(from + C::RAW, smem_u32(sV) + stage * C::KV_BYTES, in ? pow2h(ex.y - vref) : 0xffffffffu, tail);
+          const int r = w * 32 + lane;
+          for (int t = 0; ok && t < 2; ++t) {
+            uint8_t* q = sQ + t * C::QT_BYTES + r * 128;
+            float amax = 0.0f;
+            for (int i = 0; i < 8 * KSUB; ++i) {
+              const uint4 x = *reinterpret_cast<const uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
+              const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float2 f = unpack16(ws[u], 1);
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+            }
+            const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+            const float inv = pow2i(-e);
+            sRow[(uq & 1) * 256 + t * 128 + r] = static_cast<int8_t>(e);
+            for (int i = 0; i < 8 * KSUB; ++i) {
+              uint4* at = reinterpret_cast<uint4*>(q + (i >> 3) * TILE_BYTES + (((i & 7) ^ (r & 7)) << 4));
+              const uint4 x = *at;
+              uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float2 f = unpack16(ws[u], 1);
+                ws[u] = pack16(f.x * inv, f.y * inv, 0);
+              }
+              *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+            }
+          }
           fence_async_smem();
           __syncwarp();
+          if (ok && lane == 0) mbar_arrive(bar_q2);
+        }
+        // K and V tiles: this warp's 32 keys, a 16-byte piece of a code vector per lane and step. The exponents of this
+        // lane's key are fetched a tile ahead, its page two.
+        constexpr int LPR = D / 16;        // lanes of a row
+        constexpr int RPS = 32 / LPR;      // rows of a step
+        const int* trow = p.table + static_cast<long long>(v.w.seq) * p.max_pages;
+        const int page_mask = (1 << p.page_log2) - 1;
+        constexpr int NONE = -100000;
+        // (what a load returns is left alone until a later tile: any arithmetic on it here would wait for it)
+        auto page_of = [&](int j) -> int {
+          const int k = j * BN + w * 32 + lane;
+          return j < n_max && k < kleft ? __ldg(trow + ((kbase + k) >> p.page_log2)) : NONE;
+        };
+        auto exps_of = [&](int j, int pg) -> int2 {  // this lane's key's bytes in tile j, 0 past the end
+          if (j >= n_max || j * BN + w * 32 + lane >= kleft) return make_int2(0, 0);
+          if (pg < 0 || pg >= p.n_pages) pg = 0;
+          const long long vec = ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + ((kbase + j * BN + w * 32 + lane) & page_mask);
+          return make_int2(__ldg(p.k_scale + vec), __ldg(p.v_scale + vec));
+        };
+        // 2^e in both halves of a register, for e <= 0 (0 below fp16's numbers)
+        auto pow2h = [&](int e) -> uint32_t { return (e >= -14 ? (e + 15) << 10 : (e < -24 ? 0 : 1 << (e + 24))) * 0x10001u; };
+        // row of step i: w * 32 + i * RPS + lane / LPR. 16 features are two 16-byte pieces of the fp16 row; at d = 128 the
+        // lanes of the second half store them in the other order, so that a row's eight lanes always meet eight different
+        // banks. The swizzle of step i differs from that of step 0 by bit 2 of the row (d = 128) or not at all.
+        const int c0 = 2 * (lane % LPR);
+        const int flip = D == 128 ? (c0 >> 3) : 0;
+        const int r0 = w * 32 + lane / LPR;
+        const uint32_t to = (c0 >> 3) * TILE_BYTES + r0 * 128;
+        const uint32_t p0 = (((c0 + flip) & 7) ^ (r0 & 7)) << 4, p1 = (((c0 + 1 - flip) & 7) ^ (r0 & 7)) << 4;
+        const uint32_t from = smem_u32(sRaw) + r0 * D + (lane % LPR) * 16;
+        auto convert = [&](uint32_t raw, uint32_t tile, uint32_t factor, bool tail) {
+#pragma unroll
+          for (int i = 0; i < 32 / RPS; ++i) {
+            uint32_t c[4], h[8];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + i * RPS * D));
+            const uint32_t f = __shfl_sync(0xffffffffu, factor, i * RPS + lane / LPR);
+            if (tail && f == 0xffffffffu) c[0] = c[1] = c[2] = c[3] = 0u;  // past the end: whatever the slot holds
+            const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t a = e4m3x2_to_f16x2(c[u] & 0xffffu), b = e4m3x2_to_f16x2(c[u] >> 16);
+              __half2 ha = __hmul2(*reinterpret_cast<__half2*>(&a), f2), hb = __hmul2(*reinterpret_cast<__half2*>(&b), f2);
+              if (tail && f == 0xffffffffu) ha = hb = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
+              h[2 * u] = *reinterpret_cast<uint32_t*>(&ha);
+              h[2 * u + 1] = *reinterpret_cast<uint32_t*>(&hb);
+            }
+            const uint32_t dst = tile + to + i * RPS * 128, x = D == 128 ? (i & 1) * 64u : 0u;
+            const bool fl = flip != 0;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (p0 ^ x)), "r"(fl ? h[4] : h[0]), "r"(fl ? h[5] : h[1]),
+                         "r"(fl ? h[6] : h[2]), "r"(fl ? h[7] : h[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (p1 ^ x)), "r"(fl ? h[0] : h[4]), "r"(fl ? h[1] : h[5]),
+                         "r"(fl ? h[2] : h[6]), "r"(fl ? h[3] : h[7]) : "memory");
+          }
+        };
+        auto exps_in = [&](int j, int2 b) -> int2 {
+          return j * BN + w * 32 + lane < kleft ? make_int2(b.x - 127, b.y - 127) : make_int2(NONE, NONE);
+        };
+        // the largest exponents of tile j's quarter go to the other warps a tile before they are needed
+        auto send_top = [&](int j, int2 b) {
+          if (j >= n_max) return;
+          const int2 e = exps_in(j, b);
+          const int kt = __reduce_max_sync(0xffffffffu, e.x), vt = __reduce_max_sync(0xffffffffu, e.y);
           if (lane == 0) {
-            mbar_arrive(&bar_v_full[stage]);
-            mbar_arrive(&bar_raw_free[1]);
+            *reinterpret_cast<int2*>(sTop + ((kb + j) & 1) * 8 + w * 2) = make_int2(kt, vt);
+            mbar_arrive(bar_top);
+          }
+        };
+        int2 eb = exps_of(0, page_of(0));
+        int pg = page_of(1);
+        send_top(0, eb);
+        int kref = NONE, vref = NONE;  // the largest exponents so far
+        for (int j = 0; ok && j < n_max; ++j) {
+          const int stage = (kb + j) % STAGES;
+          const uint32_t free_par = (((kb + j) / STAGES) & 1u) ^ 1u, raw_par = (kb + j) & 1u;
+          const bool tail = kleft - j * BN < BN;
+          const bool in = j * BN + w * 32 + lane < kleft;
+          const int2 ex = exps_in(j, eb);
+          eb = exps_of(j + 1, pg);
+          pg = page_of(j + 2);
+          const int* top = sTop + raw_par * 8;
+          ok = wait_or_abort(smem_u32(bar_top), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 44);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int2 t = *reinterpret_cast<const int2*>(top + i * 2);
+            kref = max(kref, t.x);
+            vref = max(vref, t.y);
+          }
+          if (ok) ok = wait_or_abort(smem_u32(&bar_raw[0]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 38);
+          if (ok) ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
+            if (w == 0 && lane == 0) *reinterpret_cast<int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2) = make_int2(kref, vref);
+            convert(from, smem_u32(sK) + stage * C::KV_BYTES, in ? pow2h(ex.x - kref) : 0xffffffffu, tail);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bar_k_full[stage]);
+              mbar_arrive(&bar_raw_free[0]);
+            }
+            send_top(j + 1, eb);
+            ok = wait_or_abort(smem_u32(&bar_raw[1]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 39);
+            if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          if (ok) {
+            convert(from + C::RAW, smem_u32(sV) + stage * C::KV_BYTES, in ? pow2h(ex.y - vref) : 0xffffffffu, tail);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&bar_v_full[stage]);
+              mbar_arrive(&bar_raw_free[1]);
+            }
           }
         }
-      }
-      kb += n_max;
-      ++uq;
+        kb += n_max;
+        ++uq;
       }
     }
     tc_fence_before();

@@ -93,6 +93,43 @@ __device__ __forceinline__ Unit find_unit(int n_seqs, int rank, int lane, F piec
   return u;
 }
 
+// The same pieces in the sequences' order, a sequence's highest place first, for batches of so many sequences that looking
+// through them for every rank would take longer than a piece: a walk that goes on from the rank before (ranks
+// must not fall), 32 sequences at a time.
+struct Walker {
+  int s0 = -32, total = 0, mine = 0, before = 0;  // the 32 sequences it stands in; this lane's pieces and those before them
+  long long base = 0;                             // pieces before these sequences
+  template <class F>
+  __device__ __forceinline__ Unit find(int n_seqs, long long rank, int lane, F pieces) {
+    while (rank >= base + total) {
+      base += total;
+      s0 += 32;
+      if (s0 >= n_seqs) {
+        total = 0;
+        s0 = n_seqs;
+        Unit none = {-1, 0};
+        return none;
+      }
+      mine = s0 + lane < n_seqs ? pieces(s0 + lane) : 0;
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      before = x - mine;
+      total = __shfl_sync(0xffffffffu, x, 31);
+    }
+    const int r = static_cast<int>(rank - base);
+    const int who = __ffs(__ballot_sync(0xffffffffu, r >= before && r < before + mine)) - 1;
+    Unit u;
+    u.seq = s0 + who;
+    u.place = __shfl_sync(0xffffffffu, mine - 1 - (r - before), who);
+    return u;
+  }
+};
+constexpr int kRankedSeqs = 256;  // more sequences than this are taken in their order
+
 // e4m3 with one power of two per vector: the smallest 2^e (e >= -126) under which the largest finite
 // |x| is at most 448 = 1.75 * 2^8. A power of two costs e4m3 no precision (the code is a floating-point
 // number itself) and makes the value code * 2^e exact in fp32 and, inside its range, in 16 bits; the byte
