@@ -69,10 +69,14 @@ struct SeqCfg {
   static constexpr int FLUSH = D == 64 ? 128 : 32;
   static constexpr bool OSUM_SMEM = D == 64;
   static constexpr uint32_t OSUM_BYTES = OSUM_SMEM ? 2u * D * 128u * 4u : 0u;
+  // Results leave through 4 KiB of shared memory per softmax warp, so that a store covers whole lines: a thread's own row
+  // written 16 bytes at a time costs a wavefront per lane. d = 64 takes the running sum's place when it is not in use.
+  static constexpr bool STAGED = OSUM_SMEM || !CONV;
+  static constexpr uint32_t OUT_BYTES = STAGED && !OSUM_SMEM ? 8u * 4096u : 0u;
   static constexpr uint32_t RAW = CONV ? 128u * D : 0u;  // a K or V tile's codes as they lie in the pages
   // running exponents per tile, factors of the queries' rows, the converter warps' largest exponents
   static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 2u * 4u + 512u + 64u : 0u;
-  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 80;
+  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + OUT_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 80;
   static_assert(SMEM_BYTES <= 232448, "shared memory exceeds 227 KiB");
   static_assert(COL_O1 + D <= TMEM_COLS, "tensor memory layout exceeds 512 columns");
   // setmaxnreg shares of warpgroup 0, the two softmax warpgroups and the converters
@@ -161,7 +165,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   uint8_t* sK = sQ + 2 * C::QT_BYTES;
   uint8_t* sV = sK + STAGES * C::KV_BYTES;
   float* sOsum = reinterpret_cast<float*>(sV + STAGES * C::KV_BYTES);
-  uint8_t* sRaw = sV + STAGES * C::KV_BYTES + C::OSUM_BYTES;  // e4m3: K and V codes
+  uint8_t* sOut = sV + STAGES * C::KV_BYTES;                  // (the running sum's place, or after it)
+  uint8_t* sRaw = sV + STAGES * C::KV_BYTES + C::OSUM_BYTES + C::OUT_BYTES;  // e4m3: K and V codes
   int* sExp = reinterpret_cast<int*>(sRaw + 2 * C::RAW);       // [2 * STAGES][K, V] exponents that a tile is relative to
   int8_t* sRow = reinterpret_cast<int8_t*>(sExp + 2 * STAGES * 2);  // [2][256] exponents that the queries' rows are relative to
   int* sTop = reinterpret_cast<int*>(sRow + 512);                   // [2][4 warps][K, V] largest exponents of a tile
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     osum_ok = smid < static_cast<uint32_t>(p.n_osum);
     sOsum = p.osum + static_cast<size_t>(osum_ok ? smid : 0u) * (2 * 128 * 128);
   }
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES + 2 * C::RAW + C::EXP_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + STAGES * C::KV_BYTES + C::OSUM_BYTES + C::OUT_BYTES + 2 * C::RAW + C::EXP_BYTES);
   uint64_t* bar_q = bars;
   uint64_t* bar_k_full = bar_q + 1;
   uint64_t* bar_v_full = bar_k_full + STAGES;
@@ -809,6 +814,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       const bool write = ok && rt < p.tpt && tok < v.w.qlen;
       const int hq = v.w.hk * p.G + (r - rt * p.G);
       const long long row = static_cast<long long>(v.w.tok_first + tok) * p.Hq + hq;
+      const bool staged = C::STAGED && !(C::OSUM_SMEM && osum_ok && nkv > C::FLUSH);
+      const uint32_t buf = smem_u32(sOut) + (C::OSUM_SMEM ? wg * (D * 128 * 4) + quarter * 4096 : (warp - 4) * 4096);
       const long long prow = static_cast<long long>(v.w.split) * p.T * p.Hq + row;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -835,7 +842,43 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = has ? __uint_as_float(o[e]) * inv_l : 0.0f;
         }
-        if (write) {
+        if (staged) {
+          // this warp's 32 rows x 128 bytes, 64 features of the result or 32 of a part; pieces of 16 bytes are swapped by
+          // row against bank conflicts
+          const uint32_t at = buf + lane * 128;
+          auto put = [&](int piece, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((piece ^ (lane & 7)) << 4)), "r"(w0), "r"(w1), "r"(w2), "r"(w3)
+                         : "memory");
+          };
+          const bool part = p.n_splits > 1;
+          if (part) {
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4)
+              put(q4, __float_as_uint(y[4 * q4]), __float_as_uint(y[4 * q4 + 1]), __float_as_uint(y[4 * q4 + 2]), __float_as_uint(y[4 * q4 + 3]));
+          } else {
+#pragma unroll
+            for (int q8 = 0; q8 < 4; ++q8)
+              put((c & 1) * 4 + q8, pack2(y[8 * q8 + 0], y[8 * q8 + 1], BF16), pack2(y[8 * q8 + 2], y[8 * q8 + 3], BF16),
+                  pack2(y[8 * q8 + 4], y[8 * q8 + 5], BF16), pack2(y[8 * q8 + 6], y[8 * q8 + 7], BF16));
+          }
+          if (part || (c & 1)) {
+            uint8_t* base = part ? reinterpret_cast<uint8_t*>(p.part_o + static_cast<long long>(v.w.split) * p.T * p.Hq * D + c * 32)
+                                 : static_cast<uint8_t*>(p.out) + (c >> 1) * 128;
+            const int row_bytes = part ? D * 4 : D * 2;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = i * 4 + (lane >> 3), piece = lane & 7;
+              const int to = __shfl_sync(0xffffffffu, write ? static_cast<int>(row) : -1, rr);
+              uint4 w;
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                           : "r"(buf + rr * 128 + ((piece ^ (rr & 7)) << 4)));
+              if (to >= 0) *(reinterpret_cast<uint4*>(base + static_cast<long long>(to) * row_bytes) + piece) = w;
+            }
+            __syncwarp();
+          }
+        } else if (write) {
           if (p.n_splits == 1) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c * 32);
 #pragma unroll
