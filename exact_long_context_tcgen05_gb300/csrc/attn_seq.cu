@@ -814,7 +814,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       const bool write = ok && rt < p.tpt && tok < v.w.qlen;
       const int hq = v.w.hk * p.G + (r - rt * p.G);
       const long long row = static_cast<long long>(v.w.tok_first + tok) * p.Hq + hq;
-      const bool staged = C::STAGED && !(C::OSUM_SMEM && osum_ok && nkv > C::FLUSH);
+      // (Without key tiles nothing says that the tile's other warps have left the unit before, whose running sum may lie here.)
+      const bool staged = C::STAGED && nkv > 0 && !(C::OSUM_SMEM && osum_ok && nkv > C::FLUSH);
       const uint32_t buf = smem_u32(sOut) + (C::OSUM_SMEM ? wg * (D * 128 * 4) + quarter * 4096 : (warp - 4) * 4096);
       const long long prow = static_cast<long long>(v.w.split) * p.T * p.Hq + row;
 #pragma unroll

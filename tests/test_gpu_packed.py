@@ -85,6 +85,23 @@ def test_long_rows(cq, d, dt):
         sq.check_lse(lse[:, first:first + 100], rl, f"from {first}")
 
 
+def test_long_rows_before_short_ones(cq):
+    """Units long enough for the running sum in shared memory, followed on the same SMs by units whose second row tile is
+    empty: the long sequence's rows are bit by bit what they are alone."""
+    lens = [16500] + [100] * 200
+    q, k, v = (sq.normal((sum(lens), 8, 64), torch.float16, i) for i in (1, 2, 3))
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    alone, lalone = cq.attention_packed(q[:16500], k[:16500], v[:16500], cu[:2], causal=False, return_lse=True)
+    for _ in range(3):
+        out, lse = cq.attention_packed(q, k, v, cu, causal=False, return_lse=True)
+        assert torch.equal(out[:16500], alone) and torch.equal(lse[:, :16500], lalone)
+    _ok(cq)
+    for first in (0, 16384, 16400):
+        ref, rl, mass = sq.attend(q[first:first + 100], k[:16500], v[:16500], first, False)
+        sq.check_out(out[first:first + 100], ref, mass, torch.float16, torch.float16, f"from {first}", 16500 * 2.0 ** -34)
+        sq.check_lse(lse[:, first:first + 100], rl, f"from {first}")
+
+
 def test_strides_scale_streams_and_graph(cq):
     """Slices of a fused projection, another scale and stream, capture and replay with other lengths."""
     d, dtype, lens = 128, torch.bfloat16, [70, 200]
