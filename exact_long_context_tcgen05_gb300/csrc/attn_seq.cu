@@ -8,14 +8,16 @@
 //   Rows     a tile's 128 rows are floor(128 / G) tokens times the G query heads of one key head (row
 //            r = token r / G, head r % G), loaded by one 3-D TMA box, so that a short sequence or chunk fills tiles G
 //            times better and K/V are loaded once for the whole group.
-//   Units    a CTA takes two row tiles of one (sequence, key head); it finds its unit from cu_seqlens alone.
-//            Units are ranked by their place in their sequence, the latest (under the causal mask the
-//            heaviest) first, so that the grid ends on light ones.
-//   Split    a chunk over a long cache has few units: each may be cut into n_splits ranges of its key tiles
-//            (grid * n_splits CTAs), which leave normalised fp32 partials that seq_combine_kernel joins.
+//   Units    two row tiles of one (sequence, key head). One CTA per SM works through several, the next one's loads and
+//            first products beside the end of the last. Packed prompts: units are found from cu_seqlens alone, ranked by
+//            their place in their sequence, the latest (under the causal mask the heaviest) first.
+//   Ranges   chunks over a long cache have few units of very different lengths, so the key tiles of all units, laid end
+//            to end, are cut into one equal range per CTA, as attn_decode.cu does: a range's whole units are written out, the
+//            two others leave normalised fp32 parts that seq_combine_kernel joins. (Whole units, or every unit in the same
+//            number of ranges: 787 us against 712 for 256 units of 266 tiles, 135 against 86 for 12 ragged e4m3 sequences.)
 //   P        is rounded once to dtype for P V (2^-8 relative for bf16, as the output is; attn_fwd.cu's
-//            hi/lo split, half as many products again, serves fp32 partial results), scaled by 2^14 so that
-//            fp16 keeps its relative precision down to p = 2^-28.
+//            hi/lo split, half as many products again, serves fp32 partial results), scaled by 2^6 so that
+//            fp16 keeps its relative precision down to p = 2^-20 of the row's largest at least.
 //   Tails    rows of V past a sequence's end (another sequence's tokens, or whatever an unused slot holds) are zeroed in
 //            shared memory before the product: p = 0 does not hide an infinity or NaN there.
 //   e4m3     the producer copies code vectors as they lie in the pages, and four converter warps turn them into
@@ -76,7 +78,7 @@ struct SeqCfg {
   static constexpr uint32_t RAW = CONV ? 128u * D : 0u;  // a K or V tile's codes as they lie in the pages
   // running exponents per tile, factors of the queries' rows, the converter warps' largest exponents
   static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 2u * 4u + 512u + 64u : 0u;
-  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + OUT_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 80;
+  static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + OUT_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 112;
   static_assert(SMEM_BYTES <= 232448, "shared memory exceeds 227 KiB");
   static_assert(COL_O1 + D <= TMEM_COLS, "tensor memory layout exceeds 512 columns");
   // setmaxnreg shares of warpgroup 0, the two softmax warpgroups and the converters
@@ -89,7 +91,57 @@ struct SeqCfg {
 
 // What a CTA works on next, as its scheduling warp hands it to the others.
 struct Work {
-  int valid, seq, tok_first, qlen, kvlen, ta, hk, split;
+  int valid, seq, tok_first, qlen, kvlen, ta, hk;  // two row tiles from token ta of the sequence's
+  int jb, je;                                      // key tiles [jb, je) of those the row tiles see
+  int slot, pad0, pad1;                            // where a part goes (-1: the whole unit, to the output)
+};
+
+// A chunk's units weigh as many as the key tiles they see (one at least, for the rows that see nothing) and kUnitWeight
+// more, about what a unit costs beside them; a range weighs kLeastRange at least.
+constexpr int kUnitWeight = 2, kLeastRange = 6;
+constexpr int kPartRows = 256;  // rows of a unit, and of a part
+
+// sum over i in [0, n) of floor((a i + b) / m), a, b >= 0, m > 0, by the reduction that Euclid's algorithm makes of
+// (a, m). All values but the sum stay below 2^32.
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+  long long r = 0;
+  while (n > 0) {
+    r += static_cast<long long>(a / m) * (static_cast<long long>(n) * (n - 1) / 2) + static_cast<long long>(b / m) * n;
+    a %= m;
+    b %= m;
+    const uint32_t top = a * n + b;
+    n = top / m;
+    b = top % m;
+    const uint32_t x = m;
+    m = a;
+    a = x;
+  }
+  return r;
+}
+
+// The units of a sequence's new tokens over its positions, for one key head: unit i takes tokens [i per, (i + 1) per).
+struct ChunkUnits {
+  int seq, first, qlen, kvlen, per, units, causal;
+  __device__ __forceinline__ int last(int i) const {  // the last position that unit i sees, -1 or less for none
+    return causal ? kvlen - qlen + min((i + 1) * per, qlen) - 1 : kvlen - 1;
+  }
+  __device__ __forceinline__ int tiles(int i) const {
+    const int p = last(i);
+    return p < 0 ? 1 : p / BN + 1;
+  }
+  // what units [0, i) weigh: their last positions are an arithmetic progression (the last unit's may be less)
+  __device__ __forceinline__ long long before(int i) const {
+    long long w = static_cast<long long>(i) * (kUnitWeight + 1);
+    if (!causal) return w + static_cast<long long>(i) * (max(kvlen - 1, 0) / BN);
+    if (i == 0) return w;
+    if (i == units) {
+      w += max(kvlen - 1, 0) / BN;
+      --i;
+    }
+    const int a = kvlen - qlen + per - 1;
+    const int skip = a < 0 ? min(i, (-a + per - 1) / per) : 0;
+    return w + floor_sum(i - skip, BN, per, max(a + skip * per, 0));
+  }
 };
 
 struct SeqParams {
@@ -102,12 +154,14 @@ struct SeqParams {
   const uint8_t* v_scale;
   void* out;
   float* lse;
-  float* part_o;  // [n_splits][T][Hq][D]
-  float* part_l;  // [n_splits][T][Hq], base 2
+  float* part_o;  // [phases * CTAs][2][kPartRows][D]
+  float* part_l;  // [phases * CTAs][2][kPartRows], base 2
+  int4* meta;     // [phases * CTAs][2] the unit a range begins in the middle of: sequence (-1: none), key head, first and last
+                  // range of it; the sequence's first token and tokens, the unit's first token
   float* osum;
   int n_osum;
   int n_seqs, T, Hq, Hkv, G, tpt;  // tpt: tokens of a row tile, floor(128 / G)
-  int n_splits, max_pages, n_pages, page_log2, causal;
+  int phases, max_pages, n_pages, page_log2, causal;
   float scale_log2;
   unsigned timeout_us;
   int fault;  // test hook: 1 = block 0 never loads key tile 1
@@ -281,8 +335,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       return last < 0 ? 0 : last / BN + 1;
     };
     const int all0 = tile_kv(w.ta), all1 = tile_kv(v.tb), all = max(all0, all1);
-    v.jb = static_cast<int>(static_cast<long long>(all) * w.split / p.n_splits);
-    const int je = static_cast<int>(static_cast<long long>(all) * (w.split + 1) / p.n_splits);
+    v.jb = w.jb;
+    const int je = min(w.je, all);
     v.nkv0 = min(max(all0 - v.jb, 0), je - v.jb);
     v.nkv1 = min(max(all1 - v.jb, 0), je - v.jb);
     v.n_max = max(v.nkv0, v.nkv1);
@@ -294,10 +348,11 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   auto take = [&](int i, View* v) -> bool {
     const bool ok = wait_or_abort(smem_u32(&bar_unit[i & 1]), (i >> 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 40);
     if (!__all_sync(0xffffffffu, ok)) return false;
-    const int4 a = *reinterpret_cast<const int4*>(&sWork[i & 1]), b = *(reinterpret_cast<const int4*>(&sWork[i & 1]) + 1);
+    const int4* at = reinterpret_cast<const int4*>(&sWork[i & 1]);
+    const int4 a = at[0], b = at[1], c = at[2];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar_unit_free[i & 1]);
-    const Work w = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const Work w = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, 0, 0};
     if (!w.valid) return false;
     *v = view_of(w);
     return true;
@@ -307,33 +362,148 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::LOW));
     if (warp == 3) {
       // ------------------------------------------------------------------ units
-      const unsigned per_rank = static_cast<unsigned>(p.Hkv * p.n_splits);
       const int per = 2 * p.tpt;
-      auto pieces = [&](int k) {
-        int first;
-        return (seq_tokens(p.cu, k, p.T, &first) + per - 1) / per;
-      };
-      Walker walk;
-      for (int i = 0;; ++i) {
-        const unsigned u = static_cast<unsigned>(i) * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const int rank = static_cast<int>(u / per_rank), sub = static_cast<int>(u - rank * per_rank);
-        const Unit f = p.n_seqs > kRankedSeqs ? walk.find(p.n_seqs, rank, lane, pieces) : find_unit(p.n_seqs, rank, lane, pieces);
-        Work w = {f.seq >= 0, f.seq, 0, 0, 0, f.place * per, sub / p.n_splits, sub % p.n_splits};
-        if (w.valid) {
-          w.qlen = seq_tokens(p.cu, f.seq, p.T, &w.tok_first);
-          w.kvlen = SRC == kSrcPacked ? w.qlen : seq_positions(p.kv_lens, f.seq, static_cast<long long>(p.max_pages) << p.page_log2);
-        }
+      auto give = [&](int i, const Work& w) -> bool {
         if (i >= 2) {
           const bool ok = wait_or_abort(smem_u32(&bar_unit_free[i & 1]), ((i >> 1) - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 41);
-          if (!__all_sync(0xffffffffu, ok)) break;
+          if (!__all_sync(0xffffffffu, ok)) return false;
         }
         if (lane == 0) {
-          *reinterpret_cast<int4*>(&sWork[i & 1]) = make_int4(w.valid, w.seq, w.tok_first, w.qlen);
-          *(reinterpret_cast<int4*>(&sWork[i & 1]) + 1) = make_int4(w.kvlen, w.ta, w.hk, w.split);
+          int4* at = reinterpret_cast<int4*>(&sWork[i & 1]);
+          at[0] = make_int4(w.valid, w.seq, w.tok_first, w.qlen);
+          at[1] = make_int4(w.kvlen, w.ta, w.hk, w.jb);
+          at[2] = make_int4(w.je, w.slot, 0, 0);
           mbar_arrive(&bar_unit[i & 1]);
         }
         __syncwarp();
-        if (!w.valid) break;
+        return w.valid != 0;
+      };
+      const Work none = {0, 0, 0, 0, 0, 0, 0, 0, 0, -1, 0, 0};
+      if constexpr (SRC == kSrcPacked) {
+        auto pieces = [&](int k) {
+          int first;
+          return (seq_tokens(p.cu, k, p.T, &first) + per - 1) / per;
+        };
+        Walker walk;
+        for (int i = 0;; ++i) {
+          const unsigned u = static_cast<unsigned>(i) * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+          const int rank = static_cast<int>(u / p.Hkv);
+          const Unit f = p.n_seqs > kRankedSeqs ? walk.find(p.n_seqs, rank, lane, pieces) : find_unit(p.n_seqs, rank, lane, pieces);
+          Work w = none;
+          if (f.seq >= 0) {
+            w.valid = 1;
+            w.seq = f.seq;
+            w.qlen = w.kvlen = seq_tokens(p.cu, f.seq, p.T, &w.tok_first);
+            w.ta = f.place * per;
+            w.hk = static_cast<int>(u % p.Hkv);
+            w.je = 0x7fffffff;
+          }
+          if (!give(i, w)) break;
+        }
+      } else {
+        auto units_of = [&](int k) -> ChunkUnits {
+          ChunkUnits c;
+          c.seq = k;
+          c.qlen = seq_tokens(p.cu, k, p.T, &c.first);
+          c.kvlen = seq_positions(p.kv_lens, k, static_cast<long long>(p.max_pages) << p.page_log2);
+          c.per = per;
+          c.units = (c.qlen + per - 1) / per;
+          c.causal = p.causal;
+          return c;
+        };
+        // what 32 sequences from s0 on weigh for one key head, one a lane; *upto: this lane's and those before it
+        auto weigh = [&](int s0, long long* upto) -> long long {
+          long long x = 0;
+          if (s0 + lane < p.n_seqs) {
+            const ChunkUnits c = units_of(s0 + lane);
+            x = c.before(c.units);
+          }
+          const long long mine = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+          }
+          *upto = x;
+          return mine;
+        };
+        long long all = 0, upto, mine;
+        for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+          mine = weigh(s0, &upto);
+          all += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        int i = 0;
+        bool ok = true;
+        for (int ph = 0; ok && ph < p.phases; ++ph) {
+          // units in the order of sequences, then key heads [h0, h1), then places
+          const int h0 = static_cast<int>(static_cast<long long>(p.Hkv) * ph / p.phases);
+          const int h1 = static_cast<int>(static_cast<long long>(p.Hkv) * (ph + 1) / p.phases), nh = h1 - h0;
+          const long long W = all * nh;
+          const long long nc = min(static_cast<long long>(gridDim.x), max(W / kLeastRange, 1LL)), bx = blockIdx.x;
+          const long long w0 = W * min(bx, nc) / nc, w1 = W * min(bx + 1, nc) / nc;
+          const int range = ph * gridDim.x + blockIdx.x;
+          if (w0 >= w1) {
+            if (lane == 0) p.meta[2 * range] = make_int4(-1, 0, 0, 0);
+            continue;
+          }
+          ChunkUnits c;
+          int place = 0, hk = 0;
+          long long u0 = 0;  // where the unit begins
+          for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+            if (p.n_seqs > 32) mine = weigh(s0, &upto);
+            const unsigned who = __ballot_sync(0xffffffffu, w0 < u0 + upto * nh);
+            if (who) {
+              const int k = __ffs(who) - 1;
+              c = units_of(s0 + k);
+              u0 += __shfl_sync(0xffffffffu, upto - mine, k) * nh;
+              break;
+            }
+            u0 += __shfl_sync(0xffffffffu, upto, 31) * nh;
+          }
+          const long long head = c.before(c.units);
+          hk = static_cast<int>((w0 - u0) / head);
+          u0 += hk * head;
+          hk += h0;
+          for (int n = c.units; n > 1;) {  // the last unit that begins at w0 or before, in 32 steps at a time
+            const int step = (n + 31) / 32;
+            const bool le = lane * step < n && u0 + c.before(place + lane * step) <= w0;
+            const int k = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
+            n = min(step, n - k * step);
+            place += k * step;
+          }
+          u0 += c.before(place);
+          for (long long w = w0; ok && w < w1;) {
+            const int n = c.tiles(place) + kUnitWeight;
+            const long long next = min(u0 + n, w1);
+            const int t0 = max(static_cast<int>(w - u0) - kUnitWeight, 0), t1 = max(static_cast<int>(next - u0) - kUnitWeight, 0);
+            const bool whole = t0 == 0 && t1 == n - kUnitWeight;
+            if (w == w0 && lane == 0) {
+              // the unit this range begins in the middle of, and the ranges that hold its first and last key tile
+              const int c0 = static_cast<int>(((u0 + kUnitWeight + 1) * nc - 1) / W), c1 = static_cast<int>(((u0 + n) * nc - 1) / W);
+              const int r0 = ph * gridDim.x;
+              p.meta[2 * range] = t0 == 0 ? make_int4(-1, 0, 0, 0) : make_int4(c.seq, hk, r0 + c0, r0 + c1);
+              p.meta[2 * range + 1] = make_int4(c.first, c.qlen, place * per, 0);
+            }
+            if (t0 < t1) {  // (else the range ends before the unit's first key tile)
+              const Work g = {1, c.seq, c.first, c.qlen, c.kvlen, place * per, hk, t0, t1, whole ? -1 : 2 * range + (t0 == 0 ? 1 : 0), 0, 0};
+              ok = give(i++, g);
+            }
+            w = next;
+            u0 += n;
+            if (++place == c.units) {
+              place = 0;
+              if (++hk == h1) {
+                hk = h0;
+                for (int k = c.seq + 1; w < w1 && k < p.n_seqs; ++k) {
+                  c = units_of(k);
+                  if (c.units > 0) break;
+                }
+              }
+            }
+          }
+        }
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (ok) give(i, none);
       }
     } else if (warp == 0) {
       // ------------------------------------------------------------------ TMA producer
@@ -817,7 +987,9 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       // (Without key tiles nothing says that the tile's other warps have left the unit before, whose running sum may lie here.)
       const bool staged = C::STAGED && nkv > 0 && !(C::OSUM_SMEM && osum_ok && nkv > C::FLUSH);
       const uint32_t buf = smem_u32(sOut) + (C::OSUM_SMEM ? wg * (D * 128 * 4) + quarter * 4096 : (warp - 4) * 4096);
-      const long long prow = static_cast<long long>(v.w.split) * p.T * p.Hq + row;
+      const bool part = SRC != kSrcPacked && v.w.slot >= 0;
+      // (T * Hq < 2^31)
+      const int to_row = part ? v.w.slot * kPartRows + wg * 128 + r : static_cast<int>(row);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -851,7 +1023,6 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((piece ^ (lane & 7)) << 4)), "r"(w0), "r"(w1), "r"(w2), "r"(w3)
                          : "memory");
           };
-          const bool part = p.n_splits > 1;
           if (part) {
 #pragma unroll
             for (int q4 = 0; q4 < 8; ++q4)
@@ -863,14 +1034,14 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
                   pack2(y[8 * q8 + 4], y[8 * q8 + 5], BF16), pack2(y[8 * q8 + 6], y[8 * q8 + 7], BF16));
           }
           if (part || (c & 1)) {
-            uint8_t* base = part ? reinterpret_cast<uint8_t*>(p.part_o + static_cast<long long>(v.w.split) * p.T * p.Hq * D + c * 32)
+            uint8_t* base = part ? reinterpret_cast<uint8_t*>(p.part_o + c * 32)
                                  : static_cast<uint8_t*>(p.out) + (c >> 1) * 128;
             const int row_bytes = part ? D * 4 : D * 2;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int rr = i * 4 + (lane >> 3), piece = lane & 7;
-              const int to = __shfl_sync(0xffffffffu, write ? static_cast<int>(row) : -1, rr);
+              const int to = __shfl_sync(0xffffffffu, write ? to_row : -1, rr);
               uint4 w;
               asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                            : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
@@ -880,7 +1051,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             __syncwarp();
           }
         } else if (write) {
-          if (p.n_splits == 1) {
+          if (!part) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + c * 32);
 #pragma unroll
             for (int q8 = 0; q8 < 4; ++q8) {
@@ -892,14 +1063,14 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
               dst[q8] = w;
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + c * 32);
+            float4* dst = reinterpret_cast<float4*>(p.part_o + static_cast<long long>(to_row) * D + c * 32);
 #pragma unroll
             for (int q4 = 0; q4 < 8; ++q4) dst[q4] = make_float4(y[4 * q4], y[4 * q4 + 1], y[4 * q4 + 2], y[4 * q4 + 3]);
           }
         }
       }
       if (write) {
-        if (p.n_splits > 1) p.part_l[prow] = lse2;
+        if (part) p.part_l[to_row] = lse2;
         else if (p.lse) p.lse[static_cast<long long>(hq) * p.T + v.w.tok_first + tok] = lse2 * 0.69314718055994531f;
       }
       tc_fence_before();  // O has been read: the next unit's P hand-offs release its columns
@@ -1080,36 +1251,44 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   }
 }
 
-// Joins the partials of n_splits ranges: M = max_k lse_k, out = sum_k 2^(lse_k - lse) O_k in the order of the ranges.
+// Joins the parts of the units that several ranges share. Blocks (c, .) look after the unit that range c begins in the
+// middle of, if it is the first such one: M = max_k lse_k, out = sum_k 2^(lse_k - lse) O_k in the order of the ranges.
+constexpr int kJoinBlocks = 8;  // blocks of a unit's rows
 template <int D, int BF16>
 __global__ void __launch_bounds__(256) seq_combine_kernel(const SeqParams p) {
-  constexpr int TPR = D / 4;
+  constexpr int TPR = D / 4, RPB = 256 / TPR;  // threads of a row, rows of a block
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long e = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const long long row = e / TPR, rows = static_cast<long long>(p.T) * p.Hq;
-  const int c = static_cast<int>(e % TPR);
-  if (row >= rows) return;
-  const int tok = static_cast<int>(row / p.Hq), hq = static_cast<int>(row - static_cast<long long>(tok) * p.Hq);
-  if (tok < cu_at(p.cu, 0, p.T) || tok >= cu_at(p.cu, p.n_seqs, p.T)) return;
-  float M = -INFINITY;
-  for (int k = 0; k < p.n_splits; ++k) M = fmaxf(M, __ldcg(p.part_l + k * rows + row));
-  float L = 0.0f;
-  float4 a = make_float4(0, 0, 0, 0);
-  for (int k = 0; k < p.n_splits; ++k) {
-    const float lk = __ldcg(p.part_l + k * rows + row);
-    const float4 b = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (k * rows + row) * TPR + c);
-    if (lk == -INFINITY) continue;
-    const float w = exp2f(lk - M);
-    L += w;
-    a.x = fmaf(w, b.x, a.x);
-    a.y = fmaf(w, b.y, a.y);
-    a.z = fmaf(w, b.z, a.z);
-    a.w = fmaf(w, b.w, a.w);
+  const int4 m = __ldcg(p.meta + 2 * blockIdx.x), q = __ldcg(p.meta + 2 * blockIdx.x + 1);
+  if (m.x < 0 || static_cast<int>(blockIdx.x) != m.z + 1) return;
+  const int parts = m.w - m.z + 1, c = threadIdx.x % TPR;
+  for (int r = blockIdx.y * RPB + threadIdx.x / TPR; r < kPartRows; r += kJoinBlocks * RPB) {
+    const int rt = (r & 127) / p.G, tok = q.z + (r >> 7) * p.tpt + rt;
+    if (rt >= p.tpt || tok >= q.y) continue;
+    // the first part is its range's last piece, the others are their ranges' first
+    auto at = [&](int k) -> long long { return (2LL * (m.z + k) + (k == 0 ? 1 : 0)) * kPartRows + r; };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(p.part_l + at(k)));
+    float L = 0.0f;
+    float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float lk = __ldcg(p.part_l + at(k));
+      const float4 b = __ldcg(reinterpret_cast<const float4*>(p.part_o) + at(k) * TPR + c);
+      const float w = lk == -INFINITY ? 0.0f : exp2f(lk - M);  // (such a part is zero; NaN passes on)
+      L += w;
+      a.x = fmaf(w, b.x, a.x);
+      a.y = fmaf(w, b.y, a.y);
+      a.z = fmaf(w, b.z, a.z);
+      a.w = fmaf(w, b.w, a.w);
+    }
+    const bool has = !(L <= 0.0f);
+    const float inv = has ? 1.0f / L : 0.0f;
+    const int hq = m.y * p.G + ((r & 127) - rt * p.G);
+    const long long row = static_cast<long long>(q.x + tok) * p.Hq + hq;
+    reinterpret_cast<uint2*>(p.out)[row * TPR + c] = make_uint2(pack2(a.x * inv, a.y * inv, BF16), pack2(a.z * inv, a.w * inv, BF16));
+    if (p.lse && c == 0) p.lse[static_cast<long long>(hq) * p.T + q.x + tok] = has ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
   }
-  const bool has = !(L <= 0.0f);
-  const float inv = has ? 1.0f / L : 0.0f;
-  reinterpret_cast<uint2*>(p.out)[row * TPR + c] = make_uint2(pack2(a.x * inv, a.y * inv, BF16), pack2(a.z * inv, a.w * inv, BF16));
-  if (p.lse && c == 0) p.lse[static_cast<long long>(hq) * p.T + tok] = has ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 template <int D, int BF16, int SRC>
@@ -1135,12 +1314,13 @@ int launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv
     attr.mark(dev);
   }
   const long long sms = sm_count();
-  kern<<<static_cast<unsigned>(grid < sms ? grid : sms), C::NTHR, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
+  const unsigned ctas = static_cast<unsigned>(grid < sms ? grid : sms);
+  kern<<<ctas, C::NTHR, C::SMEM_BYTES, stream>>>(mq, mk, mv, p);
   int rc = cuda_status(cudaGetLastError(), "sequence attention kernel launch");
-  if (rc != CQSA_OK || p.n_splits == 1) return rc;
+  if (rc != CQSA_OK || SRC == kSrcPacked || ctas == 1) return rc;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.T) * p.Hq * (D / 4) + 255) / 256));
+  cfg.gridDim = dim3(ctas * p.phases, kJoinBlocks);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -1175,29 +1355,29 @@ int make_token_map(CUtensorMap* m, const void* base, int dtype, int d, int heads
 // An upper bound on the pairs of row tiles of n_seqs sequences that hold T tokens together.
 long long pairs_bound(int T, int n_seqs, int tpt) { return T / (2 * tpt) + (T < n_seqs ? T : n_seqs); }
 
-// Ranges that the key tiles of a unit are cut into: the number with the least estimated time, in microseconds. A key tile
-// takes about 1.2 (d = 64, 0.9), a range about 3 on top, and each further range writes and reads its rows in fp32 at
-// 4 TB/s. One sequence: its units go over the SMs in whole rounds. Several: their lengths are not known here, so
-// the average is taken as 2/5 of the longest, and the longest range follows on the others.
-int chunk_splits(const PagedArgs& a) {
-  const int G = a.Hq / a.Hkv, tpt = 128 / G, sms = sm_count();
+// CTAs of a chunk: one per SM, fewer when the ranges would weigh less than kLeastRange (by the caller's longest sequence; longer
+// ones are still computed, with fewer CTAs than they could use).
+int chunk_ctas(const PagedArgs& a) {
+  const int tpt = 128 / (a.Hq / a.Hkv), sms = sm_count();
   const long long by_tokens = pairs_bound(a.T, a.n_seqs, tpt);
   const long long by_longest = static_cast<long long>(a.n_seqs) * ((a.max_q_len + 2 * tpt - 1) / (2 * tpt));
-  const double units = static_cast<double>((by_tokens < by_longest ? by_tokens : by_longest) * a.Hkv);
-  const double n = (a.max_kv_len + BN - 1) / BN, tile = a.d == 64 ? 0.9 : 1.2;
-  const double part = static_cast<double>(a.T) * a.Hq * a.d * 8.0 / 4e6;
-  int best = 1;
-  double least = 1e30;
-  for (int s = 1; s <= 32 && (s == 1 || s * 4 <= n); ++s) {
-    double us = s > 1 ? s * part + 4.0 : 0.0;
-    if (a.n_seqs == 1) us += ceil(units * s / sms) * (n / s * tile + 3.0);
-    else us += n / s * tile + 3.0 + units * (0.4 * n * tile + 3.0 * s) / sms;
-    if (us < least) {
-      least = us;
-      best = s;
-    }
-  }
-  return best;
+  const long long units = (by_tokens < by_longest ? by_tokens : by_longest) * a.Hkv;
+  const long long tiles = a.max_kv_len / BN + 1;
+  const long long n = units * (tiles + kUnitWeight) / kLeastRange;  // (below 2^31 units of less than 2^25 tiles)
+  return static_cast<int>(n < 1 ? 1 : (n < sms ? n : sms));
+}
+
+// Phases of a chunk's key heads. The CTAs are spread over all units of a phase, so its keys and values are what L2 (129 MB)
+// should hold: 2,048 tokens over 34,048 positions with 8 key heads at d = 128, 139 MB, take 768 us in one phase, 733 in two
+// and 712 in three; 4 heads (70 MB) 715 in one and 722 in two. Each phase leaves up to two parts per CTA, so a CTA's share
+// of it is to be 24 key tiles at least.
+int chunk_phases(const PagedArgs& a) {
+  const int tpt = 128 / (a.Hq / a.Hkv);
+  const double tiles = (a.max_kv_len / BN + 1.0) * a.Hkv * (static_cast<double>(a.T) / (2 * tpt));
+  const double bytes = static_cast<double>(a.n_seqs) * a.max_kv_len * a.Hkv * a.d * (a.cache_dtype == CQSA_E4M3 ? 2 : 4);
+  const double most = tiles / (24.0 * chunk_ctas(a)), want = bytes < 96.0 * 1048576.0 ? 1.0 : ceil(bytes / (64.0 * 1048576.0));
+  const int n = static_cast<int>(fmin(fmin(want, most), fmin(a.Hkv, 4.0)));
+  return n < 1 ? 1 : n;
 }
 
 void fill_common(SeqParams* p, int n_seqs, int T, int Hq, int Hkv, int causal, float scale) {
@@ -1208,7 +1388,6 @@ void fill_common(SeqParams* p, int n_seqs, int T, int Hq, int Hkv, int causal, f
   p->Hkv = Hkv;
   p->G = Hq / Hkv;
   p->tpt = 128 / p->G;
-  p->n_splits = 1;
   p->causal = causal;
   p->scale_log2 = scale * 1.4426950408889634f;
   p->timeout_us = timeout_us();
@@ -1218,10 +1397,8 @@ void fill_common(SeqParams* p, int n_seqs, int T, int Hq, int Hkv, int causal, f
 }  // namespace
 
 size_t chunk_workspace(const PagedArgs& a) {
-  const size_t s = static_cast<size_t>(chunk_splits(a));
-  if (s == 1) return 0;
-  const size_t rows = static_cast<size_t>(a.T) * a.Hq;
-  return ((s * rows * a.d * 4 + 255) & ~size_t(255)) + s * rows * 4;
+  const size_t parts = 2 * static_cast<size_t>(chunk_ctas(a)) * chunk_phases(a);
+  return parts * kPartRows * (static_cast<size_t>(a.d) + 1) * 4 + parts * sizeof(int4);
 }
 
 int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
@@ -1239,11 +1416,12 @@ int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
   p.max_pages = a.max_pages;
   p.n_pages = a.n_pages;
   p.page_log2 = 31 - __builtin_clz(static_cast<unsigned>(a.page));
-  p.n_splits = chunk_splits(a);
-  const size_t rows = static_cast<size_t>(a.T) * a.Hq;
+  const int ctas = chunk_ctas(a);
+  p.phases = chunk_phases(a);
+  const size_t parts = 2 * static_cast<size_t>(ctas) * p.phases;
   p.part_o = static_cast<float*>(a.workspace);
-  p.part_l = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) +
-                                      ((static_cast<size_t>(p.n_splits) * rows * a.d * 4 + 255) & ~size_t(255)));
+  p.part_l = p.part_o + parts * kPartRows * a.d;
+  p.meta = reinterpret_cast<int4*>(p.part_l + parts * kPartRows);
   int rc = osum_slots(&p.osum, &p.n_osum);
   CUtensorMap mq, mk, mv;
   if (rc == CQSA_OK) rc = make_token_map(&mq, a.q, a.dtype, a.d, a.Hq, a.T, a.q_stride, p.G, p.tpt);
@@ -1251,9 +1429,8 @@ int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
   if (rc == CQSA_OK) rc = make_page_map(&mk, a.k_cache, a, box);
   if (rc == CQSA_OK) rc = make_page_map(&mv, a.v_cache, a, box);
   if (rc != CQSA_OK) return rc;
-  const long long grid = pairs_bound(a.T, a.n_seqs, p.tpt) * a.Hkv * p.n_splits;
-  return a.cache_dtype == CQSA_E4M3 ? dispatch<kSrcE4m3>(mq, mk, mv, p, a.d, a.dtype, grid, stream)
-                                    : dispatch<kSrcPages>(mq, mk, mv, p, a.d, a.dtype, grid, stream);
+  return a.cache_dtype == CQSA_E4M3 ? dispatch<kSrcE4m3>(mq, mk, mv, p, a.d, a.dtype, ctas, stream)
+                                    : dispatch<kSrcPages>(mq, mk, mv, p, a.d, a.dtype, ctas, stream);
 }
 
 int launch_packed(const PackedArgs& a, cudaStream_t stream) {
