@@ -411,7 +411,9 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
   }
   if constexpr (PACKED) {
     if (warp == 2) {
-      // key tiles by how many follow them in their sequence: under the causal mask, heaviest first
+      // key tiles by how many follow them in their sequence: under the causal mask, heaviest first, of all heads (in groups of
+      // heads whose rows L2 holds, as the other calls take them, the last group's heaviest tiles start late: 1,442 us against
+      // 1,328 for eight ragged prompts of 16,384 tokens together, 206 against 151 for one of 2,000)
       auto tiles = [&](int i) {
         int first;
         return (seq_tokens(p.cu, i, p.T, &first) + BT - 1) / BT;

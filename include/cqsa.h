@@ -17,9 +17,10 @@
  *   out = 0 and lse = -inf.
  *
  * Shapes and types: Q/K/V are fp16 or bf16, head dimension d in {64, 128} (the pages' kernels
- * cover "fp16/bf16 and head dims 64/128": "stream-cqsa 2.2.2 -> 2.2.3" diff, README). Masks,
- * dropout and grouped-query attention are not part of this ABI, as the pages' call rejects them
- * ("stream-cqsa 2.2.0 -> 2.2.2" diff, api.py `attention` docstring). scale == 0 means 1/sqrt(d),
+ * cover "fp16/bf16 and head dims 64/128": "stream-cqsa 2.2.2 -> 2.2.3" diff, README). Masks and
+ * dropout are not part of this ABI, and the calls on [B, H, N, d] tensors take one head count, as the pages' call
+ * rejects the rest ("stream-cqsa 2.2.0 -> 2.2.2" diff, api.py `attention` docstring); grouped heads and sequences of
+ * different lengths have calls of their own below (cqsa_attn_packed_fwd and after). scale == 0 means 1/sqrt(d),
  * the SDPA default (`scale: Optional[float] = None` in the same signature).
  *
  * Layouts: CQSA_LAYOUT_BHND is SDPA's [B, H, N, d] (contiguous). CQSA_LAYOUT_BNHD is the
@@ -362,6 +363,9 @@ int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, vo
  * kv_lens[s] - n + i. Slots past a sequence's length may hold anything. Pages may be shared between
  * sequences as long as no two tokens of one write go to the same slot.
  *
+ * A non-finite v at a position that the causal mask hides from a row, in the row's own sequence, may reach the row (as
+ * 0 * infinity does in the formula); another sequence's never does, nor what an unused slot of a page holds.
+ *
  * Every call is asynchronous on `stream` and allocates nothing. Two calls whose work may overlap on the GPU
  * need a workspace each (a captured graph keeps the one it was captured with).
  * ------------------------------------------------------------------------------------------------ */
@@ -402,9 +406,10 @@ int cqsa_kv_cache_read(void* k, void* v, const void* k_cache, const void* v_cach
 /* Attention of each sequence's new tokens (one, a few, or a chunk; already written to the cache) over its
  * positions: q device [T, Hq, d], out device [T, Hq, d] of dtype, contiguous. causal: token i sees positions up to its own;
  * otherwise all kv_lens[s]. A row that sees nothing gives out = 0, lse = -inf. max_q_len: at least the most new tokens of a
- * sequence (rows beyond it may be left as they were); max_kv_len: about the longest kv_lens (it sets how the work is
- * split, not the result). At most 32 rows per sequence and key head (max_q_len * Hq / Hkv) run as one
- * split over the keys; more run on the tensor cores in tiles of 128. P is rounded to dtype (fp16 for an e4m3
+ * sequence (rows beyond it may be left as they were; 0: every row is); max_kv_len: about the longest kv_lens (it sets how
+ * the work is split, which moves results by rounding only). At most 32 rows per sequence and key head (max_q_len * Hq / Hkv)
+ * run as one split over the keys; more run on tcgen05 in tiles of 128. Bitwise reproducible for the same arguments and
+ * lengths. P is rounded to dtype (fp16 for an e4m3
  * cache) for its product with V; sums are fp32. workspace: device memory, 16-byte aligned, of at least
  * cqsa_attn_paged_workspace_size bytes for the same arguments (0: none is needed); its contents on entry do not
  * matter. */
@@ -437,7 +442,8 @@ void cqsa_set_timeout_ms(unsigned int ms);
 
 /*
  * Test hook for the device-side bounded waits (not for production use): kind 1 makes the next
- * attention launches skip the load of key/value tile 1 in their first CTA, and kind 2 makes the next
+ * attention launches (packed and paged ones too) skip the load of key/value tile 1 in their first CTA (calls of at most
+ * 32 rows over pages: tile 0 of sequence 0 and head 0), and kind 2 makes the next
  * backward launches skip the key/value load of their first CTA, so that CTA's waits run out after the
  * timeout; the kernel then records CQSA_ERR_TIMEOUT in its device error word, drains its own copies
  * and MMAs, frees tensor memory and returns (no trap, no hang). kind 0 turns it off.

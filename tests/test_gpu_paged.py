@@ -122,6 +122,43 @@ def test_equal_pages_and_table_order(cq, hq, new, cache):
         assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+def test_chunk_ranges(cq, cache, d):
+    """Chunks whose work is cut into ranges over units of very different lengths, in one phase of key heads or several (which
+    the caller's longest length sets), and by one CTA where the caller says that there is hardly anything."""
+    new, lengths, hq, hkv, page = [300, 0, 45, 700, 33], [300, 9, 4000, 1500, 20], 8, 4, 32
+    dtype = torch.float16
+    ks, vs, kc, vc, table = sq.make_cache(lengths, hkv, d, page, torch.float32 if cache == "e4m3" else dtype, 5,
+                                          fill=0.0 if cache == "e4m3" else float("nan"), sharp=1.5)
+    scales = {}
+    if cache == "e4m3":
+        (kc, kse, kval), (vc, vse, vval) = sq.quantise(kc), sq.quantise(vc)
+        scales = {"k_scale": kse, "v_scale": vse}
+        for s, n in enumerate(lengths):
+            t = torch.arange(n, device="cuda")
+            pg = table[s].long()[t // page]
+            ks[s], vs[s] = kval[pg, :, t % page], vval[pg, :, t % page]
+    q = sq.normal((sum(new), hq, d), dtype, 3)
+    cu, kl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (sq.starts(new), lengths))
+    for causal in (True, False):
+        for most in (1, 4000, 2_000_000):
+            got = [cq.attention_paged(q, kc, vc, table, cu, kl, max(new), most, causal=causal, return_lse=True, **scales) for _ in range(2)]
+            torch.cuda.synchronize()
+            rc, code, _ = cq.cqsa_device_error()
+            assert rc == cq.CQSA_OK and code == 0
+            assert all(torch.equal(x, y) for x, y in zip(*got))
+            out, lse = got[0]
+            at = 0
+            for s, n in enumerate(new):
+                if n:
+                    ref, rl, mass = sq.attend(q[at:at + n], ks[s], vs[s], lengths[s] - n, causal)
+                    what = f"causal={causal} most={most} sequence {s}"
+                    sq.check_out(out[at:at + n], ref, mass, dtype, dtype, what, lengths[s] * 2.0 ** (-25 if cache == "e4m3" else -34))
+                    sq.check_lse(lse[:, at:at + n], rl, what)
+                at += n
+
+
 def test_graph_streams_and_workspaces(cq):
     """Captured with its own workspace and replayed on another stream beside an eager call, for lengths that change between replays."""
     d, page, dtype = 128, 16, torch.bfloat16
