@@ -33,8 +33,8 @@
 // share the key head, so dK_j and dV_j sum over the group in tensor memory, in a fixed order and without atomics.
 // Rows past a sequence's end (other sequences' tokens) are zeroed in shared memory after their loads: P = dS = 0
 // there would not hide a NaN. packed_prep_kernel and packed_out_kernel take the places of the first and last.
-// Eight ragged prompts of 16,384 tokens together, 32 query and 8 key heads, d = 128, bf16, causal: 1,320 us, of which the
-// main kernel takes 1,170 (0.81 PFLOP/s) and the two others, which move 0.94 GB, 153. What bounds a step is the chain that d = 128
+// Eight ragged prompts of 16,384 tokens together, 32 query and 8 key heads, d = 128, bf16, causal: 1,285 us, of which the
+// main kernel takes 1,140 (0.83 PFLOP/s) and the two others, which move 0.94 GB, 145. What bounds a step is the chain that d = 128
 // has in the other forms too: one slot each of Q and dO, and dQ staged over dP^T (6,300 cycles, 2,560 of them products).
 // P and dS enter the MMAs rounded to the input dtype; everything else is fp32. Head dimension 64 or 128
 // (d = 128 holds one Q/dO tile instead of two, and shares tensor and shared memory between phases: see
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     if (warp == 2) {
       // key tiles by how many follow them in their sequence: under the causal mask, heaviest first, of all heads (in groups of
       // heads whose rows L2 holds, as the other calls take them, the last group's heaviest tiles start late: 1,442 us against
-      // 1,328 for eight ragged prompts of 16,384 tokens together, 206 against 151 for one of 2,000)
+      // 1,328 then for eight ragged prompts of 16,384 tokens together, 206 against 151 for one of 2,000)
       auto tiles = [&](int i) {
         int first;
         return (seq_tokens(p.cu, i, p.T, &first) + BT - 1) / BT;
@@ -560,6 +560,13 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       } else {
         ok = ok && load_one(0, 0) && load_one(0, 1);
         for (int it = 0; ok && it + 1 < nit; ++it) {
+          if (lane == 0) {  // the one slot is in use for most of a step: the next rows wait for it in L2 (1,325 -> 1,296 us below)
+            for (int x = 0; x < HD / 64; ++x) {
+              tma_prefetch_3d(&tmG, x * 64, h * p.G, seq_first + (it0 + it + 1) * p.tpt);
+              tma_prefetch_3d(&tmQ, x * 64, h * p.G, seq_first + (it0 + it + 1) * p.tpt);
+            }
+          }
+          __syncwarp();
           ok = freed(1, static_cast<uint32_t>(it & 1)) && load_one(it + 1, 1) && freed(0, static_cast<uint32_t>(it & 1)) &&
                load_one(it + 1, 0);
         }
@@ -1293,9 +1300,9 @@ __global__ void __launch_bounds__(256) packed_out_kernel(const PackedOut o, cons
   const long long first = cu_at(cu, 0, T) * row4, last = cu_at(cu, n_seqs, T) * row4, step = T * row4;
   for (long long i = first + static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < last;
        i += static_cast<long long>(gridDim.x) * 256) {
-    float4 v = src[i];
+    float4 v = __ldcs(src + i);
     for (int k = 1; k < parts; ++k) {
-      const float4 w = src[i + k * step];
+      const float4 w = __ldcs(src + i + k * step);
       v.x += w.x;
       v.y += w.y;
       v.z += w.z;
