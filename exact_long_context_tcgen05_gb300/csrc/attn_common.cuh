@@ -16,16 +16,17 @@ __device__ __forceinline__ void record_dev_error(DevErr* err, int code, int wher
   }
 }
 
-// Wait for a barrier phase, for at most tmo_us, giving up at once when another role of the CTA has (a
-// 32-bit flag in shared memory). The thread sleeps in try_wait between looks at the flag and the clock.
+// A whole warp waits for a barrier phase, for at most tmo_us, giving up at once when another role of the CTA has (a
+// 32-bit flag in shared memory). The lanes sleep in try_wait between looks at the flag and the clock, and leave the
+// loop together: what follows (tcgen05.ld and .st, ldmatrix, mma.sync) has to be executed by a converged warp.
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, uint32_t tmo_us, uint32_t abort_addr,
                                               DevErr* err, int code, int where) {
-  if (mbar_try_wait_a(bar, parity)) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait_a(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    if (mbar_try_wait_sleep_a(bar, parity, 1000000u)) return true;
-    if (ld_shared_volatile_u32(abort_addr)) return false;
-    if (globaltimer_ns() - t0 > static_cast<uint64_t>(tmo_us) * 1000ull) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_sleep_a(bar, parity, 1000000u))) return true;
+    if (__any_sync(0xffffffffu, ld_shared_volatile_u32(abort_addr) != 0)) return false;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > static_cast<uint64_t>(tmo_us) * 1000ull)) {
       record_dev_error(err, code, where);
       st_shared_volatile_u32(abort_addr, 1u);
       return false;

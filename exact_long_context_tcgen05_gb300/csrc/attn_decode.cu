@@ -282,7 +282,6 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
         if (it >= NST)
           ok = wait_or_abort(smem_u32(&empty[stage]), ((it / NST) - 1) & 1u, p.timeout_us, a_abort, &g_decode_err,
                              kDevTimeoutKV, 40);
-        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (p.fault == 1 && wk.s == 0 && h == 0 && t == 0) {  // (every wait on the tile runs out)
           ok = false;
@@ -404,7 +403,6 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
         const int stage = it % NST;
         if (ok) ok = wait_or_abort(smem_u32(&full[stage]), (it / NST) & 1u, p.timeout_us, a_abort, &g_decode_err,
                                    kDevTimeoutKV, 41);
-        ok = __all_sync(0xffffffffu, ok);
         uint8_t* st = sm + stage * C::STAGE;
         const uint32_t sk = smem_u32(st), sv = sk + C::TILE;
         const int kw0 = kg * KW;                 // first key of this warp in the tile

@@ -317,37 +317,32 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
   // A CTA works through units u = blockIdx.x, and then one of every gridDim.x, in an order that turns round every time (the
   // heaviest of one round with the lightest of the next). Warp 3 finds them, two ahead; every other warp takes them from
   // shared memory, so a unit's loads and first products run beside the end of the one before. Barrier phases count
-  // on across units: kb key tiles of the CTA, tb of a row tile.
+  // on across units: kb key tiles so far, uq units with any.
   struct View {
     Work w;
-    int tb, jb, nkv0, nkv1, n_max, kbase, kleft, q_off;
+    int tb, n, kbase, kleft, q_off;  // n: key tiles
   };
-  // The unit's two row tiles of tpt tokens each, and its key tiles [jb, jb + n_max) of the sequence.
+  // The unit's two row tiles of tpt tokens each, and its key tiles of the sequence. Both row tiles take all of them, also those
+  // that the causal mask hides from the first, and an empty second one too: they stay in step, a tile ahead of each other at
+  // most. (With the hidden tiles left out, 3% of a ragged batch's, a second row tile that followed on an empty one ran up to a
+  // unit ahead, and its first scores were now and then wrong.)
   auto view_of = [&](const Work& w) -> View {
     View v;
     v.w = w;
     v.tb = w.ta + p.tpt;
     v.q_off = w.kvlen - w.qlen;  // position of the sequence's first new token (negative: rows that see nothing)
-    auto tile_kv = [&](int t0) -> int {  // key tiles that the row tile may see
-      const int n = min(p.tpt, w.qlen - t0);
-      if (n <= 0 || w.kvlen == 0) return 0;
-      const int last = p.causal ? min(w.kvlen - 1, v.q_off + t0 + n - 1) : w.kvlen - 1;
-      return last < 0 ? 0 : last / BN + 1;
-    };
-    const int all0 = tile_kv(w.ta), all1 = tile_kv(v.tb), all = max(all0, all1);
-    v.jb = w.jb;
-    const int je = min(w.je, all);
-    v.nkv0 = min(max(all0 - v.jb, 0), je - v.jb);
-    v.nkv1 = min(max(all1 - v.jb, 0), je - v.jb);
-    v.n_max = max(v.nkv0, v.nkv1);
-    v.kbase = v.jb * BN;             // position of the range's first key
+    // the last position that either row tile sees
+    const int t1 = min(w.ta + 2 * p.tpt, w.qlen);
+    const int last = p.causal ? min(w.kvlen, v.q_off + t1) - 1 : w.kvlen - 1;
+    v.n = max(0, min(w.je, last < 0 ? 0 : last / BN + 1) - w.jb);
+    v.kbase = w.jb * BN;             // position of the range's first key
     v.kleft = w.kvlen - v.kbase;     // positions of the sequence from there
     return v;
   };
   // The i-th unit of this CTA; false when there is none, or a role has given up.
   auto take = [&](int i, View* v) -> bool {
     const bool ok = wait_or_abort(smem_u32(&bar_unit[i & 1]), (i >> 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 40);
-    if (!__all_sync(0xffffffffu, ok)) return false;
+    if (!ok) return false;
     const int4* at = reinterpret_cast<const int4*>(&sWork[i & 1]);
     const int4 a = at[0], b = at[1], c = at[2];
     __syncwarp();
@@ -366,7 +361,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       auto give = [&](int i, const Work& w) -> bool {
         if (i >= 2) {
           const bool ok = wait_or_abort(smem_u32(&bar_unit_free[i & 1]), ((i >> 1) - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 41);
-          if (!__all_sync(0xffffffffu, ok)) return false;
+          if (!ok) return false;
         }
         if (lane == 0) {
           int4* at = reinterpret_cast<int4*>(&sWork[i & 1]);
@@ -427,6 +422,9 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           *upto = x;
           return mine;
         };
+        // (also what the joining kernel finds where a range is empty, or a wait gave up before it)
+        for (int ph = lane; ph < p.phases; ph += 32) p.meta[2 * (ph * gridDim.x + blockIdx.x)] = make_int4(-1, 0, 0, 0);
+        __syncwarp();
         long long all = 0, upto, mine;
         for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
           mine = weigh(s0, &upto);
@@ -442,10 +440,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           const long long nc = min(static_cast<long long>(gridDim.x), max(W / kLeastRange, 1LL)), bx = blockIdx.x;
           const long long w0 = W * min(bx, nc) / nc, w1 = W * min(bx + 1, nc) / nc;
           const int range = ph * gridDim.x + blockIdx.x;
-          if (w0 >= w1) {
-            if (lane == 0) p.meta[2 * range] = make_int4(-1, 0, 0, 0);
-            continue;
-          }
+          if (w0 >= w1) continue;
           ChunkUnits c;
           int place = 0, hk = 0;
           long long u0 = 0;  // where the unit begins
@@ -513,11 +508,10 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       int raw_last[2] = {0, 0};
       bool ok = true;
       for (int unit = 0; ok && take(unit, &v); ++unit) {
-        if (v.n_max == 0) continue;
-        const int tok_first = v.w.tok_first, hk = v.w.hk, kbase = v.kbase, kleft = v.kleft, n_max = v.n_max, seq = v.w.seq;
+        if (v.n == 0) continue;
+        const int tok_first = v.w.tok_first, hk = v.w.hk, kbase = v.kbase, kleft = v.kleft, n_max = v.n, seq = v.w.seq;
         if (uq > 0) {
           ok = wait_or_abort(smem_u32(bar_q_free), (uq - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 42);
-          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
         ++uq;
@@ -548,7 +542,6 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             }
             const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
             ok = wait_or_abort(smem_u32(ALIAS ? &bar_k_empty[stage] : &bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 10);
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (p.fault == 1 && blockIdx.x == 0 && j == 1) {  // (every wait on the tile runs out)
               ok = false;
@@ -569,7 +562,6 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             }
             if (ALIAS) {
               ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), (round & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 34);
-              ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
             }
             const bool tail = left < BN;
@@ -591,7 +583,6 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             if (tail) {  // at most the last key tile of the sequence
               ok = wait_or_abort(smem_u32(bar_fix), fixes & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 31);
               ++fixes;
-              ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               zero_rows<C>(sV + stage * C::KV_BYTES, left, lane);
               fence_async_smem();
@@ -618,7 +609,6 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               ok = ok && wait_or_abort(smem_u32(&bar_raw_free[x]), ((kb + j) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 36 + x);
-              ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], static_cast<uint32_t>(nb) * rows * D);
               __syncwarp();
@@ -658,15 +648,14 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       const uint32_t col_p = tmem + (t ? C::COL_P1 : C::COL_P0);
       const uint32_t col_o = tmem + (t ? C::COL_O1 : C::COL_O0);
       auto wait_all = [&](uint64_t* bar, uint32_t parity, int code, int where) -> bool {
-        const bool w = wait_or_abort(smem_u32(bar), parity, tmo_us, a_abort, &g_seq_err, code, where);
-        return __all_sync(0xffffffffu, w);
+        return wait_or_abort(smem_u32(bar), parity, tmo_us, a_abort, &g_seq_err, code, where);
       };
       View v;
-      int kb = 0, tb = 0, uq = 0;  // key tiles of the CTA, of this row tile, units with any
+      int kb = 0, uq = 0;  // key tiles, units with any
       bool ok = true;
       for (int unit = 0; ok && take(unit, &v); ++unit) {
-        const int nkv = t ? v.nkv1 : v.nkv0, n_max = v.n_max;
-        if (n_max == 0) continue;
+        const int n = v.n;
+        if (n == 0) continue;
         auto do_s = [&](int j, bool pass) {
           const int stage = (kb + j) % STAGES;
           const uint64_t b0 = dK + static_cast<uint32_t>(stage) * (C::KV_BYTES >> 4);
@@ -677,7 +666,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             issue_s<D / 32, D / 16, C::HALF>(col_s, dQ, b0, IDESC_S);
             tc_commit(&bar_s_full[t]);
             if (ALIAS) tc_commit(&bar_k_empty[stage]);
-            if (j == nkv - 1) tc_commit(bar_q_free);
+            if (j == n - 1) tc_commit(bar_q_free);
           }
           __syncwarp();
         };
@@ -699,7 +688,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             }
             if (part != 0) {
               tc_commit(&bar_pv_done[t]);
-              if (j == nkv - 1) tc_commit(&bar_o_final[t]);
+              if (j == n - 1) tc_commit(&bar_o_final[t]);
               tc_commit(&bar_v_empty[stage]);
             }
           }
@@ -707,55 +696,38 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         };
         ok = wait_all(CONVQ ? bar_q2 : bar_q, uq & 1u, kDevTimeoutQ, 11);
         ++uq;
-        if (ok && nkv > 0) {
-          ok = wait_all(&bar_k_full[kb % STAGES], (kb / STAGES) & 1u, kDevTimeoutKV, 12);
-          // (P apart: the softmax has read the last S of the unit before; P over S: P V before it in this thread's order)
-          if (!ALIAS && ok && tb > 0) ok = wait_all(&bar_s_free[t], (tb - 1) & 1u, kDevTimeoutSoftmax, 43);
-          if (ok) do_s(0, false);
-        } else if (ok && leader) {
-          mbar_arrive(bar_q_free);
-        }
-        for (int j = 0; ok && j < n_max; ++j) {
+        if (ok) ok = wait_all(&bar_k_full[kb % STAGES], (kb / STAGES) & 1u, kDevTimeoutKV, 12);
+        // (P apart: the softmax has read the last S of the unit before; P over S: P V before it in this thread's order)
+        if (!ALIAS && ok && kb > 0) ok = wait_all(&bar_s_free[t], (kb - 1) & 1u, kDevTimeoutSoftmax, 43);
+        if (ok) do_s(0, false);
+        for (int j = 0; ok && j < n; ++j) {
           const int stage = (kb + j) % STAGES, n1 = (kb + j + 1) % STAGES;
           const uint32_t par0 = ((kb + j) / STAGES) & 1u, par1 = ((kb + j + 1) / STAGES) & 1u;
-          const uint32_t tp = (tb + j) & 1u, turn = ((kb + j) & 1u) ^ (t ? 0u : 1u);
-          if (j < nkv) {
-            if (!ALIAS) {
-              if (j + 1 < nkv) {
-                ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
-                if (ok) ok = wait_all(&bar_s_free[t], tp, kDevTimeoutSoftmax, 14);
-                if (ok) do_s(j + 1, false);
-              }
-              if (ok) ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 15);
-              if (ok) ok = wait_all(&bar_p_full[t], tp, kDevTimeoutSoftmax, 16);
-              if (ok) do_pv(j, 2);
-            } else {
-              ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 15);
-              if (ok && j + 1 < nkv) ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
-              if (ok) ok = wait_all(&bar_p_half[t], tp, kDevTimeoutSoftmax, 17);
-              if (ok) ok = wait_all(&bar_turn[t], turn, kDevTimeoutMMA, 24);
-              if (ok) do_pv(j, 0);
-              if (ok) ok = wait_all(&bar_p_full[t], tp, kDevTimeoutSoftmax, 16);
-              if (ok) do_pv(j, 1);
-              // P_t(j) lies over S_t: MMAs of one issuing thread run in order, so S_t(j+1) follows P V's reads
-              if (ok && j + 1 < nkv) do_s(j + 1, true);
-              else if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
+          const uint32_t tp = (kb + j) & 1u, turn = tp ^ (t ? 0u : 1u);
+          if (!ALIAS) {
+            if (j + 1 < n) {
+              ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
+              if (ok) ok = wait_all(&bar_s_free[t], tp, kDevTimeoutSoftmax, 14);
+              if (ok) do_s(j + 1, false);
             }
+            if (ok) ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 15);
+            if (ok) ok = wait_all(&bar_p_full[t], tp, kDevTimeoutSoftmax, 16);
+            if (ok) do_pv(j, 2);
           } else {
-            // a key tile that only the other row tile sees: wait for its loads, so that the releases belong to their phases
-            ok = wait_all(&bar_k_full[stage], par0, kDevTimeoutKV, 21);
-            if (ALIAS && ok && leader) mbar_arrive(&bar_k_empty[stage]);
-            if (ok) ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 22);
-            if (ok && leader) mbar_arrive(&bar_v_empty[stage]);
-            if (ALIAS) {
-              if (ok) ok = wait_all(&bar_turn[t], turn, kDevTimeoutMMA, 25);
-              if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
-            }
+            ok = wait_all(&bar_v_full[stage], par0, kDevTimeoutKV, 15);
+            if (ok && j + 1 < n) ok = wait_all(&bar_k_full[n1], par1, kDevTimeoutKV, 13);
+            if (ok) ok = wait_all(&bar_p_half[t], tp, kDevTimeoutSoftmax, 17);
+            if (ok) ok = wait_all(&bar_turn[t], turn, kDevTimeoutMMA, 24);
+            if (ok) do_pv(j, 0);
+            if (ok) ok = wait_all(&bar_p_full[t], tp, kDevTimeoutSoftmax, 16);
+            if (ok) do_pv(j, 1);
+            // P_t(j) lies over S_t: MMAs of one issuing thread run in order, so S_t(j+1) follows P V's reads
+            if (ok && j + 1 < n) do_s(j + 1, true);
+            else if (ok && leader) mbar_arrive(&bar_turn[t ^ 1]);
           }
           __syncwarp();
         }
-        kb += n_max;
-        tb += nkv;
+        kb += n;
       }
       if (leader) tc_commit(&bar_mma_idle[warp - 1]);
       __syncwarp();
@@ -783,10 +755,10 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     const int rt = r / p.G;                     // token of this thread's row within the tile
     const int SEG = osum_ok ? C::FLUSH : (1 << 30);
     View v;
-    int kb = 0, tb = 0, uq = 0, uo = 0;  // key tiles of the CTA and of this row tile, units with any for either
+    int kb = 0, uq = 0;  // key tiles, units with any
     bool ok = true;
     for (int unit = 0; ok && take(unit, &v); ++unit) {
-      const int nkv = wg ? v.nkv1 : v.nkv0, n_max = v.n_max, kleft = v.kleft;
+      const int n = v.n, kleft = v.kleft;
       const int t0 = wg ? v.tb : v.w.ta;
       const int rel = v.q_off + t0 - v.kbase;     // key position (in the range) of the tile's first token
       const int row_lim = p.causal ? rel + rt + 1 : 0x7fffffff;
@@ -794,11 +766,11 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       float sl2 = p.scale_log2;
       float m_ref = -INFINITY, l = 0.0f, m_sum = -INFINITY;
       int ev = -100000, ev_sum = 0;  // e4m3: exponent of the values that O (the running sum) is relative to
-      for (int j0 = 0; ok && j0 < nkv; j0 += SEG) {
+      for (int j0 = 0; ok && j0 < n; j0 += SEG) {
         if (j0 > 0) {
           // fold O into the running sum, brought from its reference to the current one by an exact power of two
-          ok = wait_or_abort(a_pv_done, (tb + j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
-          if (!__all_sync(0xffffffffu, ok)) {
+          ok = wait_or_abort(a_pv_done, (kb + j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
+          if (!ok) {
             ok = false;
             break;
           }
@@ -839,10 +811,10 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           m_sum = m_ref;
           ev_sum = ev;
         }
-        const int j1 = (nkv - j0 < SEG) ? nkv : j0 + SEG;
+        const int j1 = (n - j0 < SEG) ? n : j0 + SEG;
         for (int j = j0; j < j1; ++j) {
-          ok = wait_or_abort(a_s_full, (tb + j) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
-          if (!__all_sync(0xffffffffu, ok)) {
+          ok = wait_or_abort(a_s_full, (kb + j) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
+          if (!ok) {
             ok = false;
             break;
           }
@@ -922,8 +894,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
               pk[c] = pack2(pp.x, pp.y, MB);
             }
             if (j > 0) {
-              ok = wait_or_abort(a_pv_done, (tb + j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
-              if (!__all_sync(0xffffffffu, ok)) {
+              ok = wait_or_abort(a_pv_done, (kb + j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
+              if (!ok) {
                 ok = false;
                 break;
               }
@@ -970,13 +942,12 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       }
 
       // ---------------------------------------------------------------- epilogue
-      if (ok && nkv > 0) {
-        ok = wait_or_abort(smem_u32(&bar_o_final[wg]), uo & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 20);
-        ok = __all_sync(0xffffffffu, ok);
+      if (ok && n > 0) {
+        ok = wait_or_abort(smem_u32(&bar_o_final[wg]), uq & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 20);
         tc_fence_after();
       }
       // a row with a NaN score has l = NaN and passes it on; an empty one is 0 / -inf
-      const bool has = (nkv > 0) && !(l <= 0.0f);
+      const bool has = (n > 0) && !(l <= 0.0f);
       float inv_l = has ? 1.0f / l : 0.0f;
       const float lse2 = has ? m_ref - kPShift + log2f(l) : -INFINITY;
       if (CONV) inv_l *= has ? exp2_int_any(min(max(ev, -126), 127)) : 1.0f;
@@ -984,8 +955,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       const bool write = ok && rt < p.tpt && tok < v.w.qlen;
       const int hq = v.w.hk * p.G + (r - rt * p.G);
       const long long row = static_cast<long long>(v.w.tok_first + tok) * p.Hq + hq;
-      // (Without key tiles nothing says that the tile's other warps have left the unit before, whose running sum may lie here.)
-      const bool staged = C::STAGED && nkv > 0 && !(C::OSUM_SMEM && osum_ok && nkv > C::FLUSH);
+      // (without key tiles nothing says that the tile's other warps have left the unit before, whose running sum may lie here)
+      const bool staged = C::STAGED && n > 0 && !(C::OSUM_SMEM && osum_ok && n > C::FLUSH);
       const uint32_t buf = smem_u32(sOut) + (C::OSUM_SMEM ? wg * (D * 128 * 4) + quarter * 4096 : (warp - 4) * 4096);
       const bool part = SRC != kSrcPacked && v.w.slot >= 0;
       // (T * Hq < 2^31)
@@ -993,7 +964,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        if (ok && nkv > 0) {
+        if (ok && n > 0) {
           tmem_ld32(trow + colO + c * 32, o);
           tmem_wait_ld();
           reg_fence32(o);
@@ -1002,7 +973,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
         float y[32];
-        if (osum_ok && nkv > C::FLUSH) {
+        if (osum_ok && n > C::FLUSH) {
           const float* os = sOsum + (wg * D + c * 32) * 128 + r;
           float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
           if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
@@ -1074,10 +1045,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         else if (p.lse) p.lse[static_cast<long long>(hq) * p.T + v.w.tok_first + tok] = lse2 * 0.69314718055994531f;
       }
       tc_fence_before();  // O has been read: the next unit's P hand-offs release its columns
-      kb += n_max;
-      tb += nkv;
-      uq += n_max > 0;
-      uo += nkv > 0;
+      kb += n;
+      uq += n > 0;
     }
     tc_fence_before();
     asm volatile("bar.sync 0;" ::: "memory");
@@ -1090,12 +1059,11 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
       int kb = 0, uq = 0;
       bool ok = true;
       for (int unit = 0; ok && take(unit, &v); ++unit) {
-        const int n_max = v.n_max, kbase = v.kbase, kleft = v.kleft, hk = v.w.hk;
+        const int n_max = v.n, kbase = v.kbase, kleft = v.kleft, hk = v.w.hk;
         if (n_max == 0) continue;
         if (CONVQ) {
           // queries in place: this thread's row of each tile, brought to fp16 relative to its largest power of two
           ok = wait_or_abort(smem_u32(bar_q), uq & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutQ, 32);
-          ok = __all_sync(0xffffffffu, ok);
           const int r = w * 32 + lane;
           for (int t = 0; ok && t < 2; ++t) {
             uint8_t* q = sQ + t * C::QT_BYTES + r * 128;
@@ -1216,7 +1184,6 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           }
           if (ok) ok = wait_or_abort(smem_u32(&bar_raw[0]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 38);
           if (ok) ok = wait_or_abort(smem_u32(&bar_k_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 33);
-          ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
             if (w == 0 && lane == 0) *reinterpret_cast<int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2) = make_int2(kref, vref);
@@ -1230,7 +1197,6 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             send_top(j + 1, eb);
             ok = wait_or_abort(smem_u32(&bar_raw[1]), raw_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 39);
             if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
-            ok = __all_sync(0xffffffffu, ok);
           }
           if (ok) {
             convert(from + C::RAW, smem_u32(sV) + stage * C::KV_BYTES, in ? pow2h(ex.y - vref) : 0xffffffffu, tail);

@@ -102,6 +102,27 @@ def test_long_rows_before_short_ones(cq):
         sq.check_lse(lse[:, first:first + 100], rl, f"from {first}")
 
 
+RAGGED = [1451, 67, 668, 202, 475, 107, 266, 2568, 403, 176, 0, 209, 1099, 421, 36, 95, 3230, 121, 794, 1170, 778, 1938, 110]
+
+
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (128, "f16"), (64, "bf16")])
+def test_many_units_repeat(cq, d, dt):
+    """Some fourteen units on each SM, sequences that leave a unit's second row tile empty among them: every row against the
+    definition, and bit by bit the same again and again, also behind work that has emptied L2."""
+    dtype, hq, hkv = sq.DT[dt], 32, 8
+    q, k, v = sq.normal((sum(RAGGED), hq, d), dtype, 1), sq.normal((sum(RAGGED), hkv, d), dtype, 2, 1.5), sq.normal((sum(RAGGED), hkv, d), dtype, 3)
+    cu = torch.tensor(sq.starts(RAGGED), dtype=torch.int32, device="cuda")
+    first = cq.attention_packed(q, k, v, cu, return_lse=True)
+    _ok(cq)
+    _check(*first, q, k, v, RAGGED, True)
+    other = torch.empty(100_000_000, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            other.fill_(i)
+        again = cq.attention_packed(q, k, v, cu, return_lse=True)
+        assert all(torch.equal(x, y) for x, y in zip(again, first)), f"pass {i}"
+
+
 def test_strides_scale_streams_and_graph(cq):
     """Slices of a fused projection, another scale and stream, capture and replay with other lengths."""
     d, dtype, lens = 128, torch.bfloat16, [70, 200]
@@ -264,6 +285,27 @@ def test_backward_strides_scale_stream_and_graph(cq):
         graph.replay()
         _ok(cq)
         _check_grads(got, q, k, v, out, g, lens, True, what=str(lens))
+
+
+def test_backward_many_units_repeat(cq):
+    """dk and dv repeat bit by bit over a ragged batch of many key tiles, and every gradient agrees with the formula's."""
+    d, dtype, hq, hkv, lens = 128, torch.bfloat16, 8, 2, [n // 2 for n in RAGGED]
+    q, g = (sq.normal((sum(lens), hq, d), dtype, i) for i in (1, 4))
+    k, v = (sq.normal((sum(lens), hkv, d), dtype, i) for i in (2, 3))
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    out, lse = cq.attention_packed(q, k, v, cu, return_lse=True)
+    first = cq.attention_packed_backward(q, k, v, out, g, lse, cu)
+    _ok(cq)
+    at = sq.starts(lens)
+    for s, n in enumerate(lens):
+        if n:
+            i = slice(at[s], at[s + 1])
+            ref, mass = sq.gradients(q[i], k[i], v[i], out[i], g[i], True)
+            for x, r, m in zip(first, ref, mass):
+                sq.check_grad(x[i], r, m, dtype, f"sequence {s}")
+    for _ in range(30):
+        again = cq.attention_packed_backward(q, k, v, out, g, lse, cu)
+        assert torch.equal(again[1], first[1]) and torch.equal(again[2], first[2])
 
 
 def test_backward_wait_that_gives_up(cq):

@@ -159,6 +159,42 @@ def test_chunk_ranges(cq, cache, d):
                 at += n
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cache", ["same", "e4m3"])
+def test_units_without_keys(cq, cache, d):
+    """Sequences without positions, and new tokens before the first position, between long ones: empty rows are 0 and -inf, the
+    others' are right, and all of it repeats bit by bit."""
+    new, lengths, hq, hkv, page = [150, 300, 40, 200] * 12, [0, 1900, 10, 700] * 12, 8, 2, 64
+    dtype = torch.float16
+    ks, vs, kc, vc, table = sq.make_cache(lengths, hkv, d, page, torch.float32 if cache == "e4m3" else dtype, 7,
+                                          fill=0.0 if cache == "e4m3" else float("nan"), sharp=1.5)
+    scales = {}
+    if cache == "e4m3":
+        (kc, kse, kval), (vc, vse, vval) = sq.quantise(kc), sq.quantise(vc)
+        scales = {"k_scale": kse, "v_scale": vse}
+        for s, n in enumerate(lengths):
+            t = torch.arange(n, device="cuda")
+            pg = table[s].long()[t // page] if n else t
+            ks[s], vs[s] = kval[pg, :, t % page], vval[pg, :, t % page]
+    q = sq.normal((sum(new), hq, d), dtype, 3)
+    cu, kl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (sq.starts(new), lengths))
+    first = cq.attention_paged(q, kc, vc, table, cu, kl, max(new), max(lengths), return_lse=True, **scales)
+    for _ in range(40):
+        again = cq.attention_paged(q, kc, vc, table, cu, kl, max(new), max(lengths), return_lse=True, **scales)
+        assert all(torch.equal(x, y) for x, y in zip(again, first))
+    rc, code, _ = cq.cqsa_device_error()
+    assert rc == cq.CQSA_OK and code == 0
+    out, lse = first
+    at = 0
+    for s, n in enumerate(new):
+        ref, rl, mass = sq.attend(q[at:at + n], ks[s], vs[s], lengths[s] - n, True)
+        sq.check_out(out[at:at + n], ref, mass, dtype, dtype, f"sequence {s}", lengths[s] * 2.0 ** (-25 if cache == "e4m3" else -34))
+        sq.check_lse(lse[:, at:at + n], rl, f"sequence {s}")
+        empty = max(0, n - lengths[s])
+        assert (out[at:at + empty] == 0).all() and (lse[:, at:at + empty] == float("-inf")).all()
+        at += n
+
+
 def test_graph_streams_and_workspaces(cq):
     """Captured with its own workspace and replayed on another stream beside an eager call, for lengths that change between replays."""
     d, page, dtype = 128, 16, torch.bfloat16
