@@ -25,10 +25,10 @@
 //            below it). K's power goes into the scores' scale; V's is a reference that O is rescaled to when it rises.
 //            Queries are fp16: bf16 ones are first scaled to [1, 2) by a power of two per row, in place.
 //
-// Measured: one causal prompt of 32,768 tokens, 8 query and 2 key heads, d = 64, fp16: 975 us, 1,128 TFLOP/s; 24 ragged prompts
+// Measured: one causal prompt of 32,768 tokens, 8 query and 2 key heads, d = 64, fp16: 980 us, 1,122 TFLOP/s; 24 ragged prompts
 // of 16,384 tokens together, 32 and 8 heads, d = 128, bf16: 208 us, 1,100 TFLOP/s; 2,048 tokens over 32,000 positions of 16-bit
-// pages, 32 and 8 heads, d = 128: 710 us, 1,560 TFLOP/s, over e4m3 ones 1,190 us; 12 ragged e4m3 sequences (3,000 tokens over
-// 60,000, 8 and 2 heads, d = 64): 83 us. Long rows are bound by the softmax warps' chain of a key tile (tensor-memory loads, row
+// pages, 32 and 8 heads, d = 128: 705 us, 1,570 TFLOP/s, over e4m3 ones 1,195 us; 12 ragged e4m3 sequences (3,000 tokens over
+// 60,000, 8 and 2 heads, d = 64): 85 us. Long rows are bound by the softmax warps' chain of a key tile (tensor-memory loads, row
 // maximum, 128 exponentials, P back) beside the products it waits for: the tensor pipe is 69% busy at d = 128 and 46% at
 // d = 64; short units add about three key tiles' time each for their start and end. e4m3: the converters take issue slots
 // from the softmax warps of their sub-partitions.
@@ -778,10 +778,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         if (j0 > 0) {
           // fold O into the running sum, brought from its reference to the current one by an exact power of two
           ok = wait_or_abort(a_pv_done, (kb + j0 - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 23);
-          if (!ok) {
-            ok = false;
-            break;
-          }
+          if (!ok) break;
           tc_fence_after();
           const bool have = j0 > C::FLUSH;
           float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
@@ -822,10 +819,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         const int j1 = (n - j0 < SEG) ? n : j0 + SEG;
         for (int j = j0; j < j1; ++j) {
           ok = wait_or_abort(a_s_full, (kb + j) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 18);
-          if (!ok) {
-            ok = false;
-            break;
-          }
+          if (!ok) break;
           if (CONVQ && j == 0) sl2 = p.scale_log2 * exp2_int_any(sRow[(uq & 1) * 256 + wg * 128 + r]);  // written before the queries were released
           tc_fence_after();
           uint32_t sr[128];
@@ -903,10 +897,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             }
             if (j > 0) {
               ok = wait_or_abort(a_pv_done, (kb + j - 1) & 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutMMA, 19);
-              if (!ok) {
-                ok = false;
-                break;
-              }
+              if (!ok) break;
               tc_fence_after();
             }
             tmem_st32(pbuf, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
@@ -972,6 +963,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
+        __syncwarp();  // (stores of the rows that count may have parted the lanes)
         if (ok && n > 0) {
           tmem_ld32(trow + colO + c * 32, o);
           tmem_wait_ld();
