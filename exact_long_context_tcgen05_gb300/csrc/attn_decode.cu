@@ -16,7 +16,8 @@
 //
 // A CTA: one producer warp copies key tiles page by page with TMA through a ring of stages (a lane per page
 // box); 4 warps (8 for 32 rows), each on a quarter of a tile's keys, take them through S = Q K^T, an online softmax in
-// registers, and O += P V, and join their rows in shared memory at the end of a unit's range.
+// registers, and O += P V, and join their rows in shared memory at the end of a unit's range. The tensor core truncates as it
+// accumulates, so a warp adds its O to an fp32 sum (in its part of the joining buffer) every FOLD tiles, as attn_fwd.cu does.
 //
 // e4m3 pages: codes become fp16 in registers (exact). A key's power of two multiplies its scores in fp32, a
 // value's goes onto its probability, relative to the largest exponent met so far (an integer that moves like
@@ -63,6 +64,9 @@ struct DecCfg {
   static constexpr int NST = NST_MAX > 6 ? 6 : NST_MAX;
   static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + 512;
   static constexpr int NTHR = 32 + 32 * kQuarters * NMT;
+  // Tiles between folds of O: a warp's chain is 4,096 keys, 256 products, as in attn_fwd.cu at d = 128. In one chain a range of
+  // 131,072 positions lost 2.2e-4 of sums of one sign, one of 2^21 positions 3.4e-3 (fp16's half step is 4.9e-4).
+  static constexpr int FOLD = 16384 / KT;
   static_assert(SMEM <= 232448, "shared memory exceeds 227 KiB");
 };
 
@@ -403,7 +407,30 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
         for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
       int ev = -1;  // e4m3: exponent byte the output sums are relative to
+      // The running sum that O is folded into: D / 2 values of this lane, then the references that they are relative to. (The
+      // layout of the join below is another, and is written after the next named_sync.)
+      float* sum = jbuf + kg * 16 * C::LDO + lane;
+      auto sum_factor = [&](int u) -> float {
+        const float was = sum[(D / 2 + u) * 32], a = was == -INFINITY ? 0.0f : ex2(was - m[u]);
+        return E4M3 ? a * exp2_int_any(__float_as_int(sum[(D / 2 + 2) * 32]) - ev) : a;
+      };
       for (int t = t0; t < t1; ++t, ++it) {
+        if (t > t0 && (t - t0) % C::FOLD == 0) {
+          const bool have = t - t0 > C::FOLD;
+          if (!have) named_sync(1 + mt, 32 * kQuarters);  // the unit before has been read out of the buffer
+          const float fs[2] = {have ? sum_factor(0) : 0.0f, have ? sum_factor(1) : 0.0f};
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float* at = sum + (j * 4 + i) * 32;
+              *at = (have ? *at * fs[i >> 1] : 0.0f) + o[j][i];
+              o[j][i] = 0.0f;
+            }
+          sum[(D / 2) * 32] = m[0];
+          sum[(D / 2 + 1) * 32] = m[1];
+          sum[(D / 2 + 2) * 32] = __int_as_float(ev);
+        }
         const int stage = it % NST;
         if (ok) ok = wait_or_abort(smem_u32(&full[stage]), (it / NST) & 1u, p.timeout_us, a_abort, &g_decode_err,
                                    kDevTimeoutKV, 41);
@@ -575,6 +602,13 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
+      }
+      if (t1 - t0 > C::FOLD) {
+        const float fs[2] = {sum_factor(0), sum_factor(1)};
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] += sum[(j * 4 + i) * 32] * fs[i >> 1];
       }
       // ---- join the warps' rows: each brings its sums to the common maximum and scale
       // (the exponent reference of e4m3 values is a power of two that is multiplied out here)
