@@ -65,6 +65,12 @@ constexpr int BT = 128;                         // keys per CTA tile, queries pe
 constexpr uint32_t BOX = BT * 64 * 2;           // one 128 x 64 box of 16-bit elements (16 KiB)
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NBAR = 18;
+// Packed sequences: steps between folds of dV_j and dK_j into fp32 running sums, in the SM's slot of attn_fwd.cu's array (a CTA of
+// either kernel leaves no room for another's on its SM). The tensor core truncates as it accumulates (attn_fwd.cu), and with
+// grouped heads a key tile's chain is G times as long as its sequence: in one chain same-sign sums over 16,384 tokens of 4 heads lost
+// 2e-4, over 32,768 of 16 heads 3e-3 (fp16's half step is 4.9e-4). 128 steps are 1,024 products, as in the forward at d = 64. (64 steps
+// take 1% longer on eight ragged prompts of 16,384 tokens together at d = 128.)
+constexpr int kFoldSteps = 128;
 
 // Shared- and tensor-memory layout per head dimension.
 // d = 64: K, V, a three-slot ring of Q and dO tiles (the tile two steps ahead loads while a step's
@@ -161,6 +167,8 @@ struct BwdParams {
   const int* cu;
   int n_seqs, T, Hq, Hkv, G, tpt;  // tpt: tokens of a step, floor(128 / G)
   int n_splits;  // ranges that a key tile's steps are cut into; more than one leave fp32 parts [n_splits][T][Hkv][d] in dk_acc, dv_acc
+  float* osum;   // running sums (osum_slots)
+  int n_osum;
 };
 
 __device__ __forceinline__ void record_bwd_error(int code, int where) {
@@ -193,6 +201,12 @@ __device__ __forceinline__ bool wait_abort_a(uint32_t bar, uint32_t parity, unsi
 __device__ __forceinline__ bool wait_abort(uint64_t* bar, uint32_t parity, unsigned long long tmo,
                                            volatile int* abort_flag, int code, int where) {
   return wait_abort_a(smem_u32(bar), parity, tmo, smem_u32(const_cast<int*>(abort_flag)), code, where);
+}
+
+__device__ __forceinline__ uint32_t sm_id() {
+  uint32_t id;
+  asm volatile("mov.u32 %0, %%smid;" : "=r"(id));
+  return id;
 }
 
 __device__ __forceinline__ bool elect_lane() {
@@ -460,6 +474,14 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         return;
       }
     }
+    // An SM beyond the slots (there are more than any such GPU has SMs): nothing is computed, and the error says so. A test of the slot
+    // at every fold instead costs registers in the loop of steps, 1,308 us against 1,285 (eight ragged prompts, 16,384 tokens, d = 128).
+    if (nit > kFoldSteps && sm_id() >= static_cast<uint32_t>(p.n_osum)) {
+      if (tid == 0) record_bwd_error(kDevSmSlot, 30);
+      __syncthreads();
+      if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
+      return;
+    }
   }
 
   if (warp < 4) {
@@ -676,7 +698,8 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         const uint32_t so = static_cast<uint32_t>(it % NSLOT) * SLOT16;
         tc_fence_after();
         if (leader) {
-          if (it == 0) issue_grads<1, HD, HD != 64>(tmem, dG0_mn + so, dQ0_mn + so, dS_k, dS_mn, dK_mn, IDESC_V, IDESC_Q);
+          if (it == 0 || (PACKED && it % kFoldSteps == 0))
+            issue_grads<1, HD, HD != 64>(tmem, dG0_mn + so, dQ0_mn + so, dS_k, dS_mn, dK_mn, IDESC_V, IDESC_Q);
           else issue_grads<0, HD, HD != 64>(tmem, dG0_mn + so, dQ0_mn + so, dS_k, dS_mn, dK_mn, IDESC_V, IDESC_Q);
           tc_commit(bar_m2);
           tc_commit(&bar_qfree[it % NSLOT]);
@@ -686,12 +709,13 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       // d = 128: the three gradient products one after another, with the release of dO (after dV) and of
       // Q (after dK) committed in between, so that the producer refills each as early as possible
       auto issue_grads_128 = [&](int it) {
+        const bool first = it == 0 || (PACKED && it % kFoldSteps == 0);
         tc_fence_after();
         if (leader) {
 #pragma unroll
           for (int ks = 0; ks < BT / 16; ++ks) {
             const uint32_t off = static_cast<uint32_t>(ks * (2048 >> 4));
-            if (it == 0 && ks == 0) mma_ts_imm<0>(tmem + C::COL_DV, tmem + C::col_pt(ks), dG0_mn + off, IDESC_V);
+            if (first && ks == 0) mma_ts_imm<0>(tmem + C::COL_DV, tmem + C::col_pt(ks), dG0_mn + off, IDESC_V);
             else mma_ts_imm<1>(tmem + C::COL_DV, tmem + C::col_pt(ks), dG0_mn + off, IDESC_V);
           }
           tc_commit(&bar_qfree[1]);
@@ -699,7 +723,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
           for (int ks = 0; ks < BT / 16; ++ks) {
             const uint32_t off = static_cast<uint32_t>(ks * (2048 >> 4));
             const uint32_t koff = static_cast<uint32_t>((ks >> 2) * (BOX >> 4) + (ks & 3) * 2);
-            if (it == 0 && ks == 0) mma_ss_imm<0>(tmem + C::COL_DK, dS_k + koff, dQ0_mn + off, IDESC_V);
+            if (first && ks == 0) mma_ss_imm<0>(tmem + C::COL_DK, dS_k + koff, dQ0_mn + off, IDESC_V);
             else mma_ss_imm<1>(tmem + C::COL_DK, dS_k + koff, dQ0_mn + off, IDESC_V);
           }
           tc_commit(&bar_qfree[0]);
@@ -934,6 +958,54 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       return true;
     };
 
+    // This thread's place in the running sums of dV_j (0) or dK_j (1): its key row, from feature fb on, 128 rows' float4 together.
+    // (Found when it is used: every kFoldSteps steps, it stays out of the loop's registers.)
+    auto sum_at = [&](int which, int fb) -> float4* {
+      return reinterpret_cast<float4*>(p.osum + static_cast<size_t>(sm_id()) * (2 * 128 * 128)) + (which * (HD / 4) + fb / 4) * 128 + r;
+    };
+    // Adds dV_j and dK_j of the segment that ends here into them, once its products are done and before the hand-off of the step that
+    // starts the next one.
+    auto fold = [&](bool have) {
+      constexpr int W = NWG == 4 ? 16 : 32;
+      // (not unrolled: the loop of steps would spill for it, 1% slower at d = 128)
+#pragma unroll 1
+      for (int c = 0; c < HD / NWG / W; ++c)
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+          const int fb = wg * (HD / NWG) + c * W;
+          uint32_t a[W];
+          if constexpr (W == 16) {
+            tmem_ld16(trow + (which ? C::COL_DK : C::COL_DV) + fb, a);
+            tmem_wait_ld();
+            reg_fence16(a);
+          } else {
+            tmem_ld32(trow + (which ? C::COL_DK : C::COL_DV) + fb, a);
+            tmem_wait_ld();
+            reg_fence32(a);
+          }
+          float4* to = sum_at(which, fb);
+#pragma unroll
+          for (int u = 0; u < W / 4; ++u) {
+            const float4 was = have ? __ldcg(to + u * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            __stcg(to + u * 128, make_float4(was.x + __uint_as_float(a[4 * u]), was.y + __uint_as_float(a[4 * u + 1]),
+                                             was.z + __uint_as_float(a[4 * u + 2]), was.w + __uint_as_float(a[4 * u + 3])));
+          }
+        }
+    };
+    // ... and brings the last segment's, n features from fb on, up to the whole sums
+    auto whole = [&](uint32_t* a, int which, int fb, int n) {
+      if (!PACKED || nit <= kFoldSteps) return;
+      const float4* from = sum_at(which, fb);
+#pragma unroll
+      for (int u = 0; u < n / 4; ++u) {
+        const float4 x = __ldcg(from + u * 128);
+        a[4 * u] = __float_as_uint(__uint_as_float(a[4 * u]) + x.x);
+        a[4 * u + 1] = __float_as_uint(__uint_as_float(a[4 * u + 1]) + x.y);
+        a[4 * u + 2] = __float_as_uint(__uint_as_float(a[4 * u + 2]) + x.z);
+        a[4 * u + 3] = __float_as_uint(__uint_as_float(a[4 * u + 3]) + x.w);
+      }
+    };
+
     for (int it = 0; ok && it < nit; ++it) {
       const int slot = it & 1;
       const RowVals nrow = row_vals(it + 1);  // next step's row values, stored at the end of this one
@@ -1042,6 +1114,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
                            __float_as_uint(__uint_as_float(o[4 * u + 1]) * p.scale),
                            __float_as_uint(__uint_as_float(o[4 * u + 2]) * p.scale),
                            __float_as_uint(__uint_as_float(o[4 * u + 3]) * p.scale));
+            if (PACKED && it % kFoldSteps == 0) fold(it > kFoldSteps);
             tmem_wait_st();
             fence_proxy_async_smem();
             tc_fence_before();
@@ -1085,6 +1158,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
           if (ok) {
             tc_fence_after();
             ok = stage_dq(it);
+            if (PACKED && ok && it + 1 < nit && (it + 1) % kFoldSteps == 0) fold(it + 1 > kFoldSteps);
           }
         }
       }
@@ -1108,6 +1182,8 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       tmem_wait_ld();
       reg_fence16(a);
       reg_fence16(g);
+      whole(a, 0, fb, 16);
+      whole(g, 1, fb, 16);
       const long long row = PACKED ? static_cast<long long>(seq_first + k0 + r) * p.Hkv + h
                                    : static_cast<long long>(bh) * Nkv + k0 + r;
       if (ACCUM == 1 && key_ok) {
@@ -1160,6 +1236,8 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       tmem_wait_ld();
       reg_fence32(a);
       reg_fence32(g);
+      whole(a, 0, fb, 32);
+      whole(g, 1, fb, 32);
       if (ACCUM == 1 && key_ok) {
         const long long row = static_cast<long long>(bh) * Nkv + k0 + r;
         float4* dv = reinterpret_cast<float4*>(p.dv_acc + row * HD + fb);
@@ -1506,7 +1584,8 @@ int launch_packed_bwd(const PackedArgs& a, const void* dout, void* dq, void* dk,
   const cuuint32_t dbox[3] = {32, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(p.tpt)};
   const cuuint32_t kbox[3] = {64, 1, BT};
   CUtensorMap mq, mk, mv, mg, mdq;
-  int rc = encode_map(&mq, type, 3, a.q, qdims, qs, rbox);
+  int rc = osum_slots(&p.osum, &p.n_osum);
+  if (rc == CQSA_OK) rc = encode_map(&mq, type, 3, a.q, qdims, qs, rbox);
   if (rc == CQSA_OK) rc = encode_map(&mg, type, 3, dout, qdims, gs, rbox);
   if (rc == CQSA_OK) rc = encode_map(&mk, type, 3, a.k, kdims, ks, kbox);
   if (rc == CQSA_OK) rc = encode_map(&mv, type, 3, a.v, kdims, vs, kbox);

@@ -432,7 +432,7 @@ const char* cqsa_last_error(void);
  * synchronises the device, stores the code (0 = none) and the block index, optionally clears it.
  * Returns CQSA_OK, or CQSA_ERR_TIMEOUT if a code was set. Two codes return CQSA_ERR_DEVICE instead:
  * 5, a d = 128 forward CTA (packed and paged calls' too) that ran on an SM beyond its running-sum slots (the result is
- * still exact),
+ * still exact) or a long packed backward's CTA (it stopped before computing anything),
  * and 6, a backward kernel whose dynamic shared memory base was not 1024-byte aligned (it stopped
  * before computing anything).
  */

@@ -62,3 +62,50 @@ def test_tokens_over_a_very_long_context(cq, cache, d):
         _drift(out[i], ref, hq * d, 256, f"sequence {i}")
         # a sum of n fp32 terms in no more than n / 16 steps a lane, each rounded at random: far less than 2^-16
         assert (lse[:, i].double() - rl).abs().max().item() <= 2.0 ** -15
+
+
+@pytest.mark.parametrize("d,hkv", [(64, 4), (128, 2)])
+def test_gradients_of_a_long_sequence_of_many_heads(cq, d, hkv):
+    """32,768 tokens with 16 query heads a key head: equal scores, so that dv is the mean of dout over half a million rows."""
+    n, group, dtype = 32768, 16, torch.float16
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.rand(n, group * hkv, d, generator=g, device="cuda").to(dtype)
+    k = torch.zeros(n, hkv, d, dtype=dtype, device="cuda")
+    v = torch.randn(n, hkv, d, generator=g, device="cuda").to(dtype)
+    dout = ((torch.rand(n, group * hkv, d, generator=g, device="cuda") * 0.4 + 0.8) * (1 + torch.arange(d, device="cuda") / d)).to(dtype)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, lse = cq.attention_packed(q, k, v, cu, causal=False, return_lse=True)
+    dv = cq.attention_packed_backward(q, k, v, out, dout, lse, cu, causal=False)[2]
+    torch.cuda.synchronize()
+    assert cq.cqsa_device_error()[1] == 0
+    ref = dout.reshape(n, hkv, group, d).sum((0, 2), dtype=torch.float64) / n
+    for i in (0, 5, n // 2, n - 1):
+        _drift(dv[i], ref, hkv * d, 1024, f"key {i}")
+
+
+@pytest.mark.parametrize("lens,hq,hkv", [([5000, 300], 32, 1), ([6000, 10], 32, 8)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gradients_with_running_sums(cq, lens, hq, hkv, d, dt):
+    """Key tiles whose steps are more than a fold's, cut into ranges (the first sizes) and whole (the second): every gradient against
+    the formula, dk and dv again bit by bit, and from a workspace that held NaN."""
+    dtype, total = sq.DT[dt], sum(lens)
+    q, k, v, g = (sq.normal((total, h, d), dtype, i, t) for i, h, t in ((1, hq, 1.0), (2, hkv, 1.5), (3, hkv, 1.0), (4, hq, 1.0)))
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    out, lse = cq.attention_packed(q, k, v, cu, return_lse=True)
+    got = cq.attention_packed_backward(q, k, v, out, g, lse, cu)
+    at = 0
+    for n in lens:
+        i = slice(at, at + n)
+        ref, mass = sq.gradients(q[i], k[i], v[i], out[i], g[i], True)
+        for name, x, r, m in zip(("dq", "dk", "dv"), got, ref, mass):
+            sq.check_grad(x[i], r, m, dtype, f"{name} of {n} tokens")
+        at += n
+    need = cq.cqsa_attn_packed_bwd_workspace_size(len(lens), total, hq, hkv, d)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    again = [torch.empty_like(t) for t in (q, k, v)]
+    cq.cqsa_attn_packed_bwd(q, k, v, 0, 0, 0, out, g, lse, *again, ws, need, cu, len(lens), total, hq, hkv, d, True, 0.0,
+                            cq.dtype_code(dtype))
+    assert torch.equal(again[1], got[1]) and torch.equal(again[2], got[2])
+    torch.cuda.synchronize()
+    assert cq.cqsa_device_error()[1] == 0
