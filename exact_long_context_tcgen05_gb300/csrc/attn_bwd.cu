@@ -203,6 +203,27 @@ __device__ __forceinline__ bool wait_abort(uint64_t* bar, uint32_t parity, unsig
   return wait_abort_a(smem_u32(bar), parity, tmo, smem_u32(const_cast<int*>(abort_flag)), code, where);
 }
 
+// The same by a whole warp, whose lanes leave the loop together: what follows (tcgen05.ld and .st) has to be executed by a
+// converged warp.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsigned long long tmo,
+                                          volatile int* abort_flag, int code, int where) {
+  const uint32_t a = smem_u32(bar), abort_a = smem_u32(const_cast<int*>(abort_flag));
+  if (__all_sync(0xffffffffu, mbar_try_wait_a(a, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t spins = 0;
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_a(a, parity))) return true;
+    if ((++spins & 15u) == 0) {
+      if (__any_sync(0xffffffffu, ld_shared_volatile_u32(abort_a) != 0)) return false;
+      if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > tmo)) {
+        record_bwd_error(code, where);
+        st_shared_volatile_u32(abort_a, 1u);
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ uint32_t sm_id() {
   uint32_t id;
   asm volatile("mov.u32 %0, %%smid;" : "=r"(id));
@@ -498,9 +519,9 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       uint32_t fixes = 0;
       // a tile with rows past the sequence's end lands on bar_fix; they are zeroed, then it is released
       auto fix = [&](uint8_t* tile, int r0, uint64_t* bar) -> bool {
-        const bool w = wait_abort(bar_fix, fixes & 1u, tmo, abort_flag, kBwdTimeoutLoad, 11);
+        const bool w = wait_warp(bar_fix, fixes & 1u, tmo, abort_flag, kBwdTimeoutLoad, 11);
         ++fixes;
-        if (!__all_sync(0xffffffffu, w)) return false;
+        if (!w) return false;
         zero_tail<HD>(tile, r0, lane);
         fence_proxy_async_smem();
         __syncwarp();
@@ -572,7 +593,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         return true;
       };
       auto freed = [&](int slot, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_abort(&bar_qfree[slot], parity, tmo, abort_flag, kBwdTimeoutLoad, 5));
+        return wait_warp(&bar_qfree[slot], parity, tmo, abort_flag, kBwdTimeoutLoad, 5);
       };
       if constexpr (HD == 64) {
         for (int it = 0; ok && it < nit; ++it) {
@@ -681,8 +702,10 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       const uint64_t dG0_mn = smem_desc_sw128(smem_u32(sG), LBO_MN, 1024);
       constexpr uint32_t SLOT16 = TILE >> 4;  // one slot in descriptor address units
       auto wait_all = [&](uint64_t* bar, uint32_t parity, int code, int where) -> bool {
-        const bool w = wait_abort(bar, parity, tmo, abort_flag, code, where);
-        return __all_sync(0xffffffffu, w);
+        // (No tcgen05.ld or .st follows here, so either form will do. The converged one takes 1,246 us against 1,285 in the packed call at
+        // d = 128 and 2.38 ms against 2.39 at d = 64; in the unpacked call at d = 128, 21.88 ms against 21.56.)
+        if constexpr (PACKED || HD == 64) return wait_warp(bar, parity, tmo, abort_flag, code, where);
+        return __all_sync(0xffffffffu, wait_abort(bar, parity, tmo, abort_flag, code, where));
       };
       auto issue_m1 = [&](int it) {
         const uint32_t so = static_cast<uint32_t>(it % NSLOT) * SLOT16;
@@ -808,10 +831,9 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       const bool leader = elect_lane();
       const uint64_t dK_mn = smem_desc_sw128(smem_u32(sK), 1024u, 1024);
       const uint64_t dS_mn = smem_desc_sw128(smem_u32(sdS), BOX, 1024);
-      bool ok = __all_sync(0xffffffffu, wait_abort(bar_kv, 0, tmo, abort_flag, kBwdTimeoutLoad, 1));
+      bool ok = wait_warp(bar_kv, 0, tmo, abort_flag, kBwdTimeoutLoad, 1);
       for (int it = 0; ok && it < nit; ++it) {
-        ok = __all_sync(0xffffffffu,
-                        wait_abort(bar_ready, static_cast<uint32_t>(it & 1), tmo, abort_flag, kBwdTimeoutSoftmax, 7));
+        ok = wait_warp(bar_ready, static_cast<uint32_t>(it & 1), tmo, abort_flag, kBwdTimeoutSoftmax, 7);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
@@ -908,9 +930,8 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       const bool dead = PACKED && it == nit - 1 && r >= (Nkv - (it0 + it) * p.tpt) * p.G;
       if constexpr (HD == 64) {
         bool w = true;
-        if (it >= 2) w = wait_abort(&bar_dqfree[slot], static_cast<uint32_t>(((it - 2) >> 1) & 1), tmo, abort_flag,
-                                    kBwdTimeoutSoftmax, 9);
-        w = __all_sync(0xffffffffu, w);
+        if (it >= 2) w = wait_warp(&bar_dqfree[slot], static_cast<uint32_t>(((it - 2) >> 1) & 1), tmo, abort_flag,
+                                   kBwdTimeoutSoftmax, 9);
         if (!w) return false;
       }
       // (d = 128: the staging area was released before this step's dS^T was written over it)
@@ -1009,8 +1030,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     for (int it = 0; ok && it < nit; ++it) {
       const int slot = it & 1;
       const RowVals nrow = row_vals(it + 1);  // next step's row values, stored at the end of this one
-      ok = wait_abort(bar_m1, static_cast<uint32_t>(it & 1), tmo, abort_flag, kBwdTimeoutMMA, 3);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = wait_warp(bar_m1, static_cast<uint32_t>(it & 1), tmo, abort_flag, kBwdTimeoutMMA, 3);
       uint32_t pw[QC / 2], dw[QC / 2];
       if (ok) {
         tc_fence_after();
@@ -1089,12 +1109,11 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
         // P^T and dS^T of the previous step are consumed once its products are done; its dQ is read out of
         // tensor memory while this step's P^T and dS^T go in, under one wait and one fence
         if (ok && it > 0) {
-          ok = wait_abort(bar_m2, static_cast<uint32_t>((it - 1) & 1), tmo, abort_flag, kBwdTimeoutMMA, 4);
+          ok = wait_warp(bar_m2, static_cast<uint32_t>((it - 1) & 1), tmo, abort_flag, kBwdTimeoutMMA, 4);
           const int qs = (it - 1) & 1;
           if (ok && it - 1 >= 2)
-            ok = wait_abort(&bar_dqfree[qs], static_cast<uint32_t>(((it - 3) >> 1) & 1), tmo, abort_flag,
-                            kBwdTimeoutSoftmax, 9);
-          ok = __all_sync(0xffffffffu, ok);
+            ok = wait_warp(&bar_dqfree[qs], static_cast<uint32_t>(((it - 3) >> 1) & 1), tmo, abort_flag,
+                           kBwdTimeoutSoftmax, 9);
           if (ok) {
             tc_fence_after();
             uint32_t o[16];
@@ -1128,8 +1147,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       } else {
         // the previous step's dQ, staged over the dS^T tile, must have been read by its reduction
         if (ok && it > 0) {
-          ok = wait_abort(&bar_dqfree[0], static_cast<uint32_t>((it - 1) & 1), tmo, abort_flag, kBwdTimeoutSoftmax, 9);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = wait_warp(&bar_dqfree[0], static_cast<uint32_t>((it - 1) & 1), tmo, abort_flag, kBwdTimeoutSoftmax, 9);
         }
       }
       if (ok) {
@@ -1153,8 +1171,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       if constexpr (HD == 128) {
         // this step's dQ, out of the dP^T columns before the next step's products may be issued
         if (ok) {
-          ok = wait_abort(bar_m2, static_cast<uint32_t>(it & 1), tmo, abort_flag, kBwdTimeoutMMA, 4);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = wait_warp(bar_m2, static_cast<uint32_t>(it & 1), tmo, abort_flag, kBwdTimeoutMMA, 4);
           if (ok) {
             tc_fence_after();
             ok = stage_dq(it);
@@ -1166,8 +1183,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
     }
     if (HD == 64 && ok) {
       // last step: dQ, then dV_j and dK_j rows (key row = tensor-memory lane), written once
-      ok = wait_abort(bar_m2, static_cast<uint32_t>((nit - 1) & 1), tmo, abort_flag, kBwdTimeoutMMA, 4);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = wait_warp(bar_m2, static_cast<uint32_t>((nit - 1) & 1), tmo, abort_flag, kBwdTimeoutMMA, 4);
       if (ok) {
         tc_fence_after();
         ok = stage_dq(nit - 1);
@@ -1231,6 +1247,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       if (!ok) break;
       const int fb = wg * (HD / 2) + c * 32;  // first feature of this chunk
       uint32_t a[32], g[32];
+      __syncwarp();  // (stores of the key rows that count may have parted the lanes)
       tmem_ld32(trow + C::COL_DV + fb, a);
       tmem_ld32(trow + C::COL_DK + fb, g);
       tmem_wait_ld();

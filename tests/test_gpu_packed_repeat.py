@@ -1,0 +1,76 @@
+"""Packed gradients again and again on the GPU: dk and dv are the same bits behind emptied caches and in a process's first call, where waits
+are longest and a warp's lanes could leave them apart."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from tests import _seq as sq
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+RAGGED = [725, 33, 334, 101, 237, 53, 133, 1284, 201, 88, 0, 104, 549, 210, 18, 47, 1615, 60, 397, 585, 389, 969, 55]
+
+
+@pytest.fixture(scope="module")
+def cq():
+    import exact_long_context_tcgen05_gb300 as m
+    return m
+
+
+@pytest.mark.parametrize("d,dt,hq,hkv", [(64, "f16", 8, 2), (64, "bf16", 32, 8), (128, "bf16", 32, 8), (128, "f16", 5, 1)])
+def test_backward_repeats(cq, d, dt, hq, hkv):
+    """Every gradient against the formula; then dk and dv bit by bit over 60 passes, every third behind work that has emptied L2."""
+    dtype = sq.DT[dt]
+    q, g = (sq.normal((sum(RAGGED), hq, d), dtype, i) for i in (1, 4))
+    k, v = (sq.normal((sum(RAGGED), hkv, d), dtype, i) for i in (2, 3))
+    cu = torch.tensor(sq.starts(RAGGED), dtype=torch.int32, device="cuda")
+    out, lse = cq.attention_packed(q, k, v, cu, return_lse=True)
+    other = torch.empty(100_000_000, device="cuda")
+    other.fill_(1.0)
+    first = cq.attention_packed_backward(q, k, v, out, g, lse, cu)
+    at = sq.starts(RAGGED)
+    for s, n in enumerate(RAGGED):
+        if n:
+            i = slice(at[s], at[s + 1])
+            ref, mass = sq.gradients(q[i], k[i], v[i], out[i], g[i], True)
+            for x, r, m in zip(first, ref, mass):
+                sq.check_grad(x[i], r, m, dtype, f"sequence {s}")
+    for i in range(60):
+        if i % 3 == 0:
+            other.fill_(i)
+        again = cq.attention_packed_backward(q, k, v, out, g, lse, cu)
+        assert torch.equal(again[1], first[1]) and torch.equal(again[2], first[2]), f"pass {i}"
+    torch.cuda.synchronize()
+    assert cq.cqsa_device_error()[1] == 0
+
+
+COLD = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import exact_long_context_tcgen05_gb300 as cq
+lens = {lens!r}
+d, hq, hkv, dtype = {d}, 32, 8, torch.bfloat16
+torch.manual_seed(0)
+q, k, v, g = (torch.randn(sum(lens), h, d, device="cuda").to(dtype) for h in (hq, hkv, hkv, hq))
+cu = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], device="cuda", dtype=torch.int32)
+out, lse = torch.zeros_like(q), torch.full((hq, sum(lens)), 6.0, device="cuda")
+first = cq.attention_packed_backward(q, k, v, out, g, lse, cu)   # (any out and lse will do: the process's first kernel of this library)
+for _ in range(5):
+    again = cq.attention_packed_backward(q, k, v, out, g, lse, cu)
+    assert torch.equal(first[1], again[1]) and torch.equal(first[2], again[2])
+    # dq: fp32 sums in any order, one rounding each
+    step = (first[0].float() - again[0].float()).abs() - first[0].float().abs().clamp(min=2.0 ** -10) * 2.0 ** -7
+    assert step.max().item() <= 0, step.max().item()
+assert cq.cqsa_device_error()[1] == 0
+print("equal")
+"""
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_first_call_of_a_process(d):
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", COLD.format(root=ROOT, lens=RAGGED, d=d)], capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0 and r.stdout.strip().endswith("equal"), r.stdout + r.stderr
