@@ -169,6 +169,17 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs
             const float2 p = unpack16(e4m3x2_to_f16x2(w[i]), 0);
             r[i] = pack16(p.x * s, p.y * s, BF16);
           }
+          // From this power on a code may stand for more than the type's largest value (fp16's 65,504 is held as 256 * 2^8): it reads as
+          // the largest, as what was written was finite. (Under a branch: 39 us against 41 for 16,384 tokens.)
+          if (e[kv][u] >= 127 + (BF16 ? 120 : 8)) {
+            constexpr float MOST = BF16 ? 0x1.fep127f : 65504.0f;
+            auto held = [](float x) -> float { return x > MOST ? MOST : (x < -MOST ? -MOST : x); };  // (NaN passes on)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 p = unpack16(e4m3x2_to_f16x2(w[i]), 0);
+              r[i] = pack16(held(p.x * s), held(p.y * s), BF16);
+            }
+          }
           y = make_uint4(r[0], r[1], r[2], r[3]);
         }
         if (h < a.Hkv) __stcs(reinterpret_cast<uint4*>(dst + h * D) + c, y);

@@ -396,8 +396,8 @@ int cqsa_kv_cache_write(const void* k, const void* v, long long k_stride, long l
                         int n_pages, int dtype, int cache_dtype, cudaStream_t stream);
 
 /* The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence back out of the cache (all of them where
- * that is kv_lens[s]): k, v device [T, Hkv, d], written in dtype; e4m3 values are rounded to dtype once. Tokens whose position
- * is negative or beyond the table give zeros. */
+ * that is kv_lens[s]): k, v device [T, Hkv, d], written in dtype; e4m3 values are rounded to dtype once, and finite ones past its
+ * largest value are held at that. Tokens whose position is negative or beyond the table give zeros. */
 int cqsa_kv_cache_read(void* k, void* v, const void* k_cache, const void* v_cache, const unsigned char* k_scale,
                        const unsigned char* v_scale, const int* block_table, int max_pages, const int* cu_seqlens,
                        const int* kv_lens, int n_seqs, int T, int Hkv, int d, int page_size, int n_pages, int dtype,
