@@ -668,6 +668,7 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
     T, Hq = q.shape[:2]
     q, qs = _tokens("q", q, Hq, d, q)
     dt = _code(dtype)
+    max_q_len, max_kv_len = min(max_q_len, T), min(max_kv_len, 0x7fffffff)  # (ctypes would cut larger ones down to 32 bits)
     out = _out(out, q)
     lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if return_lse else None
     if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
