@@ -480,9 +480,15 @@ def _tokens(name, t, heads, d, like):
     T = shape[0]
     s = t.stride()
     if (s[2] != 1 or (s[1] != d and heads > 1) or s[0] < heads * d or s[0] % 8 or t.data_ptr() & 15) and T > 0:
-        t = t.clone() if t.is_contiguous() else t.contiguous()
-        return t, heads * d
+        return _dense(t), heads * d
     return t, (s[0] if T > 1 else heads * d)
+
+
+def _dense(t):
+    """t, or a copy of it where it is not contiguous or not 16-byte aligned."""
+    if not t.is_contiguous():
+        return t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 def _ints(name, t, shape, device):
@@ -581,7 +587,7 @@ def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=Tru
             raise ValueError(f"{name} must be a {tuple(q.shape)} tensor of {dtype} on {device}")
     if lse.shape != (Hq, T) or lse.dtype != torch.float32 or lse.device != device:
         raise ValueError("lse must be a float32 tensor [Hq, T]")
-    out, dout, lse = out.contiguous(), dout.contiguous(), lse.contiguous()
+    out, dout, lse = _dense(out), _dense(dout), lse.contiguous()
     if grads is None:
         dq = torch.empty((T, Hq, d), dtype=dtype, device=device)
         dk, dv = (torch.empty((T, Hkv, d), dtype=dtype, device=device) for _ in range(2))

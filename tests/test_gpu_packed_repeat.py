@@ -74,3 +74,28 @@ def test_first_call_of_a_process(d):
     for _ in range(3):
         r = subprocess.run([sys.executable, "-c", COLD.format(root=ROOT, lens=RAGGED, d=d)], capture_output=True, text=True, timeout=300)
         assert r.returncode == 0 and r.stdout.strip().endswith("equal"), r.stdout + r.stderr
+
+
+def test_backward_of_offset_and_expanded_tensors(cq):
+    """out and dout at an odd offset, and dout as the expanded ones that a sum's gradient is: copied first, as q, k and v are."""
+    lens, hq, hkv, d, dtype = [70, 33], 4, 2, 64, torch.float16
+    n = sum(lens)
+    q, k, v = (sq.normal((n, h, d), dtype, i) for i, h in ((1, hq), (2, hkv), (3, hkv)))
+    cu = torch.tensor(sq.starts(lens), dtype=torch.int32, device="cuda")
+    out, lse = cq.attention_packed(q, k, v, cu, return_lse=True)
+    odd = torch.empty(n * hq * d + 1, dtype=dtype, device="cuda")[1:].view(n, hq, d)
+    odd_lse = torch.empty(hq * n + 1, device="cuda")[1:].view(hq, n)
+    odd.copy_(out)
+    odd_lse.copy_(lse)
+    for dout in (torch.ones((), dtype=dtype, device="cuda").expand(n, hq, d), odd):
+        want = cq.attention_packed_backward(q, k, v, out, dout.clone(memory_format=torch.contiguous_format), lse, cu)
+        got = cq.attention_packed_backward(q, k, v, odd, dout, odd_lse, cu)
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        at = 0
+        for m in lens:
+            i = slice(at, at + m)
+            ref, mass = sq.gradients(q[i], k[i], v[i], out[i], dout[i], True)
+            for x, r, w in zip(got, ref, mass):
+                sq.check_grad(x[i], r, w, dtype)
+            at += m
+    assert cq.cqsa_device_error()[1] == 0
