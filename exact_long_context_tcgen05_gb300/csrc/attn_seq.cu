@@ -1391,12 +1391,13 @@ int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
   int rc = osum_slots(&p.osum, &p.n_osum);
   CUtensorMap mq, mk, mv;
   if (rc == CQSA_OK) rc = make_token_map(&mq, a.q, a.dtype, a.d, a.Hq, a.T, a.q_stride, p.G, p.tpt);
+  // (e4m3 pages are copied as they lie, without maps: the queries' stands in for theirs)
+  if (rc == CQSA_OK && a.cache_dtype == CQSA_E4M3) return dispatch<kSrcE4m3>(mq, mq, mq, p, a.d, a.dtype, ctas, stream);
   const int box = a.page < BN ? a.page : BN;
   if (rc == CQSA_OK) rc = make_page_map(&mk, a.k_cache, a, box);
   if (rc == CQSA_OK) rc = make_page_map(&mv, a.v_cache, a, box);
   if (rc != CQSA_OK) return rc;
-  return a.cache_dtype == CQSA_E4M3 ? dispatch<kSrcE4m3>(mq, mk, mv, p, a.d, a.dtype, ctas, stream)
-                                    : dispatch<kSrcPages>(mq, mk, mv, p, a.d, a.dtype, ctas, stream);
+  return dispatch<kSrcPages>(mq, mk, mv, p, a.d, a.dtype, ctas, stream);
 }
 
 int launch_packed(const PackedArgs& a, cudaStream_t stream) {
