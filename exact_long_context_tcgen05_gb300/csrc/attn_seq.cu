@@ -17,7 +17,8 @@
 //            number of ranges: 787 us against 712 for 256 units of 266 tiles, 135 against 86 for 12 ragged e4m3 sequences.)
 //   P        is rounded once to dtype for P V (2^-8 relative for bf16, as the output is; attn_fwd.cu's
 //            hi/lo split, half as many products again, serves fp32 partial results), scaled by 2^6 so that
-//            fp16 keeps its relative precision down to p = 2^-20 of the row's largest at least.
+//            fp16 keeps its relative precision down to p = 2^-19 of the row's largest at least (the reference is a
+//            whole number, up to 1 above the row's maximum).
 //   Tails    rows of V past a sequence's end (another sequence's tokens, or whatever an unused slot holds) are zeroed in
 //            shared memory before the product: p = 0 does not hide an infinity or NaN there.
 //   e4m3     the producer copies code vectors as they lie in the pages, and four converter warps turn them into
