@@ -94,9 +94,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // Row maximum of 128 scores: three-input max, four independent chains.
 __device__ __forceinline__ float row_max128(const float (&x)[128]) {
-  float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+  float m0 = fmaxf(x[0], x[1]), m1 = fmaxf(x[2], x[3]), m2 = fmaxf(x[4], x[5]), m3 = fmaxf(x[6], x[7]);
 #pragma unroll
-  for (int c = 4; c < 128; c += 8) {
+  for (int c = 8; c < 128; c += 8) {
     m0 = max3(m0, x[c], x[c + 1]);
     m1 = max3(m1, x[c + 2], x[c + 3]);
     m2 = max3(m2, x[c + 4], x[c + 5]);
