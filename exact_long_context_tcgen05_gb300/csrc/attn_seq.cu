@@ -3,8 +3,8 @@
 // (cqsa_attn_paged_fwd with more than 32 rows per sequence and key head).
 //
 // The pipeline is attn_fwd2_kernel's (attn_fwd.cu): TMA producer, one MMA-issuing warp per query tile, one
-// softmax warpgroup per query tile, tcgen05 products accumulating in tensor memory, an integer running reference
-// maximum with rare exact rescales. What differs:
+// softmax warpgroup per query tile, tcgen05 products accumulating in tensor memory, a running reference
+// maximum that moves by whole numbers with rare exact rescales. What differs:
 //   Rows     a tile's 128 rows are floor(128 / G) tokens times the G query heads of one key head (row
 //            r = token r / G, head r % G), loaded by one 3-D TMA box, so that a short sequence or chunk fills tiles G
 //            times better and K/V are loaded once for the whole group.
@@ -17,8 +17,8 @@
 //            number of ranges: 787 us against 712 for 256 units of 266 tiles, 135 against 86 for 12 ragged e4m3 sequences.)
 //   P        is rounded once to dtype for P V (2^-8 relative for bf16, as the output is; attn_fwd.cu's
 //            hi/lo split, half as many products again, serves fp32 partial results), scaled by 2^6 so that
-//            fp16 keeps its relative precision down to p = 2^-19 of the row's largest at least (the reference is a
-//            whole number, up to 1 above the row's maximum).
+//            fp16 keeps its relative precision down to p = 2^-19 of the row's largest at least (the reference may lie
+//            up to 1 above the row's maximum).
 //   Tails    rows of V past a sequence's end (another sequence's tokens, or whatever an unused slot holds) are zeroed in
 //            shared memory before the product: p = 0 does not hide an infinity or NaN there.
 //   e4m3     the producer copies code vectors as they lie in the pages, and four converter warps turn them into
@@ -197,6 +197,9 @@ __device__ __forceinline__ void issue_o(uint32_t ocol, uint32_t pcol, uint64_t v
     else mma_ts_i<1>(ocol, pcol + ks * 8, bd, idesc);
   }
 }
+
+// 2^k for a difference k <= 0 of two references of a row, a whole number (but for what fp32 rounds off very large ones).
+__device__ __forceinline__ float exp2_whole(float k) { return exp2_int(rintf(k)); }
 
 // 2^(x sl2 - m) for a pair of scores.
 __device__ __forceinline__ float2 exp2_pair(float x0, float x1, float2 sl2v, float2 nm) {
@@ -782,7 +785,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           if (!ok) break;
           tc_fence_after();
           const bool have = j0 > C::FLUSH;
-          float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
+          float sc = (m_sum == -INFINITY) ? 0.0f : exp2_whole(m_sum - m_ref);
           if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
           if (C::OSUM_SMEM) {
 #pragma unroll
@@ -861,13 +864,18 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           const float tmax = row_max128(x) * slt;
           float al_l = 1.0f;  // what the row's sum is multiplied by (the values' exponent does not matter to it)
           if (tmax > m_ref + kTau || (m_ref == -INFINITY && tmax > -INFINITY)) {
-            const float m_new = ceilf(tmax);
-            if (m_ref != -INFINITY) {
-              al_l = exp2_int(m_ref - m_new);
+            // From the first tile's largest score on by whole numbers, so that rescales are powers of two. That score is taken to fp32's
+            // steps beside 768, 2^-14 for most, which leave room for those steps. A row of one key then has P = 2^6 once P is
+            // rounded, and gives its value's bits (ragged prompts at d = 128: 217 us against 215 with ceilf(tmax)).
+            if (m_ref == -INFINITY) {
+              m_ref = (tmax + 768.0f) - 768.0f;
+            } else {
+              const float up = ceilf(tmax - m_ref);
+              m_ref += up;
+              al_l = exp2_int(-up);
               alpha *= al_l;
               rescale = true;
             }
-            m_ref = m_new;
           }
           // O takes the new reference (the running sum keeps its own), once PV_t(j-1) has been accumulated
           auto rescale_o = [&]() {
@@ -976,7 +984,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         float y[32];
         if (osum_ok && n > C::FLUSH) {
           const float* os = sOsum + (wg * D + c * 32) * 128 + r;
-          float sc = (m_sum == -INFINITY) ? 0.0f : exp2_int(m_sum - m_ref);
+          float sc = (m_sum == -INFINITY) ? 0.0f : exp2_whole(m_sum - m_ref);
           if (CONV) sc *= exp2_int(static_cast<float>(max(ev_sum - ev, -200)));
           float prev[32];
 #pragma unroll
