@@ -109,3 +109,33 @@ def test_gradients_with_running_sums(cq, lens, hq, hkv, d, dt):
     assert torch.equal(again[1], got[1]) and torch.equal(again[2], got[2])
     torch.cuda.synchronize()
     assert cq.cqsa_device_error()[1] == 0
+
+
+def test_running_sums_of_calls_at_once(cq):
+    """Forward, backward and chunk calls whose running sums lie in the SMs' slots, on three streams at once: each gives what it gives
+    alone."""
+    d, hq, hkv, page, dtype = 128, 8, 2, 64, torch.float16
+    n = [9000, 8200, 9500]
+    q, k, v, g = ([sq.normal((m, h, d), dtype, 4 * i + j) for i, m in enumerate(n)] for j, h in enumerate((hq, hkv, hkv, hq)))
+    cu = [torch.tensor([0, m], dtype=torch.int32, device="cuda") for m in n]
+    out, lse = cq.attention_packed(q[1], k[1], v[1], cu[1], return_lse=True)
+    pages = -(-n[2] // page)
+    kc, vc = (torch.zeros(pages, hkv, page, d, dtype=dtype, device="cuda") for _ in range(2))
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    cq.kv_cache_write(k[2], v[2], kc, vc, table, cu[2], cu[2][1:])
+    new = torch.tensor([0, 500], dtype=torch.int32, device="cuda")
+    calls = [lambda s: [cq.attention_packed(q[0], k[0], v[0], cu[0], stream=s)],
+             lambda s: list(cq.attention_packed_backward(q[1], k[1], v[1], out, g[1], lse, cu[1], stream=s)[1:]),
+             lambda s: [cq.attention_paged(q[2][-500:], kc, vc, table, new, cu[2][1:], 500, 1, stream=s)]]
+    want = [f(None) for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for i in range(20):
+        got = [None] * 3
+        for j in range(3):
+            at = (i + j) % 3
+            got[at] = calls[at](streams[at])
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b)), f"pass {i}"
+    assert cq.cqsa_device_error()[1] == 0

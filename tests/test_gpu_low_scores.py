@@ -81,3 +81,37 @@ def test_dense(cq, causal, dt, d):
         u = sq.U[dtype]
         tol = 1.01 * (u * r.abs() + u * m[0] + d * 2.0 ** -23 * m[1] + 2.0 ** -25 * m[2] + 2.0 ** -25) + extra
         assert ((a[0].transpose(0, 1).double() - r).abs() <= tol).all(), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("order", ["rising", "falling"])
+def test_scores_that_move(cq, order, dt, d):
+    """Scores that go from -300 to 300 along the keys, or back, a little every key: each tile's weights leave those of the one before far
+    behind, or count for nothing beside them."""
+    dtype, n, hq, hkv, page = sq.DT[dt], 700, 4, 2, 32
+    g = torch.Generator().manual_seed(1)
+    q = torch.zeros(n, hq, d)
+    q[:, :, :2] = 8.0
+    k = torch.zeros(n, hkv, d)
+    step = torch.linspace(-300, 300, n) if order == "rising" else torch.linspace(300, -300, n)
+    k[:, :, 0] = torch.round(step)[:, None]                                   # whole numbers up to 300: exact in fp16, and in bf16 to 256
+    k[:, :, 0] = k[:, :, 0].to(dtype).float()
+    k[:, :, 1] = torch.randint(-1, 2, (n, hkv), generator=g).float()
+    q, k, v = q.to(dtype).cuda(), k.to(dtype).cuda(), sq.normal((n, hkv, d), dtype, 3)
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [n]))
+    pages = -(-n // page)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    kc, vc = (torch.zeros(pages, hkv, page, d, dtype=dtype, device="cuda") for _ in range(2))
+    cq.kv_cache_write(k, v, kc, vc, table, cu, lens)
+    for causal in (True, False):
+        ref, rl, mass = sq.attend(q, k, v, 0, causal, SCALE)
+        out, lse = cq.attention_packed(q, k, v, cu, causal=causal, scale=SCALE, return_lse=True)
+        _check(out, lse, ref, rl, mass, dtype, what=f"packed causal={causal}")
+        for new in (1, 4, n):
+            i = slice(n - new, n)
+            out, lse = cq.attention_paged(q[i], kc, vc, table, torch.tensor([0, new], dtype=torch.int32, device="cuda"), lens, new, n,
+                                          causal=causal, scale=SCALE, return_lse=True)
+            _check(out, lse, ref[i], rl[:, i], mass[i], dtype, what=f"{new} tokens causal={causal}")
+    torch.cuda.synchronize()
+    assert cq.cqsa_device_error()[1] == 0
