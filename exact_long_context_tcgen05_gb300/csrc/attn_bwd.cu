@@ -33,9 +33,9 @@
 // share the key head, so dK_j and dV_j sum over the group in tensor memory, in a fixed order and without atomics.
 // Rows past a sequence's end (other sequences' tokens) are zeroed in shared memory after their loads: P = dS = 0
 // there would not hide a NaN. packed_prep_kernel and packed_out_kernel take the places of the first and last.
-// Eight ragged prompts of 16,384 tokens together, 32 query and 8 key heads, d = 128, bf16, causal: 1,285 us, of which the
-// main kernel takes 1,140 (0.83 PFLOP/s) and the two others, which move 0.94 GB, 145. What bounds a step is the chain that d = 128
-// has in the other forms too: one slot each of Q and dO, and dQ staged over dP^T (6,300 cycles, 2,560 of them products).
+// Eight ragged prompts of 16,384 tokens together, 32 query and 8 key heads, d = 128, bf16, causal: 1,250 us, of which the
+// main kernel takes 1,105 (0.86 PFLOP/s) and the two others, which move 0.94 GB, 145. What bounds a step is the chain that d = 128
+// has in the other forms too: one slot each of Q and dO, and dQ staged over dP^T (6,100 cycles, 2,560 of them products).
 // P and dS enter the MMAs rounded to the input dtype; everything else is fp32. Head dimension 64 or 128
 // (d = 128 holds one Q/dO tile instead of two, and shares tensor and shared memory between phases: see
 // BwdCfg).
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(BwdThreads<HD>::NTHR, 1)
       } else {
         ok = ok && load_one(0, 0) && load_one(0, 1);
         for (int it = 0; ok && it + 1 < nit; ++it) {
-          if (lane == 0) {  // the one slot is in use for most of a step: the next rows wait for it in L2 (1,325 -> 1,296 us below)
+          if (lane == 0) {  // the one slot is in use for most of a step: the next rows wait for it in L2 (2% of the call's time)
             for (int x = 0; x < HD / 64; ++x) {
               tma_prefetch_3d(&tmG, x * 64, h * p.G, seq_first + (it0 + it + 1) * p.tpt);
               tma_prefetch_3d(&tmQ, x * 64, h * p.G, seq_first + (it0 + it + 1) * p.tpt);
@@ -1561,7 +1561,7 @@ long long packed_tiles(int n_seqs, int T, int Hkv) { return (T / BT + static_cas
 
 // Ranges of steps per key tile: a CTA takes a key tile through all its queries, so few tiles leave SMs idle and the first
 // tile of the longest sequence sets the time. Each range costs fp32 parts and a CTA's set-up, so about two CTAs per SM are
-// aimed at (9 sequences, 4,099 tokens, 2 key heads at d = 64: 88 us in one range, 50 in three, 61 in five, 77 in eight).
+// aimed at (9 sequences, 4,099 tokens, 2 key heads at d = 64: 87 us in one range, 46 in three, 53 in five, 67 in nine).
 constexpr int kPackedFill = 2;
 int packed_splits(int n_seqs, int T, int Hkv) {
   const long long s = static_cast<long long>(sm_count()) * kPackedFill / std::max<long long>(1, packed_tiles(n_seqs, T, Hkv));

@@ -25,8 +25,8 @@
 // exact but for elements 2^-14 below the row's largest, whose error stays under 2^-25 of it.
 //
 // Measured, one token of each sequence, 32 query and 8 key heads, d = 128: 64 sequences of 300,000 bf16 positions together
-// 197 us (1.23 GB, 6.2 TB/s); 128 of 500,000 e4m3 positions 204 us (1.03 GB, 5.1 TB/s: conversions and exponents keep the warps
-// at 43% of issue, and two CTAs an SM at memory for three quarters of the time); one of 3,001 fp16 positions 12 us on the GPU.
+// 202 us (1.23 GB, 6.1 TB/s); 128 of 500,000 e4m3 positions 204 us (1.03 GB, 5.1 TB/s: conversions and exponents keep the warps
+// at 44% of issue, and two CTAs an SM at memory for three quarters of the time); one of 3,001 fp16 positions 12 us on the GPU.
 #include <math.h>
 #include <string.h>
 
@@ -800,6 +800,11 @@ int decode_ctas(const PagedArgs& a) {
 
 }  // namespace
 
+// Up to 32 rows per sequence and key head, by the caller's most new tokens; 32 are this kernel's two row tiles. 32 rows of each sequence here and
+// in attn_seq.cu's kernel, us: d = 128, 64 sequences of some 290,000 positions together 251 / 261 over 16-bit pages and 284 / 489 over
+// e4m3 ones, 8 sequences of 44,000 16-bit ones 75 / 65, of 112,000 e4m3 ones 122 / 169; d = 64 61 / 67, 59 / 87, 35 / 39, 35 / 44. 16 rows:
+// 207 / 253, 157 / 470, 56 / 65, 74 / 169; 54 / 67, 38 / 88, 27 / 41, 30 / 46. (From there on one longer chunk in a batch
+// takes its single tokens along; over e4m3 pages that is a step, 284 to 510 us for the first.)
 bool decode_applies(const PagedArgs& a) { return static_cast<long long>(a.max_q_len) * (a.Hq / a.Hkv) <= 32; }
 
 size_t decode_workspace(const PagedArgs& a) {

@@ -26,10 +26,10 @@
 //            below it). K's power goes into the scores' scale; V's is a reference that O is rescaled to when it rises.
 //            Queries are fp16: bf16 ones are first scaled to [1, 2) by a power of two per row, in place.
 //
-// Measured: one causal prompt of 32,768 tokens, 8 query and 2 key heads, d = 64, fp16: 980 us, 1,122 TFLOP/s; 24 ragged prompts
-// of 16,384 tokens together, 32 and 8 heads, d = 128, bf16: 208 us, 1,100 TFLOP/s; 2,048 tokens over 32,000 positions of 16-bit
-// pages, 32 and 8 heads, d = 128: 705 us, 1,570 TFLOP/s, over e4m3 ones 1,195 us; 12 ragged e4m3 sequences (3,000 tokens over
-// 60,000, 8 and 2 heads, d = 64): 85 us. Long rows are bound by the softmax warps' chain of a key tile (tensor-memory loads, row
+// Measured, a pass among others whose inputs L2 does not hold: one causal prompt of 32,768 tokens, 8 query and 2 key heads, d = 64, fp16:
+// 1,014 us, 1,085 TFLOP/s; 24 ragged prompts of 16,384 tokens together, 32 and 8 heads, d = 128, bf16: 219 us, 1,050 TFLOP/s; 2,048
+// tokens over 32,000 positions of 16-bit pages, 32 and 8 heads, d = 128: 765 us, 1,450 TFLOP/s (705 in a loop on one input; over e4m3
+// ones 1,195 there); 12 ragged e4m3 sequences (3,000 tokens over 60,000, 8 and 2 heads, d = 64): 81 us. Long rows are bound by the softmax warps' chain of a key tile (tensor-memory loads, row
 // maximum, 128 exponentials, P back) beside the products it waits for: the tensor pipe is 69% busy at d = 128 and 46% at
 // d = 64; short units add about three key tiles' time each for their start and end. e4m3: the converters take issue slots
 // from the softmax warps of their sub-partitions.

@@ -367,9 +367,8 @@ int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, vo
  * 0 * infinity does in the formula); another sequence's never does, nor what an unused slot of a page holds.
  *
  * Precision. Scores are fp32 and their exponent one rounded multiply-add; P (and dS) is rounded once to 16 bits for its product, where
- * cqsa_attn_fwd multiplies bf16 P in two parts: a bf16 call moved here from there has about the error of its output's own rounding twice
- * over. Accumulators are folded into fp32 sums (the tensor core truncates as it accumulates). bf16 values are summed under factors of
- * up to 2^14: results are right while the largest |v| times a sequence's positions stays below 2^113 (about 1e34), beyond that a sum may
+ * cqsa_attn_fwd multiplies bf16 P in two parts: a bf16 call moved here from there has about 1.4 times the error. Accumulators are folded
+ * into fp32 sums (the tensor core truncates as it accumulates). bf16 values are summed under factors of up to 2^14: results are right while the largest |v| times a sequence's positions stays below 2^113 (about 1e34), beyond that a sum may
  * become infinite where its result is not. Over e4m3 pages, V (and in chunks K) is taken relative to the largest power of two so far in
  * the sequence: chunks lose what lies below 2^-24 of that vector's largest value, single tokens' P V what lies below 2^-28 of it.
  *
