@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libcqsa_gb300.so")
 
 CQSA_OK, CQSA_ERR_INVALID, CQSA_ERR_UNSUPPORTED, CQSA_ERR_CUDA, CQSA_ERR_OOM, CQSA_ERR_TIMEOUT, CQSA_ERR_DEVICE = (
     0, -1, -2, -3, -4, -5, -6)
-CQSA_F16, CQSA_BF16, CQSA_F32, CQSA_E4M3 = 0, 1, 2, 3
+CQSA_F16, CQSA_BF16, CQSA_F32, CQSA_E4M3, CQSA_INT4 = 0, 1, 2, 3, 4
 CQSA_LAYOUT_BHND, CQSA_LAYOUT_BNHD = 0, 1
 CQSA_ENGINE_CLASSIC, CQSA_ENGINE_WAVE = 0, 1
 
@@ -27,7 +27,7 @@ EXPORTED = ("cqsa_attn_fwd", "cqsa_attn_fwd_chunk", "cqsa_merge_partials", "cqsa
             "cqsa_status_string", "cqsa_last_error", "cqsa_device_error", "cqsa_set_timeout_ms",
             "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes", "cqsa_attn_packed_fwd",
             "cqsa_attn_packed_bwd_workspace_size", "cqsa_attn_packed_bwd", "cqsa_kv_cache_write",
-            "cqsa_kv_cache_read", "cqsa_attn_paged_workspace_size", "cqsa_attn_paged_fwd")
+            "cqsa_kv_cache_read", "cqsa_attn_paged_workspace_size", "cqsa_attn_paged_fwd", "cqsa_kv_cache_append")
 CQSA_STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -101,6 +101,8 @@ def _load() -> ctypes.CDLL:
                                         _i, _i, _i, _vp]
     lib.cqsa_kv_cache_read.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                                        _vp]
+    lib.cqsa_kv_cache_append.argtypes = [_vp, _vp, _vp, _ll, _ll, _ll, _vp, _vp, _ll, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp,
+                                         _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]
     lib.cqsa_attn_paged_workspace_size.argtypes = [_i] * 10
     lib.cqsa_attn_paged_workspace_size.restype = ctypes.c_size_t
     lib.cqsa_attn_paged_fwd.argtypes = [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
@@ -338,6 +340,16 @@ def cqsa_kv_cache_read(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ma
                                          d, page_size, n_pages, dtype, cache_dtype, _stream(stream)))
 
 
+def cqsa_kv_cache_append(q, k, v, q_stride, k_stride, v_stride, q_out, cos_sin, max_pos, rot_dim, interleaved, k_cache, v_cache,
+                         k_scale, v_scale, block_table, max_pages, cu_seqlens, kv_lens, n_seqs, T, Hq, Hkv, d, page_size,
+                         n_pages, dtype, cache_dtype, stream=None) -> int:
+    return _check(lib.cqsa_kv_cache_append(_ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride, _ptr(q_out), _ptr(cos_sin),
+                                           max_pos, rot_dim, int(bool(interleaved)), _ptr(k_cache), _ptr(v_cache),
+                                           _ptr(k_scale), _ptr(v_scale), _ptr(block_table), max_pages, _ptr(cu_seqlens),
+                                           _ptr(kv_lens), n_seqs, T, Hq, Hkv, d, page_size, n_pages, dtype, cache_dtype,
+                                           _stream(stream)))
+
+
 def cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page_size, max_q_len, max_kv_len, dtype, cache_dtype) -> int:
     return int(lib.cqsa_attn_paged_workspace_size(n_seqs, T, Hq, Hkv, d, page_size, max_q_len, max_kv_len, dtype,
                                                   cache_dtype))
@@ -506,35 +518,49 @@ def _out(out, q):
     return out
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, dtype, device):
-    """The checks that the calls on a paged cache share; returns the cache's dtype code, n_seqs, max_pages, the three index
-    tensors and the scales' addresses."""
+def _kind(k_cache, k_scale, dtype):
+    """A cache's dtype code and head dimension: dtype's own, or for bytes e4m3 (scales [n_pages, Hkv, page_size]) or 4 bits
+    (scales [n_pages, Hkv, page_size, d / 32])."""
     torch = _tc()
-    shape, kind = k_cache.shape, k_cache.dtype
+    kind = k_cache.dtype
+    if kind == dtype:
+        return _code(dtype), k_cache.shape[3]
+    if kind == torch.uint8 and k_scale is not None and len(k_scale.shape) == 4:
+        return CQSA_INT4, 2 * k_cache.shape[3]
+    if kind == torch.uint8 or kind == torch.float8_e4m3fn:
+        return CQSA_E4M3, k_cache.shape[3]
+    raise ValueError(f"a cache of {kind} does not go with tokens of {dtype}")
+
+
+def _scale(name, t, shape, code, d, device):
+    """The scales beside a cache of that shape: their address (None for a 16-bit cache, which takes none)."""
+    if code != CQSA_E4M3 and code != CQSA_INT4:
+        if t is not None:
+            raise ValueError("a 16-bit cache takes no scales")
+        return None
+    want = shape[:3] if code == CQSA_E4M3 else (*shape[:3], d // 32)
+    if t is None or t.element_size() != 1 or t.shape != want or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous byte tensor {tuple(want)} on {device}")
+    return t.data_ptr()
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, dtype, device):
+    """The checks that the calls on a paged cache share; returns the cache's dtype code, its head dimension, n_seqs, max_pages, the
+    three index tensors and the scales' addresses."""
+    shape = k_cache.shape
     if device.type != "cuda" or k_cache.device != device or v_cache.device != device:
         raise ValueError("k_cache and v_cache must be CUDA tensors on the tokens' device")
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != kind:
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache must be tensors of one shape and dtype [n_pages, Hkv, page_size, d]")
     if not k_cache.is_contiguous() or not v_cache.is_contiguous():
         raise ValueError("k_cache and v_cache must be contiguous")
-    ks = vs = None
-    if kind == dtype:
-        code = _code(dtype)
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("a 16-bit cache takes no scales")
-    elif kind == torch.uint8 or kind == torch.float8_e4m3fn:
-        code = CQSA_E4M3
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is None or t.element_size() != 1 or t.shape != shape[:3] or t.device != device or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous byte tensor [n_pages, Hkv, page_size] beside an e4m3 cache")
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    else:
-        raise ValueError(f"a cache of {kind} does not go with tokens of {dtype}")
+    code, d = _kind(k_cache, k_scale, dtype)
+    ks, vs = _scale("k_scale", k_scale, shape, code, d, device), _scale("v_scale", v_scale, shape, code, d, device)
     table = block_table.shape
     if len(table) != 2 or kv_lens.shape != table[:1]:
         raise ValueError("block_table must be [n_seqs, max_pages] and kv_lens [n_seqs]")
     n_seqs = table[0]
-    return (code, n_seqs, table[1], _ints("block_table", block_table, table, device),
+    return (code, d, n_seqs, table[1], _ints("block_table", block_table, table, device),
             _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), device), _ints("kv_lens", kv_lens, (n_seqs,), device), ks, vs)
 
 
@@ -607,20 +633,78 @@ def attention_packed_backward(q, k, v, out, dout, lse, cu_seqlens, *, causal=Tru
 
 def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, k_scale=None, v_scale=None, stream=None):
     """New tokens k, v [T, Hkv, d] into their pages of the caches [n_pages, Hkv, page_size, d] (k's dtype, or
-    uint8 / float8_e4m3fn codes with byte tensors k_scale, v_scale [n_pages, Hkv, page_size])."""
+    uint8 / float8_e4m3fn codes with byte tensors k_scale, v_scale [n_pages, Hkv, page_size], or 4 bits: uint8
+    [n_pages, Hkv, page_size, d / 2] with byte tensors [n_pages, Hkv, page_size, d / 32])."""
     ctx = _elsewhere(k.device, stream)
     if ctx is not None:
         with ctx:
             return kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, k_scale=k_scale, v_scale=v_scale)
-    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
-                                                                kv_lens, k.dtype, k.device)
-    n_pages, Hkv, page, d = k_cache.shape
+    code, d, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                   kv_lens, k.dtype, k.device)
+    n_pages, Hkv, page = k_cache.shape[:3]
     (k, ks), (v, vs) = _tokens("k", k, Hkv, d, k), _tokens("v", v, Hkv, d, k)
     if v.shape != k.shape:
         raise ValueError("k and v must have one shape")
     _check(lib.cqsa_kv_cache_write(k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
                                    table.data_ptr(), max_pages, cu.data_ptr(), lens.data_ptr(), n_seqs, k.shape[0], Hkv, d,
                                    page, n_pages, _code(k.dtype), code, _current(k.device)))
+
+
+def rotary_table(n_positions, rot_dim, *, base=10000.0, inv_freq=None, device="cuda"):
+    """The table of cosines and sines that kv_cache_append takes, float32 [n_positions, rot_dim], its angles in 64 bits: position t
+    and pair j turn by t * base^(-2 j / rot_dim), or by t * inv_freq[j]."""
+    torch = _tc()
+    if inv_freq is None:
+        inv_freq = float(base) ** (-torch.arange(rot_dim // 2, dtype=torch.float64, device=device) * 2 / rot_dim)
+    else:
+        inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+    if rot_dim < 2 or rot_dim % 2 or inv_freq.shape != (rot_dim // 2,):
+        raise ValueError("rot_dim must be even, and inv_freq hold rot_dim / 2 values")
+    angle = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * inv_freq
+    return torch.cat([torch.cos(angle), torch.sin(angle)], -1).float()
+
+
+def kv_cache_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, interleaved=False, k_scale=None,
+                    v_scale=None, q_out=None, stream=None):
+    """kv_cache_write with the position rotation applied to the keys on the way, and to the tokens' queries q [T, Hq, d] beside them:
+    returns the rotated queries (in `q_out`, a contiguous tensor like q, or q itself where that is contiguous, if given; None where q is
+    None). cos_sin: float32 [positions, rot_dim], row t the cosines and then the sines of position t's rot_dim / 2 angles
+    (rotary_table makes it); a token at a position past it is skipped. Pairs are features j and j + rot_dim / 2, or 2 j and 2 j + 1
+    (interleaved)."""
+    torch = _tc()
+    device, dtype = k.device, k.dtype
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_cache_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens, kv_lens, interleaved=interleaved,
+                                   k_scale=k_scale, v_scale=v_scale, q_out=q_out)
+    code, d, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                   kv_lens, dtype, device)
+    n_pages, Hkv, page = k_cache.shape[:3]
+    (k, ks), (v, vs) = _tokens("k", k, Hkv, d, k), _tokens("v", v, Hkv, d, k)
+    T = k.shape[0]
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    if len(cos_sin.shape) != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != device:
+        raise ValueError(f"cos_sin must be a float32 tensor [positions, rot_dim] on {device}")
+    cos_sin = _dense(cos_sin)
+    Hq = qs = 0
+    if q is not None:
+        if len(q.shape) != 3 or q.shape[0] != T:
+            raise ValueError("q must be [T, Hq, d] with k's T")
+        Hq = q.shape[1]
+        if q_out is not None and q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():
+            raise ValueError("q_out may be q only where that is contiguous")
+        q, qs = _tokens("q", q, Hq, d, k)
+        q_out = _out(q_out, q)
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    _check(lib.cqsa_kv_cache_append(q.data_ptr() if Hq else None, k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                                    q_out.data_ptr() if Hq else None, cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                                    1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc, table.data_ptr(),
+                                    max_pages, cu.data_ptr(), lens.data_ptr(), n_seqs, T, Hq, Hkv, d, page, n_pages,
+                                    _code(dtype), code, _current(device)))
+    return q_out
 
 
 def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, *, k_scale=None, v_scale=None, out=None,
@@ -634,9 +718,9 @@ def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, 
         with ctx:
             return kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, k_scale=k_scale,
                                  v_scale=v_scale, out=out)
-    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
-                                                                kv_lens, dtype, device)
-    n_pages, Hkv, page, d = k_cache.shape
+    code, d, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                   kv_lens, dtype, device)
+    n_pages, Hkv, page = k_cache.shape[:3]
     if out is None:
         k, v = (torch.empty((T, Hkv, d), dtype=dtype, device=device) for _ in range(2))
     else:
@@ -666,9 +750,9 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
             return attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len, max_kv_len,
                                    causal=causal, scale=scale, k_scale=k_scale, v_scale=v_scale, return_lse=return_lse,
                                    out=out, workspace=workspace)
-    code, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
-                                                                kv_lens, dtype, device)
-    n_pages, Hkv, page, d = k_cache.shape
+    code, d, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                   kv_lens, dtype, device)
+    n_pages, Hkv, page = k_cache.shape[:3]
     if len(q.shape) != 3:
         raise ValueError("q must be [T, Hq, d]")
     T, Hq = q.shape[:2]

@@ -109,7 +109,7 @@ struct CacheArgs {
   void* v_out;
   void* k_cache;        // [n_pages, Hkv, page, d]
   void* v_cache;
-  unsigned char* k_scale;  // e4m3: [n_pages, Hkv, page] exponent bytes
+  unsigned char* k_scale;  // e4m3: [n_pages, Hkv, page] exponent bytes; 4 bits: [n_pages, Hkv, page, d / 32] scales
   unsigned char* v_scale;
   const int* table;     // [n_seqs, max_pages]
   const int* cu;
@@ -118,6 +118,15 @@ struct CacheArgs {
   int n_seqs, T, Hkv, d, page, n_pages, max_pages, dtype, cache_dtype;
 };
 int launch_kv_cache(const CacheArgs& a, bool write, cudaStream_t stream);
+// What appending adds to writing: the queries, and the rotation.
+struct AppendArgs {
+  const void* q;        // [T, Hq, d], q_stride elements from token to token (Hq 0: none)
+  void* q_out;          // [T, Hq, d]
+  const float* cos_sin; // [max_pos, rot]: cosines of rot / 2 pairs, then their sines
+  long long q_stride, max_pos;
+  int Hq, rot, interleaved;
+};
+int launch_kv_append(const CacheArgs& a, const AppendArgs& r, cudaStream_t stream);
 
 struct PagedArgs {
   const void* q;        // [T, Hq, d]

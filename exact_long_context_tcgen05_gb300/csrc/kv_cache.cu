@@ -22,28 +22,36 @@ namespace {
 
 constexpr int kWarps = 4;    // warps (tokens) of a block
 constexpr int kAhead = 4;    // steps whose loads, of K and of V, are in flight
+constexpr int kAppendWarps = 8;  // warps of an appending block
 
-// Where token `token` of the packed tensor lives: its vectors' index at head 0 (a head is `page` vectors
-// further), -1 for a token of no sequence, -2 for a position below zero or beyond the table, or (writing) a
-// page outside the cache.
-__device__ __forceinline__ long long cache_row(const CacheArgs& a, int token, int lane, bool writing) {
+enum : int { kCacheSame = 0, kCacheE4m3 = 1, kCacheInt4 = 2 };
+
+// The sequence of token `token` of the packed tensor and its position there; false for a token of no sequence.
+__device__ __forceinline__ bool find_token(const CacheArgs& a, int token, int lane, int* seq, long long* pos) {
   int s, first, n, len;
   if (a.n_seqs <= 32) {
     const int k = min(lane, a.n_seqs - 1);
     const int c0 = cu_at(a.cu, k, a.T), c1 = cu_at(a.cu, k + 1, a.T), L = __ldg(a.kv_lens + k);
     const unsigned has = __ballot_sync(0xffffffffu, lane < a.n_seqs && c0 <= token && token < c1);
-    if (!has) return -1;
+    if (!has) return false;
     s = 31 - __clz(has);
     first = __shfl_sync(0xffffffffu, c0, s);
     n = __shfl_sync(0xffffffffu, c1, s) - first;
     len = __shfl_sync(0xffffffffu, L, s);
   } else {
     s = seq_of_token(a.cu, a.n_seqs, a.T, token, lane);
-    if (s < 0) return -1;
+    if (s < 0) return false;
     len = __ldg(a.kv_lens + s);
     n = seq_tokens(a.cu, s, a.T, &first);
   }
-  const long long pos = static_cast<long long>(len) - n + (token - first);
+  *seq = s;
+  *pos = static_cast<long long>(len) - n + (token - first);
+  return true;
+}
+
+// Where position `pos` of sequence s lives: its vectors' index at head 0 (a head is `page` vectors further), -2 for a
+// position below zero or beyond the table, or (writing) a page outside the cache.
+__device__ __forceinline__ long long row_of(const CacheArgs& a, int s, long long pos, bool writing) {
   if (pos < 0 || pos >= static_cast<long long>(a.max_pages) * a.page) return -2;
   const int page_log2 = 31 - __clz(a.page), slot = static_cast<int>(pos) & (a.page - 1);
   const int p = __ldg(a.table + static_cast<long long>(s) * a.max_pages + (static_cast<int>(pos) >> page_log2));
@@ -54,7 +62,73 @@ __device__ __forceinline__ long long cache_row(const CacheArgs& a, int token, in
   return ((static_cast<long long>(p) * a.Hkv) << page_log2) + slot;
 }
 
-template <int D, int BF16, bool E4M3>
+// The same for token `token` of the packed tensor; -1 for a token of no sequence.
+__device__ __forceinline__ long long cache_row(const CacheArgs& a, int token, int lane, bool writing) {
+  int s;
+  long long pos;
+  return find_token(a, token, lane, &s, &pos) ? row_of(a, s, pos, writing) : -1;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& x, int bf16, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack16(w[i], bf16);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+// A vector into a quantised cache: lane c of its LPV lanes holds features 8 c .. 8 c + 7. The whole warp calls; `on`: this lane's
+// vector is to be written, at vector index `at`.
+template <int KIND, int LPV>
+__device__ __forceinline__ void put_vector(uint8_t* cache, uint8_t* scale, long long at, int c, bool on, float (&f)[8]) {
+  float amax = 0.0f;
+  if (KIND == kCacheE4m3) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float m = fabsf(f[i]);
+      const bool finite = m < INFINITY;
+      amax = fmaxf(amax, finite ? m : 0.0f);
+      if (!finite) f[i] = NAN;
+    }
+#pragma unroll
+    for (int o = LPV / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const int e = e4m3_exponent(amax);
+    const float inv = pow2i(-e);
+    uint2 codes;
+    codes.x = to_e4m3x2(f[0] * inv, f[1] * inv) | (to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
+    codes.y = to_e4m3x2(f[4] * inv, f[5] * inv) | (to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
+    if (on) {
+      reinterpret_cast<uint2*>(cache)[at * LPV + c] = codes;
+      if (c == 0) scale[at] = static_cast<uint8_t>(e + 127);
+    }
+  } else {
+    // four lanes hold the 32 features of a scale
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float m = fabsf(f[i]);
+      amax = fmaxf(amax, m < INFINITY ? m : INFINITY);  // (NaN counts as infinity)
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint32_t b = int4_scale_byte(amax);
+    const float unit = int4_scale(b);
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = min(max(__float2int_rn(__fdiv_rn(f[i], unit)), -7), 7);
+      word |= static_cast<uint32_t>(q + 8) << (4 * i);
+    }
+    if (b == 255u) word = 0x88888888u;
+    if (on) {
+      reinterpret_cast<uint32_t*>(cache)[at * LPV + c] = word;
+      if ((c & 3) == 0) scale[at * (LPV / 4) + (c >> 2)] = static_cast<uint8_t>(b);
+    }
+  }
+}
+
+template <int D, int BF16, int KIND>
 __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheArgs a) {
   constexpr int LPV = D / 8;        // lanes of a vector
   constexpr int HPS = 32 / LPV;     // heads of a step
@@ -85,41 +159,18 @@ __global__ void __launch_bounds__(32 * kWarps) cache_write_kernel(const CacheArg
         const int h = h0 + u * HPS + hl;
         const long long at = row + static_cast<long long>(h) * a.page;
         uint8_t* cache = static_cast<uint8_t*>(kv ? a.v_cache : a.k_cache);
-        if (!E4M3) {
+        if constexpr (KIND == kCacheSame) {
           if (h < a.Hkv) reinterpret_cast<uint4*>(cache)[at * LPV + c] = x[kv][u];
-          continue;
-        }
-        const uint32_t w[4] = {x[kv][u].x, x[kv][u].y, x[kv][u].z, x[kv][u].w};
-        float f[8], amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 p = unpack16(w[i], BF16);
-          f[2 * i] = p.x;
-          f[2 * i + 1] = p.y;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float m = fabsf(f[i]);
-          const bool finite = m < INFINITY;
-          amax = fmaxf(amax, finite ? m : 0.0f);
-          if (!finite) f[i] = NAN;
-        }
-#pragma unroll
-        for (int o = LPV / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const int e = e4m3_exponent(amax);
-        const float inv = pow2i(-e);
-        uint2 codes;
-        codes.x = to_e4m3x2(f[0] * inv, f[1] * inv) | (to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
-        codes.y = to_e4m3x2(f[4] * inv, f[5] * inv) | (to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
-        if (h < a.Hkv) {
-          reinterpret_cast<uint2*>(cache)[at * LPV + c] = codes;
-          if (c == 0) (kv ? a.v_scale : a.k_scale)[at] = static_cast<uint8_t>(e + 127);
+        } else {
+          float f[8];
+          unpack8(x[kv][u], BF16, f);
+          put_vector<KIND, LPV>(cache, kv ? a.v_scale : a.k_scale, at, c, h < a.Hkv, f);
         }
       }
   }
 }
 
-template <int D, int BF16, bool E4M3>
+template <int D, int BF16, int KIND>
 __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs a) {
   constexpr int LPV = D / 8;
   constexpr int HPS = 32 / LPV;
@@ -142,7 +193,10 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs
         x[kv][u] = make_uint4(0, 0, 0, 0);
         e[kv][u] = 0;
         if (h < a.Hkv && row >= 0) {
-          if (E4M3) {
+          if (KIND == kCacheInt4) {
+            x[kv][u].x = __ldg(reinterpret_cast<const uint32_t*>(cache) + at * LPV + c);
+            e[kv][u] = __ldg((kv ? a.v_scale : a.k_scale) + at * (LPV / 4) + (c >> 2));
+          } else if (KIND == kCacheE4m3) {
             const uint2 w = __ldg(reinterpret_cast<const uint2*>(cache) + at * LPV + c);
             x[kv][u].x = w.x;
             x[kv][u].y = w.y;
@@ -159,7 +213,18 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs
         const int h = h0 + u * HPS + hl;
         uint16_t* dst = static_cast<uint16_t*>(kv ? a.v_out : a.k_out) + token * (static_cast<long long>(a.Hkv) * D);
         uint4 y = x[kv][u];
-        if (E4M3) {
+        if (KIND == kCacheInt4) {
+          // whole number * scale: 7 significant bits at most, exact in either 16-bit type
+          const float s = int4_scale(static_cast<uint32_t>(e[kv][u]));
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(static_cast<int>((y.x >> (4 * i)) & 15u) - 8) * s;
+          if (!BF16) {  // (7 * 61,440: values past fp16's largest read as the largest)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = f[i] > 65504.0f ? 65504.0f : (f[i] < -65504.0f ? -65504.0f : f[i]);
+          }
+          y = make_uint4(pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
+        } else if (KIND == kCacheE4m3) {
           // code * 2^e: exact in fp32 but for its subnormals, then one rounding to 16 bits
           const float s = exp2_byte(static_cast<uint32_t>(e[kv][u]));
           const uint32_t w[4] = {y.x & 0xffffu, y.x >> 16, y.y & 0xffffu, y.y >> 16};
@@ -187,26 +252,147 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs
   }
 }
 
-template <int D, int BF16>
-int launch_d(const CacheArgs& a, bool write, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + kWarps - 1) / kWarps));
-  if (write) {
-    if (a.cache_dtype == CQSA_E4M3) cache_write_kernel<D, BF16, true><<<grid, 32 * kWarps, 0, stream>>>(a);
-    else cache_write_kernel<D, BF16, false><<<grid, 32 * kWarps, 0, stream>>>(a);
-  } else {
-    if (a.cache_dtype == CQSA_E4M3) cache_read_kernel<D, BF16, true><<<grid, 32 * kWarps, 0, stream>>>(a);
-    else cache_read_kernel<D, BF16, false><<<grid, 32 * kWarps, 0, stream>>>(a);
+// New tokens into their pages with the position rotation applied on the way, and their queries rotated beside them. A pair
+// (x, y) of a token's first `rot` features turns by its position's angle: x cos - y sin, y cos + x sin, each product and sum rounded once
+// in 32 bits (no fused multiply-add), so that the result is the same as from elementary operations in any program.
+//
+// wpt warps share a token: its Hq + 2 Hkv vectors, 16 bytes of 16-bit data a lane as above. Paired features that lie in different
+// lanes (the first half of the rotated ones with the second) are exchanged as they were loaded, four shuffles a vector, which leaves
+// every lane its own 8 features, whatever `rot` is, and quantising as it is for a plain write. The data's loads go out first, then
+// come sequence and position, then the row of the table of cosines and sines beside the page.
+template <int D, int BF16, int KIND>
+__global__ void __launch_bounds__(32 * kAppendWarps) cache_append_kernel(const CacheArgs a, const AppendArgs r, int wpt) {
+  constexpr int LPV = D / 8, VPS = 32 / LPV, AHEAD = 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long token = static_cast<long long>(blockIdx.x) * (kAppendWarps / wpt) + warp / wpt;
+  if (token >= a.T) return;
+  const int part = warp & (wpt - 1), hl = lane / LPV, c = lane % LPV;
+  const int nv = r.Hq + 2 * a.Hkv, step = wpt * VPS;
+  const uint16_t* q = static_cast<const uint16_t*>(r.q) + token * r.q_stride;
+  const uint16_t* k = static_cast<const uint16_t*>(a.k) + token * a.k_stride;
+  const uint16_t* v = static_cast<const uint16_t*>(a.v) + token * a.v_stride;
+  uint4 x[AHEAD];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int i = i0 + u * step;
+      const uint16_t* from = i < r.Hq ? q + i * D : (i < r.Hq + a.Hkv ? k + (i - r.Hq) * D : v + (i - r.Hq - a.Hkv) * D);
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (i < nv) x[u] = *(reinterpret_cast<const uint4*>(from) + c);  // (q_out may be q: not through the read-only path)
+    }
+  };
+  load(part * VPS + hl);
+  int s;
+  long long pos;
+  if (!find_token(a, static_cast<int>(token), lane, &s, &pos)) return;  // behind the last sequence: left as it was
+  if (pos < 0 || pos >= r.max_pos) return;
+  const long long row = row_of(a, s, pos, true);
+  // this lane's cosines and sines, the sine's sign for its place in the pair
+  const int half = r.rot >> 1;
+  const bool turns = 8 * c < r.rot;
+  float cs[8], sn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = sn[i] = 0.0f;
+  int from = lane;  // where the other of each pair is
+  if (turns) {
+    const float* at = r.cos_sin + pos * r.rot;
+    if (r.interleaved) {
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(at + 4 * c)), s4 = __ldg(reinterpret_cast<const float4*>(at + half + 4 * c));
+      const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cs[i] = cc[i >> 1];
+        sn[i] = i & 1 ? ss[i >> 1] : -ss[i >> 1];
+      }
+    } else {
+      const bool second = 8 * c >= half;
+      const int j = second ? 8 * c - half : 8 * c;
+      from = second ? lane - (half >> 3) : lane + (half >> 3);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(at + j) + i), s4 = __ldg(reinterpret_cast<const float4*>(at + half + j) + i);
+        cs[4 * i] = c4.x; cs[4 * i + 1] = c4.y; cs[4 * i + 2] = c4.z; cs[4 * i + 3] = c4.w;
+        sn[4 * i] = s4.x; sn[4 * i + 1] = s4.y; sn[4 * i + 2] = s4.z; sn[4 * i + 3] = s4.w;
+      }
+      if (!second) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+      }
+    }
   }
+  for (int i0 = part * VPS; i0 < nv; i0 += AHEAD * step) {
+    if (i0 != part * VPS) load(i0 + hl);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      if (i0 + u * step >= nv) break;  // (the same for the whole warp)
+      const int i = i0 + u * step + hl;
+      const bool is_q = i < r.Hq, is_v = i >= r.Hq + a.Hkv, on = i < nv;
+      const int h = is_q ? i : (is_v ? i - r.Hq - a.Hkv : i - r.Hq);
+      float f[8], g[8];
+      unpack8(x[u], BF16, f);
+      if (r.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = f[e ^ 1];
+      } else {
+        uint4 y;
+        y.x = __shfl_sync(0xffffffffu, x[u].x, from);
+        y.y = __shfl_sync(0xffffffffu, x[u].y, from);
+        y.z = __shfl_sync(0xffffffffu, x[u].z, from);
+        y.w = __shfl_sync(0xffffffffu, x[u].w, from);
+        unpack8(y, BF16, g);
+      }
+      const bool turn = turns && !is_v;  // (what does not turn is left alone: 0 times an infinity beside it would not be)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = turn ? __fadd_rn(__fmul_rn(f[e], cs[e]), __fmul_rn(g[e], sn[e])) : f[e];
+      const uint4 y = make_uint4(pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
+      if (is_q) *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.q_out) + (token * r.Hq + h) * D) + c) = turn ? y : x[u];
+      if (i0 + u * step + VPS <= r.Hq) continue;  // queries only (the same for the whole warp)
+      const bool put = on && !is_q && row >= 0;
+      const long long at = row + static_cast<long long>(h) * a.page;
+      uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache);
+      if constexpr (KIND == kCacheSame) {
+        if (put) reinterpret_cast<uint4*>(cache)[at * LPV + c] = turn ? y : x[u];
+      } else {
+        put_vector<KIND, LPV>(cache, is_v ? a.v_scale : a.k_scale, at, c, put, f);
+      }
+    }
+  }
+}
+
+template <int D, int BF16, int KIND>
+int launch_t(const CacheArgs& a, const AppendArgs* r, bool write, cudaStream_t stream) {
+  if (r) {
+    // A token's chain of loads (counts, position, page and table row) is what a small step takes: its vectors then go to as
+    // many warps as there are; with many tokens two warps each keep the loads in flight that memory wants.
+    const int wpt = a.T <= 2 * sm_count() ? kAppendWarps : 2, per = kAppendWarps / wpt;
+    const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + per - 1) / per));
+    cache_append_kernel<D, BF16, KIND><<<grid, 32 * kAppendWarps, 0, stream>>>(a, *r, wpt);
+    return cuda_status(cudaGetLastError(), "cache append kernel launch");
+  }
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + kWarps - 1) / kWarps));
+  if (write) cache_write_kernel<D, BF16, KIND><<<grid, 32 * kWarps, 0, stream>>>(a);
+  else cache_read_kernel<D, BF16, KIND><<<grid, 32 * kWarps, 0, stream>>>(a);
   return cuda_status(cudaGetLastError(), write ? "cache write kernel launch" : "cache read kernel launch");
+}
+
+template <int D, int BF16>
+int launch_d(const CacheArgs& a, const AppendArgs* r, bool write, cudaStream_t stream) {
+  if (a.cache_dtype == CQSA_E4M3) return launch_t<D, BF16, kCacheE4m3>(a, r, write, stream);
+  if (a.cache_dtype == CQSA_INT4) return launch_t<D, BF16, kCacheInt4>(a, r, write, stream);
+  return launch_t<D, BF16, kCacheSame>(a, r, write, stream);
+}
+
+int launch(const CacheArgs& a, const AppendArgs* r, bool write, cudaStream_t stream) {
+  if (a.T == 0) return CQSA_OK;
+  const bool bf = a.dtype == CQSA_BF16;
+  if (a.d == 64) return bf ? launch_d<64, 1>(a, r, write, stream) : launch_d<64, 0>(a, r, write, stream);
+  return bf ? launch_d<128, 1>(a, r, write, stream) : launch_d<128, 0>(a, r, write, stream);
 }
 
 }  // namespace
 
-int launch_kv_cache(const CacheArgs& a, bool write, cudaStream_t stream) {
-  if (a.T == 0) return CQSA_OK;
-  const bool bf = a.dtype == CQSA_BF16;
-  if (a.d == 64) return bf ? launch_d<64, 1>(a, write, stream) : launch_d<64, 0>(a, write, stream);
-  return bf ? launch_d<128, 1>(a, write, stream) : launch_d<128, 0>(a, write, stream);
-}
+int launch_kv_cache(const CacheArgs& a, bool write, cudaStream_t stream) { return launch(a, nullptr, write, stream); }
+
+int launch_kv_append(const CacheArgs& a, const AppendArgs& r, cudaStream_t stream) { return launch(a, &r, true, stream); }
 
 }  // namespace cqsa

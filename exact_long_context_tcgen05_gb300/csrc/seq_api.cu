@@ -129,11 +129,11 @@ int check_cache(int Hkv, const void* k_cache, const void* v_cache, const void* k
     set_error("n_pages * Hkv = %lld is too large (2^31 - 1 at most)", static_cast<long long>(n_pages) * Hkv);
     return CQSA_ERR_UNSUPPORTED;
   }
-  if (cache_dtype == CQSA_E4M3) {
-    if (!k_scale || !v_scale) return invalid("an e4m3 cache needs k_scale and v_scale");
+  if (cache_dtype == CQSA_E4M3 || cache_dtype == CQSA_INT4) {
+    if (!k_scale || !v_scale) return invalid("an e4m3 or 4-bit cache needs k_scale and v_scale");
     if (!aligned(k_scale, 16) || !aligned(v_scale, 16)) return invalid("k_scale and v_scale must be 16-byte aligned");
   } else if (cache_dtype != dtype) {
-    set_error("cache_dtype %d must be the tokens' dtype or CQSA_E4M3", cache_dtype);
+    set_error("cache_dtype %d must be the tokens' dtype, CQSA_E4M3 or CQSA_INT4", cache_dtype);
     return CQSA_ERR_UNSUPPORTED;
   }
   return CQSA_OK;
@@ -287,6 +287,44 @@ int cqsa_kv_cache_write(const void* k, const void* v, long long k_stride, long l
   return launch_kv_cache(a, true, stream);
 }
 
+int cqsa_kv_cache_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride, long long v_stride,
+                         void* q_out, const float* cos_sin, long long max_pos, int rot_dim, int interleaved, void* k_cache,
+                         void* v_cache, unsigned char* k_scale, unsigned char* v_scale, const int* block_table, int max_pages,
+                         const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int Hq, int Hkv, int d, int page_size,
+                         int n_pages, int dtype, int cache_dtype, cudaStream_t stream) {
+  set_error("%s", "");
+  CacheArgs a;
+  int rc = cache_args(&a, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, cu_seqlens, kv_lens, n_seqs, T, Hkv,
+                      d, page_size, n_pages, dtype, cache_dtype);
+  if (rc != CQSA_OK) return rc;
+  if (Hq < 0 || Hq > 1 << 20 || Hkv > 1 << 20 || static_cast<long long>(T) * Hq > 0x7fffffffLL) {
+    set_error("Hq = %d, Hkv = %d: heads must be at most 2^20, Hq not negative, and T * Hq below 2^31", Hq, Hkv);
+    return CQSA_ERR_INVALID;
+  }
+  if (rot_dim < 16 || rot_dim > d || rot_dim % 16) {
+    set_error("rot_dim = %d must be a multiple of 16 from 16 to the head dim", rot_dim);
+    return CQSA_ERR_INVALID;
+  }
+  if (max_pos < 1 || max_pos > 0x7fffffffLL) return invalid("max_pos must be from 1 to 2^31 - 1");
+  if (!cos_sin || !aligned(cos_sin, 16)) return invalid("cos_sin must be a non-null 16-byte aligned device pointer");
+  if (Hq > 0) rc = resolve_stride(&q_stride, Hq, d, "q");
+  if (rc == CQSA_OK) rc = resolve_stride(&k_stride, Hkv, d, "k");
+  if (rc == CQSA_OK) rc = resolve_stride(&v_stride, Hkv, d, "v");
+  if (rc != CQSA_OK) return rc;
+  if (T > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16)))
+    return invalid("k and v must be non-null 16-byte aligned device pointers");
+  if (T > 0 && Hq > 0 && (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16)))
+    return invalid("q and q_out must be non-null 16-byte aligned device pointers");
+  if (q == q_out && Hq > 0 && T > 0 && q_stride != static_cast<long long>(Hq) * d)
+    return invalid("q_out may be q only where q's tokens lie end to end");
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  const AppendArgs r = {q, q_out, cos_sin, q_stride, max_pos, Hq, rot_dim, interleaved != 0};
+  return launch_kv_append(a, r, stream);
+}
+
 int cqsa_kv_cache_read(void* k, void* v, const void* k_cache, const void* v_cache, const unsigned char* k_scale,
                        const unsigned char* v_scale, const int* block_table, int max_pages, const int* cu_seqlens,
                        const int* kv_lens, int n_seqs, int T, int Hkv, int d, int page_size, int n_pages, int dtype,
@@ -320,6 +358,10 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
   set_error("%s", "");
   int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
   if (rc == CQSA_OK) rc = check_cache(Hkv, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page_size, n_pages, dtype, cache_dtype);
+  if (rc == CQSA_OK && cache_dtype == CQSA_INT4) {
+    set_error("attention over a 4-bit cache is not supported");
+    rc = CQSA_ERR_UNSUPPORTED;
+  }
   if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
   if (rc != CQSA_OK) return rc;
   if (!cu_seqlens || !kv_lens || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))

@@ -153,6 +153,19 @@ __device__ __forceinline__ float exp2_byte(uint32_t b) {
   return __uint_as_float(b ? b << 23 : 0x400000u);
 }
 
+// 4 bits: whole numbers -7 to 7 (kept + 8) times a scale for 32 neighbouring features, (1 + m / 8) 2^(e - 15) for its byte
+// 8 e + m (fp16's bits below the sign, but for the lower mantissa): the largest |x| over 7, rounded to nearest even. Four significant
+// bits of a scale keep every product with a whole number exact in 16 bits. The byte of a group with a value that is
+// not finite is 255, a NaN.
+constexpr uint32_t kInt4Least = 0x38800000u, kInt4Most = 0x47700000u;  // 2^-14 and 1.875 * 2^15
+__device__ __forceinline__ uint32_t int4_scale_byte(float amax) {
+  if (!(amax < INFINITY)) return 255u;
+  uint32_t u = __float_as_uint(__fdiv_rn(amax, 7.0f));
+  u += 0x7ffffu + ((u >> 20) & 1u);
+  return (min(max(u, kInt4Least), kInt4Most) >> 20) - (112u << 3);
+}
+__device__ __forceinline__ float int4_scale(uint32_t b) { return b >= 248u ? NAN : __uint_as_float((b << 20) + (112u << 23)); }
+
 // Two floats to two e4m3 codes (the first in the low byte), rounded to nearest even.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t r;

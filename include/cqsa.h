@@ -48,7 +48,7 @@ typedef enum {
                                 (see cqsa_device_error) */
 } cqsa_status;
 
-typedef enum { CQSA_F16 = 0, CQSA_BF16 = 1, CQSA_F32 = 2 /* outputs only */, CQSA_E4M3 = 3 /* caches only */ } cqsa_dtype;
+typedef enum { CQSA_F16 = 0, CQSA_BF16 = 1, CQSA_F32 = 2 /* outputs only */, CQSA_E4M3 = 3 /* caches only */, CQSA_INT4 = 4 /* caches only */ } cqsa_dtype;
 typedef enum { CQSA_LAYOUT_BHND = 0, CQSA_LAYOUT_BNHD = 1 } cqsa_layout;
 
 /*
@@ -358,7 +358,11 @@ int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, vo
  * block_table[s][t / page_size]. cache_dtype: dtype itself, or CQSA_E4M3: each vector is e4m3 codes times one
  * power of two, 2^(b - 127) for its byte b in k_scale / v_scale (device [n_pages, Hkv, page_size], 16-byte
  * aligned; ignored otherwise). The power is the smallest (at least 2^-126) under which the vector's largest finite magnitude is
- * at most 448; codes are rounded to nearest even; an infinity becomes NaN. kv_lens: device int32 [n_seqs], the
+ * at most 448; codes are rounded to nearest even; an infinity becomes NaN. Or CQSA_INT4: caches of [n_pages, Hkv, page_size, d / 2]
+ * bytes, scales [n_pages, Hkv, page_size, d / 32]. 32 neighbouring features share a scale, their largest magnitude / 7 rounded to
+ * nearest even to 4 significant bits and held to [2^-14, 61440]; its byte 8 e + m stands for (1 + m / 8) 2^(e - 15). A value is the nearest (even)
+ * whole multiple of it, held to -7 .. 7; a byte holds the multiples + 8 of two neighbouring features, the first in its low four bits. A group with a value that
+ * is not finite has the byte 255, and reads as NaN. kv_lens: device int32 [n_seqs], the
  * positions of each sequence, its new tokens included: token i of a sequence's n new tokens has position
  * kv_lens[s] - n + i. Slots past a sequence's length may hold anything. Pages may be shared between
  * sequences as long as no two tokens of one write go to the same slot.
@@ -400,6 +404,19 @@ int cqsa_kv_cache_write(const void* k, const void* v, long long k_stride, long l
                         unsigned char* k_scale, unsigned char* v_scale, const int* block_table, int max_pages,
                         const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int Hkv, int d, int page_size,
                         int n_pages, int dtype, int cache_dtype, cudaStream_t stream);
+
+/* The same with the position rotation applied on the way, for the new tokens' keys and, beside them, their queries: of a vector's first
+ * rot_dim features (a multiple of 16, 16 to d) the pairs j and j + rot_dim / 2 (interleaved: 2 j and 2 j + 1) turn by their
+ * position's angle, (x, y) -> (x c - y s, y c + x s). cos_sin: device fp32 [max_pos, rot_dim], 16-byte aligned, row t the cosines of position t's rot_dim / 2
+ * angles, then their sines. q device [T, Hq, d], q_out device [T, Hq, d] contiguous (it may be q, where that is contiguous); Hq = 0: no queries.
+ * Products and sums are rounded in 32 bits one by one, the result once to dtype, or into the cache's code. v is written as it is.
+ * A token whose position is negative or not below max_pos is skipped, its row of q_out too; one that has no slot (as above) has its query
+ * rotated all the same. */
+int cqsa_kv_cache_append(const void* q, const void* k, const void* v, long long q_stride, long long k_stride, long long v_stride,
+                         void* q_out, const float* cos_sin, long long max_pos, int rot_dim, int interleaved, void* k_cache,
+                         void* v_cache, unsigned char* k_scale, unsigned char* v_scale, const int* block_table, int max_pages,
+                         const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int Hq, int Hkv, int d, int page_size,
+                         int n_pages, int dtype, int cache_dtype, cudaStream_t stream);
 
 /* The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence back out of the cache (all of them where
  * that is kv_lens[s]): k, v device [T, Hkv, d], written in dtype; e4m3 values are rounded to dtype once, and finite ones past its
