@@ -14,6 +14,7 @@ namespace cqsa {
 int device_error_word(DevErr* out, int clear);  // attn_fwd.cu (owns the forward's device word)
 int bwd_error_word(DevErr* out, int clear);     // attn_bwd.cu (the backward's)
 int decode_error_word(DevErr* out, int clear);  // attn_decode.cu
+int decode4_error_word(DevErr* out, int clear);  // attn_decode4.cu
 int seq_error_word(DevErr* out, int clear);     // attn_seq.cu
 int device_error_word_on(DevErr* out, cudaStream_t s);  // read on one stream; cleared when set
 int bwd_error_word_on(DevErr* out, cudaStream_t s);
@@ -148,7 +149,7 @@ int cqsa_device_error(int* code, int* block, int clear) {
   DevErr e;
   int rc = cuda_status(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
   if (rc != CQSA_OK) return rc;
-  int (*const words[])(DevErr*, int) = {device_error_word, bwd_error_word, decode_error_word, seq_error_word};
+  int (*const words[])(DevErr*, int) = {device_error_word, bwd_error_word, decode_error_word, decode4_error_word, seq_error_word};
   for (auto word : words) {
     rc = word(&e, clear);
     if (rc != CQSA_OK) return rc;

@@ -32,6 +32,7 @@
 
 #include "attn_common.cuh"
 #include "cqsa_internal.h"
+#include "decode_common.cuh"
 #include "seq_common.cuh"
 #include "sm103_ptx.cuh"
 
@@ -39,11 +40,6 @@ namespace cqsa {
 namespace {
 
 __device__ DevErr g_decode_err;
-
-constexpr int kQuarters = 4;  // warps that share a tile's keys
-// Probabilities are kept as 2^14 p (and so are their sums): fp16 holds them without loss of relative precision
-// down to p = 2^-28, where plain p would turn subnormal at 2^-14.
-constexpr float kPShift = 14.0f;
 
 constexpr int decode_occ(bool e4m3, int nmt) { return e4m3 && nmt == 1 ? 2 : 1; }
 
@@ -70,50 +66,6 @@ struct DecCfg {
   static_assert(SMEM <= 232448, "shared memory exceeds 227 KiB");
 };
 
-struct DecParams {
-  const void* q;
-  void* out;
-  float* lse;
-  float* part_o;  // [2 * CTAs][16 * NMT][D]
-  float* part_l;  // [2 * CTAs][16 * NMT], base 2
-  int4* meta;     // [CTAs][2] the unit a CTA's range begins in the middle of: sequence (-1: none), head, first and last
-                  // CTA of it; the sequence's first token and tokens
-  const int* table;
-  const int* cu;
-  const int* kv_lens;
-  const uint8_t* k_scale;
-  const uint8_t* v_scale;
-  long long q_stride;
-  int n_seqs, T, Hq, Hkv, G, max_pages, n_pages, page_log2, causal;
-  float scale_log2;
-  unsigned timeout_us;
-  int fault;  // test hook: 1 = the first key tile of sequence 0 and head 0 is never loaded
-};
-
-__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
-}
-template <int BF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if (BF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Byte offset of 16-byte chunk c of row r of a tile of ROWB-byte rows as TMA's 128-byte (64-byte for
 // 64-byte rows) swizzle lays it down.
 template <int ROWB>
@@ -127,50 +79,6 @@ __device__ __forceinline__ uint32_t sw_off(int r, int c) {
 template <int D>
 __device__ __forceinline__ uint32_t tile16_off(int r, int c) {
   return static_cast<uint32_t>((r >> 3) * (1024 * (D / 64)) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
-// A unit counts as its key tiles and kUnit more: what its queries' loads and the joining of its rows cost. Without them
-// a CTA that gets many short sequences finishes late (128 ragged sequences of e4m3: the last CTA at 311 us, the mean at 231).
-constexpr int kUnit = 2;
-
-// Where a CTA's walk over its range stands: sequence, the length of each of its units, tokens and positions.
-struct Walk {
-  int s, n, qlen, first, len;
-  long long base;  // where the sequence's first unit begins
-};
-
-// What a range [w, w1) does in the unit it stands in: head, and key tiles [t0, t1) (none when it only reaches into the
-// unit's kUnit). `next`: where the unit (or the range) ends.
-struct Piece {
-  int h, t0, t1;
-  long long next;
-};
-__device__ __forceinline__ Piece piece_at(const Walk& k, long long w, long long w1) {
-  Piece r;
-  const long long rel = w - k.base;
-  r.h = static_cast<int>(rel / k.n);
-  const long long u0 = k.base + static_cast<long long>(r.h) * k.n;
-  r.next = min(u0 + k.n, w1);
-  r.t0 = max(0, static_cast<int>(w - u0) - kUnit);
-  r.t1 = max(0, static_cast<int>(r.next - u0) - kUnit);
-  return r;
-}
-
-template <int KT>
-__device__ __forceinline__ void walk_load(const DecParams& p, Walk& w) {
-  w.qlen = seq_tokens(p.cu, w.s, p.T, &w.first);
-  w.len = seq_positions(p.kv_lens, w.s, static_cast<long long>(p.max_pages) << p.page_log2);
-  // a sequence without new tokens is no work; one without positions is one empty tile (its rows are zero)
-  w.n = w.qlen == 0 ? 0 : max(1, (w.len + KT - 1) / KT) + kUnit;
-}
-template <int KT>
-__device__ __forceinline__ void walk_next(const DecParams& p, Walk& w) {
-  do {
-    w.base += static_cast<long long>(w.n) * p.Hkv;
-    ++w.s;
-    if (w.s >= p.n_seqs) return;
-    walk_load<KT>(p, w);
-  } while (w.n == 0);
 }
 
 template <int D, int BF16, bool E4M3, int NMT>
@@ -187,8 +95,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
   uint64_t* empty = full + NST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NST);
   long long* s_base = reinterpret_cast<long long*>(empty + NST + 1);
-  long long* s_sum = s_base + 1;  // total tiles
-  int* s_seq = reinterpret_cast<int*>(s_sum + 1);
+  int* s_seq = reinterpret_cast<int*>(s_base + 1);
   long long* s_warp = reinterpret_cast<long long*>(s_seq + 2);  // [32]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -201,65 +108,8 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
     *s_seq = -1;
     fence_mbar_init();
   }
-  // the tiles of all sequences, and the sequence this CTA's range begins in
-  auto tiles_of = [&](int s) -> long long {
-    if (s >= p.n_seqs) return 0;
-    Walk w;
-    w.s = s;
-    walk_load<KT>(p, w);
-    return static_cast<long long>(w.n) * p.Hkv;
-  };
-  constexpr int NW = NTHR / 32;
-  auto block_scan = [&](long long v, long long* before) -> long long {  // total; *before: sum over lower threads
-    long long x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    long long b = 0, t = 0;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      if (i < warp) b += s_warp[i];
-      t += s_warp[i];
-    }
-    *before = b + x - v;
-    return t;
-  };
-  long long mine, before;
-  {
-    Walk w;
-    w.s = tid;
-    w.n = 0;
-    if (tid < p.n_seqs) walk_load<KT>(p, w);
-    mine = static_cast<long long>(w.n) * p.Hkv;
-  }
-  long long W = block_scan(mine, &before);  // the first NTHR sequences
-  const long long W_first = W;
-  long long unused;
-  for (int s0 = NTHR; s0 < p.n_seqs; s0 += NTHR) W += block_scan(tiles_of(s0 + tid), &unused);
-  // every range holds a tile: with fewer tiles than CTAs (sequences shorter than the caller said) the last CTAs idle
-  const long long nc = min(static_cast<long long>(gridDim.x), W);
-  const long long bx = blockIdx.x;
-  const long long w0 = bx < nc ? W * bx / nc : 0, w1 = bx < nc ? W * (bx + 1) / nc : 0;
-  if (w0 < w1 && before <= w0 && w0 < before + mine) {
-    *s_seq = tid;
-    *s_base = before;
-  }
-  for (long long base = W_first, s0 = NTHR; base <= w0 && s0 < p.n_seqs; s0 += NTHR) {
-    const long long v = tiles_of(static_cast<int>(s0) + tid);
-    const long long t = block_scan(v, &before);
-    before += base;
-    if (w0 < w1 && before <= w0 && w0 < before + v) {
-      *s_seq = static_cast<int>(s0) + tid;
-      *s_base = before;
-    }
-    base += t;
-  }
-  __syncthreads();
+  const Range rg = find_range<KT, NTHR>(p, s_warp, s_base, s_seq);
+  const long long W = rg.all, nc = rg.ctas, w0 = rg.begin, w1 = rg.end;
   // the joining kernel may be set up from here on; it waits for this grid's end before it reads anything
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t a_abort = smem_u32(const_cast<int*>(abort_flag));
@@ -270,7 +120,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
   if (wk.s >= 0) walk_load<KT>(p, wk);
   if (wk.s < 0) {
     if (tid == 0) p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-  } else if (warp == NW - 1) {
+  } else if (warp == NTHR / 32 - 1) {
     // ------------------------------------------------------------------ producer warp
     if (lane == 0) {
       prefetch_tensormap(&tmK);
@@ -284,7 +134,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
     for (long long w = w0; ok && w < w1;) {
       const Piece pc = piece_at(wk, w, w1);
       const int h = pc.h, t0 = pc.t0, t1 = pc.t1;
-      const int* row = p.table + static_cast<long long>(wk.s) * p.max_pages;
+      const int* row = p.table + wk.s * p.row_seq + h * p.row_head;
       for (int t = t0; ok && t < t1; ++t, ++it) {
         const int stage = it % NST;
         if (it >= NST)
@@ -688,70 +538,6 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
   __syncthreads();
 }
 
-// Joins the partials of the units that several ranges share. Block c looks after the unit that range c begins in
-// the middle of, if it is the first such range: M = max lse_k, lse = M + log2 sum 2^(lse_k - M),
-// out = sum 2^(lse_k - lse) O_k, in the order of the ranges (deterministic).
-// A warp takes a row (d = 128: a float4 a lane; d = 64: two rows): its lanes fetch the parts' lse side by side, and the
-// parts' values are fetched eight at a time before they are needed, so the chain is two trips to L2 for up to 32 parts.
-template <int D, int BF16>
-__global__ void __launch_bounds__(128) combine_kernel(const DecParams p, int rows) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 m = __ldcg(p.meta + 2 * blockIdx.x), q = __ldcg(p.meta + 2 * blockIdx.x + 1);
-  if (m.x < 0 || static_cast<int>(blockIdx.x) != m.z + 1) return;
-  const int h = m.y, c0 = m.z, parts = m.w - c0 + 1;
-  const int first = q.x, n = min(rows, q.y * p.G);  // the sequence's first token and rows
-  constexpr int LPR = D / 4;       // lanes of a row
-  constexpr int RPW = 32 / LPR;    // rows of a warp
-  const int lane = threadIdx.x & 31, c = lane % LPR;
-  auto slot_of = [&](int k) -> long long { return 2LL * (c0 + k) + (k == 0 ? 1 : 0); };
-  for (int r0 = (threadIdx.x >> 5) * RPW; r0 < n; r0 += 4 * RPW) {
-    const int r = min(r0 + lane / LPR, n - 1);  // (a row past the end repeats the last one)
-    float M = -INFINITY, L = 0.0f;
-    float4 a = make_float4(0, 0, 0, 0);
-    for (int k0 = 0; k0 < parts; k0 += LPR) {
-      const int kk = min(LPR, parts - k0);
-      const float lk = c < kk ? __ldcg(p.part_l + slot_of(k0 + c) * rows + r) : -INFINITY;
-      float top = lk;
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float Mn = fmaxf(M, top), Mu = Mn == -INFINITY ? 0.0f : Mn;
-      const float fix = M == -INFINITY ? 0.0f : exp2f(M - Mu);
-      const float w = lk == -INFINITY ? 0.0f : exp2f(lk - Mu);  // NaN passes on
-      M = Mn;
-      L *= fix;
-      a.x *= fix;
-      a.y *= fix;
-      a.z *= fix;
-      a.w *= fix;
-      for (int k = 0; k < kk; k += 8) {
-        float4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (slot_of(k0 + min(k + u, kk - 1)) * rows + r) * LPR + c);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const float wu = __shfl_sync(0xffffffffu, w, (lane & ~(LPR - 1)) + min(k + u, LPR - 1));
-          if (k + u < kk) {
-            L += wu;
-            a.x = fmaf(wu, v[u].x, a.x);
-            a.y = fmaf(wu, v[u].y, a.y);
-            a.z = fmaf(wu, v[u].z, a.z);
-            a.w = fmaf(wu, v[u].w, a.w);
-          }
-        }
-      }
-    }
-    const float inv = L > 0.0f ? 1.0f / L : (L != L ? NAN : 0.0f);
-    const int tok = r / p.G, hq = h * p.G + (r - tok * p.G);
-    const long long at = static_cast<long long>(first + tok) * p.Hq + hq;
-    reinterpret_cast<uint2*>(p.out)[at * LPR + c] =
-        make_uint2(pack16(a.x * inv, a.y * inv, BF16), pack16(a.z * inv, a.w * inv, BF16));
-    if (p.lse && c == 0)
-      p.lse[static_cast<long long>(hq) * p.T + first + tok] =
-          L > 0.0f ? (M + log2f(L)) * 0.69314718055994531f : (L != L ? NAN : -INFINITY);
-  }
-}
-
 template <int D, int BF16, bool E4M3, int NMT>
 int launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, int ctas, cudaStream_t stream) {
   using C = DecCfg<D, E4M3, NMT>;
@@ -765,18 +551,7 @@ int launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, i
   }
   kern<<<ctas, C::NTHR, C::SMEM, stream>>>(mk, mv, p);
   int rc = cuda_status(cudaGetLastError(), "paged attention kernel launch");
-  if (rc != CQSA_OK || ctas == 1) return rc;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, combine_kernel<D, BF16>, p, 16 * NMT), "paged attention joining kernel launch");
+  return rc == CQSA_OK ? launch_combine<D, BF16>(p, 16 * NMT, ctas, stream) : rc;
 }
 
 template <int D, int BF16, bool E4M3>
@@ -784,9 +559,15 @@ int launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p
   return rows <= 16 ? launch_t<D, BF16, E4M3, 1>(mk, mv, p, ctas, s) : launch_t<D, BF16, E4M3, 2>(mk, mv, p, ctas, s);
 }
 
-int tile_keys(const PagedArgs& a) { return a.cache_dtype == CQSA_E4M3 || a.d == 64 ? 128 : 64; }
+int tile_keys(const PagedArgs& a) {
+  return a.cache_dtype == CQSA_INT4 ? kDecode4Tile : (a.cache_dtype == CQSA_E4M3 || a.d == 64 ? 128 : 64);
+}
 
-int decode_rows(const PagedArgs& a) { return static_cast<long long>(a.max_q_len) * (a.Hq / a.Hkv) <= 16 ? 16 : 32; }
+// Rows of a unit, as the kernel that takes it lays them out.
+int decode_rows(const PagedArgs& a) {
+  const long long n = static_cast<long long>(a.max_q_len) * (a.Hq / a.Hkv);
+  return a.cache_dtype == CQSA_INT4 && n <= 8 ? 8 : (n <= 16 ? 16 : 32);
+}
 
 // One CTA per SM, fewer when there are fewer key tiles (by the caller's longest sequence; longer ones are
 // still computed, with fewer CTAs than they could use).
@@ -794,7 +575,8 @@ int decode_ctas(const PagedArgs& a) {
   const long long kt = tile_keys(a);
   const long long tiles = (a.max_kv_len + kt - 1) / kt;
   const long long all = ((tiles < 1 ? 1 : tiles) + kUnit) * a.n_seqs * a.Hkv;
-  const int most = sm_count() * decode_occ(a.cache_dtype == CQSA_E4M3, decode_rows(a) / 16);
+  const int rows = decode_rows(a);
+  const int most = sm_count() * (a.cache_dtype == CQSA_INT4 ? decode4_occ(rows) : decode_occ(a.cache_dtype == CQSA_E4M3, rows / 16));
   return static_cast<int>(all < most ? all : most);
 }
 
@@ -840,6 +622,8 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream) {
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
   p.q_stride = a.q_stride;
+  p.row_seq = a.row_seq;
+  p.row_head = a.row_head;
   p.n_seqs = a.n_seqs;
   p.T = a.T;
   p.Hq = a.Hq;
@@ -853,6 +637,7 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream) {
   p.timeout_us = timeout_us();
   p.fault = debug_fault();
   const bool bf = a.dtype == CQSA_BF16;
+  if (a.cache_dtype == CQSA_INT4) return launch_decode4(mk, mv, p, a.d, bf, rr, ctas, stream);
   if (a.cache_dtype == CQSA_E4M3) {
     if (a.d == 64) return bf ? launch_rows<64, 1, true>(mk, mv, p, rr, ctas, stream) : launch_rows<64, 0, true>(mk, mv, p, rr, ctas, stream);
     return bf ? launch_rows<128, 1, true>(mk, mv, p, rr, ctas, stream) : launch_rows<128, 0, true>(mk, mv, p, rr, ctas, stream);

@@ -1,0 +1,612 @@
+// Attention of a few new tokens (one, in a serving step) of each sequence over its pages of a 4-bit cache.
+//
+// A unit's rows, the split over the CTAs and the joining of parts are attn_decode.cu's. What a quarter of the bytes changes: a cached
+// vector of 128 features is 68 bytes, and at the memory's rate an SM has some six cycles, 23 warp instructions, for a key's and a
+// value's 256 numbers, so the kernel is laid out to spend few instructions on each.
+//
+// Products are S^T = K Q^T and O^T = V^T P^T on mma.sync's 16 x 8 x 16 tiles: the cache gives the 16 rows and the queries the 8
+// columns, so that up to 8 rows (4 query heads of a key head, say) waste nothing and each 4-bit number is turned into fp16 once for
+// them. In both, one ldmatrix of 8 keys x 32 features leaves each lane a word whose four nibbles are four fragments: nibble n of its
+// halves is a pair of neighbouring k for K (features 8 t + n and 8 t + n + 4), of neighbouring keys for V (transposed), as
+// the products want them; queries and results follow that order of the features. A pair of nibbles becomes a pair of fp16
+// numbers by one and-or (1024 + c, or 1024 + 16 c for the odd nibbles) and one add or multiply-add that is exact.
+//
+// Scales: K's multiplies the sums of its 32 features (fp32), V's goes onto the probabilities (one packed multiplication for 32
+// features x 2 keys), relative to the largest power of two met so far, so that P times the scale keeps fp16's precision down to 2^-28 of the
+// largest. P^T's fragment is S^T's transposed, one movmatrix for 8 keys. Queries are fp16, as in attn_decode.cu over e4m3.
+#include <math.h>
+#include <string.h>
+
+#include "attn_common.cuh"
+#include "cqsa_internal.h"
+#include "decode_common.cuh"
+#include "seq_common.cuh"
+#include "sm103_ptx.cuh"
+
+namespace cqsa {
+namespace {
+
+__device__ DevErr g_decode4_err;
+
+// NT: column tiles of 8 rows that a warp takes, NMT: groups of warps that take further rows.
+template <int D, int NT, int NMT>
+struct Dec4Cfg {
+  static constexpr int KT = kDecode4Tile, KW = KT / kQuarters;  // keys of a tile, of a warp
+  static constexpr int ROWB = D / 2, SPK = D / 32;              // bytes of a vector's codes, its scales
+  static constexpr uint32_t TILE = KT * ROWB, SCALES = KT * SPK;
+  static constexpr uint32_t STAGE = 2 * (TILE + SCALES);
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int LDO = D + 12;  // row of the joining buffer: it also holds a warp's running sum, D / 4 values a lane and column tile and its references
+  static constexpr uint32_t JOIN = static_cast<uint32_t>(NMT) * kQuarters * ROWS * LDO * 4;
+  static constexpr uint32_t ML = NMT * kQuarters * 2 * ROWS * 4;
+  static constexpr int OCC = decode4_occ(ROWS * NMT);
+  static constexpr int NST_MAX = static_cast<int>((232448 / OCC - (OCC - 1) * 1024 - 1024 - 512 - JOIN - ML) / STAGE);
+  static constexpr int NST = NST_MAX > 8 ? 8 : NST_MAX;
+  static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + 512;
+  static constexpr int NTHR = 32 + 32 * kQuarters * NMT;
+  static constexpr int FOLD = 16384 / KT;  // tiles between folds of O into the running sum, as in attn_decode.cu
+  static_assert(SMEM <= 232448 && NST >= 2, "shared memory exceeds 227 KiB");
+  static_assert(32 * (NT * D / 4 + 2 * NT + 1) <= ROWS * LDO, "the running sum does not fit the joining buffer");
+  static_assert(STAGE % 512 == 0, "a stage does not begin where its swizzle does");
+};
+
+// Byte offset of 16-byte chunk c of row r under TMA's 64-byte (32-byte for 32-byte rows) swizzle.
+template <int ROWB>
+__device__ __forceinline__ uint32_t sw4_off(int r, int c) {
+  if (ROWB == 64) return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+  return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
+}
+
+// The four pairs of whole numbers of a word, nibble n of both halves in x[n], as fp16 (exact).
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&x)[4]) {
+  const __half2 m1032 = __floats2half2_rn(-1032.0f, -1032.0f), m72 = __floats2half2_rn(-72.0f, -72.0f);
+  const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
+    const __half2 a = __hadd2(*reinterpret_cast<__half2*>(&lo), m1032);
+    const __half2 b = __hfma2(*reinterpret_cast<__half2*>(&hi), r16, m72);
+    x[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
+    x[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
+    w >>= 8;
+  }
+}
+
+__device__ __forceinline__ uint32_t transposed8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_2u32(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+// A key's scale bytes, one for each 32 features.
+template <int SPK>
+__device__ __forceinline__ uint32_t scales_of(uint32_t base, int key) {
+  return SPK == 4 ? ld_shared_u32(base + key * 4) : ld_shared_u16(base + key * 2);
+}
+
+template <int D, int BF16, int NT, int NMT>
+__global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>::OCC)
+    decode4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecParams p) {
+  using C = Dec4Cfg<D, NT, NMT>;
+  constexpr int KT = C::KT, KW = C::KW, NST = C::NST, NTHR = C::NTHR, ROWS = C::ROWS, SPK = C::SPK;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* join = reinterpret_cast<float*>(sm + NST * C::STAGE);
+  float* ml = join + C::JOIN / 4;  // [NMT][kQuarters][m ROWS | l ROWS]
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ml) + C::ML);
+  uint64_t* empty = full + NST;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NST);
+  long long* s_base = reinterpret_cast<long long*>(empty + NST + 1);
+  int* s_seq = reinterpret_cast<int*>(s_base + 1);
+  long long* s_warp = reinterpret_cast<long long*>(s_seq + 2);  // [NTHR / 32]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kQuarters * NMT);
+    }
+    *abort_flag = 0;
+    *s_seq = -1;
+    fence_mbar_init();
+  }
+  const Range rg = find_range<KT, NTHR>(p, s_warp, s_base, s_seq);
+  const long long W = rg.all, nc = rg.ctas, w0 = rg.begin, w1 = rg.end;
+  // the joining kernel may be set up from here on; it waits for this grid's end before it reads anything
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t a_abort = smem_u32(const_cast<int*>(abort_flag));
+  Walk wk;
+  wk.s = *s_seq;
+  wk.base = *s_base;
+  wk.n = 0;
+  if (wk.s >= 0) walk_load<KT>(p, wk);
+  if (wk.s < 0) {
+    if (tid == 0) p.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  } else if (warp == NTHR / 32 - 1) {
+    // ------------------------------------------------------------------ producer warp
+    if (lane == 0) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+    }
+    const int page = 1 << p.page_log2;
+    const int rows = min(page, KT);  // rows of a box
+    const int boxes = KT / rows;     // page boxes of a tile
+    int it = 0;
+    bool ok = true;
+    for (long long w = w0; ok && w < w1;) {
+      const Piece pc = piece_at(wk, w, w1);
+      const int h = pc.h, t0 = pc.t0, t1 = pc.t1;
+      const int* row = p.table + wk.s * p.row_seq + h * p.row_head;
+      for (int t = t0; ok && t < t1; ++t, ++it) {
+        const int stage = it % NST;
+        if (it >= NST)
+          ok = wait_or_abort(smem_u32(&empty[stage]), ((it / NST) - 1) & 1u, p.timeout_us, a_abort, &g_decode4_err,
+                             kDevTimeoutKV, 40);
+        if (!ok) break;
+        if (p.fault == 1 && wk.s == 0 && h == 0 && t == 0) {  // (every wait on the tile runs out)
+          ok = false;
+          break;
+        }
+        uint8_t* st = sm + stage * C::STAGE;
+        const int k0 = t * KT;
+        const int nb = min(boxes, max(0, (wk.len - k0 + rows - 1) >> (31 - __clz(rows))));
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(nb) * rows * 2 * (C::ROWB + SPK));
+        __syncwarp();
+        for (int i = lane; i < nb; i += 32) {
+          const int pos = k0 + i * rows;
+          const int pg = page_at(row, pos >> p.page_log2, p.n_pages), y = pos & (page - 1);
+          const uint32_t off = static_cast<uint32_t>(i * rows) * C::ROWB;
+          const int block = pg * p.Hkv + h;
+          tma_load_3d(st + off, &tmK, &full[stage], 0, y, block);
+          tma_load_3d(st + C::TILE + off, &tmV, &full[stage], 0, y, block);
+          const long long at = ((static_cast<long long>(block) << p.page_log2) + y) * SPK;
+          uint8_t* sc = st + 2 * C::TILE + i * rows * SPK;
+          bulk_load(sc, p.k_scale + at, rows * SPK, &full[stage]);
+          bulk_load(sc + C::SCALES, p.v_scale + at, rows * SPK, &full[stage]);
+        }
+      }
+      w = pc.next;
+      if (w < w1 && h == p.Hkv - 1) walk_next<KT>(p, wk);
+    }
+    __syncwarp();
+    // every copy issued has landed before the CTA ends (bounded)
+    for (int j = max(0, it - NST); j < it; ++j)
+      mbar_wait_bounded(&full[j % NST], (j / NST) & 1u, p.timeout_us * 1000ull);
+  } else {
+    // ------------------------------------------------------------------ key warps
+    const int mt = warp / kQuarters, kg = warp % kQuarters;  // group of rows, quarter of the keys
+    const int g = lane >> 2, t4 = lane & 3;
+    float* jbuf = join + mt * kQuarters * ROWS * C::LDO;
+    float* mlb = ml + mt * kQuarters * 2 * ROWS;
+    bool ok = true;
+    int it = 0;
+    for (long long w = w0; w < w1;) {
+      const Piece pc = piece_at(wk, w, w1);
+      const int h = pc.h, t0 = pc.t0, t1 = pc.t1;
+      if (w == w0 && tid == 0) {
+        // the unit this range begins in the middle of, and the CTAs whose ranges hold its first and last tile
+        const long long u0 = wk.base + static_cast<long long>(h) * wk.n, u1 = u0 + wk.n - 1;
+        const int c0 = static_cast<int>(((u0 + kUnit + 1) * nc - 1) / W), c1 = static_cast<int>(((u1 + 1) * nc - 1) / W);
+        p.meta[2 * blockIdx.x] = t0 == 0 ? make_int4(-1, 0, 0, 0) : make_int4(wk.s, h, c0, c1);
+        p.meta[2 * blockIdx.x + 1] = make_int4(wk.first, wk.qlen, 0, 0);
+      }
+      if (t1 <= t0) {
+        w = pc.next;
+        if (w < w1 && h == p.Hkv - 1) walk_next<KT>(p, wk);
+        continue;
+      }
+      // ---- this lane's queries (row g of each column tile, 8 features of every 32), and what its two columns (rows 2 t4, 2 t4 + 1) see
+      uint32_t qf[NT][D / 32][4];
+      int lim[NT][2];
+      float rs[NT][2];  // factor from a raw score to the base-2 exponent
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = (mt * NT + nt) * 8 + g, tok = r / p.G;
+        const bool valid = tok < wk.qlen;
+        const uint16_t* qr = static_cast<const uint16_t*>(p.q) + static_cast<long long>(wk.first + tok) * p.q_stride +
+                             static_cast<long long>(h * p.G + (r - tok * p.G)) * D + 8 * t4;
+        uint4 x[D / 32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) x[c] = valid ? __ldg(reinterpret_cast<const uint4*>(qr + c * 32)) : make_uint4(0, 0, 0, 0);
+        int e = 0;
+        if (BF16) {
+          float amax = 0.0f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const uint32_t ws[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = unpack16(ws[i], 1);
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          // 2^-e brings the row's largest value into [1, 2); held to the exponents whose inverse is normal
+          e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
+          const float inv = pow2i(-e);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ws[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = unpack16(ws[i], 1);
+              ws[i] = pack16(f.x * inv, f.y * inv, 0);
+            }
+            x[c] = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {  // features 8 t4 + n and 8 t4 + 4 + n
+          qf[nt][c][0] = __byte_perm(x[c].x, x[c].z, 0x5410);
+          qf[nt][c][1] = __byte_perm(x[c].x, x[c].z, 0x7632);
+          qf[nt][c][2] = __byte_perm(x[c].y, x[c].w, 0x5410);
+          qf[nt][c][3] = __byte_perm(x[c].y, x[c].w, 0x7632);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int tk = ((mt * NT + nt) * 8 + 2 * t4 + u) / p.G;
+          lim[nt][u] = tk >= wk.qlen ? 0 : (p.causal ? min(wk.len, wk.len - wk.qlen + tk + 1) : wk.len);
+          rs[nt][u] = p.scale_log2;
+          if (BF16) rs[nt][u] *= pow2i(__shfl_sync(0xffffffffu, e, (2 * t4 + u) * 4));
+        }
+      }
+      const int lim_all = p.causal ? wk.len - wk.qlen + 1 : wk.len;  // keys that every row sees
+      const bool full_rows = wk.qlen * p.G >= ROWS * NMT;
+      float o[NT][D / 32][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[nt][c][i >> 2][i & 3] = 0.0f;
+      float m[NT][2], l[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          m[nt][u] = -INFINITY;
+          l[nt][u] = 0.0f;
+        }
+      int ev = -1;  // exponent (biased by 15) of the value scales that the output sums are relative to
+      // The running sum that O is folded into: this lane's values, then the references that they are relative to. (The
+      // layout of the join below is another, and is written after the next named_sync.)
+      constexpr int NO = NT * D / 4;
+      float* sum = jbuf + kg * ROWS * C::LDO + lane;
+      auto sum_factor = [&](int nt, int u) -> float {
+        const float was = sum[(NO + 2 * nt + u) * 32], a = was == -INFINITY ? 0.0f : ex2(was - m[nt][u]);
+        return a * exp2_int_any(__float_as_int(sum[(NO + 2 * NT) * 32]) - ev);
+      };
+      for (int t = t0; t < t1; ++t, ++it) {
+        if (t > t0 && (t - t0) % C::FOLD == 0) {
+          const bool have = t - t0 > C::FOLD;
+          if (!have) named_sync(1 + mt, 32 * kQuarters);  // the unit before has been read out of the buffer
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float fs[2] = {have ? sum_factor(nt, 0) : 0.0f, have ? sum_factor(nt, 1) : 0.0f};
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float* at = sum + ((nt * (D / 32) + c) * 8 + i) * 32;
+                float& x = o[nt][c][i >> 2][i & 3];
+                *at = (have ? *at * fs[i & 1] : 0.0f) + x;
+                x = 0.0f;
+              }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            sum[(NO + 2 * nt) * 32] = m[nt][0];
+            sum[(NO + 2 * nt + 1) * 32] = m[nt][1];
+          }
+          sum[(NO + 2 * NT) * 32] = __int_as_float(ev);
+        }
+        const int stage = it % NST;
+        if (ok) ok = wait_or_abort(smem_u32(&full[stage]), (it / NST) & 1u, p.timeout_us, a_abort, &g_decode4_err,
+                                   kDevTimeoutKV, 41);
+        const uint32_t sk = smem_u32(sm) + stage * C::STAGE, sv = sk + C::TILE;
+        const int kw0 = kg * KW;                 // first key of this warp in the tile
+        const int k0 = t * KT + kw0;             // its position
+        const int left = wk.len - k0;            // positions of the sequence from there
+        const uint32_t ksc = sk + 2 * C::TILE + kw0 * SPK, vsc = ksc + C::SCALES;
+        // ---- a lane looks at one key's scales: is there a NaN among the keys', which is the largest of the values'
+        uint32_t kword = scales_of<SPK>(ksc, lane), vword = scales_of<SPK>(vsc, lane);
+        if (lane >= left) kword = vword = 0u;  // slots past the end hold anything
+        const unsigned nans = __ballot_sync(0xffffffffu, ((kword & 0x7f7f7f7fu) + 0x01010101u) & kword & 0x80808080u);
+        uint32_t top = max(vword & 255u, (vword >> 8) & 255u);
+        if (SPK == 4) top = max(top, max((vword >> 16) & 255u, vword >> 24));
+        top = min(__reduce_max_sync(0xffffffffu, top), 247u) >> 3;
+        if (static_cast<int>(top) > ev) {
+          const float a = ev < 0 ? 0.0f : exp2_int_any(ev - static_cast<int>(top));
+          ev = static_cast<int>(top);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[nt][c][i >> 2][i & 3] *= a;
+        }
+        // ---- S^T = K Q^T, 16 keys and 32 features at a time, each 32 features' sums times their key's scale
+        float s[KW / 16][NT][4];
+#pragma unroll
+        for (int j = 0; j < KW / 16; ++j) {
+          const uint32_t wa = scales_of<SPK>(ksc, j * 16 + g), wb = scales_of<SPK>(ksc, j * 16 + 8 + g);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t b[4];
+            ldsm4(sk + sw4_off<C::ROWB>(kw0 + j * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), c * 2 + (lane >> 4)), b);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int gr = 2 * c + x;
+              uint32_t lo[4], hi[4];  // keys 0-7 and 8-15
+              nibbles(b[2 * x], lo);
+              nibbles(b[2 * x + 1], hi);
+              const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+              // (a byte is the exponent and upper mantissa of an fp32 number, 2^112 too small)
+              const float fa = __uint_as_float(__byte_perm(wa, 0, 0x4440 + gr) * (1u << 20) + (112u << 23));
+              const float fb = __uint_as_float(__byte_perm(wb, 0, 0x4440 + gr) * (1u << 20) + (112u << 23));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma16816<0>(acc, a0, qf[nt][gr][0], qf[nt][gr][1]);
+                mma16816<0>(acc, a1, qf[nt][gr][2], qf[nt][gr][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float f = i < 2 ? fa : fb;
+                  s[j][nt][i] = gr == 0 ? acc[i] * f : fmaf(acc[i], f, s[j][nt][i]);
+                }
+              }
+            }
+          }
+        }
+        if (nans) {  // (a scale of 255 stands for NaN)
+#pragma unroll
+          for (int j = 0; j < KW / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if ((nans >> (j * 16 + 8 * i + g)) & 1u) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) s[j][nt][2 * i] = s[j][nt][2 * i + 1] = NAN;
+              }
+        }
+        // ---- scores in base 2, masks, running maximum, P^T (rounded to fp16) as the second product's operand
+        const bool mask = left < KW || k0 + KW > lim_all || !full_rows;
+        uint32_t pf[KW / 16][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < KW / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x = s[j][nt][i] * rs[nt][i & 1];
+              if (mask && k0 + j * 16 + (i >> 1) * 8 + g >= lim[nt][i & 1]) x = -INFINITY;
+              s[j][nt][i] = x;
+              mx[i & 1] = fmaxf(mx[i & 1], x);
+            }
+          float al[2], mu[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int of = 4; of < 32; of <<= 1) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], of));
+            const float mn = fmaxf(m[nt][u], mx[u]);
+            mu[u] = mn == -INFINITY ? 0.0f : mn;
+            al[u] = ex2(m[nt][u] - mu[u]);  // 0 while the row has seen nothing
+            mu[u] -= kPShift;
+            m[nt][u] = mn;
+            l[nt][u] *= al[u];
+          }
+          if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[nt][c][i >> 2][i & 3] *= al[i & 1];
+          }
+#pragma unroll
+          for (int j = 0; j < KW / 16; ++j) {
+            float pr[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              pr[i] = ex2(s[j][nt][i] - mu[i & 1]);
+              l[nt][i & 1] += pr[i];
+            }
+            pf[j][nt][0] = transposed8x8(pack16(pr[0], pr[1], 0));
+            pf[j][nt][1] = transposed8x8(pack16(pr[2], pr[3], 0));
+          }
+        }
+        // ---- O^T += V^T P^T, P times the values' scales relative to 2^(ev - 15)
+        const uint32_t adj = static_cast<uint32_t>(max(15 - ev, 0)) * 0x04000400u;
+#pragma unroll
+        for (int j = 0; j < KW / 16; ++j) {
+          uint32_t svp[SPK][2];  // scales of this lane's keys 2 t4, 2 t4 + 1 (and 8 further) as fp16 pairs
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int key = j * 16 + x * 8 + 2 * t4;
+            // (bytes of slots past the end become 0: their codes are finite, and their probabilities 0)
+            if (SPK == 4) {
+              uint2 ws = ld_shared_2u32(vsc + key * 4);
+              if (left < KW) {
+                if (key >= left) ws.x = 0u;
+                if (key + 1 >= left) ws.y = 0u;
+              }
+              const uint32_t e0 = ws.x & 0x00ff00ffu, e1 = ws.y & 0x00ff00ffu;
+              const uint32_t o0 = (ws.x >> 8) & 0x00ff00ffu, o1 = (ws.y >> 8) & 0x00ff00ffu;
+              svp[0][x] = __byte_perm(e0, e1, 0x5410) * 128u + adj;
+              svp[1][x] = __byte_perm(o0, o1, 0x5410) * 128u + adj;
+              svp[SPK - 2][x] = __byte_perm(e0, e1, 0x7632) * 128u + adj;
+              svp[SPK - 1][x] = __byte_perm(o0, o1, 0x7632) * 128u + adj;
+            } else {
+              uint32_t ws = ld_shared_u32(vsc + key * 2);
+              if (left < KW) {
+                if (key >= left) ws = 0u;
+                else if (key + 1 >= left) ws &= 0xffffu;
+              }
+              svp[0][x] = (ws & 0x00ff00ffu) * 128u + adj;
+              svp[1][x] = ((ws >> 8) & 0x00ff00ffu) * 128u + adj;
+            }
+          }
+          if (ev > 15) {
+            const __half2 f2 = __float2half2_rn(pow2i(15 - ev));
+            const uint32_t f = *reinterpret_cast<const uint32_t*>(&f2);
+#pragma unroll
+            for (int c = 0; c < SPK; ++c) {
+              svp[c][0] = mul2(svp[c][0], f);
+              svp[c][1] = mul2(svp[c][1], f);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t b[4];
+            ldsm4t(sv + sw4_off<C::ROWB>(kw0 + j * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), c * 2 + (lane >> 4)), b);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int gr = 2 * c + x;
+              uint32_t lo[4], hi[4];
+              nibbles(b[2 * x], lo);
+              nibbles(b[2 * x + 1], hi);
+              const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]}, a1[4] = {lo[2], lo[3], hi[2], hi[3]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t p0 = mul2(pf[j][nt][0], svp[gr][0]), p1 = mul2(pf[j][nt][1], svp[gr][1]);
+                mma16816<0>(o[nt][gr][0], a0, p0, p1);
+                mma16816<0>(o[nt][gr][1], a1, p0, p1);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+      }
+      if (t1 - t0 > C::FOLD) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float fs[2] = {sum_factor(nt, 0), sum_factor(nt, 1)};
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[nt][c][i >> 2][i & 3] += sum[((nt * (D / 32) + c) * 8 + i) * 32] * fs[i & 1];
+        }
+      }
+      // ---- join the warps' rows: each brings its sums to the common maximum and scale (the values' reference is a power of
+      // two that is multiplied out here)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int of = 4; of < 32; of <<= 1) l[nt][u] += __shfl_xor_sync(0xffffffffu, l[nt][u], of);
+          if (g == 0) {
+            mlb[kg * 2 * ROWS + nt * 8 + 2 * t4 + u] = m[nt][u];
+            mlb[kg * 2 * ROWS + ROWS + nt * 8 + 2 * t4 + u] = l[nt][u];
+          }
+        }
+      named_sync(1 + mt, 32 * kQuarters);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int row = nt * 8 + 2 * t4 + u;
+          float M = -INFINITY, L = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kQuarters; ++i) M = fmaxf(M, mlb[i * 2 * ROWS + row]);
+          const float Mu = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+          for (int i = 0; i < kQuarters; ++i) L += mlb[i * 2 * ROWS + ROWS + row] * ex2(mlb[i * 2 * ROWS + row] - Mu);
+          float f = L > 0.0f ? ex2(m[nt][u] - Mu) / L : (L != L ? NAN : 0.0f);
+          f *= ev < 0 ? 0.0f : exp2_int_any(ev - 15);
+          float* at = jbuf + (kg * ROWS + row) * C::LDO;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float4 y = make_float4(o[nt][c][0][u] * f, o[nt][c][0][2 + u] * f, o[nt][c][1][u] * f, o[nt][c][1][2 + u] * f);
+            if (f == 0.0f) y = make_float4(0, 0, 0, 0);  // (a row that sees nothing, beside values that are not finite)
+            *reinterpret_cast<float4*>(at + c * 32 + 4 * g) = y;
+          }
+          if (kg == 0 && g == 0)  // a column of the padding carries the rows' lse
+            at[D] = L > 0.0f ? M - kPShift + log2f(L) : (L != L ? NAN : -INFINITY);
+        }
+      named_sync(1 + mt, 32 * kQuarters);
+      const bool whole = t0 == 0 && t1 == wk.n - kUnit;
+      const long long slot = 2 * static_cast<long long>(blockIdx.x) + (t0 == 0 ? 1 : 0);
+      for (int e = kg * 32 + lane; e < ROWS * (D / 4); e += 32 * kQuarters) {
+        const int row = e / (D / 4), c = e % (D / 4);
+        const int r = mt * ROWS + row, tok = r / p.G;
+        if (tok >= wk.qlen || !ok) continue;
+        float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kQuarters; ++i) {
+          const float4 b = *reinterpret_cast<const float4*>(jbuf + (i * ROWS + row) * C::LDO + c * 4);
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+        if (whole) {
+          const long long at = static_cast<long long>(wk.first + tok) * p.Hq + h * p.G + (r - tok * p.G);
+          reinterpret_cast<uint2*>(p.out)[at * (D / 4) + c] = make_uint2(pack16(a.x, a.y, BF16), pack16(a.z, a.w, BF16));
+          if (p.lse && c == 0)
+            p.lse[static_cast<long long>(h * p.G + (r - tok * p.G)) * p.T + wk.first + tok] = jbuf[row * C::LDO + D] * 0.69314718055994531f;
+        } else {
+          reinterpret_cast<float4*>(p.part_o)[(slot * (ROWS * NMT) + r) * (D / 4) + c] = a;
+          if (c == 0) p.part_l[slot * (ROWS * NMT) + r] = jbuf[row * C::LDO + D];
+        }
+      }
+      w = pc.next;
+      if (w < w1 && h == p.Hkv - 1) walk_next<KT>(p, wk);
+    }
+  }
+  __syncthreads();
+}
+
+template <int D, int BF16, int NT, int NMT>
+int launch4_t(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, int ctas, cudaStream_t stream) {
+  using C = Dec4Cfg<D, NT, NMT>;
+  auto kern = decode4_kernel<D, BF16, NT, NMT>;
+  static PerDeviceOnce attr;
+  int dev = 0;
+  if (!attr.done(&dev)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(4-bit paged attention smem)");
+    attr.mark(dev);
+  }
+  kern<<<ctas, C::NTHR, C::SMEM, stream>>>(mk, mv, p);
+  const int rc = cuda_status(cudaGetLastError(), "4-bit paged attention kernel launch");
+  return rc == CQSA_OK ? launch_combine<D, BF16>(p, 8 * NT * NMT, ctas, stream) : rc;
+}
+
+template <int D, int BF16>
+int launch4_d(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, int rows, int ctas, cudaStream_t s) {
+  if (rows == 8) return launch4_t<D, BF16, 1, 1>(mk, mv, p, ctas, s);
+  return rows == 16 ? launch4_t<D, BF16, 2, 1>(mk, mv, p, ctas, s) : launch4_t<D, BF16, 2, 2>(mk, mv, p, ctas, s);
+}
+
+}  // namespace
+
+int launch_decode4(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, int d, int bf16, int rows, int ctas,
+                   cudaStream_t stream) {
+  if (d == 64) return bf16 ? launch4_d<64, 1>(mk, mv, p, rows, ctas, stream) : launch4_d<64, 0>(mk, mv, p, rows, ctas, stream);
+  return bf16 ? launch4_d<128, 1>(mk, mv, p, rows, ctas, stream) : launch4_d<128, 0>(mk, mv, p, rows, ctas, stream);
+}
+
+DEV_ERR_READERS(decode4, g_decode4_err)
+
+}  // namespace cqsa

@@ -141,6 +141,7 @@ struct PagedArgs {
   const int* kv_lens;
   void* workspace;
   long long q_stride;
+  long long row_seq, row_head;  // the pages of sequence s and key head h: from table + s * row_seq + h * row_head on
   int n_seqs, T, Hq, Hkv, d, page, n_pages, max_pages, max_q_len, max_kv_len, causal, dtype, cache_dtype;
   float scale;          // resolved
 };
@@ -174,7 +175,7 @@ int encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const 
                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
 // A cache by blocks (page * Hkv + head), with boxes of `rows` slots of one block: 16-bit data as (64 features, 8 slots,
 // half of the features, 8-slot group, block), which lands as [group][half][8 slots][64 features] under the 128-byte
-// swizzle; e4m3 as (feature, slot, block), a whole vector a row (128- or 64-byte swizzle, the row's size).
+// swizzle; e4m3 and 4 bits as (byte, slot, block), a whole vector a row (128-, 64- or 32-byte swizzle, the row's size).
 int make_page_map(CUtensorMap* m, const void* cache, const PagedArgs& a, int rows);
 
 // Copy tokens [t0, t0+n) of a [B,H,N,d] / [B,N,H,d] tensor (host or device) into a packed chunk buffer.

@@ -40,13 +40,13 @@ int encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const 
 
 int make_page_map(CUtensorMap* m, const void* cache, const PagedArgs& a, int rows) {
   const cuuint64_t blocks = static_cast<cuuint64_t>(a.n_pages) * a.Hkv;  // (page, head)
-  if (a.cache_dtype == CQSA_E4M3) {
-    const cuuint64_t vec = static_cast<cuuint64_t>(a.d);
+  if (a.cache_dtype == CQSA_E4M3 || a.cache_dtype == CQSA_INT4) {
+    const cuuint64_t vec = static_cast<cuuint64_t>(a.cache_dtype == CQSA_INT4 ? a.d / 2 : a.d);
     const cuuint64_t dims[3] = {vec, static_cast<cuuint64_t>(a.page), blocks};
     const cuuint64_t strides[2] = {vec, vec * a.page};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(a.d), static_cast<cuuint32_t>(rows), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(vec), static_cast<cuuint32_t>(rows), 1};
     return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, cache, dims, strides, box,
-                             a.d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                             vec == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : (vec == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B));
   }
   const cuuint64_t vec = static_cast<cuuint64_t>(a.d) * 2, halves = static_cast<cuuint64_t>(a.d / 64);
   const cuuint64_t dims[5] = {64, 8, halves, static_cast<cuuint64_t>(a.page / 8), blocks};
@@ -358,8 +358,8 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
   set_error("%s", "");
   int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
   if (rc == CQSA_OK) rc = check_cache(Hkv, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page_size, n_pages, dtype, cache_dtype);
-  if (rc == CQSA_OK && cache_dtype == CQSA_INT4) {
-    set_error("attention over a 4-bit cache is not supported");
+  if (rc == CQSA_OK && cache_dtype == CQSA_INT4 && static_cast<long long>(max_q_len < T ? max_q_len : T) * (Hq / Hkv) > 32) {
+    set_error("more than 32 rows of a sequence and key head over a 4-bit cache are not supported");
     rc = CQSA_ERR_UNSUPPORTED;
   }
   if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
@@ -391,6 +391,7 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
   a.q_stride = q_stride;
   a.n_pages = n_pages;
   a.max_pages = max_pages;
+  a.row_seq = max_pages;
   a.causal = causal != 0;
   a.scale = resolve_scale(scale, d);
   return decode_applies(a) ? launch_decode(a, stream) : launch_chunk(a, stream);

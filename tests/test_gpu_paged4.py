@@ -1,0 +1,234 @@
+"""Attention over a cache held in 4 bits on the GPU against its definition in 64 bits: single tokens and a few; grouped heads;
+ragged lengths; empty rows; scales of every size; what lies in unused slots."""
+import math
+
+import pytest
+import torch
+
+from tests import _seq as sq
+from tests import _seq4 as s4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def cq():
+    import exact_long_context_tcgen05_gb300 as m
+    return m
+
+
+def make_cache4(lengths, hkv, d, page, seed, sizes=(0,), sharp=1.5):
+    """Keys and values of each sequence (64 bits, what the cache stands for), and the cache: pages in a shuffled order, unused slots of codes 0
+    under NaN scales. `sizes`: powers of two that the values of successive slots are multiplied by."""
+    _, _, kc, vc, table = sq.make_cache(lengths, hkv, d, page, torch.float32, seed, fill=0.0, sharp=sharp)
+    factor = torch.exp2(torch.tensor(sizes, dtype=torch.float32, device="cuda"))[torch.arange(page, device="cuda") % len(sizes)]
+    (kq, kse, kval), (vq, vse, vval) = s4.quantise4(kc), s4.quantise4(vc * factor[None, None, :, None])
+    used = torch.zeros(kc.shape[:3], dtype=torch.bool, device="cuda")
+    kk, vv = [], []
+    for s, n in enumerate(lengths):
+        t = torch.arange(n, device="cuda")
+        pg = table[s].long()[t // page] if n else t
+        used[pg, :, t % page] = True
+        kk.append(kval[pg, :, t % page])
+        vv.append(vval[pg, :, t % page])
+    for codes, scale in ((kq, kse), (vq, vse)):
+        codes[~used] = 0
+        scale[~used] = 0xff
+    return kk, vv, kq, vq, kse, vse, table
+
+
+def call(cq, q, kq, vq, kse, vse, table, new, lengths, causal=True, **kw):
+    cu = torch.tensor(sq.starts(new), dtype=torch.int32, device="cuda")
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = cq.attention_paged(q, kq, vq, table, cu, lens, max(new), max(lengths), causal=causal, k_scale=kse, v_scale=vse,
+                                  return_lse=True, out=torch.full_like(q, 7.0), **kw)
+    torch.cuda.synchronize()
+    rc, code, _ = cq.cqsa_device_error()
+    assert rc == cq.CQSA_OK and code == 0
+    return out, lse
+
+
+def check(out, lse, q, ks, vs, new, lengths, causal, what, scale=None):
+    """Probabilities are rounded to fp16, and once more when their value's scale is multiplied in: twice 2^-11 relative. They are kept as
+    2^14 p (a chunk's: as 2^5 p at least), times a scale relative to the largest power of two of one: a product below fp16's normal
+    numbers is off by 2^-25, that is by 2^-39 (2^-30) times the largest scale at most, times a whole number up to 7."""
+    at = 0
+    for s, n in enumerate(new):
+        if n == 0:
+            continue
+        ref, rl, mass = sq.attend(q[at:at + n], ks[s], vs[s], lengths[s] - n, causal, scale)
+        chunk = max(new) * (q.shape[1] // ks[s].shape[1]) > 32
+        largest = vs[s].abs().max().item() if lengths[s] else 0.0
+        floor = lengths[s] * 2.0 * largest * 2.0 ** (-30 if chunk else -39)
+        assert torch.isfinite(out[at:at + n]).all(), what
+        u = sq.U[q.dtype]
+        tol = 1.01 * (u * ref.abs() + (2 * 2.0 ** -11 + 2.0 ** -16) * mass) + 2.0 ** -24 + floor
+        excess = ((out[at:at + n].double() - ref).abs() - tol).max().item()
+        assert excess <= 0, f"{what} sequence {s}: {excess:.3e} beyond the tolerance"
+        sq.check_lse(lse[:, at:at + n], rl, f"{what} sequence {s}")
+        at += n
+    assert (out[at:] == 7.0).all(), f"{what}: rows behind the last sequence"
+
+
+CASES = [
+    # new tokens, lengths, Hq, Hkv, page
+    ([1], [1], 1, 1, 16),
+    ([1], [3001], 8, 2, 16),
+    ([1, 1, 1, 1, 1], [1, 16, 17, 129, 1000], 8, 2, 32),
+    ([1] * 37, [1 + 61 * i for i in range(37)], 4, 1, 64),
+    ([1, 0, 1], [5000, 77, 300], 5, 1, 128),
+    ([1] * 200, [(i * 37) % 90 + 1 for i in range(200)], 2, 2, 16),   # more sequences than the kernel has threads
+    ([1, 1], [700, 33], 9, 1, 16),                                    # 9 rows
+    ([1, 1], [700, 129], 32, 1, 256),                                 # 32 heads of a key head
+    ([2, 2, 1, 3], [2, 200, 64, 127], 8, 2, 256),
+    ([4, 4], [900, 64], 32, 4, 16),                                   # 32 rows
+    ([17, 2], [333, 2], 2, 2, 64),                                    # 17 rows
+    ([6, 3, 2], [0, 2, 1], 4, 2, 16),                                 # sequences shorter than their new tokens: empty rows
+    ([1, 1], [0, 40], 4, 2, 16),
+]
+
+
+@pytest.mark.parametrize("new,lengths,hq,hkv,page", CASES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("sizes", [(0,), (0, 3, -5, 1, -2), (-9, -8, -13)])
+def test_paged_4bit(cq, new, lengths, hq, hkv, page, d, dt, sizes):
+    ks, vs, *cache = make_cache4(lengths, hkv, d, page, 17 + len(new), sizes)
+    q = sq.normal((sum(new) + 2, hq, d), sq.DT[dt], 3)
+    for causal in (True, False):
+        out, lse = call(cq, q, *cache, new, lengths, causal)
+        check(out, lse, q, ks, vs, new, lengths, causal, f"causal={causal}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [4, 12])
+def test_large_and_rising_scales(cq, d, hq):
+    """Values from 2^-14's to 2^14's scales, rising and falling along the sequence; keys of large and small scales under queries that bring
+    their scores back."""
+    lengths, page = [700], 16
+    for powers in ([-12, 0, 12], [12, 0, -12], [-3, 10, 2]):
+        ks, vs, kq, vq, kse, vse, table = make_cache4(lengths, 1, d, page, 5, sharp=1.0)
+        at = torch.arange(700, device="cuda") // 256
+        pg, slot = table[0].long()[torch.arange(700, device="cuda") // page], torch.arange(700, device="cuda") % page
+        by = torch.tensor(powers, device="cuda")[at]
+        vse[pg, :, slot] = (vse[pg, :, slot].int() + 8 * by[:, None, None].int()).clamp(8, 247).to(torch.uint8)
+        vs[0] = s4.values4(vq[pg, :, slot], vse[pg, :, slot])
+        for dt, kpow in (("f16", 0), ("bf16", 10), ("bf16", -10)):
+            k_now = kse.clone()
+            k_now[pg, :, slot] = (kse[pg, :, slot].int() + 8 * kpow).clamp(8, 247).to(torch.uint8)
+            k64 = s4.values4(kq[pg, :, slot], k_now[pg, :, slot])
+            q = (sq.normal((1, hq, d), torch.float32, 3) * 2.0 ** -kpow).to(sq.DT[dt])
+            out, lse = call(cq, q, kq, vq, k_now, vse, table, [1], lengths)
+            ref, rl, mass = sq.attend(q, k64, vs[0], 699, True)
+            scale = s4.scale_of(vse[pg, :, slot]).max().item()
+            tol = 1.01 * (sq.U[q.dtype] * ref.abs() + (2.0 ** -10 + 2.0 ** -16) * mass) + 2.0 ** -24 + 700 * 14 * scale * 2.0 ** -38
+            assert ((out.double() - ref).abs() <= tol).all()
+            sq.check_lse(lse, rl)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 7])
+def test_not_a_number(cq, d, new):
+    """A NaN scale of a key makes the rows that see it NaN, one of a value its 32 features; sequences beside it are untouched, and so are rows
+    before a NaN key and empty rows."""
+    hq, hkv, page, lengths = 4, 2, 16, [300, 200]
+    ks, vs, kq, vq, kse, vse, table = make_cache4(lengths, hkv, d, page, 9)
+    q = sq.normal((2 * new + 2, hq, d), torch.float16, 3)
+    clean = call(cq, q, kq, vq, kse, vse, table, [new, new], lengths)
+    bad_v, bad_k = vse.clone(), kse.clone()
+    bad_v[table[0, 100 // page], 1, 100 % page, 1] = 255
+    out, lse = call(cq, q, kq, vq, kse, bad_v, table, [new, new], lengths)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[:new, 2:, 32:64] = True
+    n = 2 * new  # (lse of the rows behind the last sequence is left as it was allocated)
+    assert torch.equal(torch.isnan(out), want) and torch.equal(lse[:, :n], clean[1][:, :n])
+    assert torch.equal(out[new:], clean[0][new:]) and torch.equal(out[:, :2], clean[0][:, :2])
+    last = lengths[0] - 1  # the last token's own key: the rows before it do not see it
+    bad_k[table[0, last // page], 0, last % page, 0] = 255
+    out, lse = call(cq, q, kq, vq, bad_k, vse, table, [new, new], lengths)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[new - 1, :2] = True
+    assert torch.equal(torch.isnan(out), want) and torch.equal(torch.isnan(lse[:, :n]), want[:n, :, 0].T)
+    empty, elses = call(cq, q, kq, vq, kse, bad_v, table, [new, new], [0, 200])
+    assert (empty[:new] == 0).all() and (elses[:, :new] == -math.inf).all()
+
+
+@pytest.mark.parametrize("hq,new", [(4, 1), (4, 5)])
+def test_equal_pages_and_table_order(cq, hq, new):
+    """The result does not depend on where pages lie, and repeats bit by bit."""
+    d, page, n = 128, 32, 777
+    got = []
+    for seed_order in (1, 2):
+        ks, vs, kq, vq, kse, vse, table = make_cache4([n, n], 2, d, page, 31)
+        order = torch.randperm(kq.shape[0], generator=torch.Generator().manual_seed(seed_order)).cuda()
+        inverse = torch.argsort(order)
+        kq, vq, kse, vse = (x[order].contiguous() for x in (kq, vq, kse, vse))
+        table = torch.where(table >= 0, inverse[table.long().clamp(min=0)].int(), table)
+        q = sq.normal((2 * new, hq, d), torch.float16, 3)
+        for _ in range(2):
+            got.append(call(cq, q, kq, vq, kse, vse, table, [new, new], [n, n]))
+    for o, l in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_sums(cq, d):
+    """One sequence long enough for a warp's sums to be folded many times, values of one sign: what the tensor core cuts off as it accumulates
+    stays below 2^-13 of the sum (256 products, 2^-23 each at most, twice)."""
+    n, page, hq, hkv = 2 ** 18 + 77, 256, 4, 1
+    pages = -(-n // page)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc = torch.randn(pages, hkv, page, d, generator=g, device="cuda") * 0.05
+    vc = torch.rand(pages, hkv, page, d, generator=g, device="cuda") + 0.5
+    (kq, kse, kval), (vq, vse, vval) = s4.quantise4(kc), s4.quantise4(vc)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    q = sq.normal((1, hq, d), torch.float16, 5)
+    cu, lens = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+    for most in (1, n):  # one CTA for all of it, and one a range
+        out = cq.attention_paged(q, kq, vq, table, cu, lens, 1, most, k_scale=kse, v_scale=vse)
+        k, v = kval[:, 0].reshape(-1, d)[:n, None], vval[:, 0].reshape(-1, d)[:n, None]
+        ref, _, mass = sq.attend(q, k, v, n - 1, True)
+        # (roundings of 2^18 probabilities that point either way add little)
+        assert ((out.double() - ref).abs() <= (2.0 ** -11 + 2.0 ** -13 + 2.0 ** -13) * mass).all()
+
+
+def test_graph_streams_and_workspaces(cq):
+    """Captured with its own workspace and replayed beside an eager call on another stream, for lengths that change between replays."""
+    d, page, lengths = 128, 16, [1000, 333, 64]
+    ks, vs, kq, vq, kse, vse, table = make_cache4(lengths, 2, d, page, 41)
+    q, other = sq.normal((3, 8, d), torch.bfloat16, 4), sq.normal((3, 8, d), torch.bfloat16, 5)
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):  # (the kernel's first call, maybe)
+        out, lse = cq.attention_paged(q, kq, vq, table, cu, lens, 1, 1000, return_lse=True, k_scale=kse, v_scale=vse)
+    for now in (lengths, [17, 333, 1], [1000, 2, 63]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        eager, elses = cq.attention_paged(other, kq, vq, table, cu, lens, 1, 1000, return_lse=True, stream=side, k_scale=kse, v_scale=vse)
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, l, x in ((out, lse, q), (eager, elses, other)):
+            pad = torch.full((1, 8, d), 7.0, dtype=x.dtype, device="cuda")
+            check(torch.cat([o, pad]), l, x, [k[:n] for k, n in zip(ks, now)], [v[:n] for v, n in zip(vs, now)], [1, 1, 1], now, True, "graph")
+
+
+def test_waits_give_up(cq):
+    """A key tile that never arrives: the kernel gives up after the limit, the error word says so, and the next call is right."""
+    ks, vs, *cache = make_cache4([1000], 2, 64, 32, 3)
+    q = sq.normal((1, 8, 64), torch.float16, 3)
+    pad = torch.full((1, 8, 64), 7.0, dtype=q.dtype, device="cuda")
+    cq.cqsa_set_timeout_ms(200)
+    try:
+        cq.cqsa_debug_set_fault(1)
+        cu, lens = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([1000], dtype=torch.int32, device="cuda")
+        cq.attention_paged(q, cache[0], cache[1], cache[4], cu, lens, 1, 1000, k_scale=cache[2], v_scale=cache[3])
+        torch.cuda.synchronize()
+        rc, code, _ = cq.cqsa_device_error(clear=True)
+        assert rc == cq.CQSA_ERR_TIMEOUT and code != 0
+    finally:
+        cq.cqsa_debug_set_fault(0)
+        cq.cqsa_set_timeout_ms(0)
+    out, lse = call(cq, q, *cache, [1], [1000])
+    check(torch.cat([out, pad]), lse, q, ks, vs, [1], [1000], True, "after")
