@@ -55,11 +55,11 @@ constexpr uint32_t TMEM_COLS = 512;
 // 2^14 above and, with full precision, 2^-14 below.
 constexpr float kPShift = 6.0f, kTau = 8.0f;
 
-enum : int { kSrcPacked = 0, kSrcPages = 1, kSrcE4m3 = 2 };
+enum : int { kSrcPacked = 0, kSrcPages = 1, kSrcE4m3 = 2, kSrcInt4 = 3 };
 
 template <int D, int SRC>
 struct SeqCfg {
-  static constexpr bool CONV = SRC == kSrcE4m3;
+  static constexpr bool INT4 = SRC == kSrcInt4, CONV = SRC == kSrcE4m3 || INT4;
   // P over S where tensor memory (d = 128) or registers (beside the converter warps) leave no room for both
   static constexpr bool ALIAS = D == 128 || CONV;
   static constexpr int KSUB = D / 64;
@@ -84,7 +84,8 @@ struct SeqCfg {
   // written 16 bytes at a time costs a wavefront per lane. d = 64 takes the running sum's place when it is not in use.
   static constexpr bool STAGED = OSUM_SMEM || !CONV;
   static constexpr uint32_t OUT_BYTES = STAGED && !OSUM_SMEM ? 8u * 4096u : 0u;
-  static constexpr uint32_t RAW = CONV ? 128u * D : 0u;  // a K or V tile's codes as they lie in the pages
+  static constexpr uint32_t ROW = INT4 ? D / 2 : D;      // bytes of a vector's codes
+  static constexpr uint32_t RAW = CONV ? 128u * ROW : 0u;  // a K or V tile's codes as they lie in the pages
   // running exponents per tile, factors of the queries' rows, the converter warps' largest exponents
   static constexpr uint32_t EXP_BYTES = CONV ? 2u * STAGES * 2u * 4u + 512u + 64u : 0u;
   static constexpr uint32_t SMEM_BYTES = 1024 + 2 * QT_BYTES + 2 * STAGES * KV_BYTES + OSUM_BYTES + OUT_BYTES + 2 * RAW + EXP_BYTES + NBARS * 8 + 112;
@@ -157,7 +158,7 @@ struct SeqParams {
   const int* cu;
   const int* kv_lens;  // null: a sequence's positions are its tokens (packed prompts)
   const int* table;
-  const uint8_t* k_cache;  // e4m3 only (16-bit pages go through the tensor maps)
+  const uint8_t* k_cache;  // e4m3 and 4 bits only (16-bit pages go through the tensor maps)
   const uint8_t* v_cache;
   const uint8_t* k_scale;
   const uint8_t* v_scale;
@@ -616,16 +617,16 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             if (lane < nb) {
               const int pos = kbase + j * BN + lane * rows;
               const int pg = page_at(trow, pos >> p.page_log2, p.n_pages);
-              at = (((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + (pos & (page - 1))) * D;
+              at = (((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + (pos & (page - 1))) * C::ROW;
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               ok = ok && wait_or_abort(smem_u32(&bar_raw_free[x]), ((kb + j) & 1u) ^ 1u, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 36 + x);
               if (!ok) break;
-              if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], static_cast<uint32_t>(nb) * rows * D);
+              if (lane == 0) mbar_arrive_expect_tx(&bar_raw[x], static_cast<uint32_t>(nb) * rows * C::ROW);
               __syncwarp();
               if (lane < nb)
-                bulk_load(sRaw + x * C::RAW + lane * rows * D, (x ? p.v_cache : p.k_cache) + at, rows * D, &bar_raw[x]);
+                bulk_load(sRaw + x * C::RAW + lane * rows * C::ROW, (x ? p.v_cache : p.k_cache) + at, rows * C::ROW, &bar_raw[x]);
               raw_last[x] = kb + j + 1;
             }
           }
@@ -1060,7 +1061,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     tc_fence_before();
     asm volatile("bar.sync 0;" ::: "memory");
   } else {
-    // ------------------------------------------------------------------ e4m3 converters
+    // ------------------------------------------------------------------ converters of e4m3 and 4-bit codes
     if constexpr (CONV) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::CVT));
       const int w = warp - 12;
@@ -1107,7 +1108,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         }
         // K and V tiles: this warp's 32 keys, a 16-byte piece of a code vector per lane and step. The exponents of this
         // lane's key are fetched a tile ahead, its page two.
-        constexpr int LPR = D / 16;        // lanes of a row
+        constexpr int LPR = C::ROW / 16;   // lanes of a row
         constexpr int RPS = 32 / LPR;      // rows of a step
         const int* trow = p.table + static_cast<long long>(v.w.seq) * p.max_pages;
         const int page_mask = (1 << p.page_log2) - 1;
@@ -1117,10 +1118,14 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           const int k = j * BN + w * 32 + lane;
           return j < n_max && k < kleft ? __ldg(trow + ((kbase + k) >> p.page_log2)) : NONE;
         };
-        auto exps_of = [&](int j, int pg) -> int2 {  // this lane's key's bytes in tile j, 0 past the end
+        auto exps_of = [&](int j, int pg) -> int2 {  // this lane's key's bytes in tile j (4 bits: a byte for each 32 features), 0 past the end
           if (j >= n_max || j * BN + w * 32 + lane >= kleft) return make_int2(0, 0);
           if (pg < 0 || pg >= p.n_pages) pg = 0;
           const long long vec = ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_log2) + ((kbase + j * BN + w * 32 + lane) & page_mask);
+          if constexpr (C::INT4 && D == 128)
+            return make_int2(__ldg(reinterpret_cast<const int*>(p.k_scale) + vec), __ldg(reinterpret_cast<const int*>(p.v_scale) + vec));
+          if constexpr (C::INT4 && D == 64)
+            return make_int2(__ldg(reinterpret_cast<const uint16_t*>(p.k_scale) + vec), __ldg(reinterpret_cast<const uint16_t*>(p.v_scale) + vec));
           return make_int2(__ldg(p.k_scale + vec), __ldg(p.v_scale + vec));
         };
         // 2^e in both halves of a register, for e <= 0 (0 below fp16's numbers)
@@ -1133,7 +1138,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
         const int r0 = w * 32 + lane / LPR;
         const uint32_t to = (c0 >> 3) * TILE_BYTES + r0 * 128;
         const uint32_t p0 = (((c0 + flip) & 7) ^ (r0 & 7)) << 4, p1 = (((c0 + 1 - flip) & 7) ^ (r0 & 7)) << 4;
-        const uint32_t from = smem_u32(sRaw) + r0 * D + (lane % LPR) * 16;
+        const uint32_t from = smem_u32(sRaw) + r0 * C::ROW + (lane % LPR) * 16;
         auto convert = [&](uint32_t raw, uint32_t tile, uint32_t factor, bool tail) {
 #pragma unroll
           for (int i = 0; i < 32 / RPS; ++i) {
@@ -1158,7 +1163,51 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
                          "r"(fl ? h[2] : h[6]), "r"(fl ? h[3] : h[7]) : "memory");
           }
         };
+        // 4 bits: a lane's 16 bytes are the 32 features of a scale, four pieces of the fp16 row. Lanes of the row's second half
+        // (d = 128) take their words in the order 2, 3, 0, 1, so that a row's and its neighbour's lanes meet eight different banks.
+        [[maybe_unused]] auto convert4 = [&](uint32_t raw, uint32_t tile, uint32_t word, int ref, int j) {
+          const int gr = lane % LPR;
+          const bool flip4 = gr >= 2;
+          const __half2 mul = __floats2half2_rn(1.0f, 0.0625f), add = __floats2half2_rn(-1032.0f, -72.0f);
+#pragma unroll
+          for (int i = 0; i < 32 / RPS; ++i) {
+            const int rw = i * RPS + lane / LPR, row = w * 32 + rw;
+            uint32_t c[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(raw + i * RPS * static_cast<int>(C::ROW)));
+            const uint32_t b = (__shfl_sync(0xffffffffu, word, rw) >> (8 * gr)) & 255u;
+            // relative to 2^ref, at least every scale so far but for its mantissa; zero past the end, where codes are whatever the slot holds
+            const float f = j * BN + row < kleft ? int4_scale(b) * exp2_int_any(-ref) : 0.0f;
+            const __half2 f2 = __float2half2_rn(f);
+            const uint32_t dst = tile + (gr >> 1) * TILE_BYTES + row * 128;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t cw = flip4 ? c[u ^ 2] : c[u];
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // a byte's two numbers from its low and high four bits: 1024 + c and 1024 + 16 c as fp16 numbers, then c - 8 (exact)
+                uint32_t x = (__byte_perm(cw, 0, e * 0x1111) & 0x00f0000fu) | 0x64006400u;
+                const __half2 y = __hmul2(__hfma2(*reinterpret_cast<__half2*>(&x), mul, add), f2);
+                h[e] = *reinterpret_cast<const uint32_t*>(&y);
+              }
+              const int piece = ((gr & 1) << 2) | (flip4 ? u ^ 2 : u);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + ((piece ^ (row & 7)) << 4)), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+            }
+          }
+        };
         auto exps_in = [&](int j, int2 b) -> int2 {
+          if constexpr (C::INT4) {  // the largest exponent of the scales that are numbers
+            auto top = [](uint32_t x) -> int {
+              uint32_t t = 0;
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) {
+                const uint32_t y = (x >> (8 * i)) & 255u;
+                t = max(t, y >= 248u ? 0u : y);
+              }
+              return static_cast<int>(t >> 3) - 15;
+            };
+            return j * BN + w * 32 + lane < kleft ? make_int2(top(b.x), top(b.y)) : make_int2(NONE, NONE);
+          }
           return j * BN + w * 32 + lane < kleft ? make_int2(b.x - 127, b.y - 127) : make_int2(NONE, NONE);
         };
         // the largest exponents of tile j's quarter go to the other warps a tile before they are needed
@@ -1180,7 +1229,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           const uint32_t free_par = (((kb + j) / STAGES) & 1u) ^ 1u, raw_par = (kb + j) & 1u;
           const bool tail = kleft - j * BN < BN;
           const bool in = j * BN + w * 32 + lane < kleft;
-          const int2 ex = exps_in(j, eb);
+          const int2 ex = C::INT4 ? eb : exps_in(j, eb);
           eb = exps_of(j + 1, pg);
           pg = page_of(j + 2);
           const int* top = sTop + raw_par * 8;
@@ -1196,7 +1245,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           if (ok) {
             // twice as many slots as stages: a K stage is free once S is, before the softmax has read its exponents
             if (w == 0 && lane == 0) *reinterpret_cast<int2*>(sExp + ((kb + j) % (2 * STAGES)) * 2) = make_int2(kref, vref);
-            convert(from, smem_u32(sK) + stage * C::KV_BYTES, in ? pow2h(ex.x - kref) : 0xffffffffu, tail);
+            if constexpr (C::INT4) convert4(from, smem_u32(sK) + stage * C::KV_BYTES, static_cast<uint32_t>(ex.x), kref, j);
+            else convert(from, smem_u32(sK) + stage * C::KV_BYTES, in ? pow2h(ex.x - kref) : 0xffffffffu, tail);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1208,7 +1258,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             if (ok) ok = wait_or_abort(smem_u32(&bar_v_empty[stage]), free_par, tmo_us, a_abort, &g_seq_err, kDevTimeoutKV, 35);
           }
           if (ok) {
-            convert(from + C::RAW, smem_u32(sV) + stage * C::KV_BYTES, in ? pow2h(ex.y - vref) : 0xffffffffu, tail);
+            if constexpr (C::INT4) convert4(from + C::RAW, smem_u32(sV) + stage * C::KV_BYTES, static_cast<uint32_t>(ex.y), vref, j);
+            else convert(from + C::RAW, smem_u32(sV) + stage * C::KV_BYTES, in ? pow2h(ex.y - vref) : 0xffffffffu, tail);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -1349,7 +1400,8 @@ int chunk_ctas(const PagedArgs& a) {
 int chunk_phases(const PagedArgs& a) {
   const int tpt = 128 / (a.Hq / a.Hkv);
   const double tiles = (a.max_kv_len / BN + 1.0) * a.Hkv * (static_cast<double>(a.T) / (2 * tpt));
-  const double bytes = static_cast<double>(a.n_seqs) * a.max_kv_len * a.Hkv * a.d * (a.cache_dtype == CQSA_E4M3 ? 2 : 4);
+  const double vector = a.cache_dtype == CQSA_INT4 ? 1.0625 * a.d : (a.cache_dtype == CQSA_E4M3 ? 2.0 * a.d : 4.0 * a.d);  // bytes of a key and a value
+  const double bytes = static_cast<double>(a.n_seqs) * a.max_kv_len * a.Hkv * vector;
   const double most = tiles / (24.0 * chunk_ctas(a)), want = bytes < 96.0 * 1048576.0 ? 1.0 : ceil(bytes / (64.0 * 1048576.0));
   const int n = static_cast<int>(fmin(fmin(want, most), fmin(a.Hkv, 4.0)));
   return n < 1 ? 1 : n;
@@ -1402,6 +1454,7 @@ int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
   if (rc == CQSA_OK) rc = make_token_map(&mq, a.q, a.dtype, a.d, a.Hq, a.T, a.q_stride, p.G, p.tpt);
   // (e4m3 pages are copied as they lie, without maps: the queries' stands in for theirs)
   if (rc == CQSA_OK && a.cache_dtype == CQSA_E4M3) return dispatch<kSrcE4m3>(mq, mq, mq, p, a.d, a.dtype, ctas, stream);
+  if (rc == CQSA_OK && a.cache_dtype == CQSA_INT4) return dispatch<kSrcInt4>(mq, mq, mq, p, a.d, a.dtype, ctas, stream);
   const int box = a.page < BN ? a.page : BN;
   if (rc == CQSA_OK) rc = make_page_map(&mk, a.k_cache, a, box);
   if (rc == CQSA_OK) rc = make_page_map(&mv, a.v_cache, a, box);

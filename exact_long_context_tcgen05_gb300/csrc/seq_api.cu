@@ -358,10 +358,6 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
   set_error("%s", "");
   int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
   if (rc == CQSA_OK) rc = check_cache(Hkv, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page_size, n_pages, dtype, cache_dtype);
-  if (rc == CQSA_OK && cache_dtype == CQSA_INT4 && static_cast<long long>(max_q_len < T ? max_q_len : T) * (Hq / Hkv) > 32) {
-    set_error("more than 32 rows of a sequence and key head over a 4-bit cache are not supported");
-    rc = CQSA_ERR_UNSUPPORTED;
-  }
   if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
   if (rc != CQSA_OK) return rc;
   if (!cu_seqlens || !kv_lens || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))

@@ -232,3 +232,99 @@ def test_waits_give_up(cq):
         cq.cqsa_set_timeout_ms(0)
     out, lse = call(cq, q, *cache, [1], [1000])
     check(torch.cat([out, pad]), lse, q, ks, vs, [1], [1000], True, "after")
+
+
+CHUNKS = [
+    # new tokens, lengths, Hq, Hkv, page
+    ([3, 1, 5], [3, 1, 700], 14, 2, 16),                              # a group of 7 heads, just over 32 rows
+    ([64, 1, 0, 130], [64, 400, 9, 1130], 8, 2, 16),
+    ([300], [2300], 4, 4, 64),
+    ([257, 128], [257, 129], 6, 2, 32),
+    ([70], [70], 64, 1, 16),                                          # one key head for 64
+    ([40, 3, 2], [0, 2, 1], 4, 2, 16),                                # sequences shorter than their new tokens: empty rows
+    ([33, 40], [5000, 33], 1, 1, 256),
+]
+
+
+@pytest.mark.parametrize("new,lengths,hq,hkv,page", CHUNKS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("sizes", [(0,), (0, 3, -5, 1, -2), (-9, -8, -13)])
+def test_chunks_4bit(cq, new, lengths, hq, hkv, page, d, dt, sizes):
+    ks, vs, *cache = make_cache4(lengths, hkv, d, page, 17 + len(new), sizes)
+    q = sq.normal((sum(new) + 2, hq, d), sq.DT[dt], 3)
+    for causal in (True, False):
+        out, lse = call(cq, q, *cache, new, lengths, causal)
+        check(out, lse, q, ks, vs, new, lengths, causal, f"causal={causal}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunk_ranges(cq, d):
+    """Chunks whose work is cut into ranges over units of very different lengths, in one phase of key heads or several, and by one
+    CTA; twice the same bit by bit."""
+    new, lengths, hq, hkv, page = [300, 0, 45, 700, 33], [300, 9, 4000, 1500, 20], 8, 4, 32
+    ks, vs, kq, vq, kse, vse, table = make_cache4(lengths, hkv, d, page, 5, (0, 2, -1))
+    q = sq.normal((sum(new), hq, d), torch.float16, 3)
+    cu, kl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (sq.starts(new), lengths))
+    pad = torch.full((1, hq, d), 7.0, dtype=q.dtype, device="cuda")
+    for causal in (True, False):
+        for most in (1, 4000, 2_000_000):
+            got = [cq.attention_paged(q, kq, vq, table, cu, kl, max(new), most, causal=causal, return_lse=True, k_scale=kse, v_scale=vse)
+                   for _ in range(2)]
+            torch.cuda.synchronize()
+            assert cq.cqsa_device_error()[1] == 0
+            assert all(torch.equal(x, y) for x, y in zip(*got))
+            check(torch.cat([got[0][0], pad]), got[0][1], q, ks, vs, new, lengths, causal, f"causal={causal} most={most}")
+
+
+@pytest.mark.parametrize("powers", [[0, 3, 6], [5, -3, 1], [-2, -2, 7]])
+@pytest.mark.parametrize("d,dt", [(128, "f16"), (128, "bf16"), (64, "f16"), (64, "bf16")])
+def test_chunks_with_running_sums(cq, d, dt, powers):
+    """Units long enough for running sums of O, values whose sizes rise and fall from one segment to the next, through the cache's own
+    write."""
+    dtype, hq, hkv, page, new = sq.DT[dt], 8, 2, 64, [300, 130]
+    segment = 4096 if d == 128 else 16384
+    lengths = [2 * segment + 900, segment + 1100]
+    per = [-(-n // page) for n in lengths]
+    kc, vc = (torch.zeros(sum(per), hkv, page, d // 2, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales = {n: torch.zeros(sum(per), hkv, page, d // 32, dtype=torch.uint8, device="cuda") for n in ("k_scale", "v_scale")}
+    table = torch.zeros(2, max(per), dtype=torch.int32, device="cuda")
+    order = torch.randperm(sum(per), generator=torch.Generator().manual_seed(3)).to(torch.int32).cuda()
+    table[0, :per[0]], table[1, :per[1]] = order[:per[0]], order[per[0]:]
+    ks, vs = [], []
+    for s, n in enumerate(lengths):
+        by = torch.exp2(torch.tensor(powers, dtype=torch.float64, device="cuda"))[(torch.arange(n, device="cuda") // segment).clamp(max=2)][:, None, None]
+        k = (sq.normal((n, hkv, d), torch.float64, 10 + s) * by ** 0.25).to(dtype)
+        v = (sq.normal((n, hkv, d), torch.float64, 20 + s) * by).to(dtype)
+        cq.kv_cache_write(k, v, kc, vc, table[s:s + 1].contiguous(), torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                          torch.tensor([n], dtype=torch.int32, device="cuda"), **scales)
+        ks.append(s4.quantise4(k)[2])
+        vs.append(s4.quantise4(v)[2])
+    q = sq.normal((sum(new), hq, d), dtype, 5)
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (sq.starts(new), lengths))
+    pad = torch.full((1, hq, d), 7.0, dtype=dtype, device="cuda")
+    for most in (1, max(lengths)):
+        for causal in (True, False):
+            out, lse = cq.attention_paged(q, kc, vc, table, cu, lens, max(new), most, causal=causal, return_lse=True, **scales)
+            torch.cuda.synchronize()
+            assert cq.cqsa_device_error()[1] == 0
+            check(torch.cat([out, pad]), lse, q, ks, vs, new, lengths, causal, f"most={most} causal={causal}")
+
+
+def test_chunk_nan(cq):
+    """A NaN scale of a key makes the rows that see it NaN; a value's the 32 features of its head's rows; other sequences and heads are untouched."""
+    d, hq, hkv, page, new, lengths = 128, 4, 2, 16, [40, 50], [300, 200]
+    ks, vs, kq, vq, kse, vse, table = make_cache4(lengths, hkv, d, page, 9)
+    q = sq.normal((90, hq, d), torch.bfloat16, 3)
+    clean = call(cq, q, kq, vq, kse, vse, table, new, lengths)
+    bad_v, bad_k = vse.clone(), kse.clone()
+    bad_v[table[0, 100 // page], 1, 100 % page, 1] = 255
+    bad_k[table[0, 279 // page], 0, 279 % page, 3] = 255  # the position of new token 19
+    out, lse = call(cq, q, kq, vq, kse, bad_v, table, new, lengths)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[:40, 2:, 32:64] = True
+    assert torch.equal(torch.isnan(out), want) and torch.equal(out[~want], clean[0][~want])
+    out, lse = call(cq, q, kq, vq, bad_k, vse, table, new, lengths)
+    want[:] = False
+    want[19:40, :2] = True
+    assert torch.equal(torch.isnan(out), want) and torch.equal(torch.isnan(lse), want[..., 0].T)
