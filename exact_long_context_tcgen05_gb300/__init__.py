@@ -27,7 +27,8 @@ EXPORTED = ("cqsa_attn_fwd", "cqsa_attn_fwd_chunk", "cqsa_merge_partials", "cqsa
             "cqsa_status_string", "cqsa_last_error", "cqsa_device_error", "cqsa_set_timeout_ms",
             "cqsa_debug_set_fault", "cqsa_version", "cqsa_set_stream_kv_resident_bytes", "cqsa_attn_packed_fwd",
             "cqsa_attn_packed_bwd_workspace_size", "cqsa_attn_packed_bwd", "cqsa_kv_cache_write",
-            "cqsa_kv_cache_read", "cqsa_attn_paged_workspace_size", "cqsa_attn_paged_fwd", "cqsa_kv_cache_append")
+            "cqsa_kv_cache_read", "cqsa_attn_paged_workspace_size", "cqsa_attn_paged_fwd", "cqsa_kv_cache_append",
+            "cqsa_kv_page_bounds", "cqsa_attn_selected_workspace_size", "cqsa_attn_selected_fwd")
 CQSA_STATIC_SCRATCH_BYTES = 32 << 20
 
 
@@ -107,6 +108,11 @@ def _load() -> ctypes.CDLL:
     lib.cqsa_attn_paged_workspace_size.restype = ctypes.c_size_t
     lib.cqsa_attn_paged_fwd.argtypes = [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i,
                                         _i, _i, _i, _i, _i, _f, _i, _i, _vp, ctypes.c_size_t, _vp]
+    lib.cqsa_kv_page_bounds.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp]
+    lib.cqsa_attn_selected_workspace_size.argtypes = [_i] * 9
+    lib.cqsa_attn_selected_workspace_size.restype = ctypes.c_size_t
+    lib.cqsa_attn_selected_fwd.argtypes = [_vp, _ll, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i,
+                                           _i, _i, _i, _i, _i, _f, _i, _i, _vp, ctypes.c_size_t, _vp]
     lib.cqsa_release_cache.argtypes = []
     lib.cqsa_release_cache.restype = _i
     lib.cqsa_status_string.argtypes = [_i]
@@ -363,6 +369,27 @@ def cqsa_attn_paged_fwd(q, q_stride, out, lse, k_cache, v_cache, k_scale, v_scal
                                           _ptr(kv_lens), n_seqs, T, max_q_len, max_kv_len, Hq, Hkv, d, page_size,
                                           n_pages, int(bool(causal)), float(scale), dtype, cache_dtype, _ptr(workspace),
                                           int(workspace_bytes), _stream(stream)))
+
+
+def cqsa_kv_page_bounds(k_cache, k_scale, bounds, bounds_exp, block_table, max_pages, cu_seqlens, kv_lens, n_seqs, T, max_q_len,
+                        Hkv, d, page_size, n_pages, dtype, cache_dtype, stream=None) -> int:
+    return _check(lib.cqsa_kv_page_bounds(_ptr(k_cache), _ptr(k_scale), _ptr(bounds), _ptr(bounds_exp), _ptr(block_table),
+                                          max_pages, _ptr(cu_seqlens), _ptr(kv_lens), n_seqs, T, max_q_len, Hkv, d, page_size,
+                                          n_pages, dtype, cache_dtype, _stream(stream)))
+
+
+def cqsa_attn_selected_workspace_size(T, Hq, Hkv, d, page_size, n_select, max_kv_len, dtype, cache_dtype) -> int:
+    return int(lib.cqsa_attn_selected_workspace_size(T, Hq, Hkv, d, page_size, n_select, max_kv_len, dtype, cache_dtype))
+
+
+def cqsa_attn_selected_fwd(q, q_stride, out, lse, pages, k_cache, v_cache, k_scale, v_scale, bounds, bounds_exp, block_table,
+                           max_pages, cu_seqlens, kv_lens, n_seqs, T, n_select, max_kv_len, Hq, Hkv, d, page_size, n_pages,
+                           scale, dtype, cache_dtype, workspace, workspace_bytes, stream=None) -> int:
+    return _check(lib.cqsa_attn_selected_fwd(_ptr(q), q_stride, _ptr(out), _ptr(lse), _ptr(pages), _ptr(k_cache), _ptr(v_cache),
+                                             _ptr(k_scale), _ptr(v_scale), _ptr(bounds), _ptr(bounds_exp), _ptr(block_table),
+                                             max_pages, _ptr(cu_seqlens), _ptr(kv_lens), n_seqs, T, n_select, max_kv_len, Hq, Hkv,
+                                             d, page_size, n_pages, float(scale), dtype, cache_dtype, _ptr(workspace),
+                                             int(workspace_bytes), _stream(stream)))
 
 
 def cqsa_set_stream_kv_resident_bytes(nbytes: int) -> None:
@@ -779,3 +806,84 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
                                    n_pages, 1 if causal else 0, 0.0 if scale is None else scale, dt, code,
                                    workspace.data_ptr(), size, _current(device)))
     return (out, lse) if return_lse else out
+
+
+def _bounds(bounds, bounds_exp, n_pages, Hkv, d, device):
+    torch = _tc()
+    if bounds.dtype != torch.int8 or bounds.shape != (n_pages, Hkv, 2, d) or bounds.device != device or not bounds.is_contiguous():
+        raise ValueError(f"bounds must be a contiguous int8 tensor [{n_pages}, {Hkv}, 2, {d}] on {device}")
+    if bounds_exp.dtype != torch.uint8 or bounds_exp.shape != (n_pages, Hkv) or bounds_exp.device != device or not bounds_exp.is_contiguous():
+        raise ValueError(f"bounds_exp must be a contiguous uint8 tensor [{n_pages}, {Hkv}] on {device}")
+
+
+def kv_page_bounds(k_cache, block_table, cu_seqlens, kv_lens, bounds, bounds_exp, max_q_len, *, k_scale=None, stream=None):
+    """The bounds that attention_selected reads, of the pages that hold the sequences' new tokens: bounds int8 [n_pages, Hkv, 2, d] (largest and
+    smallest key of each feature), bounds_exp uint8 [n_pages, Hkv] (their power of two). Call it after every write into the cache; max_q_len: about the
+    most new tokens of a sequence."""
+    torch = _tc()
+    device = k_cache.device
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return kv_page_bounds(k_cache, block_table, cu_seqlens, kv_lens, bounds, bounds_exp, max_q_len, k_scale=k_scale)
+    dtype = k_cache.dtype if k_cache.dtype in _codes else torch.float16  # (bytes stand for numbers of neither type)
+    # (the values' cache and scales are not looked at: the keys' stand in for them)
+    code, d, n_seqs, max_pages, table, cu, lens, ksc, _ = _cache(k_cache, k_cache, k_scale, k_scale, block_table, cu_seqlens,
+                                                                 kv_lens, dtype, device)
+    n_pages, Hkv, page = k_cache.shape[:3]
+    _bounds(bounds, bounds_exp, n_pages, Hkv, d, device)
+    T = 0x7fffffff // max(Hkv, 1)  # (no token is looked at: any count that cu_seqlens cannot pass)
+    _check(lib.cqsa_kv_page_bounds(k_cache.data_ptr(), ksc, bounds.data_ptr(), bounds_exp.data_ptr(), table.data_ptr(), max_pages,
+                                   cu.data_ptr(), lens.data_ptr(), n_seqs, T, min(max_q_len, 0x7fffffff), Hkv, d, page, n_pages,
+                                   _code(dtype), code, _current(device)))
+
+
+def attention_selected(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, bounds, bounds_exp, n_select, max_kv_len, *, scale=None,
+                       k_scale=None, v_scale=None, return_lse=False, return_pages=False, out=None, workspace=None, stream=None):
+    """Attention of each new token q [T, Hq, d] over n_select pages of its sequence: its own, and for each key head the others whose bounds
+    (kv_page_bounds) give the highest scores. Returns out [T, Hq, d] (and lse [Hq, T] fp32, and the pages, int32 [T, Hkv, n_select], ascending
+    indices into the sequence's row of block_table, -1 behind them; rows behind the last sequence are left as they were). max_kv_len: at least the longest kv_lens. `workspace`: a byte
+    tensor of at least cqsa_attn_selected_workspace_size bytes (allocated if not given)."""
+    torch = _tc()
+    device, dtype = q.device, q.dtype
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return attention_selected(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, bounds, bounds_exp, n_select, max_kv_len,
+                                      scale=scale, k_scale=k_scale, v_scale=v_scale, return_lse=return_lse,
+                                      return_pages=return_pages, out=out, workspace=workspace)
+    code, d, n_seqs, max_pages, table, cu, lens, ksc, vsc = _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens,
+                                                                   kv_lens, dtype, device)
+    n_pages, Hkv, page = k_cache.shape[:3]
+    if len(q.shape) != 3:
+        raise ValueError("q must be [T, Hq, d]")
+    T, Hq = q.shape[:2]
+    q, qs = _tokens("q", q, Hq, d, q)
+    _bounds(bounds, bounds_exp, n_pages, Hkv, d, device)
+    dt = _code(dtype)
+    if n_select < 1 or n_select * page > 1 << 24:
+        raise ValueError("n_select must be positive, and n_select * page_size at most 2^24")
+    max_kv_len = min(max_kv_len, 0x7fffffff)
+    out = _out(out, q)
+    lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if return_lse else None
+    pages = torch.empty((T, Hkv, n_select), dtype=torch.int32, device=device) if return_pages else None
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    if workspace is None:
+        key = (T, Hq, Hkv, d, page, n_select, max_kv_len, dt, code, device.index)
+        size = _sizes.get(key)
+        if size is None:
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            size = _sizes[key] = lib.cqsa_attn_selected_workspace_size(*key[:-1])
+        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _check(lib.cqsa_attn_selected_fwd(q.data_ptr(), qs, out.data_ptr(), lse.data_ptr() if return_lse else None,
+                                      pages.data_ptr() if return_pages else None, k_cache.data_ptr(), v_cache.data_ptr(), ksc, vsc,
+                                      bounds.data_ptr(), bounds_exp.data_ptr(), table.data_ptr(), max_pages, cu.data_ptr(),
+                                      lens.data_ptr(), n_seqs, T, n_select, max_kv_len, Hq, Hkv, d, page, n_pages,
+                                      0.0 if scale is None else scale, dt, code, workspace.data_ptr(), size, _current(device)))
+    if not return_lse and not return_pages:
+        return out
+    return (out, *((lse,) if return_lse else ()), *((pages,) if return_pages else ()))

@@ -153,6 +153,38 @@ int launch_decode(const PagedArgs& a, cudaStream_t stream);
 size_t chunk_workspace(const PagedArgs& a);
 int launch_chunk(const PagedArgs& a, cudaStream_t stream);
 
+// Bounds of the keys of pages, and the selection of pages by them (attn_select.cu).
+struct BoundsArgs {
+  const void* k_cache;
+  const unsigned char* k_scale;
+  signed char* bounds;   // [n_pages, Hkv, 2, d]
+  unsigned char* exps;   // [n_pages, Hkv]
+  const int* table;
+  const int* cu;
+  const int* kv_lens;
+  int n_seqs, T, Hkv, d, page, n_pages, max_pages, dtype, cache_dtype;
+};
+int launch_page_bounds(const BoundsArgs& a, int max_q_len, cudaStream_t stream);
+struct SelectArgs {
+  const void* q;         // [T, Hq, d], q_stride elements from token to token
+  const signed char* bounds;
+  const unsigned char* exps;
+  const int* table;
+  const int* cu;
+  const int* kv_lens;
+  int* pages;            // [T, Hkv, n_select] of the sequence's table, or null
+  void* workspace;
+  long long q_stride;
+  int n_seqs, T, G, Hkv, d, page, n_pages, max_pages, most_pages, n_select, dtype;
+  // what launch_select lays out in the workspace: scores of some tokens, and for the attention each token as a sequence of its own
+  float* scores;
+  int* list;             // [T, Hkv, n_select] pages of the cache
+  int* cu_out;           // [T + 1]
+  int* lens_out;         // [T]
+};
+size_t select_workspace(const SelectArgs& a);
+int launch_select(SelectArgs* a, cudaStream_t stream);
+
 // Whole prompts packed end to end (attn_seq.cu; backward: attn_bwd.cu).
 struct PackedArgs {
   const void* q;        // [T, Hq, d], `*_stride` elements from token to token

@@ -221,6 +221,43 @@ int paged_sizes(PagedArgs* a, int n_seqs, int T, int Hq, int Hkv, int d, int pag
   return CQSA_OK;
 }
 
+// The sizes of a selection, and of the attention behind it, in which each token is a sequence of its own.
+int selected_sizes(SelectArgs* s, PagedArgs* a, int n_seqs, int T, int Hq, int Hkv, int d, int page, int n_select, int max_kv_len,
+                   int dtype, int cache_dtype) {
+  int rc = check_seqs(n_seqs, T, Hq, Hkv, d, 0.0f, dtype);
+  if (rc != CQSA_OK) return rc;
+  if (Hq / Hkv > 32) {
+    set_error("%d query heads for a key head are not supported over selected pages (32 at most)", Hq / Hkv);
+    return CQSA_ERR_UNSUPPORTED;
+  }
+  if (page < 16 || page > 256 || (page & (page - 1))) {
+    set_error("page size %d is not supported (16, 32, 64, 128 or 256)", page);
+    return CQSA_ERR_UNSUPPORTED;
+  }
+  if (max_kv_len < 0) return invalid("max_kv_len must be >= 0");
+  if (n_select < 1 || static_cast<long long>(n_select) * page > 1 << 24) {
+    set_error("n_select = %d must be positive, and n_select * page_size at most 2^24", n_select);
+    return CQSA_ERR_INVALID;
+  }
+  if (static_cast<long long>(T) * Hkv > 0x7fffffffLL / n_select) {
+    set_error("T * Hkv * n_select = %lld is too large (2^31 - 1 at most)", static_cast<long long>(T) * Hkv * n_select);
+    return CQSA_ERR_UNSUPPORTED;
+  }
+  rc = paged_sizes(a, T < 1 ? 1 : T, T, Hq, Hkv, d, page, 1, n_select * page, dtype, cache_dtype);
+  if (rc != CQSA_OK) return rc;
+  memset(s, 0, sizeof(*s));
+  s->n_seqs = n_seqs;
+  s->T = T;
+  s->G = Hq / Hkv;
+  s->Hkv = Hkv;
+  s->d = d;
+  s->page = page;
+  s->most_pages = max_kv_len < page ? 1 : (max_kv_len - 1) / page + 1;
+  s->n_select = n_select;
+  s->dtype = dtype;
+  return CQSA_OK;
+}
+
 size_t paged_workspace(const PagedArgs& a) {
   if (a.T == 0) return 0;
   return decode_applies(a) ? decode_workspace(a) : chunk_workspace(a);
@@ -391,6 +428,93 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
   a.causal = causal != 0;
   a.scale = resolve_scale(scale, d);
   return decode_applies(a) ? launch_decode(a, stream) : launch_chunk(a, stream);
+}
+
+int cqsa_kv_page_bounds(const void* k_cache, const unsigned char* k_scale, signed char* bounds, unsigned char* bounds_exp,
+                        const int* block_table, int max_pages, const int* cu_seqlens, const int* kv_lens, int n_seqs, int T,
+                        int max_q_len, int Hkv, int d, int page_size, int n_pages, int dtype, int cache_dtype,
+                        cudaStream_t stream) {
+  set_error("%s", "");
+  CacheArgs c;
+  // (the keys' cache and scales stand in for the values', which are not looked at)
+  const int rc = cache_args(&c, const_cast<void*>(k_cache), const_cast<void*>(k_cache), const_cast<unsigned char*>(k_scale),
+                            const_cast<unsigned char*>(k_scale), block_table, max_pages, cu_seqlens, kv_lens, n_seqs, T, Hkv, d,
+                            page_size, n_pages, dtype, cache_dtype);
+  if (rc != CQSA_OK) return rc;
+  if (max_q_len < 0) return invalid("max_q_len must be >= 0");
+  if (!bounds || !bounds_exp || !aligned(bounds, 16)) return invalid("bounds (16-byte aligned) and bounds_exp must be non-null device pointers");
+  if (T == 0) return CQSA_OK;
+  const BoundsArgs a = {k_cache, k_scale, bounds, bounds_exp, block_table, cu_seqlens, kv_lens, n_seqs, T, Hkv, d, page_size, n_pages,
+                        max_pages, dtype, cache_dtype};
+  return launch_page_bounds(a, max_q_len, stream);
+}
+
+size_t cqsa_attn_selected_workspace_size(int T, int Hq, int Hkv, int d, int page_size, int n_select, int max_kv_len, int dtype,
+                                         int cache_dtype) {
+  SelectArgs s;
+  PagedArgs a;
+  if (selected_sizes(&s, &a, 1, T, Hq, Hkv, d, page_size, n_select, max_kv_len, dtype, cache_dtype) != CQSA_OK || T == 0) return 0;
+  return select_workspace(s) + decode_workspace(a);
+}
+
+int cqsa_attn_selected_fwd(const void* q, long long q_stride, void* out, float* lse, int* pages, const void* k_cache,
+                           const void* v_cache, const unsigned char* k_scale, const unsigned char* v_scale,
+                           const signed char* bounds, const unsigned char* bounds_exp, const int* block_table, int max_pages,
+                           const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int n_select, int max_kv_len, int Hq,
+                           int Hkv, int d, int page_size, int n_pages, float scale, int dtype, int cache_dtype, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  set_error("%s", "");
+  int rc = check_seqs(n_seqs, T, Hq, Hkv, d, scale, dtype);
+  if (rc == CQSA_OK) rc = check_cache(Hkv, k_cache, v_cache, k_scale, v_scale, block_table, max_pages, page_size, n_pages, dtype, cache_dtype);
+  if (rc == CQSA_OK) rc = resolve_stride(&q_stride, Hq, d, "q");
+  SelectArgs s;
+  PagedArgs a;
+  if (rc == CQSA_OK) rc = selected_sizes(&s, &a, n_seqs, T, Hq, Hkv, d, page_size, n_select, max_kv_len, dtype, cache_dtype);
+  if (rc != CQSA_OK) return rc;
+  if (!cu_seqlens || !kv_lens || !aligned(cu_seqlens, 4) || !aligned(kv_lens, 4))
+    return invalid("cu_seqlens and kv_lens must be non-null 4-byte aligned device pointers");
+  if (!bounds || !bounds_exp || !aligned(bounds, 16)) return invalid("bounds (16-byte aligned) and bounds_exp must be non-null device pointers");
+  if (T == 0) return CQSA_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(pages, 4))
+    return invalid("q and out must be non-null 16-byte aligned device pointers (lse and pages 4-byte)");
+  const size_t part = select_workspace(s), need = part + decode_workspace(a);
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) {
+    set_error("a 16-byte aligned workspace of the %zu bytes that cqsa_attn_selected_workspace_size reports is needed (got %zu)",
+              need, workspace ? workspace_bytes : static_cast<size_t>(0));
+    return CQSA_ERR_INVALID;
+  }
+  s.q = q;
+  s.bounds = bounds;
+  s.exps = bounds_exp;
+  s.table = block_table;
+  s.cu = cu_seqlens;
+  s.kv_lens = kv_lens;
+  s.pages = pages;
+  s.workspace = workspace;
+  s.q_stride = q_stride;
+  s.n_pages = n_pages;
+  s.max_pages = max_pages;
+  rc = launch_select(&s, stream);
+  if (rc != CQSA_OK) return rc;
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.table = s.list;
+  a.cu = s.cu_out;
+  a.kv_lens = s.lens_out;
+  a.workspace = static_cast<uint8_t*>(workspace) + part;
+  a.q_stride = q_stride;
+  a.n_pages = n_pages;
+  a.max_pages = n_select;
+  a.row_head = n_select;
+  a.row_seq = static_cast<long long>(Hkv) * n_select;
+  a.causal = 1;
+  a.scale = resolve_scale(scale, d);
+  return launch_decode(a, stream);
 }
 
 }  // extern "C"

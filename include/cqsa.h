@@ -444,6 +444,36 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
                         int Hkv, int d, int page_size, int n_pages, int causal, float scale, int dtype, int cache_dtype,
                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Bounds of a cache's keys by pages, for the selection below: of the pages that hold the sequences' new tokens (or, for each sequence, its last
+ * cu_seqlens[s+1] - cu_seqlens[s] positions; all of them where that is kv_lens[s]), from their slots below kv_lens[s]. bounds: device int8
+ * [n_pages, Hkv, 2, d], 16-byte aligned, the largest and the smallest key of each feature as the nearest (even) whole multiples of 2^(b - 127) for the
+ * byte b in bounds_exp, device [n_pages, Hkv]: the smallest power (2^-126 at least) under which all are at most 127 in magnitude. A page with a
+ * key that is not finite gets the byte 255, and is selected first. Other pages' bounds are left as they were; call it after every write.
+ * T: at least cu_seqlens[n_seqs]; max_q_len: about the most new tokens of a sequence (it sets how the work is split). k_scale: as above. */
+int cqsa_kv_page_bounds(const void* k_cache, const unsigned char* k_scale, signed char* bounds, unsigned char* bounds_exp,
+                        const int* block_table, int max_pages, const int* cu_seqlens, const int* kv_lens, int n_seqs, int T,
+                        int max_q_len, int Hkv, int d, int page_size, int n_pages, int dtype, int cache_dtype,
+                        cudaStream_t stream);
+
+/* Attention of each new token (already written to the cache, its pages' bounds up to date) over n_select pages of its sequence, for each key head its
+ * own: the page that holds the token's position, up to it, and the n_select - 1 pages before that one with the highest scores, the first of
+ * equal ones; all of them where there are fewer. A page's score is max over the query heads h of the key head of
+ * sum_f max(q_hf hi_f, q_hf lo_f) with the page's bounds hi and lo and q in 8 bits as the bounds are, a power of two for each head's vector: whole
+ * numbers times powers of two, the same in any order (an element of q that is not finite counts as 0). out, lse, q and
+ * types as in cqsa_attn_paged_fwd, causal; at most 32 query heads for a key head. pages: device int32 [T, Hkv, n_select] or NULL: the
+ * indices into the sequence's row of block_table, ascending, -1 behind them. max_kv_len: at least the longest kv_lens (pages that begin
+ * there or behind are not selected, but for a token's own). n_select * page_size <= 2^24. Bitwise reproducible for the same arguments and lengths.
+ * workspace: device memory, 16-byte aligned, of at least cqsa_attn_selected_workspace_size bytes for the same arguments; its contents on
+ * entry do not matter. */
+size_t cqsa_attn_selected_workspace_size(int T, int Hq, int Hkv, int d, int page_size, int n_select, int max_kv_len, int dtype,
+                                         int cache_dtype);
+int cqsa_attn_selected_fwd(const void* q, long long q_stride, void* out, float* lse, int* pages, const void* k_cache,
+                           const void* v_cache, const unsigned char* k_scale, const unsigned char* v_scale,
+                           const signed char* bounds, const unsigned char* bounds_exp, const int* block_table, int max_pages,
+                           const int* cu_seqlens, const int* kv_lens, int n_seqs, int T, int n_select, int max_kv_len, int Hq,
+                           int Hkv, int d, int page_size, int n_pages, float scale, int dtype, int cache_dtype, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
 /* Human-readable name of a status code. */
 const char* cqsa_status_string(int status);
 
