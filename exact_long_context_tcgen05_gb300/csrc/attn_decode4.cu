@@ -39,10 +39,12 @@ struct Dec4Cfg {
   static constexpr int LDO = D + 12;  // row of the joining buffer: it also holds a warp's running sum, D / 4 values a lane and column tile and its references
   static constexpr uint32_t JOIN = static_cast<uint32_t>(NMT) * kQuarters * ROWS * LDO * 4;
   static constexpr uint32_t ML = NMT * kQuarters * 2 * ROWS * 4;
+  // a warp's scales of a tile: K's in fp32 by keys, V's in fp16 by 32 features, in the order of the second product's operand
+  static constexpr uint32_t WSC = KW * SPK * 6, WSCALES = NMT * kQuarters * WSC;
   static constexpr int OCC = decode4_occ(ROWS * NMT);
-  static constexpr int NST_MAX = static_cast<int>((232448 / OCC - (OCC - 1) * 1024 - 1024 - 512 - JOIN - ML) / STAGE);
+  static constexpr int NST_MAX = static_cast<int>((232448 / OCC - (OCC - 1) * 1024 - 1024 - 512 - JOIN - ML - WSCALES) / STAGE);
   static constexpr int NST = NST_MAX > 8 ? 8 : NST_MAX;
-  static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + 512;
+  static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + WSCALES + 512;
   static constexpr int NTHR = 32 + 32 * kQuarters * NMT;
   static constexpr int FOLD = 16384 / KT;  // tiles between folds of O into the running sum, as in attn_decode.cu
   static_assert(SMEM <= 232448 && NST >= 2, "shared memory exceeds 227 KiB");
@@ -93,10 +95,16 @@ __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_shared_2u32(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-  return v;
+template <int N>
+__device__ __forceinline__ void ld_shared_n(uint32_t a, uint32_t (&r)[N]) {
+  static_assert(N == 2 || N == 4, "8 or 16 bytes");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
 }
 // A key's scale bytes, one for each 32 features.
 template <int SPK>
@@ -113,7 +121,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* join = reinterpret_cast<float*>(sm + NST * C::STAGE);
   float* ml = join + C::JOIN / 4;  // [NMT][kQuarters][m ROWS | l ROWS]
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ml) + C::ML);
+  uint8_t* wsc = reinterpret_cast<uint8_t*>(ml) + C::ML;  // [NMT * kQuarters][K's floats | V's halves]
+  uint64_t* full = reinterpret_cast<uint64_t*>(wsc + C::WSCALES);
   uint64_t* empty = full + NST;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + NST);
   long long* s_base = reinterpret_cast<long long*>(empty + NST + 1);
@@ -198,6 +207,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
     const int g = lane >> 2, t4 = lane & 3;
     float* jbuf = join + mt * kQuarters * ROWS * C::LDO;
     float* mlb = ml + mt * kQuarters * 2 * ROWS;
+    const uint32_t wk32 = smem_u32(wsc) + warp * C::WSC, wv = wk32 + KW * SPK * 4;
     bool ok = true;
     int it = 0;
     for (long long w = w0; w < w1;) {
@@ -329,28 +339,54 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
         const int k0 = t * KT + kw0;             // its position
         const int left = wk.len - k0;            // positions of the sequence from there
         const uint32_t ksc = sk + 2 * C::TILE + kw0 * SPK, vsc = ksc + C::SCALES;
-        // ---- a lane looks at one key's scales: is there a NaN among the keys', which is the largest of the values'
-        uint32_t kword = scales_of<SPK>(ksc, lane), vword = scales_of<SPK>(vsc, lane);
-        if (lane >= left) kword = vword = 0u;  // slots past the end hold anything
-        const unsigned nans = __ballot_sync(0xffffffffu, ((kword & 0x7f7f7f7fu) + 0x01010101u) & kword & 0x80808080u);
-        uint32_t top = max(vword & 255u, (vword >> 8) & 255u);
-        if (SPK == 4) top = max(top, max((vword >> 16) & 255u, vword >> 24));
-        top = min(__reduce_max_sync(0xffffffffu, top), 247u) >> 3;
-        if (static_cast<int>(top) > ev) {
-          const float a = ev < 0 ? 0.0f : exp2_int_any(ev - static_cast<int>(top));
-          ev = static_cast<int>(top);
+        // ---- each lane turns one key's scales into numbers for its warp: a byte is an fp16 number's upper bits but for the sign (255 a NaN).
+        // V's are relative to 2^(ev - 15), the largest power of two met so far.
+        {
+          uint32_t kword = scales_of<SPK>(ksc, lane), vword = scales_of<SPK>(vsc, lane);
+          if (lane >= left) kword = vword = 0u;  // slots past the end hold anything
+          const uint32_t ve = vword & 0x00ff00ffu, vo = (vword >> 8) & 0x00ff00ffu;
+          const uint32_t most = __vmaxu2(ve, vo);
+          uint32_t top = SPK == 4 ? max(most & 0xffffu, most >> 16) : most;
+          top = min(__reduce_max_sync(0xffffffffu, top), 247u) >> 3;
+          if (static_cast<int>(top) > ev) {
+            const float a = ev < 0 ? 0.0f : exp2_int_any(ev - static_cast<int>(top));
+            ev = static_cast<int>(top);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c)
+              for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o[nt][c][i >> 2][i & 3] *= a;
+                for (int i = 0; i < 8; ++i) o[nt][c][i >> 2][i & 3] *= a;
+          }
+          const uint32_t adj = static_cast<uint32_t>(max(15 - ev, 0)) * 0x04000400u;
+          uint32_t h[2] = {ve * 128u + adj, vo * 128u + adj};
+          if (ev > 15) {
+            const __half2 f2 = __float2half2_rn(pow2i(15 - ev));
+            h[0] = mul2(h[0], *reinterpret_cast<const uint32_t*>(&f2));
+            h[1] = mul2(h[1], *reinterpret_cast<const uint32_t*>(&f2));
+          }
+          // key 16 j + 8 x + 2 t + e at [32 features][t][j][x][e]
+          const uint32_t vat = wv + ((lane >> 1) & 3) * (KW / 2) + (lane >> 3) * 4 + (lane & 1) * 2;
+          st_shared_u16(vat, h[0]);
+          st_shared_u16(vat + 2 * KW, h[1]);
+          const uint32_t ke = (kword & 0x00ff00ffu) * 128u, ko = ((kword >> 8) & 0x00ff00ffu) * 128u;
+          const float2 fe = unpack16(ke, 0), fo = unpack16(ko, 0);
+          if (SPK == 4) {
+            st_shared_u16(vat + 4 * KW, h[0] >> 16);
+            st_shared_u16(vat + 6 * KW, h[1] >> 16);
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(wk32 + lane * 16), "f"(fe.x), "f"(fo.x), "f"(fe.y), "f"(fo.y) : "memory");
+          } else {
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(wk32 + lane * 8), "f"(fe.x), "f"(fo.x) : "memory");
+          }
+          __syncwarp();
         }
         // ---- S^T = K Q^T, 16 keys and 32 features at a time, each 32 features' sums times their key's scale
         float s[KW / 16][NT][4];
 #pragma unroll
         for (int j = 0; j < KW / 16; ++j) {
-          const uint32_t wa = scales_of<SPK>(ksc, j * 16 + g), wb = scales_of<SPK>(ksc, j * 16 + 8 + g);
+          uint32_t fa[SPK], fb[SPK];
+          ld_shared_n<SPK>(wk32 + (j * 16 + g) * (4 * SPK), fa);
+          ld_shared_n<SPK>(wk32 + (j * 16 + 8 + g) * (4 * SPK), fb);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             uint32_t b[4];
@@ -362,9 +398,6 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
               nibbles(b[2 * x], lo);
               nibbles(b[2 * x + 1], hi);
               const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-              // (a byte is the exponent and upper mantissa of an fp32 number, 2^112 too small)
-              const float fa = __uint_as_float(__byte_perm(wa, 0, 0x4440 + gr) * (1u << 20) + (112u << 23));
-              const float fb = __uint_as_float(__byte_perm(wb, 0, 0x4440 + gr) * (1u << 20) + (112u << 23));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -372,22 +405,12 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
                 mma16816<0>(acc, a1, qf[nt][gr][2], qf[nt][gr][3]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const float f = i < 2 ? fa : fb;
+                  const float f = __uint_as_float(i < 2 ? fa[gr] : fb[gr]);
                   s[j][nt][i] = gr == 0 ? acc[i] * f : fmaf(acc[i], f, s[j][nt][i]);
                 }
               }
             }
           }
-        }
-        if (nans) {  // (a scale of 255 stands for NaN)
-#pragma unroll
-          for (int j = 0; j < KW / 16; ++j)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if ((nans >> (j * 16 + 8 * i + g)) & 1u) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s[j][nt][2 * i] = s[j][nt][2 * i + 1] = NAN;
-              }
         }
         // ---- scores in base 2, masks, running maximum, P^T (rounded to fp16) as the second product's operand
         const bool mask = left < KW || k0 + KW > lim_all || !full_rows;
@@ -398,12 +421,19 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
 #pragma unroll
           for (int j = 0; j < KW / 16; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float x = s[j][nt][i] * rs[nt][i & 1];
-              if (mask && k0 + j * 16 + (i >> 1) * 8 + g >= lim[nt][i & 1]) x = -INFINITY;
-              s[j][nt][i] = x;
-              mx[i & 1] = fmaxf(mx[i & 1], x);
-            }
+            for (int i = 0; i < 4; ++i) s[j][nt][i] *= rs[nt][i & 1];
+          if (mask) {
+#pragma unroll
+            for (int j = 0; j < KW / 16; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (k0 + j * 16 + (i >> 1) * 8 + g >= lim[nt][i & 1]) s[j][nt][i] = -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < KW / 16; ++j) {
+            mx[0] = max3(mx[0], s[j][nt][0], s[j][nt][2]);
+            mx[1] = max3(mx[1], s[j][nt][1], s[j][nt][3]);
+          }
           float al[2], mu[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -434,48 +464,14 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
             pf[j][nt][1] = transposed8x8(pack16(pr[2], pr[3], 0));
           }
         }
-        // ---- O^T += V^T P^T, P times the values' scales relative to 2^(ev - 15)
-        const uint32_t adj = static_cast<uint32_t>(max(15 - ev, 0)) * 0x04000400u;
+        // ---- O^T += V^T P^T, P times the values' scales
 #pragma unroll
-        for (int j = 0; j < KW / 16; ++j) {
-          uint32_t svp[SPK][2];  // scales of this lane's keys 2 t4, 2 t4 + 1 (and 8 further) as fp16 pairs
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t sc[2][KW / 8];  // scales of this lane's keys for two times 32 features: [j][x] pairs of 2 t4, 2 t4 + 1
+          ld_shared_n<KW / 8>(wv + (2 * c) * (2 * KW) + t4 * (KW / 2), sc[0]);
+          ld_shared_n<KW / 8>(wv + (2 * c + 1) * (2 * KW) + t4 * (KW / 2), sc[1]);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int key = j * 16 + x * 8 + 2 * t4;
-            // (bytes of slots past the end become 0: their codes are finite, and their probabilities 0)
-            if (SPK == 4) {
-              uint2 ws = ld_shared_2u32(vsc + key * 4);
-              if (left < KW) {
-                if (key >= left) ws.x = 0u;
-                if (key + 1 >= left) ws.y = 0u;
-              }
-              const uint32_t e0 = ws.x & 0x00ff00ffu, e1 = ws.y & 0x00ff00ffu;
-              const uint32_t o0 = (ws.x >> 8) & 0x00ff00ffu, o1 = (ws.y >> 8) & 0x00ff00ffu;
-              svp[0][x] = __byte_perm(e0, e1, 0x5410) * 128u + adj;
-              svp[1][x] = __byte_perm(o0, o1, 0x5410) * 128u + adj;
-              svp[SPK - 2][x] = __byte_perm(e0, e1, 0x7632) * 128u + adj;
-              svp[SPK - 1][x] = __byte_perm(o0, o1, 0x7632) * 128u + adj;
-            } else {
-              uint32_t ws = ld_shared_u32(vsc + key * 2);
-              if (left < KW) {
-                if (key >= left) ws = 0u;
-                else if (key + 1 >= left) ws &= 0xffffu;
-              }
-              svp[0][x] = (ws & 0x00ff00ffu) * 128u + adj;
-              svp[1][x] = ((ws >> 8) & 0x00ff00ffu) * 128u + adj;
-            }
-          }
-          if (ev > 15) {
-            const __half2 f2 = __float2half2_rn(pow2i(15 - ev));
-            const uint32_t f = *reinterpret_cast<const uint32_t*>(&f2);
-#pragma unroll
-            for (int c = 0; c < SPK; ++c) {
-              svp[c][0] = mul2(svp[c][0], f);
-              svp[c][1] = mul2(svp[c][1], f);
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
+          for (int j = 0; j < KW / 16; ++j) {
             uint32_t b[4];
             ldsm4t(sv + sw4_off<C::ROWB>(kw0 + j * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), c * 2 + (lane >> 4)), b);
 #pragma unroll
@@ -487,7 +483,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
               const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]}, a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t p0 = mul2(pf[j][nt][0], svp[gr][0]), p1 = mul2(pf[j][nt][1], svp[gr][1]);
+                const uint32_t p0 = mul2(pf[j][nt][0], sc[x][2 * j]), p1 = mul2(pf[j][nt][1], sc[x][2 * j + 1]);
                 mma16816<0>(o[nt][gr][0], a0, p0, p1);
                 mma16816<0>(o[nt][gr][1], a1, p0, p1);
               }
