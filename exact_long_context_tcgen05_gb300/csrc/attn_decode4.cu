@@ -59,19 +59,35 @@ __device__ __forceinline__ uint32_t sw4_off(int r, int c) {
   return static_cast<uint32_t>(r * 32 + ((c ^ ((r >> 2) & 1)) << 4));
 }
 
+// Constants of the conversion below, in registers that the compiler does not know the values of (it would load them anew for every word).
+struct Magic {
+  uint32_t base, sub0, mul1, sub1;
+  __device__ __forceinline__ Magic() {
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(base));  // 1024, 1024
+    asm volatile("mov.b32 %0, 0xe408e408;" : "=r"(sub0));  // -1032, -1032
+    asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(mul1));  // 1 / 16, 1 / 16
+    asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(sub1));  // -72, -72
+  }
+};
+
 // The four pairs of whole numbers of a word, nibble n of both halves in x[n], as fp16 (exact).
-__device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&x)[4]) {
-  const __half2 m1032 = __floats2half2_rn(-1032.0f, -1032.0f), m72 = __floats2half2_rn(-72.0f, -72.0f);
-  const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
+__device__ __forceinline__ void nibbles(const Magic& k, uint32_t w, uint32_t (&x)[4]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
-    const __half2 a = __hadd2(*reinterpret_cast<__half2*>(&lo), m1032);
-    const __half2 b = __hfma2(*reinterpret_cast<__half2*>(&hi), r16, m72);
-    x[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
-    x[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
+    uint32_t lo, hi;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(lo) : "r"(w), "r"(k.base));  // (w & mask) | base
+    asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(hi) : "r"(w), "r"(k.base));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(x[2 * i]) : "r"(lo), "r"(k.sub0));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(x[2 * i + 1]) : "r"(hi), "r"(k.mul1), "r"(k.sub1));
     w >>= 8;
   }
+}
+
+// A product whose sums begin at zero (named so, the zeros take no registers).
+__device__ __forceinline__ void mma16816_from0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transposed8x8(uint32_t x) {
@@ -207,9 +223,11 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
     const int g = lane >> 2, t4 = lane & 3;
     float* jbuf = join + mt * kQuarters * ROWS * C::LDO;
     float* mlb = ml + mt * kQuarters * 2 * ROWS;
+    const Magic magic;
     const uint32_t wk32 = smem_u32(wsc) + warp * C::WSC, wv = wk32 + KW * SPK * 4;
     bool ok = true;
-    int it = 0;
+    int stage = 0;
+    uint32_t parity = 0;
     for (long long w = w0; w < w1;) {
       const Piece pc = piece_at(wk, w, w1);
       const int h = pc.h, t0 = pc.t0, t1 = pc.t1;
@@ -282,7 +300,6 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
         }
       }
       const int lim_all = p.causal ? wk.len - wk.qlen + 1 : wk.len;  // keys that every row sees
-      const bool full_rows = wk.qlen * p.G >= ROWS * NMT;
       float o[NT][D / 32][2][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -307,7 +324,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
         const float was = sum[(NO + 2 * nt + u) * 32], a = was == -INFINITY ? 0.0f : ex2(was - m[nt][u]);
         return a * exp2_int_any(__float_as_int(sum[(NO + 2 * NT) * 32]) - ev);
       };
-      for (int t = t0; t < t1; ++t, ++it) {
+      for (int t = t0; t < t1; ++t) {
         if (t > t0 && (t - t0) % C::FOLD == 0) {
           const bool have = t - t0 > C::FOLD;
           if (!have) named_sync(1 + mt, 32 * kQuarters);  // the unit before has been read out of the buffer
@@ -331,8 +348,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
           }
           sum[(NO + 2 * NT) * 32] = __int_as_float(ev);
         }
-        const int stage = it % NST;
-        if (ok) ok = wait_or_abort(smem_u32(&full[stage]), (it / NST) & 1u, p.timeout_us, a_abort, &g_decode4_err,
+        if (ok) ok = wait_or_abort(smem_u32(&full[stage]), parity, p.timeout_us, a_abort, &g_decode4_err,
                                    kDevTimeoutKV, 41);
         const uint32_t sk = smem_u32(sm) + stage * C::STAGE, sv = sk + C::TILE;
         const int kw0 = kg * KW;                 // first key of this warp in the tile
@@ -395,13 +411,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
             for (int x = 0; x < 2; ++x) {
               const int gr = 2 * c + x;
               uint32_t lo[4], hi[4];  // keys 0-7 and 8-15
-              nibbles(b[2 * x], lo);
-              nibbles(b[2 * x + 1], hi);
+              nibbles(magic, b[2 * x], lo);
+              nibbles(magic, b[2 * x + 1], hi);
               const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma16816<0>(acc, a0, qf[nt][gr][0], qf[nt][gr][1]);
+                float acc[4];
+                mma16816_from0(acc, a0, qf[nt][gr][0], qf[nt][gr][1]);
                 mma16816<0>(acc, a1, qf[nt][gr][2], qf[nt][gr][3]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -413,7 +429,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
           }
         }
         // ---- scores in base 2, masks, running maximum, P^T (rounded to fp16) as the second product's operand
-        const bool mask = left < KW || k0 + KW > lim_all || !full_rows;
+        // (rows behind the unit's last have queries of zero, and are not written)
+        const bool mask = left < KW || k0 + KW > lim_all;
         uint32_t pf[KW / 16][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -439,11 +456,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
           for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int of = 4; of < 32; of <<= 1) mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], of));
-            const float mn = fmaxf(m[nt][u], mx[u]);
-            mu[u] = mn == -INFINITY ? 0.0f : mn;
-            al[u] = ex2(m[nt][u] - mu[u]);  // 0 while the row has seen nothing
-            mu[u] -= kPShift;
-            m[nt][u] = mn;
+            // The reference may lie up to 1 below the largest score: 2^15 p times a scale below 2 stays below fp16's largest, and rows in
+            // mid-sequence rescale O less often.
+            const float was = m[nt][u];
+            const bool up = mx[u] > was + 1.0f;
+            if (up) m[nt][u] = mx[u];
+            al[u] = up ? ex2(was - mx[u]) : 1.0f;  // (0 for a row that has seen nothing yet)
+            mu[u] = (m[nt][u] == -INFINITY ? 0.0f : m[nt][u]) - kPShift;
             l[nt][u] *= al[u];
           }
           if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
@@ -478,8 +497,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
             for (int x = 0; x < 2; ++x) {
               const int gr = 2 * c + x;
               uint32_t lo[4], hi[4];
-              nibbles(b[2 * x], lo);
-              nibbles(b[2 * x + 1], hi);
+              nibbles(magic, b[2 * x], lo);
+              nibbles(magic, b[2 * x + 1], hi);
               const uint32_t a0[4] = {lo[0], lo[1], hi[0], hi[1]}, a1[4] = {lo[2], lo[3], hi[2], hi[3]};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
@@ -492,6 +511,10 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == NST) {
+          stage = 0;
+          parity ^= 1u;
+        }
       }
       if (t1 - t0 > C::FOLD) {
 #pragma unroll

@@ -1169,6 +1169,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           const int gr = lane % LPR;
           const bool flip4 = gr >= 2;
           const __half2 mul = __floats2half2_rn(1.0f, 0.0625f), add = __floats2half2_rn(-1032.0f, -72.0f);
+          uint32_t base;  // (a register: as a number it would take a second instruction beside the mask)
+          asm volatile("mov.b32 %0, 0x64006400;" : "=r"(base));
 #pragma unroll
           for (int i = 0; i < 32 / RPS; ++i) {
             const int rw = i * RPS + lane / LPR, row = w * 32 + rw;
@@ -1186,7 +1188,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 // a byte's two numbers from its low and high four bits: 1024 + c and 1024 + 16 c as fp16 numbers, then c - 8 (exact)
-                uint32_t x = (__byte_perm(cw, 0, e * 0x1111) & 0x00f0000fu) | 0x64006400u;
+                uint32_t x;
+                asm("lop3.b32 %0, %1, 0x00f0000f, %2, 0xea;" : "=r"(x) : "r"(__byte_perm(cw, 0, e * 0x1111)), "r"(base));  // (. & mask) | base
                 const __half2 y = __hmul2(__hfma2(*reinterpret_cast<__half2*>(&x), mul, add), f2);
                 h[e] = *reinterpret_cast<const uint32_t*>(&y);
               }
