@@ -576,7 +576,7 @@ int decode_ctas(const PagedArgs& a) {
   const long long tiles = (a.max_kv_len + kt - 1) / kt;
   const long long all = ((tiles < 1 ? 1 : tiles) + kUnit) * a.n_seqs * a.Hkv;
   const int rows = decode_rows(a);
-  const int most = sm_count() * (a.cache_dtype == CQSA_INT4 ? decode4_occ(rows) : decode_occ(a.cache_dtype == CQSA_E4M3, rows / 16));
+  const int most = sm_count() * (a.cache_dtype == CQSA_INT4 ? decode4_occ(rows, a.d) : decode_occ(a.cache_dtype == CQSA_E4M3, rows / 16));
   return static_cast<int>(all < most ? all : most);
 }
 

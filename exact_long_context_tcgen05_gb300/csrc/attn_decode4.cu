@@ -41,7 +41,7 @@ struct Dec4Cfg {
   static constexpr uint32_t ML = NMT * kQuarters * 2 * ROWS * 4;
   // a warp's scales of a tile: K's in fp32 by keys, V's in fp16 by 32 features, in the order of the second product's operand
   static constexpr uint32_t WSC = KW * SPK * 6, WSCALES = NMT * kQuarters * WSC;
-  static constexpr int OCC = decode4_occ(ROWS * NMT);
+  static constexpr int OCC = decode4_occ(ROWS * NMT, D);
   static constexpr int NST_MAX = static_cast<int>((232448 / OCC - (OCC - 1) * 1024 - 1024 - 512 - JOIN - ML - WSCALES) / STAGE);
   static constexpr int NST = NST_MAX > 8 ? 8 : NST_MAX;
   static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + WSCALES + 512;

@@ -125,6 +125,7 @@ struct AppendArgs {
   const float* cos_sin; // [max_pos, rot]: cosines of rot / 2 pairs, then their sines
   long long q_stride, max_pos;
   int Hq, rot, interleaved;
+  float minus_zero;     // -0.0f (kv_cache.cu says what for)
 };
 int launch_kv_append(const CacheArgs& a, const AppendArgs& r, cudaStream_t stream);
 

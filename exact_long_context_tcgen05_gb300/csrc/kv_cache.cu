@@ -113,13 +113,20 @@ __device__ __forceinline__ void put_vector(uint8_t* cache, uint8_t* scale, long 
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint32_t b = int4_scale_byte(amax);
-    const float unit = int4_scale(b);
+    const float unit = int4_scale(b), inv = __frcp_rn(unit);
+    // The 32-bit quotient f / unit from the reciprocal: one correction by the remainder, which is exact. The corrected value is within 2^-46 of the
+    // quotient before it is rounded, and a quotient by a number of four significant bits is further than 2^-30 from every border between
+    // two roundings, so it is the rounded quotient. A sum with 1.5 * 2^23 + 8 then leaves the nearest (even) whole number + 8 in its lowest bits.
     uint32_t word = 0;
+    const bool cut = b == 247u;  // the largest scale: magnitudes past 7 of it are held
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int q = min(max(__float2int_rn(__fdiv_rn(f[i], unit)), -7), 7);
-      word |= static_cast<uint32_t>(q + 8) << (4 * i);
+      float q = f[i] * inv;
+      q = fmaf(fmaf(-q, unit, f[i]), inv, q);
+      if (cut) q = fminf(fmaxf(f[i] * inv, -7.0f), 7.0f);
+      word += __float_as_uint(__fadd_rn(q, 12582920.0f)) << (4 * i);
     }
+    word -= 0x4b400000u * 0x11111111u;  // the sums' exponents and upper bits, shifted together
     if (b == 255u) word = 0x88888888u;
     if (on) {
       reinterpret_cast<uint32_t*>(cache)[at * LPV + c] = word;
@@ -256,119 +263,187 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs
 // (x, y) of a token's first `rot` features turns by its position's angle: x cos - y sin, y cos + x sin, each product and sum rounded once
 // in 32 bits (no fused multiply-add), so that the result is the same as from elementary operations in any program.
 //
-// wpt warps share a token: its Hq + 2 Hkv vectors, 16 bytes of 16-bit data a lane as above. Paired features that lie in different
-// lanes (the first half of the rotated ones with the second) are exchanged as they were loaded, four shuffles a vector, which leaves
-// every lane its own 8 features, whatever `rot` is, and quantising as it is for a plain write. The data's loads go out first, then
-// come sequence and position, then the row of the table of cosines and sines beside the page.
-template <int D, int BF16, int KIND>
-__global__ void __launch_bounds__(32 * kAppendWarps) cache_append_kernel(const CacheArgs a, const AppendArgs r, int wpt) {
-  constexpr int LPV = D / 8, VPS = 32 / LPV, AHEAD = 3;
+// wpt warps share a token: its queries, then its keys, then its values. Keys and values lie as in a plain write, 8 features a lane, so that
+// quantising is as there; features that are paired across lanes (the first half of the rotated ones with the second) are exchanged as they were
+// loaded, four shuffles a vector, whatever `rot` is. Queries, most of the data, need no such thing: where all features turn, a
+// lane takes 8 features of the first half and their partners, and turns both (kHalves). The first loads go out before the token's
+// sequence and position are looked up, the row of cosines and sines beside the page. Bound by memory for many tokens, by that chain for few.
+enum : int { kHalves = 0, kNeighbours = 1, kPartHalves = 2 };  // all features, paired by halves; pairs of neighbours; fewer features by halves
+
+// (x cos, y cos') + (x' sin, y' sin') of two features, every product and sum rounded. The assembler makes one multiply-add of a packed product and
+// a packed sum, also of mul.rn and add.rn, so a product is a multiply-add with a -0 that comes as an
+// argument of the kernel (`none`).
+__device__ __forceinline__ float2 turned2(float2 f, float2 c, float2 g, float2 s, float2 none) {
+  return __fadd2_rn(__ffma2_rn(f, c, none), __ffma2_rn(g, s, none));
+}
+
+__device__ __forceinline__ void unpack4x2(const uint4& x, int bf16, float2 (&f)[4]) {
+  f[0] = unpack16(x.x, bf16);
+  f[1] = unpack16(x.y, bf16);
+  f[2] = unpack16(x.z, bf16);
+  f[3] = unpack16(x.w, bf16);
+}
+__device__ __forceinline__ uint4 pack4x2(const float2 (&f)[4], int bf16) {
+  return make_uint4(pack16(f[0].x, f[0].y, bf16), pack16(f[1].x, f[1].y, bf16), pack16(f[2].x, f[2].y, bf16), pack16(f[3].x, f[3].y, bf16));
+}
+
+template <int D, int BF16, int KIND, int MODE>
+__global__ void __launch_bounds__(32 * kAppendWarps, 3) cache_append_kernel(const CacheArgs a, const AppendArgs r, int wpt) {
+  constexpr int LPV = D / 8, VPS = 32 / LPV;                        // lanes of a vector and vectors of a step
+  constexpr int LPQ = MODE == kHalves ? LPV / 2 : LPV, QPS = 32 / LPQ;  // the same of queries
+  constexpr int QB = MODE == kHalves ? 2 : 1, QA = MODE == kHalves ? 2 : 3, KA = 4;  // 16-byte pieces of a lane; steps that are loaded ahead
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long token = static_cast<long long>(blockIdx.x) * (kAppendWarps / wpt) + warp / wpt;
   if (token >= a.T) return;
-  const int part = warp & (wpt - 1), hl = lane / LPV, c = lane % LPV;
-  const int nv = r.Hq + 2 * a.Hkv, step = wpt * VPS;
-  const uint16_t* q = static_cast<const uint16_t*>(r.q) + token * r.q_stride;
-  const uint16_t* k = static_cast<const uint16_t*>(a.k) + token * a.k_stride;
-  const uint16_t* v = static_cast<const uint16_t*>(a.v) + token * a.v_stride;
-  uint4 x[AHEAD];
-  auto load = [&](int i0) {
+  const int part = warp & (wpt - 1), hl = lane / LPV, c = lane % LPV, ql = lane / LPQ, qc = lane % LPQ;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(r.q) + token * r.q_stride) + qc;
+  uint4* q_out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.q_out) + token * r.Hq * D) + qc;
+  uint4 x[QA][QB], y[KA];
+  auto load_q = [&](int h0) {  // (q_out may be q: not through the read-only path)
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int i = i0 + u * step;
-      const uint16_t* from = i < r.Hq ? q + i * D : (i < r.Hq + a.Hkv ? k + (i - r.Hq) * D : v + (i - r.Hq - a.Hkv) * D);
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (i < nv) x[u] = *(reinterpret_cast<const uint4*>(from) + c);  // (q_out may be q: not through the read-only path)
+    for (int u = 0; u < QA; ++u) {
+      const int h = h0 + u * wpt * QPS + ql;
+#pragma unroll
+      for (int b = 0; b < QB; ++b) x[u][b] = h < r.Hq ? q[h * LPV + b * LPQ] : make_uint4(0, 0, 0, 0);
     }
   };
-  load(part * VPS + hl);
+  auto load_kv = [&](const void* from, long long stride, int h0) {
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(from) + token * stride) + c;
+#pragma unroll
+    for (int u = 0; u < KA; ++u) {
+      const int h = h0 + u * wpt * VPS + hl;
+      y[u] = h < a.Hkv ? __ldg(at + h * LPV) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  load_q(part * QPS);
   int s;
   long long pos;
   if (!find_token(a, static_cast<int>(token), lane, &s, &pos)) return;  // behind the last sequence: left as it was
   if (pos < 0 || pos >= r.max_pos) return;
+  load_kv(a.k, a.k_stride, part * VPS);
   const long long row = row_of(a, s, pos, true);
-  // this lane's cosines and sines, the sine's sign for its place in the pair
+  // cosines and sines of this lane's 8 features (of its first 8, for queries by halves); zeros where it turns none
   const int half = r.rot >> 1;
-  const bool turns = 8 * c < r.rot;
-  float cs[8], sn[8];
+  const bool turns = MODE == kHalves || 8 * c < r.rot, second = MODE != kNeighbours && 8 * c >= half;
+  float2 cs[4], sn[4], none;
+  none.x = none.y = r.minus_zero;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = sn[i] = 0.0f;
-  int from = lane;  // where the other of each pair is
+  for (int i = 0; i < 4; ++i) cs[i] = sn[i] = make_float2(0.0f, 0.0f);
   if (turns) {
     const float* at = r.cos_sin + pos * r.rot;
-    if (r.interleaved) {
+    if (MODE == kNeighbours) {
       const float4 c4 = __ldg(reinterpret_cast<const float4*>(at + 4 * c)), s4 = __ldg(reinterpret_cast<const float4*>(at + half + 4 * c));
       const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cs[i] = cc[i >> 1];
-        sn[i] = i & 1 ? ss[i >> 1] : -ss[i >> 1];
+      for (int i = 0; i < 4; ++i) {
+        cs[i] = make_float2(cc[i], cc[i]);
+        sn[i] = make_float2(-ss[i], ss[i]);
       }
     } else {
-      const bool second = 8 * c >= half;
-      const int j = second ? 8 * c - half : 8 * c;
-      from = second ? lane - (half >> 3) : lane + (half >> 3);
+      const int j = MODE == kHalves ? 8 * (c % (LPV / 2)) : (second ? 8 * c - half : 8 * c);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float4 c4 = __ldg(reinterpret_cast<const float4*>(at + j) + i), s4 = __ldg(reinterpret_cast<const float4*>(at + half + j) + i);
-        cs[4 * i] = c4.x; cs[4 * i + 1] = c4.y; cs[4 * i + 2] = c4.z; cs[4 * i + 3] = c4.w;
-        sn[4 * i] = s4.x; sn[4 * i + 1] = s4.y; sn[4 * i + 2] = s4.z; sn[4 * i + 3] = s4.w;
-      }
-      if (!second) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sn[i] = -sn[i];
+        cs[2 * i] = make_float2(c4.x, c4.y);
+        cs[2 * i + 1] = make_float2(c4.z, c4.w);
+        sn[2 * i] = make_float2(s4.x, s4.y);
+        sn[2 * i + 1] = make_float2(s4.z, s4.w);
       }
     }
   }
-  for (int i0 = part * VPS; i0 < nv; i0 += AHEAD * step) {
-    if (i0 != part * VPS) load(i0 + hl);
+  const int other = second ? lane - (half >> 3) : (turns ? lane + (half >> 3) : lane);  // the lane of this one's partners
+  // this lane's 8 features of a vector turned, by halves with the sines' sign for its place in the pair in sn
+  auto turn = [&](const uint4& v, float2 (&f)[4]) {
+    unpack4x2(v, BF16, f);
+    float2 g[4];
+    if (MODE == kNeighbours) {
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      if (i0 + u * step >= nv) break;  // (the same for the whole warp)
-      const int i = i0 + u * step + hl;
-      const bool is_q = i < r.Hq, is_v = i >= r.Hq + a.Hkv, on = i < nv;
-      const int h = is_q ? i : (is_v ? i - r.Hq - a.Hkv : i - r.Hq);
-      float f[8], g[8];
-      unpack8(x[u], BF16, f);
-      if (r.interleaved) {
+      for (int i = 0; i < 4; ++i) g[i] = make_float2(f[i].y, f[i].x);
+    } else {
+      const uint4 w = make_uint4(__shfl_sync(0xffffffffu, v.x, other), __shfl_sync(0xffffffffu, v.y, other),
+                                 __shfl_sync(0xffffffffu, v.z, other), __shfl_sync(0xffffffffu, v.w, other));
+      unpack4x2(w, BF16, g);
+    }
+    if (turns) {  // (what does not turn is left alone: 0 times an infinity would not be)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = f[e ^ 1];
+      for (int i = 0; i < 4; ++i) f[i] = turned2(f[i], cs[i], g[i], sn[i], none);
+    }
+  };
+  auto sign = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (MODE != kNeighbours && !second) sn[i] = make_float2(-sn[i].x, -sn[i].y);
+  };
+  if (MODE != kHalves) sign();
+  for (int h0 = part * QPS; h0 < r.Hq; h0 += QA * wpt * QPS) {
+    if (h0 != part * QPS) load_q(h0);
+#pragma unroll
+    for (int u = 0; u < QA; ++u) {
+      const int h = h0 + u * wpt * QPS + ql;
+      if (h0 + u * wpt * QPS >= r.Hq) break;  // (the same for the whole warp)
+      float2 f[4];
+      if constexpr (MODE == kHalves) {
+        float2 g[4], o[4];
+        unpack4x2(x[u][0], BF16, f);
+        unpack4x2(x[u][QB - 1], BF16, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[i] = turned2(f[i], cs[i], g[i], make_float2(-sn[i].x, -sn[i].y), none);
+          g[i] = turned2(g[i], cs[i], f[i], sn[i], none);
+        }
+        if (h < r.Hq) {
+          q_out[h * LPV] = pack4x2(o, BF16);
+          q_out[h * LPV + LPQ] = pack4x2(g, BF16);
+        }
       } else {
-        uint4 y;
-        y.x = __shfl_sync(0xffffffffu, x[u].x, from);
-        y.y = __shfl_sync(0xffffffffu, x[u].y, from);
-        y.z = __shfl_sync(0xffffffffu, x[u].z, from);
-        y.w = __shfl_sync(0xffffffffu, x[u].w, from);
-        unpack8(y, BF16, g);
+        turn(x[u][0], f);
+        if (h < r.Hq) q_out[h * LPV] = turns ? pack4x2(f, BF16) : x[u][0];
       }
-      const bool turn = turns && !is_v;  // (what does not turn is left alone: 0 times an infinity beside it would not be)
+    }
+  }
+  if (MODE == kHalves) sign();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = turn ? __fadd_rn(__fmul_rn(f[e], cs[e]), __fmul_rn(g[e], sn[e])) : f[e];
-      const uint4 y = make_uint4(pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
-      if (is_q) *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(r.q_out) + (token * r.Hq + h) * D) + c) = turn ? y : x[u];
-      if (i0 + u * step + VPS <= r.Hq) continue;  // queries only (the same for the whole warp)
-      const bool put = on && !is_q && row >= 0;
-      const long long at = row + static_cast<long long>(h) * a.page;
-      uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache);
-      if constexpr (KIND == kCacheSame) {
-        if (put) reinterpret_cast<uint4*>(cache)[at * LPV + c] = turn ? y : x[u];
-      } else {
-        put_vector<KIND, LPV>(cache, is_v ? a.v_scale : a.k_scale, at, c, put, f);
+  for (int kv = 0; kv < 2; ++kv) {
+    uint8_t* cache = static_cast<uint8_t*>(kv ? a.v_cache : a.k_cache);
+    uint8_t* scale = kv ? a.v_scale : a.k_scale;
+    for (int h0 = part * VPS; h0 < a.Hkv; h0 += KA * wpt * VPS) {
+      if (kv) load_kv(a.v, a.v_stride, h0);
+      else if (h0 != part * VPS) load_kv(a.k, a.k_stride, h0);
+#pragma unroll
+      for (int u = 0; u < KA; ++u) {
+        const int h = h0 + u * wpt * VPS + hl;
+        if (h0 + u * wpt * VPS >= a.Hkv) break;  // (the same for the whole warp)
+        const bool put = h < a.Hkv && row >= 0;
+        const long long at = row + static_cast<long long>(h) * a.page;
+        float2 f[4];
+        if (!kv) turn(y[u], f);
+        else if (KIND != kCacheSame) unpack4x2(y[u], BF16, f);
+        if constexpr (KIND == kCacheSame) {
+          if (put) reinterpret_cast<uint4*>(cache)[at * LPV + c] = !kv && turns ? pack4x2(f, BF16) : y[u];
+        } else {
+          float e[8] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+          put_vector<KIND, LPV>(cache, scale, at, c, put, e);
+        }
       }
     }
   }
 }
 
 template <int D, int BF16, int KIND>
+int launch_append(const CacheArgs& a, const AppendArgs& r, cudaStream_t stream) {
+  // A token's chain of loads (counts, position, page and table row) is what a small step takes: its vectors then go to as
+  // many warps as there are. With many tokens a warp each (16,384 tokens of 8 and 2 heads of 64: 25 us against 32 with two warps each).
+  const int wpt = a.T <= 2 * sm_count() ? kAppendWarps : 1, per = kAppendWarps / wpt;
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + per - 1) / per));
+  if (r.interleaved) cache_append_kernel<D, BF16, KIND, kNeighbours><<<grid, 32 * kAppendWarps, 0, stream>>>(a, r, wpt);
+  else if (r.rot == D) cache_append_kernel<D, BF16, KIND, kHalves><<<grid, 32 * kAppendWarps, 0, stream>>>(a, r, wpt);
+  else cache_append_kernel<D, BF16, KIND, kPartHalves><<<grid, 32 * kAppendWarps, 0, stream>>>(a, r, wpt);
+  return cuda_status(cudaGetLastError(), "cache append kernel launch");
+}
+
+template <int D, int BF16, int KIND>
 int launch_t(const CacheArgs& a, const AppendArgs* r, bool write, cudaStream_t stream) {
-  if (r) {
-    // A token's chain of loads (counts, position, page and table row) is what a small step takes: its vectors then go to as
-    // many warps as there are; with many tokens two warps each keep the loads in flight that memory wants.
-    const int wpt = a.T <= 2 * sm_count() ? kAppendWarps : 2, per = kAppendWarps / wpt;
-    const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + per - 1) / per));
-    cache_append_kernel<D, BF16, KIND><<<grid, 32 * kAppendWarps, 0, stream>>>(a, *r, wpt);
-    return cuda_status(cudaGetLastError(), "cache append kernel launch");
-  }
+  if (r) return launch_append<D, BF16, KIND>(a, *r, stream);
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + kWarps - 1) / kWarps));
   if (write) cache_write_kernel<D, BF16, KIND><<<grid, 32 * kWarps, 0, stream>>>(a);
   else cache_read_kernel<D, BF16, KIND><<<grid, 32 * kWarps, 0, stream>>>(a);

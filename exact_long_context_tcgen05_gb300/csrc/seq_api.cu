@@ -358,7 +358,7 @@ int cqsa_kv_cache_append(const void* q, const void* k, const void* v, long long 
   a.v = v;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  const AppendArgs r = {q, q_out, cos_sin, q_stride, max_pos, Hq, rot_dim, interleaved != 0};
+  const AppendArgs r = {q, q_out, cos_sin, q_stride, max_pos, Hq, rot_dim, interleaved != 0, -0.0f};
   return launch_kv_append(a, r, stream);
 }
 
