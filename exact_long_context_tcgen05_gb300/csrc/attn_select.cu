@@ -6,11 +6,9 @@
 // upper bound of the page's dot products. The sums are whole numbers below 2^21 and are scaled by powers of two, so every order of summation
 // gives the same score and every run and program the same choice.
 //
-// Three kernels before the attention: bounds_kernel (a block per page and head that new tokens came into), score_kernel (d / 16 lanes read a page's
-// two vectors, 16 bytes each; dp4a against the group's queries in shared memory, positive parts with the largest, negative ones with the
-// smallest keys; four pages a lane at a time, so that a query's words are read once for them and their sums are added up across the lanes
-// in four exchanges) and select_kernel (a block per token and head: the n-th largest score by a count of its upper, middle and lower bits, then
-// the pages from there on up in ascending order, equal scores first come). The attention itself is attn_decode.cu's and attn_decode4.cu's: each
+// Three kernels before the attention: bounds_kernel (a block per page and head that new tokens came into), score_kernel (the products of pages and
+// queries; bound by the reading of bounds for single tokens) and select_few_kernel or select_kernel (a block per token and head: the n-th largest
+// score, then the pages from there on up in ascending order, equal scores first come). The attention itself is attn_decode.cu's and attn_decode4.cu's: each
 // token is a sequence of its own whose table, one for each key head, lists the pages chosen, its own page last, so that only the end of
 // the last page is masked.
 #include <math.h>
@@ -156,106 +154,188 @@ __device__ __forceinline__ void token_position(const SelectArgs& a, int token, i
   *pos = max(len - n + (token - first), -1);
 }
 
-// Scores of kScorePages pages for a token and key head. Scores are written for the pages before the token's own.
-constexpr int kScoreThreads = 256, kScorePages = 256, kMostHeads = 32;
-template <int D, int BF16>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectArgs a, int token0) {
-  constexpr int LP = D / 16, GROUPS = 32 / LP, STEP = 4 * GROUPS;  // lanes of a page; pages side by side, and of a warp's step
-  __shared__ uint4 s_q[kMostHeads][2][LP];
-  __shared__ int s_e[kMostHeads];
-  __shared__ int s_at[2];
-  const int splits = (a.most_pages + kScorePages - 1) / kScorePages;
+// Scores of pages for some tokens of a sequence and a key head, on the tensor cores (`splits` blocks take kScorePages pages each in turn): 16 pages x (largest | smallest keys), whole
+// numbers that fp16 holds exactly, times (positive | negative parts) of 8 rows' queries; sums stay below 2^22, exact in fp32 in any
+// order. A token's heads are padded to a power of two `gp` of rows, so that its maximum is one over neighbouring columns. The order of
+// the features along the products is the one in which a lane reads 16 bytes of bounds and 32 of queries. Scores are written for
+// the pages before a token's own.
+constexpr int kScoreThreads = 256, kScorePages = kScoreThreads / 32 * 16, kScoreRows = 64;
+__device__ __forceinline__ void product16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two whole numbers of 8 bits (already moved to 0 .. 255) as fp16 numbers.
+__device__ __forceinline__ uint32_t whole2(uint32_t w, uint32_t order) {
+  const uint32_t x = __byte_perm(w, 0x64646464u, order);  // 1024 + byte
+  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&x), __floats2half2_rn(-1152.0f, -1152.0f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ONE: a single tile of 8 rows (single tokens of up to 8 heads), whose fragments need not be kept from one tile of rows to the next.
+template <int D, int BF16, bool ONE>
+__global__ void __launch_bounds__(kScoreThreads, ONE ? 4 : 2) score_kernel(const SelectArgs a, int token0, int tokens, int at_once, int gp, int splits) {
+  constexpr int J = D / 32, LDQ = 2 * D + 8;  // pieces of 16 features that a lane reads of a page, row of the queries
+  constexpr int ROWS = ONE ? 8 : kScoreRows;
+  __shared__ __align__(16) uint16_t s_q[ROWS * LDQ];
+  __shared__ float s_f[ROWS], s_add[ROWS];
+  __shared__ int s_e[ROWS];
   const int unit = static_cast<int>(blockIdx.x / splits), base = static_cast<int>(blockIdx.x % splits) * kScorePages;
-  const int token = token0 + unit / a.Hkv, h = unit % a.Hkv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (warp == 0) {
-    int s, pos;
-    token_position(a, token, lane, &s, &pos);
-    if (lane == 0) {
-      s_at[0] = s;
-      s_at[1] = pos;
+  const int h = unit % a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+  const int page_log2 = 31 - __clz(a.page), last = min(token0 + (unit / a.Hkv + 1) * at_once, token0 + tokens);
+  for (int token = token0 + unit / a.Hkv * at_once; token < last;) {
+    // the tokens of one sequence from `token` on (every warp looks for itself: what follows then waits for nobody)
+    const int s = seq_of_token(a.cu, a.n_seqs, a.T, token, lane);
+    int first = 0, n = 0, pos0 = 0, ns;  // pos0: the first one's position
+    if (s >= 0) {
+      n = seq_tokens(a.cu, s, a.T, &first);
+      pos0 = seq_positions(a.kv_lens, s, static_cast<long long>(a.max_pages) * a.page) - n + (token - first);
+      ns = min(first + n, last) - token;
+    } else {
+      ns = (token < cu_at(a.cu, 0, a.T) ? min(cu_at(a.cu, 0, a.T), last) : last) - token;
     }
-  }
-  __syncthreads();
-  const int page_log2 = 31 - __clz(a.page);
-  const int P = s_at[1] < 0 ? 0 : min(s_at[1] >> page_log2, a.most_pages);
-  if (base >= P) return;
-  // the group's queries as whole numbers, positive and negative parts apart
-  for (int g = warp; g < a.G; g += kScoreThreads / 32) {
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + static_cast<long long>(token) * a.q_stride + static_cast<long long>(h * a.G + g) * D;
-    uint2 x = make_uint2(0, 0);
-    if (lane < D / 4) x = __ldg(reinterpret_cast<const uint2*>(q) + lane);
-    const float2 lo = unpack16(x.x, BF16), hi = unpack16(x.y, BF16);
-    float f[4] = {lo.x, lo.y, hi.x, hi.y}, top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!(fabsf(f[i]) < INFINITY)) f[i] = 0.0f;  // (its row is not a number whatever it attends to)
-      top = fmaxf(top, fabsf(f[i]));
+    const int P = s < 0 || pos0 + ns <= 0 ? 0 : min((pos0 + ns - 1) >> page_log2, a.most_pages);  // pages before the last of them
+    if (base >= P) {  // (the same for the whole block)
+      token += ns;
+      continue;
     }
+    const int* row = a.table + static_cast<long long>(s) * a.max_pages;
+    const int stride = splits * kScorePages;
+    uint4 x[2][J];  // the bounds of pages p0 + g and p0 + 8 + g: fetched a step ahead, the first before the queries are ready
+    int ek[2];
+    auto fetch = [&](int p0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = bound_exponent(top);
-    const float inv = pow2i(-e);
-    uint32_t up = 0, down = 0;
+      for (int u = 0; u < 2; ++u) {
+        const long long blk = static_cast<long long>(page_at(row, min(p0 + 8 * u + g, P - 1), a.n_pages)) * a.Hkv + h;
+        const uint4* at = reinterpret_cast<const uint4*>(a.bounds + blk * (2 * D)) + t4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int v = __float2int_rn(f[i] * inv);
-      up |= static_cast<uint32_t>(max(v, 0)) << (8 * i);
-      down |= (static_cast<uint32_t>(min(v, 0)) & 255u) << (8 * i);
-    }
-    if (lane < D / 4) {
-      reinterpret_cast<uint32_t*>(&s_q[g][0][0])[lane] = up;
-      reinterpret_cast<uint32_t*>(&s_q[g][1][0])[lane] = down;
-    }
-    if (lane == 0) s_e[g] = e;
-  }
-  __syncthreads();
-  int etop = s_e[0];
-  for (int g = 1; g < a.G; ++g) etop = max(etop, s_e[g]);
-  const int c = lane % LP;
-  const int* row = a.table + static_cast<long long>(s_at[0]) * a.max_pages;
-  float* out = a.scores + static_cast<long long>(unit) * a.most_pages;
-  for (int p0 = base + warp * STEP; p0 < min(base + kScorePages, P); p0 += kScoreThreads / 32 * STEP) {
-    uint4 hi[4], lo[4];
-    long long blk[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int p = min(p0 + u * GROUPS + lane / LP, P - 1);
-      blk[u] = static_cast<long long>(page_at(row, p, a.n_pages)) * a.Hkv + h;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint4* at = reinterpret_cast<const uint4*>(a.bounds + blk[u] * (2 * D));
-      hi[u] = __ldg(at + c);
-      lo[u] = __ldg(at + LP + c);
-    }
-    // lane c ends up with page c % 4 of its group
-    const long long mine = c & 2 ? (c & 1 ? blk[3] : blk[2]) : (c & 1 ? blk[1] : blk[0]);
-    const int ek = __ldg(a.exps + mine);
-    float best = -INFINITY;
-    for (int g = 0; g < a.G; ++g) {
-      const uint4 up = s_q[g][0][c], down = s_q[g][1][c];
-      int x[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        int v = __dp4a(static_cast<int>(up.x), static_cast<int>(hi[u].x), 0);
-        v = __dp4a(static_cast<int>(up.y), static_cast<int>(hi[u].y), v);
-        v = __dp4a(static_cast<int>(up.z), static_cast<int>(hi[u].z), v);
-        v = __dp4a(static_cast<int>(up.w), static_cast<int>(hi[u].w), v);
-        v = __dp4a(static_cast<int>(down.x), static_cast<int>(lo[u].x), v);
-        v = __dp4a(static_cast<int>(down.y), static_cast<int>(lo[u].y), v);
-        v = __dp4a(static_cast<int>(down.z), static_cast<int>(lo[u].z), v);
-        x[u] = __dp4a(static_cast<int>(down.w), static_cast<int>(lo[u].w), v);
+        for (int j = 0; j < J; ++j) x[u][j] = __ldg(at + 4 * j);
+        ek[u] = __ldg(a.exps + blk);
       }
-      const bool b0 = c & 1, b1 = c & 2;
-      const int k0 = (b0 ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, b0 ? x[0] : x[1], 1);
-      const int k1 = (b0 ? x[3] : x[2]) + __shfl_xor_sync(0xffffffffu, b0 ? x[2] : x[3], 1);
-      int k = (b1 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, b1 ? k0 : k1, 2);
-      if (LP == 8) k += __shfl_xor_sync(0xffffffffu, k, 4);
-      best = fmaxf(best, ldexpf(static_cast<float>(k), s_e[g] - etop));
+    };
+    if (base + warp * 16 < P) fetch(base + warp * 16);
+    // the queries as whole numbers, positive and negative parts apart; rows without a head are zeros whose scores do not count
+    const int rows = (ns * gp + 7) & ~7;
+    for (int r = warp; r < rows; r += kScoreThreads / 32) {
+      const int i = r / gp, head = r - i * gp;
+      const bool real = i < ns && head < a.G;
+      constexpr int F = D / 32;
+      float f[F], top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < F; ++e) f[e] = 0.0f;
+      if (real) {
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + static_cast<long long>(token + i) * a.q_stride + static_cast<long long>(h * a.G + head) * D + lane * F;
+#pragma unroll
+        for (int e = 0; e < F; e += 2) {
+          const float2 p = unpack16(__ldg(reinterpret_cast<const uint32_t*>(q + e)), BF16);
+          f[e] = p.x;
+          f[e + 1] = p.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < F; ++e) {
+        if (!(fabsf(f[e]) < INFINITY)) f[e] = 0.0f;  // (its row is not a number whatever it attends to)
+        top = fmaxf(top, fabsf(f[e]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int ex = bound_exponent(top);
+      const float inv = pow2i(-ex);
+      uint16_t* to = s_q + r * LDQ + lane * F;
+#pragma unroll
+      for (int e = 0; e < F; e += 2) {
+        const float v0 = rintf(f[e] * inv), v1 = rintf(f[e + 1] * inv);
+        *reinterpret_cast<uint32_t*>(to + e) = pack16(fmaxf(v0, 0.0f), fmaxf(v1, 0.0f), 0);
+        *reinterpret_cast<uint32_t*>(to + D + e) = pack16(fminf(v0, 0.0f), fminf(v1, 0.0f), 0);
+      }
+      if (lane == 0) {
+        s_e[r] = real ? ex : -100000;
+        s_add[r] = real ? 0.0f : -INFINITY;
+      }
     }
-    const int p = p0 + (c & 3) * GROUPS + lane / LP;
-    if (c < 4 && p < min(base + kScorePages, P)) out[p] = ek == 255 ? INFINITY : ldexpf(best, ek - 127) + 0.0f;  // (no -0)
+    __syncthreads();
+    // a head's power of two relative to the largest of its token's heads
+    for (int r = threadIdx.x; r < rows; r += kScoreThreads) {
+      const int r0 = r / gp * gp;
+      int top = -100000;
+      for (int i = r0; i < min(r0 + gp, rows); ++i) top = max(top, s_e[i]);
+      const int k = s_e[r] - top;
+      s_f[r] = k < -126 ? 0.0f : pow2i(k);
+    }
+    __syncthreads();
+    for (int p0 = base + warp * 16; p0 < P; p0 += stride) {
+      // 16 features of two pages as four products' fragments
+      auto fragments = [&](int j, uint32_t (&fr)[4][4]) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t w[4] = {x[u][j].x, x[u][j].y, x[u][j].z, x[u][j].w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t y = w[m] ^ 0x80808080u;
+            fr[m][u] = whole2(y, 0x4140);
+            fr[m][2 + u] = whole2(y, 0x4342);
+          }
+        }
+      };
+      auto multiply = [&](float (&c)[4], const uint32_t (&fr)[4][4], int n0, int j) {
+        const uint4* b = reinterpret_cast<const uint4*>(s_q + (n0 + g) * LDQ) + 2 * t4 + 8 * j;
+        const uint4 lo = b[0], hi = b[1];
+        product16816(c, fr[0], lo.x, lo.y);
+        product16816(c, fr[1], lo.z, lo.w);
+        product16816(c, fr[2], hi.x, hi.y);
+        product16816(c, fr[3], hi.z, hi.w);
+      };
+      uint32_t kept[ONE ? 1 : J][4][4];
+      float c1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        fragments(j, kept[ONE ? 0 : j]);
+        if (ONE) multiply(c1, kept[0], 0, j);
+      }
+      const bool odd0 = ek[0] == 255, odd1 = ek[1] == 255;
+      const float unit0 = odd0 ? 0.0f : pow2i(ek[0] - 127), unit1 = odd1 ? 0.0f : pow2i(ek[1] - 127);
+      if (p0 + stride < P) fetch(p0 + stride);
+      float best[2] = {-INFINITY, -INFINITY};
+      for (int n0 = 0; n0 < (ONE ? 1 : rows); n0 += 8) {
+        float c[4] = {c1[0], c1[1], c1[2], c1[3]};
+        if (!ONE) {
+#pragma unroll
+          for (int j = 0; j < J; ++j) multiply(c, kept[j], n0, j);
+        }
+        const float2 f = *reinterpret_cast<const float2*>(s_f + n0 + 2 * t4), add = *reinterpret_cast<const float2*>(s_add + n0 + 2 * t4);
+        const float v[2][2] = {{c[0] * f.x + add.x, c[1] * f.y + add.y}, {c[2] * f.x + add.x, c[3] * f.y + add.y}};
+        auto put = [&](int i, const float (&w)[2]) {  // token i of the segment, pages g and g + 8
+          const int own = min((pos0 + i) >> page_log2, P);
+          float* out = a.scores + (static_cast<long long>(token - token0 + i) * a.Hkv + h) * a.most_pages;
+          if (i < ns && pos0 + i >= 0) {  // (a page that is not finite comes first; + 0: no -0)
+            if (p0 + g < own) out[p0 + g] = odd0 ? INFINITY : w[0] * unit0 + 0.0f;
+            if (p0 + 8 + g < own) out[p0 + 8 + g] = odd1 ? INFINITY : w[1] * unit1 + 0.0f;
+          }
+        };
+        if (gp == 1) {
+          const float w0[2] = {v[0][0], v[1][0]}, w1[2] = {v[0][1], v[1][1]};
+          put(n0 + 2 * t4, w0);
+          put(n0 + 2 * t4 + 1, w1);
+          continue;
+        }
+        float w[2] = {fmaxf(v[0][0], v[0][1]), fmaxf(v[1][0], v[1][1])};
+        for (int o = 1; 2 * o < min(gp, 8); o <<= 1)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) w[u] = fmaxf(w[u], __shfl_xor_sync(0xffffffffu, w[u], o));
+        if (gp <= 8) {
+          if ((2 * t4 & (gp - 1)) == 0) put((n0 + 2 * t4) / gp, w);
+          continue;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) best[u] = fmaxf(best[u], w[u]);
+        if ((n0 + 8) % gp == 0) {
+          if (t4 == 0) put(n0 / gp, best);
+          best[0] = best[1] = -INFINITY;
+        }
+      }
+    }
+    token += ns;
+    __syncthreads();
   }
 }
 
@@ -265,6 +345,167 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// What a block of the selection works on: a token and key head. Writes, for the first key head, the token as a sequence of its own.
+struct Choice {
+  int seq, pos, page_log2, pages, take;  // pages before the token's own, and how many of them are chosen
+};
+__device__ __forceinline__ Choice choice_of(const SelectArgs& a, int token, int h, int (&s_at)[2]) {
+  if (threadIdx.x < 32) {
+    int s, pos;
+    token_position(a, token, threadIdx.x, &s, &pos);
+    if (threadIdx.x == 0) {
+      s_at[0] = s;
+      s_at[1] = pos;
+    }
+  }
+  __syncthreads();
+  Choice c;
+  c.seq = s_at[0];
+  c.pos = s_at[1];
+  c.page_log2 = 31 - __clz(a.page);
+  c.pages = c.pos < 0 ? 0 : min(c.pos >> c.page_log2, a.most_pages);
+  c.take = min(a.n_select - 1, c.pages);
+  if (h == 0 && threadIdx.x == 0) {
+    const int c0 = cu_at(a.cu, 0, a.T), c1 = cu_at(a.cu, a.n_seqs, a.T);
+    a.cu_out[token] = min(max(token, c0), c1);
+    if (token == a.T - 1) a.cu_out[a.T] = min(max(a.T, c0), c1);
+    a.lens_out[token] = c.pos < 0 ? 0 : (c.take << c.page_log2) + (c.pos & (a.page - 1)) + 1;
+  }
+  return c;
+}
+
+// The block's list of chosen pages, indices into the token's row of the table until here, as the user's list and as pages of the cache; behind them
+// the token's own page, and nothing.
+__device__ __forceinline__ void finish_list(const SelectArgs& a, const Choice& c, const int* row, int* pages, int* list) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n_select; i += blockDim.x) {
+    const int p = i < c.take ? list[i] : (i == c.take && c.pos >= 0 ? c.pos >> c.page_log2 : -1);
+    if (pages) pages[i] = p;
+    list[i] = p >= 0 ? page_at(row, p, a.n_pages) : 0;
+  }
+}
+
+// Scores that shared memory holds: the k-th largest is found two bits at a time by counting, which ends as soon as a bound separates just k
+// (after some ten rounds mostly). Threads and warps take what pages there are, not as many as the longest sequence has.
+constexpr int kFewThreads = 256, kFewPages = 16384;
+__global__ void __launch_bounds__(kFewThreads) select_few_kernel(const SelectArgs a, int token0) {
+  constexpr int W = kFewThreads / 32;
+  extern __shared__ uint32_t s_x[];
+  __shared__ int s_at[2], s_count[2][W][2], s_gt[W], s_eq[W];
+  const int unit = static_cast<int>(blockIdx.x), token = token0 + unit / a.Hkv, h = unit % a.Hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Choice c = choice_of(a, token, h, s_at);
+  if (c.seq < 0) return;  // behind the last sequence: left as it was
+  const int P = c.pages, k = c.take;
+  int* pages = a.pages ? a.pages + (static_cast<long long>(token) * a.Hkv + h) * a.n_select : nullptr;
+  int* list = a.list + (static_cast<long long>(token) * a.Hkv + h) * a.n_select;
+  const int* row = a.table + static_cast<long long>(c.seq) * a.max_pages;
+  if (k > 0) {
+    const float* score = a.scores + static_cast<long long>(unit) * a.most_pages;
+    // `least`: more than it are chosen, and of its equals the first `equals`
+    uint32_t least = 0, hi = 0, lo = 0xffffffffu;
+    int equals = 0;
+#pragma unroll 4
+    for (int i = tid; i < P; i += kFewThreads) {
+      const uint32_t x = ordered(__ldcg(score + i));
+      s_x[i] = x;
+      hi = max(hi, x);
+      lo = min(lo, x);
+    }
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    if (lane == 0) {
+      s_count[1][warp][0] = static_cast<int>(hi);
+      s_count[1][warp][1] = static_cast<int>(lo);
+    }
+    __syncthreads();
+    if (k < P) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        hi = max(hi, static_cast<uint32_t>(s_count[1][w][0]));
+        lo = min(lo, static_cast<uint32_t>(s_count[1][w][1]));
+      }
+      // what the largest and the smallest score have in common all have
+      const int first = (31 - __clz(static_cast<int>((hi ^ lo) | 1u))) & ~1;
+      uint32_t known = first == 30 ? 0u : hi & ~((4u << first) - 1u);  // the k-th largest is at least this
+      bool exact = false;
+      int buf = 0;
+#pragma unroll 1
+      for (int shift = first; shift >= 0; shift -= 2) {
+        const uint32_t b1 = known + (1u << shift), b2 = known + (2u << shift), b3 = known + (3u << shift);
+        int n1 = 0, n2 = 0, n3 = 0;
+#pragma unroll 4
+        for (int i = tid; i < P; i += kFewThreads) {
+          const uint32_t x = s_x[i];
+          n1 += x >= b1;
+          n2 += x >= b2;
+          n3 += x >= b3;
+        }
+        const int both = __reduce_add_sync(0xffffffffu, n1 | n2 << 16);  // (below 2^14 each)
+        n3 = __reduce_add_sync(0xffffffffu, n3);
+        if (lane == 0) {
+          s_count[buf][warp][0] = both;
+          s_count[buf][warp][1] = n3;
+        }
+        __syncthreads();
+        n1 = n2 = n3 = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int v = s_count[buf][w][0];
+          n1 += v & 0xffff;
+          n2 += v >> 16;
+          n3 += s_count[buf][w][1];
+        }
+        buf ^= 1;
+        const int step = n3 >= k ? 3 : (n2 >= k ? 2 : (n1 >= k ? 1 : 0));
+        known += static_cast<uint32_t>(step) << shift;
+        if ((step == 3 && n3 == k) || (step == 2 && n2 == k) || (step == 1 && n1 == k)) {
+          exact = true;
+          break;
+        }
+      }
+      least = exact ? known - 1 : known;  // (a bound that separates k of more is not 0)
+      if (!exact) equals = P;             // as many as there is room for
+    }
+    // chosen pages in ascending order: a warp takes a run of them, counts, and writes from where the runs before it end
+    const int run = ((P + W - 1) / W + 31) & ~31, i0 = warp * run;
+    int gt = 0, eq = 0;
+    for (int i = i0 + lane; i < i0 + run; i += 32) {
+      const uint32_t x = i < P ? s_x[i] : 0u;  // (a score is never 0 here)
+      gt += __popc(__ballot_sync(0xffffffffu, x > least));
+      eq += __popc(__ballot_sync(0xffffffffu, x == least && x != 0u));
+    }
+    if (lane == 0) {
+      s_gt[warp] = gt;
+      s_eq[warp] = eq;
+    }
+    __syncthreads();
+    int above = 0, at = 0, eq_before = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) above += s_gt[w];
+    if (equals) equals = k - above;
+    for (int w = 0; w < warp; ++w) {
+      at += s_gt[w] + min(s_eq[w], max(equals - eq_before, 0));
+      eq_before += s_eq[w];
+    }
+    for (int i = i0 + lane; i < i0 + run; i += 32) {
+      const uint32_t x = i < P ? s_x[i] : 0u;
+      const bool is_eq = x == least && x != 0u;
+      const unsigned be = __ballot_sync(0xffffffffu, is_eq), below = (1u << lane) - 1u;
+      const bool take = x > least || (is_eq && eq_before + __popc(be & below) < equals);
+      const unsigned bt = __ballot_sync(0xffffffffu, take);
+      if (take) {
+        const int to = at + __popc(bt & below);
+        if (to < k) list[to] = i;
+      }
+      at += __popc(bt);
+      eq_before += __popc(be);
+    }
+  }
+  finish_list(a, c, row, pages, list);
+}
+
+// Any number of pages: the k-th largest score by counts of its upper, middle and lower bits in shared memory.
 constexpr int kSelectThreads = 512, kBins = 2048;
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs a, int token0) {
   constexpr int W = kSelectThreads / 32, BPT = kBins / kSelectThreads;
@@ -273,24 +514,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs
   __shared__ uint32_t s_found[2];
   const int unit = static_cast<int>(blockIdx.x), token = token0 + unit / a.Hkv, h = unit % a.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) {
-    int s, pos;
-    token_position(a, token, lane, &s, &pos);
-    if (lane == 0) {
-      s_at[0] = s;
-      s_at[1] = pos;
-    }
-  }
-  __syncthreads();
-  const int s = s_at[0], pos = s_at[1], page_log2 = 31 - __clz(a.page);
-  const int P = pos < 0 ? 0 : min(pos >> page_log2, a.most_pages);
-  const int k = min(a.n_select - 1, P);  // pages beside the token's own
-  if (h == 0 && tid == 0) {  // each token as a sequence of its own
-    const int c0 = cu_at(a.cu, 0, a.T), c1 = cu_at(a.cu, a.n_seqs, a.T);
-    a.cu_out[token] = min(max(token, c0), c1);
-    if (token == a.T - 1) a.cu_out[a.T] = min(max(a.T, c0), c1);
-    a.lens_out[token] = pos < 0 ? 0 : (k << page_log2) + (pos & (a.page - 1)) + 1;
-  }
+  const Choice c = choice_of(a, token, h, s_at);
+  const int s = c.seq, P = c.pages, k = c.take;
   if (s < 0) return;  // behind the last sequence: left as it was
   const float* score = a.scores + static_cast<long long>(unit) * a.most_pages;
   uint32_t least = 0;  // the k-th largest score, and how many of its equals are taken
@@ -372,21 +597,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectArgs
       const unsigned bt = __ballot_sync(0xffffffffu, take);
       if (take) {
         const int to = at + __popc(bt & below);
-        if (to < k) {
-          if (pages) pages[to] = i;
-          list[to] = page_at(row, i, a.n_pages);
-        }
+        if (to < k) list[to] = i;
       }
       at += __popc(bt);
       eq_before += __popc(be);
     }
   }
-  // the token's own page, and nothing behind it
-  for (int i = k + tid; i < a.n_select; i += kSelectThreads) {
-    const bool own = i == k && pos >= 0;
-    if (pages) pages[i] = own ? pos >> page_log2 : -1;
-    list[i] = own ? page_at(row, pos >> page_log2, a.n_pages) : 0;
-  }
+  finish_list(a, c, row, pages, list);
 }
 
 template <int D, int BF16>
@@ -395,6 +612,26 @@ int launch_bounds_d(const BoundsArgs& a, dim3 grid, cudaStream_t stream) {
   else if (a.cache_dtype == CQSA_INT4) bounds_kernel<D, BF16, kCacheInt4><<<grid, kBoundThreads, 0, stream>>>(a);
   else bounds_kernel<D, BF16, kCacheSame><<<grid, kBoundThreads, 0, stream>>>(a);
   return cuda_status(cudaGetLastError(), "page bounds kernel launch");
+}
+
+template <bool ONE>
+int launch_scores(const SelectArgs& a, int token0, int tokens, int at_once, int gp, cudaStream_t stream) {
+  // Blocks for about eight a SM, whatever the longest sequence is: in a ragged batch most are far shorter. (48 sequences of 1,000,000 positions in pages of 32
+  // together, a block for each 256 pages of the longest: 28 us.)
+  const long long units = (tokens + at_once - 1LL) / at_once * a.Hkv, most = (a.most_pages + kScorePages - 1) / kScorePages;
+  const long long want = 8LL * sm_count() / units;
+  const int splits = static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
+  if (units * splits > 0x7fffffffLL) {
+    set_error("selection is too large for one launch (%lld blocks)", units * splits);
+    return CQSA_ERR_UNSUPPORTED;
+  }
+  const unsigned grid = static_cast<unsigned>(units * splits);
+  const bool bf = a.dtype == CQSA_BF16;
+  if (a.d == 64 && bf) score_kernel<64, 1, ONE><<<grid, kScoreThreads, 0, stream>>>(a, token0, tokens, at_once, gp, splits);
+  else if (a.d == 64) score_kernel<64, 0, ONE><<<grid, kScoreThreads, 0, stream>>>(a, token0, tokens, at_once, gp, splits);
+  else if (bf) score_kernel<128, 1, ONE><<<grid, kScoreThreads, 0, stream>>>(a, token0, tokens, at_once, gp, splits);
+  else score_kernel<128, 0, ONE><<<grid, kScoreThreads, 0, stream>>>(a, token0, tokens, at_once, gp, splits);
+  return cuda_status(cudaGetLastError(), "page score kernel launch");
 }
 
 // Tokens whose scores are held at a time: 64 MiB of them, one token's at least.
@@ -434,25 +671,30 @@ int launch_select(SelectArgs* args, cudaStream_t stream) {
   ws += (static_cast<size_t>(a.T) * a.Hkv * a.n_select * 4 + 255) & ~size_t(255);
   a.cu_out = reinterpret_cast<int*>(ws);
   a.lens_out = a.cu_out + a.T + 1;
-  const long long splits = (a.most_pages + kScorePages - 1) / kScorePages;
+  // tokens of a block of scores: as many as a sequence has on average, which share the reading of its bounds, in 64 rows at most
+  const bool few = a.most_pages <= kFewPages;
+  if (few && a.most_pages > 11 * 1024) {  // beyond the 48 KiB (with the kernel's own) that every kernel may use
+    static PerDeviceOnce attr;
+    int dev = 0;
+    if (!attr.done(&dev)) {
+      const cudaError_t e = cudaFuncSetAttribute(select_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewPages * 4);
+      if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(page selection smem)");
+      attr.mark(dev);
+    }
+  }
+  int gp = 1, block_tokens = 1;
+  while (gp < a.G) gp *= 2;
+  while (block_tokens < (a.T + a.n_seqs - 1) / a.n_seqs && 2 * block_tokens * gp <= kScoreRows) block_tokens *= 2;
   for (int t = 0; t < a.T; t += at_once) {
     const int n = a.T - t < at_once ? a.T - t : at_once;
-    const long long units = static_cast<long long>(n) * a.Hkv, blocks = units * splits;
-    if (blocks > 0x7fffffffLL) {
-      set_error("selection is too large for one launch (%lld blocks)", blocks);
-      return CQSA_ERR_UNSUPPORTED;
-    }
-    const unsigned grid = static_cast<unsigned>(blocks);
     if (a.n_select > 1) {
-      const bool bf = a.dtype == CQSA_BF16;
-      if (a.d == 64 && bf) score_kernel<64, 1><<<grid, kScoreThreads, 0, stream>>>(a, t);
-      else if (a.d == 64) score_kernel<64, 0><<<grid, kScoreThreads, 0, stream>>>(a, t);
-      else if (bf) score_kernel<128, 1><<<grid, kScoreThreads, 0, stream>>>(a, t);
-      else score_kernel<128, 0><<<grid, kScoreThreads, 0, stream>>>(a, t);
-      const int rc = cuda_status(cudaGetLastError(), "page score kernel launch");
+      const int rc = block_tokens * gp <= 8 ? launch_scores<true>(a, t, n, block_tokens, gp, stream)
+                                            : launch_scores<false>(a, t, n, block_tokens, gp, stream);
       if (rc != CQSA_OK) return rc;
     }
-    select_kernel<<<static_cast<unsigned>(units), kSelectThreads, 0, stream>>>(a, t);
+    const unsigned units = static_cast<unsigned>(static_cast<long long>(n) * a.Hkv);
+    if (few) select_few_kernel<<<units, kFewThreads, static_cast<unsigned>(a.most_pages) * 4, stream>>>(a, t);
+    else select_kernel<<<units, kSelectThreads, 0, stream>>>(a, t);
     const int rc = cuda_status(cudaGetLastError(), "page selection kernel launch");
     if (rc != CQSA_OK) return rc;
   }

@@ -288,10 +288,10 @@ __device__ __forceinline__ uint4 pack4x2(const float2 (&f)[4], int bf16) {
 }
 
 template <int D, int BF16, int KIND, int MODE>
-__global__ void __launch_bounds__(32 * kAppendWarps, 3) cache_append_kernel(const CacheArgs a, const AppendArgs r, int wpt) {
+__global__ void __launch_bounds__(32 * kAppendWarps, D == 64 ? 4 : 3) cache_append_kernel(const CacheArgs a, const AppendArgs r, int wpt) {
   constexpr int LPV = D / 8, VPS = 32 / LPV;                        // lanes of a vector and vectors of a step
   constexpr int LPQ = MODE == kHalves ? LPV / 2 : LPV, QPS = 32 / LPQ;  // the same of queries
-  constexpr int QB = MODE == kHalves ? 2 : 1, QA = MODE == kHalves ? 2 : 3, KA = 4;  // 16-byte pieces of a lane; steps that are loaded ahead
+  constexpr int QB = MODE == kHalves ? 2 : 1, QA = MODE == kHalves ? 2 : 3, KA = D == 64 ? 2 : 4;  // 16-byte pieces of a lane; steps that are loaded ahead
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long token = static_cast<long long>(blockIdx.x) * (kAppendWarps / wpt) + warp / wpt;
   if (token >= a.T) return;

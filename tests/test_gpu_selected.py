@@ -317,3 +317,31 @@ def test_no_tokens_and_refusals(cq):
             f()
     with pytest.raises(cq.CqsaError):
         cq.attention_selected(q, kc, vc, table, cu, lens, *bounds, 3, -1)
+
+
+@pytest.mark.parametrize("P", [1, 2, 31, 33, 255, 257, 1000, 5000, 11200, 16383, 16384, 20000])
+def test_choice_against_a_sort(cq, P):
+    """Choices of every kind of size among P pages whose scores have many equal values, one sign, or hardly any bits in common."""
+    d, page, g = 64, 16, torch.Generator(device="cuda").manual_seed(P)
+    kc = torch.zeros(P + 1, 1, page, d, dtype=torch.float16, device="cuda")
+    table = torch.arange(P + 1, dtype=torch.int32, device="cuda")[None].contiguous()
+    q = torch.zeros(1, 1, d, dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0  # a page's score is its first bound, largest key
+    cu, lens = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([P * page + 1], dtype=torch.int32, device="cuda")
+    for kind in range(4):
+        bounds = torch.zeros(P + 1, 1, 2, d, dtype=torch.int8, device="cuda")
+        exps = torch.full((P + 1, 1), 127, dtype=torch.uint8, device="cuda")
+        if kind == 0:
+            bounds[..., 0] = torch.randint(-2, 3, (P + 1, 1, 1), generator=g, device="cuda").to(torch.int8)
+        elif kind == 1:
+            bounds[..., 0] = torch.randint(1, 128, (P + 1, 1, 1), generator=g, device="cuda").to(torch.int8)
+        elif kind == 2:
+            bounds[..., 0] = torch.randint(-127, 128, (P + 1, 1, 1), generator=g, device="cuda").to(torch.int8)
+            exps = torch.randint(60, 190, (P + 1, 1), generator=g, device="cuda").to(torch.uint8)
+        score = bounds[:P, 0, 0, 0].double() * torch.exp2(exps[:P, 0].double() - 127)
+        for n_select in sorted({1, 2, P // 2 + 1, P, P + 1, P + 2}):
+            _, pages = cq.attention_selected(q, kc, kc, table, cu, lens, bounds, exps, n_select, P * page + 1, return_pages=True)
+            best = torch.sort(score, dim=0, descending=True, stable=True)[1][:n_select - 1].sort()[0].int()
+            want = torch.full((n_select,), -1, dtype=torch.int32, device="cuda")
+            want[:len(best)], want[len(best)] = best, P
+            assert torch.equal(pages[0, 0], want), (kind, n_select)
