@@ -464,24 +464,29 @@ def attention_backward(q, k, v, out, dout, lse, *, causal=False, scale=None, str
 
 _torch = None
 _codes: dict = {}
+_get_device = _raw_stream = None  # the current device's index; the current stream of a device
 
 
 def _tc():
     """torch, imported by the first call that needs it."""
-    global _torch
+    global _torch, _get_device, _raw_stream
     if _torch is None:
         import torch
-        _torch = torch
         _codes.update({torch.float16: CQSA_F16, torch.bfloat16: CQSA_BF16})
+        # (torch.cuda's functions of the same purpose, without their checks: a tensor on a GPU has been met by then)
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+        _torch = torch
     return _torch
 
 
 def _elsewhere(device, stream):
     """A context that makes `device` current and `stream` its current stream, or None where they already are."""
-    torch = _tc()
+    torch = _torch or _tc()
     if device.type != "cuda":
         raise ValueError("the tensors must be on a CUDA device")
-    here = device.index == torch.cuda.current_device()
+    here = device.index == _get_device()
     if here and stream is None:
         return None
     import contextlib
@@ -497,9 +502,7 @@ def _elsewhere(device, stream):
 
 def _current(device):
     """The cudaStream_t of the device's current stream."""
-    torch = _tc()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return (raw(device.index) if raw else torch.cuda.current_stream(device).cuda_stream) or None
+    return _raw_stream(device.index) or None
 
 
 def _code(dtype):
@@ -537,9 +540,8 @@ def _ints(name, t, shape, device):
 
 
 def _out(out, q):
-    torch = _tc()
     if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return q.new_empty(q.shape)
     if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {tuple(q.shape)} tensor of {q.dtype} on {q.device}")
     return out
@@ -565,30 +567,40 @@ def _scale(name, t, shape, code, d, device):
         if t is not None:
             raise ValueError("a 16-bit cache takes no scales")
         return None
-    want = shape[:3] if code == CQSA_E4M3 else (*shape[:3], d // 32)
-    if t is None or t.element_size() != 1 or t.shape != want or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous byte tensor {tuple(want)} on {device}")
+    if t is None or t.element_size() != 1 or t.device != device or not t.is_contiguous() or t.shape != (
+            shape[:3] if code == CQSA_E4M3 else (shape[0], shape[1], shape[2], d // 32)):
+        raise ValueError(f"{name} must be a contiguous byte tensor, [n_pages, Hkv, page_size] for e4m3 codes and "
+                         f"[n_pages, Hkv, page_size, d / 32] for 4 bits, on {device}")
     return t.data_ptr()
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, kv_lens, dtype, device):
     """The checks that the calls on a paged cache share; returns the cache's dtype code, its head dimension, n_seqs, max_pages, the
     three index tensors and the scales' addresses."""
-    shape = k_cache.shape
-    if device.type != "cuda" or k_cache.device != device or v_cache.device != device:
+    i32, index = (_torch or _tc()).int32, device.index
+    if index is None or k_cache.get_device() != index or v_cache.get_device() != index:
         raise ValueError("k_cache and v_cache must be CUDA tensors on the tokens' device")
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != k_cache.dtype:
+    shape, kind = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache is not k_cache and (v_cache.shape != shape or v_cache.dtype is not kind):
         raise ValueError("k_cache and v_cache must be tensors of one shape and dtype [n_pages, Hkv, page_size, d]")
     if not k_cache.is_contiguous() or not v_cache.is_contiguous():
         raise ValueError("k_cache and v_cache must be contiguous")
-    code, d = _kind(k_cache, k_scale, dtype)
-    ks, vs = _scale("k_scale", k_scale, shape, code, d, device), _scale("v_scale", v_scale, shape, code, d, device)
+    if kind is dtype and k_scale is None and v_scale is None:
+        code, d, ks, vs = _code(dtype), shape[3], None, None
+    else:
+        code, d = _kind(k_cache, k_scale, dtype)
+        ks = _scale("k_scale", k_scale, shape, code, d, device)
+        vs = ks if v_scale is k_scale else _scale("v_scale", v_scale, shape, code, d, device)
     table = block_table.shape
     if len(table) != 2 or kv_lens.shape != table[:1]:
         raise ValueError("block_table must be [n_seqs, max_pages] and kv_lens [n_seqs]")
-    n_seqs = table[0]
-    return (code, d, n_seqs, table[1], _ints("block_table", block_table, table, device),
-            _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), device), _ints("kv_lens", kv_lens, (n_seqs,), device), ks, vs)
+    n_seqs, max_pages = table
+    if not (block_table.dtype is i32 and cu_seqlens.dtype is i32 and kv_lens.dtype is i32 and block_table.get_device() == index
+            and cu_seqlens.get_device() == index and kv_lens.get_device() == index and cu_seqlens.shape == (n_seqs + 1,)
+            and block_table.is_contiguous() and cu_seqlens.is_contiguous() and kv_lens.is_contiguous()):  # (else: what is wrong, or a copy)
+        block_table, cu_seqlens = _ints("block_table", block_table, table, device), _ints("cu_seqlens", cu_seqlens, (n_seqs + 1,), device)
+        kv_lens = _ints("kv_lens", kv_lens, (n_seqs,), device)
+    return code, d, n_seqs, max_pages, block_table, cu_seqlens, kv_lens, ks, vs
 
 
 def _packed(q, k, v, cu_seqlens):
@@ -787,7 +799,7 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
     dt = _code(dtype)
     max_q_len, max_kv_len = min(max_q_len, T), min(max_kv_len, 0x7fffffff)  # (ctypes would cut larger ones down to 32 bits)
     out = _out(out, q)
-    lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if return_lse else None
+    lse = q.new_empty((Hq, T), dtype=torch.float32) if return_lse else None
     if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if workspace is None:
@@ -797,7 +809,7 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
             if len(_sizes) >= 4096:  # (lengths differ from step to step)
                 _sizes.clear()
             size = _sizes[key] = lib.cqsa_attn_paged_workspace_size(*key[:-1])
-        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+        workspace = q.new_empty(size or 16, dtype=torch.uint8)
     else:
         size = workspace.numel() * workspace.element_size()
     _check(lib.cqsa_attn_paged_fwd(q.data_ptr(), qs, out.data_ptr(), lse.data_ptr() if return_lse else None,
@@ -865,8 +877,8 @@ def attention_selected(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, bo
         raise ValueError("n_select must be positive, and n_select * page_size at most 2^24")
     max_kv_len = min(max_kv_len, 0x7fffffff)
     out = _out(out, q)
-    lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if return_lse else None
-    pages = torch.empty((T, Hkv, n_select), dtype=torch.int32, device=device) if return_pages else None
+    lse = q.new_empty((Hq, T), dtype=torch.float32) if return_lse else None
+    pages = q.new_empty((T, Hkv, n_select), dtype=torch.int32) if return_pages else None
     if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     if workspace is None:
@@ -876,7 +888,7 @@ def attention_selected(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, bo
             if len(_sizes) >= 4096:
                 _sizes.clear()
             size = _sizes[key] = lib.cqsa_attn_selected_workspace_size(*key[:-1])
-        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+        workspace = q.new_empty(size or 16, dtype=torch.uint8)
     else:
         size = workspace.numel() * workspace.element_size()
     _check(lib.cqsa_attn_selected_fwd(q.data_ptr(), qs, out.data_ptr(), lse.data_ptr() if return_lse else None,

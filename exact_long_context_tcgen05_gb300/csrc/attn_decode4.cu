@@ -36,19 +36,19 @@ struct Dec4Cfg {
   static constexpr uint32_t TILE = KT * ROWB, SCALES = KT * SPK;
   static constexpr uint32_t STAGE = 2 * (TILE + SCALES);
   static constexpr int ROWS = 8 * NT;
-  static constexpr int LDO = D + 12;  // row of the joining buffer: it also holds a warp's running sum, D / 4 values a lane and column tile and its references
+  static constexpr int LDO = D + 4;   // row of the joining buffer, which also holds a warp's running sum, D / 4 values a lane and column tile
   static constexpr uint32_t JOIN = static_cast<uint32_t>(NMT) * kQuarters * ROWS * LDO * 4;
   static constexpr uint32_t ML = NMT * kQuarters * 2 * ROWS * 4;
   // a warp's scales of a tile: K's in fp32 by keys, V's in fp16 by 32 features, in the order of the second product's operand
   static constexpr uint32_t WSC = KW * SPK * 6, WSCALES = NMT * kQuarters * WSC;
   static constexpr int OCC = decode4_occ(ROWS * NMT, D);
-  static constexpr int NST_MAX = static_cast<int>((232448 / OCC - (OCC - 1) * 1024 - 1024 - 512 - JOIN - ML - WSCALES) / STAGE);
+  static constexpr int NST_MAX = static_cast<int>((233472 / OCC - 1024 - 1024 - 256 - JOIN - ML - WSCALES) / STAGE);
   static constexpr int NST = NST_MAX > 8 ? 8 : NST_MAX;
-  static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + WSCALES + 512;
+  static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + WSCALES + 256;
   static constexpr int NTHR = 32 + 32 * kQuarters * NMT;
   static constexpr int FOLD = 16384 / KT;  // tiles between folds of O into the running sum, as in attn_decode.cu
   static_assert(SMEM <= 232448 && NST >= 2, "shared memory exceeds 227 KiB");
-  static_assert(32 * (NT * D / 4 + 2 * NT + 1) <= ROWS * LDO, "the running sum does not fit the joining buffer");
+  static_assert(32 * NT * D / 4 <= ROWS * LDO, "the running sum does not fit the joining buffer");
   static_assert(STAGE % 512 == 0, "a stage does not begin where its swizzle does");
 };
 
@@ -316,13 +316,13 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
           l[nt][u] = 0.0f;
         }
       int ev = -1;  // exponent (biased by 15) of the value scales that the output sums are relative to
-      // The running sum that O is folded into: this lane's values, then the references that they are relative to. (The
-      // layout of the join below is another, and is written after the next named_sync.)
-      constexpr int NO = NT * D / 4;
+      // The running sum that O is folded into: this lane's values, and the references of the rows and of the values' scales that they are
+      // relative to. (The layout of the join below is another, and is written after the next named_sync.)
       float* sum = jbuf + kg * ROWS * C::LDO + lane;
+      float* refs = mlb + kg * 2 * ROWS;
       auto sum_factor = [&](int nt, int u) -> float {
-        const float was = sum[(NO + 2 * nt + u) * 32], a = was == -INFINITY ? 0.0f : ex2(was - m[nt][u]);
-        return a * exp2_int_any(__float_as_int(sum[(NO + 2 * NT) * 32]) - ev);
+        const float was = refs[nt * 8 + 2 * t4 + u], a = was == -INFINITY ? 0.0f : ex2(was - m[nt][u]);
+        return a * exp2_int_any(__float_as_int(refs[ROWS]) - ev);
       };
       for (int t = t0; t < t1; ++t) {
         if (t > t0 && (t - t0) % C::FOLD == 0) {
@@ -341,12 +341,12 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
                 x = 0.0f;
               }
           }
+          __syncwarp();
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            sum[(NO + 2 * nt) * 32] = m[nt][0];
-            sum[(NO + 2 * nt + 1) * 32] = m[nt][1];
-          }
-          sum[(NO + 2 * NT) * 32] = __int_as_float(ev);
+          for (int nt = 0; nt < NT; ++nt)
+            if (g == 0) *reinterpret_cast<float2*>(refs + nt * 8 + 2 * t4) = make_float2(m[nt][0], m[nt][1]);
+          if (lane == 0) refs[ROWS] = __int_as_float(ev);
+          __syncwarp();
         }
         if (ok) ok = wait_or_abort(smem_u32(&full[stage]), parity, p.timeout_us, a_abort, &g_decode4_err,
                                    kDevTimeoutKV, 41);
@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
       }
       // ---- join the warps' rows: each brings its sums to the common maximum and scale (the values' reference is a power of
       // two that is multiplied out here)
+      __syncwarp();  // (the sum's references lie where the rows' go)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

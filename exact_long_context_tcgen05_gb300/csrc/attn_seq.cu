@@ -172,10 +172,15 @@ struct SeqParams {
   int n_osum;
   int n_seqs, T, Hq, Hkv, G, tpt;  // tpt: tokens of a row tile, floor(128 / G)
   int phases, max_pages, n_pages, page_log2, causal;
+  long long most;  // positions that a sequence's pages can hold
+  // 4-bit pages: where a sequence's keys and values lie as 16-bit numbers, in pages of kFullPage positions of a scratch cache (-1: nowhere), or null. Kernels
+  // of 16-bit pages take the sequences that do, the one of 4-bit pages the others.
+  const int* full;
   float scale_log2;
   unsigned timeout_us;
   int fault;  // test hook: 1 = block 0 never loads key tile 1
 };
+constexpr int kFullPage = 128;
 
 // Feature steps [K0, K1) of S = Q K^T; HALF: bytes from a K tile's first 64 features to the others.
 template <int K0, int K1, uint32_t HALF>
@@ -413,7 +418,8 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           ChunkUnits c;
           c.seq = k;
           c.qlen = seq_tokens(p.cu, k, p.T, &c.first);
-          c.kvlen = seq_positions(p.kv_lens, k, static_cast<long long>(p.max_pages) << p.page_log2);
+          c.kvlen = seq_positions(p.kv_lens, k, p.most);
+          if (p.full && (__ldg(p.full + k) >= 0) != (SRC == kSrcPages)) c.qlen = 0;
           c.per = per;
           c.units = (c.qlen + per - 1) / per;
           c.causal = p.causal;
@@ -542,6 +548,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           const int rows = min(page, BN);
           const int boxes = BN / rows;
           const int* trow = SRC == kSrcPages ? p.table + static_cast<long long>(seq) * p.max_pages : nullptr;
+          const int full = SRC == kSrcPages && p.full ? __ldg(p.full + seq) : -1;
           for (int j = 0; j < n_max; ++j) {
             const int stage = (kb + j) % STAGES;
             const uint32_t round = (kb + j) / STAGES;
@@ -550,7 +557,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
             int pg = 0, y = 0;
             if (SRC == kSrcPages && lane < nb) {  // page entries are fetched before the wait
               const int pos = kbase + j * BN + lane * rows;
-              pg = page_at(trow, pos >> p.page_log2, p.n_pages);
+              pg = full >= 0 ? full + (pos >> p.page_log2) : page_at(trow, pos >> p.page_log2, p.n_pages);
               y = pos & (page - 1);
             }
             const uint32_t bytes = static_cast<uint32_t>(nb) * rows * 128u * KSUB;
@@ -1320,6 +1327,96 @@ __global__ void __launch_bounds__(256) seq_combine_kernel(const SeqParams p) {
   }
 }
 
+// ---- 4-bit pages as 16-bit numbers, for sequences whose keys many row tiles read
+// A tile of 4-bit keys and values costs the converter warps of a CTA some 2,600 cycles beyond what a 16-bit one takes, for every unit of 256 rows that reads
+// it; unpacking it once into memory costs the whole GPU 13 ns, two such tiles' worth on one SM. So a sequence of two full units
+// or more is unpacked first, as far as the scratch pages go, and read as 16-bit pages: 2,048 tokens over 32,000 positions, 32 and 8 heads of
+// 128, 748 us against 1,359. The others go to a second kernel, which short batches do not gain from: 12 ragged sequences, 3,000 tokens over 60,000
+// positions, 8 and 2 heads of 64, some 30 key tiles a CTA (72 by the longest sequence), take 84 us packed and 100 in two kernels.
+constexpr int kFullRows = 512;                      // rows of a sequence and key head from which on it is unpacked
+constexpr int kFullTiles = 96;                      // key tiles of a CTA, by the caller's longest sequence, from which on any is
+constexpr size_t kFullBytes = size_t(512) << 20;    // the most that the scratch pages take
+
+// Where each sequence's scratch pages begin, in the sequences' order while they last. One warp.
+__global__ void __launch_bounds__(32) full_pages_kernel(const int* cu, const int* kv_lens, int n_seqs, int T, int G, long long most, int pages, int* full,
+                                                        int* total) {
+  int used = 0;
+  for (int s0 = 0; s0 < n_seqs; s0 += 32) {
+    const int s = s0 + threadIdx.x;
+    int need = 0;
+    if (s < n_seqs) {
+      int first;
+      const long long rows = static_cast<long long>(seq_tokens(cu, s, T, &first)) * G;
+      if (rows >= kFullRows) need = min((seq_positions(kv_lens, s, most) + kFullPage - 1) / kFullPage, pages + 1);
+    }
+    int upto = need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (static_cast<int>(threadIdx.x) >= o) upto = min(upto + y, pages + 1);
+    }
+    const bool fits = need > 0 && used + upto <= pages;
+    if (s < n_seqs) full[s] = fits ? used + upto - need : -1;
+    const unsigned in = __ballot_sync(0xffffffffu, fits);
+    const int last = in ? 31 - __clz(in) : 0;
+    const int now = __shfl_sync(0xffffffffu, upto, last);
+    if (__any_sync(0xffffffffu, need > 0 && !fits)) {  // what comes behind one that does not fit stays packed
+      if (in) used += now;
+      for (int r = s0 + 32 + threadIdx.x; r < n_seqs; r += 32) full[r] = -1;
+      break;
+    }
+    if (in) used += now;
+  }
+  if (threadIdx.x == 0) *total = used;
+}
+
+// One scratch page of one key head a block: 128 positions' keys and values, a scale's 32 numbers (16 bytes) a thread and step.
+template <int D, int BF16>
+__global__ void __launch_bounds__(256) unpack_kernel(const SeqParams p, const int* total, uint16_t* k_full, uint16_t* v_full) {
+  constexpr int PIECES = D / 32;
+  const int page = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, lane = threadIdx.x & 31;
+  if (page >= __ldg(total)) return;
+  // the last sequence whose pages begin at `page` or before (they rise along the sequences that have any)
+  int seq = -1;
+  for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+    const int b = s0 + lane < p.n_seqs ? __ldg(p.full + s0 + lane) : -1;
+    const unsigned in = __ballot_sync(0xffffffffu, b >= 0 && b <= page);
+    if (in) seq = s0 + 31 - __clz(in);
+  }
+  const int pos0 = (page - __ldg(p.full + seq)) * kFullPage, len = seq_positions(p.kv_lens, seq, p.most);
+  const int* row = p.table + static_cast<long long>(seq) * p.max_pages;
+#pragma unroll
+  for (int i = threadIdx.x; i < kFullPage * PIECES; i += 256) {
+    const int slot = i / PIECES, piece = i % PIECES, pos = pos0 + slot;
+    if (pos >= len) continue;  // (rows behind a sequence's end are masked, and zeroed where they are read)
+    const long long vec = ((static_cast<long long>(page_at(row, pos >> p.page_log2, p.n_pages)) * p.Hkv + h) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
+    const long long to = ((static_cast<long long>(page) * p.Hkv + h) * kFullPage + slot) * D + piece * 32;
+    uint4 x[2];
+    uint32_t b[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      x[kv] = __ldg(reinterpret_cast<const uint4*>(kv ? p.v_cache : p.k_cache) + vec * PIECES + piece);
+      b[kv] = __ldg((kv ? p.v_scale : p.k_scale) + vec * PIECES + piece);
+    }
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const float s = int4_scale(b[kv]);
+      const uint32_t w[4] = {x[kv].x, x[kv].y, x[kv].z, x[kv].w};
+      uint4* dst = reinterpret_cast<uint4*>((kv ? v_full : k_full) + to);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          f[e] = static_cast<float>(static_cast<int>((w[u] >> (4 * e)) & 15u) - 8) * s;
+          if (!BF16) f[e] = f[e] > 65504.0f ? 65504.0f : (f[e] < -65504.0f ? -65504.0f : f[e]);  // (as they are read back)
+        }
+        dst[u] = make_uint4(pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
+      }
+    }
+  }
+}
+
 template <int D, int BF16, int SRC>
 int launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const SeqParams& p, long long grid,
              cudaStream_t stream) {
@@ -1426,10 +1523,93 @@ void fill_common(SeqParams* p, int n_seqs, int T, int Hq, int Hkv, int causal, f
 
 }  // namespace
 
-size_t chunk_workspace(const PagedArgs& a) {
+namespace {
+
+size_t parts_workspace(const PagedArgs& a) {
   const size_t parts = 2 * static_cast<size_t>(chunk_ctas(a)) * chunk_phases(a);
   return parts * kPartRows * (static_cast<size_t>(a.d) + 1) * 4 + parts * sizeof(int4);
 }
+
+// A 4-bit batch read as 16-bit pages: the same but for the cache's type (which sets the phases).
+PagedArgs as_full(const PagedArgs& a) {
+  PagedArgs f = a;
+  f.cache_dtype = a.dtype;
+  f.page = kFullPage;
+  return f;
+}
+
+// Scratch pages of 4-bit sequences, by the caller's counts and longest sequence: as many as the sequences that are long enough may need, within kFullBytes.
+int full_pages(const PagedArgs& a) {
+  const long long G = a.Hq / a.Hkv;
+  if (a.cache_dtype != CQSA_INT4 || a.max_q_len * G < kFullRows) return 0;
+  const long long by_tokens = a.T * G / kFullRows, seqs = by_tokens < a.n_seqs ? by_tokens : a.n_seqs;
+  const long long longest = (a.max_kv_len + kFullPage - 1LL) / kFullPage, want = seqs * longest;
+  if (static_cast<double>(longest) * a.Hkv * (static_cast<double>(a.T) * G / kPartRows) < static_cast<double>(kFullTiles) * chunk_ctas(a)) return 0;
+  const long long most = static_cast<long long>(kFullBytes / (static_cast<size_t>(kFullPage) * a.Hkv * a.d * 4));
+  return static_cast<int>(want < most ? want : most);
+}
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t chunk_workspace(const PagedArgs& a) {
+  const int pages = full_pages(a);
+  if (pages == 0) return parts_workspace(a);
+  const size_t one = parts_workspace(a), two = parts_workspace(as_full(a));
+  return up256(one > two ? one : two) + up256((static_cast<size_t>(a.n_seqs) + 1) * 4) + 2 * static_cast<size_t>(pages) * a.Hkv * kFullPage * a.d * 2;
+}
+
+namespace {
+
+// The parts' place in the workspace, and how a batch is cut.
+int set_split(SeqParams* p, const PagedArgs& a) {
+  const int ctas = chunk_ctas(a);
+  p->phases = chunk_phases(a);
+  const size_t parts = 2 * static_cast<size_t>(ctas) * p->phases;
+  p->part_o = static_cast<float*>(a.workspace);
+  p->part_l = p->part_o + parts * kPartRows * a.d;
+  p->meta = reinterpret_cast<int4*>(p->part_l + parts * kPartRows);
+  p->page_log2 = 31 - __builtin_clz(static_cast<unsigned>(a.page));
+  return ctas;
+}
+
+int launch_pages(SeqParams p, const CUtensorMap& mq, const PagedArgs& a, cudaStream_t stream) {
+  const int ctas = set_split(&p, a), box = a.page < BN ? a.page : BN;
+  CUtensorMap mk, mv;
+  int rc = make_page_map(&mk, a.k_cache, a, box);
+  if (rc == CQSA_OK) rc = make_page_map(&mv, a.v_cache, a, box);
+  return rc == CQSA_OK ? dispatch<kSrcPages>(mq, mk, mv, p, a.d, a.dtype, ctas, stream) : rc;
+}
+
+// Unpacks what full_pages allows for and attends to those sequences.
+int launch_full(SeqParams* p, const CUtensorMap& mq, const PagedArgs& a, int pages, cudaStream_t stream) {
+  const size_t one = parts_workspace(a), two = parts_workspace(as_full(a));
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace) + up256(one > two ? one : two);
+  int* full = reinterpret_cast<int*>(ws);
+  uint16_t* k_full = reinterpret_cast<uint16_t*>(ws + up256((static_cast<size_t>(a.n_seqs) + 1) * 4));
+  uint16_t* v_full = k_full + static_cast<size_t>(pages) * a.Hkv * kFullPage * a.d;
+  p->full = full;
+  full_pages_kernel<<<1, 32, 0, stream>>>(a.cu, a.kv_lens, a.n_seqs, a.T, p->G, p->most, pages, full, full + a.n_seqs);
+  int rc = cuda_status(cudaGetLastError(), "scratch page kernel launch");
+  if (rc != CQSA_OK) return rc;
+  set_split(p, a);
+  const unsigned grid = static_cast<unsigned>(pages) * a.Hkv;
+  const bool bf = a.dtype == CQSA_BF16;
+  if (a.d == 64 && bf) unpack_kernel<64, 1><<<grid, 256, 0, stream>>>(*p, full + a.n_seqs, k_full, v_full);
+  else if (a.d == 64) unpack_kernel<64, 0><<<grid, 256, 0, stream>>>(*p, full + a.n_seqs, k_full, v_full);
+  else if (bf) unpack_kernel<128, 1><<<grid, 256, 0, stream>>>(*p, full + a.n_seqs, k_full, v_full);
+  else unpack_kernel<128, 0><<<grid, 256, 0, stream>>>(*p, full + a.n_seqs, k_full, v_full);
+  rc = cuda_status(cudaGetLastError(), "unpacking kernel launch");
+  if (rc != CQSA_OK) return rc;
+  PagedArgs f = as_full(a);
+  f.k_cache = k_full;
+  f.v_cache = v_full;
+  f.n_pages = pages;
+  return launch_pages(*p, mq, f, stream);
+}
+
+}  // namespace
 
 int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
   SeqParams p;
@@ -1445,24 +1625,18 @@ int launch_chunk(const PagedArgs& a, cudaStream_t stream) {
   p.lse = a.lse;
   p.max_pages = a.max_pages;
   p.n_pages = a.n_pages;
-  p.page_log2 = 31 - __builtin_clz(static_cast<unsigned>(a.page));
-  const int ctas = chunk_ctas(a);
-  p.phases = chunk_phases(a);
-  const size_t parts = 2 * static_cast<size_t>(ctas) * p.phases;
-  p.part_o = static_cast<float*>(a.workspace);
-  p.part_l = p.part_o + parts * kPartRows * a.d;
-  p.meta = reinterpret_cast<int4*>(p.part_l + parts * kPartRows);
+  p.most = static_cast<long long>(a.max_pages) * a.page;
   int rc = osum_slots(&p.osum, &p.n_osum);
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq;
   if (rc == CQSA_OK) rc = make_token_map(&mq, a.q, a.dtype, a.d, a.Hq, a.T, a.q_stride, p.G, p.tpt);
-  // (e4m3 pages are copied as they lie, without maps: the queries' stands in for theirs)
-  if (rc == CQSA_OK && a.cache_dtype == CQSA_E4M3) return dispatch<kSrcE4m3>(mq, mq, mq, p, a.d, a.dtype, ctas, stream);
-  if (rc == CQSA_OK && a.cache_dtype == CQSA_INT4) return dispatch<kSrcInt4>(mq, mq, mq, p, a.d, a.dtype, ctas, stream);
-  const int box = a.page < BN ? a.page : BN;
-  if (rc == CQSA_OK) rc = make_page_map(&mk, a.k_cache, a, box);
-  if (rc == CQSA_OK) rc = make_page_map(&mv, a.v_cache, a, box);
   if (rc != CQSA_OK) return rc;
-  return dispatch<kSrcPages>(mq, mk, mv, p, a.d, a.dtype, ctas, stream);
+  if (a.cache_dtype != CQSA_E4M3 && a.cache_dtype != CQSA_INT4) return launch_pages(p, mq, a, stream);
+  if (const int pages = full_pages(a)) rc = launch_full(&p, mq, a, pages, stream);
+  if (rc != CQSA_OK) return rc;
+  // (these pages are copied as they lie, without maps: the queries' stands in for theirs)
+  const int ctas = set_split(&p, a);
+  return a.cache_dtype == CQSA_E4M3 ? dispatch<kSrcE4m3>(mq, mq, mq, p, a.d, a.dtype, ctas, stream)
+                                    : dispatch<kSrcInt4>(mq, mq, mq, p, a.d, a.dtype, ctas, stream);
 }
 
 int launch_packed(const PackedArgs& a, cudaStream_t stream) {

@@ -374,7 +374,8 @@ int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, vo
  * cqsa_attn_fwd multiplies bf16 P in two parts: a bf16 call moved here from there has about 1.4 times the error. Accumulators are folded
  * into fp32 sums (the tensor core truncates as it accumulates). bf16 values are summed under factors of up to 2^14: results are right while the largest |v| times a sequence's positions stays below 2^113 (about 1e34), beyond that a sum may
  * become infinite where its result is not. Over e4m3 pages, V (and in chunks K) is taken relative to the largest power of two so far in
- * the sequence: chunks lose what lies below 2^-24 of that vector's largest value, single tokens' P V what lies below 2^-28 of it.
+ * the sequence: chunks lose what lies below 2^-24 of that vector's largest value, single tokens' P V what lies below 2^-28 of it. Over 4-bit
+ * pages likewise (with the scales' powers of two), and single tokens' P times a value's scale is rounded to fp16 once more.
  *
  * Every call is asynchronous on `stream` and allocates nothing. Two calls whose work may overlap on the GPU
  * need a workspace each (a captured graph keeps the one it was captured with).
@@ -433,7 +434,9 @@ int cqsa_kv_cache_read(void* k, void* v, const void* k_cache, const void* v_cach
  * the work is split, which moves results by rounding only). At most 32 rows per sequence and key head (max_q_len * Hq / Hkv)
  * run as one split over the keys; more run on tcgen05 in tiles of 128. Bitwise reproducible for the same arguments and
  * lengths. P is rounded to dtype (fp16 for an e4m3
- * cache) for its product with V; sums are fp32. workspace: device memory, 16-byte aligned, of at least
+ * or 4-bit cache) for its product with V; sums are fp32. Over a 4-bit cache, where there is much
+ * to do by T and max_kv_len, sequences with at least 512 rows for a key head are first unpacked to dtype in the workspace (up to 512 MiB), values past fp16's largest held
+ * at it, and read as 16-bit ones, P rounded to dtype. workspace: device memory, 16-byte aligned, of at least
  * cqsa_attn_paged_workspace_size bytes for the same arguments (0: none is needed); its contents on entry do not
  * matter. */
 size_t cqsa_attn_paged_workspace_size(int n_seqs, int T, int Hq, int Hkv, int d, int page_size, int max_q_len, int max_kv_len,

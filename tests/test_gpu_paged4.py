@@ -328,3 +328,91 @@ def test_chunk_nan(cq):
     want[:] = False
     want[19:40, :2] = True
     assert torch.equal(torch.isnan(out), want) and torch.equal(torch.isnan(lse), want[..., 0].T)
+
+
+def _checked(cq, q, kq, vq, kse, vse, table, ks, vs, new, lengths, most, what):
+    """Twice the same bit by bit and captured, and right with either rounding of the probabilities (which sequences are unpacked is the workspace's matter)."""
+    cu, kl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (sq.starts(new), lengths))
+    for causal in (True, False):
+        def run():
+            return cq.attention_paged(q, kq, vq, table, cu, kl, max(new), most, causal=causal, return_lse=True, k_scale=kse, v_scale=vse)
+        out, lse = run()
+        assert all(torch.equal(x, y) for x, y in zip(run(), (out, lse)))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            again = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert cq.cqsa_device_error()[1] == 0
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+        at = 0
+        for s, n in enumerate(new):
+            if n:
+                ref, rl, mass = sq.attend(q[at:at + n], ks[s], vs[s], lengths[s] - n, causal)
+                tol = 1.01 * (sq.U[q.dtype] * ref.abs() + (max(sq.U[q.dtype], 2.0 ** -10) + 2.0 ** -16) * mass) + 2.0 ** -24 + lengths[s] * 2.0 ** -25
+                assert ((out[at:at + n].double() - ref).abs() <= tol).all(), (what, causal, s)
+                sq.check_lse(lse[:, at:at + n], rl, f"{what} {causal} {s}")
+            at += n
+
+
+def _space(cq, q, new, hkv, page, most, packed):
+    """The workspace's size beyond what the packed kernel alone needs (a longest length of 1 asks for no more)."""
+    T, hq, d = q.shape
+    size = [cq.cqsa_attn_paged_workspace_size(len(new), T, hq, hkv, d, page, max(new), m, cq.dtype_code(q.dtype), cq.CQSA_INT4) for m in (most, packed)]
+    return size[0] - size[1]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_unpacked_sequences(cq, d, dt):
+    """A batch whose longer sequences are unpacked (by a longest length that says much work) or not: lengths beside multiples of a scratch page, sequences
+    without positions and of a few tokens among them."""
+    new = [130, 1, 128, 0, 127, 300, 129, 4, 200]
+    lengths = [129, 900, 128, 70, 1000, 2049, 0, 40, 3000]
+    hq, hkv, page = 8, 2, 16
+    ks, vs, *cache = make_cache4(lengths, hkv, d, page, 5, (0, 2, -1))
+    q = sq.normal((sum(new), hq, d), sq.DT[dt], 3)
+    assert _space(cq, q, new, hkv, page, 100_000, 3000) > 200 << 20
+    for most in (100_000, 3000, 0):
+        _checked(cq, q, *cache, ks, vs, new, lengths, most, most)
+
+
+def test_more_than_the_scratch_pages(cq):
+    """Sequences longer than the caller said: the first are unpacked as far as the scratch pages go, the others are read packed."""
+    d, hq, hkv, page = 64, 32, 8, 64
+    new, lengths = [1500, 900, 20, 1700, 1000, 600, 64, 2000], [1500, 1000, 700, 6000, 5000, 600, 640, 4100]
+    ks, vs, *cache = make_cache4(lengths, hkv, d, page, 6)
+    q = sq.normal((sum(new), hq, d), torch.float16, 3)
+    # 16 pages of 128 for each of 8 sequences; the six that are long enough need 145
+    assert 128 * 128 * hkv * d * 4 <= _space(cq, q, new, hkv, page, 2000, 500) < 200 * 128 * hkv * d * 4
+    _checked(cq, q, *cache, ks, vs, new, lengths, 2000, "2000")
+
+
+def test_unpacked_extremes(cq):
+    """Values past fp16's largest are held at it where a sequence is unpacked to fp16, a NaN scale stays one, and bf16 holds all of a 4-bit cache's range."""
+    d, hq, hkv, page, n, new = 128, 8, 2, 32, 400, 130
+    for dt in ("f16", "bf16"):
+        ks, vs, kq, vq, kse, vse, table = make_cache4([n], hkv, d, page, 9)
+        t = torch.arange(n, device="cuda")
+        pg, slot = table[0].long()[t // page], t % page
+        big = vse.clone()
+        big[pg, :, slot, 0] = 246  # scales of 14 / 8 * 2^15 = 57,344: multiples up to 401,408
+        v64 = s4.values4(vq[pg, :, slot], big[pg, :, slot])
+        if dt == "f16":
+            v64 = v64.clamp(-65504, 65504)
+        q = sq.normal((new, hq, d), sq.DT[dt], 3)
+        cu, lens = torch.tensor([0, new], dtype=torch.int32, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
+
+        def run(v_scale):  # (a longest length that says much work: the sequence is unpacked)
+            return cq.attention_paged(q, kq, vq, table, cu, lens, new, 1_000_000, k_scale=kse, v_scale=v_scale)
+        out = run(big)
+        ref, rl, mass = sq.attend(q, ks[0], v64, n - new, True)
+        tol = 1.01 * (sq.U[q.dtype] * ref.abs() + (max(sq.U[q.dtype], 2.0 ** -10) + 2.0 ** -16) * mass) + 2.0 ** -24
+        fits = ref.abs() < (60000 if dt == "f16" else 1e9)
+        assert ((out.double() - ref).abs() <= tol)[fits].all()
+        bad = vse.clone()
+        bad[pg[100], 1, slot[100], 1] = 255
+        out = run(bad)
+        want = torch.zeros_like(out, dtype=torch.bool)
+        want[:, 4:, 32:64] = True
+        assert torch.equal(torch.isnan(out), want)
