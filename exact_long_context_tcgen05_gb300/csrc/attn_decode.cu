@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
           }
         }
         // ---- scores in base 2, masks, running maximum
-        const bool mask = left < KW || k0 + KW > lim_all || lim[0] == 0 || lim[1] == 0;
+        // (rows behind the unit's last have queries of zero, and are not written)
+        const bool mask = left < KW || k0 + KW > lim_all;
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < KW / 8; ++j)
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
           mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
           const float mn = fmaxf(m[u], mx[u]);
           mu[u] = mn == -INFINITY ? 0.0f : mn;
-          al[u] = ex2(m[u] - mu[u]);  // 0 while the row has seen nothing
+          al[u] = m[u] == mn ? 1.0f : ex2(m[u] - mu[u]);  // (a row that has seen nothing yet is 0 either way)
           mu[u] -= kPShift;
           m[u] = mn;
           l[u] *= al[u];

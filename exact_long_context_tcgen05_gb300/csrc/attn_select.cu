@@ -216,41 +216,48 @@ __global__ void __launch_bounds__(kScoreThreads, ONE ? 4 : 2) score_kernel(const
     if (base + warp * 16 < P) fetch(base + warp * 16);
     // the queries as whole numbers, positive and negative parts apart; rows without a head are zeros whose scores do not count
     const int rows = (ns * gp + 7) & ~7;
-    for (int r = warp; r < rows; r += kScoreThreads / 32) {
-      const int i = r / gp, head = r - i * gp;
-      const bool real = i < ns && head < a.G;
-      constexpr int F = D / 32;
-      float f[F], top = 0.0f;
+    constexpr int F = D / 32, RA = ONE ? 1 : 4, RS = kScoreThreads / 32;  // features of a lane; rows whose loads go out together, and their distance
+    for (int r0 = warp; r0 < rows; r0 += RA * RS) {
+      float f[RA][F], top[RA];
 #pragma unroll
-      for (int e = 0; e < F; ++e) f[e] = 0.0f;
-      if (real) {
+      for (int u = 0; u < RA; ++u) {
+        const int r = r0 + u * RS, i = r / gp, head = r - i * gp;
         const uint16_t* q = static_cast<const uint16_t*>(a.q) + static_cast<long long>(token + i) * a.q_stride + static_cast<long long>(h * a.G + head) * D + lane * F;
 #pragma unroll
         for (int e = 0; e < F; e += 2) {
-          const float2 p = unpack16(__ldg(reinterpret_cast<const uint32_t*>(q + e)), BF16);
-          f[e] = p.x;
-          f[e + 1] = p.y;
+          const float2 p = unpack16(r < rows && i < ns && head < a.G ? __ldg(reinterpret_cast<const uint32_t*>(q + e)) : 0u, BF16);
+          f[u][e] = p.x;
+          f[u][e + 1] = p.y;
         }
       }
 #pragma unroll
-      for (int e = 0; e < F; ++e) {
-        if (!(fabsf(f[e]) < INFINITY)) f[e] = 0.0f;  // (its row is not a number whatever it attends to)
-        top = fmaxf(top, fabsf(f[e]));
+      for (int u = 0; u < RA; ++u) {
+        top[u] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < F; ++e) {
+          if (!(fabsf(f[u][e]) < INFINITY)) f[u][e] = 0.0f;  // (its row is not a number whatever it attends to)
+          top[u] = fmaxf(top[u], fabsf(f[u][e]));
+        }
+        top[u] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top[u])));  // (bits of numbers from 0 on are in order)
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int ex = bound_exponent(top);
-      const float inv = pow2i(-ex);
-      uint16_t* to = s_q + r * LDQ + lane * F;
+      for (int u = 0; u < RA; ++u) {
+        const int r = r0 + u * RS, i = r / gp, head = r - i * gp;
+        if (r >= rows) break;
+        const bool real = i < ns && head < a.G;
+        const int ex = bound_exponent(top[u]);
+        const float inv = pow2i(-ex);
+        uint16_t* to = s_q + r * LDQ + lane * F;
 #pragma unroll
-      for (int e = 0; e < F; e += 2) {
-        const float v0 = rintf(f[e] * inv), v1 = rintf(f[e + 1] * inv);
-        *reinterpret_cast<uint32_t*>(to + e) = pack16(fmaxf(v0, 0.0f), fmaxf(v1, 0.0f), 0);
-        *reinterpret_cast<uint32_t*>(to + D + e) = pack16(fminf(v0, 0.0f), fminf(v1, 0.0f), 0);
-      }
-      if (lane == 0) {
-        s_e[r] = real ? ex : -100000;
-        s_add[r] = real ? 0.0f : -INFINITY;
+        for (int e = 0; e < F; e += 2) {
+          const float v0 = rintf(f[u][e] * inv), v1 = rintf(f[u][e + 1] * inv);
+          *reinterpret_cast<uint32_t*>(to + e) = pack16(fmaxf(v0, 0.0f), fmaxf(v1, 0.0f), 0);
+          *reinterpret_cast<uint32_t*>(to + D + e) = pack16(fminf(v0, 0.0f), fminf(v1, 0.0f), 0);
+        }
+        if (lane == 0) {
+          s_e[r] = real ? ex : -100000;
+          s_add[r] = real ? 0.0f : -INFINITY;
+        }
       }
     }
     __syncthreads();
