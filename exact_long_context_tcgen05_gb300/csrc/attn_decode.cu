@@ -41,9 +41,11 @@ namespace {
 
 __device__ DevErr g_decode_err;
 
-constexpr int decode_occ(bool e4m3, int nmt) { return e4m3 && nmt == 1 ? 2 : 1; }
+// CTAs of an SM. Over selected pages, most of which L2 holds, two also over 16-bit pages: the warps' chain of products and exponentials sets
+// the pace there, not memory (200 tokens of 32 and 8 heads of 128, 16 pages of 64 each: the call takes 176 us with one, 153 with two).
+constexpr int decode_occ(bool e4m3, int nmt, bool selected) { return nmt == 1 && (e4m3 || selected) ? 2 : 1; }
 
-template <int D, bool E4M3, int NMT>
+template <int D, bool E4M3, int NMT, int CTAS>
 struct DecCfg {
   static constexpr int KT = E4M3 ? 128 : (D == 64 ? 128 : 64);   // keys of a tile
   static constexpr int KW = KT / kQuarters;                      // keys of a warp
@@ -55,7 +57,7 @@ struct DecCfg {
   static constexpr uint32_t JOIN = static_cast<uint32_t>(NMT) * kQuarters * 16 * LDO * 4;
   static constexpr uint32_t ML = NMT * kQuarters * 32 * 4;            // m and l of each warp's rows
   // CTAs of an SM
-  static constexpr int OCC = decode_occ(E4M3, NMT);
+  static constexpr int OCC = CTAS;
   static constexpr int NST_MAX = static_cast<int>((232448 / OCC - (OCC - 1) * 1024 - 1024 - 512 - JOIN - ML) / STAGE);
   static constexpr int NST = NST_MAX > 6 ? 6 : NST_MAX;
   static constexpr uint32_t SMEM = 1024 + NST * STAGE + JOIN + ML + 512;
@@ -81,10 +83,10 @@ __device__ __forceinline__ uint32_t tile16_off(int r, int c) {
   return static_cast<uint32_t>((r >> 3) * (1024 * (D / 64)) + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-template <int D, int BF16, bool E4M3, int NMT>
-__global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NMT>::OCC)
+template <int D, int BF16, bool E4M3, int NMT, int CTAS>
+__global__ void __launch_bounds__(DecCfg<D, E4M3, NMT, CTAS>::NTHR, CTAS)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const DecParams p) {
-  using C = DecCfg<D, E4M3, NMT>;
+  using C = DecCfg<D, E4M3, NMT, CTAS>;
   constexpr int KT = C::KT, KW = C::KW, NST = C::NST, NTHR = C::NTHR;
   constexpr int MB = E4M3 ? 0 : BF16;  // type of the products: e4m3 pages are fp16 after conversion
   extern __shared__ uint8_t smem_raw[];
@@ -539,10 +541,10 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT>::NTHR, DecCfg<D, E4M3, NM
   __syncthreads();
 }
 
-template <int D, int BF16, bool E4M3, int NMT>
+template <int D, int BF16, bool E4M3, int NMT, int CTAS>
 int launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, int ctas, cudaStream_t stream) {
-  using C = DecCfg<D, E4M3, NMT>;
-  auto kern = decode_kernel<D, BF16, E4M3, NMT>;
+  using C = DecCfg<D, E4M3, NMT, CTAS>;
+  auto kern = decode_kernel<D, BF16, E4M3, NMT, CTAS>;
   static PerDeviceOnce attr;
   int dev = 0;
   if (!attr.done(&dev)) {
@@ -557,7 +559,9 @@ int launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, i
 
 template <int D, int BF16, bool E4M3>
 int launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, int rows, int ctas, cudaStream_t s) {
-  return rows <= 16 ? launch_t<D, BF16, E4M3, 1>(mk, mv, p, ctas, s) : launch_t<D, BF16, E4M3, 2>(mk, mv, p, ctas, s);
+  if (rows > 16) return launch_t<D, BF16, E4M3, 2, 1>(mk, mv, p, ctas, s);
+  if (E4M3 || p.row_head != 0) return launch_t<D, BF16, E4M3, 1, 2>(mk, mv, p, ctas, s);
+  return launch_t<D, BF16, E4M3, 1, E4M3 ? 2 : 1>(mk, mv, p, ctas, s);
 }
 
 int tile_keys(const PagedArgs& a) {
@@ -577,7 +581,7 @@ int decode_ctas(const PagedArgs& a) {
   const long long tiles = (a.max_kv_len + kt - 1) / kt;
   const long long all = ((tiles < 1 ? 1 : tiles) + kUnit) * a.n_seqs * a.Hkv;
   const int rows = decode_rows(a);
-  const int most = sm_count() * (a.cache_dtype == CQSA_INT4 ? decode4_occ(rows, a.d) : decode_occ(a.cache_dtype == CQSA_E4M3, rows / 16));
+  const int most = sm_count() * (a.cache_dtype == CQSA_INT4 ? decode4_occ(rows, a.d) : decode_occ(a.cache_dtype == CQSA_E4M3, rows / 16, a.row_head != 0));
   return static_cast<int>(all < most ? all : most);
 }
 

@@ -245,6 +245,8 @@ int selected_sizes(SelectArgs* s, PagedArgs* a, int n_seqs, int T, int Hq, int H
   }
   rc = paged_sizes(a, T < 1 ? 1 : T, T, Hq, Hkv, d, page, 1, n_select * page, dtype, cache_dtype);
   if (rc != CQSA_OK) return rc;
+  a->row_head = n_select;
+  a->row_seq = static_cast<long long>(Hkv) * n_select;
   memset(s, 0, sizeof(*s));
   s->n_seqs = n_seqs;
   s->T = T;
@@ -510,8 +512,6 @@ int cqsa_attn_selected_fwd(const void* q, long long q_stride, void* out, float* 
   a.q_stride = q_stride;
   a.n_pages = n_pages;
   a.max_pages = n_select;
-  a.row_head = n_select;
-  a.row_seq = static_cast<long long>(Hkv) * n_select;
   a.causal = 1;
   a.scale = resolve_scale(scale, d);
   return launch_decode(a, stream);
