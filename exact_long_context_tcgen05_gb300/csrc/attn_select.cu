@@ -623,10 +623,11 @@ int launch_bounds_d(const BoundsArgs& a, dim3 grid, cudaStream_t stream) {
 
 template <bool ONE>
 int launch_scores(const SelectArgs& a, int token0, int tokens, int at_once, int gp, cudaStream_t stream) {
-  // Blocks for about eight a SM, whatever the longest sequence is: in a ragged batch most are far shorter. (48 sequences of 1,000,000 positions in pages of 32
-  // together, a block for each 256 pages of the longest: 28 us.)
+  // Blocks for so many a SM, whatever the longest sequence is: in a ragged batch most are far shorter. (48 sequences of 1,000,000 positions in pages of
+  // 32 together, the whole call: 94 us with 4, 73 with 8, 71 with 12, 77 with 40. Blocks of several tiles of rows begin with more work: 46 us with 4 and 49
+  // with 8 for 60 tokens over 400,000 positions.)
   const long long units = (tokens + at_once - 1LL) / at_once * a.Hkv, most = (a.most_pages + kScorePages - 1) / kScorePages;
-  const long long want = 8LL * sm_count() / units;
+  const long long want = static_cast<long long>(ONE ? 12 : 4) * sm_count() / units;
   const int splits = static_cast<int>(want < 1 ? 1 : (want < most ? want : most));
   if (units * splits > 0x7fffffffLL) {
     set_error("selection is too large for one launch (%lld blocks)", units * splits);
