@@ -875,7 +875,7 @@ def attention_selected(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, bo
     dt = _code(dtype)
     if n_select < 1 or n_select * page > 1 << 24:
         raise ValueError("n_select must be positive, and n_select * page_size at most 2^24")
-    max_kv_len = min(max_kv_len, 0x7fffffff)
+    max_kv_len = min(max_kv_len, max_pages * page)  # (there is a score for each page up to it)
     out = _out(out, q)
     lse = q.new_empty((Hq, T), dtype=torch.float32) if return_lse else None
     pages = q.new_empty((T, Hkv, n_select), dtype=torch.int32) if return_pages else None
