@@ -459,12 +459,14 @@ def attention_backward(q, k, v, out, dout, lse, *, causal=False, scale=None, str
 
 # Sequences of different lengths: torch conveniences (checks and marshalling only). They run on the tensors' own
 # device, whichever is current, on `stream` (a torch stream or a cudaStream_t value) or that device's current
-# stream; what they allocate belongs to that stream. A serving step makes one of these calls per layer, so they look at
-# each tensor once and pass addresses straight on.
+# stream; what they allocate belongs to that stream. A serving step makes several of these calls per layer, so those over a cache
+# first hand their arguments to a compiled function that does the same for ordinary ones (csrc/binding.cpp), and look at them
+# themselves where that returns None: something to refuse, to copy, or to run on another device or stream.
 
 _torch = None
 _codes: dict = {}
 _get_device = _raw_stream = None  # the current device's index; the current stream of a device
+_fast = None  # the compiled functions
 
 
 def _tc():
@@ -503,6 +505,22 @@ def _elsewhere(device, stream):
 def _current(device):
     """The cudaStream_t of the device's current stream."""
     return _raw_stream(device.index) or None
+
+
+def _compiled():
+    """The compiled functions, loaded by the first call."""
+    global _fast
+    if _fast is None:
+        import importlib.machinery
+        import importlib.util
+        torch = _tc()
+        path = os.path.join(_PKG, "_build", f"cqsa_torch-{torch.__version__}.so")
+        if not os.path.exists(path):
+            raise ImportError(f"the torch binding is not built ({path}); run `python -m exact_long_context_tcgen05_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("cqsa_torch", path)
+        _fast = importlib.util.module_from_spec(importlib.util.spec_from_file_location("cqsa_torch", path, loader=loader))
+        loader.exec_module(_fast)
+    return _fast
 
 
 def _code(dtype):
@@ -674,6 +692,11 @@ def kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, *, 
     """New tokens k, v [T, Hkv, d] into their pages of the caches [n_pages, Hkv, page_size, d] (k's dtype, or
     uint8 / float8_e4m3fn codes with byte tensors k_scale, v_scale [n_pages, Hkv, page_size], or 4 bits: uint8
     [n_pages, Hkv, page_size, d / 2] with byte tensors [n_pages, Hkv, page_size, d / 32])."""
+    if stream is None:
+        rc = (_fast or _compiled()).kv_cache_write(k, v, k_cache, v_cache, block_table, cu_seqlens, kv_lens, k_scale, v_scale)
+        if rc is not None:
+            _check(rc)
+            return
     ctx = _elsewhere(k.device, stream)
     if ctx is not None:
         with ctx:
@@ -710,6 +733,11 @@ def kv_cache_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens,
     None). cos_sin: float32 [positions, rot_dim], row t the cosines and then the sines of position t's rot_dim / 2 angles
     (rotary_table makes it); a token at a position past it is skipped. Pairs are features j and j + rot_dim / 2, or 2 j and 2 j + 1
     (interleaved)."""
+    if stream is None:
+        got = (_fast or _compiled()).kv_cache_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens, kv_lens, interleaved,
+                                                     k_scale, v_scale, q_out)
+        if got is not None:
+            return got if got.__class__ is not int else _check(got)
     torch = _tc()
     device, dtype = k.device, k.dtype
     ctx = _elsewhere(device, stream)
@@ -750,7 +778,11 @@ def kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, dtype, 
                   stream=None):
     """The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as (k, v) [T, Hkv, d] of dtype (into `out`, a
     pair of such tensors, if given)."""
-    torch = _tc()
+    torch = _torch or _tc()
+    if stream is None and out is None and dtype in _codes:
+        got = (_fast or _compiled()).kv_cache_read(k_cache, v_cache, block_table, cu_seqlens, kv_lens, T, _codes[dtype], k_scale, v_scale)
+        if got is not None:
+            return got if got.__class__ is not int else _check(got)
     device = k_cache.device
     ctx = _elsewhere(device, stream)
     if ctx is not None:
@@ -781,6 +813,11 @@ def attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q
     """Attention of each sequence's new tokens q [T, Hq, d] over its positions in the paged cache: out [T, Hq, d] (and
     lse [Hq, T] fp32). max_q_len: at least the most new tokens of a sequence; max_kv_len: about the longest kv_lens.
     `workspace`: a byte tensor of at least cqsa_attn_paged_workspace_size bytes (allocated if not given)."""
+    if stream is None:
+        got = (_fast or _compiled()).attention_paged(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len, max_kv_len, causal,
+                                                     scale, k_scale, v_scale, return_lse, out, workspace)
+        if got is not None:
+            return got if got.__class__ is not int else _check(got)
     torch = _tc()
     device, dtype = q.device, q.dtype
     ctx = _elsewhere(device, stream)
@@ -832,6 +869,11 @@ def kv_page_bounds(k_cache, block_table, cu_seqlens, kv_lens, bounds, bounds_exp
     """The bounds that attention_selected reads, of the pages that hold the sequences' new tokens: bounds int8 [n_pages, Hkv, 2, d] (largest and
     smallest key of each feature), bounds_exp uint8 [n_pages, Hkv] (their power of two). Call it after every write into the cache; max_q_len: about the
     most new tokens of a sequence."""
+    if stream is None:
+        rc = (_fast or _compiled()).kv_page_bounds(k_cache, block_table, cu_seqlens, kv_lens, bounds, bounds_exp, max_q_len, k_scale)
+        if rc is not None:
+            _check(rc)
+            return
     torch = _tc()
     device = k_cache.device
     ctx = _elsewhere(device, stream)
@@ -856,6 +898,11 @@ def attention_selected(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, bo
     (kv_page_bounds) give the highest scores. Returns out [T, Hq, d] (and lse [Hq, T] fp32, and the pages, int32 [T, Hkv, n_select], ascending
     indices into the sequence's row of block_table, -1 behind them; rows behind the last sequence are left as they were). max_kv_len: at least the longest kv_lens. `workspace`: a byte
     tensor of at least cqsa_attn_selected_workspace_size bytes (allocated if not given)."""
+    if stream is None:
+        got = (_fast or _compiled()).attention_selected(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, bounds, bounds_exp, n_select,
+                                                        max_kv_len, scale, k_scale, v_scale, return_lse, return_pages, out, workspace)
+        if got is not None:
+            return got if got.__class__ is not int else _check(got)
     torch = _tc()
     device, dtype = q.device, q.dtype
     ctx = _elsewhere(device, stream)
