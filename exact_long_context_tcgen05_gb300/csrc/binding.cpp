@@ -150,6 +150,15 @@ bool space(PyObject* given, size_t need, const Tensor& q, int device, Tensor* ws
 PyObject* none() { Py_RETURN_NONE; }
 PyObject* wrapped(const Tensor& t) { return THPVariable_Wrap(t); }
 
+// A call of the C ABI with the interpreter free for other threads (a launch waits while the GPU's queue is full).
+template <class F>
+int call(F f) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int rc = f();
+  PyEval_RestoreThread(state);
+  return rc;
+}
+
 // One tensor or a tuple of those that are there.
 PyObject* results(std::initializer_list<const Tensor*> all) {
   Py_ssize_t n = 0;
@@ -190,10 +199,12 @@ PyObject* attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const size_t need = cqsa_attn_paged_workspace_size(c.n_seqs, T, Hq, c.Hkv, c.d, c.page, max_q, max_kv, dt, c.code);
   if (!result(a[13], *q, device, &out) || !space(a[14], need, *q, device, &ws, &bytes)) return none();
   if (want_lse) lse = fresh({Hq, T}, at::kFloat, *q);
-  const int rc = cqsa_attn_paged_fwd(address(*q), qs, address(out), want_lse ? static_cast<float*>(address(lse)) : nullptr, address(*c.k),
+  const int rc = call([&] {
+    return cqsa_attn_paged_fwd(address(*q), qs, address(out), want_lse ? static_cast<float*>(address(lse)) : nullptr, address(*c.k),
                                      address(*c.v), c.ks, c.vs, static_cast<int*>(address(*c.table)), c.max_pages,
                                      static_cast<int*>(address(*c.cu)), static_cast<int*>(address(*c.lens)), c.n_seqs, T, max_q, max_kv, Hq,
                                      c.Hkv, c.d, c.page, c.n_pages, causal, scale, dt, c.code, address(ws), bytes, stream);
+  });
   if (rc != CQSA_OK) return PyLong_FromLong(rc);
   return results({&out, want_lse ? &lse : nullptr});
   END_HANDLE_TH_ERRORS
@@ -211,7 +222,7 @@ PyObject* kv_cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   q = tensor(a[0]);
   v = tensor(a[2]);
   turn = tensor(a[3]);
-  const int dt = type_code(*k);
+  const int dt = type_code(*k), interleaved = PyObject_IsTrue(a[9]);
   if (dt < 0 || !q || q->dim() != 3 || !c.take(a[4], a[5], a[6], a[7], a[8], a[10], a[11], device, dt)) return none();
   const int64_t T = k->size(0), Hq = q->size(1);
   const auto type = k->scalar_type();
@@ -223,10 +234,12 @@ PyObject* kv_cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return none();
   Tensor out;
   if (!result(a[12], *q, device, &out)) return none();
-  const int rc = cqsa_kv_cache_append(address(*q), address(*k), address(*v), qs, ks, vs, address(out), static_cast<float*>(address(*turn)),
-                                      turn->size(0), static_cast<int>(turn->size(1)), PyObject_IsTrue(a[9]), address(*c.k), address(*c.v), c.ks,
+  const int rc = call([&] {
+    return cqsa_kv_cache_append(address(*q), address(*k), address(*v), qs, ks, vs, address(out), static_cast<float*>(address(*turn)),
+                                      turn->size(0), static_cast<int>(turn->size(1)), interleaved, address(*c.k), address(*c.v), c.ks,
                                       c.vs, static_cast<int*>(address(*c.table)), c.max_pages, static_cast<int*>(address(*c.cu)),
                                       static_cast<int*>(address(*c.lens)), c.n_seqs, T, Hq, c.Hkv, c.d, c.page, c.n_pages, dt, c.code, stream);
+  });
   if (rc != CQSA_OK) return PyLong_FromLong(rc);
   if (a[12] != Py_None) {  // the caller's own object
     Py_INCREF(a[12]);
@@ -250,9 +263,11 @@ PyObject* kv_cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t T = k->size(0);
   const Tensor* v = tensor(a[1]);
   if (T > 0x7fffffff || !tokens(k, device, k->scalar_type(), T, c.Hkv, c.d, &ks) || !tokens(v, device, k->scalar_type(), T, c.Hkv, c.d, &vs)) return none();
-  const int rc = cqsa_kv_cache_write(address(*k), address(*v), ks, vs, address(*c.k), address(*c.v), c.ks, c.vs, static_cast<int*>(address(*c.table)),
+  const int rc = call([&] {
+    return cqsa_kv_cache_write(address(*k), address(*v), ks, vs, address(*c.k), address(*c.v), c.ks, c.vs, static_cast<int*>(address(*c.table)),
                                      c.max_pages, static_cast<int*>(address(*c.cu)), static_cast<int*>(address(*c.lens)), c.n_seqs, T, c.Hkv, c.d,
                                      c.page, c.n_pages, dt, c.code, stream);
+  });
   return PyLong_FromLong(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -267,9 +282,11 @@ PyObject* kv_cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!here(cache, &device, &stream) || !count(a[5], &T) || !count(a[6], &dt) || !c.take(a[0], a[1], a[2], a[3], a[4], a[7], a[8], device, dt)) return none();
   const auto type = dt == CQSA_F16 ? at::kHalf : at::kBFloat16;
   const Tensor k = fresh({T, c.Hkv, c.d}, type, *cache), v = fresh({T, c.Hkv, c.d}, type, *cache);
-  const int rc = cqsa_kv_cache_read(address(k), address(v), address(*c.k), address(*c.v), c.ks, c.vs, static_cast<int*>(address(*c.table)), c.max_pages,
+  const int rc = call([&] {
+    return cqsa_kv_cache_read(address(k), address(v), address(*c.k), address(*c.v), c.ks, c.vs, static_cast<int*>(address(*c.table)), c.max_pages,
                                     static_cast<int*>(address(*c.cu)), static_cast<int*>(address(*c.lens)), c.n_seqs, T, c.Hkv, c.d, c.page, c.n_pages,
                                     dt, c.code, stream);
+  });
   if (rc != CQSA_OK) return PyLong_FromLong(rc);
   return results({&k, &v});
   END_HANDLE_TH_ERRORS
@@ -291,10 +308,12 @@ PyObject* kv_page_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!here(k, &device, &stream) || !count(a[6], &max_q)) return none();
   const int own = type_code(*k), dt = own < 0 ? CQSA_F16 : own;  // (bytes stand for numbers of neither type)
   if (!c.take(a[0], nullptr, a[1], a[2], a[3], a[7], nullptr, device, dt) || !bounds_of(a[4], a[5], c, &bounds, &exps)) return none();
-  const int rc = cqsa_kv_page_bounds(address(*c.k), c.ks, static_cast<signed char*>(address(*bounds)), static_cast<unsigned char*>(address(*exps)),
+  const int rc = call([&] {
+    return cqsa_kv_page_bounds(address(*c.k), c.ks, static_cast<signed char*>(address(*bounds)), static_cast<unsigned char*>(address(*exps)),
                                      static_cast<int*>(address(*c.table)), c.max_pages, static_cast<int*>(address(*c.cu)),
                                      static_cast<int*>(address(*c.lens)), c.n_seqs, 0x7fffffff / (c.Hkv > 1 ? c.Hkv : 1), max_q, c.Hkv, c.d, c.page,
                                      c.n_pages, dt, c.code, stream);
+  });
   return PyLong_FromLong(rc);
   END_HANDLE_TH_ERRORS
 }
@@ -322,12 +341,14 @@ PyObject* attention_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!result(a[15], *q, device, &out) || !space(a[16], need, *q, device, &ws, &bytes)) return none();
   if (want_lse) lse = fresh({Hq, T}, at::kFloat, *q);
   if (want_pages) pages = fresh({T, c.Hkv, n_select}, at::kInt, *q);
-  const int rc = cqsa_attn_selected_fwd(address(*q), qs, address(out), want_lse ? static_cast<float*>(address(lse)) : nullptr,
+  const int rc = call([&] {
+    return cqsa_attn_selected_fwd(address(*q), qs, address(out), want_lse ? static_cast<float*>(address(lse)) : nullptr,
                                         want_pages ? static_cast<int*>(address(pages)) : nullptr, address(*c.k), address(*c.v), c.ks, c.vs,
                                         static_cast<signed char*>(address(*bounds)), static_cast<unsigned char*>(address(*exps)),
                                         static_cast<int*>(address(*c.table)), c.max_pages, static_cast<int*>(address(*c.cu)),
                                         static_cast<int*>(address(*c.lens)), c.n_seqs, T, n_select, max_kv, Hq, c.Hkv, c.d, c.page, c.n_pages, scale,
                                         dt, c.code, address(ws), bytes, stream);
+  });
   if (rc != CQSA_OK) return PyLong_FromLong(rc);
   return results({&out, want_lse ? &lse : nullptr, want_pages ? &pages : nullptr});
   END_HANDLE_TH_ERRORS
