@@ -1331,7 +1331,7 @@ __global__ void __launch_bounds__(256) seq_combine_kernel(const SeqParams p) {
 // A tile of 4-bit keys and values costs the converter warps of a CTA some 2,600 cycles beyond what a 16-bit one takes, for every unit of 256 rows that reads
 // it; unpacking it once into memory costs the whole GPU 13 ns, two such tiles' worth on one SM. So a sequence of two full units
 // or more is unpacked first, as far as the scratch pages go, and read as 16-bit pages: 2,048 tokens over 32,000 positions, 32 and 8 heads of
-// 128, 748 us against 1,359. The others go to a second kernel, which short batches do not gain from: 12 ragged sequences, 3,000 tokens over 60,000
+// 128, 731 us against 1,359. The others go to a second kernel, which short batches do not gain from: 12 ragged sequences, 3,000 tokens over 60,000
 // positions, 8 and 2 heads of 64, some 30 key tiles a CTA (72 by the longest sequence), take 84 us packed and 100 in two kernels.
 constexpr int kFullRows = 512;                      // rows of a sequence and key head from which on it is unpacked
 constexpr int kFullTiles = 96;                      // key tiles of a CTA, by the caller's longest sequence, from which on any is
@@ -1370,10 +1370,11 @@ __global__ void __launch_bounds__(32) full_pages_kernel(const int* cu, const int
   if (threadIdx.x == 0) *total = used;
 }
 
-// One scratch page of one key head a block: 128 positions' keys and values, a scale's 32 numbers (16 bytes) a thread and step.
+// One scratch page of one key head a block: 128 positions' keys and values. A lane turns 4 bytes, 8 numbers, into 16, so that a warp's loads and stores cover
+// whole lines (with 16 bytes into 64 a lane 42 us for 34,048 positions of 8 heads of 128, 176 MB; so 30).
 template <int D, int BF16>
 __global__ void __launch_bounds__(256) unpack_kernel(const SeqParams p, const int* total, uint16_t* k_full, uint16_t* v_full) {
-  constexpr int PIECES = D / 32;
+  constexpr int WORDS = D / 8, AT_ONCE = 4;
   const int page = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, lane = threadIdx.x & 31;
   if (page >= __ldg(total)) return;
   // the last sequence whose pages begin at `page` or before (they rise along the sequences that have any)
@@ -1385,33 +1386,39 @@ __global__ void __launch_bounds__(256) unpack_kernel(const SeqParams p, const in
   }
   const int pos0 = (page - __ldg(p.full + seq)) * kFullPage, len = seq_positions(p.kv_lens, seq, p.most);
   const int* row = p.table + static_cast<long long>(seq) * p.max_pages;
+  const uint32_t* codes[2] = {reinterpret_cast<const uint32_t*>(p.k_cache), reinterpret_cast<const uint32_t*>(p.v_cache)};
+  const uint8_t* scales[2] = {p.k_scale, p.v_scale};
+  for (int i0 = threadIdx.x; i0 < kFullPage * WORDS; i0 += 256 * AT_ONCE) {
+    uint32_t w[AT_ONCE][2], b[AT_ONCE][2];
 #pragma unroll
-  for (int i = threadIdx.x; i < kFullPage * PIECES; i += 256) {
-    const int slot = i / PIECES, piece = i % PIECES, pos = pos0 + slot;
-    if (pos >= len) continue;  // (rows behind a sequence's end are masked, and zeroed where they are read)
-    const long long vec = ((static_cast<long long>(page_at(row, pos >> p.page_log2, p.n_pages)) * p.Hkv + h) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
-    const long long to = ((static_cast<long long>(page) * p.Hkv + h) * kFullPage + slot) * D + piece * 32;
-    uint4 x[2];
-    uint32_t b[2];
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const int slot = (i0 + u * 256) / WORDS, word = (i0 + u * 256) % WORDS, pos = pos0 + slot;
+      w[u][0] = w[u][1] = b[u][0] = b[u][1] = 0u;
+      if (pos < len) {
+        const long long vec = ((static_cast<long long>(page_at(row, pos >> p.page_log2, p.n_pages)) * p.Hkv + h) << p.page_log2) + (pos & ((1 << p.page_log2) - 1));
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      x[kv] = __ldg(reinterpret_cast<const uint4*>(kv ? p.v_cache : p.k_cache) + vec * PIECES + piece);
-      b[kv] = __ldg((kv ? p.v_scale : p.k_scale) + vec * PIECES + piece);
+        for (int kv = 0; kv < 2; ++kv) {
+          w[u][kv] = __ldg(codes[kv] + vec * WORDS + word);
+          b[u][kv] = __ldg(scales[kv] + vec * (D / 32) + (word >> 2));
+        }
+      }
     }
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const float s = int4_scale(b[kv]);
-      const uint32_t w[4] = {x[kv].x, x[kv].y, x[kv].z, x[kv].w};
-      uint4* dst = reinterpret_cast<uint4*>((kv ? v_full : k_full) + to);
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const int slot = (i0 + u * 256) / WORDS, word = (i0 + u * 256) % WORDS;
+      if (pos0 + slot >= len) continue;  // (rows behind a sequence's end are masked, and zeroed where they are read)
+      const long long to = ((static_cast<long long>(page) * p.Hkv + h) * kFullPage + slot) * WORDS + word;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int kv = 0; kv < 2; ++kv) {
+        const float s = int4_scale(b[u][kv]);
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          f[e] = static_cast<float>(static_cast<int>((w[u] >> (4 * e)) & 15u) - 8) * s;
+          f[e] = static_cast<float>(static_cast<int>((w[u][kv] >> (4 * e)) & 15u) - 8) * s;
           if (!BF16) f[e] = f[e] > 65504.0f ? 65504.0f : (f[e] < -65504.0f ? -65504.0f : f[e]);  // (as they are read back)
         }
-        dst[u] = make_uint4(pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
+        reinterpret_cast<uint4*>(kv ? v_full : k_full)[to] =
+            make_uint4(pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
       }
     }
   }
