@@ -11,6 +11,11 @@
 // score, then the pages from there on up in ascending order, equal scores first come). The attention itself is attn_decode.cu's and attn_decode4.cu's: each
 // token is a sequence of its own whose table, one for each key head, lists the pages chosen, its own page last, so that only the end of
 // the last page is masked.
+//
+// Measured in a captured graph, bounds of the new pages included: 48 sequences of 1,000,000 4-bit positions together, 32 and 8 heads of 128, 64 pages
+// of 32 each: 71 us (kernel by kernel, cold: bounds 6, scores 25, choice 14, attention 31, joining 5); one token over 131,072 fp16 positions,
+// 32 pages of 64: 24 us, five launches; 200 tokens over 65,536: 154 us, of which the attention's reading of 839 MB of pages, each token's own, is most.
+// On half of the first the score kernel has 24% of memory's rate and 49% of issue: loads in flight bound it.
 #include <math.h>
 #include <string.h>
 

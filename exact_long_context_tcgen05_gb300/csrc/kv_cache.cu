@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs
 // quantising is as there; features that are paired across lanes (the first half of the rotated ones with the second) are exchanged as they were
 // loaded, four shuffles a vector, whatever `rot` is. Queries, most of the data, need no such thing: where all features turn, a
 // lane takes 8 features of the first half and their partners, and turns both (kHalves). The first loads go out before the token's
-// sequence and position are looked up, the row of cosines and sines beside the page. Bound by memory for many tokens, by that chain for few.
+// sequence and position are looked up, the row of cosines and sines beside the page. Many tokens are bound by memory and issue together, few by that chain.
+// Measured: 16,384 bf16 tokens of 32 and 8 heads of 128 into 4 bits and back 85 us in a captured graph (447 MB, 5.2 TB/s; this kernel alone, cold, 68 us at
+// 61% of memory's rate and 54% of issue); of 8 and 2 heads of 64 in fp16 into e4m3 and back 26 us; a step of 24 tokens 4.2 us.
 enum : int { kHalves = 0, kNeighbours = 1, kPartHalves = 2 };  // all features, paired by halves; pairs of neighbours; fewer features by halves
 
 // (x cos, y cos') + (x' sin, y' sin') of two features, every product and sum rounded. The assembler makes one multiply-add of a packed product and
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, D == 64 ? 4 : 3) cache_appe
 template <int D, int BF16, int KIND>
 int launch_append(const CacheArgs& a, const AppendArgs& r, cudaStream_t stream) {
   // A token's chain of loads (counts, position, page and table row) is what a small step takes: its vectors then go to as
-  // many warps as there are. With many tokens a warp each (16,384 tokens of 8 and 2 heads of 64: 25 us against 32 with two warps each).
+  // many warps as there are. With many tokens a warp each (16,384 tokens of 8 and 2 heads of 64, this kernel's first form: 25 us against 32 with two warps each).
   const int wpt = a.T <= 2 * sm_count() ? kAppendWarps : 1, per = kAppendWarps / wpt;
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.T) + per - 1) / per));
   if (r.interleaved) cache_append_kernel<D, BF16, KIND, kNeighbours><<<grid, 32 * kAppendWarps, 0, stream>>>(a, r, wpt);
