@@ -118,12 +118,13 @@ __device__ __forceinline__ void put_vector(uint8_t* cache, uint8_t* scale, long 
     // quotient before it is rounded, and a quotient by a number of four significant bits is further than 2^-30 from every border between
     // two roundings, so it is the rounded quotient. A sum with 1.5 * 2^23 + 8 then leaves the nearest (even) whole number + 8 in its lowest bits.
     uint32_t word = 0;
-    const bool cut = b == 247u;  // the largest scale: magnitudes past 7 of it are held
+    // Under the largest scale magnitudes past 7 of it are held there first (7 * 61,440 is a number): their quotient's remainder could overflow.
+    const float most = b == 247u ? 7.0f * 61440.0f : INFINITY;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float q = f[i] * inv;
-      q = fmaf(fmaf(-q, unit, f[i]), inv, q);
-      if (cut) q = fminf(fmaxf(f[i] * inv, -7.0f), 7.0f);
+      const float x = fminf(fmaxf(f[i], -most), most);
+      float q = x * inv;
+      q = fmaf(fmaf(-q, unit, x), inv, q);
       word += __float_as_uint(__fadd_rn(q, 12582920.0f)) << (4 * i);
     }
     word -= 0x4b400000u * 0x11111111u;  // the sums' exponents and upper bits, shifted together

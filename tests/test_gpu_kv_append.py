@@ -242,3 +242,27 @@ def test_no_tokens(cq):
     assert got.shape == z.shape
     k, v = cq.kv_cache_read(kc, vc, ints[:1, None], ints, ints[:1], 0, torch.float16, k_scale=ks, v_scale=vs)
     assert k.shape == (0, 2, 64) and v.shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_ties_under_the_largest_scale(cq, d):
+    """Odd multiples of half of the largest scale, 61,440, go to the even whole number, and what lies past 7 of it is held there: groups whose largest is
+    7 scales, and more, up to the type's largest."""
+    page, half = 16, 30720.0
+    x = torch.zeros(4, 1, d, dtype=torch.bfloat16, device="cuda")
+    ties = torch.tensor([s * (2 * n + 1) * half for n in range(7) for s in (1, -1)], device="cuda")
+    x[..., :14] = ties.to(x.dtype)
+    assert torch.equal(x[0, 0, :14].float(), ties)  # (they are bf16 numbers)
+    for i, top in enumerate((14 * half, 16 * half, 2.0 ** 100, float(torch.finfo(torch.bfloat16).max))):
+        x[i, :, 31] = -top
+    x[..., 32:64] = x[..., :32].flip(-1)
+    kc, vc, ks, vs = _caches("4bit", 2, 1, page, d, x.dtype)
+    table = torch.tensor([[1]], dtype=torch.int32, device="cuda")
+    cu, lens = torch.tensor([0, 4], dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
+    cq.kv_cache_write(x, x, kc, vc, table, cu, lens, k_scale=ks, v_scale=vs)
+    code, byte, val = s4.quantise4(x)
+    assert (byte[..., :2] == 247).all()
+    want = torch.tensor([s * 2 * ((n + 1) // 2) * 61440.0 for n in range(7) for s in (1, -1)], dtype=torch.float64, device="cuda")
+    assert torch.equal(val[0, 0, :14], want) and (val[:, 0, 31] == -7 * 61440.0).all()
+    for cache, scale in ((kc, ks), (vc, vs)):
+        assert torch.equal(cache[1, :, :4].transpose(0, 1), code) and torch.equal(scale[1, :, :4].transpose(0, 1), byte)
