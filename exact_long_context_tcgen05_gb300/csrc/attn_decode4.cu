@@ -365,10 +365,20 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
         {
           uint32_t kword = scales_of<SPK>(ksc, lane), vword = scales_of<SPK>(vsc, lane);
           if (lane >= left) kword = vword = 0u;  // slots past the end hold anything
-          const uint32_t ve = vword & 0x00ff00ffu, vo = (vword >> 8) & 0x00ff00ffu;
-          const uint32_t most = __vmaxu2(ve, vo);
-          uint32_t top = SPK == 4 ? max(most & 0xffffu, most >> 16) : most;
-          top = min(__reduce_max_sync(0xffffffffu, top), 247u) >> 3;
+          uint32_t ve = vword & 0x00ff00ffu, vo = (vword >> 8) & 0x00ff00ffu, nan[2] = {0u, 0u};
+          auto largest = [&]() -> uint32_t {
+            const uint32_t most = __vmaxu2(ve, vo);
+            return __reduce_max_sync(0xffffffffu, SPK == 4 ? max(most & 0xffffu, most >> 16) : most);
+          };
+          uint32_t top = largest();
+          if (top > 247u) {  // a NaN is no size that the numbers beside it could be relative to
+            nan[0] = __vcmpgtu2(ve, 0x00f700f7u);
+            nan[1] = __vcmpgtu2(vo, 0x00f700f7u);
+            ve &= ~nan[0];
+            vo &= ~nan[1];
+            top = largest();
+          }
+          top >>= 3;
           if (static_cast<int>(top) > ev) {
             const float a = ev < 0 ? 0.0f : exp2_int_any(ev - static_cast<int>(top));
             ev = static_cast<int>(top);
@@ -386,6 +396,8 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
             h[0] = mul2(h[0], *reinterpret_cast<const uint32_t*>(&f2));
             h[1] = mul2(h[1], *reinterpret_cast<const uint32_t*>(&f2));
           }
+          h[0] |= nan[0];
+          h[1] |= nan[1];
           // key 16 j + 8 x + 2 t + e at [32 features][t][j][x][e]
           const uint32_t vat = wv + ((lane >> 1) & 3) * (KW / 2) + (lane >> 3) * 4 + (lane & 1) * 2;
           st_shared_u16(vat, h[0]);

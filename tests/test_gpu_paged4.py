@@ -153,6 +153,25 @@ def test_not_a_number(cq, d, new):
     assert (empty[:new] == 0).all() and (elses[:, :new] == -math.inf).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 7])
+@pytest.mark.parametrize("powers", [(-10,), (0,), (0, 9, -6)])
+def test_numbers_beside_a_nan_value(cq, d, new, powers):
+    """A NaN scale of a value takes nothing from the other features of its head, however small their values are: they are as near to the formula as without it."""
+    hq, page, lengths = 4, 16, [300]
+    ks, vs, kq, vq, kse, vse, table = make_cache4(lengths, 1, d, page, 9, powers)
+    q = sq.normal((new, hq, d), torch.float16, 3)
+    pad = torch.full((1, hq, d), 7.0, dtype=q.dtype, device="cuda")
+    clean = call(cq, q, kq, vq, kse, vse, table, [new], lengths)
+    bad = vse.clone()
+    for at in (0, 131):  # a warp's first key, and one in mid-sequence
+        bad[table[0, at // page], 0, at % page, 1] = 255
+    out, lse = call(cq, q, kq, vq, kse, bad, table, [new], lengths)
+    assert torch.isnan(out[..., 32:64]).all() and torch.equal(lse, clean[1])
+    rest = torch.cat([out[..., :32], clean[0][..., 32:64], out[..., 64:]], -1)
+    check(torch.cat([rest, pad]), torch.cat([lse, torch.zeros_like(lse[:, :1])], 1), q, ks, vs, [new], lengths, True, "beside a NaN")
+
+
 @pytest.mark.parametrize("hq,new", [(4, 1), (4, 5)])
 def test_equal_pages_and_table_order(cq, hq, new):
     """The result does not depend on where pages lie, and repeats bit by bit."""
