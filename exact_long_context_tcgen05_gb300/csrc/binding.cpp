@@ -150,13 +150,26 @@ bool space(PyObject* given, size_t need, const Tensor& q, int device, Tensor* ws
 PyObject* none() { Py_RETURN_NONE; }
 PyObject* wrapped(const Tensor& t) { return THPVariable_Wrap(t); }
 
-// A call of the C ABI with the interpreter free for other threads (a launch waits while the GPU's queue is full).
+// The interpreter free for other threads; taken back whichever way the block is left (a tensor without memory of its own throws when asked for its address).
+struct Released {
+  PyThreadState* state = PyEval_SaveThread();
+  Released() = default;
+  Released(const Released&) = delete;
+  ~Released() { PyEval_RestoreThread(state); }
+};
+
+// A call of the C ABI with the interpreter free (a launch waits while the GPU's queue is full).
 template <class F>
 int call(F f) {
-  PyThreadState* state = PyEval_SaveThread();
-  const int rc = f();
-  PyEval_RestoreThread(state);
-  return rc;
+  const Released released;
+  return f();
+}
+
+// Whether an argument is true; throws, the interpreter's error set, where it cannot say.
+bool truth(PyObject* o) {
+  const int r = PyObject_IsTrue(o);
+  if (r < 0) throw python_error();
+  return r != 0;
 }
 
 // One tensor or a tuple of those that are there.
@@ -189,7 +202,7 @@ PyObject* attention_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   long long qs;
   Cache c;
   if (!here(q, &device, &stream) || q->dim() != 3 || !count(a[6], &max_q) || !count(a[7], &max_kv) || !number(a[9], &scale)) return none();
-  const int dt = type_code(*q), causal = PyObject_IsTrue(a[8]), want_lse = PyObject_IsTrue(a[12]);
+  const int dt = type_code(*q), causal = truth(a[8]), want_lse = truth(a[12]);
   if (dt < 0 || !c.take(a[1], a[2], a[3], a[4], a[5], a[10], a[11], device, dt)) return none();
   const int64_t T = q->size(0), Hq = q->size(1);
   if (T > 0x7fffffff || Hq > 0x7fffffff || !tokens(q, device, q->scalar_type(), T, Hq, c.d, &qs)) return none();
@@ -222,7 +235,7 @@ PyObject* kv_cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   q = tensor(a[0]);
   v = tensor(a[2]);
   turn = tensor(a[3]);
-  const int dt = type_code(*k), interleaved = PyObject_IsTrue(a[9]);
+  const int dt = type_code(*k), interleaved = truth(a[9]);
   if (dt < 0 || !q || q->dim() != 3 || !c.take(a[4], a[5], a[6], a[7], a[8], a[10], a[11], device, dt)) return none();
   const int64_t T = k->size(0), Hq = q->size(1);
   const auto type = k->scalar_type();
@@ -329,7 +342,7 @@ PyObject* attention_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
   long long qs;
   Cache c;
   if (!here(q, &device, &stream) || q->dim() != 3 || !count(a[8], &n_select) || !count(a[9], &max_kv) || !number(a[10], &scale)) return none();
-  const int dt = type_code(*q), want_lse = PyObject_IsTrue(a[13]), want_pages = PyObject_IsTrue(a[14]);
+  const int dt = type_code(*q), want_lse = truth(a[13]), want_pages = truth(a[14]);
   if (dt < 0 || !c.take(a[1], a[2], a[3], a[4], a[5], a[11], a[12], device, dt) || !bounds_of(a[6], a[7], c, &bounds, &exps)) return none();
   const int64_t T = q->size(0), Hq = q->size(1), slots = static_cast<int64_t>(c.max_pages) * c.page;
   if (T > 0x7fffffff || Hq > 0x7fffffff || !tokens(q, device, q->scalar_type(), T, Hq, c.d, &qs)) return none();

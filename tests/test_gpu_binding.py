@@ -94,6 +94,32 @@ def test_what_it_leaves_to_python(cq):
         cq.attention_paged(q, kc, vc, table, cu, lens, 1, 40, scale=float("nan"))
 
 
+class _Undecided:
+    def __bool__(self):
+        raise TypeError("neither")
+
+
+def test_errors_come_back_as_exceptions(cq):
+    """A tensor without memory of its own (its address is asked for while the interpreter is free) and an argument that is neither true nor false: exceptions, and the next call
+    works."""
+    d, page, hkv = 64, 16, 2
+    q = sq.normal((1, 4, d), torch.float16, 3)
+    k, v, kc, vc, table = sq.make_cache([40], hkv, d, page, torch.float16, 3)
+    cu, lens = torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([40], dtype=torch.int32, device="cuda")
+    want = cq.attention_paged(q, kc, vc, table, cu, lens, 1, 40)
+    f = cq._compiled().attention_paged
+    for _ in range(3):
+        with pytest.raises(RuntimeError, match="storage"):  # (one of a batch that vmap goes over)
+            torch.vmap(lambda c: f(q, c, c, table, cu, lens, 1, 40, True, None, None, None, False, None, None))(kc[None])
+        with pytest.raises(TypeError, match="neither"):
+            f(q, kc, vc, table, cu, lens, 1, 40, True, None, None, None, _Undecided(), None, None)
+    done = []
+    t = threading.Thread(target=lambda: done.append(1))  # (another thread gets its turn)
+    t.start()
+    t.join()
+    assert done and torch.equal(cq.attention_paged(q, kc, vc, table, cu, lens, 1, 40), want)
+
+
 def test_threads(cq):
     """Calls from several threads at once, each on its own stream."""
     d, page = 64, 16
