@@ -697,7 +697,7 @@ int launch_select(SelectArgs* args, cudaStream_t stream) {
   }
   int gp = 1, block_tokens = 1;
   while (gp < a.G) gp *= 2;
-  while (block_tokens < (a.T + a.n_seqs - 1) / a.n_seqs && 2 * block_tokens * gp <= kScoreRows) block_tokens *= 2;
+  while (block_tokens <= (a.T - 1) / a.n_seqs && 2 * block_tokens * gp <= kScoreRows) block_tokens *= 2;
   for (int t = 0; t < a.T; t += at_once) {
     const int n = a.T - t < at_once ? a.T - t : at_once;
     if (a.n_select > 1) {
