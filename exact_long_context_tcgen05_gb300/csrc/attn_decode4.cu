@@ -16,8 +16,8 @@
 // largest. P^T's fragment is S^T's transposed, one movmatrix for 8 keys. Queries are fp16, as in attn_decode.cu over e4m3.
 //
 // Measured in a captured graph: one token of each of 128 sequences, 1,000,000 bf16 positions together, 32 query and 8 key heads, d = 128: 235 us
-// (1.09 GB, 4.6 TB/s). On half of the positions the warps issue in 62% of the cycles, the integer pipe in 52%, and 32 keys of a warp
-// are 712 instructions, some 400 of them unpacking and products: that, not memory (55%), sets the pace. Four tokens of each of 40
+// (1.09 GB, 4.6 TB/s). On half of the positions the warps issue in 63% of the cycles, the integer pipe in 52%, and 32 keys of a warp
+// are 723 instructions, some 400 of them unpacking and products: that, not memory (55%), sets the pace. Four tokens of each of 40
 // sequences, 400,000 positions, 8 and 2 heads of 64: 37 us; one over 4,001 positions 12 us.
 #include <math.h>
 #include <string.h>
