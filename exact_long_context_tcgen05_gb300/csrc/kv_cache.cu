@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const CacheArgs
         const int h = h0 + u * HPS + hl;
         const long long at = row + static_cast<long long>(h) * a.page;
         const uint8_t* cache = static_cast<const uint8_t*>(kv ? a.v_cache : a.k_cache);
-        x[kv][u] = make_uint4(0, 0, 0, 0);
+        x[kv][u] = make_uint4(KIND == kCacheInt4 ? 0x88888888u : 0u, 0, 0, 0);  // zeros, for a token without a position
         e[kv][u] = 0;
         if (h < a.Hkv && row >= 0) {
           if (KIND == kCacheInt4) {

@@ -266,3 +266,23 @@ def test_ties_under_the_largest_scale(cq, d):
     assert torch.equal(val[0, 0, :14], want) and (val[:, 0, 31] == -7 * 61440.0).all()
     for cache, scale in ((kc, ks), (vc, vs)):
         assert torch.equal(cache[1, :, :4].transpose(0, 1), code) and torch.equal(scale[1, :, :4].transpose(0, 1), byte)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["same", "e4m3", "4bit"])
+def test_read_without_a_position(cq, kind, dt, d):
+    """Tokens before the first position, and behind the table's last, read as zeros from every kind of cache; the others as from a call without them."""
+    page, hkv, dtype = 16, 3, sq.DT[dt]
+    kc, vc, ks, vs = _caches(kind, 4, hkv, page, d, dtype)
+    table = torch.tensor([[2], [1]], dtype=torch.int32, device="cuda")
+    cu, lens = torch.tensor([0, 16, 32], dtype=torch.int32, device="cuda"), torch.tensor([16, 16], dtype=torch.int32, device="cuda")
+    k, v = sq.normal((32, hkv, d), dtype, 3), sq.normal((32, hkv, d), dtype, 4)
+    cq.kv_cache_write(k, v, kc, vc, table, cu, lens, k_scale=ks, v_scale=vs)
+    every = cq.kv_cache_read(kc, vc, table, cu, lens, 32, dtype, k_scale=ks, v_scale=vs)
+    # 10 tokens before and 5 of positions 0 .. 4; 4 of positions 12 .. 15 and 6 behind
+    cu, lens = torch.tensor([0, 15, 25], dtype=torch.int32, device="cuda"), torch.tensor([5, 22], dtype=torch.int32, device="cuda")
+    got = cq.kv_cache_read(kc, vc, table, cu, lens, 25, dtype, k_scale=ks, v_scale=vs, out=tuple(torch.full((25, hkv, d), 5.0, dtype=dtype, device="cuda") for _ in range(2)))
+    for g, w in zip(got, every):
+        assert (g[:10] == 0).all() and (g[19:] == 0).all()
+        assert torch.equal(g[10:15], w[:5]) and torch.equal(g[15:19], w[28:])
