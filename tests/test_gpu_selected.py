@@ -345,3 +345,19 @@ def test_choice_against_a_sort(cq, P):
             want = torch.full((n_select,), -1, dtype=torch.int32, device="cuda")
             want[:len(best)], want[len(best)] = best, P
             assert torch.equal(pages[0, 0], want), (kind, n_select)
+
+
+@pytest.mark.parametrize("width,hkv", [(16384, 8), (300000, 2)])
+def test_tokens_in_rounds(cq, width, hkv):
+    """More scores than are held at a time (64 MiB: 128 tokens, 27 tokens), so that rounds begin and end inside of sequences: the same as in one round."""
+    d, page, dtype, lengths, new = 64, 16, torch.float16, [900, 333, 64, 2000], [150, 1, 30, 120]
+    ks, vs, kc, vc, kscale, vscale, table = make("4bit", lengths, hkv, d, page, dtype, 7, 1.0)
+    q = sq.normal((sum(new) + 2, 2 * hkv, d), dtype, 3)
+    assert sum(new) > (64 << 20) // (hkv * width * 4)
+    out, lse, pages, bounds = run(cq, q, kc, vc, kscale, vscale, table, new, lengths, 6)
+    check(out, lse, pages, q, ks, vs, new, lengths, 6, page, "4bit")
+    wide = torch.zeros(len(lengths), width, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    again = run(cq, q, kc, vc, kscale, vscale, wide, new, lengths, 6, most=width * page, bounds=bounds)
+    n = sum(new)
+    assert torch.equal(out, again[0]) and torch.equal(lse[:, :n], again[1][:, :n]) and torch.equal(pages[:n], again[2][:n])
