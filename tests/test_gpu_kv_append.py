@@ -248,7 +248,7 @@ def test_no_tokens(cq):
 def test_ties_under_the_largest_scale(cq, d):
     """Odd multiples of half of the largest scale, 61,440, go to the even whole number, and what lies past 7 of it is held there: groups whose largest is
     7 scales, and more, up to the type's largest."""
-    page, half = 16, 30720.0
+    page, half = 16, 61440.0 / 2
     x = torch.zeros(4, 1, d, dtype=torch.bfloat16, device="cuda")
     ties = torch.tensor([s * (2 * n + 1) * half for n in range(7) for s in (1, -1)], device="cuda")
     x[..., :14] = ties.to(x.dtype)
