@@ -360,7 +360,7 @@ int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, vo
  * aligned; ignored otherwise). The power is the smallest (at least 2^-126) under which the vector's largest finite magnitude is
  * at most 448; codes are rounded to nearest even; an infinity becomes NaN. Or CQSA_INT4: caches of [n_pages, Hkv, page_size, d / 2]
  * bytes, scales [n_pages, Hkv, page_size, d / 32]. 32 neighbouring features share a scale, their largest magnitude / 7 rounded to
- * nearest even to 4 significant bits and held to [2^-14, 61440]; its byte 8 e + m stands for (1 + m / 8) 2^(e - 15). A value is the nearest (even)
+ * nearest even to 4 significant bits and held to [2^-14, 61440]; its byte 8 e + m stands for (1 + m / 8) 2^(e - 15), any from 248 on for a NaN, in every call. A value is the nearest (even)
  * whole multiple of it, held to -7 .. 7; a byte holds the multiples + 8 of two neighbouring features, the first in its low four bits. A group with a value that
  * is not finite has the byte 255, and reads as NaN. kv_lens: device int32 [n_seqs], the
  * positions of each sequence, its new tokens included: token i of a sequence's n new tokens has position
