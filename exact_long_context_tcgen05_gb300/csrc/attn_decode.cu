@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT, CTAS>::NTHR, CTAS)
         continue;
       }
       // ---- the rows' queries as A fragments, and the keys each of this thread's two rows may see
+      const int pos0 = seq_first_position(p.kv_lens, wk.s, wk.qlen);
       uint32_t qf[D / 16][4];
       int lim[2];
       float rs[2];  // factor from a raw score to the base-2 exponent
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT, CTAS>::NTHR, CTAS)
         const int r = mt * 16 + g + 8 * u;
         const int tok = r / p.G;
         const bool valid = tok < wk.qlen;
-        lim[u] = !valid ? 0 : (p.causal ? min(wk.len, wk.len - wk.qlen + tok + 1) : wk.len);
+        lim[u] = !valid ? 0 : (p.causal ? min(wk.len, pos0 + tok + 1) : wk.len);
         const uint16_t* qr = static_cast<const uint16_t*>(p.q) + static_cast<long long>(wk.first + tok) * p.q_stride +
                              static_cast<long long>(h * p.G + (r - tok * p.G)) * D;
         rs[u] = p.scale_log2;
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(DecCfg<D, E4M3, NMT, CTAS>::NTHR, CTAS)
           }
         }
       }
-      const int lim_all = p.causal ? wk.len - wk.qlen + 1 : wk.len;  // keys that every row sees
+      const int lim_all = p.causal ? pos0 + 1 : wk.len;  // keys that every row sees
       float o[D / 8][4];
 #pragma unroll
       for (int j = 0; j < D / 8; ++j)

@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
         continue;
       }
       // ---- this lane's queries (row g of each column tile, 8 features of every 32), and what its two columns (rows 2 t4, 2 t4 + 1) see
+      const int pos0 = seq_first_position(p.kv_lens, wk.s, wk.qlen);
       uint32_t qf[NT][D / 32][4];
       int lim[NT][2];
       float rs[NT][2];  // factor from a raw score to the base-2 exponent
@@ -305,12 +306,12 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int tk = ((mt * NT + nt) * 8 + 2 * t4 + u) / p.G;
-          lim[nt][u] = tk >= wk.qlen ? 0 : (p.causal ? min(wk.len, wk.len - wk.qlen + tk + 1) : wk.len);
+          lim[nt][u] = tk >= wk.qlen ? 0 : (p.causal ? min(wk.len, pos0 + tk + 1) : wk.len);
           rs[nt][u] = p.scale_log2;
           if (BF16) rs[nt][u] *= pow2i(__shfl_sync(0xffffffffu, e, (2 * t4 + u) * 4));
         }
       }
-      const int lim_all = p.causal ? wk.len - wk.qlen + 1 : wk.len;  // keys that every row sees
+      const int lim_all = p.causal ? pos0 + 1 : wk.len;  // keys that every row sees
       float o[NT][D / 32][2][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)

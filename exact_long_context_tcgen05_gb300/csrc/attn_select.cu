@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const BoundsArgs 
   const int page_log2 = 31 - __clz(a.page);
   const int len = seq_positions(a.kv_lens, s, static_cast<long long>(a.max_pages) << page_log2);
   if (n == 0 || len == 0) return;
-  const int p0 = max(len - n, 0) >> page_log2, p1 = (len - 1) >> page_log2;
+  const int p0 = max(seq_first_position(a.kv_lens, s, n), 0) >> page_log2, p1 = (len - 1) >> page_log2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = threadIdx.x % LPV;
   for (int p = p0 + static_cast<int>(blockIdx.y); p <= p1; p += static_cast<int>(gridDim.y)) {
     const int pg = __ldg(a.table + static_cast<long long>(s) * a.max_pages + p);
@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const BoundsArgs 
   }
 }
 
-// Token `token`'s sequence and position (a whole warp); position -1 for a token of no sequence or before the first position.
+// Token `token`'s sequence and position (a whole warp); position -1 for a token of no sequence or before the first position, the
+// table's last for one behind it.
 __device__ __forceinline__ void token_position(const SelectArgs& a, int token, int lane, int* seq, int* pos) {
   const int s = seq_of_token(a.cu, a.n_seqs, a.T, token, lane);
   *seq = s;
@@ -155,8 +156,7 @@ __device__ __forceinline__ void token_position(const SelectArgs& a, int token, i
   if (s < 0) return;
   int first;
   const int n = seq_tokens(a.cu, s, a.T, &first);
-  const int len = seq_positions(a.kv_lens, s, static_cast<long long>(a.max_pages) * a.page);
-  *pos = max(len - n + (token - first), -1);
+  *pos = max(min(seq_first_position(a.kv_lens, s, n) + (token - first), a.max_pages * a.page - 1), -1);
 }
 
 // Scores of pages for some tokens of a sequence and a key head, on the tensor cores (`splits` blocks take kScorePages pages each in turn): 16 pages x (largest | smallest keys), whole
@@ -194,12 +194,13 @@ __global__ void __launch_bounds__(kScoreThreads, ONE ? 4 : 2) score_kernel(const
     int first = 0, n = 0, pos0 = 0, ns;  // pos0: the first one's position
     if (s >= 0) {
       n = seq_tokens(a.cu, s, a.T, &first);
-      pos0 = seq_positions(a.kv_lens, s, static_cast<long long>(a.max_pages) * a.page) - n + (token - first);
+      pos0 = seq_first_position(a.kv_lens, s, n) + (token - first);
       ns = min(first + n, last) - token;
     } else {
       ns = (token < cu_at(a.cu, 0, a.T) ? min(cu_at(a.cu, 0, a.T), last) : last) - token;
     }
-    const int P = s < 0 || pos0 + ns <= 0 ? 0 : min((pos0 + ns - 1) >> page_log2, a.most_pages);  // pages before the last of them
+    // pages before the last of them (a token behind the table stands in its last page)
+    const int P = s < 0 || pos0 + ns <= 0 ? 0 : min(min(pos0 + ns - 1, a.max_pages * a.page - 1) >> page_log2, a.most_pages);
     if (base >= P) {  // (the same for the whole block)
       token += ns;
       continue;

@@ -103,7 +103,7 @@ struct SeqCfg {
 struct Work {
   int valid, seq, tok_first, qlen, kvlen, ta, hk;  // two row tiles from token ta of the sequence's
   int jb, je;                                      // key tiles [jb, je) of those the row tiles see
-  int slot, pad0, pad1;                            // where a part goes (-1: the whole unit, to the output)
+  int slot, pos0, pad;                             // where a part goes (-1: the whole unit, to the output); position of the sequence's first token
 };
 
 // A chunk's units weigh as many as the key tiles they see (one at least, for the rows that see nothing) and kUnitWeight
@@ -131,24 +131,25 @@ __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t 
 
 // The units of a sequence's new tokens over its positions, for one key head: unit i takes tokens [i per, (i + 1) per).
 struct ChunkUnits {
-  int seq, first, qlen, kvlen, per, units, causal;
+  int seq, first, qlen, kvlen, pos0, per, units, causal;
   __device__ __forceinline__ int last(int i) const {  // the last position that unit i sees, -1 or less for none
-    return causal ? kvlen - qlen + min((i + 1) * per, qlen) - 1 : kvlen - 1;
+    return causal ? min(kvlen, pos0 + min((i + 1) * per, qlen)) - 1 : kvlen - 1;
   }
   __device__ __forceinline__ int tiles(int i) const {
     const int p = last(i);
     return p < 0 ? 1 : p / BN + 1;
   }
-  // what units [0, i) weigh: their last positions are an arithmetic progression (the last unit's may be less)
+  // what units [0, i) weigh: their last positions are an arithmetic progression up to the last that there is
   __device__ __forceinline__ long long before(int i) const {
     long long w = static_cast<long long>(i) * (kUnitWeight + 1);
     if (!causal) return w + static_cast<long long>(i) * (max(kvlen - 1, 0) / BN);
-    if (i == 0) return w;
-    if (i == units) {
-      w += max(kvlen - 1, 0) / BN;
-      --i;
+    const int rising = max(kvlen - pos0 - 1, 0) / per;  // units that end before it
+    if (i > rising) {
+      w += static_cast<long long>(i - rising) * (max(kvlen - 1, 0) / BN);
+      i = rising;
     }
-    const int a = kvlen - qlen + per - 1;
+    if (i == 0) return w;
+    const int a = pos0 + per - 1;
     const int skip = a < 0 ? min(i, (-a + per - 1) / per) : 0;
     return w + floor_sum(i - skip, BN, per, max(a + skip * per, 0));
   }
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     View v;
     v.w = w;
     v.tb = w.ta + p.tpt;
-    v.q_off = w.kvlen - w.qlen;  // position of the sequence's first new token (negative: rows that see nothing)
+    v.q_off = w.pos0;  // position of the sequence's first new token (negative: rows that see nothing)
     // the last position that either row tile sees
     const int t1 = min(w.ta + 2 * p.tpt, w.qlen);
     const int last = p.causal ? min(w.kvlen, v.q_off + t1) - 1 : w.kvlen - 1;
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
     const int4 a = at[0], b = at[1], c = at[2];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar_unit_free[i & 1]);
-    const Work w = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, 0, 0};
+    const Work w = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, 0};
     if (!w.valid) return false;
     *v = view_of(w);
     return true;
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           int4* at = reinterpret_cast<int4*>(&sWork[i & 1]);
           at[0] = make_int4(w.valid, w.seq, w.tok_first, w.qlen);
           at[1] = make_int4(w.kvlen, w.ta, w.hk, w.jb);
-          at[2] = make_int4(w.je, w.slot, 0, 0);
+          at[2] = make_int4(w.je, w.slot, w.pos0, 0);
           mbar_arrive(&bar_unit[i & 1]);
         }
         __syncwarp();
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
           c.seq = k;
           c.qlen = seq_tokens(p.cu, k, p.T, &c.first);
           c.kvlen = seq_positions(p.kv_lens, k, p.most);
+          c.pos0 = seq_first_position(p.kv_lens, k, c.qlen);
           if (p.full && (__ldg(p.full + k) >= 0) != (SRC == kSrcPages)) c.qlen = 0;
           c.per = per;
           c.units = (c.qlen + per - 1) / per;
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(SeqCfg<D, SRC>::NTHR, 1)
               p.meta[2 * range + 1] = make_int4(c.first, c.qlen, place * per, 0);
             }
             if (t0 < t1) {  // (else the range ends before the unit's first key tile)
-              const Work g = {1, c.seq, c.first, c.qlen, c.kvlen, place * per, hk, t0, t1, whole ? -1 : 2 * range + (t0 == 0 ? 1 : 0), 0, 0};
+              const Work g = {1, c.seq, c.first, c.qlen, c.kvlen, place * per, hk, t0, t1, whole ? -1 : 2 * range + (t0 == 0 ? 1 : 0), c.pos0, 0};
               ok = give(i++, g);
             }
             w = next;

@@ -26,6 +26,10 @@ __device__ __forceinline__ int seq_positions(const int* kv_lens, int s, long lon
   return n > most ? static_cast<int>(most) : n;
 }
 
+// The position of the first of a sequence's n new tokens (below zero: those before the first position see nothing). It goes by the
+// sequence's own length, also where that passes what its row of the page table can name.
+__device__ __forceinline__ int seq_first_position(const int* kv_lens, int s, int n) { return max(__ldg(kv_lens + s), 0) - n; }
+
 // A page index held inside the cache: an entry outside it stands for page 0.
 __device__ __forceinline__ int page_at(const int* row, int i, int n_pages) {
   const int p = __ldg(row + i);

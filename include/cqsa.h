@@ -364,7 +364,8 @@ int cqsa_attn_fwd_chunked_static(const void* q, const void* k, const void* v, vo
  * whole multiple of it, held to -7 .. 7; a byte holds the multiples + 8 of two neighbouring features, the first in its low four bits. A group with a value that
  * is not finite has the byte 255, and reads as NaN. kv_lens: device int32 [n_seqs], the
  * positions of each sequence, its new tokens included: token i of a sequence's n new tokens has position
- * kv_lens[s] - n + i. Slots past a sequence's length may hold anything. Pages may be shared between
+ * kv_lens[s] - n + i, in every call, also where kv_lens[s] passes max_pages * page_size: a token behind the table is skipped by a write, sees
+ * all that the table holds, and stands in its last page where pages are selected. Slots past a sequence's length may hold anything. Pages may be shared between
  * sequences as long as no two tokens of one write go to the same slot.
  *
  * A non-finite v at a position that the causal mask hides from a row, in the row's own sequence, may reach the row (as
