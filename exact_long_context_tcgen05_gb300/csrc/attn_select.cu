@@ -82,6 +82,29 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const BoundsArgs 
     const int pg = __ldg(a.table + static_cast<long long>(s) * a.max_pages + p);
     if (pg < 0 || pg >= a.n_pages) continue;  // (the same for the whole block)
     const int slots = min(a.page, len - (p << page_log2));
+    // Of sequences that share the page and whose new tokens are in it, the one that fills it furthest writes its bounds (equal ones write the same). Every block
+    // looks through all sequences: a step of 48 takes 4.0 us in place of 3.4, of 300 8.5 and 7.1, of 3,000 121 and 51.
+    if (slots < a.page && a.n_seqs > 1) {
+      bool further = false;
+      constexpr int AT_ONCE = 4;  // (lengths whose loads are in flight together)
+      for (int o0 = threadIdx.x; o0 < a.n_seqs; o0 += AT_ONCE * kBoundThreads) {
+        int l[AT_ONCE], c0[AT_ONCE], c1[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          const int o = min(o0 + u * kBoundThreads, a.n_seqs - 1);
+          l[u] = __ldg(a.kv_lens + o);
+          c0[u] = cu_at(a.cu, o, a.T);
+          c1[u] = cu_at(a.cu, o + 1, a.T);
+        }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          const int o = min(o0 + u * kBoundThreads, a.n_seqs - 1);
+          if (l[u] > len && c1[u] > c0[u] && l[u] - (c1[u] - c0[u]) < (p + 1) << page_log2)
+            further |= __ldg(a.table + static_cast<long long>(o) * a.max_pages + p) == pg;
+        }
+      }
+      if (__syncthreads_or(further)) continue;
+    }
     const long long block = static_cast<long long>(pg) * a.Hkv + h;
     float hi[8], lo[8];
 #pragma unroll

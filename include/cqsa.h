@@ -452,7 +452,8 @@ int cqsa_attn_paged_fwd(const void* q, long long q_stride, void* out, float* lse
  * cu_seqlens[s+1] - cu_seqlens[s] positions; all of them where that is kv_lens[s]), from their slots below kv_lens[s]. bounds: device int8
  * [n_pages, Hkv, 2, d], 16-byte aligned, the largest and the smallest key of each feature as the nearest (even) whole multiples of 2^(b - 127) for the
  * byte b in bounds_exp, device [n_pages, Hkv]: the smallest power (2^-126 at least) under which all are at most 127 in magnitude. A page with a
- * key that is not finite gets the byte 255, and is selected first. Other pages' bounds are left as they were; call it after every write.
+ * key that is not finite gets the byte 255, and is selected first. Other pages' bounds are left as they were; call it after every write. A page that several
+ * sequences share, at one index of their rows, gets the bounds of the slots that the longest of those with new tokens in it fills; a page stands once in a row.
  * T: at least cu_seqlens[n_seqs]; max_q_len: about the most new tokens of a sequence (it sets how the work is split). k_scale: as above. */
 int cqsa_kv_page_bounds(const void* k_cache, const unsigned char* k_scale, signed char* bounds, unsigned char* bounds_exp,
                         const int* block_table, int max_pages, const int* cu_seqlens, const int* kv_lens, int n_seqs, int T,
