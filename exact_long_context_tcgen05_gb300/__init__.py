@@ -507,19 +507,36 @@ def _current(device):
     return _raw_stream(device.index) or None
 
 
+def _binding_path():
+    """Where build.py leaves the compiled functions for this torch and interpreter."""
+    import importlib.machinery
+    return os.path.join(_PKG, "_build", f"cqsa_torch-{_tc().__version__}{importlib.machinery.EXTENSION_SUFFIXES[0]}")
+
+
+class _NotBuilt:
+    """In place of the compiled functions where there are none: they leave every call to Python."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _compiled():
     """The compiled functions, loaded by the first call."""
     global _fast
     if _fast is None:
         import importlib.machinery
         import importlib.util
-        torch = _tc()
-        path = os.path.join(_PKG, "_build", f"cqsa_torch-{torch.__version__}.so")
-        if not os.path.exists(path):
-            raise ImportError(f"the torch binding is not built ({path}); run `python -m exact_long_context_tcgen05_gb300.build`")
-        loader = importlib.machinery.ExtensionFileLoader("cqsa_torch", path)
-        _fast = importlib.util.module_from_spec(importlib.util.spec_from_file_location("cqsa_torch", path, loader=loader))
-        loader.exec_module(_fast)
+        path = _binding_path()
+        if os.path.exists(path):
+            loader = importlib.machinery.ExtensionFileLoader("cqsa_torch", path)
+            fast = importlib.util.module_from_spec(importlib.util.spec_from_file_location("cqsa_torch", path, loader=loader))
+            loader.exec_module(fast)
+            _fast = fast
+        else:
+            import warnings
+            warnings.warn(f"the torch binding is not built ({path}): calls over a cache take some 15 to 30 us longer on the host; "
+                          "`python -m exact_long_context_tcgen05_gb300.build` builds it", RuntimeWarning, stacklevel=3)
+            _fast = _NotBuilt()
     return _fast
 
 

@@ -42,9 +42,11 @@ def _stale(target: str, deps) -> bool:
 
 
 def binding_path() -> str:
-    """The torch binding, one for each version of torch (it links to torch's own libraries)."""
+    """The torch binding, one for each version of torch (it links to torch's own libraries) and interpreter."""
+    import importlib.machinery
+
     import torch
-    return os.path.join(BUILD, f"cqsa_torch-{torch.__version__}.so")
+    return os.path.join(BUILD, f"cqsa_torch-{torch.__version__}{importlib.machinery.EXTENSION_SUFFIXES[0]}")
 
 
 def _binding_commands(obj: str, target: str) -> list:
@@ -62,7 +64,48 @@ def _binding_commands(obj: str, target: str) -> list:
              "-ltorch_python"]]
 
 
+def _run(cmd, verbose: bool) -> str:
+    """Runs a compiler; returns what went wrong, or an empty string."""
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return f"{' '.join(cmd)}: {e}"
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    return f"compiler failed: {' '.join(cmd)}" if r.returncode else ""
+
+
+class _Binding:
+    """The torch binding: compiled beside the library's sources, linked to the library."""
+
+    def __init__(self, force: bool, verbose: bool):
+        self.verbose, self.target, self.failed = verbose, "", ""
+        try:
+            self.target = binding_path()
+        except ImportError as e:
+            self.failed = str(e)
+            return
+        self.obj, self.tmp = os.path.splitext(self.target)[0] + ".o", self.target + f".{os.getpid()}.tmp"
+        self.compile, self.link = _binding_commands(self.obj, self.tmp)
+        self.stale = force or _stale(self.obj, [BINDING, os.path.join(ROOT, "include", "cqsa.h")])
+
+    def make_object(self):
+        if not self.failed and self.stale:
+            self.failed = _run(self.compile, self.verbose)
+
+    def make(self):
+        if not self.failed and (self.stale or _stale(self.target, [self.obj, LIB])):
+            self.failed = _run(self.link, self.verbose)
+            if not self.failed:
+                os.replace(self.tmp, self.target)
+        if self.failed:
+            if os.path.exists(self.target):  # (one of older sources)
+                os.remove(self.target)
+            sys.stderr.write(f"the torch binding is not built, calls over a cache take longer on the host: {self.failed}\n")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library, and beside it the torch binding where there are a torch and a C++ compiler: calls work without that one, more slowly on the host."""
     os.makedirs(BUILD, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(ROOT, "include", "cqsa.h")]
     objs, jobs = [], []
@@ -73,32 +116,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(o)
         if force or _stale(o, [s, *hdrs]):
             jobs.append([cc, *_flags(), "-c", s, "-o", o])
-    bind = binding_path()
-    bind_obj = bind.replace(".so", ".o")
-    compile_bind, link_bind = _binding_commands(bind_obj, bind + f".{os.getpid()}.tmp")
-    if force or _stale(bind_obj, [BINDING, os.path.join(ROOT, "include", "cqsa.h")]):
-        jobs.append(compile_bind)
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            results = list(ex.map(lambda cmd: subprocess.run(cmd, capture_output=True, text=True), jobs))
-        for cmd, r in zip(jobs, results):
-            if verbose or r.returncode != 0:
-                sys.stderr.write(r.stdout + r.stderr)
-            if r.returncode != 0:
-                raise RuntimeError(f"compiler failed: {' '.join(cmd)}")
+    bind = _Binding(force, verbose)
+    with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        beside = ex.submit(bind.make_object)
+        for wrong in list(ex.map(lambda cmd: _run(cmd, verbose), jobs)):
+            if wrong:
+                raise RuntimeError(wrong)
+        beside.result()
     if force or jobs or _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
-        r = subprocess.run([cc, *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs, "-cudart", "static"], capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("nvcc link failed")
+        wrong = _run([cc, *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs, "-cudart", "static"], verbose)
+        if wrong:
+            raise RuntimeError(wrong)
         os.replace(tmp, LIB)
-    if force or _stale(bind, [bind_obj, LIB]):
-        r = subprocess.run(link_bind, capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("linking the torch binding failed")
-        os.replace(link_bind[link_bind.index("-o") + 1], bind)
+    bind.make()
     return LIB
 
 
