@@ -592,7 +592,9 @@ int decode_ctas(const PagedArgs& a) {
 // in attn_seq.cu's kernel, us: d = 128, 64 sequences of some 290,000 positions together 251 / 261 over 16-bit pages and 284 / 489 over
 // e4m3 ones, 8 sequences of 44,000 16-bit ones 75 / 65, of 112,000 e4m3 ones 122 / 169; d = 64 61 / 67, 59 / 87, 35 / 39, 35 / 44. 16 rows:
 // 207 / 253, 157 / 470, 56 / 65, 74 / 169; 54 / 67, 38 / 88, 27 / 41, 30 / 46. (From there on one longer chunk in a batch
-// takes its single tokens along; over e4m3 pages that is a step, 284 to 510 us for the first.)
+// takes its single tokens along; over e4m3 pages that is a step, 284 to 510 us for the first.) Over 4-bit pages, 32 rows here / there (8 rows here):
+// 64 sequences of some 300,000 positions 334 / 554 (96) at d = 128 and 63 / 89 (23) at d = 64, 8 of 44,000 60 / 85 (21) and 20 / 27 (14), 8 of
+// 112,000 116 / 176 (38) and 29 / 39 (16). From 36 to 256 rows the chunk kernel takes those 553 to 679 and 89 to 95, 85 to 104 and 27 to 32.
 bool decode_applies(const PagedArgs& a) { return static_cast<long long>(a.max_q_len) * (a.Hq / a.Hkv) <= 32; }
 
 size_t decode_workspace(const PagedArgs& a) {

@@ -15,10 +15,11 @@
 // features x 2 keys), relative to the largest power of two met so far, so that P times the scale keeps fp16's precision down to 2^-28 of the
 // largest. P^T's fragment is S^T's transposed, one movmatrix for 8 keys. Queries are fp16, as in attn_decode.cu over e4m3.
 //
-// Measured in a captured graph: one token of each of 128 sequences, 1,000,000 bf16 positions together, 32 query and 8 key heads, d = 128: 235 us
-// (1.09 GB, 4.6 TB/s). On half of the positions the warps issue in 63% of the cycles, the integer pipe in 52%, and 32 keys of a warp
-// are 723 instructions, some 400 of them unpacking and products: that, not memory (55%), sets the pace. Four tokens of each of 40
-// sequences, 400,000 positions, 8 and 2 heads of 64: 37 us; one over 4,001 positions 12 us.
+// Measured in a captured graph: one token of each of 128 sequences, 1,000,000 bf16 positions together, 32 query and 8 key heads, d = 128: 238 us
+// (1.09 GB, 4.6 TB/s), 167 at d = 64. On half of the positions the warps issue in 63% of the cycles (69% at d = 64), the integer
+// pipe in 52%, and 32 keys of a warp are 731 instructions, some 400 of them unpacking and products: that, not memory (55%), sets the
+// pace. Four tokens of each of 40 sequences, 400,000 positions, 8 and 2 heads of 64: 38 us; one over 4,001 positions 12 us (the torch
+// calls some 2 us more).
 #include <math.h>
 #include <string.h>
 
@@ -410,8 +411,9 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
           const uint32_t vat = scale_at<KW>(wv, lane);
           st_shared_u16(vat, h[0]);
           st_shared_u16(vat + 2 * KW, h[1]);
-          // K's as bf16 numbers, the upper halves of fp32 ones, two bytes at a time. With 112 more as its exponent a byte from 248 on is an infinity or a NaN: times 2^-112, and
-          // plus 0 times itself, it is a NaN, and the others are what they stand for. (A test for the former takes 244 us where this takes 242.)
+          // K's as bf16 numbers, the upper halves of fp32 ones, two bytes at a time. With 112 more as its exponent a byte from 248 on is
+          // an infinity or a NaN: times 2^-112, and plus 0 times itself, it is a NaN, and the others are what they stand for. (A test for
+          // the former takes 244 us where this takes 242.)
           auto units = [](uint32_t bytes) -> uint32_t {
             uint32_t r;
             asm("{.reg .b32 z;\n\tmul.rn.bf16x2 z, %1, %2;\n\tfma.rn.bf16x2 %0, %1, %3, z;}" : "=r"(r) : "r"(bytes * 16u + 0x70007000u), "r"(0u), "r"(0x07800780u));
@@ -544,9 +546,10 @@ __global__ void __launch_bounds__(Dec4Cfg<D, NT, NMT>::NTHR, Dec4Cfg<D, NT, NMT>
             }
           }
         };
-        // Where the largest scale's power is 1 or more others may lie 15 powers and more below it. A round by themselves takes them times 2^15, with P times 2^-15: P times a
-        // scale is the same, and P is exact from 2^-13 on, below which these are under 2^-28 of the largest scale's power. (Before the main round, so that
-        // what it needs is not held beside that one's sums: a call for 128 sequences of 1,000,000 positions takes 241 us, 244 with this round behind it, 238 without it.)
+        // Where the largest scale's power is 1 or more others may lie 15 powers and more below it. A round by themselves takes them
+        // times 2^15, with P times 2^-15: P times a scale is the same, and P is exact from 2^-13 on, below which these are under 2^-28 of
+        // the largest scale's power. (Before the main round, so that what it needs is not held beside that one's sums: a call for 128
+        // sequences of 1,000,000 positions takes 241 us, 244 with this round behind it, 238 without it.)
         if (__builtin_expect(ev >= 15, 0)) {
           int key;  // (the lane, read anew: nothing is kept in registers for this)
           asm volatile("mov.u32 %0, %%laneid;" : "=r"(key));

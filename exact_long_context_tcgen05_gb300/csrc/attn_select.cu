@@ -13,8 +13,10 @@
 // the last page is masked.
 //
 // Measured in a captured graph, bounds of the new pages included: 48 sequences of 1,000,000 4-bit positions together, 32 and 8 heads of 128, 64 pages
-// of 32 each: 71 us (kernel by kernel, cold: bounds 6, scores 25, choice 14, attention 31, joining 5); one token over 131,072 fp16 positions,
-// 32 pages of 64: 24 us, five launches; 200 tokens over 65,536: 154 us, of which the attention's reading of 839 MB of pages, each token's own, is most.
+// of 32 each: 72 us (kernel by kernel, cold: bounds 7, scores 22, choice 14, attention 32, joining 5); one token over 131,072 fp16 positions,
+// 32 pages of 64: 24 us, five launches; 200 tokens over 65,536: 155 us, of which the attention's reading of 839 MB of pages, each token's own, is most.
+// (The torch calls take some 8 us more on the host.) A chunk's time grows with its tokens, 0.54 us each from 1,000 to 8,192 over these positions, 16 pages of
+// 64: 0.81 to 0.87 of what attention over all of them takes.
 // On half of the first the score kernel has 24% of memory's rate and 49% of issue: loads in flight bound it.
 #include <math.h>
 #include <string.h>
@@ -654,7 +656,8 @@ template <bool ONE>
 int launch_scores(const SelectArgs& a, int token0, int tokens, int at_once, int gp, cudaStream_t stream) {
   // Blocks for so many a SM, whatever the longest sequence is: in a ragged batch most are far shorter. (48 sequences of 1,000,000 positions in pages of
   // 32 together, the whole call: 94 us with 4, 73 with 8, 71 with 12, 77 with 40. Blocks of several tiles of rows begin with more work: 46 us with 4 and 49
-  // with 8 for 60 tokens over 400,000 positions.)
+  // with 8 for 60 tokens over 400,000 positions, 56 and 63 at 32 and 8 heads of 128. Otherwise 1 to 128 sequences
+  // of 1 to 1,000 tokens differ by 3% at most between 2 and 40, 48 ragged ones of d = 128 by 8%: 51 us with 8, 52 with 12, 55 with 24.)
   const long long units = (tokens + at_once - 1LL) / at_once * a.Hkv, most = (a.most_pages + kScorePages - 1) / kScorePages;
   const long long want = static_cast<long long>(ONE ? 12 : 4) * sm_count() / units;
   const int splits = static_cast<int>(want < 1 ? 1 : (want < most ? want : most));

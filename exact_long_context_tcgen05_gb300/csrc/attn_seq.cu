@@ -1335,6 +1335,14 @@ __global__ void __launch_bounds__(256) seq_combine_kernel(const SeqParams p) {
 // or more is unpacked first, as far as the scratch pages go, and read as 16-bit pages: 2,048 tokens over 32,000 positions, 32 and 8 heads of
 // 128, 731 us against 1,359. The others go to a second kernel, which short batches do not gain from: 12 ragged sequences, 3,000 tokens over 60,000
 // positions, 8 and 2 heads of 64, some 30 key tiles a CTA (72 by the longest sequence), take 84 us packed and 100 in two kernels.
+// Where the two forms cross, packed / unpacked (key tiles a CTA by the longest sequence; 8 and 2 heads of 64 in fp16, then 32 and 8 of 128 in bf16):
+//   2,048 tokens of one sequence        (13) 42 / 46, (20) 54 / 53, (59) 118 / 96, (112) 204 / 156, (217) 385 / 277
+//                                       (54) 195 / 117, (133) 435 / 239, (448) 1,381 / 730
+//   8 sequences of 56 to 455 of them    (27) 59 / 84, (53) 87 / 113, (106) 147 / 189, (211) 267 / 286
+//                                       (30) 134 / 152, (57) 206 / 197, (109) 316 / 291, (214) 581 / 484, (424) 1,062 / 802
+//   rows a sequence, over 8,000 positions each, with work enough (unpacked as far as the scratch pages go): 512 225 / 244 and 848 / 856, 768 220 / 216 and 803 / 716, 1,024 219 / 202 and 813 / 549;
+//   of 256 rows, one unit, 242 / 326 and 869 / 978
+// kFullTiles lies between the crossings of the two kinds, which the caller's numbers do not tell apart. Below it bf16 rows keep P in fp16.
 constexpr int kFullRows = 512;                      // rows of a sequence and key head from which on it is unpacked
 constexpr int kFullTiles = 96;                      // key tiles of a CTA, by the caller's longest sequence, from which on any is
 constexpr size_t kFullBytes = size_t(512) << 20;    // the most that the scratch pages take

@@ -262,7 +262,8 @@ int launch_combine(const DecParams& p, int rows, int ctas, cudaStream_t stream) 
 
 // attn_decode4.cu: the kernel over 4-bit pages, for `rows` (8, 16 or 32) rows of a unit.
 // CTAs of an SM, of 5 warps (9 for 32 rows): three leave a thread 128 registers, which hold the sums of 8 rows at d = 128 and of 16 at d = 64; four leave
-// 96, enough for 8 rows at d = 64 (128 sequences of 1,000,000 positions 165 us against 183; at d = 128 they spill, 253 against 235).
+// 96, enough for 8 rows at d = 64 (128 sequences of 1,000,000 positions 165 us against 183; at d = 128 they spill, 253 against 235; both
+// measured before scales far below the largest had a round of their own).
 constexpr int decode4_occ(int rows, int d) { return rows == 8 ? (d == 64 ? 4 : 3) : (rows == 16 ? (d == 64 ? 3 : 2) : 1); }
 constexpr int kDecode4Tile = 128;  // keys of its tiles
 int launch_decode4(const CUtensorMap& mk, const CUtensorMap& mv, const DecParams& p, int d, int bf16, int rows, int ctas, cudaStream_t stream);

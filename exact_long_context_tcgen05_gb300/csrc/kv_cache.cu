@@ -114,7 +114,7 @@ __device__ __forceinline__ void put_vector(uint8_t* cache, uint8_t* scale, long 
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint32_t b = int4_scale_byte(amax);
     const float unit = int4_scale(b), inv = __frcp_rn(unit);
-    // The 32-bit quotient f / unit from the reciprocal: one correction by the remainder, which is exact. The corrected value is within 2^-46 of the
+    // The 32-bit quotient f / unit from the reciprocal with one correction by the remainder, which is exact (Markstein's method). The corrected value is within 2^-46 of the
     // quotient before it is rounded, and a quotient by a number of four significant bits is further than 2^-30 from every border between
     // two roundings, so it is the rounded quotient. A sum with 1.5 * 2^23 + 8 then leaves the nearest (even) whole number + 8 in its lowest bits.
     uint32_t word = 0;
